@@ -384,6 +384,114 @@ moe_status moe_layer_forward_profiled(const moe_config* cfg, const moe_weights* 
 moe_status moe_bias_update(int32_t E, const int32_t* counts, float* expert_bias, float decay,
                            float rate, moe_stream_t stream);
 
+/* ---- Routing from given logits, and its gradient ------------------------------------------------
+ * For callers that have the router logits [T, E] already (a linear layer of their own, or a trained
+ * router with another score): scores, choice and weights of a token, and the gradient of the
+ * weights to the logits. With l the logits of a token:
+ *   score   s = softmax over all E experts of l     (MOE_SCORE_SOFTMAX)
+ *           s = 1 / (1 + exp(-l))                   (MOE_SCORE_SIGMOID)
+ *   rank    r = s + expert_bias (a balance bias; it steers the choice only); an expert whose logit
+ *           is -inf (switched off) or NaN ranks below every other, whatever its bias
+ *   groups  n_groups > 0: E / n_groups consecutive experts form a group, ranked by its largest r
+ *           (group_top2 = 0) or by the sum of its two largest (group_top2 = 1; a switched-off second
+ *           adds nothing); only the topk_groups best groups are searched
+ *   choice  the top_k largest r, r descending
+ *   weight  scale * s, or scale * s / (sum of s over the chosen experts) with renormalize = 1
+ * Every tie goes to the lower index. Chosen scores that are all zero (every expert of the token
+ * switched off, say) have weight 0. A row with a NaN (softmax: or a +inf) still has top_k different
+ * experts, and NaN weights. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* Element types of the entry points that take more than one. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
+
+typedef struct {
+  int32_t T, E, top_k;   /* tokens, experts, experts per token; limits as in moe_config */
+  int32_t score;         /* moe_score */
+  int32_t n_groups;      /* 0: off; else <= 64 and a divisor of E */
+  int32_t topk_groups;   /* groups kept; top_k <= topk_groups * E / n_groups */
+  int32_t group_top2;    /* 0 or 1 */
+  int32_t renormalize;   /* 0 or 1 */
+  float scale;           /* finite factor on the weights */
+  int32_t dtype;         /* of logits and d_logits: MOE_DTYPE_F32 or MOE_DTYPE_BF16 */
+  int64_t ld;            /* elements from one row of logits to the next; 0: E */
+} moe_gate_config;
+
+/* logits [T, E] of cfg->dtype with row stride cfg->ld, aligned to their element; expert_bias [E]
+ * fp32 or NULL. Writes topk_idx [T, k] int32, topk_w [T, k] fp32 and, unless NULL, scores [T, E]
+ * fp32 (s, for a balance loss). topk_idx suits moe_permute. No workspace. Asynchronous on stream;
+ * T = 0 launches nothing. */
+moe_status moe_route_logits(const moe_gate_config* cfg, const void* logits,
+                            const float* expert_bias, int32_t* topk_idx, float* topk_w,
+                            float* scores, moe_stream_t stream);
+
+/* d_logits [T, E] (contiguous, cfg->dtype) = gradient of a loss whose gradients to topk_w and
+ * scores are d_topk_w [T, k] and d_scores [T, E] (fp32; either may be NULL, not both). topk_idx as
+ * moe_route_logits wrote it: the choice is a constant of the gradient (an index outside [0, E) adds
+ * nothing). The bias has no gradient. A row whose chosen scores are all zero has gradient 0 from its
+ * weights. */
+moe_status moe_route_logits_backward(const moe_gate_config* cfg, const void* logits,
+                                     const int32_t* topk_idx, const float* d_topk_w,
+                                     const float* d_scores, void* d_logits, moe_stream_t stream);
+
+/* ---- 8-bit weights and activations ----------------------------------------------------------------
+ * Products of 8-bit integers with one scale per token and one per output channel: half the weight
+ * bytes of bf16 in decode and prefill alike (weight_bits = 8 above keeps the activations in 16 bits,
+ * has a scale per 128 weights and is built for decode). Symmetric, no zero point. */
+
+/* One set of n matrices [K -> N]: q [n, N, K] (each output channel's K codes contiguous), scale
+ * [n, N] fp32, weight = q * scale. Written by moe_quantize_channels. */
+typedef struct {
+  const int8_t* q;
+  const float* scale;
+} moe_int8_matrix;
+
+typedef struct {
+  moe_int8_matrix gate, up, down;          /* [E]: d -> d_ff, d -> d_ff, d_ff -> d */
+  moe_int8_matrix sh_gate, sh_up, sh_down; /* [S], n_shared > 0 only */
+} moe_int8_weights;
+
+/* Rows of x [T, d] (dtype: moe_dtype; row stride ld elements, 0: d) to 8 bits: scale[t] =
+ * max |x[t]| * fl(1 / 127), q[t, j] = clamp(rint(x[t, j] / scale[t]), -127, 127), rint to nearest even, all in
+ * fp32. A zero row has scale 0 and q 0. A row with a NaN or an infinity has that as its scale (NaN
+ * before infinity), so products with it are not finite either. q [T, d] contiguous. 1 <= d. x aligned
+ * to its element; rows of 16-byte pieces (pointers and strides) move faster. */
+moe_status moe_quantize_rows(int32_t T, int32_t d, int32_t dtype, const void* x, int64_t ld,
+                             int8_t* q, float* scale, moe_stream_t stream);
+
+/* One-time weight preparation: W [n_mat, K, N] bf16 (this library's weight layout) to q [n_mat, N, K]
+ * and scale [n_mat, N], by the same rule over the K weights of each output channel. */
+moe_status moe_quantize_channels(int32_t n_mat, int32_t K, int32_t N, const uint16_t* W, int8_t* q,
+                                 float* scale, moe_stream_t stream);
+
+/* y[r, n] = (sum_k q_x[r, k] * q_w[e, n, k]) * s_x[r] * s_w[e, n] for the rows r of segment e,
+ * offsets[e] <= r < offsets[e + 1] (offsets: int32 [n_mat + 1] on the device, ascending from 0 to at
+ * most rows; NULL: n_mat is 1 and owns every row). Rows past offsets[n_mat] are not written. Offsets
+ * that descend or leave [0, rows] make that segment empty and set MOE_DEVFAULT_BAD_TILE.
+ *   q_x [rows, K], q_w [n_mat, N, K] 16-byte aligned; s_x [rows], s_w [n_mat, N] fp32; y [rows, N] of
+ *   y_dtype (moe_dtype; fp16 becomes infinite past its range), aligned to its element.
+ *   The sum is exact while every partial sum stays below 2^24 in magnitude, and within fp32's
+ *   rounding past that. Limits: 1 <= n_mat <= 256; K a multiple of 16, K <= 65536; 1 <= N < 2^27. */
+moe_status moe_int8_matmul_workspace_size(int32_t rows, int32_t K, int32_t N, int32_t n_mat,
+                                          size_t* bytes);
+moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, const int8_t* q_x,
+                           const float* s_x, const int8_t* q_w, const float* s_w,
+                           const int32_t* offsets, int32_t y_dtype, void* y, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+
+/* Steps 6-9 on 8-bit weights and activations: the contract of moe_grouped_ffn_quantized (x bf16,
+ * perm_slot, offsets, topk_w; fp16 y_slot rows [T*k + S*T, d] with dropped slots' rows not written)
+ * with cfg->weight_bits = 0. The rows of x, and of H = silu(G) * U after it, are quantized as by
+ * moe_quantize_rows (H from fp32). moe_combine (MOE_Y_F16) reads y_slot. ws: a workspace of
+ * moe_grouped_ffn_int8_workspace_size bytes cleared once by moe_workspace_init; its status word is
+ * read by moe_device_status (MOE_DEVFAULT_FP16_RANGE: a slot value was past fp16's range and was
+ * clamped; MOE_DEVFAULT_BAD_TILE: offsets or perm_slot were inconsistent). */
+moe_status moe_grouped_ffn_int8_workspace_size(const moe_config* cfg, size_t* bytes);
+moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const int32_t* perm_slot,
+                                const int32_t* offsets, const float* topk_w,
+                                const moe_int8_weights* w, uint16_t* y_slot, void* ws,
+                                size_t ws_bytes, moe_stream_t stream);
+
 /* Failure-detection check of this device: runs the library's two kinds of bounded device wait,
  * each against a condition that never comes true, with a wait limit of limit_ns (100 us .. 2 s;
  * the layer's own waits use 2 s). One is the mbarrier wait of the tensor-core pipelines (a

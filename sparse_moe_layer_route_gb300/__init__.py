@@ -19,12 +19,17 @@ ROUTE_PLAIN, ROUTE_BIAS_SELECT, ROUTE_GUMBEL = 0, 1, 2
 DEVFAULT_BAD_EXPERT_INDEX, DEVFAULT_PIPELINE_TIMEOUT, DEVFAULT_BAD_TILE = 0x1, 0x2, 0x4
 DEVFAULT_FP16_RANGE = 0x8
 Y_F16, Y_F32 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 
 EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_prepare_router", "moe_route",
            "moe_permute", "moe_permute_noalloc", "moe_overflow_reroute", "moe_grouped_ffn",
            "moe_grouped_ffn_quantized", "moe_quantize_weights", "moe_combine",
            "moe_layer_forward", "moe_layer_forward_profiled", "moe_layer_forward_host",
-           "moe_pack_f16", "moe_bias_update", "moe_check_bounded_waits", "moe_device_status",
+           "moe_pack_f16", "moe_bias_update", "moe_route_logits", "moe_route_logits_backward",
+           "moe_quantize_rows", "moe_quantize_channels", "moe_int8_matmul_workspace_size",
+           "moe_int8_matmul", "moe_grouped_ffn_int8_workspace_size", "moe_grouped_ffn_int8",
+            "moe_check_bounded_waits", "moe_device_status",
            "moe_status_string")
 
 
@@ -80,6 +85,28 @@ class MoeRouteOut(ctypes.Structure):
                 ("topk_idx", "topk_w", "counts", "offsets", "perm_slot", "slot_pos")]
 
 
+class GateConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "E", "top_k", "score", "n_groups", "topk_groups", "group_top2",
+                 "renormalize")] + \
+        [("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("ld", ctypes.c_int64)]
+
+    @classmethod
+    def make(cls, T, E, top_k, score=SCORE_SOFTMAX, n_groups=0, topk_groups=0, group_top2=False,
+             renormalize=True, scale=1.0, dtype=DTYPE_F32, ld=0):
+        return cls(T, E, top_k, score, n_groups, topk_groups, int(bool(group_top2)),
+                   int(bool(renormalize)), scale, dtype, ld)
+
+
+class MoeInt8Matrix(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class MoeInt8Weights(ctypes.Structure):
+    _names = ("gate", "up", "down", "sh_gate", "sh_up", "sh_down")
+    _fields_ = [(n, MoeInt8Matrix) for n in _names]
+
+
 _lib = None
 
 
@@ -116,6 +143,17 @@ def lib():
         L.moe_bias_update.argtypes = [ctypes.c_int32, P, P, ctypes.c_float, ctypes.c_float, P]
         L.moe_device_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
         L.moe_check_bounded_waits.argtypes = [ctypes.c_int64, P, P, S, P]
+        gcfgp, i64 = ctypes.POINTER(GateConfig), ctypes.c_int64
+        L.moe_route_logits.argtypes = [gcfgp, P, P, P, P, P, P]
+        L.moe_route_logits_backward.argtypes = [gcfgp, P, P, P, P, P, P]
+        L.moe_quantize_rows.argtypes = [i32, i32, i32, P, i64, P, P, P]
+        L.moe_quantize_channels.argtypes = [i32, i32, i32, P, P, P, P]
+        L.moe_int8_matmul_workspace_size.argtypes = [i32, i32, i32, i32,
+                                                     ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_int8_matmul.argtypes = [i32, i32, i32, i32, P, P, P, P, P, i32, P, P, S, P]
+        L.moe_grouped_ffn_int8_workspace_size.argtypes = [cfgp, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_grouped_ffn_int8.argtypes = [cfgp, P, P, P, P, ctypes.POINTER(MoeInt8Weights), P, P,
+                                           S, P]
         L.moe_status_string.argtypes = [I]
         L.moe_status_string.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -337,6 +375,167 @@ def bias_update(counts, expert_bias, decay=0.99, rate=0.01, stream=None):
     """In place: expert_bias <- decay*expert_bias - rate*counts/(mean(counts)+1e-8)."""
     _check(lib().moe_bias_update(expert_bias.numel(), _ptr(counts), _ptr(expert_bias), decay, rate,
                                  _stream(stream)), "moe_bias_update")
+
+
+def _dtype_code(t, where):
+    code = _DTYPES.get(str(t.dtype))
+    if code is None:
+        raise ValueError(f"{where}: element type {t.dtype} is not supported")
+    return code
+
+
+_DTYPES = {"torch.float32": DTYPE_F32, "torch.bfloat16": DTYPE_BF16, "torch.float16": DTYPE_F16}
+
+
+def _expect(where, name, t, shape, dtype):
+    """t: a contiguous tensor of this shape and element type on the GPU."""
+    if tuple(t.shape) != shape or str(t.dtype) != dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor {dtype} {shape}, not "
+                         f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+
+
+def _expect_logits(where, gcfg, logits):
+    if tuple(logits.shape) != (gcfg.T, gcfg.E) or not logits.is_cuda or \
+            _DTYPES.get(str(logits.dtype)) != gcfg.dtype or \
+            (gcfg.T > 1 and logits.stride(0) != (gcfg.ld or gcfg.E)) or \
+            (gcfg.E > 1 and logits.stride(1) != 1):
+        raise ValueError(f"{where}: logits {logits.dtype} {tuple(logits.shape)} (strides "
+                         f"{logits.stride()}) on {logits.device} do not fit the configuration")
+
+
+def route_logits(gcfg: GateConfig, logits, expert_bias, topk_idx, topk_w, scores=None, stream=None):
+    """Experts and weights from given router logits [T, E] (see moe_route_logits); scores: optional
+    fp32 [T, E] that receives every expert's score."""
+    w, T, E, k = "moe_route_logits", gcfg.T, gcfg.E, gcfg.top_k
+    _expect_logits(w, gcfg, logits)
+    if expert_bias is not None:
+        _expect(w, "expert_bias", expert_bias, (E,), "torch.float32")
+    _expect(w, "topk_idx", topk_idx, (T, k), "torch.int32")
+    _expect(w, "topk_w", topk_w, (T, k), "torch.float32")
+    if scores is not None:
+        _expect(w, "scores", scores, (T, E), "torch.float32")
+    _check(lib().moe_route_logits(ctypes.byref(gcfg), logits.data_ptr(), _ptr(expert_bias),
+                                  topk_idx.data_ptr(), topk_w.data_ptr(), _ptr(scores),
+                                  _stream(stream)), w)
+
+
+def route_logits_backward(gcfg: GateConfig, logits, topk_idx, d_topk_w, d_scores, d_logits,
+                          stream=None):
+    """d_logits from the gradients of topk_w and scores (either may be None)."""
+    w, T, E, k = "moe_route_logits_backward", gcfg.T, gcfg.E, gcfg.top_k
+    _expect_logits(w, gcfg, logits)
+    _expect(w, "topk_idx", topk_idx, (T, k), "torch.int32")
+    if d_topk_w is not None:
+        _expect(w, "d_topk_w", d_topk_w, (T, k), "torch.float32")
+    if d_scores is not None:
+        _expect(w, "d_scores", d_scores, (T, E), "torch.float32")
+    _expect(w, "d_logits", d_logits, (T, E), str(logits.dtype))
+    _check(lib().moe_route_logits_backward(ctypes.byref(gcfg), logits.data_ptr(),
+                                           topk_idx.data_ptr(), _ptr(d_topk_w), _ptr(d_scores),
+                                           d_logits.data_ptr(), _stream(stream)), w)
+
+
+def quantize_rows(x, q, scale, stream=None):
+    """x [T, d] (fp32, bf16 or fp16; rows may be strided) to q int8 [T, d] and scale fp32 [T]."""
+    w = "moe_quantize_rows"
+    T, d = x.shape
+    if not x.is_cuda or (d > 1 and x.stride(1) != 1):
+        raise ValueError(f"{w}: x must be a CUDA tensor with unit stride inside a row")
+    _expect(w, "q", q, (T, d), "torch.int8")
+    _expect(w, "scale", scale, (T,), "torch.float32")
+    _check(lib().moe_quantize_rows(T, d, _dtype_code(x, w), x.data_ptr(),
+                                   x.stride(0) if T > 1 else d, q.data_ptr(), scale.data_ptr(),
+                                   _stream(stream)), w)
+
+
+def quantize_channels(W, stream=None):
+    """One-time preparation of bf16 weights W [n, K, N] (or [K, N]) for the 8-bit products: (q int8
+    [n, N, K], scale fp32 [n, N]), new tensors on W's device."""
+    import torch
+    n, (K, N) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
+    _expect("moe_quantize_channels", "W", W, tuple(W.shape), "torch.bfloat16")
+    q = torch.empty((n, N, K), dtype=torch.int8, device=W.device)
+    scale = torch.empty((n, N), dtype=torch.float32, device=W.device)
+    _check(lib().moe_quantize_channels(n, K, N, W.data_ptr(), q.data_ptr(), scale.data_ptr(),
+                                       _stream(stream)), "moe_quantize_channels")
+    return q, scale
+
+
+def int8_matmul_workspace_size(rows, K, N, n_mat) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_int8_matmul_workspace_size(rows, K, N, n_mat, ctypes.byref(n)),
+           "moe_int8_matmul_workspace_size")
+    return n.value
+
+
+def grouped_ffn_int8_workspace_size(cfg: MoeConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_grouped_ffn_int8_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_grouped_ffn_int8_workspace_size")
+    return n.value
+
+
+def alloc_int8_workspace(nbytes, device="cuda"):
+    """A workspace of nbytes for the 8-bit entry points, its status word cleared."""
+    import torch
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    workspace_init(ws)
+    return ws
+
+
+def int8_matmul(q_x, s_x, q_w, s_w, offsets, y, ws, stream=None):
+    """y [rows, N] (fp32, bf16 or fp16) = (q_x q_w[e]^T) * s_x * s_w[e] over the row segments of
+    offsets (int32 [n + 1] on the device; None: one matrix for every row)."""
+    w = "moe_int8_matmul"
+    rows, K = q_x.shape
+    n, N = q_w.shape[0], q_w.shape[1]
+    _expect(w, "q_x", q_x, (rows, K), "torch.int8")
+    _expect(w, "s_x", s_x, (rows,), "torch.float32")
+    _expect(w, "q_w", q_w, (n, N, K), "torch.int8")
+    _expect(w, "s_w", s_w, (n, N), "torch.float32")
+    if offsets is not None:
+        _expect(w, "offsets", offsets, (n + 1,), "torch.int32")
+    _expect(w, "y", y, (rows, N), str(y.dtype))
+    _check(lib().moe_int8_matmul(rows, K, N, n, q_x.data_ptr(), s_x.data_ptr(), q_w.data_ptr(),
+                                 s_w.data_ptr(), _ptr(offsets), _dtype_code(y, w), y.data_ptr(),
+                                 _ptr(ws), ws.numel(), _stream(stream)), w)
+
+
+def make_int8_weights(gate, up, down, sh_gate=None, sh_up=None, sh_down=None) -> MoeInt8Weights:
+    """From quantize_channels() results (kept alive by the struct)."""
+    mats = (gate, up, down, sh_gate, sh_up, sh_down)
+    for m in mats:
+        if m is not None:
+            n, N, K = m[0].shape
+            _expect("make_int8_weights", "q", m[0], (n, N, K), "torch.int8")
+            _expect("make_int8_weights", "scale", m[1], (n, N), "torch.float32")
+    w = MoeInt8Weights(*[MoeInt8Matrix() if m is None else MoeInt8Matrix(_ptr(m[0]), _ptr(m[1]))
+                         for m in mats])
+    w._tensors = mats
+    return w
+
+
+def grouped_ffn_int8(cfg, x, perm_slot, offsets, topk_w, weights: MoeInt8Weights, y_slot, ws,
+                     stream=None):
+    """y_slot [T*k + S*T, d] float16: the routed and shared experts on 8-bit weights and
+    activations (see moe_grouped_ffn_int8)."""
+    w, T, d, k = "moe_grouped_ffn_int8", cfg.T, cfg.d, cfg.top_k
+    _expect(w, "x", x, (T, d), "torch.bfloat16")
+    _expect(w, "perm_slot", perm_slot, (T * k,), "torch.int32")
+    _expect(w, "offsets", offsets, (cfg.E + 1,), "torch.int32")
+    if topk_w is not None:
+        _expect(w, "topk_w", topk_w, (T, k), "torch.float32")
+    _expect(w, "y_slot", y_slot, (T * (k + cfg.n_shared), d), "torch.float16")
+    for name, n, N, K in (("gate", cfg.E, cfg.d_ff, d), ("up", cfg.E, cfg.d_ff, d),
+                          ("down", cfg.E, d, cfg.d_ff), ("sh_gate", cfg.n_shared, cfg.d_ff, d),
+                          ("sh_up", cfg.n_shared, cfg.d_ff, d),
+                          ("sh_down", cfg.n_shared, d, cfg.d_ff)):
+        m = weights._tensors[MoeInt8Weights._names.index(name)]
+        if n and (m is None or tuple(m[0].shape) != (n, N, K)):
+            raise ValueError(f"{w}: weights.{name} must hold {(n, N, K)}")
+    _check(lib().moe_grouped_ffn_int8(ctypes.byref(cfg), _ptr(x), _ptr(perm_slot), _ptr(offsets),
+                                      _ptr(topk_w), ctypes.byref(weights), _ptr(y_slot), _ptr(ws),
+                                      ws.numel(), _stream(stream)), w)
 
 
 def check_bounded_waits(limit_ns, expired, ws, stream=None):

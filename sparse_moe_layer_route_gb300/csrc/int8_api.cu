@@ -1,0 +1,205 @@
+// Entry points of the 8-bit weights and activations (declarations and contracts: include/moe.h):
+// validation, workspace carving and launch sequencing.
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "int8.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr size_t kHead = 512;  // status word and counter block, as in every workspace
+
+bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+int dtype_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+bool dtype_ok(int dtype) {
+  return dtype == MOE_DTYPE_F32 || dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16;
+}
+moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+moe_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  return ws == nullptr || !aligned(ws, 256) || ws_bytes < need ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+moe_status check_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat) {
+  if (rows < 0 || K < 1 || N < 1 || n_mat < 1) return MOE_ERR_INVALID_ARG;
+  if (n_mat > 256 || K % 16 != 0 || K > 65536 || N >= (1 << 27)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Buffers of one FFN call.
+struct FfnLayout {
+  size_t qx, sx, h, qh, sh, total;
+};
+FfnLayout ffn_layout(const Shape& s) {
+  FfnLayout L;
+  size_t o = kHead;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = (o + bytes + 255) / 256 * 256;
+    return at;
+  };
+  L.qx = take((size_t)s.T * s.d);
+  L.sx = take(4ull * s.T);
+  // fp32: an fp16 H (2^-12 of the value) would move about 1 code in 150 by one when H is quantized
+  // (3.5e-3 of the layer output's norm measured), fp32 moves none to speak of
+  L.h = take(4ull * s.rows * s.f);
+  L.qh = take((size_t)s.rows * s.f);
+  L.sh = take(4ull * s.rows);
+  L.total = o;
+  return L;
+}
+
+bool mat_ok(const moe_int8_matrix& m) {
+  return m.q && m.scale && aligned(m.q, 16) && aligned(m.scale, 4);
+}
+
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_quantize_rows(int32_t T, int32_t d, int32_t dtype, const void* x, int64_t ld,
+                             int8_t* q, float* scale, moe_stream_t stream) {
+  if (T < 0 || d < 1 || !dtype_ok(dtype) || (ld != 0 && ld < d)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !q || !scale || !aligned(x, dtype_bytes(dtype)) || !aligned(scale, 4))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(
+      launch_quantize_rows(T, d, dtype, x, ld != 0 ? ld : d, q, scale, (cudaStream_t)stream));
+}
+
+moe_status moe_quantize_channels(int32_t n_mat, int32_t K, int32_t N, const uint16_t* W, int8_t* q,
+                                 float* scale, moe_stream_t stream) {
+  if (n_mat < 1 || K < 1 || N < 1 || !W || !q || !scale) return MOE_ERR_INVALID_ARG;
+  if (!aligned(W, 2) || !aligned(scale, 4)) return MOE_ERR_INVALID_ARG;
+  if (n_mat > 65535) return MOE_ERR_UNSUPPORTED;
+  return cuda_status(launch_quantize_channels(n_mat, K, N, W, q, scale, (cudaStream_t)stream));
+}
+
+moe_status moe_int8_matmul_workspace_size(int32_t rows, int32_t K, int32_t N, int32_t n_mat,
+                                          size_t* bytes) {
+  const moe_status r = check_matmul(rows, K, N, n_mat);
+  if (r != MOE_OK) return r;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = kHead;
+  return MOE_OK;
+}
+
+moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, const int8_t* q_x,
+                           const float* s_x, const int8_t* q_w, const float* s_w,
+                           const int32_t* offsets, int32_t y_dtype, void* y, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  moe_status r = check_matmul(rows, K, N, n_mat);
+  if (r != MOE_OK) return r;
+  if (!dtype_ok(y_dtype) || (offsets == nullptr && n_mat != 1)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!q_x || !s_x || !q_w || !s_w || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned(q_x, 16) || !aligned(q_w, 16) || !aligned(s_x, 4) || !aligned(s_w, 4) ||
+      !aligned(offsets, 4) || !aligned(y, dtype_bytes(y_dtype)))
+    return MOE_ERR_INVALID_ARG;
+  size_t need = 0;
+  moe_int8_matmul_workspace_size(rows, K, N, n_mat, &need);
+  if ((r = check_ws(ws, ws_bytes, need)) != MOE_OK) return r;
+  Int8Gemm g = {};
+  g.qx = q_x;
+  g.sx = s_x;
+  g.qw = q_w;
+  g.sw = s_w;
+  g.offsets = offsets;
+  g.out = y;
+  g.out_dtype = y_dtype;
+  g.status = at<int>(ws, 0);
+  g.rows = rows;
+  g.K = K;
+  g.N = N;
+  g.n_mat = n_mat;
+  g.T = 1;
+  g.k = 1;
+  return cuda_status(launch_int8_gemm(kInt8Matrix, g, (cudaStream_t)stream));
+}
+
+moe_status moe_grouped_ffn_int8_workspace_size(const moe_config* cfg, size_t* bytes) {
+  size_t plain = 0;
+  const moe_status r = moe_workspace_size(cfg, &plain);  // the layer's checks of a configuration
+  if (r != MOE_OK) return r;
+  if (bytes == nullptr || cfg->weight_bits != 0) return MOE_ERR_INVALID_ARG;
+  *bytes = cfg->T == 0 ? kHead : ffn_layout(make_shape(*cfg)).total;
+  return MOE_OK;
+}
+
+moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const int32_t* perm_slot,
+                                const int32_t* offsets, const float* topk_w,
+                                const moe_int8_weights* w, uint16_t* y_slot, void* ws,
+                                size_t ws_bytes, moe_stream_t stream) {
+  size_t need = 0;
+  moe_status r = moe_grouped_ffn_int8_workspace_size(cfg, &need);
+  if (r != MOE_OK) return r;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x || !perm_slot || !offsets || !w || !y_slot) return MOE_ERR_INVALID_ARG;
+  if (!mat_ok(w->gate) || !mat_ok(w->up) || !mat_ok(w->down)) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_shared > 0 && (!mat_ok(w->sh_gate) || !mat_ok(w->sh_up) || !mat_ok(w->sh_down)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(y_slot, 16) || !aligned(perm_slot, 4) || !aligned(offsets, 4) ||
+      !aligned(topk_w, 4))
+    return MOE_ERR_INVALID_ARG;
+  if ((r = check_ws(ws, ws_bytes, need)) != MOE_OK) return r;
+  const Shape s = make_shape(*cfg);
+  const FfnLayout L = ffn_layout(s);
+  const cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = launch_quantize_rows(s.T, s.d, MOE_DTYPE_BF16, x, s.d, at<int8_t>(ws, L.qx),
+                                       at<float>(ws, L.sx), st);
+  Int8Gemm g = {};
+  g.qx = at<int8_t>(ws, L.qx);
+  g.sx = at<float>(ws, L.sx);
+  g.qw = w->gate.q;
+  g.sw = w->gate.scale;
+  g.qw2 = w->up.q;
+  g.sw2 = w->up.scale;
+  g.sh_qw = w->sh_gate.q;
+  g.sh_sw = w->sh_gate.scale;
+  g.sh_qw2 = w->sh_up.q;
+  g.sh_sw2 = w->sh_up.scale;
+  g.offsets = offsets;
+  g.perm_slot = perm_slot;
+  g.out = at<float>(ws, L.h);
+  g.status = at<int>(ws, 0);
+  g.rows = (int)s.TK;
+  g.K = s.d;
+  g.N = s.f;
+  g.n_mat = s.E;
+  g.S = s.S;
+  g.T = s.T;
+  g.k = s.k;
+  if (e == cudaSuccess) e = launch_int8_gemm(kInt8SwiGLU, g, st);
+  // every row of H, those past the last kept position included: they are not read after this
+  if (e == cudaSuccess)
+    e = launch_quantize_rows((int)s.rows, s.f, MOE_DTYPE_F32, at<float>(ws, L.h), s.f,
+                             at<int8_t>(ws, L.qh), at<float>(ws, L.sh), st);
+  g.qx = at<int8_t>(ws, L.qh);
+  g.sx = at<float>(ws, L.sh);
+  g.qw = w->down.q;
+  g.sw = w->down.scale;
+  g.qw2 = nullptr;
+  g.sw2 = nullptr;
+  g.sh_qw = w->sh_down.q;
+  g.sh_sw = w->sh_down.scale;
+  g.sh_qw2 = nullptr;
+  g.sh_sw2 = nullptr;
+  g.topk_w = topk_w;
+  g.out = y_slot;
+  g.K = s.f;
+  g.N = s.d;
+  if (e == cudaSuccess) e = launch_int8_gemm(kInt8Slot, g, st);
+  return cuda_status(e);
+}
+
+}  // extern "C"
