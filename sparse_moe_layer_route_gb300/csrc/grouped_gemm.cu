@@ -796,11 +796,12 @@ bool make_tmap_2d(CUtensorMap* m, const void* ptr, long long rows, long long col
 }
 
 bool make_tmap_3d(CUtensorMap* m, const void* ptr, long long n, long long rows, long long cols,
-                  int box_cols, int box_rows, CUtensorMapDataType dt) {
+                  int box_cols, int box_rows, CUtensorMapDataType dt, int elem_bytes) {
   auto fn = encode_fn_impl();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
-  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)rows * cols * 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * elem_bytes,
+                                 (cuuint64_t)rows * cols * elem_bytes};
   const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,

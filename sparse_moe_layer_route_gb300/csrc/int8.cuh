@@ -22,21 +22,34 @@ __device__ __forceinline__ int int8_code(float x, float scale) {
   return max(-127, min(127, v));
 }
 
-// One grouped product. Segment e < n_mat holds rows [offsets[e], offsets[e + 1]) (offsets NULL: all
-// rows); with shared experts, segment n_mat + s is rows [rows + s * T, rows + (s + 1) * T).
+// Four codes to fp16: with the sign bit flipped a code c is the byte c + 128; 0x6400 | byte is the fp16
+// 1024 + byte (fp16 counts by ones from 1024 to 2048), and subtracting 1152 is exact.
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = codes ^ 0x80808080u;
+  lo = __byte_perm(u, 0x64646464u, 0x4140);
+  hi = __byte_perm(u, 0x64646464u, 0x4342);
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+}
+
+// One grouped product. Segment e < n_mat holds positions [offsets[e], offsets[e + 1]) (offsets
+// NULL: all `rows`); with shared experts, segment n_mat + s is positions
+// [rows + s * T, rows + (s + 1) * T). The activations' codes are held in fp16 (exact), row p for
+// position p, except that the SwiGLU pass's shared experts all read rows [rows, rows + T).
 struct Int8Gemm {
-  const int8_t* qx;        // A rows [.., K]
-  const float* sx;
+  const uint16_t* xq;      // [x_rows, K] fp16
+  const float* sx;         // [x_rows]
+  long long x_rows;
   const int8_t *qw, *qw2;  // [n_mat, N, K]; qw2: the up projection of the SwiGLU pass
   const float *sw, *sw2;
   const int8_t *sh_qw, *sh_qw2;  // shared experts [S, N, K]
   const float *sh_sw, *sh_sw2;
   const int32_t* offsets;
-  const int32_t* perm_slot;  // SwiGLU and slot passes: position -> slot (slot / k is the token)
+  const int32_t* perm_slot;  // slot pass: position -> slot
   const float* topk_w;       // slot pass: gate per slot (NULL: 1)
   void* out;
   int* status;
-  int rows, K, N, n_mat, S, T, k;
+  int rows, K, N, n_mat, S, T;
   int out_dtype;             // matrix pass
 };
 
@@ -51,5 +64,16 @@ cudaError_t launch_quantize_rows(int T, int d, int dtype, const void* x, long lo
                                  float* scale, cudaStream_t st);
 cudaError_t launch_quantize_channels(int n_mat, int K, int N, const uint16_t* W, int8_t* q,
                                      float* scale, cudaStream_t st);
+// fp16 copies of int8 codes (n a multiple of 16; both 16-byte aligned).
+cudaError_t launch_widen_codes(const int8_t* q, uint16_t* xq, long long n, cudaStream_t st);
+// The FFN's activations in expert order: rows [0, TK) from the token of slot perm_slot[p] (written
+// for p < offsets[E]; a slot outside [0, TK) becomes a zero row and MOE_DEVFAULT_BAD_TILE), then,
+// with shared experts, rows [TK, TK + T) from every token. Codes in fp16.
+cudaError_t launch_quantize_gather(const Shape& s, const uint16_t* x, const int32_t* perm_slot,
+                                   const int32_t* offsets, uint16_t* xq, float* sx, int* status,
+                                   cudaStream_t st);
+// H [rows, f] fp32 to fp16 codes and scales; positions in [offsets[E], TK) are skipped.
+cudaError_t launch_quantize_hidden(const Shape& s, const float* h, const int32_t* offsets,
+                                   uint16_t* hq, float* sh, cudaStream_t st);
 
 }  // namespace moe

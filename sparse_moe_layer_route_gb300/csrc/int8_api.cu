@@ -30,7 +30,7 @@ moe_status check_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat) {
 
 // Buffers of one FFN call.
 struct FfnLayout {
-  size_t qx, sx, h, qh, sh, total;
+  size_t xq, sx, h, hq, sh, total;
 };
 FfnLayout ffn_layout(const Shape& s) {
   FfnLayout L;
@@ -40,12 +40,13 @@ FfnLayout ffn_layout(const Shape& s) {
     o = (o + bytes + 255) / 256 * 256;
     return at;
   };
-  L.qx = take((size_t)s.T * s.d);
-  L.sx = take(4ull * s.T);
+  const size_t x_rows = s.TK + (s.S > 0 ? s.T : 0);
+  L.xq = take(2ull * x_rows * s.d);
+  L.sx = take(4ull * x_rows);
   // fp32: an fp16 H (2^-12 of the value) would move about 1 code in 150 by one when H is quantized
   // (3.5e-3 of the layer output's norm measured), fp32 moves none to speak of
   L.h = take(4ull * s.rows * s.f);
-  L.qh = take((size_t)s.rows * s.f);
+  L.hq = take(2ull * s.rows * s.f);
   L.sh = take(4ull * s.rows);
   L.total = o;
   return L;
@@ -90,7 +91,7 @@ moe_status moe_int8_matmul_workspace_size(int32_t rows, int32_t K, int32_t N, in
   const moe_status r = check_matmul(rows, K, N, n_mat);
   if (r != MOE_OK) return r;
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-  *bytes = kHead;
+  *bytes = kHead + ((size_t)rows * K * 2 + 255) / 256 * 256;
   return MOE_OK;
 }
 
@@ -109,8 +110,13 @@ moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, co
   size_t need = 0;
   moe_int8_matmul_workspace_size(rows, K, N, n_mat, &need);
   if ((r = check_ws(ws, ws_bytes, need)) != MOE_OK) return r;
+  const cudaStream_t st = (cudaStream_t)stream;
+  uint16_t* xq = at<uint16_t>(ws, kHead);
+  const cudaError_t e = launch_widen_codes(q_x, xq, (long long)rows * K, st);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
   Int8Gemm g = {};
-  g.qx = q_x;
+  g.xq = xq;
+  g.x_rows = rows;
   g.sx = s_x;
   g.qw = q_w;
   g.sw = s_w;
@@ -123,8 +129,7 @@ moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, co
   g.N = N;
   g.n_mat = n_mat;
   g.T = 1;
-  g.k = 1;
-  return cuda_status(launch_int8_gemm(kInt8Matrix, g, (cudaStream_t)stream));
+  return cuda_status(launch_int8_gemm(kInt8Matrix, g, st));
 }
 
 moe_status moe_grouped_ffn_int8_workspace_size(const moe_config* cfg, size_t* bytes) {
@@ -155,10 +160,12 @@ moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const 
   const Shape s = make_shape(*cfg);
   const FfnLayout L = ffn_layout(s);
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = launch_quantize_rows(s.T, s.d, MOE_DTYPE_BF16, x, s.d, at<int8_t>(ws, L.qx),
-                                       at<float>(ws, L.sx), st);
+  int* status = at<int>(ws, 0);
+  cudaError_t e = launch_quantize_gather(s, x, perm_slot, offsets, at<uint16_t>(ws, L.xq),
+                                         at<float>(ws, L.sx), status, st);
   Int8Gemm g = {};
-  g.qx = at<int8_t>(ws, L.qx);
+  g.xq = at<uint16_t>(ws, L.xq);
+  g.x_rows = s.TK + (s.S > 0 ? s.T : 0);
   g.sx = at<float>(ws, L.sx);
   g.qw = w->gate.q;
   g.sw = w->gate.scale;
@@ -169,23 +176,22 @@ moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const 
   g.sh_qw2 = w->sh_up.q;
   g.sh_sw2 = w->sh_up.scale;
   g.offsets = offsets;
-  g.perm_slot = perm_slot;
   g.out = at<float>(ws, L.h);
-  g.status = at<int>(ws, 0);
+  g.status = status;
   g.rows = (int)s.TK;
   g.K = s.d;
   g.N = s.f;
   g.n_mat = s.E;
   g.S = s.S;
   g.T = s.T;
-  g.k = s.k;
   if (e == cudaSuccess) e = launch_int8_gemm(kInt8SwiGLU, g, st);
-  // every row of H, those past the last kept position included: they are not read after this
   if (e == cudaSuccess)
-    e = launch_quantize_rows((int)s.rows, s.f, MOE_DTYPE_F32, at<float>(ws, L.h), s.f,
-                             at<int8_t>(ws, L.qh), at<float>(ws, L.sh), st);
-  g.qx = at<int8_t>(ws, L.qh);
+    e = launch_quantize_hidden(s, at<float>(ws, L.h), offsets, at<uint16_t>(ws, L.hq),
+                               at<float>(ws, L.sh), st);
+  g.xq = at<uint16_t>(ws, L.hq);
+  g.x_rows = s.rows;
   g.sx = at<float>(ws, L.sh);
+  g.perm_slot = perm_slot;
   g.qw = w->down.q;
   g.sw = w->down.scale;
   g.qw2 = nullptr;

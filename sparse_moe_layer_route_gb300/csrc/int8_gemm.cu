@@ -1,6 +1,27 @@
-// Grouped products of 8-bit integers over row segments, with a scale per row and per output channel.
+// Grouped products of 8-bit integers over row segments, with a scale per row and per output channel,
+// on the 5th-generation tensor cores.
 //
-// A CTA computes 64 rows x 64 channels with 4-way integer dot products, exact in 32-bit integers.
+//   D[channel, row] = sum_k qw[channel, k] * xq[row, k],  out[row, channel] = D * sx[row] * sw[channel]
+//
+// sm_103a's 8-bit integer tensor rate is far below its 16-bit one, so the codes are multiplied as fp16:
+// whole numbers up to 128 are exact there, their products are exact, and fp32 sums of them are exact
+// below 2^24. The weights stay 8-bit in memory and in shared memory; they are widened on the way to the
+// MMA, whose A operand they are (M = 128 output channels) out of tensor memory. That costs the tile no
+// shared-memory writes and leaves the 16-bit B operand (the rows, widened once per call) as the only
+// matrix the MMA reads from shared memory.
+//
+// One persistent CTA per SM, a unit = two 128-channel tiles (SwiGLU pass: the gate and the up projection
+// of the same channels) x up to NT rows of one segment:
+//   warp 0       TMA producer, 128 k per stage: two [128 channels x 128 B] code tiles and two
+//                [NT rows x 64 k] fp16 tiles, all 128-byte swizzled
+//   warp 1       MMA issuer: M = 128, N = the unit's rows rounded up to 16, K = 16
+//   warp 2       TMEM allocator
+//   warps 4-7    epilogue: scales, SwiGLU or gate weight, stores (32 channels of a row per warp)
+//   warps 8-15   widen the codes, four warps per channel tile: 64 codes of a thread's channel from
+//                shared memory to 32 TMEM columns (a slot of 64 k for both tiles is 64 columns)
+// Units go expert by expert, channel tile by channel tile, rows innermost, so CTAs that run together
+// share each weight tile through L2. Every wait is bounded (MOE_DEVFAULT_PIPELINE_TIMEOUT on expiry).
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -8,13 +29,29 @@
 
 #include "int8.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTM = 64, kTN = 64, kTK = 64;  // rows, channels, codes per step
-constexpr int kLd = kTK / 4 + 1;             // words per staged row (odd: no bank conflicts)
+constexpr int kThreads = 512;
+constexpr int kCh = 128;                 // channels per tile (MMA M)
+constexpr int kStageK = 128;             // k per shared-memory stage
+constexpr int kABytes = kCh * kStageK;   // 16 KB per channel tile
+constexpr int kMaxSegs = 256 + 4;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
+
+// NB accumulator buffers of 2 NT columns, SA slots of widened weights of 64 columns.
+template <int NT, int NB, int SA>
+struct Cfg {
+  static constexpr int kBBytes = NT * kStageK * 2;
+  static constexpr int kStageBytes = 2 * kABytes + kBBytes;
+  static constexpr int kStages = 218 * 1024 / kStageBytes > 6 ? 6 : 218 * 1024 / kStageBytes;
+  static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
+  static constexpr int kACol = NB * 2 * NT;  // first column of the weight slots
+  static_assert(kACol + SA * 64 <= 512, "TMEM columns");
+  static_assert(NT % 16 == 0, "MMA N; B sub-tiles stay 1024-byte aligned");
+};
 
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 constexpr uint32_t kF16Clamp = 0x477FF000u;  // 65520.0f: the first value past fp16's range
@@ -25,163 +62,473 @@ __device__ __forceinline__ uint16_t f16_sat(float v) {
   return (uint16_t)r;
 }
 
-template <int PASS>
-__global__ void __launch_bounds__(kThreads) int8_gemm_kernel(const Int8Gemm g) {
-  constexpr bool PAIR = PASS == kInt8SwiGLU;
-  __shared__ int xs[kTM][kLd], ws[PAIR ? 2 : 1][kTN][kLd];
-  __shared__ int seg_expert, seg_row0, seg_rows;
-  griddep_wait();
-  // which segment the row tile blockIdx.y belongs to
-  if (threadIdx.x == 0) {
-    int tile = blockIdx.y, e = 0;
-    seg_expert = -1;
-    for (; e < g.n_mat + g.S; ++e) {
-      int r0 = 0, r1 = g.rows;
-      if (e >= g.n_mat) {
-        r0 = g.rows + (e - g.n_mat) * g.T;
-        r1 = r0 + g.T;
-      } else if (g.offsets != nullptr) {
-        r0 = g.offsets[e];
-        r1 = g.offsets[e + 1];
-        if (r0 < 0 || r1 < r0 || r1 > g.rows) {
-          atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
-          r1 = r0 = 0;
-        }
+struct Unit {
+  int seg;      // expert, or n_mat + shared expert
+  int ct;       // channel tile pair
+  int row0;     // first position
+  int rows;     // 1..NT
+  int brow0;    // first row of the activations
+};
+
+// Row tiles before each segment (first[n_segs] = all of them) and the segments' first positions.
+struct SegTable {
+  int first[kMaxSegs + 1];
+  int row0[kMaxSegs];
+  int rows[kMaxSegs];
+  int warp_tot[kThreads / 32];
+};
+
+// Called by every thread of the CTA.
+__device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, int NT) {
+  const int n = g.n_mat + g.S, i = threadIdx.x;
+  const int lane = i & 31, warp = i >> 5;
+  int r0 = 0, nr = 0;
+  if (i < g.n_mat) {
+    int r1 = g.rows;
+    if (g.offsets != nullptr) {
+      r0 = g.offsets[i];
+      r1 = g.offsets[i + 1];
+      if (r0 < 0 || r1 < r0 || r1 > g.rows) {
+        atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
+        r0 = r1 = 0;
       }
-      const int nt = (r1 - r0 + kTM - 1) / kTM;
-      if (tile < nt) {
-        seg_expert = e;
-        seg_row0 = r0 + tile * kTM;
-        seg_rows = min(kTM, r1 - seg_row0);
-        break;
-      }
-      tile -= nt;
     }
+    nr = r1 - r0;
+  } else if (i < n) {
+    r0 = g.rows + (i - g.n_mat) * g.T;
+    nr = g.T;
+  }
+  const int nt = (nr + NT - 1) / NT;
+  int v = nt;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) t.warp_tot[warp] = v;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += t.warp_tot[w];
+  if (i < n) {
+    t.first[i] = base + v - nt;
+    t.row0[i] = r0;
+    t.rows[i] = nr;
+    if (i == n - 1) t.first[n] = base + v;
   }
   __syncthreads();
-  if (seg_expert < 0) return;
-  const bool sh = seg_expert >= g.n_mat;
-  const long long ex = sh ? seg_expert - g.n_mat : seg_expert;
-  const int n0 = blockIdx.x * kTN;
-  const int8_t* w1 = (sh ? g.sh_qw : g.qw) + ex * g.N * g.K;
-  const int8_t* w2 = PAIR ? (sh ? g.sh_qw2 : g.qw2) + ex * g.N * g.K : nullptr;
-  // this thread stages 16 codes of one row per step: row threadIdx.x / 4, piece threadIdx.x % 4
-  const int lr = threadIdx.x >> 2, lc = threadIdx.x & 3;
-  long long xrow = -1;
-  if (lr < seg_rows) {
-    xrow = seg_row0 + lr;
-    if (PASS == kInt8SwiGLU) {
-      if (sh) {
-        xrow = (xrow - g.rows) % g.T;
-      } else {
-        const int slot = g.perm_slot[xrow];
-        if (slot < 0 || slot >= g.rows) {
-          atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
-          xrow = -1;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ Unit find_unit(const SegTable& t, const Int8Gemm& g, int n_ct, int NT,
+                                          long long w) {
+  int lo = 0, hi = g.n_mat + g.S;  // first[lo] * n_ct <= w < first[hi] * n_ct
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((long long)t.first[mid] * n_ct <= w)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int local = (int)(w - (long long)t.first[lo] * n_ct);
+  const int nt = t.first[lo + 1] - t.first[lo];
+  Unit u;
+  u.seg = lo;
+  u.ct = local / nt;
+  const int off = (local - u.ct * nt) * NT;
+  u.row0 = t.row0[lo] + off;
+  u.rows = min(NT, t.rows[lo] - off);
+  // the SwiGLU pass's shared experts read the same rows of x
+  u.brow0 = PAIR && lo >= g.n_mat ? g.rows + off : u.row0;
+  return u;
+}
+
+template <int PASS, int NT, int NB, int SA>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_gemm_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmA2,
+                     const __grid_constant__ CUtensorMap tmShA,
+                     const __grid_constant__ CUtensorMap tmShA2, const Int8Gemm g) {
+  using C = Cfg<NT, NB, SA>;
+  constexpr bool PAIR = PASS == kInt8SwiGLU;
+  constexpr int STAGES = C::kStages;
+  constexpr int UCH = PAIR ? kCh : 2 * kCh;  // output channels per unit
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ SegTable segs;
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const uint32_t bar0 = base + STAGES * C::kStageBytes;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto afull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
+  auto aempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + SA + s); };
+  auto dfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 * SA + b); };
+  auto dempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 * SA + NB + b); };
+  constexpr int kBars = 2 * STAGES + 2 * SA + 2 * NB;
+  const uint32_t mma_done_bar = bar0 + 8u * kBars;
+  static_assert(8 * (kBars + 1) + 8 <= 256, "barrier block");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + STAGES * C::kStageBytes + 8 * (kBars + 1));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 9);  // eight widening warps and the MMAs
+    }
+    for (int s = 0; s < SA; ++s) {
+      ptx::mbar_init(afull_bar(s), 8);
+      ptx::mbar_init(aempty_bar(s), 1);
+    }
+    for (int b = 0; b < NB; ++b) {
+      ptx::mbar_init(dfull_bar(b), 1);
+      ptx::mbar_init(dempty_bar(b), 4);
+    }
+    ptx::mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    ptx::fence_mbarrier_init();
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
+    if (PAIR) ptx::prefetch_tmap(&tmA2);
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  griddep_wait();  // everything above touched only shared memory, TMEM and parameters
+  build_segments(segs, g, NT);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int n_ct = (g.N + UCH - 1) / UCH;
+  const int n_sub = (g.K + 63) / 64;           // 64-k slots per unit
+  const int n_stage = (n_sub + 1) / 2;         // 128-k stages per unit
+  const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, last_parity = 0;  // per stage: ever issued, its parity
+      bool ok = true;
+      for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
+        const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
+        const bool sh = u.seg >= g.n_mat;
+        const int ex = sh ? u.seg - g.n_mat : u.seg;
+        const CUtensorMap* a0 = sh ? &tmShA : &tmA;
+        const CUtensorMap* a1 = PAIR ? (sh ? &tmShA2 : &tmA2) : a0;
+        const int ch0 = u.ct * UCH, ch1 = PAIR ? ch0 : ch0 + kCh;
+        const bool two = ch1 < g.N;
+        for (int i = 0; i < n_stage; ++i) {
+          if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, g.status,
+                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sA = base + stage * C::kStageBytes, sB = sA + 2 * kABytes;
+          const uint32_t fb = full_bar(stage);
+          const bool half = 2 * i + 1 < n_sub;  // the stage's second 64 k hold something
+          ptx::mbar_arrive_expect_tx(
+              fb, (two ? 2 : 1) * kABytes + (half ? C::kBBytes : C::kBBytes / 2));
+          ptx::tma_load_3d(sA, a0, fb, i * kStageK, ch0, ex);
+          if (two) ptx::tma_load_3d(sA + kABytes, a1, fb, i * kStageK, ch1, ex);
+          ptx::tma_load_2d(sB, &tmB, fb, i * kStageK, u.brow0);
+          if (half) ptx::tma_load_2d(sB + C::kBBytes / 2, &tmB, fb, i * kStageK + 64, u.brow0);
+          issued |= 1u << stage;
+          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // never leave while a copy into this CTA's shared memory may still be in flight
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) {
+          volatile int no_abort = 0;
+          ptx::mbar_wait_bounded(full_bar(s), (last_parity >> s) & 1u, &no_abort, g.status,
+                                 MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs / 4);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      int stage = 0, slot = 0, acc = 0;
+      uint32_t phase = 0, slot_phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
+        const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
+        const bool two = PAIR || u.ct * UCH + kCh < g.N;
+        const uint32_t idesc =
+            ptx::idesc_f16kind_f32(kCh, (uint32_t)((u.rows + 15) & ~15), 0, 0, 0u);
+        if (!ptx::mbar_wait_bounded(dempty_bar(acc), acc_phase ^ 1u, abort_flag, g.status,
+                                    MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs))
+          break;
+        ptx::tc_fence_after();
+        const uint32_t d0 = tmem_base + (uint32_t)(acc * 2 * NT), d1 = d0 + NT;
+        for (int i = 0; i < n_stage && ok; ++i) {
+          if (!ptx::mbar_wait_bounded(full_bar(stage), phase, abort_flag, g.status,
+                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sB = base + stage * C::kStageBytes + 2 * kABytes;
+          for (int h = 0; h < 2 && 2 * i + h < n_sub; ++h) {
+            if (!ptx::mbar_wait_bounded(afull_bar(slot), slot_phase, abort_flag, g.status,
+                                        MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t a0 = tmem_base + C::kACol + slot * 64;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              // B: K-major, 128 B rows, 8-row groups 1024 B apart; a K step of 16 = +32 B
+              const uint64_t bdesc =
+                  ptx::smem_desc_sw128(sB + h * (C::kBBytes / 2) + kk * 32, 16, 1024);
+              const uint32_t more = (i | h | kk) != 0 ? 1u : 0u;
+              ptx::umma_f16_ta(d0, a0 + kk * 8, bdesc, idesc, more);
+              if (two) ptx::umma_f16_ta(d1, a0 + 32 + kk * 8, bdesc, idesc, more);
+            }
+            ptx::umma_commit(aempty_bar(slot));
+            if (++slot == SA) {
+              slot = 0;
+              slot_phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          ptx::umma_commit(empty_bar(stage));
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::umma_commit(dfull_bar(acc));
+        if (++acc == NB) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      // all MMAs issued by this thread have finished before TMEM is released
+      ptx::umma_commit(mma_done_bar);
+      volatile int no_abort = 0;
+      ptx::mbar_wait_bounded(mma_done_bar, 0, &no_abort, g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
+                             kWaitLimitNs / 4);
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ widening warps
+    const int tile = (warp - 8) >> 2, q = warp & 3;  // channel tile; TMEM lanes [32 q, 32 q + 32)
+    const int row = 32 * q + lane;
+    int stage = 0, slot = 0;
+    uint32_t phase = 0, slot_phase = 0;
+    bool ok = true;
+    for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
+      const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
+      const bool on = PAIR || tile == 0 || u.ct * UCH + kCh < g.N;
+      for (int i = 0; i < n_stage && ok; ++i) {
+        if (!ptx::mbar_wait_bounded_warp(full_bar(stage), phase, abort_flag, g.status,
+                                         MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = gbase + stage * C::kStageBytes + tile * kABytes + row * kStageK;
+        for (int h = 0; h < 2 && 2 * i + h < n_sub; ++h) {
+          uint32_t r[32];
+          if (on) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              // 16-byte piece 4 h + c of the row sits at piece (4 h + c) ^ (row mod 8)
+              const uint4 v =
+                  *reinterpret_cast<const uint4*>(src + (((4 * h + c) ^ (row & 7)) << 4));
+              widen4(v.x, r[8 * c], r[8 * c + 1]);
+              widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+              widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+              widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+            }
+          }
+          if (h == 1 || 2 * i + 1 == n_sub) {  // the stage's codes are in registers
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(empty_bar(stage));
+          }
+          if (!ptx::mbar_wait_bounded_warp(aempty_bar(slot), slot_phase ^ 1u, abort_flag, g.status,
+                                           MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          if (on) {
+            ptx::tc_fence_after();
+            ptx::tmem_st_32x32b_x32(tmem_base + ((uint32_t)(32 * q) << 16) +
+                                        (uint32_t)(C::kACol + slot * 64 + tile * 32),
+                                    r);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(afull_bar(slot));
+          if (++slot == SA) {
+            slot = 0;
+            slot_phase ^= 1u;
+          }
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ epilogue
+    constexpr int CW = NT % 32 == 0 ? 32 : 16;  // columns (rows of the output) per step
+    const int q = warp - 4;
+    int acc = 0;
+    uint32_t acc_phase = 0, clamp = 0u;
+    for (long long w = blockIdx.x; w < total; w += gridDim.x) {
+      const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
+      const bool sh = u.seg >= g.n_mat;
+      const long long ex = sh ? u.seg - g.n_mat : u.seg;
+      const int ch0 = u.ct * UCH + 32 * q + lane, ch1 = PAIR ? ch0 : ch0 + kCh;
+      const bool in0 = ch0 < g.N, in1 = ch1 < g.N;
+      const float* sw = (sh ? g.sh_sw : g.sw) + ex * g.N;
+      const float* sw2 = PAIR ? (sh ? g.sh_sw2 : g.sw2) + ex * g.N : sw;
+      const float w0 = in0 ? sw[ch0] : 0.0f, w1 = in1 ? sw2[ch1] : 0.0f;
+      // lane c holds the scale and the output row of column c of each step
+      float sx[NT / CW];
+      int orow[NT / CW];
+#pragma unroll
+      for (int c = 0; c < NT / CW; ++c) {
+        const int r = c * CW + (lane & (CW - 1));
+        sx[c] = 0.0f;
+        orow[c] = -1;
+        if (r < u.rows) {
+          sx[c] = g.sx[u.brow0 + r];
+          orow[c] = u.row0 + r;
+          if (PASS == kInt8Slot && !sh) {
+            const int slot = g.perm_slot[u.row0 + r];
+            const bool good = slot >= 0 && slot < g.rows;
+            orow[c] = good ? slot : -1;
+            if (good && g.topk_w != nullptr) sx[c] *= g.topk_w[slot];
+          }
+        }
+      }
+      if (!ptx::mbar_wait_bounded_warp(dfull_bar(acc), acc_phase, abort_flag, g.status,
+                                       MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs))
+        break;
+      ptx::tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * 2 * NT);
+#pragma unroll
+      for (int c = 0; c < NT / CW; ++c) {
+        if (c * CW >= u.rows) break;
+        uint32_t v0[CW], v1[CW];
+        if constexpr (CW == 32) {
+          ptx::tmem_ld_32x32b_x32(taddr + c * CW, v0);
+          ptx::tmem_ld_32x32b_x32(taddr + NT + c * CW, v1);
         } else {
-          xrow = slot / g.k;
+          ptx::tmem_ld_32x32b_x16(taddr + c * CW, v0);
+          ptx::tmem_ld_32x32b_x16(taddr + NT + c * CW, v1);
+        }
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < CW; ++j) {
+          const int to = __shfl_sync(0xffffffffu, orow[c], j);
+          const float s = __shfl_sync(0xffffffffu, sx[c], j);
+          if (to < 0) continue;  // past the segment, or a slot out of range
+          const long long at = (long long)to * g.N;
+          float y0 = __uint_as_float(v0[j]) * (s * w0), y1 = __uint_as_float(v1[j]) * (s * w1);
+          if (PASS == kInt8SwiGLU) {
+            if (in0) static_cast<float*>(g.out)[at + ch0] = y0 / (1.0f + __expf(-y0)) * y1;
+          } else if (PASS == kInt8Slot) {
+            uint16_t* y = static_cast<uint16_t*>(g.out) + at;
+            if (in0) {
+              y[ch0] = f16_sat(y0);
+              clamp = max(clamp, mag_bits(y0));
+            }
+            if (in1) {
+              y[ch1] = f16_sat(y1);
+              clamp = max(clamp, mag_bits(y1));
+            }
+          } else if (g.out_dtype == MOE_DTYPE_F32) {
+            float* y = static_cast<float*>(g.out) + at;
+            if (in0) y[ch0] = y0;
+            if (in1) y[ch1] = y1;
+          } else if (g.out_dtype == MOE_DTYPE_BF16) {
+            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(g.out) + at;
+            if (in0) y[ch0] = __float2bfloat16(y0);
+            if (in1) y[ch1] = __float2bfloat16(y1);
+          } else {
+            __half* y = static_cast<__half*>(g.out) + at;
+            if (in0) y[ch0] = __float2half(y0);
+            if (in1) y[ch1] = __float2half(y1);
+          }
         }
       }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(dempty_bar(acc));
+      if (++acc == NB) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
     }
+    if (PASS == kInt8Slot && __any_sync(0xffffffffu, clamp >= kF16Clamp) && lane == 0)
+      atomicOr(g.status, MOE_DEVFAULT_FP16_RANGE);
   }
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[PAIR ? 2 : 1][4][4] = {};
-  for (int k0 = 0; k0 < g.K; k0 += kTK) {
-    const int kk = k0 + lc * 16;
-    int4 v = make_int4(0, 0, 0, 0), u = v, u2 = v;
-    if (kk < g.K) {
-      if (xrow >= 0) v = *reinterpret_cast<const int4*>(g.qx + xrow * g.K + kk);
-      if (n0 + lr < g.N) {
-        u = *reinterpret_cast<const int4*>(w1 + (long long)(n0 + lr) * g.K + kk);
-        if (PAIR) u2 = *reinterpret_cast<const int4*>(w2 + (long long)(n0 + lr) * g.K + kk);
-      }
-    }
-    __syncthreads();
-    const int c = lc * 4;
-    xs[lr][c] = v.x, xs[lr][c + 1] = v.y, xs[lr][c + 2] = v.z, xs[lr][c + 3] = v.w;
-    ws[0][lr][c] = u.x, ws[0][lr][c + 1] = u.y, ws[0][lr][c + 2] = u.z, ws[0][lr][c + 3] = u.w;
-    if (PAIR) {
-      int(*w)[kLd] = ws[PAIR ? 1 : 0];
-      w[lr][c] = u2.x, w[lr][c + 1] = u2.y, w[lr][c + 2] = u2.z, w[lr][c + 3] = u2.w;
-    }
-    __syncthreads();
-#pragma unroll 4
-    for (int kw = 0; kw < kTK / 4; ++kw) {
-      int av[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) av[i] = xs[ty + 16 * i][kw];
-#pragma unroll
-      for (int m = 0; m < (PAIR ? 2 : 1); ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int bv = ws[m][tx + 16 * j][kw];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][i][j] = __dp4a(av[i], bv, acc[m][i][j]);
-        }
-    }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, 512);
   }
-  uint32_t mx = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty + 16 * i;
-    if (r >= seg_rows) continue;
-    const long long p = seg_row0 + r;
-    long long orow = p, srow = p;
-    float gate = 1.0f;
-    if (PASS != kInt8Matrix) {
-      if (sh) {
-        srow = PASS == kInt8SwiGLU ? (p - g.rows) % g.T : p;
-      } else {
-        const int slot = g.perm_slot[p];
-        if (slot < 0 || slot >= g.rows) continue;
-        if (PASS == kInt8SwiGLU) srow = slot / g.k;
-        if (PASS == kInt8Slot) {
-          orow = slot;
-          if (g.topk_w != nullptr) gate = g.topk_w[slot];
-        }
-      }
-    }
-    const float sx = g.sx[srow];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx + 16 * j;
-      if (n >= g.N) continue;
-      float v = (float)acc[0][i][j] * (sx * (sh ? g.sh_sw : g.sw)[ex * g.N + n]);
-      const long long at = orow * g.N + n;
-      if (PASS == kInt8Matrix) {
-        if (g.out_dtype == MOE_DTYPE_F32)
-          static_cast<float*>(g.out)[at] = v;
-        else if (g.out_dtype == MOE_DTYPE_BF16)
-          static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16(v);
-        else
-          static_cast<__half*>(g.out)[at] = __float2half(v);
-        continue;
-      }
-      if (PASS == kInt8SwiGLU) {
-        const float up =
-            (float)acc[PAIR ? 1 : 0][i][j] * (sx * (sh ? g.sh_sw2 : g.sw2)[ex * g.N + n]);
-        static_cast<float*>(g.out)[at] = v / (1.0f + __expf(-v)) * up;
-        continue;
-      }
-      v *= gate;
-      mx = max(mx, mag_bits(v));
-      static_cast<uint16_t*>(g.out)[at] = f16_sat(v);
-    }
+}
+
+template <int PASS, int NT, int NB, int SA>
+cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
+  using C = Cfg<NT, NB, SA>;
+  constexpr CUtensorMapDataType kCode = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUtensorMap b, a, a2, sa, sa2;
+  bool ok = make_tmap_2d(&b, g.xq, g.x_rows, g.K, 64, NT, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) &&
+            make_tmap_3d(&a, g.qw, g.n_mat, g.N, g.K, kStageK, kCh, kCode, 1);
+  a2 = a;
+  if (ok && PASS == kInt8SwiGLU)
+    ok = make_tmap_3d(&a2, g.qw2, g.n_mat, g.N, g.K, kStageK, kCh, kCode, 1);
+  sa = a;
+  sa2 = a2;
+  if (ok && g.S > 0) {
+    ok = make_tmap_3d(&sa, g.sh_qw, g.S, g.N, g.K, kStageK, kCh, kCode, 1);
+    if (ok && PASS == kInt8SwiGLU)
+      ok = make_tmap_3d(&sa2, g.sh_qw2, g.S, g.N, g.K, kStageK, kCh, kCode, 1);
   }
-  if (PASS == kInt8Slot && mx >= kF16Clamp) atomicOr(g.status, MOE_DEVFAULT_FP16_RANGE);
+  if (!ok) return cudaErrorInvalidValue;
+  auto kern = int8_gemm_kernel<PASS, NT, NB, SA>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(num_sms()), dim3(kThreads), C::kSmemBytes, st, b, a, a2, sa, sa2, g);
+}
+
+template <int PASS>
+cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
+  // rows per segment on average (an even spread): short segments leave most of a wide tile empty, and
+  // a narrow one leaves shared memory for more weight tiles in flight
+  const long long mean = g.rows / g.n_mat;
+  if (mean <= 32) return launch_one<PASS, 32, 2, 6>(g, st);
+  return launch_one<PASS, 96, 2, 2>(g, st);
 }
 
 }  // namespace
 
 cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st) {
-  const long long tiles =
-      g.rows / kTM + g.n_mat + (long long)g.S * ((g.T + kTM - 1) / kTM);  // an upper bound
-  if (tiles > 65535) return cudaErrorInvalidValue;
-  const dim3 grid((g.N + kTN - 1) / kTN, (unsigned)tiles), block(kThreads);
   switch (pass) {
-    case kInt8Matrix: return launch_k(int8_gemm_kernel<kInt8Matrix>, grid, block, 0, st, g);
-    case kInt8SwiGLU: return launch_k(int8_gemm_kernel<kInt8SwiGLU>, grid, block, 0, st, g);
-    default: return launch_k(int8_gemm_kernel<kInt8Slot>, grid, block, 0, st, g);
+    case kInt8Matrix: return launch_pass<kInt8Matrix>(g, st);
+    case kInt8SwiGLU: return launch_pass<kInt8SwiGLU>(g, st);
+    default: return launch_pass<kInt8Slot>(g, st);
   }
 }
 

@@ -245,9 +245,10 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
 // 2-D over a row-major [rows, cols] 16-bit matrix with a box of box_cols (inner) x box_rows.
 bool make_tmap_2d(CUtensorMap* m, const void* ptr, long long rows, long long cols, int box_cols,
                   int box_rows, CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
-// 3-D over a row-major [n, rows, cols] 16-bit tensor with a box of box_cols x box_rows x 1.
+// 3-D over a row-major [n, rows, cols] tensor (elem_bytes each) with a box of
+// box_cols x box_rows x 1.
 bool make_tmap_3d(CUtensorMap* m, const void* ptr, long long n, long long rows, long long cols,
                   int box_cols, int box_rows,
-                  CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+                  CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, int elem_bytes = 2);
 
 }  // namespace moe
