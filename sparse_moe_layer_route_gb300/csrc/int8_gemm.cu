@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       // ---------------------------------------------------------------- TMA producer
       int stage = 0;
       uint32_t phase = 0, issued = 0, last_parity = 0;  // per stage: ever issued, its parity
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (ptx::elect_one()) {
       // ---------------------------------------------------------------- MMA issuer
       int stage = 0, slot = 0, acc = 0;
       uint32_t phase = 0, slot_phase = 0, acc_phase = 0;
