@@ -59,6 +59,7 @@ enum Int8Pass {
   kInt8Slot = 2     // out [slot, N] fp16 = gate weight * product
 };
 
+cudaError_t launch_int8_gemm_pair(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
 cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
 cudaError_t launch_quantize_rows(int T, int d, int dtype, const void* x, long long ld, int8_t* q,
                                  float* scale, cudaStream_t st);

@@ -28,122 +28,30 @@
 #include <cstdint>
 
 #include "int8.cuh"
+#include "int8_units.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kCh = 128;                 // channels per tile (MMA M)
-constexpr int kStageK = 128;             // k per shared-memory stage
-constexpr int kABytes = kCh * kStageK;   // 16 KB per channel tile
-constexpr int kMaxSegs = 256 + 4;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
+constexpr int kABytes = kInt8Ch * kInt8StageK;   // 16 KB per channel tile
 
 // NB accumulator buffers of 2 NT columns, SA slots of widened weights of 64 columns.
 template <int NT, int NB, int SA>
 struct Cfg {
-  static constexpr int kBBytes = NT * kStageK * 2;
+  static constexpr int kBBytes = NT * kInt8StageK * 2;
   static constexpr int kStageBytes = 2 * kABytes + kBBytes;
-  static constexpr int kStages = 218 * 1024 / kStageBytes > 6 ? 6 : 218 * 1024 / kStageBytes;
-  static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
+  static constexpr int kStages = 204 * 1024 / kStageBytes > 6 ? 6 : 204 * 1024 / kStageBytes;
+  static constexpr int kSmemBytes =
+      kStages * kStageBytes + 2 * kInt8StepBytes + 1024 /*align*/ + 256 /*barriers*/;
   static constexpr int kACol = NB * 2 * NT;  // first column of the weight slots
   static_assert(kACol + SA * 64 <= 512, "TMEM columns");
-  static_assert(NT % 16 == 0, "MMA N; B sub-tiles stay 1024-byte aligned");
+  static_assert(NT % 32 == 0, "epilogue steps; B sub-tiles stay 1024-byte aligned");
 };
 
-__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-constexpr uint32_t kF16Clamp = 0x477FF000u;  // 65520.0f: the first value past fp16's range
-
-__device__ __forceinline__ uint16_t f16_sat(float v) {
-  uint32_t r;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(v));
-  return (uint16_t)r;
-}
-
-struct Unit {
-  int seg;      // expert, or n_mat + shared expert
-  int ct;       // channel tile pair
-  int row0;     // first position
-  int rows;     // 1..NT
-  int brow0;    // first row of the activations
-};
-
-// Row tiles before each segment (first[n_segs] = all of them) and the segments' first positions.
-struct SegTable {
-  int first[kMaxSegs + 1];
-  int row0[kMaxSegs];
-  int rows[kMaxSegs];
-  int warp_tot[kThreads / 32];
-};
-
-// Called by every thread of the CTA.
-__device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, int NT) {
-  const int n = g.n_mat + g.S, i = threadIdx.x;
-  const int lane = i & 31, warp = i >> 5;
-  int r0 = 0, nr = 0;
-  if (i < g.n_mat) {
-    int r1 = g.rows;
-    if (g.offsets != nullptr) {
-      r0 = g.offsets[i];
-      r1 = g.offsets[i + 1];
-      if (r0 < 0 || r1 < r0 || r1 > g.rows) {
-        atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
-        r0 = r1 = 0;
-      }
-    }
-    nr = r1 - r0;
-  } else if (i < n) {
-    r0 = g.rows + (i - g.n_mat) * g.T;
-    nr = g.T;
-  }
-  const int nt = (nr + NT - 1) / NT;
-  int v = nt;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  if (lane == 31) t.warp_tot[warp] = v;
-  __syncthreads();
-  int base = 0;
-  for (int w = 0; w < warp; ++w) base += t.warp_tot[w];
-  if (i < n) {
-    t.first[i] = base + v - nt;
-    t.row0[i] = r0;
-    t.rows[i] = nr;
-    if (i == n - 1) t.first[n] = base + v;
-  }
-  __syncthreads();
-}
-
-template <bool PAIR>
-__device__ __forceinline__ Unit find_unit(const SegTable& t, const Int8Gemm& g, int n_ct, int NT,
-                                          long long w) {
-  int lo = 0, hi = g.n_mat + g.S;  // first[lo] * n_ct <= w < first[hi] * n_ct
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((long long)t.first[mid] * n_ct <= w)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int local = (int)(w - (long long)t.first[lo] * n_ct);
-  const int nt = t.first[lo + 1] - t.first[lo];
-  Unit u;
-  u.seg = lo;
-  u.ct = local / nt;
-  const int off = (local - u.ct * nt) * NT;
-  u.row0 = t.row0[lo] + off;
-  u.rows = min(NT, t.rows[lo] - off);
-  // the SwiGLU pass's shared experts read the same rows of x
-  u.brow0 = PAIR && lo >= g.n_mat ? g.rows + off : u.row0;
-  return u;
-}
-
-template <int PASS, int NT, int NB, int SA>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int PASS, int OUT, int NT, int NB, int SA>
+__global__ void __launch_bounds__(kInt8Threads, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmA2,
                      const __grid_constant__ CUtensorMap tmShA,
@@ -151,14 +59,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<NT, NB, SA>;
   constexpr bool PAIR = PASS == kInt8SwiGLU;
   constexpr int STAGES = C::kStages;
-  constexpr int UCH = PAIR ? kCh : 2 * kCh;  // output channels per unit
+  constexpr int UCH = PAIR ? kInt8Ch : 2 * kInt8Ch;  // output channels per unit
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ SegTable segs;
+  __shared__ __align__(16) float unit_sx[2][NT];  // row scales, output rows of the epilogue's unit
+  __shared__ int unit_orow[2][NT];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
-  const uint32_t bar0 = base + STAGES * C::kStageBytes;
+  uint8_t* const stage_out = gbase + STAGES * C::kStageBytes;  // the epilogue's two steps
+  const uint32_t bar0 = base + STAGES * C::kStageBytes + 2 * kInt8StepBytes;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto afull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
@@ -168,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kBars = 2 * STAGES + 2 * SA + 2 * NB;
   const uint32_t mma_done_bar = bar0 + 8u * kBars;
   static_assert(8 * (kBars + 1) + 8 <= 256, "barrier block");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + STAGES * C::kStageBytes + 8 * (kBars + 1));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stage_out + 2 * kInt8StepBytes + 8 * (kBars + 1));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -221,11 +132,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ex = sh ? u.seg - g.n_mat : u.seg;
         const CUtensorMap* a0 = sh ? &tmShA : &tmA;
         const CUtensorMap* a1 = PAIR ? (sh ? &tmShA2 : &tmA2) : a0;
-        const int ch0 = u.ct * UCH, ch1 = PAIR ? ch0 : ch0 + kCh;
+        const int ch0 = u.ct * UCH, ch1 = PAIR ? ch0 : ch0 + kInt8Ch;
         const bool two = ch1 < g.N;
         for (int i = 0; i < n_stage; ++i) {
           if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, g.status,
-                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
             break;
           }
@@ -234,10 +145,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool half = 2 * i + 1 < n_sub;  // the stage's second 64 k hold something
           ptx::mbar_arrive_expect_tx(
               fb, (two ? 2 : 1) * kABytes + (half ? C::kBBytes : C::kBBytes / 2));
-          ptx::tma_load_3d(sA, a0, fb, i * kStageK, ch0, ex);
-          if (two) ptx::tma_load_3d(sA + kABytes, a1, fb, i * kStageK, ch1, ex);
-          ptx::tma_load_2d(sB, &tmB, fb, i * kStageK, u.brow0);
-          if (half) ptx::tma_load_2d(sB + C::kBBytes / 2, &tmB, fb, i * kStageK + 64, u.brow0);
+          ptx::tma_load_3d(sA, a0, fb, i * kInt8StageK, ch0, ex);
+          if (two) ptx::tma_load_3d(sA + kABytes, a1, fb, i * kInt8StageK, ch1, ex);
+          ptx::tma_load_2d(sB, &tmB, fb, i * kInt8StageK, u.brow0);
+          if (half) ptx::tma_load_2d(sB + C::kBBytes / 2, &tmB, fb, i * kInt8StageK + 64, u.brow0);
           issued |= 1u << stage;
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) {
@@ -251,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (issued & (1u << s)) {
           volatile int no_abort = 0;
           ptx::mbar_wait_bounded(full_bar(s), (last_parity >> s) & 1u, &no_abort, g.status,
-                                 MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs / 4);
+                                 MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs / 4);
         }
     }
     __syncwarp();
@@ -263,24 +174,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
         const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
-        const bool two = PAIR || u.ct * UCH + kCh < g.N;
+        const bool two = PAIR || u.ct * UCH + kInt8Ch < g.N;
         const uint32_t idesc =
-            ptx::idesc_f16kind_f32(kCh, (uint32_t)((u.rows + 15) & ~15), 0, 0, 0u);
+            ptx::idesc_f16kind_f32(kInt8Ch, (uint32_t)((u.rows + 15) & ~15), 0, 0, 0u);
         if (!ptx::mbar_wait_bounded(dempty_bar(acc), acc_phase ^ 1u, abort_flag, g.status,
-                                    MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs))
+                                    MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs))
           break;
         ptx::tc_fence_after();
         const uint32_t d0 = tmem_base + (uint32_t)(acc * 2 * NT), d1 = d0 + NT;
         for (int i = 0; i < n_stage && ok; ++i) {
           if (!ptx::mbar_wait_bounded(full_bar(stage), phase, abort_flag, g.status,
-                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
             break;
           }
           const uint32_t sB = base + stage * C::kStageBytes + 2 * kABytes;
           for (int h = 0; h < 2 && 2 * i + h < n_sub; ++h) {
             if (!ptx::mbar_wait_bounded(afull_bar(slot), slot_phase, abort_flag, g.status,
-                                        MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+                                        MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
               ok = false;
               break;
             }
@@ -319,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::umma_commit(mma_done_bar);
       volatile int no_abort = 0;
       ptx::mbar_wait_bounded(mma_done_bar, 0, &no_abort, g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
-                             kWaitLimitNs / 4);
+                             kInt8WaitNs / 4);
     }
     __syncwarp();
   } else if (warp >= 8) {
@@ -331,14 +242,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
       const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
-      const bool on = PAIR || tile == 0 || u.ct * UCH + kCh < g.N;
+      const bool on = PAIR || tile == 0 || u.ct * UCH + kInt8Ch < g.N;
       for (int i = 0; i < n_stage && ok; ++i) {
         if (!ptx::mbar_wait_bounded_warp(full_bar(stage), phase, abort_flag, g.status,
-                                         MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+                                         MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
           ok = false;
           break;
         }
-        const uint8_t* src = gbase + stage * C::kStageBytes + tile * kABytes + row * kStageK;
+        const uint8_t* src = gbase + stage * C::kStageBytes + tile * kABytes + row * kInt8StageK;
         for (int h = 0; h < 2 && 2 * i + h < n_sub; ++h) {
           uint32_t r[32];
           if (on) {
@@ -358,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) ptx::mbar_arrive(empty_bar(stage));
           }
           if (!ptx::mbar_wait_bounded_warp(aempty_bar(slot), slot_phase ^ 1u, abort_flag, g.status,
-                                           MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs)) {
+                                           MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
             break;
           }
@@ -385,98 +296,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue
-    constexpr int CW = NT % 32 == 0 ? 32 : 16;  // columns (rows of the output) per step
-    const int q = warp - 4;
-    int acc = 0;
+    using P = Panel<PASS, OUT, kInt8Ch>;
+    const int q = warp - 4, t = threadIdx.x - 128, chl = 32 * q + lane;
+    int acc = 0, ub = 0, sb = 0;  // accumulator; buffers of the unit's rows and of the step
     uint32_t acc_phase = 0, clamp = 0u;
     for (long long w = blockIdx.x; w < total; w += gridDim.x) {
       const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
       const bool sh = u.seg >= g.n_mat;
       const long long ex = sh ? u.seg - g.n_mat : u.seg;
-      const int ch0 = u.ct * UCH + 32 * q + lane, ch1 = PAIR ? ch0 : ch0 + kCh;
-      const bool in0 = ch0 < g.N, in1 = ch1 < g.N;
+      const int ch0 = u.ct * UCH, ch1 = PAIR ? ch0 : ch0 + kInt8Ch;
+      const bool in0 = ch0 + chl < g.N, in1 = ch1 + chl < g.N, two = ch1 < g.N;
       const float* sw = (sh ? g.sh_sw : g.sw) + ex * g.N;
       const float* sw2 = PAIR ? (sh ? g.sh_sw2 : g.sw2) + ex * g.N : sw;
-      const float w0 = in0 ? sw[ch0] : 0.0f, w1 = in1 ? sw2[ch1] : 0.0f;
-      // lane c holds the scale and the output row of column c of each step
-      float sx[NT / CW];
-      int orow[NT / CW];
-#pragma unroll
-      for (int c = 0; c < NT / CW; ++c) {
-        const int r = c * CW + (lane & (CW - 1));
-        sx[c] = 0.0f;
-        orow[c] = -1;
-        if (r < u.rows) {
-          sx[c] = g.sx[u.brow0 + r];
-          orow[c] = u.row0 + r;
-          if (PASS == kInt8Slot && !sh) {
-            const int slot = g.perm_slot[u.row0 + r];
-            const bool good = slot >= 0 && slot < g.rows;
-            orow[c] = good ? slot : -1;
-            if (good && g.topk_w != nullptr) sx[c] *= g.topk_w[slot];
-          }
-        }
-      }
-      if (!ptx::mbar_wait_bounded_warp(dfull_bar(acc), acc_phase, abort_flag, g.status,
-                                       MOE_DEVFAULT_PIPELINE_TIMEOUT, kWaitLimitNs))
+      const float w0 = in0 ? sw[ch0 + chl] : 0.0f, w1 = in1 ? sw2[ch1 + chl] : 0.0f;
+      float* usx = unit_sx[ub];
+      int* orow = unit_orow[ub];
+      ub ^= 1;
+      for (int r = t; r < NT; r += 128) unit_row<PASS>(g, u, r, orow[r], usx[r]);
+      if (!epilogue_all(ptx::mbar_wait_bounded_warp(dfull_bar(acc), acc_phase, abort_flag,
+                                                    g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
+                                                    kInt8WaitNs)))
         break;
       ptx::tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * 2 * NT);
+      // one panel of staged steps: value(j) is this thread's channel of row c * 32 + j; slot pass:
+      // bit j of rows_on, that row is written
+      auto steps = [&](int c, int ch, bool in, uint32_t rows_on, auto value) {
 #pragma unroll
-      for (int c = 0; c < NT / CW; ++c) {
-        if (c * CW >= u.rows) break;
-        uint32_t v0[CW], v1[CW];
-        if constexpr (CW == 32) {
-          ptx::tmem_ld_32x32b_x32(taddr + c * CW, v0);
-          ptx::tmem_ld_32x32b_x32(taddr + NT + c * CW, v1);
-        } else {
-          ptx::tmem_ld_32x32b_x16(taddr + c * CW, v0);
-          ptx::tmem_ld_32x32b_x16(taddr + NT + c * CW, v1);
-        }
-        ptx::tmem_wait_ld();
+        for (int j0 = 0; j0 < 32; j0 += P::kCols) {
+          uint8_t* buf = stage_out + sb * kInt8StepBytes;
 #pragma unroll
-        for (int j = 0; j < CW; ++j) {
-          const int to = __shfl_sync(0xffffffffu, orow[c], j);
-          const float s = __shfl_sync(0xffffffffu, sx[c], j);
-          if (to < 0) continue;  // past the segment, or a slot out of range
-          const long long at = (long long)to * g.N;
-          float y0 = __uint_as_float(v0[j]) * (s * w0), y1 = __uint_as_float(v1[j]) * (s * w1);
-          if (PASS == kInt8SwiGLU) {
-            if (in0) static_cast<float*>(g.out)[at + ch0] = y0 / (1.0f + __expf(-y0)) * y1;
-          } else if (PASS == kInt8Slot) {
-            uint16_t* y = static_cast<uint16_t*>(g.out) + at;
-            if (in0) {
-              y[ch0] = f16_sat(y0);
-              clamp = max(clamp, mag_bits(y0));
-            }
-            if (in1) {
-              y[ch1] = f16_sat(y1);
-              clamp = max(clamp, mag_bits(y1));
-            }
-          } else if (g.out_dtype == MOE_DTYPE_F32) {
-            float* y = static_cast<float*>(g.out) + at;
-            if (in0) y[ch0] = y0;
-            if (in1) y[ch1] = y1;
-          } else if (g.out_dtype == MOE_DTYPE_BF16) {
-            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(g.out) + at;
-            if (in0) y[ch0] = __float2bfloat16(y0);
-            if (in1) y[ch1] = __float2bfloat16(y1);
-          } else {
-            __half* y = static_cast<__half*>(g.out) + at;
-            if (in0) y[ch0] = __float2half(y0);
-            if (in1) y[ch1] = __float2half(y1);
+          for (int j = 0; j < P::kCols; ++j) {
+            const float y = value(j0 + j);
+            P::put(buf, j, chl, y);
+            if (PASS == kInt8Slot && in && ((rows_on >> (j0 + j)) & 1u))
+              clamp = max(clamp, mag_bits(y));
           }
+          epilogue_barrier();
+          P::flush(g, buf, orow + c * 32 + j0, ch, t);
+          sb ^= 1;
+        }
+      };
+#pragma unroll 1
+      for (int c = 0; c * 32 < u.rows; ++c) {
+        uint32_t v0[32], v1[32];
+        float sx[32];
+        ptx::tmem_ld_32x32b_x32(taddr + c * 32, v0);
+        ptx::tmem_ld_32x32b_x32(taddr + NT + c * 32, v1);
+        load_scales(usx + c * 32, sx);
+        const uint32_t rows_on =
+            PASS == kInt8Slot ? __ballot_sync(0xffffffffu, orow[c * 32 + lane] >= 0) : 0u;
+        ptx::tmem_wait_ld();
+        if ((c + 1) * 32 >= u.rows) {  // the accumulators are in registers
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(dempty_bar(acc));
+        }
+        if constexpr (PAIR) {
+          steps(c, ch0, in0, rows_on, [&](int j) {
+            const float gv = __uint_as_float(v0[j]) * (sx[j] * w0);
+            return gv / (1.0f + __expf(-gv)) * (__uint_as_float(v1[j]) * (sx[j] * w1));
+          });
+        } else {
+          steps(c, ch0, in0, rows_on, [&](int j) { return __uint_as_float(v0[j]) * (sx[j] * w0); });
+          if (two)
+            steps(c, ch1, in1, rows_on,
+                  [&](int j) { return __uint_as_float(v1[j]) * (sx[j] * w1); });
         }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(dempty_bar(acc));
       if (++acc == NB) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
-    if (PASS == kInt8Slot && __any_sync(0xffffffffu, clamp >= kF16Clamp) && lane == 0)
+    if (PASS == kInt8Slot && __any_sync(0xffffffffu, clamp >= kInt8F16Clamp) && lane == 0)
       atomicOr(g.status, MOE_DEVFAULT_FP16_RANGE);
   }
 
@@ -488,47 +381,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int PASS, int NT, int NB, int SA>
+template <int PASS, int OUT, int NT, int NB, int SA>
 cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
   using C = Cfg<NT, NB, SA>;
   constexpr CUtensorMapDataType kCode = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   CUtensorMap b, a, a2, sa, sa2;
   bool ok = make_tmap_2d(&b, g.xq, g.x_rows, g.K, 64, NT, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) &&
-            make_tmap_3d(&a, g.qw, g.n_mat, g.N, g.K, kStageK, kCh, kCode, 1);
+            make_tmap_3d(&a, g.qw, g.n_mat, g.N, g.K, kInt8StageK, kInt8Ch, kCode, 1);
   a2 = a;
   if (ok && PASS == kInt8SwiGLU)
-    ok = make_tmap_3d(&a2, g.qw2, g.n_mat, g.N, g.K, kStageK, kCh, kCode, 1);
+    ok = make_tmap_3d(&a2, g.qw2, g.n_mat, g.N, g.K, kInt8StageK, kInt8Ch, kCode, 1);
   sa = a;
   sa2 = a2;
   if (ok && g.S > 0) {
-    ok = make_tmap_3d(&sa, g.sh_qw, g.S, g.N, g.K, kStageK, kCh, kCode, 1);
+    ok = make_tmap_3d(&sa, g.sh_qw, g.S, g.N, g.K, kInt8StageK, kInt8Ch, kCode, 1);
     if (ok && PASS == kInt8SwiGLU)
-      ok = make_tmap_3d(&sa2, g.sh_qw2, g.S, g.N, g.K, kStageK, kCh, kCode, 1);
+      ok = make_tmap_3d(&sa2, g.sh_qw2, g.S, g.N, g.K, kInt8StageK, kInt8Ch, kCode, 1);
   }
   if (!ok) return cudaErrorInvalidValue;
-  auto kern = int8_gemm_kernel<PASS, NT, NB, SA>;
+  auto kern = int8_gemm_kernel<PASS, OUT, NT, NB, SA>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(num_sms()), dim3(kThreads), C::kSmemBytes, st, b, a, a2, sa, sa2, g);
+  return launch_k(kern, dim3(num_sms()), dim3(kInt8Threads), C::kSmemBytes, st, b, a, a2, sa, sa2, g);
 }
 
-template <int PASS>
+template <int PASS, int OUT>
 cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
   // rows per segment on average (an even spread): short segments leave most of a wide tile empty, and
   // a narrow one leaves shared memory for more weight tiles in flight
   const long long mean = g.rows / g.n_mat;
-  if (mean <= 32) return launch_one<PASS, 32, 2, 6>(g, st);
-  return launch_one<PASS, 96, 2, 2>(g, st);
+  if (mean <= 32) return launch_one<PASS, OUT, 32, 2, 6>(g, st);
+  return launch_one<PASS, OUT, 96, 2, 2>(g, st);
 }
 
 }  // namespace
 
 cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st) {
+  if (g.rows / g.n_mat > 96) return launch_int8_gemm_pair(pass, g, st);
   switch (pass) {
-    case kInt8Matrix: return launch_pass<kInt8Matrix>(g, st);
-    case kInt8SwiGLU: return launch_pass<kInt8SwiGLU>(g, st);
-    default: return launch_pass<kInt8Slot>(g, st);
+    case kInt8SwiGLU: return launch_pass<kInt8SwiGLU, MOE_DTYPE_F32>(g, st);
+    case kInt8Slot: return launch_pass<kInt8Slot, MOE_DTYPE_F16>(g, st);
+    default: break;
+  }
+  switch (g.out_dtype) {
+    case MOE_DTYPE_F32: return launch_pass<kInt8Matrix, MOE_DTYPE_F32>(g, st);
+    case MOE_DTYPE_BF16: return launch_pass<kInt8Matrix, MOE_DTYPE_BF16>(g, st);
+    default: return launch_pass<kInt8Matrix, MOE_DTYPE_F16>(g, st);
   }
 }
 

@@ -1,0 +1,443 @@
+// Grouped products of 8-bit integers for long row segments: the product of int8_gemm.cu on pairs of
+// CTAs (a cluster of two) that share one tcgen05 MMA of M = 256.
+//
+// With one CTA a tile's operand traffic through shared memory (weight codes in and out, rows in, and
+// read by the MMA) takes longer than its MMAs: (64 / N + 0.75) of their time for two 128-channel tiles
+// x N rows, 1.25 at N = 128. Here each CTA widens 128 channels into its own tensor memory but stages
+// only half of the rows, which the MMA reads once for both: 40 KB per 64 k against 49 KB of shared-memory
+// bandwidth in the 384 clk that N = 192 takes, and half the widening per MMA.
+//
+// A unit is 256 channels (SwiGLU pass: 128 channels of gate and up) x up to 192 rows of one segment.
+// Rank r of a pair holds channels [128 r, 128 r + 128) and rows [n / 2 * r, n / 2 * (r + 1)) of the n
+// rows the MMA takes (the unit's rows rounded up to 32). SwiGLU pass: rank r holds 64 channels; TMEM lanes
+// 32 w + l, l < 16, hold the gate codes of channel 16 w + l and lanes 32 w + 16 + l the up codes, so that
+// a warp's epilogue swaps halves by shuffles. Roles per CTA (512 threads):
+//   warp 0       TMA producer: the CTA's 128 code rows x 128 B and two [96 rows x 64 k] fp16 tiles a stage
+//   warp 1       MMA issuer (rank 0)
+//   warp 2       TMEM allocator: two accumulators of 192 columns, four 32-column slots of widened codes
+//   warps 4-7    epilogue, overlapping the next unit's MMAs
+//   warps 8-15   widen: four warps the first 64 k of each stage, four the second
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "int8.cuh"
+#include "int8_units.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kNT = 192;                            // rows per unit (MMA N)
+constexpr int kABytes = kInt8Ch * kInt8StageK;      // 16 KB of codes
+constexpr int kBSub = kNT / 2 * 128;                // one [96 rows x 64 k] fp16 tile
+constexpr int kStageBytes = kABytes + 2 * kBSub;    // 40 KB
+constexpr int kStages = 5;
+constexpr int kAcc = 2;                             // accumulators
+constexpr int kSlots = 4;                           // widened codes, 64 k each
+constexpr int kSlotCol = kAcc * kNT;                   // their first TMEM column
+constexpr int kBars = 3 * kStages + 2 * kSlots + 2 * kAcc + 1;
+constexpr int kSmemBytes =
+    kStages * kStageBytes + 2 * kInt8StepBytes + 1024 /*align*/ + 512 /*barriers*/;
+static_assert(kSlotCol + kSlots * 32 <= 512, "TMEM columns");
+static_assert(8 * kBars + 8 <= 512, "barrier block");
+
+template <int PASS, int OUT>
+__global__ void __launch_bounds__(kInt8Threads, 1)
+    int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmB,
+                          const __grid_constant__ CUtensorMap tmA,
+                          const __grid_constant__ CUtensorMap tmA2,
+                          const __grid_constant__ CUtensorMap tmShA,
+                          const __grid_constant__ CUtensorMap tmShA2, const Int8Gemm g) {
+  constexpr bool GLU = PASS == kInt8SwiGLU;
+  constexpr int UCH = GLU ? 128 : 256;  // output channels per unit
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ SegTable segs;
+  __shared__ __align__(16) float unit_sx[2][kNT];  // row scales, output rows of the epilogue's unit
+  __shared__ int unit_orow[2][kNT];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  uint8_t* const stage_out = gbase + kStages * kStageBytes;  // the epilogue's two steps
+  const uint32_t bar0 = base + kStages * kStageBytes + 2 * kInt8StepBytes;
+  auto codes_bar = [&](int s) { return bar0 + 8u * s; };              // own codes have landed
+  auto rows_bar = [&](int s) { return bar0 + 8u * (kStages + s); };   // rank 0: both CTAs' rows
+  auto empty_bar = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
+  auto afull_bar = [&](int s) { return bar0 + 8u * (3 * kStages + s); };  // rank 0: both CTAs
+  auto aempty_bar = [&](int s) { return bar0 + 8u * (3 * kStages + kSlots + s); };
+  auto dfull_bar = [&](int b) { return bar0 + 8u * (3 * kStages + 2 * kSlots + b); };
+  auto dempty_bar = [&](int b) { return bar0 + 8u * (3 * kStages + 2 * kSlots + kAcc + b); };  // rank 0
+  const uint32_t mma_done_bar = bar0 + 8u * (kBars - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stage_out + 2 * kInt8StepBytes + 8 * kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_rank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(codes_bar(s), 1);
+      ptx::mbar_init(rows_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 9);  // eight widening warps and the pair's MMAs
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      ptx::mbar_init(afull_bar(s), 8);  // four widening warps of each CTA
+      ptx::mbar_init(aempty_bar(s), 1);
+    }
+    for (int b = 0; b < kAcc; ++b) {
+      ptx::mbar_init(dfull_bar(b), 1);
+      ptx::mbar_init(dempty_bar(b), 8);  // four epilogue warps of each CTA
+    }
+    ptx::mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    ptx::fence_mbarrier_init();
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
+    if (GLU) ptx::prefetch_tmap(&tmA2);
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc_cg2(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish_cg2();
+  }
+  griddep_wait();  // everything above touched only shared memory, TMEM and parameters
+  build_segments(segs, g, kNT);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // the peer's barriers are initialised
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int n_ct = (g.N + UCH - 1) / UCH;
+  const int n_sub = (g.K + 63) / 64;
+  const int n_stage = (n_sub + 1) / 2;
+  const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct;
+  const long long pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  auto mma_rows = [](const Unit& u) { return (u.rows + 31) & ~31; };
+
+  if (warp == 0) {
+    if (ptx::elect_one()) {
+      // ---------------------------------------------------------------- TMA producer (both)
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, last_parity = 0;  // per stage: ever issued, its parity
+      bool ok = true;
+      for (long long w = pair; w < total && ok; w += n_pairs) {
+        const Unit u = find_unit<GLU>(segs, g, n_ct, kNT, w);
+        const bool sh = u.seg >= g.n_mat;
+        const int ex = sh ? u.seg - g.n_mat : u.seg;
+        const CUtensorMap* a0 = sh ? &tmShA : &tmA;
+        const CUtensorMap* a1 = GLU ? (sh ? &tmShA2 : &tmA2) : a0;
+        const int ch0 = u.ct * UCH + (int)rank * (UCH / 2), ch1 = GLU ? ch0 : ch0 + 64;
+        const int brow = u.brow0 + (int)rank * (mma_rows(u) / 2);
+        for (int i = 0; i < n_stage; ++i) {
+          if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, g.status,
+                                              MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sA = base + stage * kStageBytes, sB = sA + kABytes;
+          const uint32_t cb = codes_bar(stage);
+          const uint32_t rb = leader ? rows_bar(stage) : ptx::mapa_shared(rows_bar(stage), 0);
+          const bool half = 2 * i + 1 < n_sub;  // the stage's second 64 k hold something
+          ptx::mbar_arrive_expect_tx(cb, kABytes);
+          ptx::tma_load_3d(sA, a0, cb, i * kInt8StageK, ch0, ex);
+          ptx::tma_load_3d(sA + kABytes / 2, a1, cb, i * kInt8StageK, ch1, ex);
+          if (leader) ptx::mbar_arrive_expect_tx(rb, 2 * (half ? 2 * kBSub : kBSub));
+          ptx::tma_load_2d_cg2(sB, &tmB, rb, i * kInt8StageK, brow);
+          if (half) ptx::tma_load_2d_cg2(sB + kBSub, &tmB, rb, i * kInt8StageK + 64, brow);
+          issued |= 1u << stage;
+          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // never leave while a copy into either CTA's shared memory may still be in flight (the rows
+      // of both are counted on rank 0)
+      for (int s = 0; s < kStages; ++s)
+        if (issued & (1u << s)) {
+          volatile int no_abort = 0;
+          ptx::mbar_wait_bounded(codes_bar(s), (last_parity >> s) & 1u, &no_abort,
+                                         g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
+                                         kInt8WaitNs / 4);
+          if (leader)
+            ptx::mbar_wait_bounded(rows_bar(s), (last_parity >> s) & 1u, &no_abort,
+                                           g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
+                                           kInt8WaitNs / 4);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (leader && ptx::elect_one()) {
+      // ---------------------------------------------------------------- MMA issuer (rank 0)
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, sub = 0, acc_phase = 0;  // sub: 64-k slots used so far
+      bool ok = true;
+      for (long long w = pair; w < total && ok; w += n_pairs) {
+        const Unit u = find_unit<GLU>(segs, g, n_ct, kNT, w);
+        const uint32_t idesc = ptx::idesc_f16kind_f32(256, (uint32_t)mma_rows(u), 0, 0, 0u);
+        if (!ptx::mbar_wait_bounded(dempty_bar(acc), acc_phase ^ 1u, abort_flag, g.status,
+                                            MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs))
+          break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * kNT);
+        for (int i = 0; i < n_stage && ok; ++i) {
+          if (!ptx::mbar_wait_bounded(rows_bar(stage), phase, abort_flag, g.status,
+                                              MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
+            ok = false;
+            break;
+          }
+          const uint64_t bd =
+              ptx::smem_desc_sw128(base + stage * kStageBytes + kABytes, 16, 1024);
+          for (int h = 0; h < 2 && 2 * i + h < n_sub; ++h, ++sub) {
+            const uint32_t slot = sub & (kSlots - 1);
+            if (!ptx::mbar_wait_bounded(afull_bar(slot), (sub / kSlots) & 1u, abort_flag,
+                                                g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
+                                                kInt8WaitNs)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t a = tmem_base + kSlotCol + slot * 32;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              // rows: K-major, 128 B each, 8-row groups 1024 B apart; a K step of 16 = +32 B
+              ptx::umma_f16_ta_cg2(d, a + kk * 8, bd + (uint64_t)((h * kBSub + kk * 32) >> 4),
+                                   idesc, (i | h | kk) != 0 ? 1u : 0u);
+            ptx::umma_commit_cg2(aempty_bar(slot), 0x3);
+          }
+          if (!ok) break;
+          ptx::umma_commit_cg2(empty_bar(stage), 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::umma_commit_cg2(dfull_bar(acc), 0x3);
+        if (++acc == kAcc) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      // all MMAs issued by this thread have finished before TMEM is released
+      ptx::umma_commit_cg2(mma_done_bar, 0x1);
+      volatile int no_abort = 0;
+      ptx::mbar_wait_bounded(mma_done_bar, 0, &no_abort, g.status,
+                                     MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs / 4);
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ widening warps (both)
+    const int h = (warp - 8) >> 2, q = warp & 3;  // half of the stage; TMEM lanes [32 q, 32 q + 32)
+    const int row = GLU ? 16 * q + (lane & 15) + 64 * (lane >> 4) : 32 * q + lane;
+    int stage = 0;
+    uint32_t phase = 0, sub = 0;
+    bool ok = true;
+    for (long long w = pair; w < total && ok; w += n_pairs) {
+      for (int i = 0; i < n_stage; ++i) {
+        if (!ptx::mbar_wait_bounded_warp(codes_bar(stage), phase, abort_flag, g.status,
+                                                 MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
+          ok = false;
+          break;
+        }
+        const bool on = 2 * i + h < n_sub;
+        uint32_t r[32];
+        if (on) {
+          const uint8_t* src = gbase + stage * kStageBytes + row * kInt8StageK;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // 16-byte piece 4 h + c of the row sits at piece (4 h + c) ^ (row mod 8)
+            const uint4 v =
+                *reinterpret_cast<const uint4*>(src + (((4 * h + c) ^ (row & 7)) << 4));
+            widen4(v.x, r[8 * c], r[8 * c + 1]);
+            widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+            widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+            widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty_bar(stage));  // the codes are in registers
+        if (on) {
+          const uint32_t mine = sub + (uint32_t)(2 * i + h), slot = mine & (kSlots - 1);
+          if (!ptx::mbar_wait_bounded_warp(
+                  aempty_bar(slot), ((mine / kSlots) & 1u) ^ 1u, abort_flag, g.status,
+                  MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          ptx::tmem_st_32x32b_x32(
+              tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(kSlotCol + slot * 32), r);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader)
+              ptx::mbar_arrive(afull_bar(slot));
+            else
+              ptx::mbar_arrive_remote(ptx::mapa_shared(afull_bar(slot), 0));
+          }
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      sub += (uint32_t)n_sub;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ epilogue (both)
+    using P = Panel<PASS, OUT, GLU ? 64 : 128>;
+    const int q = warp - 4, t = threadIdx.x - 128;
+    const int up = GLU ? lane >> 4 : 0;  // this lane's accumulators belong to the up projection
+    const int chl = GLU ? 16 * q + (lane & 15) : 32 * q + lane;  // channel of the CTA's panel
+    int acc = 0, ub = 0, sb = 0;  // accumulator; buffers of the unit's rows and of the step
+    uint32_t acc_phase = 0, clamp = 0u;
+    for (long long w = pair; w < total; w += n_pairs) {
+      const Unit u = find_unit<GLU>(segs, g, n_ct, kNT, w);
+      const bool sh = u.seg >= g.n_mat;
+      const long long ex = sh ? u.seg - g.n_mat : u.seg;
+      const int ch0 = u.ct * UCH + (int)rank * (UCH / 2);
+      const bool in = ch0 + chl < g.N;
+      const float* sw = (up ? (sh ? g.sh_sw2 : g.sw2) : (sh ? g.sh_sw : g.sw)) + ex * g.N;
+      const float wc = in ? sw[ch0 + chl] : 0.0f;
+      float* usx = unit_sx[ub];
+      int* orow = unit_orow[ub];
+      ub ^= 1;
+      for (int r = t; r < kNT; r += 128) unit_row<PASS>(g, u, r, orow[r], usx[r]);
+      if (!epilogue_all(ptx::mbar_wait_bounded_warp(dfull_bar(acc), acc_phase, abort_flag,
+                                                    g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
+                                                    kInt8WaitNs)))
+        break;
+      ptx::tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * kNT);
+#pragma unroll 1
+      for (int c = 0; c * 32 < u.rows; ++c) {
+        uint32_t v[32];
+        float sx[32];
+        ptx::tmem_ld_32x32b_x32(taddr + c * 32, v);
+        load_scales(usx + c * 32, sx);
+        // PASS slot: bit j, row c * 32 + j is written
+        const uint32_t rows_on =
+            PASS == kInt8Slot ? __ballot_sync(0xffffffffu, in && orow[c * 32 + lane] >= 0) : 0u;
+        ptx::tmem_wait_ld();
+        if ((c + 1) * 32 >= u.rows) {  // the accumulator is in registers
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader)
+              ptx::mbar_arrive(dempty_bar(acc));
+            else
+              ptx::mbar_arrive_remote(ptx::mapa_shared(dempty_bar(acc), 0));
+          }
+        }
+        if constexpr (GLU) {
+          // gate lanes finish columns 0-15, up lanes columns 16-31: each sends the other half over
+          uint8_t* buf = stage_out + sb * kInt8StepBytes;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float x = __uint_as_float(v[j]) * wc, y = __uint_as_float(v[16 + j]) * wc;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? x : y, 16);
+            const int col = j + 16 * up;
+            const float s = up ? sx[16 + j] : sx[j];
+            const float gv = (up ? got : x) * s, uv = (up ? y : got) * s;
+            P::put(buf, col, chl, gv / (1.0f + __expf(-gv)) * uv);
+          }
+          epilogue_barrier();
+          P::flush(g, buf, orow + c * 32, ch0, t);
+          sb ^= 1;
+        } else {
+#pragma unroll
+          for (int j0 = 0; j0 < 32; j0 += P::kCols) {
+            uint8_t* buf = stage_out + sb * kInt8StepBytes;
+#pragma unroll
+            for (int j = 0; j < P::kCols; ++j) {
+              const float y = __uint_as_float(v[j0 + j]) * (sx[j0 + j] * wc);
+              P::put(buf, j, chl, y);
+              if (PASS == kInt8Slot && ((rows_on >> (j0 + j)) & 1u))
+                clamp = max(clamp, mag_bits(y));
+            }
+            epilogue_barrier();
+            P::flush(g, buf, orow + c * 32 + j0, ch0, t);
+            sb ^= 1;
+          }
+        }
+      }
+      if (++acc == kAcc) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (PASS == kInt8Slot && __any_sync(0xffffffffu, clamp >= kInt8F16Clamp) && lane == 0)
+      atomicOr(g.status, MOE_DEVFAULT_FP16_RANGE);
+  }
+
+  // every copy into either CTA has landed and every MMA has finished once the producers and rank 0's
+  // MMA thread are here; neither CTA leaves (nor frees TMEM) before both are
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  if (warp == 2) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_cg2(tmem_base, 512);
+  }
+}
+
+template <int PASS, int OUT>
+cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
+  constexpr CUtensorMapDataType kCode = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUtensorMap b, a, a2, sa, sa2;
+  bool ok = make_tmap_2d(&b, g.xq, g.x_rows, g.K, 64, kNT / 2, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) &&
+            make_tmap_3d(&a, g.qw, g.n_mat, g.N, g.K, kInt8StageK, 64, kCode, 1);
+  a2 = a;
+  if (ok && PASS == kInt8SwiGLU)
+    ok = make_tmap_3d(&a2, g.qw2, g.n_mat, g.N, g.K, kInt8StageK, 64, kCode, 1);
+  sa = a;
+  sa2 = a2;
+  if (ok && g.S > 0) {
+    ok = make_tmap_3d(&sa, g.sh_qw, g.S, g.N, g.K, kInt8StageK, 64, kCode, 1);
+    if (ok && PASS == kInt8SwiGLU)
+      ok = make_tmap_3d(&sa2, g.sh_qw2, g.S, g.N, g.K, kInt8StageK, 64, kCode, 1);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  auto kern = int8_gemm_pair_kernel<PASS, OUT>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms() / 2 * 2);  // persistent: one CTA pair per two SMs
+  cfg.blockDim = dim3(kInt8Threads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, b, a, a2, sa, sa2, g);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_gemm_pair(Int8Pass pass, const Int8Gemm& g, cudaStream_t st) {
+  switch (pass) {
+    case kInt8SwiGLU: return launch_one<kInt8SwiGLU, MOE_DTYPE_F32>(g, st);
+    case kInt8Slot: return launch_one<kInt8Slot, MOE_DTYPE_F16>(g, st);
+    default: break;
+  }
+  switch (g.out_dtype) {
+    case MOE_DTYPE_F32: return launch_one<kInt8Matrix, MOE_DTYPE_F32>(g, st);
+    case MOE_DTYPE_BF16: return launch_one<kInt8Matrix, MOE_DTYPE_BF16>(g, st);
+    default: return launch_one<kInt8Matrix, MOE_DTYPE_F16>(g, st);
+  }
+}
+
+}  // namespace moe

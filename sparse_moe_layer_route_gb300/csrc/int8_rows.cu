@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "int8.cuh"
@@ -14,85 +15,198 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 
-// One CTA per row.
+// Eight consecutive elements of a row, loaded as 16-byte pieces.
 template <typename XT>
-__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const XT* __restrict__ x,
-                                                                 long long ld, int d,
-                                                                 int8_t* __restrict__ q,
-                                                                 float* __restrict__ scale) {
-  __shared__ uint32_t warp_top[kThreads / 32];
+struct Vec8 {
+  uint4 p;
+  __device__ __forceinline__ void load(const XT* at) { p = *reinterpret_cast<const uint4*>(at); }
+  __device__ __forceinline__ void get(float (&v)[8]) const;
+};
+template <>
+__device__ __forceinline__ void Vec8<__nv_bfloat16>::get(float (&v)[8]) const {
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void Vec8<__half>::get(float (&v)[8]) const {
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <>
+struct Vec8<float> {
+  float4 p, q;
+  __device__ __forceinline__ void load(const float* at) {
+    p = reinterpret_cast<const float4*>(at)[0];
+    q = reinterpret_cast<const float4*>(at)[1];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
+    v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+  }
+};
+
+// Where the codes go: 8-bit, or 16-bit for the tensor cores (whole numbers up to 127 are exact in
+// fp16). c: the codes as floats.
+__device__ __forceinline__ void store_codes8(int8_t* at, const float (&c)[8]) {
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(c[i] + 12582912.0f);  // low byte: the code
+  uint2 o;
+  o.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  o.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  *reinterpret_cast<uint2*>(at) = o;
+}
+__device__ __forceinline__ void store_codes8(uint16_t* at, const float (&c)[8]) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(c[2 * i], c[2 * i + 1]);
+    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ void store_code(int8_t* at, int c) { *at = (int8_t)c; }
+__device__ __forceinline__ void store_code(uint16_t* at, int c) {
+  *at = __half_as_ushort(__int2half_rn(c));
+}
+
+// The largest magnitude bits over the threads of a row: a warp (W = 32) or a CTA of W threads.
+template <int W>
+__device__ __forceinline__ uint32_t row_max(uint32_t top, uint32_t* warp_top) {
+  top = __reduce_max_sync(kFull, top);
+  if (W > 32) {
+    if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W / 32; ++w) top = max(top, warp_top[w]);
+  }
+  return top;
+}
+
+// One row by W threads, thread t of them. VEC: rows in 16-byte pieces, d a multiple of 8 and at most
+// 64 W; the row stays in registers between its two passes. x / scale is first taken as x * (1 / scale),
+// within 2.3e-5 of the quotient for codes up to 127; where that is within 1e-4 of halfway between two
+// codes (about one value in 5000) the division decides. So the codes are those of the division at a
+// third of its instructions.
+template <int W, bool VEC, typename XT, typename QT>
+__device__ __forceinline__ void quantize_row(const XT* __restrict__ row, int d,
+                                             QT* __restrict__ out, float* __restrict__ scale,
+                                             int t, uint32_t* warp_top) {
+  uint32_t top = 0u;
+  if constexpr (VEC) {
+    constexpr int NV = 8;
+    Vec8<XT> x[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((i * W + t) * 8 < d) x[i].load(row + (i * W + t) * 8);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((i * W + t) * 8 < d) {
+        float v[8];
+        x[i].get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+      }
+    const float s = int8_scale(row_max<W>(top, warp_top));
+    if (t == 0) *scale = s;
+    const bool plain = s > 1e-30f && s < 1e30f;  // 1 / s is a normal number
+    const float r = plain ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((i * W + t) * 8 < d) {
+        float v[8], c[8];
+        x[i].get(v);
+        bool near = !plain;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float y = __fmul_rn(v[j], r);
+          c[j] = __fsub_rn(__fadd_rn(y, 12582912.0f), 12582912.0f);  // rint
+          near |= fabsf(y - c[j]) > 0.4999f;
+        }
+        if (near) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) c[j] = (float)int8_code(v[j], s);
+        }
+        store_codes8(out + (i * W + t) * 8, c);
+      }
+  } else {
+    for (int j = t; j < d; j += W)
+      top = max(top, __float_as_uint(to_f32(row[j])) & 0x7fffffffu);
+    const float s = int8_scale(row_max<W>(top, warp_top));
+    if (t == 0) *scale = s;
+    for (int j = t; j < d; j += W) store_code(out + j, int8_code(to_f32(row[j]), s));
+  }
+}
+
+// Rows of x to 8-bit codes. W = 32: a warp per row, else a CTA of W threads.
+template <int W, bool VEC, typename XT>
+__global__ void __launch_bounds__(W == 32 ? kThreads : W)
+    quantize_rows_kernel(const XT* __restrict__ x, long long ld, int T, int d,
+                         int8_t* __restrict__ q, float* __restrict__ scale) {
+  __shared__ uint32_t warp_top[W / 32];
   griddep_wait();
-  const XT* row = x + (long long)blockIdx.x * ld;
-  uint32_t top = 0u;
-  for (int j = threadIdx.x; j < d; j += kThreads)
-    top = max(top, __float_as_uint(to_f32(row[j])) & 0x7fffffffu);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) top = max(top, warp_top[w]);
-  const float s = int8_scale(top);
-  if (threadIdx.x == 0) scale[blockIdx.x] = s;
-  for (int j = threadIdx.x; j < d; j += kThreads)
-    q[(long long)blockIdx.x * d + j] = (int8_t)int8_code(to_f32(row[j]), s);
+  const long long p = W == 32 ? (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)
+                              : (long long)blockIdx.x;
+  if (p >= T) return;
+  quantize_row<W, VEC>(x + p * ld, d, q + p * d, scale + p, W == 32 ? threadIdx.x & 31 : threadIdx.x,
+                       warp_top);
 }
 
-// Codes of one row in fp16, for the tensor cores (whole numbers up to 127 are exact there).
-template <typename XT>
-__device__ __forceinline__ void code_row(const XT* __restrict__ row, int d,
-                                         uint16_t* __restrict__ out, float* __restrict__ scale,
-                                         uint32_t* warp_top) {
-  uint32_t top = 0u;
-  for (int j = threadIdx.x; j < d; j += kThreads)
-    top = max(top, __float_as_uint(to_f32(row[j])) & 0x7fffffffu);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) top = max(top, warp_top[w]);
-  const float s = int8_scale(top);
-  if (threadIdx.x == 0) *scale = s;
-  for (int j = threadIdx.x; j < d; j += kThreads)
-    out[j] = __half_as_ushort(__int2half_rn(int8_code(to_f32(row[j]), s)));
-}
-
-__global__ void __launch_bounds__(kThreads) quantize_gather_kernel(
+template <int W, bool VEC>
+__global__ void __launch_bounds__(W == 32 ? kThreads : W) quantize_gather_kernel(
     const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ perm_slot,
-    const int32_t* __restrict__ offsets, int E, int k, int d, int TK, uint16_t* __restrict__ xq,
-    float* __restrict__ sx, int* status) {
-  __shared__ uint32_t warp_top[kThreads / 32];
+    const int32_t* __restrict__ offsets, int E, int k, int d, int TK, int rows,
+    uint16_t* __restrict__ xq, float* __restrict__ sx, int* status) {
+  __shared__ uint32_t warp_top[W / 32];
   griddep_wait();
-  const int p = blockIdx.x;
-  long long t = p - TK;  // shared experts: every token
+  const long long p = W == 32 ? (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)
+                              : (long long)blockIdx.x;
+  const int t = W == 32 ? threadIdx.x & 31 : threadIdx.x;
+  if (p >= rows) return;
+  long long token = p - TK;  // shared experts: every token
   if (p < TK) {
     if (p >= offsets[E]) return;
     const int slot = perm_slot[p];
-    t = slot / k;
+    token = slot / k;
     if (slot < 0 || slot >= TK) {
-      for (int j = threadIdx.x; j < d; j += kThreads) xq[(long long)p * d + j] = 0;
-      if (threadIdx.x == 0) {
+      for (int j = t; j < d; j += W) xq[p * d + j] = 0;
+      if (t == 0) {
         sx[p] = 0.0f;
         atomicOr(status, MOE_DEVFAULT_BAD_TILE);
       }
       return;
     }
   }
-  code_row(x + t * d, d, xq + (long long)p * d, sx + p, warp_top);
+  quantize_row<W, VEC>(x + token * d, d, xq + p * d, sx + p, t, warp_top);
 }
 
-__global__ void __launch_bounds__(kThreads) quantize_hidden_kernel(
-    const float* __restrict__ h, const int32_t* __restrict__ offsets, int E, int f, int TK,
-    uint16_t* __restrict__ hq, float* __restrict__ sh) {
-  __shared__ uint32_t warp_top[kThreads / 32];
+template <int W, bool VEC>
+__global__ void __launch_bounds__(W == 32 ? kThreads : W)
+    quantize_hidden_kernel(const float* __restrict__ h, const int32_t* __restrict__ offsets, int E,
+                           int f, int TK, long long rows, uint16_t* __restrict__ hq,
+                           float* __restrict__ sh) {
+  __shared__ uint32_t warp_top[W / 32];
   griddep_wait();
-  const long long p = blockIdx.x;
-  if (p < TK && p >= offsets[E]) return;
-  code_row(h + p * f, f, hq + p * f, sh + p, warp_top);
+  const long long p = W == 32 ? (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)
+                              : (long long)blockIdx.x;
+  if (p >= rows || (p < TK && p >= offsets[E])) return;
+  quantize_row<W, VEC>(h + p * f, f, hq + p * f, sh + p, W == 32 ? threadIdx.x & 31 : threadIdx.x,
+                       warp_top);
 }
 
 __global__ void __launch_bounds__(kThreads) widen_codes_kernel(const int4* __restrict__ q,
@@ -148,19 +262,52 @@ __global__ void __launch_bounds__(kThreads) quantize_channels_kernel(
 
 }  // namespace
 
+namespace {
+
+// Calls f(W, VEC) for rows of d elements: a warp per row up to 2048 elements, else a CTA, with the row in
+// registers up to 8192 (128 threads) or 16384 (256); vec: rows are in 16-byte pieces of eight elements.
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <typename F>
+cudaError_t by_row(int d, bool vec, F f) {
+  if (d <= 2048) return vec ? f(Int<32>{}, std::true_type{}) : f(Int<32>{}, std::false_type{});
+  if (vec && d <= 8192) return f(Int<128>{}, std::true_type{});
+  if (vec && d <= 16384) return f(Int<256>{}, std::true_type{});
+  return f(Int<256>{}, std::false_type{});
+}
+template <int W>
+dim3 row_grid(long long rows) {
+  return dim3((unsigned)(W == 32 ? (rows + kThreads / 32 - 1) / (kThreads / 32) : rows));
+}
+template <int W>
+dim3 row_block() {
+  return dim3(W == 32 ? kThreads : W);
+}
+
+template <typename XT>
+cudaError_t quantize_rows_as(int T, int d, const XT* x, long long ld, int8_t* q, float* scale,
+                             cudaStream_t st) {
+  const bool vec = d % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
+                   (T == 1 || ld * sizeof(XT) % 16 == 0) &&
+                   reinterpret_cast<uintptr_t>(q) % 8 == 0;
+  return by_row(d, vec, [&](auto w, auto v) {
+    constexpr int W = decltype(w)::value;
+    return launch_k(quantize_rows_kernel<W, decltype(v)::value, XT>, row_grid<W>(T),
+                    row_block<W>(), 0, st, x, ld, T, d, q, scale);
+  });
+}
+
+}  // namespace
+
 cudaError_t launch_quantize_rows(int T, int d, int dtype, const void* x, long long ld, int8_t* q,
                                  float* scale, cudaStream_t st) {
-  const dim3 grid(T), block(kThreads);
   switch (dtype) {
     case MOE_DTYPE_BF16:
-      return launch_k(quantize_rows_kernel<__nv_bfloat16>, grid, block, 0, st,
-                      static_cast<const __nv_bfloat16*>(x), ld, d, q, scale);
+      return quantize_rows_as(T, d, static_cast<const __nv_bfloat16*>(x), ld, q, scale, st);
     case MOE_DTYPE_F16:
-      return launch_k(quantize_rows_kernel<__half>, grid, block, 0, st,
-                      static_cast<const __half*>(x), ld, d, q, scale);
+      return quantize_rows_as(T, d, static_cast<const __half*>(x), ld, q, scale, st);
     default:
-      return launch_k(quantize_rows_kernel<float>, grid, block, 0, st,
-                      static_cast<const float*>(x), ld, d, q, scale);
+      return quantize_rows_as(T, d, static_cast<const float*>(x), ld, q, scale, st);
   }
 }
 
@@ -181,15 +328,22 @@ cudaError_t launch_quantize_gather(const Shape& s, const uint16_t* x, const int3
                                    const int32_t* offsets, uint16_t* xq, float* sx, int* status,
                                    cudaStream_t st) {
   const long long rows = s.TK + (s.S > 0 ? s.T : 0);
-  return launch_k(quantize_gather_kernel, dim3((unsigned)rows), dim3(kThreads), 0, st,
-                  reinterpret_cast<const __nv_bfloat16*>(x), perm_slot, offsets, s.E, s.k, s.d,
-                  (int)s.TK, xq, sx, status);
+  return by_row(s.d, true, [&](auto w, auto v) {  // d is a multiple of 64, x 16-byte aligned
+    constexpr int W = decltype(w)::value;
+    return launch_k(quantize_gather_kernel<W, decltype(v)::value>, row_grid<W>(rows),
+                    row_block<W>(), 0, st, reinterpret_cast<const __nv_bfloat16*>(x), perm_slot,
+                    offsets, s.E, s.k, s.d, (int)s.TK, (int)rows, xq, sx, status);
+  });
 }
 
 cudaError_t launch_quantize_hidden(const Shape& s, const float* h, const int32_t* offsets,
                                    uint16_t* hq, float* sh, cudaStream_t st) {
-  return launch_k(quantize_hidden_kernel, dim3((unsigned)s.rows), dim3(kThreads), 0, st, h,
-                  offsets, s.E, s.f, (int)s.TK, hq, sh);
+  return by_row(s.f, true, [&](auto w, auto v) {
+    constexpr int W = decltype(w)::value;
+    return launch_k(quantize_hidden_kernel<W, decltype(v)::value>, row_grid<W>(s.rows),
+                    row_block<W>(), 0, st, h, offsets, s.E, s.f, (int)s.TK, (long long)s.rows, hq,
+                    sh);
+  });
 }
 
 }  // namespace moe

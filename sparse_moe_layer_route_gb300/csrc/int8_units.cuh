@@ -1,0 +1,208 @@
+// What the 8-bit product kernels share: the work units of a grouped product and its stores.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "int8.cuh"
+
+namespace moe {
+
+constexpr int kInt8Threads = 512;
+constexpr int kInt8Ch = 128;                       // channels per MMA tile of one CTA (TMEM lanes)
+constexpr int kInt8StageK = 128;                   // k per shared-memory stage
+constexpr uint64_t kInt8WaitNs = 2000000000ull;    // 2 s per wait
+constexpr int kMaxSegs = 256 + 4;
+
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+constexpr uint32_t kInt8F16Clamp = 0x477FF000u;  // 65520.0f: the first value past fp16's range
+
+__device__ __forceinline__ uint16_t f16_sat(float v) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(v));
+  return (uint16_t)r;
+}
+
+struct Unit {
+  int seg;      // expert, or n_mat + shared expert
+  int ct;       // channel tile
+  int row0;     // first position
+  int rows;     // 1..NT
+  int brow0;    // first row of the activations
+};
+
+// Row tiles before each segment (first[n_segs] = all of them) and the segments' first positions.
+struct SegTable {
+  int first[kMaxSegs + 1];
+  int row0[kMaxSegs];
+  int rows[kMaxSegs];
+  int warp_tot[kInt8Threads / 32];
+};
+
+// Called by every thread of a CTA of kInt8Threads threads.
+__device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, int NT) {
+  const int n = g.n_mat + g.S, i = threadIdx.x;
+  const int lane = i & 31, warp = i >> 5;
+  int r0 = 0, nr = 0;
+  if (i < g.n_mat) {
+    int r1 = g.rows;
+    if (g.offsets != nullptr) {
+      r0 = g.offsets[i];
+      r1 = g.offsets[i + 1];
+      if (r0 < 0 || r1 < r0 || r1 > g.rows) {
+        atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
+        r0 = r1 = 0;
+      }
+    }
+    nr = r1 - r0;
+  } else if (i < n) {
+    r0 = g.rows + (i - g.n_mat) * g.T;
+    nr = g.T;
+  }
+  const int nt = (nr + NT - 1) / NT;
+  int v = nt;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) t.warp_tot[warp] = v;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += t.warp_tot[w];
+  if (i < n) {
+    t.first[i] = base + v - nt;
+    t.row0[i] = r0;
+    t.rows[i] = nr;
+    if (i == n - 1) t.first[n] = base + v;
+  }
+  __syncthreads();
+}
+
+// X_SHARED: the shared experts all read rows [rows, rows + T) of the activations (SwiGLU pass).
+template <bool X_SHARED>
+__device__ __forceinline__ Unit find_unit(const SegTable& t, const Int8Gemm& g, int n_ct, int NT,
+                                          long long w) {
+  int lo = 0, hi = g.n_mat + g.S;  // first[lo] * n_ct <= w < first[hi] * n_ct
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((long long)t.first[mid] * n_ct <= w)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int local = (int)(w - (long long)t.first[lo] * n_ct);
+  const int nt = t.first[lo + 1] - t.first[lo];
+  Unit u;
+  u.seg = lo;
+  u.ct = local / nt;
+  const int off = (local - u.ct * nt) * NT;
+  u.row0 = t.row0[lo] + off;
+  u.rows = min(NT, t.rows[lo] - off);
+  u.brow0 = X_SHARED && lo >= g.n_mat ? g.rows + off : u.row0;
+  return u;
+}
+
+// The output row and the row scale of position row0 + r of a unit: -1 past the unit's rows or where the slot is out of range.
+template <int PASS>
+__device__ __forceinline__ void unit_row(const Int8Gemm& g, const Unit& u, int r, int& orow,
+                                         float& sx) {
+  sx = 0.0f;
+  orow = -1;
+  if (r >= u.rows) return;
+  sx = g.sx[u.brow0 + r];
+  orow = u.row0 + r;
+  if (PASS == kInt8Slot && u.seg < g.n_mat) {
+    const int slot = g.perm_slot[u.row0 + r];
+    const bool good = slot >= 0 && slot < g.rows;
+    orow = good ? slot : -1;
+    if (good && g.topk_w != nullptr) sx *= g.topk_w[slot];
+  }
+}
+
+// ---------------------------------------------------------------------------- epilogue stores
+// An accumulator row is one output channel, so a thread's values belong to as many output rows, two or
+// four bytes in each. They pass through shared memory: a step stages kCols output rows of a panel of CH
+// channels (8 KB), and the four epilogue warps write them back as 16-byte pieces of whole rows. Two
+// buffers, so one barrier per step: a buffer is rewritten after the next step's barrier. (Stored
+// straight from the accumulators, an epilogue took about 150 clk per column, longer than the MMAs of a
+// unit with K = 1408.)
+constexpr int kInt8StepBytes = 8192;
+
+// The scales of 32 consecutive rows to registers, before the step's stores: the compiler keeps a shared
+// load behind the shared stores in front of it, and 32 of those in turn cost 3000 clk a step.
+__device__ __forceinline__ void load_scales(const float* usx, float (&s)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 4)
+    *reinterpret_cast<float4*>(s + j) = *reinterpret_cast<const float4*>(usx + j);
+}
+
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// A barrier that tells every epilogue thread whether `ok` held in all of them.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+template <int PASS, int OUT, int CH>
+struct Panel {
+  static constexpr int kSize = OUT == MOE_DTYPE_F32 ? 4 : 2;
+  static constexpr int kRowBytes = CH * kSize;
+  static constexpr int kCols = kInt8StepBytes / kRowBytes;  // output rows per step
+  static constexpr int kPieces = kRowBytes / 16;
+
+  static __device__ __forceinline__ void put(uint8_t* buf, int col, int ch, float y) {
+    uint8_t* at = buf + col * kRowBytes + ch * kSize;
+    if (OUT == MOE_DTYPE_F32)
+      *reinterpret_cast<float*>(at) = y;
+    else if (OUT == MOE_DTYPE_BF16)
+      *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16(y);
+    else if (PASS == kInt8Slot)
+      *reinterpret_cast<uint16_t*>(at) = f16_sat(y);
+    else
+      *reinterpret_cast<__half*>(at) = __float2half(y);
+  }
+
+  // t: 0..127. The step's rows to the output: channels [ch0, ch0 + CH) of rows orow[0, kCols).
+  static __device__ __forceinline__ void flush(const Int8Gemm& g, const uint8_t* buf,
+                                               const int* orow, int ch0, int t) {
+    uint8_t* out = static_cast<uint8_t*>(g.out);
+    const long long row_bytes = (long long)g.N * kSize;
+    if (ch0 + CH <= g.N && ((row_bytes | reinterpret_cast<long long>(out)) & 15) == 0) {
+      constexpr int kRows = 128 / kPieces;
+      const int piece = t % kPieces, r0 = t / kPieces;
+      uint4 v[kCols / kRows];
+#pragma unroll
+      for (int i = 0; i < kCols / kRows; ++i)
+        v[i] = *reinterpret_cast<const uint4*>(buf + (r0 + i * kRows) * kRowBytes + piece * 16);
+#pragma unroll
+      for (int i = 0; i < kCols / kRows; ++i) {
+        const int to = orow[r0 + i * kRows];
+        if (to >= 0)
+          *reinterpret_cast<uint4*>(out + to * row_bytes + (long long)ch0 * kSize + piece * 16) =
+              v[i];
+      }
+    } else if (t < CH && ch0 + t < g.N) {  // the last channels, or rows that are not in 16-byte pieces
+      for (int r = 0; r < kCols; ++r) {
+        const int to = orow[r];
+        if (to < 0) continue;
+        uint8_t* dst = out + to * row_bytes + (long long)(ch0 + t) * kSize;
+        const uint8_t* src = buf + r * kRowBytes + t * kSize;
+        if (kSize == 4)
+          *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+        else
+          *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+      }
+    }
+  }
+};
+
+}  // namespace moe
