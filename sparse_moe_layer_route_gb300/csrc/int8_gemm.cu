@@ -19,8 +19,8 @@
 //   warps 4-7    epilogue: scales, SwiGLU or gate weight, stores (32 channels of a row per warp)
 //   warps 8-15   widen the codes, four warps per channel tile: 64 codes of a thread's channel from
 //                shared memory to 32 TMEM columns (a slot of 64 k for both tiles is 64 columns)
-// Units go expert by expert, channel tile by channel tile, rows innermost, so CTAs that run together
-// share each weight tile through L2. Every wait is bounded (MOE_DEVFAULT_PIPELINE_TIMEOUT on expiry).
+// Units go segment by segment (find_unit), so CTAs that run together share weights and rows through L2.
+// Every wait is bounded (MOE_DEVFAULT_PIPELINE_TIMEOUT on expiry).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         if constexpr (PAIR) {
           steps(c, ch0, in0, rows_on, [&](int j) {
             const float gv = __uint_as_float(v0[j]) * (sx[j] * w0);
-            return gv / (1.0f + __expf(-gv)) * (__uint_as_float(v1[j]) * (sx[j] * w1));
+            return swiglu(gv, __uint_as_float(v1[j]) * (sx[j] * w1));
           });
         } else {
           steps(c, ch0, in0, rows_on, [&](int j) { return __uint_as_float(v0[j]) * (sx[j] * w0); });

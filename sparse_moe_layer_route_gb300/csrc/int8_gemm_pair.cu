@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
             const int col = j + 16 * up;
             const float s = up ? sx[16 + j] : sx[j];
             const float gv = (up ? got : x) * s, uv = (up ? y : got) * s;
-            P::put(buf, col, chl, gv / (1.0f + __expf(-gv)) * uv);
+            P::put(buf, col, chl, swiglu(gv, uv));
           }
           epilogue_barrier();
           P::flush(g, buf, orow + c * 32, ch0, t);

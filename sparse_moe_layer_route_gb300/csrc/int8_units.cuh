@@ -13,6 +13,9 @@ constexpr int kInt8Ch = 128;                       // channels per MMA tile of o
 constexpr int kInt8StageK = 128;                   // k per shared-memory stage
 constexpr uint64_t kInt8WaitNs = 2000000000ull;    // 2 s per wait
 constexpr int kMaxSegs = 256 + 4;
+// Channel tiles per block of units. A prefill product of 16384 x 7168 rows: with 16 tiles in a row of row
+// tiles each wave read all 235 MB of rows again, 634 us; blocks of 8 read them twice.
+constexpr int kCtBlock = 8;
 
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 constexpr uint32_t kInt8F16Clamp = 0x477FF000u;  // 65520.0f: the first value past fp16's range
@@ -21,6 +24,12 @@ __device__ __forceinline__ uint16_t f16_sat(float v) {
   uint32_t r;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(v));
   return (uint16_t)r;
+}
+
+// silu(g) * u. The quotient is the reciprocal's (2 ulp): an exact division branches, which kept the
+// epilogue's elements from overlapping (180 clk each).
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
 struct Unit {
@@ -91,12 +100,16 @@ __device__ __forceinline__ Unit find_unit(const SegTable& t, const Int8Gemm& g, 
     else
       hi = mid;
   }
+  // a segment's units go in blocks of kCtBlock channel tiles, in a block by row tiles: CTAs that run
+  // together share the weights of a block and read each row tile once per block
   const int local = (int)(w - (long long)t.first[lo] * n_ct);
   const int nt = t.first[lo + 1] - t.first[lo];
+  const int blk = local / (nt * kCtBlock), in = local - blk * (nt * kCtBlock);
+  const int wide = min(kCtBlock, n_ct - blk * kCtBlock);
   Unit u;
   u.seg = lo;
-  u.ct = local / nt;
-  const int off = (local - u.ct * nt) * NT;
+  u.ct = blk * kCtBlock + in % wide;
+  const int off = in / wide * NT;
   u.row0 = t.row0[lo] + off;
   u.rows = min(NT, t.rows[lo] - off);
   u.brow0 = X_SHARED && lo >= g.n_mat ? g.rows + off : u.row0;
