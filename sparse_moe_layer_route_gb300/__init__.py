@@ -377,75 +377,98 @@ def bias_update(counts, expert_bias, decay=0.99, rate=0.01, stream=None):
                                  _stream(stream)), "moe_bias_update")
 
 
+class _Torch:
+    """What the tensor checks need of torch, looked up once (the module loads without torch)."""
+
+    def __init__(self):
+        import torch
+        self.f32, self.bf16, self.f16 = torch.float32, torch.bfloat16, torch.float16
+        self.i8, self.i32 = torch.int8, torch.int32
+        self.code = {self.f32: DTYPE_F32, self.bf16: DTYPE_BF16, self.f16: DTYPE_F16}
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+_torch_names = None
+
+
+def _names() -> _Torch:
+    global _torch_names
+    if _torch_names is None:
+        _torch_names = _Torch()
+    return _torch_names
+
+
+def _stream_of(stream, t):
+    """The raw handle of `stream`, or of the current stream of tensor t's device."""
+    if stream is None:
+        raw = _names().raw_stream
+        return raw(t.get_device()) if raw is not None else _stream(None)
+    return _stream(stream)
+
+
 def _dtype_code(t, where):
-    code = _DTYPES.get(str(t.dtype))
+    code = _names().code.get(t.dtype)
     if code is None:
         raise ValueError(f"{where}: element type {t.dtype} is not supported")
     return code
 
 
-_DTYPES = {"torch.float32": DTYPE_F32, "torch.bfloat16": DTYPE_BF16, "torch.float16": DTYPE_F16}
-
-
 def _expect(where, name, t, shape, dtype):
-    """t: a contiguous tensor of this shape and element type on the GPU."""
-    if tuple(t.shape) != shape or str(t.dtype) != dtype or not t.is_contiguous() or not t.is_cuda:
+    """t: a contiguous tensor of this shape and element type on the GPU. Its address."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor {dtype} {shape}, not "
                          f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+    return t.data_ptr()
 
 
-def _expect_logits(where, gcfg, logits):
-    if tuple(logits.shape) != (gcfg.T, gcfg.E) or not logits.is_cuda or \
-            _DTYPES.get(str(logits.dtype)) != gcfg.dtype or \
-            (gcfg.T > 1 and logits.stride(0) != (gcfg.ld or gcfg.E)) or \
-            (gcfg.E > 1 and logits.stride(1) != 1):
+def _expect_logits(where, gcfg, T, E, logits):
+    if logits.shape != (T, E) or not logits.is_cuda or \
+            _names().code.get(logits.dtype) != gcfg.dtype or \
+            logits.stride() != (gcfg.ld or E, 1) and not (
+                (T <= 1 or logits.stride(0) == (gcfg.ld or E)) and
+                (E <= 1 or logits.stride(1) == 1)):
         raise ValueError(f"{where}: logits {logits.dtype} {tuple(logits.shape)} (strides "
                          f"{logits.stride()}) on {logits.device} do not fit the configuration")
+    return logits.data_ptr()
 
 
 def route_logits(gcfg: GateConfig, logits, expert_bias, topk_idx, topk_w, scores=None, stream=None):
     """Experts and weights from given router logits [T, E] (see moe_route_logits); scores: optional
     fp32 [T, E] that receives every expert's score."""
-    w, T, E, k = "moe_route_logits", gcfg.T, gcfg.E, gcfg.top_k
-    _expect_logits(w, gcfg, logits)
-    if expert_bias is not None:
-        _expect(w, "expert_bias", expert_bias, (E,), "torch.float32")
-    _expect(w, "topk_idx", topk_idx, (T, k), "torch.int32")
-    _expect(w, "topk_w", topk_w, (T, k), "torch.float32")
-    if scores is not None:
-        _expect(w, "scores", scores, (T, E), "torch.float32")
-    _check(lib().moe_route_logits(ctypes.byref(gcfg), logits.data_ptr(), _ptr(expert_bias),
-                                  topk_idx.data_ptr(), topk_w.data_ptr(), _ptr(scores),
-                                  _stream(stream)), w)
+    w, T, E, k, n = "moe_route_logits", gcfg.T, gcfg.E, gcfg.top_k, _names()
+    _check(lib().moe_route_logits(
+        ctypes.byref(gcfg), _expect_logits(w, gcfg, T, E, logits),
+        None if expert_bias is None else _expect(w, "expert_bias", expert_bias, (E,), n.f32),
+        _expect(w, "topk_idx", topk_idx, (T, k), n.i32),
+        _expect(w, "topk_w", topk_w, (T, k), n.f32),
+        None if scores is None else _expect(w, "scores", scores, (T, E), n.f32),
+        _stream_of(stream, logits)), w)
 
 
 def route_logits_backward(gcfg: GateConfig, logits, topk_idx, d_topk_w, d_scores, d_logits,
                           stream=None):
     """d_logits from the gradients of topk_w and scores (either may be None)."""
-    w, T, E, k = "moe_route_logits_backward", gcfg.T, gcfg.E, gcfg.top_k
-    _expect_logits(w, gcfg, logits)
-    _expect(w, "topk_idx", topk_idx, (T, k), "torch.int32")
-    if d_topk_w is not None:
-        _expect(w, "d_topk_w", d_topk_w, (T, k), "torch.float32")
-    if d_scores is not None:
-        _expect(w, "d_scores", d_scores, (T, E), "torch.float32")
-    _expect(w, "d_logits", d_logits, (T, E), str(logits.dtype))
-    _check(lib().moe_route_logits_backward(ctypes.byref(gcfg), logits.data_ptr(),
-                                           topk_idx.data_ptr(), _ptr(d_topk_w), _ptr(d_scores),
-                                           d_logits.data_ptr(), _stream(stream)), w)
+    w, T, E, k, n = "moe_route_logits_backward", gcfg.T, gcfg.E, gcfg.top_k, _names()
+    _check(lib().moe_route_logits_backward(
+        ctypes.byref(gcfg), _expect_logits(w, gcfg, T, E, logits),
+        _expect(w, "topk_idx", topk_idx, (T, k), n.i32),
+        None if d_topk_w is None else _expect(w, "d_topk_w", d_topk_w, (T, k), n.f32),
+        None if d_scores is None else _expect(w, "d_scores", d_scores, (T, E), n.f32),
+        _expect(w, "d_logits", d_logits, (T, E), logits.dtype),
+        _stream_of(stream, logits)), w)
 
 
 def quantize_rows(x, q, scale, stream=None):
     """x [T, d] (fp32, bf16 or fp16; rows may be strided) to q int8 [T, d] and scale fp32 [T]."""
-    w = "moe_quantize_rows"
+    w, n = "moe_quantize_rows", _names()
     T, d = x.shape
-    if not x.is_cuda or (d > 1 and x.stride(1) != 1):
+    step, unit = x.stride()
+    if not x.is_cuda or (d > 1 and unit != 1):
         raise ValueError(f"{w}: x must be a CUDA tensor with unit stride inside a row")
-    _expect(w, "q", q, (T, d), "torch.int8")
-    _expect(w, "scale", scale, (T,), "torch.float32")
-    _check(lib().moe_quantize_rows(T, d, _dtype_code(x, w), x.data_ptr(),
-                                   x.stride(0) if T > 1 else d, q.data_ptr(), scale.data_ptr(),
-                                   _stream(stream)), w)
+    _check(lib().moe_quantize_rows(T, d, _dtype_code(x, w), x.data_ptr(), step if T > 1 else d,
+                                   _expect(w, "q", q, (T, d), n.i8),
+                                   _expect(w, "scale", scale, (T,), n.f32),
+                                   _stream_of(stream, x)), w)
 
 
 def quantize_channels(W, stream=None):
@@ -453,11 +476,11 @@ def quantize_channels(W, stream=None):
     [n, N, K], scale fp32 [n, N]), new tensors on W's device."""
     import torch
     n, (K, N) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
-    _expect("moe_quantize_channels", "W", W, tuple(W.shape), "torch.bfloat16")
+    _expect("moe_quantize_channels", "W", W, tuple(W.shape), torch.bfloat16)
     q = torch.empty((n, N, K), dtype=torch.int8, device=W.device)
     scale = torch.empty((n, N), dtype=torch.float32, device=W.device)
     _check(lib().moe_quantize_channels(n, K, N, W.data_ptr(), q.data_ptr(), scale.data_ptr(),
-                                       _stream(stream)), "moe_quantize_channels")
+                                       _stream_of(stream, W)), "moe_quantize_channels")
     return q, scale
 
 
@@ -486,32 +509,30 @@ def alloc_int8_workspace(nbytes, device="cuda"):
 def int8_matmul(q_x, s_x, q_w, s_w, offsets, y, ws, stream=None):
     """y [rows, N] (fp32, bf16 or fp16) = (q_x q_w[e]^T) * s_x * s_w[e] over the row segments of
     offsets (int32 [n + 1] on the device; None: one matrix for every row)."""
-    w = "moe_int8_matmul"
+    w, t = "moe_int8_matmul", _names()
     rows, K = q_x.shape
-    n, N = q_w.shape[0], q_w.shape[1]
-    _expect(w, "q_x", q_x, (rows, K), "torch.int8")
-    _expect(w, "s_x", s_x, (rows,), "torch.float32")
-    _expect(w, "q_w", q_w, (n, N, K), "torch.int8")
-    _expect(w, "s_w", s_w, (n, N), "torch.float32")
-    if offsets is not None:
-        _expect(w, "offsets", offsets, (n + 1,), "torch.int32")
-    _expect(w, "y", y, (rows, N), str(y.dtype))
-    _check(lib().moe_int8_matmul(rows, K, N, n, q_x.data_ptr(), s_x.data_ptr(), q_w.data_ptr(),
-                                 s_w.data_ptr(), _ptr(offsets), _dtype_code(y, w), y.data_ptr(),
-                                 _ptr(ws), ws.numel(), _stream(stream)), w)
+    n, N, _ = q_w.shape
+    _check(lib().moe_int8_matmul(
+        rows, K, N, n, _expect(w, "q_x", q_x, (rows, K), t.i8),
+        _expect(w, "s_x", s_x, (rows,), t.f32), _expect(w, "q_w", q_w, (n, N, K), t.i8),
+        _expect(w, "s_w", s_w, (n, N), t.f32),
+        None if offsets is None else _expect(w, "offsets", offsets, (n + 1,), t.i32),
+        _dtype_code(y, w), _expect(w, "y", y, (rows, N), y.dtype), ws.data_ptr(), ws.numel(),
+        _stream_of(stream, q_x)), w)
 
 
 def make_int8_weights(gate, up, down, sh_gate=None, sh_up=None, sh_down=None) -> MoeInt8Weights:
     """From quantize_channels() results (kept alive by the struct)."""
-    mats = (gate, up, down, sh_gate, sh_up, sh_down)
+    mats, t = (gate, up, down, sh_gate, sh_up, sh_down), _names()
     for m in mats:
         if m is not None:
             n, N, K = m[0].shape
-            _expect("make_int8_weights", "q", m[0], (n, N, K), "torch.int8")
-            _expect("make_int8_weights", "scale", m[1], (n, N), "torch.float32")
+            _expect("make_int8_weights", "q", m[0], (n, N, K), t.i8)
+            _expect("make_int8_weights", "scale", m[1], (n, N), t.f32)
     w = MoeInt8Weights(*[MoeInt8Matrix() if m is None else MoeInt8Matrix(_ptr(m[0]), _ptr(m[1]))
                          for m in mats])
     w._tensors = mats
+    w._shapes = tuple(None if m is None else tuple(m[0].shape) for m in mats)
     return w
 
 
@@ -519,23 +540,19 @@ def grouped_ffn_int8(cfg, x, perm_slot, offsets, topk_w, weights: MoeInt8Weights
                      stream=None):
     """y_slot [T*k + S*T, d] float16: the routed and shared experts on 8-bit weights and
     activations (see moe_grouped_ffn_int8)."""
-    w, T, d, k = "moe_grouped_ffn_int8", cfg.T, cfg.d, cfg.top_k
-    _expect(w, "x", x, (T, d), "torch.bfloat16")
-    _expect(w, "perm_slot", perm_slot, (T * k,), "torch.int32")
-    _expect(w, "offsets", offsets, (cfg.E + 1,), "torch.int32")
-    if topk_w is not None:
-        _expect(w, "topk_w", topk_w, (T, k), "torch.float32")
-    _expect(w, "y_slot", y_slot, (T * (k + cfg.n_shared), d), "torch.float16")
-    for name, n, N, K in (("gate", cfg.E, cfg.d_ff, d), ("up", cfg.E, cfg.d_ff, d),
-                          ("down", cfg.E, d, cfg.d_ff), ("sh_gate", cfg.n_shared, cfg.d_ff, d),
-                          ("sh_up", cfg.n_shared, cfg.d_ff, d),
-                          ("sh_down", cfg.n_shared, d, cfg.d_ff)):
-        m = weights._tensors[MoeInt8Weights._names.index(name)]
-        if n and (m is None or tuple(m[0].shape) != (n, N, K)):
-            raise ValueError(f"{w}: weights.{name} must hold {(n, N, K)}")
-    _check(lib().moe_grouped_ffn_int8(ctypes.byref(cfg), _ptr(x), _ptr(perm_slot), _ptr(offsets),
-                                      _ptr(topk_w), ctypes.byref(weights), _ptr(y_slot), _ptr(ws),
-                                      ws.numel(), _stream(stream)), w)
+    w, t = "moe_grouped_ffn_int8", _names()
+    T, d, k, E, f, S = cfg.T, cfg.d, cfg.top_k, cfg.E, cfg.d_ff, cfg.n_shared
+    into, back = (E, f, d), (E, d, f)
+    want = (into, into, back) + (((S, f, d), (S, f, d), (S, d, f)) if S else ())
+    if weights._shapes[:len(want)] != want:
+        raise ValueError(f"{w}: weights of shapes {weights._shapes} do not fit the configuration")
+    _check(lib().moe_grouped_ffn_int8(
+        ctypes.byref(cfg), _expect(w, "x", x, (T, d), t.bf16),
+        _expect(w, "perm_slot", perm_slot, (T * k,), t.i32),
+        _expect(w, "offsets", offsets, (E + 1,), t.i32),
+        None if topk_w is None else _expect(w, "topk_w", topk_w, (T, k), t.f32),
+        ctypes.byref(weights), _expect(w, "y_slot", y_slot, (T * (k + S), d), t.f16),
+        ws.data_ptr(), ws.numel(), _stream_of(stream, x)), w)
 
 
 def check_bounded_waits(limit_ns, expired, ws, stream=None):

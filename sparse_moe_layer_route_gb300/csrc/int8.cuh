@@ -34,10 +34,11 @@ __device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& h
 
 // One grouped product. Segment e < n_mat holds positions [offsets[e], offsets[e + 1]) (offsets
 // NULL: all `rows`); with shared experts, segment n_mat + s is positions
-// [rows + s * T, rows + (s + 1) * T). The activations' codes are held in fp16 (exact), row p for
+// [rows + s * T, rows + (s + 1) * T). The activations' codes, in fp16 (exact) or 8 bits, have row p for
 // position p, except that the SwiGLU pass's shared experts all read rows [rows, rows + T).
 struct Int8Gemm {
-  const uint16_t* xq;      // [x_rows, K] fp16
+  const uint16_t* xq;      // [x_rows, K] fp16 (tensor cores)
+  const int8_t* x8;        // [x_rows, K] (launch_int8_gemv)
   const float* sx;         // [x_rows]
   long long x_rows;
   const int8_t *qw, *qw2;  // [n_mat, N, K]; qw2: the up projection of the SwiGLU pass
@@ -59,7 +60,10 @@ enum Int8Pass {
   kInt8Slot = 2     // out [slot, N] fp16 = gate weight * product
 };
 
+// Tensor cores: long segments on CTA pairs (int8_gemm_pair.cu), others on single CTAs (int8_gemm.cu).
 cudaError_t launch_int8_gemm_pair(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
+// A few rows (int8_gemv.cu); most_rows: no segment has more.
+cudaError_t launch_int8_gemv(Int8Pass pass, const Int8Gemm& g, int most_rows, cudaStream_t st);
 cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
 cudaError_t launch_quantize_rows(int T, int d, int dtype, const void* x, long long ld, int8_t* q,
                                  float* scale, cudaStream_t st);
@@ -69,12 +73,14 @@ cudaError_t launch_quantize_channels(int n_mat, int K, int N, const uint16_t* W,
 cudaError_t launch_widen_codes(const int8_t* q, uint16_t* xq, long long n, cudaStream_t st);
 // The FFN's activations in expert order: rows [0, TK) from the token of slot perm_slot[p] (written
 // for p < offsets[E]; a slot outside [0, TK) becomes a zero row and MOE_DEVFAULT_BAD_TILE), then,
-// with shared experts, rows [TK, TK + T) from every token. Codes in fp16.
+// with shared experts, rows [TK, TK + T) from every token. Codes as uint16_t (fp16) or int8_t.
+template <typename QT>
 cudaError_t launch_quantize_gather(const Shape& s, const uint16_t* x, const int32_t* perm_slot,
-                                   const int32_t* offsets, uint16_t* xq, float* sx, int* status,
+                                   const int32_t* offsets, QT* xq, float* sx, int* status,
                                    cudaStream_t st);
-// H [rows, f] fp32 to fp16 codes and scales; positions in [offsets[E], TK) are skipped.
-cudaError_t launch_quantize_hidden(const Shape& s, const float* h, const int32_t* offsets,
-                                   uint16_t* hq, float* sh, cudaStream_t st);
+// H [rows, f] fp32 to codes and scales; positions in [offsets[E], TK) are skipped.
+template <typename QT>
+cudaError_t launch_quantize_hidden(const Shape& s, const float* h, const int32_t* offsets, QT* hq,
+                                   float* sh, cudaStream_t st);
 
 }  // namespace moe

@@ -10,6 +10,7 @@ namespace moe {
 namespace {
 
 constexpr size_t kHead = 512;  // status word and counter block, as in every workspace
+constexpr int kFewRows = 4;    // tokens up to which the products take int8_gemv.cu
 
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 int dtype_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
@@ -111,11 +112,7 @@ moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, co
   moe_int8_matmul_workspace_size(rows, K, N, n_mat, &need);
   if ((r = check_ws(ws, ws_bytes, need)) != MOE_OK) return r;
   const cudaStream_t st = (cudaStream_t)stream;
-  uint16_t* xq = at<uint16_t>(ws, kHead);
-  const cudaError_t e = launch_widen_codes(q_x, xq, (long long)rows * K, st);
-  if (e != cudaSuccess) return MOE_ERR_CUDA;
   Int8Gemm g = {};
-  g.xq = xq;
   g.x_rows = rows;
   g.sx = s_x;
   g.qw = q_w;
@@ -129,7 +126,14 @@ moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, co
   g.N = N;
   g.n_mat = n_mat;
   g.T = 1;
-  return cuda_status(launch_int8_gemm(kInt8Matrix, g, st));
+  if (rows <= kFewRows) {
+    g.x8 = q_x;
+    return cuda_status(launch_int8_gemv(kInt8Matrix, g, rows, st));
+  }
+  uint16_t* xq = at<uint16_t>(ws, kHead);
+  g.xq = xq;
+  const cudaError_t e = launch_widen_codes(q_x, xq, (long long)rows * K, st);
+  return cuda_status(e != cudaSuccess ? e : launch_int8_gemm(kInt8Matrix, g, st));
 }
 
 moe_status moe_grouped_ffn_int8_workspace_size(const moe_config* cfg, size_t* bytes) {
@@ -160,11 +164,12 @@ moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const 
   const Shape s = make_shape(*cfg);
   const FfnLayout L = ffn_layout(s);
   const cudaStream_t st = (cudaStream_t)stream;
+  // few tokens: 8-bit codes and integer dot products, else fp16 codes and the tensor cores
+  const bool few = s.T <= kFewRows;
   int* status = at<int>(ws, 0);
-  cudaError_t e = launch_quantize_gather(s, x, perm_slot, offsets, at<uint16_t>(ws, L.xq),
-                                         at<float>(ws, L.sx), status, st);
   Int8Gemm g = {};
   g.xq = at<uint16_t>(ws, L.xq);
+  g.x8 = at<int8_t>(ws, L.xq);
   g.x_rows = s.TK + (s.S > 0 ? s.T : 0);
   g.sx = at<float>(ws, L.sx);
   g.qw = w->gate.q;
@@ -184,27 +189,36 @@ moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const 
   g.n_mat = s.E;
   g.S = s.S;
   g.T = s.T;
-  if (e == cudaSuccess) e = launch_int8_gemm(kInt8SwiGLU, g, st);
+  auto product = [&](Int8Pass pass) {
+    return few ? launch_int8_gemv(pass, g, s.T, st) : launch_int8_gemm(pass, g, st);
+  };
+  cudaError_t e =
+      few ? launch_quantize_gather(s, x, perm_slot, offsets, at<int8_t>(ws, L.xq),
+                                   at<float>(ws, L.sx), status, st)
+          : launch_quantize_gather(s, x, perm_slot, offsets, at<uint16_t>(ws, L.xq),
+                                   at<float>(ws, L.sx), status, st);
+  if (e == cudaSuccess) e = product(kInt8SwiGLU);
   if (e == cudaSuccess)
-    e = launch_quantize_hidden(s, at<float>(ws, L.h), offsets, at<uint16_t>(ws, L.hq),
-                               at<float>(ws, L.sh), st);
+    e = few ? launch_quantize_hidden(s, at<float>(ws, L.h), offsets, at<int8_t>(ws, L.hq),
+                                     at<float>(ws, L.sh), st)
+            : launch_quantize_hidden(s, at<float>(ws, L.h), offsets, at<uint16_t>(ws, L.hq),
+                                     at<float>(ws, L.sh), st);
   g.xq = at<uint16_t>(ws, L.hq);
+  g.x8 = at<int8_t>(ws, L.hq);
   g.x_rows = s.rows;
   g.sx = at<float>(ws, L.sh);
   g.perm_slot = perm_slot;
   g.qw = w->down.q;
   g.sw = w->down.scale;
-  g.qw2 = nullptr;
-  g.sw2 = nullptr;
   g.sh_qw = w->sh_down.q;
   g.sh_sw = w->sh_down.scale;
-  g.sh_qw2 = nullptr;
-  g.sh_sw2 = nullptr;
+  g.qw2 = g.sh_qw2 = nullptr;
+  g.sw2 = g.sh_sw2 = nullptr;
   g.topk_w = topk_w;
   g.out = y_slot;
   g.K = s.f;
   g.N = s.d;
-  if (e == cudaSuccess) e = launch_int8_gemm(kInt8Slot, g, st);
+  if (e == cudaSuccess) e = product(kInt8Slot);
   return cuda_status(e);
 }
 

@@ -1,0 +1,219 @@
+// Grouped products of 8-bit integers for a few rows: every weight is read once, by integer dot products
+// of four (exact in 32 bits), with no tile to fill.
+//
+// Bound by the weight bytes. A warp takes kStreams output channels (SwiGLU pass: half as many channels of
+// gate and of up) of one row tile of R rows and runs down K, 16 codes a lane and step: one 16-byte load per
+// channel, past L1, four steps of each in flight (8 KB a warp), and one load per row, from L1, where the
+// SM's warps share the rows. The lanes' sums meet in one reduction per channel and row. A tile of
+// tensor-core units has 128 channels, so a single row of a [14336 x 4096] product would occupy 56 of the
+// 152 SMs for 30 us; here its 3584 warps spread over all of them.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "int8.cuh"
+#include "int8_units.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStreams = 4;  // channels in flight per warp
+constexpr int kSteps = 4;    // 512-byte steps of each in flight
+
+// 16 weight codes, read once: not kept in L1.
+__device__ __forceinline__ int4 load_once(const int8_t* p) {
+  int4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <int OUT, bool SLOT>
+__device__ __forceinline__ void store_one(void* out, long long at, float y) {
+  if (OUT == MOE_DTYPE_F32)
+    static_cast<float*>(out)[at] = y;
+  else if (OUT == MOE_DTYPE_BF16)
+    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16(y);
+  else if (SLOT)
+    static_cast<uint16_t*>(out)[at] = f16_sat(y);
+  else
+    static_cast<__half*>(out)[at] = __float2half(y);
+}
+
+// Row tile `tile` (R rows) of the segments, counted segment by segment: found by the CTA's first warp,
+// 32 segments at a time. seg -1: past the last tile.
+template <int R>
+__device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int tile, int lane) {
+  const int n = g.n_mat + g.S;
+  int before = 0;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const int s = s0 + lane;
+    int r0 = 0, nr = 0;
+    if (s < g.n_mat) {
+      int r1 = g.rows;
+      if (g.offsets != nullptr) {
+        r0 = g.offsets[s];
+        r1 = g.offsets[s + 1];
+        if (r0 < 0 || r1 < r0 || r1 > g.rows) {
+          atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
+          r0 = r1 = 0;
+        }
+      }
+      nr = r1 - r0;
+    } else if (s < n) {
+      r0 = g.rows + (s - g.n_mat) * g.T;
+      nr = g.T;
+    }
+    const int nt = (nr + R - 1) / R;
+    int v = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
+    }
+    const int first = before + v - nt;
+    const unsigned hit = __ballot_sync(0xffffffffu, tile >= first && tile < first + nt);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int off = (tile - __shfl_sync(0xffffffffu, first, src)) * R;
+      Unit u;
+      u.seg = s0 + src;
+      u.ct = 0;
+      u.row0 = __shfl_sync(0xffffffffu, r0, src) + off;
+      u.rows = min(R, __shfl_sync(0xffffffffu, nr, src) - off);
+      u.brow0 = x_shared && u.seg >= g.n_mat ? g.rows + off : u.row0;
+      return u;
+    }
+    before += __shfl_sync(0xffffffffu, v, 31);
+  }
+  Unit u;
+  u.seg = -1;
+  u.ct = u.row0 = u.rows = u.brow0 = 0;
+  return u;
+}
+
+template <int PASS, int OUT, int R>
+__global__ void __launch_bounds__(kThreads) int8_gemv_kernel(const Int8Gemm g) {
+  constexpr bool GLU = PASS == kInt8SwiGLU;
+  constexpr int CH = GLU ? kStreams / 2 : kStreams;  // channels per warp
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Unit u = find_tile<R>(g, GLU, blockIdx.y, lane);  // every warp: no barrier
+  if (u.seg < 0) return;
+  const int ch0 = (blockIdx.x * (kThreads / 32) + warp) * CH;
+  if (ch0 >= g.N) return;
+  const bool sh = u.seg >= g.n_mat;
+  const long long ex = sh ? u.seg - g.n_mat : u.seg;
+  const int8_t* wa = (sh ? g.sh_qw : g.qw) + ex * g.N * g.K;
+  const int8_t* wb = GLU ? (sh ? g.sh_qw2 : g.qw2) + ex * g.N * g.K : wa;
+  const int8_t* w[kStreams];
+#pragma unroll
+  for (int c = 0; c < kStreams; ++c) {
+    const int ch = min(ch0 + (GLU ? c % CH : c), g.N - 1);  // past the end: the last channel again
+    w[c] = (GLU && c >= CH ? wb : wa) + (long long)ch * g.K + lane * 16;
+  }
+  const int8_t* x[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    x[r] = g.x8 + (long long)(u.brow0 + min(r, u.rows - 1)) * g.K + lane * 16;
+  int acc[kStreams][R];
+#pragma unroll
+  for (int c = 0; c < kStreams; ++c)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[c][r] = 0;
+  for (int k0 = 0; k0 < g.K; k0 += 512 * kSteps) {
+    int4 v[kSteps][kStreams];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int k = k0 + i * 512;
+      if (k + lane * 16 < g.K) {
+#pragma unroll
+        for (int c = 0; c < kStreams; ++c) v[i][c] = load_once(w[c] + k);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int k = k0 + i * 512;
+      if (k + lane * 16 < g.K) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int4 a = __ldg(reinterpret_cast<const int4*>(x[r] + k));
+#pragma unroll
+          for (int c = 0; c < kStreams; ++c) {
+            acc[c][r] = __dp4a(v[i][c].x, a.x, acc[c][r]);
+            acc[c][r] = __dp4a(v[i][c].y, a.y, acc[c][r]);
+            acc[c][r] = __dp4a(v[i][c].z, a.z, acc[c][r]);
+            acc[c][r] = __dp4a(v[i][c].w, a.w, acc[c][r]);
+          }
+        }
+      }
+    }
+  }
+  // lane r * CH + c finishes row r, channel ch0 + c
+  float mine = 0.0f, mine2 = 0.0f;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int s = __reduce_add_sync(0xffffffffu, acc[c][r]);
+      if (lane == r * CH + c) mine = (float)s;
+      if (GLU) {
+        const int s2 = __reduce_add_sync(0xffffffffu, acc[GLU ? CH + c : c][r]);
+        if (lane == r * CH + c) mine2 = (float)s2;
+      }
+    }
+  const int r = lane / CH, ch = ch0 + lane % CH;
+  bool clamped = false;
+  if (r < u.rows && r < R && ch < g.N) {
+    int orow;
+    float sx;
+    unit_row<PASS>(g, u, r, orow, sx);
+    if (orow >= 0) {
+      const long long at = (long long)orow * g.N + ch;
+      float y = mine * (sx * (sh ? g.sh_sw : g.sw)[ex * g.N + ch]);
+      if (GLU) y = swiglu(y, mine2 * (sx * (sh ? g.sh_sw2 : g.sw2)[ex * g.N + ch]));
+      store_one<OUT, PASS == kInt8Slot>(g.out, at, y);
+      clamped = PASS == kInt8Slot && mag_bits(y) >= kInt8F16Clamp;
+    }
+  }
+  if (PASS == kInt8Slot && clamped) atomicOr(g.status, MOE_DEVFAULT_FP16_RANGE);
+}
+
+template <int PASS, int OUT>
+cudaError_t launch_out(const Int8Gemm& g, int most_rows, cudaStream_t st) {
+  constexpr int kCta = kThreads / 32 * (PASS == kInt8SwiGLU ? kStreams / 2 : kStreams);
+  const unsigned gx = (unsigned)((g.N + kCta - 1) / kCta);
+  auto go = [&](auto kern, int R) {
+    // an upper bound of the row tiles: a segment's rows over R and one ragged tile each, and no more
+    // than one tile per row
+    const long long tiles =
+        min((long long)g.rows, (long long)g.rows / R + g.n_mat) + (long long)g.S * ((g.T + R - 1) / R);
+    if (tiles > 65535) return cudaErrorInvalidValue;
+    return launch_k(kern, dim3(gx, (unsigned)tiles), dim3(kThreads), 0, st, g);
+  };
+  if (most_rows <= 1) return go(int8_gemv_kernel<PASS, OUT, 1>, 1);
+  if (most_rows <= 2) return go(int8_gemv_kernel<PASS, OUT, 2>, 2);
+  if (most_rows <= 4) return go(int8_gemv_kernel<PASS, OUT, 4>, 4);
+  return go(int8_gemv_kernel<PASS, OUT, 8>, 8);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_gemv(Int8Pass pass, const Int8Gemm& g, int most_rows, cudaStream_t st) {
+  switch (pass) {
+    case kInt8SwiGLU: return launch_out<kInt8SwiGLU, MOE_DTYPE_F32>(g, most_rows, st);
+    case kInt8Slot: return launch_out<kInt8Slot, MOE_DTYPE_F16>(g, most_rows, st);
+    default: break;
+  }
+  switch (g.out_dtype) {
+    case MOE_DTYPE_F32: return launch_out<kInt8Matrix, MOE_DTYPE_F32>(g, most_rows, st);
+    case MOE_DTYPE_BF16: return launch_out<kInt8Matrix, MOE_DTYPE_BF16>(g, most_rows, st);
+    default: return launch_out<kInt8Matrix, MOE_DTYPE_F16>(g, most_rows, st);
+  }
+}
+
+}  // namespace moe

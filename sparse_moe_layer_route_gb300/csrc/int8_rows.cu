@@ -167,11 +167,11 @@ __global__ void __launch_bounds__(W == 32 ? kThreads : W)
                        warp_top);
 }
 
-template <int W, bool VEC>
+template <int W, bool VEC, typename QT>
 __global__ void __launch_bounds__(W == 32 ? kThreads : W) quantize_gather_kernel(
     const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ perm_slot,
     const int32_t* __restrict__ offsets, int E, int k, int d, int TK, int rows,
-    uint16_t* __restrict__ xq, float* __restrict__ sx, int* status) {
+    QT* __restrict__ xq, float* __restrict__ sx, int* status) {
   __shared__ uint32_t warp_top[W / 32];
   griddep_wait();
   const long long p = W == 32 ? (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)
@@ -195,10 +195,10 @@ __global__ void __launch_bounds__(W == 32 ? kThreads : W) quantize_gather_kernel
   quantize_row<W, VEC>(x + token * d, d, xq + p * d, sx + p, t, warp_top);
 }
 
-template <int W, bool VEC>
+template <int W, bool VEC, typename QT>
 __global__ void __launch_bounds__(W == 32 ? kThreads : W)
     quantize_hidden_kernel(const float* __restrict__ h, const int32_t* __restrict__ offsets, int E,
-                           int f, int TK, long long rows, uint16_t* __restrict__ hq,
+                           int f, int TK, long long rows, QT* __restrict__ hq,
                            float* __restrict__ sh) {
   __shared__ uint32_t warp_top[W / 32];
   griddep_wait();
@@ -324,26 +324,39 @@ cudaError_t launch_widen_codes(const int8_t* q, uint16_t* xq, long long n, cudaS
                   reinterpret_cast<uint4*>(xq), n16);
 }
 
+template <typename QT>
 cudaError_t launch_quantize_gather(const Shape& s, const uint16_t* x, const int32_t* perm_slot,
-                                   const int32_t* offsets, uint16_t* xq, float* sx, int* status,
+                                   const int32_t* offsets, QT* xq, float* sx, int* status,
                                    cudaStream_t st) {
   const long long rows = s.TK + (s.S > 0 ? s.T : 0);
   return by_row(s.d, true, [&](auto w, auto v) {  // d is a multiple of 64, x 16-byte aligned
     constexpr int W = decltype(w)::value;
-    return launch_k(quantize_gather_kernel<W, decltype(v)::value>, row_grid<W>(rows),
+    return launch_k(quantize_gather_kernel<W, decltype(v)::value, QT>, row_grid<W>(rows),
                     row_block<W>(), 0, st, reinterpret_cast<const __nv_bfloat16*>(x), perm_slot,
                     offsets, s.E, s.k, s.d, (int)s.TK, (int)rows, xq, sx, status);
   });
 }
 
-cudaError_t launch_quantize_hidden(const Shape& s, const float* h, const int32_t* offsets,
-                                   uint16_t* hq, float* sh, cudaStream_t st) {
+template <typename QT>
+cudaError_t launch_quantize_hidden(const Shape& s, const float* h, const int32_t* offsets, QT* hq,
+                                   float* sh, cudaStream_t st) {
   return by_row(s.f, true, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value;
-    return launch_k(quantize_hidden_kernel<W, decltype(v)::value>, row_grid<W>(s.rows),
+    return launch_k(quantize_hidden_kernel<W, decltype(v)::value, QT>, row_grid<W>(s.rows),
                     row_block<W>(), 0, st, h, offsets, s.E, s.f, (int)s.TK, (long long)s.rows, hq,
                     sh);
   });
 }
+
+template cudaError_t launch_quantize_gather<uint16_t>(const Shape&, const uint16_t*, const int32_t*,
+                                                     const int32_t*, uint16_t*, float*, int*,
+                                                     cudaStream_t);
+template cudaError_t launch_quantize_gather<int8_t>(const Shape&, const uint16_t*, const int32_t*,
+                                                   const int32_t*, int8_t*, float*, int*,
+                                                   cudaStream_t);
+template cudaError_t launch_quantize_hidden<uint16_t>(const Shape&, const float*, const int32_t*,
+                                                     uint16_t*, float*, cudaStream_t);
+template cudaError_t launch_quantize_hidden<int8_t>(const Shape&, const float*, const int32_t*,
+                                                   int8_t*, float*, cudaStream_t);
 
 }  // namespace moe
