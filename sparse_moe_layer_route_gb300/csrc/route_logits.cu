@@ -1,10 +1,18 @@
 // Routing from given logits (softmax or sigmoid scores, balance bias, expert groups, top-k,
 // renormalised weights) and the gradient of its weights and scores to the logits.
 //
-// One warp per token. Lane l holds the logits of experts [l * NV, (l + 1) * NV), NV the power of two
-// with 32 * NV >= E, so the lowest lane that holds a value also holds its lowest index.
+// Forward: one warp per token and persistent warps, so the bias stays in registers and the next row is
+// on its way. Lane l holds experts [l * NV, (l + 1) * NV), NV the power of two with 32 * NV >= E: the
+// lowest lane that holds a value also holds its lowest index. Bound by instructions, not bytes: a row of
+// 256 fp32 logits is 1 KB, 0.15 us of one SM's share of HBM, and its 256 exact sigmoids alone are about
+// 130 warp instructions. So each lane keeps its two best experts, and a round of the top-k is one
+// warp-wide integer maximum over the lanes' best, a ballot for the lowest lane and a shuffle; a lane is
+// searched again only when two of its experts were taken.
+// Backward: one warp per token, or per four tokens where only the chosen experts have a gradient: their
+// values are put into zeroed rows in shared memory, which are written in 16-byte pieces. Bound by HBM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -13,7 +21,8 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;  // tokens per CTA
+constexpr int kWarps = 8;      // tokens at a time per CTA
+constexpr int kCtasPerSm = 4;  // resident CTAs of the forward kernel (its registers)
 constexpr unsigned kFull = 0xffffffffu;
 
 // Order-preserving key of a rank: larger float, larger key. 0 is below every key (an expert that
@@ -45,6 +54,15 @@ __device__ __forceinline__ float warp_max(float v) {
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
+// The same value for -80 <= l, without the division's branch: one Newton step from a reciprocal within
+// an ulp is the correctly rounded one (Markstein 1990) unless the divisor's mantissa is all ones.
+__device__ __forceinline__ float sigmoid_fast(float l) {
+  const float d = 1.0f + expf(-l);
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d));
+  return fmaf(fmaf(-d, y, 1.0f), y, y);
+}
+
 // a + b as an unevaluated pair (hi, lo) added to (hi, lo): the softmax denominator in about 46
 // bits. Rounded once to fp32 it does not depend on the order of the sum, so neither does a choice
 // that adds the bias to the probabilities (fp64 adds run at a small fraction of this rate here).
@@ -66,18 +84,21 @@ struct GateArgs {
   long long ld;
   int T, E, k, G, Gk;
   bool top2, renorm;
+  bool vec, vec_scores;  // rows of logits / scores are in 16-byte pieces
+  int lanes;             // lanes per group where a group is a power of two of whole lanes, else 0
   float scale;
 };
 
-// Softmax of the warp's logits (experts beyond E are -infinity): s and nothing else. An all
-// switched-off row has every score 0.
+// Softmax of the warp's logits (experts beyond E are -infinity). top and total: the row's exp offset and
+// denominator (1 for an all switched-off row, whose scores are 0).
 template <int NV>
-__device__ __forceinline__ void softmax_scores(const float (&l)[NV], float (&s)[NV]) {
+__device__ __forceinline__ void softmax_scores(const float (&l)[NV], float (&s)[NV], float& top,
+                                               float& total) {
   float m = l[0];
 #pragma unroll
   for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
   m = warp_max(m);
-  const float top = m == -INFINITY ? 0.0f : m;
+  top = m == -INFINITY ? 0.0f : m;
   float hi = 0.0f, lo = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -88,136 +109,265 @@ __device__ __forceinline__ void softmax_scores(const float (&l)[NV], float (&s)[
   for (int o = 16; o; o >>= 1)
     pair_add(hi, lo, __shfl_xor_sync(kFull, hi, o), __shfl_xor_sync(kFull, lo, o));
   // lanes may differ in the last place of lo only; lane 0's pair is everyone's
-  const float total = __shfl_sync(kFull, __fadd_rn(hi, lo), 0);
+  total = __shfl_sync(kFull, __fadd_rn(hi, lo), 0);
+  total = total == 0.0f ? 1.0f : total;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) s[i] = s[i] / (total == 0.0f ? 1.0f : total);
+  for (int i = 0; i < NV; ++i) s[i] = s[i] / total;
+}
+
+// NV consecutive elements from p; vec: p is aligned to min(16, their bytes) and all are there.
+template <int NV>
+__device__ __forceinline__ void load_run(const float* p, float (&v)[NV]) {
+  if constexpr (NV >= 4) {
+#pragma unroll
+    for (int i = 0; i < NV; i += 4)
+      *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(p + i);
+  } else if constexpr (NV == 2) {
+    *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p);
+  } else {
+    v[0] = p[0];
+  }
+}
+template <int NV>
+__device__ __forceinline__ void load_run(const __nv_bfloat16* p, float (&v)[NV]) {
+  if constexpr (NV == 1) {
+    v[0] = __bfloat162float(p[0]);
+  } else {
+    uint32_t w[NV / 2];
+    if constexpr (NV == 8)
+      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    else if constexpr (NV == 4)
+      *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    else
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+    for (int i = 0; i < NV / 2; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+// This lane's logits of a row; -infinity past E.
+template <int NV, typename LT>
+__device__ __forceinline__ void load_row(const LT* row, int e0, int E, bool vec, float (&l)[NV]) {
+  if (vec && e0 + NV <= E) {
+    load_run<NV>(row + e0, l);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = e0 + i < E ? load_logit(row + e0 + i) : -INFINITY;
+  }
+}
+
+// The lane's two largest keys and their slots among those whose bit of `gone` is clear; a tie keeps the
+// lower slot first.
+template <int NV>
+__device__ __forceinline__ void two_best(const uint32_t (&key)[NV], uint32_t gone, uint32_t& b1,
+                                         int& i1, uint32_t& b2, int& i2) {
+  b1 = b2 = 0u;
+  i1 = i2 = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t v = (gone >> i) & 1u ? 0u : key[i];
+    const bool p = v > b1, q = v > b2;
+    i2 = p ? i1 : (q ? i : i2);
+    b2 = max(b2, min(b1, v));
+    i1 = p ? i : i1;
+    b1 = max(b1, v);
+  }
+}
+
+// Groups of any size: lane g ranks groups g and g + 32 from a copy of the row's keys in shared memory.
+// Sets the bits of `gone` whose experts' groups are not kept.
+template <int NV>
+__device__ __forceinline__ void drop_groups(const GateArgs& a, const uint32_t (&key)[NV],
+                                               uint32_t* mine, int e0, int lane, uint32_t& gone) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (e0 + i < a.E) mine[e0 + i] = key[i];
+  __syncwarp();
+  const int size = a.E / a.G;
+  uint32_t gk[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int g = lane + 32 * h;
+    gk[h] = 0u;
+    if (g < a.G) {
+      uint32_t b1 = 0u, b2 = 0u;
+      for (int i = 0; i < size; ++i) {
+        const uint32_t v = mine[g * size + i];
+        b2 = max(b2, min(b1, v));
+        b1 = max(b1, v);
+      }
+      gk[h] = a.top2 && b2 > kMaskedKey ? rank_key(key_rank(b1) + key_rank(b2)) : b1;
+    }
+  }
+  __syncwarp();  // the copy is overwritten by the warp's next row
+  int before[2] = {0, 0};
+  for (int g = 0; g < a.G; ++g) {
+    const uint32_t v = __shfl_sync(kFull, g < 32 ? gk[0] : gk[1], g & 31);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) before[h] += v > gk[h] || (v == gk[h] && g < lane + 32 * h);
+  }
+  const unsigned keep0 = __ballot_sync(kFull, lane < a.G && before[0] < a.Gk);
+  const unsigned keep1 = __ballot_sync(kFull, lane + 32 < a.G && before[1] < a.Gk);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int g = min(e0 + i, a.E - 1) / size;
+    if (!(((g < 32 ? keep0 : keep1) >> (g & 31)) & 1u)) gone |= 1u << i;
+  }
 }
 
 template <int NV, typename LT, bool SIGMOID>
-__global__ void __launch_bounds__(32 * kWarps) gate_kernel(const GateArgs a) {
-  extern __shared__ uint32_t group_smem[];  // [kWarps][E] keys, only with groups
+__global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const GateArgs a) {
+  extern __shared__ uint32_t group_smem[];  // [kWarps][E] keys, only for groups that cross lanes
+  __shared__ int picked[kWarps][8];          // a row's choices
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long t = (long long)blockIdx.x * kWarps + warp;
-  if (t >= a.T) return;
-  const LT* row = static_cast<const LT*>(a.logits) + t * a.ld;
+  const unsigned below = (1u << lane) - 1u;  // lanes before this one
   const int e0 = lane * NV;
-  float l[NV], s[NV];
-  bool bad = false;  // a NaN (softmax: or +infinity) in the row
+  const int group = a.lanes > 0 ? lane / a.lanes : 0;
+  const LT* logits = static_cast<const LT*>(a.logits);
+  const long long step = (long long)gridDim.x * kWarps;
+  float bias[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    l[i] = e0 + i < a.E ? load_logit(row + e0 + i) : -INFINITY;
-    bad |= l[i] != l[i] || (!SIGMOID && l[i] == INFINITY);
-  }
-  bad = __any_sync(kFull, bad);
-  const bool need_scores = SIGMOID || a.bias != nullptr || a.scores != nullptr || !a.renorm;
-  if (need_scores) {
-    if (SIGMOID) {
+  for (int i = 0; i < NV; ++i)
+    bias[i] = a.bias != nullptr && e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
+  const bool need_scores = SIGMOID || a.bias != nullptr || a.scores != nullptr;
+  long long t = (long long)blockIdx.x * kWarps + warp;
+  float l[NV];
+  if (t < a.T) load_row<NV>(logits + t * a.ld, e0, a.E, a.vec, l);
+  for (; t < a.T; t += step) {
+    float next[NV];
+    if (t + step < a.T) load_row<NV>(logits + (t + step) * a.ld, e0, a.E, a.vec, next);
+    const LT* row = logits + t * a.ld;
+    bool bad = false;  // a NaN (softmax: or +infinity) in the row
 #pragma unroll
-      for (int i = 0; i < NV; ++i) s[i] = sigmoid(l[i]);
-    } else {
-      softmax_scores<NV>(l, s);
-    }
-    if (a.scores != nullptr) {
+    for (int i = 0; i < NV; ++i) bad |= SIGMOID ? l[i] != l[i] : !(l[i] < INFINITY);
+    bad = __any_sync(kFull, bad);
+    float s[NV], top = 0.0f, total = 1.0f;
+    if (need_scores || (!SIGMOID && !a.renorm)) {
+      if (SIGMOID) {
+        bool low = false;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (e0 + i < a.E) a.scores[t * a.E + e0 + i] = s[i];
-    }
-  }
-  uint32_t key[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float r = l[i];
-    if (a.bias != nullptr)
-      r = e0 + i < a.E ? s[i] + a.bias[e0 + i] : -INFINITY;
-    else if (SIGMOID)
-      r = s[i];
-    // r is NaN where the logit, the softmax or the bias is
-    key[i] = e0 + i >= a.E ? 0u : (r != r || l[i] != l[i] || l[i] == -INFINITY) ? kMaskedKey
-                                                                               : rank_key(r);
-  }
-  if (a.G > 0) {
-    uint32_t* mine = group_smem + warp * a.E;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (e0 + i < a.E) mine[e0 + i] = key[i];
-    __syncwarp();
-    const int size = a.E / a.G;
-    uint32_t gk[2];  // ranks of groups lane and lane + 32
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int g = lane + 32 * h;
-      gk[h] = 0u;
-      if (g < a.G) {
-        uint32_t b1 = 0u, b2 = 0u;
-        for (int i = 0; i < size; ++i) {
-          const uint32_t v = mine[g * size + i];
-          b2 = max(b2, min(b1, v));
-          b1 = max(b1, v);
+        for (int i = 0; i < NV; ++i) {
+          s[i] = l[i] == -INFINITY ? 0.0f : sigmoid_fast(l[i]);
+          low |= l[i] < -80.0f && l[i] > -INFINITY;
         }
-        gk[h] = a.top2 && b2 > kMaskedKey ? rank_key(key_rank(b1) + key_rank(b2)) : b1;
+        if (low) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) s[i] = sigmoid(l[i]);
+        }
+      } else {
+        softmax_scores<NV>(l, s, top, total);
+      }
+      if (a.scores != nullptr) {
+        float* to = a.scores + t * a.E + e0;
+        if (a.vec_scores && e0 + NV <= a.E) {
+          if constexpr (NV >= 4) {
+#pragma unroll
+            for (int i = 0; i < NV; i += 4)
+              *reinterpret_cast<float4*>(to + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) to[i] = s[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (e0 + i < a.E) to[i] = s[i];
+        }
       }
     }
-    // a group is kept when fewer than Gk groups precede it
-    int before[2] = {0, 0};
-    for (int g = 0; g < a.G; ++g) {
-      const uint32_t v = __shfl_sync(kFull, g < 32 ? gk[0] : gk[1], g & 31);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        before[h] += v > gk[h] || (v == gk[h] && g < lane + 32 * h);
-    }
-    const unsigned keep0 = __ballot_sync(kFull, lane < a.G && before[0] < a.Gk);
-    const unsigned keep1 = __ballot_sync(kFull, lane + 32 < a.G && before[1] < a.Gk);
+    uint32_t key[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int g = (e0 + i) / size;
-      if (e0 + i < a.E && !(((g < 32 ? keep0 : keep1) >> (g & 31)) & 1u)) key[i] = 0u;
+      float r = l[i];
+      if (a.bias != nullptr)
+        r = s[i] + bias[i];
+      else if (SIGMOID)
+        r = s[i];
+      // r is NaN where the logit, the softmax or the bias is; past E the key is 0
+      key[i] = l[i] > -INFINITY && r == r ? rank_key(r) : kMaskedKey;
+      if (e0 + i >= a.E) key[i] = 0u;
     }
-  }
-  // top-k: the warp's largest key, lowest lane and lowest slot first
-  int my_idx = 0;  // lane j: the j-th choice
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < NV; ++i) best = max(best, key[i]);
-    const uint32_t top = __reduce_max_sync(kFull, best);
-    const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
-    int slot = 0;
-#pragma unroll
-    for (int i = NV - 1; i >= 0; --i)
-      if (key[i] == top) slot = i;
-    if (lane == owner) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i == slot) key[i] = 0u;
+    uint32_t b1, b2, gone = 0u;  // this lane's best two; its slots that are taken or cannot be
+    int i1, i2;
+    two_best<NV>(key, 0u, b1, i1, b2, i2);
+    if (a.G > 0) {
+      if (a.lanes > 0) {  // a group is `lanes` whole lanes, a power of two
+        uint32_t g1 = b1, g2 = b2;
+        for (int o = 1; o < a.lanes; o <<= 1) {
+          const uint32_t p1 = __shfl_xor_sync(kFull, g1, o), p2 = __shfl_xor_sync(kFull, g2, o);
+          g2 = max(min(g1, p1), max(g2, p2));
+          g1 = max(g1, p1);
+        }
+        if (a.top2 && g2 > kMaskedKey) g1 = rank_key(key_rank(g1) + key_rank(g2));
+        // kept when fewer than Gk groups precede it
+        int before = 0;
+#pragma unroll 4
+        for (int g = 0; g < a.G; ++g) {
+          const uint32_t v = __shfl_sync(kFull, g1, g * a.lanes);
+          before += v > g1 || (v == g1 && g < group);
+        }
+        if (before >= a.Gk) {
+          b1 = b2 = 0u;
+          gone = 0xffffffffu;
+        }
+      } else {
+        drop_groups<NV>(a, key, group_smem + warp * a.E, e0, lane, gone);
+        two_best<NV>(key, gone, b1, i1, b2, i2);
+      }
     }
-    const int e = __shfl_sync(kFull, e0 + slot, owner);
-    if (lane == j) my_idx = e;
-  }
-  // weights: lane j < k recomputes its choice's score from the logit
-  const bool on = lane < a.k;
-  float w = 0.0f;
-  if (SIGMOID) {
-    w = on ? sigmoid(load_logit(row + my_idx)) : 0.0f;
-  } else if (a.renorm) {  // softmax over the chosen logits: the same quotient without underflow
+    // top-k: the largest key over the lanes, lowest lane first; its lane notes the choice
+    bool one = false;  // this lane's second best moved up: b2 is not its next
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t best = __reduce_max_sync(kFull, b1);
+      const unsigned at = __ballot_sync(kFull, b1 == best);
+      const bool mine = b1 == best && (at & below) == 0u;
+      bool again = false;
+      if (mine) {
+        picked[warp][j] = e0 + i1;
+        gone |= 1u << i1;
+        again = one;
+        b1 = b2;
+        i1 = i2;
+        one = true;
+      }
+      if (__any_sync(kFull, again)) {
+        uint32_t n1, n2;
+        int m1, m2;
+        two_best<NV>(key, gone, n1, m1, n2, m2);
+        if (again) {
+          b1 = n1, b2 = n2, i1 = m1, i2 = m2;
+          one = false;
+        }
+      }
+    }
+    __syncwarp();
+    const int my_idx = picked[warp][lane & 7];
+    __syncwarp();  // it is written again for the warp's next row
+    // weights: lane j < k recomputes its choice's score from the logit
+    const bool on = lane < a.k;
     const float sel = on ? load_logit(row + my_idx) : -INFINITY;
-    const float m = warp_max(sel);
-    w = on ? expf(sel - (m == -INFINITY ? 0.0f : m)) : 0.0f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const float v = __shfl_sync(kFull, s[i], my_idx / NV);
-      if (my_idx % NV == i) w = v;
+    float w;
+    if (SIGMOID) {
+      w = on ? sigmoid(sel) : 0.0f;
+    } else if (a.renorm) {  // softmax over the chosen logits: the same quotient without underflow
+      const float m = warp_max(sel);
+      w = on ? expf(sel - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+    } else {
+      w = expf(sel - top) / total;
     }
-    w = on ? w : 0.0f;
-  }
-  if (a.renorm) {
-    const float total = warp_sum(w);
-    w = total == 0.0f ? 0.0f : w / total;
-  }
-  if (on) {
-    a.idx[t * a.k + lane] = my_idx;
-    a.w[t * a.k + lane] = bad ? NAN : a.scale * w;
+    if (a.renorm) {
+      const float sum = warp_sum(w);
+      w = sum == 0.0f ? 0.0f : w / sum;
+    }
+    if (on) {
+      a.idx[t * a.k + lane] = my_idx;
+      a.w[t * a.k + lane] = bad ? NAN : a.scale * w;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = next[i];
   }
 }
 
@@ -230,6 +380,7 @@ struct GateGradArgs {
   long long ld;
   int T, E, k;
   bool renorm;
+  bool vec;  // rows of logits, scores and d_logits are in pieces of four experts
   float scale;
 };
 
@@ -238,74 +389,185 @@ struct GateGradArgs {
 //   sigmoid, renormalised: D = sum of the chosen s, ds_j += c (dw_j - sum_i dw_i s_i / D) / D
 //   not renormalised: ds_j += c dw_j
 //   then softmax: dl += s (ds - sum_e s_e ds_e);  sigmoid: dl = ds s (1 - s).
+__device__ __forceinline__ float lanes_sum(float v, int W) {
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return W > 8 ? __shfl_sync(kFull, v, 0) : v;  // the other lanes' values are 0
+}
+__device__ __forceinline__ float lanes_max(float v, int W) {
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return W > 8 ? __shfl_sync(kFull, v, 0) : v;
+}
+
+// g of a token's chosen experts, one per lane (at most eight) of a row of W = 8 or 32 lanes: the
+// gradient to its score, or to its logit where only the chosen experts have one (TO_LOGIT).
+template <bool SIGMOID, bool TO_LOGIT, int W>
+__device__ __forceinline__ float chosen_gradient(const GateGradArgs& a, bool on, float sel,
+                                                 float dw) {
+  if (SIGMOID) {
+    float g = dw;
+    if (a.renorm) {
+      const float sj = on ? sigmoid(sel) : 0.0f;
+      const float total = lanes_sum(sj, W);
+      const float dot = lanes_sum(dw * sj, W);
+      g = total == 0.0f ? 0.0f : (dw - dot / total) / total;
+    }
+    if (!TO_LOGIT) return g;
+    // s (1 - s) = x / (1 + x)^2 with x = exp(-|l|): no cancellation at either end
+    const float x = expf(-fabsf(sel));
+    return on ? g * (x / ((1.0f + x) * (1.0f + x))) : 0.0f;
+  }
+  if (!a.renorm) return dw;
+  const float m = lanes_max(sel, W);
+  float u = on ? expf(sel - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+  const float total = lanes_sum(u, W);
+  u = total == 0.0f ? 0.0f : u / total;
+  return u * (dw - lanes_sum(u * dw, W));
+}
+
+// Adds the chosen experts' values to a zeroed row of E floats in shared memory (an index that comes twice
+// adds twice).
+template <int NV>
+__device__ __forceinline__ void scatter_row(float* mine, int lane, int my_idx, float g) {
+#pragma unroll
+  for (int i = 0; i < NV; i += 4)
+    if (NV >= 4)
+      *reinterpret_cast<float4*>(mine + i / 4 * 128 + lane * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (NV < 4) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) mine[i * 32 + lane] = 0.0f;
+  }
+  __syncwarp();
+  if (my_idx >= 0) atomicAdd(mine + my_idx, g);
+  __syncwarp();
+}
+
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                            *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// Only the chosen experts have a gradient (no d_scores, and not a softmax without renormalisation).
+// Eight lanes per token, four consecutive tokens per warp, whose rows of d_logits are one run of 4 E
+// elements, put together in shared memory.
+template <int NV, typename LT, bool SIGMOID>
+__global__ void __launch_bounds__(32 * kWarps) gate_grad_chosen_kernel(const GateGradArgs a) {
+  __shared__ __align__(16) float rows[kWarps][4 * 32 * NV];
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long t0 = ((long long)blockIdx.x * kWarps + warp) * 4;
+  if (t0 >= a.T) return;
+  const int j = lane & 7, n = (int)min(4LL, a.T - t0);
+  const long long t = t0 + (lane >> 3);
+  int my_idx = j < a.k && t < a.T ? a.idx[t * a.k + j] : -1;
+  if (my_idx >= a.E) my_idx = -1;
+  const bool on = my_idx >= 0;
+  const float dw = on ? a.scale * a.d_w[t * a.k + j] : 0.0f;
+  const float sel =
+      on ? load_logit(static_cast<const LT*>(a.logits) + t * a.ld + my_idx) : -INFINITY;
+  float* mine = rows[warp];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    *reinterpret_cast<float4*>(mine + (i * 32 + lane) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float g = chosen_gradient<SIGMOID, true, 8>(a, on, sel, dw);
+  __syncwarp();
+  if (on) atomicAdd(mine + (lane >> 3) * a.E + my_idx, g);  // an index that comes twice adds twice
+  __syncwarp();
+  LT* out = static_cast<LT*>(a.d_logits) + t0 * a.E;
+  if (a.vec) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * 32 + lane) * 4;
+      if (e < n * a.E) {
+        const float4 v = *reinterpret_cast<const float4*>(mine + e);
+        store4(out + e, v.x, v.y, v.z, v.w);
+      }
+    }
+  } else {
+    for (int e = lane; e < n * a.E; e += 32) store_logit(out + e, mine[e]);
+  }
+}
+
+// Every expert has a gradient. Lane l holds experts i / 4 * 128 + 4 l + i % 4 (NV >= 4), so that rows
+// move in whole lines.
 template <int NV, typename LT, bool SIGMOID>
 __global__ void __launch_bounds__(32 * kWarps) gate_grad_kernel(const GateGradArgs a) {
+  __shared__ __align__(16) float rows[kWarps][32 * NV];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long t = (long long)blockIdx.x * kWarps + warp;
   if (t >= a.T) return;
   const LT* row = static_cast<const LT*>(a.logits) + t * a.ld;
   LT* out = static_cast<LT*>(a.d_logits) + t * a.E;
-  const int e0 = lane * NV;
-  // the chosen experts: lane j < k
-  int my_idx = lane < a.k ? a.idx[t * a.k + lane] : -1;
-  if (my_idx >= a.E) my_idx = -1;
-  const bool on = my_idx >= 0;
-  const float dw = on && a.d_w != nullptr ? a.scale * a.d_w[t * a.k + lane] : 0.0f;
-  const float sel = on ? load_logit(row + my_idx) : -INFINITY;
-  float g = dw;  // gradient of the choice: to its score, or (softmax, renormalised) to its logit
-  if (a.renorm) {
-    if (SIGMOID) {
-      const float sj = on ? sigmoid(sel) : 0.0f;
-      const float total = warp_sum(sj);
-      const float dot = warp_sum(dw * sj);
-      g = total == 0.0f ? 0.0f : (dw - dot / total) / total;
-    } else {
-      const float m = warp_max(sel);
-      float u = on ? expf(sel - (m == -INFINITY ? 0.0f : m)) : 0.0f;
-      const float total = warp_sum(u);
-      u = total == 0.0f ? 0.0f : u / total;
-      g = u * (dw - warp_sum(u * dw));
-    }
-  }
-  const bool to_logit = !SIGMOID && a.renorm;  // g is already a logit's gradient
-  float ds[NV], gl[NV];
+  const float* dsr = a.d_scores != nullptr ? a.d_scores + t * a.E : nullptr;
+  auto expert = [&](int i) { return NV >= 4 ? i / 4 * 128 + lane * 4 + i % 4 : i * 32 + lane; };
+  float l[NV], ds[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    ds[i] = a.d_scores != nullptr && e0 + i < a.E ? a.d_scores[t * a.E + e0 + i] : 0.0f;
-    gl[i] = 0.0f;
+    ds[i] = 0.0f;
+    l[i] = -INFINITY;
   }
-  for (int j = 0; j < a.k; ++j) {
-    const int e = __shfl_sync(kFull, my_idx, j);
-    const float v = __shfl_sync(kFull, g, j);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (e == e0 + i) (to_logit ? gl[i] : ds[i]) += v;
+  for (int i = 0; i < NV; ++i) {
+    const int e = expert(i);
+    if (NV >= 4 && a.vec) {
+      if (i % 4 == 0 && e < a.E) {
+        load_run<4>(row + e, *reinterpret_cast<float(*)[4]>(l + i));
+        if (dsr != nullptr) load_run<4>(dsr + e, *reinterpret_cast<float(*)[4]>(ds + i));
+      }
+    } else if (e < a.E) {
+      l[i] = load_logit(row + e);
+      if (dsr != nullptr) ds[i] = dsr[e];
+    }
   }
+  int my_idx = lane < a.k && a.d_w != nullptr ? a.idx[t * a.k + lane] : -1;
+  if (my_idx >= a.E) my_idx = -1;
+  const bool on = my_idx >= 0;
+  const float dw = on ? a.scale * a.d_w[t * a.k + lane] : 0.0f;
+  const float sel = on ? load_logit(row + my_idx) : -INFINITY;
+  const float g = chosen_gradient<SIGMOID, false, 32>(a, on, sel, dw);
+  float* mine = rows[warp];
+  scatter_row<NV>(mine, lane, my_idx, g);
+  float gl[NV];
   if (SIGMOID) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (e0 + i < a.E) {
-        // s (1 - s) = x / (1 + x)^2 with x = exp(-|l|): no cancellation at either end
-        const float x = expf(-fabsf(load_logit(row + e0 + i)));
-        gl[i] = ds[i] * (x / ((1.0f + x) * (1.0f + x)));
+      const float x = expf(-fabsf(l[i]));
+      gl[i] = (ds[i] + mine[expert(i)]) * (x / ((1.0f + x) * (1.0f + x)));
+    }
+  } else {
+    // renormalised, the chosen values are logits' gradients already; else scores'
+    float s[NV], top, total, dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      gl[i] = mine[expert(i)];
+      if (!a.renorm) {
+        ds[i] += gl[i];
+        gl[i] = 0.0f;
       }
     }
-  } else if (a.d_scores != nullptr || !a.renorm) {
-    float l[NV], s[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = e0 + i < a.E ? load_logit(row + e0 + i) : -INFINITY;
-    softmax_scores<NV>(l, s);
-    float dot = 0.0f;
+    softmax_scores<NV>(l, s, top, total);
 #pragma unroll
     for (int i = 0; i < NV; ++i) dot += s[i] * ds[i];
     dot = warp_sum(dot);
 #pragma unroll
     for (int i = 0; i < NV; ++i) gl[i] += s[i] * (ds[i] - dot);
   }
+  if (NV >= 4 && a.vec) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (e0 + i < a.E) store_logit(out + e0 + i, gl[i]);
+    for (int i = 0; i < NV; i += 4)
+      if (expert(i) < a.E)
+        store4(out + expert(i), gl[i], gl[(i + 1) % NV], gl[(i + 2) % NV], gl[(i + 3) % NV]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (expert(i) < a.E) store_logit(out + expert(i), gl[i]);
+  }
 }
 
 int lane_values(int E) {
@@ -316,12 +578,20 @@ int lane_values(int E) {
 
 template <int NV, typename LT, bool SIGMOID>
 cudaError_t gate_one(const GateArgs& a, cudaStream_t st) {
-  const size_t smem = a.G > 0 ? sizeof(uint32_t) * kWarps * a.E : 0;
-  return launch_k(gate_kernel<NV, LT, SIGMOID>, dim3((a.T + kWarps - 1) / kWarps),
+  const size_t smem = a.G > 0 && a.lanes == 0 ? sizeof(uint32_t) * kWarps * a.E : 0;
+  // persistent: at most as many CTAs as the GPU holds at once
+  const long long ctas = ((long long)a.T + kWarps - 1) / kWarps;
+  return launch_k(gate_kernel<NV, LT, SIGMOID>,
+                  dim3((unsigned)std::min(ctas, (long long)num_sms() * kCtasPerSm)),
                   dim3(32 * kWarps), smem, st, a);
 }
 template <int NV, typename LT, bool SIGMOID>
 cudaError_t gate_grad_one(const GateGradArgs& a, cudaStream_t st) {
+  const bool chosen = a.d_scores == nullptr && (SIGMOID || a.renorm);
+  if (chosen)
+    return launch_k(gate_grad_chosen_kernel<NV, LT, SIGMOID>,
+                    dim3((unsigned)(((long long)a.T + 4 * kWarps - 1) / (4 * kWarps))),
+                    dim3(32 * kWarps), 0, st, a);
   return launch_k(gate_grad_kernel<NV, LT, SIGMOID>, dim3((a.T + kWarps - 1) / kWarps),
                   dim3(32 * kWarps), 0, st, a);
 }
@@ -391,6 +661,11 @@ moe_status moe_route_logits(const moe_gate_config* cfg, const void* logits,
   a.top2 = cfg->group_top2 != 0;
   a.renorm = cfg->renormalize != 0;
   a.scale = cfg->scale;
+  a.vec = aligned(logits, 16) && a.ld * (bf16 ? 2 : 4) % 16 == 0;
+  a.vec_scores = aligned(scores, 16) && a.E % 4 == 0;
+  const int nv = lane_values(a.E), size = a.G > 0 ? a.E / a.G : 0;
+  const int lanes = size % nv == 0 ? size / nv : 0;
+  a.lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
   const bool sig = cfg->score == MOE_SCORE_SIGMOID;
   const cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = [&]() -> cudaError_t {
@@ -425,6 +700,9 @@ moe_status moe_route_logits_backward(const moe_gate_config* cfg, const void* log
   a.k = cfg->top_k;
   a.renorm = cfg->renormalize != 0;
   a.scale = cfg->scale;
+  const int piece = bf16 ? 8 : 16;  // four logits
+  a.vec = a.E % 4 == 0 && aligned(logits, piece) && a.ld % 4 == 0 && aligned(d_logits, piece) &&
+          aligned(d_scores, 16);
   const bool sig = cfg->score == MOE_SCORE_SIGMOID;
   const cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = [&]() -> cudaError_t {
