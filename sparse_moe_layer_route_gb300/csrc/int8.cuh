@@ -52,12 +52,14 @@ struct Int8Gemm {
   int* status;
   int rows, K, N, n_mat, S, T;
   int out_dtype;             // matrix pass
+  int splits;                // partial pass: pieces of K
 };
 
 enum Int8Pass {
   kInt8Matrix = 0,  // out [rows, N] = product
   kInt8SwiGLU = 1,  // out [rows + S T, N] fp32 = silu(gate product) * (up product)
-  kInt8Slot = 2     // out [slot, N] fp16 = gate weight * product
+  kInt8Slot = 2,    // out [slot, N] fp16 = gate weight * product
+  kInt8Partial = 3  // out [splits][rows, N] fp32 = sums over one piece of K, without scales
 };
 
 // Tensor cores: long segments on CTA pairs (int8_gemm_pair.cu), others on single CTAs (int8_gemm.cu).
@@ -65,6 +67,11 @@ cudaError_t launch_int8_gemm_pair(Int8Pass pass, const Int8Gemm& g, cudaStream_t
 // A few rows (int8_gemv.cu); most_rows: no segment has more.
 cudaError_t launch_int8_gemv(Int8Pass pass, const Int8Gemm& g, int most_rows, cudaStream_t st);
 cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
+// Pieces of K that give a product with few work units something to do on every SM (1: none), for a
+// matrix pass of this shape; and that product: partial sums to `part` (int8_splits() * rows * N floats),
+// then their sums, scaled, to g.out.
+int int8_splits(long long rows, int K, int N, int n_mat);
+cudaError_t launch_int8_split(const Int8Gemm& g, float* part, cudaStream_t st);
 cudaError_t launch_quantize_rows(int T, int d, int dtype, const void* x, long long ld, int8_t* q,
                                  float* scale, cudaStream_t st);
 cudaError_t launch_quantize_channels(int n_mat, int K, int N, const uint16_t* W, int8_t* q,

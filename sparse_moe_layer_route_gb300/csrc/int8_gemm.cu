@@ -25,7 +25,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "int8.cuh"
 #include "int8_units.cuh"
@@ -118,7 +120,18 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   const int n_ct = (g.N + UCH - 1) / UCH;
   const int n_sub = (g.K + 63) / 64;           // 64-k slots per unit
   const int n_stage = (n_sub + 1) / 2;         // 128-k stages per unit
-  const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct;
+  // partial pass: a unit is done in pieces, each some of its stages
+  const int splits = PASS == kInt8Partial ? g.splits : 1;
+  const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct * splits;
+  auto unit_of = [&](long long w) {
+    return find_unit<PAIR>(segs, g, n_ct, NT, PASS == kInt8Partial ? w / splits : w);
+  };
+  auto first_stage = [&](long long w) {
+    return PASS == kInt8Partial ? (int)(w % splits) * n_stage / splits : 0;
+  };
+  auto end_stage = [&](long long w) {
+    return PASS == kInt8Partial ? ((int)(w % splits) + 1) * n_stage / splits : n_stage;
+  };
 
   if (warp == 0) {
     if (ptx::elect_one()) {
@@ -127,14 +140,15 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       uint32_t phase = 0, issued = 0, last_parity = 0;  // per stage: ever issued, its parity
       bool ok = true;
       for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
-        const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
+        const Unit u = unit_of(w);
         const bool sh = u.seg >= g.n_mat;
         const int ex = sh ? u.seg - g.n_mat : u.seg;
         const CUtensorMap* a0 = sh ? &tmShA : &tmA;
         const CUtensorMap* a1 = PAIR ? (sh ? &tmShA2 : &tmA2) : a0;
         const int ch0 = u.ct * UCH, ch1 = PAIR ? ch0 : ch0 + kInt8Ch;
         const bool two = ch1 < g.N;
-        for (int i = 0; i < n_stage; ++i) {
+        const int i1 = end_stage(w);
+        for (int i = first_stage(w); i < i1; ++i) {
           if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, g.status,
                                       MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
@@ -173,7 +187,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       uint32_t phase = 0, slot_phase = 0, acc_phase = 0;
       bool ok = true;
       for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
-        const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
+        const Unit u = unit_of(w);
         const bool two = PAIR || u.ct * UCH + kInt8Ch < g.N;
         const uint32_t idesc =
             ptx::idesc_f16kind_f32(kInt8Ch, (uint32_t)((u.rows + 15) & ~15), 0, 0, 0u);
@@ -182,7 +196,8 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
           break;
         ptx::tc_fence_after();
         const uint32_t d0 = tmem_base + (uint32_t)(acc * 2 * NT), d1 = d0 + NT;
-        for (int i = 0; i < n_stage && ok; ++i) {
+        const int i0 = first_stage(w), i1 = end_stage(w);
+        for (int i = i0; i < i1 && ok; ++i) {
           if (!ptx::mbar_wait_bounded(full_bar(stage), phase, abort_flag, g.status,
                                       MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
@@ -202,7 +217,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
               // B: K-major, 128 B rows, 8-row groups 1024 B apart; a K step of 16 = +32 B
               const uint64_t bdesc =
                   ptx::smem_desc_sw128(sB + h * (C::kBBytes / 2) + kk * 32, 16, 1024);
-              const uint32_t more = (i | h | kk) != 0 ? 1u : 0u;
+              const uint32_t more = ((i - i0) | h | kk) != 0 ? 1u : 0u;
               ptx::umma_f16_ta(d0, a0 + kk * 8, bdesc, idesc, more);
               if (two) ptx::umma_f16_ta(d1, a0 + 32 + kk * 8, bdesc, idesc, more);
             }
@@ -241,9 +256,10 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     uint32_t phase = 0, slot_phase = 0;
     bool ok = true;
     for (long long w = blockIdx.x; w < total && ok; w += gridDim.x) {
-      const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
+      const Unit u = unit_of(w);
       const bool on = PAIR || tile == 0 || u.ct * UCH + kInt8Ch < g.N;
-      for (int i = 0; i < n_stage && ok; ++i) {
+      const int i1 = end_stage(w);
+      for (int i = first_stage(w); i < i1 && ok; ++i) {
         if (!ptx::mbar_wait_bounded_warp(full_bar(stage), phase, abort_flag, g.status,
                                          MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
           ok = false;
@@ -301,14 +317,21 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     int acc = 0, ub = 0, sb = 0;  // accumulator; buffers of the unit's rows and of the step
     uint32_t acc_phase = 0, clamp = 0u;
     for (long long w = blockIdx.x; w < total; w += gridDim.x) {
-      const Unit u = find_unit<PAIR>(segs, g, n_ct, NT, w);
+      const Unit u = unit_of(w);
       const bool sh = u.seg >= g.n_mat;
       const long long ex = sh ? u.seg - g.n_mat : u.seg;
       const int ch0 = u.ct * UCH, ch1 = PAIR ? ch0 : ch0 + kInt8Ch;
       const bool in0 = ch0 + chl < g.N, in1 = ch1 + chl < g.N, two = ch1 < g.N;
-      const float* sw = (sh ? g.sh_sw : g.sw) + ex * g.N;
-      const float* sw2 = PAIR ? (sh ? g.sh_sw2 : g.sw2) + ex * g.N : sw;
-      const float w0 = in0 ? sw[ch0 + chl] : 0.0f, w1 = in1 ? sw2[ch1 + chl] : 0.0f;
+      float w0 = 1.0f, w1 = 1.0f;
+      if (PASS != kInt8Partial) {
+        const float* sw = (sh ? g.sh_sw : g.sw) + ex * g.N;
+        const float* sw2 = PAIR ? (sh ? g.sh_sw2 : g.sw2) + ex * g.N : sw;
+        w0 = in0 ? sw[ch0 + chl] : 0.0f;
+        w1 = in1 ? sw2[ch1 + chl] : 0.0f;
+      }
+      // partial pass: this piece's plane of the output
+      uint8_t* out = static_cast<uint8_t*>(g.out);
+      if (PASS == kInt8Partial) out += (w % splits) * 4ll * g.rows * g.N;
       float* usx = unit_sx[ub];
       int* orow = unit_orow[ub];
       ub ^= 1;
@@ -333,7 +356,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
               clamp = max(clamp, mag_bits(y));
           }
           epilogue_barrier();
-          P::flush(g, buf, orow + c * 32 + j0, ch, t);
+          P::flush(out, g.N, buf, orow + c * 32 + j0, ch, t);
           sb ^= 1;
         }
       };
@@ -415,7 +438,68 @@ cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
   return launch_one<PASS, OUT, 96, 2, 2>(g, st);
 }
 
+// y = (sum of the pieces, in their order) * row scale * channel scale; rows past the last segment are left.
+template <typename YT>
+__global__ void __launch_bounds__(256) join_splits_kernel(const float* __restrict__ part,
+                                                          const Int8Gemm g) {
+  griddep_wait();
+  const int row = blockIdx.y;
+  int seg = 0;
+  if (g.offsets != nullptr) {
+    // the last segment that begins at or before the row and reaches it (bad offsets were reported by
+    // the product, which left their rows out)
+    int lo = 0, hi = g.n_mat;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (g.offsets[mid] <= row)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    seg = lo;
+    const int r0 = g.offsets[seg], r1 = g.offsets[seg + 1];
+    if (r0 < 0 || r1 > g.rows || row < r0 || row >= r1) return;
+  }
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= g.N) return;
+  const long long at = (long long)row * g.N + n, plane = (long long)g.rows * g.N;
+  float sum = 0.0f;
+  for (int i = 0; i < g.splits; ++i) sum += part[i * plane + at];
+  sum *= g.sx[row] * g.sw[(long long)seg * g.N + n];
+  if constexpr (sizeof(YT) == 4)
+    static_cast<float*>(g.out)[at] = sum;
+  else if constexpr (std::is_same<YT, __nv_bfloat16>::value)
+    static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16(sum);
+  else
+    static_cast<__half*>(g.out)[at] = __float2half(sum);
+}
+
 }  // namespace
+
+int int8_splits(long long rows, int K, int N, int n_mat) {
+  constexpr int kSms = 152;
+  const long long mean = rows / n_mat, per = mean <= 32 ? 32 : 96;
+  const long long units = (mean + per - 1) / per * n_mat * ((N + 255) / 256);
+  if (units == 0 || units * 2 > kSms || rows > 65535) return 1;
+  // at least four 128-k stages a piece: shorter ones spend their time on filling the pipeline
+  return (int)std::max(1ll, std::min(kSms / units, (long long)(K / kInt8StageK / 4)));
+}
+
+cudaError_t launch_int8_split(const Int8Gemm& g, float* part, cudaStream_t st) {
+  Int8Gemm p = g;
+  p.splits = int8_splits(g.rows, g.K, g.N, g.n_mat);
+  p.out = part;
+  cudaError_t e = launch_pass<kInt8Partial, MOE_DTYPE_F32>(p, st);
+  if (e != cudaSuccess) return e;
+  p.out = g.out;
+  const dim3 grid((g.N + 255) / 256, g.rows), block(256);
+  switch (g.out_dtype) {
+    case MOE_DTYPE_F32: return launch_k(join_splits_kernel<float>, grid, block, 0, st, part, p);
+    case MOE_DTYPE_BF16:
+      return launch_k(join_splits_kernel<__nv_bfloat16>, grid, block, 0, st, part, p);
+    default: return launch_k(join_splits_kernel<__half>, grid, block, 0, st, part, p);
+  }
+}
 
 cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st) {
   if (g.rows / g.n_mat > 96) return launch_int8_gemm_pair(pass, g, st);

@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
             P::put(buf, col, chl, swiglu(gv, uv));
           }
           epilogue_barrier();
-          P::flush(g, buf, orow + c * 32, ch0, t);
+          P::flush(static_cast<uint8_t*>(g.out), g.N, buf, orow + c * 32, ch0, t);
           sb ^= 1;
         } else {
 #pragma unroll
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
                 clamp = max(clamp, mag_bits(y));
             }
             epilogue_barrier();
-            P::flush(g, buf, orow + c * 32 + j0, ch0, t);
+            P::flush(static_cast<uint8_t*>(g.out), g.N, buf, orow + c * 32 + j0, ch0, t);
             sb ^= 1;
           }
         }

@@ -3,7 +3,7 @@
 //
 // Bound by the weight bytes. A warp takes kStreams output channels (SwiGLU pass: half as many channels of
 // gate and of up) of one row tile of R rows and runs down K, 16 codes a lane and step: one 16-byte load per
-// channel, past L1, four steps of each in flight (8 KB a warp), and one load per row, from L1, where the
+// channel, past L1, two steps of each in flight (4 KB a warp), and one load per row, from L1, where the
 // SM's warps share the rows. The lanes' sums meet in one reduction per channel and row. A tile of
 // tensor-core units has 128 channels, so a single row of a [14336 x 4096] product would occupy 56 of the
 // 152 SMs for 30 us; here its 3584 warps spread over all of them.
@@ -19,9 +19,12 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+// Small CTAs, two steps and at most 85 registers: 24 warps of 4 KB in flight each on an SM, and an even
+// last wave (one [14336 x 4096] row 11 us; with 256 threads, four steps and 16 warps 14.6 us).
+constexpr int kThreads = 128;
+constexpr int kCtasPerSm = 6;
 constexpr int kStreams = 4;  // channels in flight per warp
-constexpr int kSteps = 4;    // 512-byte steps of each in flight
+constexpr int kSteps = 2;    // 512-byte steps of each in flight
 
 // 16 weight codes, read once: not kept in L1.
 __device__ __forceinline__ int4 load_once(const int8_t* p) {
@@ -48,16 +51,29 @@ __device__ __forceinline__ void store_one(void* out, long long at, float y) {
 // 32 segments at a time. seg -1: past the last tile.
 template <int R>
 __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int tile, int lane) {
+  constexpr int kParts = (kMaxSegs + 31) / 32;
   const int n = g.n_mat + g.S;
+  int bound[kParts][2];  // every load in flight before the first is needed
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+    const int s = p * 32 + lane;
+    bound[p][0] = bound[p][1] = 0;
+    if (g.offsets != nullptr && s < g.n_mat) {
+      bound[p][0] = g.offsets[s];
+      bound[p][1] = g.offsets[s + 1];
+    }
+  }
   int before = 0;
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    const int s = s0 + lane;
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+    const int s0 = p * 32, s = s0 + lane;
+    if (s0 >= n) break;
     int r0 = 0, nr = 0;
     if (s < g.n_mat) {
       int r1 = g.rows;
       if (g.offsets != nullptr) {
-        r0 = g.offsets[s];
-        r1 = g.offsets[s + 1];
+        r0 = bound[p][0];
+        r1 = bound[p][1];
         if (r0 < 0 || r1 < r0 || r1 > g.rows) {
           atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
           r0 = r1 = 0;
@@ -97,7 +113,8 @@ __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int 
 }
 
 template <int PASS, int OUT, int R>
-__global__ void __launch_bounds__(kThreads) int8_gemv_kernel(const Int8Gemm g) {
+__global__ void __launch_bounds__(kThreads, R == 8 ? 4 : kCtasPerSm)
+    int8_gemv_kernel(const Int8Gemm g) {
   constexpr bool GLU = PASS == kInt8SwiGLU;
   constexpr int CH = GLU ? kStreams / 2 : kStreams;  // channels per warp
   griddep_wait();

@@ -27,6 +27,17 @@ struct Vec8 {
   uint4 p;
   __device__ __forceinline__ void load(const XT* at) { p = *reinterpret_cast<const uint4*>(at); }
   __device__ __forceinline__ void get(float (&v)[8]) const;
+  // Largest magnitudes so far, one per half of a word (16-bit magnitudes order as their bits do).
+  __device__ __forceinline__ void top(uint32_t& pair) const {
+    pair = __vimax3_u16x2(pair, p.x & 0x7fff7fffu, p.y & 0x7fff7fffu);
+    pair = __vimax3_u16x2(pair, p.z & 0x7fff7fffu, p.w & 0x7fff7fffu);
+  }
+  // The larger of the two as fp32 bits.
+  static __device__ __forceinline__ uint32_t top_bits(uint32_t pair) {
+    const uint32_t m = max(pair & 0xffffu, pair >> 16);
+    if (std::is_same<XT, __half>::value) return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    return m << 16;
+  }
 };
 template <>
 __device__ __forceinline__ void Vec8<__nv_bfloat16>::get(float (&v)[8]) const {
@@ -58,24 +69,33 @@ struct Vec8<float> {
     v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
     v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
   }
+  __device__ __forceinline__ void top(uint32_t& t) const {
+    float v[8];
+    get(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = max(t, __float_as_uint(v[j]) & 0x7fffffffu);
+  }
+  static __device__ __forceinline__ uint32_t top_bits(uint32_t t) { return t; }
 };
 
 // Where the codes go: 8-bit, or 16-bit for the tensor cores (whole numbers up to 127 are exact in
-// fp16). c: the codes as floats.
-__device__ __forceinline__ void store_codes8(int8_t* at, const float (&c)[8]) {
+// fp16). m: the codes plus kMagic, 1.5 * 2^23, whose fp32 neighbours are one apart: adding it rounds to the
+// nearest whole number, and the sum's low byte is the code.
+constexpr float kMagic = 12582912.0f;
+__device__ __forceinline__ void store_codes8(int8_t* at, const float (&m)[8]) {
   uint32_t b[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(c[i] + 12582912.0f);  // low byte: the code
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(m[i]);
   uint2 o;
   o.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   o.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
   *reinterpret_cast<uint2*>(at) = o;
 }
-__device__ __forceinline__ void store_codes8(uint16_t* at, const float (&c)[8]) {
+__device__ __forceinline__ void store_codes8(uint16_t* at, const float (&m)[8]) {
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(c[2 * i], c[2 * i + 1]);
+    const __half2 h = __floats2half2_rn(m[2 * i] - kMagic, m[2 * i + 1] - kMagic);
     o[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -116,33 +136,27 @@ __device__ __forceinline__ void quantize_row(const XT* __restrict__ row, int d,
       if ((i * W + t) * 8 < d) x[i].load(row + (i * W + t) * 8);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if ((i * W + t) * 8 < d) {
-        float v[8];
-        x[i].get(v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
-      }
-    const float s = int8_scale(row_max<W>(top, warp_top));
+      if ((i * W + t) * 8 < d) x[i].top(top);
+    const float s = int8_scale(row_max<W>(Vec8<XT>::top_bits(top), warp_top));
     if (t == 0) *scale = s;
     const bool plain = s > 1e-30f && s < 1e30f;  // 1 / s is a normal number
     const float r = plain ? __frcp_rn(s) : 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if ((i * W + t) * 8 < d) {
-        float v[8], c[8];
+        float v[8], m[8], far = 0.0f;  // far: the largest distance from a whole number
         x[i].get(v);
-        bool near = !plain;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float y = __fmul_rn(v[j], r);
-          c[j] = __fsub_rn(__fadd_rn(y, 12582912.0f), 12582912.0f);  // rint
-          near |= fabsf(y - c[j]) > 0.4999f;
+          m[j] = __fadd_rn(y, kMagic);
+          far = fmaxf(far, fabsf(__fsub_rn(y, __fsub_rn(m[j], kMagic))));
         }
-        if (near) {
+        if (far > 0.4999f || !plain) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) c[j] = (float)int8_code(v[j], s);
+          for (int j = 0; j < 8; ++j) m[j] = (float)int8_code(v[j], s) + kMagic;
         }
-        store_codes8(out + (i * W + t) * 8, c);
+        store_codes8(out + (i * W + t) * 8, m);
       }
   } else {
     for (int j = t; j < d; j += W)
@@ -180,8 +194,8 @@ __global__ void __launch_bounds__(W == 32 ? kThreads : W) quantize_gather_kernel
   if (p >= rows) return;
   long long token = p - TK;  // shared experts: every token
   if (p < TK) {
-    if (p >= offsets[E]) return;
-    const int slot = perm_slot[p];
+    const int n_kept = offsets[E], slot = perm_slot[p];  // both loads in flight
+    if (p >= n_kept) return;
     token = slot / k;
     if (slot < 0 || slot >= TK) {
       for (int j = t; j < d; j += W) xq[p * d + j] = 0;
@@ -266,10 +280,12 @@ namespace {
 
 // Calls f(W, VEC) for rows of d elements: a warp per row up to 2048 elements, else a CTA, with the row in
 // registers up to 8192 (128 threads) or 16384 (256); vec: rows are in 16-byte pieces of eight elements.
+// So few rows that most SMs have none take 512 threads each: then one row's time is the kernel's.
 template <int N>
 using Int = std::integral_constant<int, N>;
 template <typename F>
-cudaError_t by_row(int d, bool vec, F f) {
+cudaError_t by_row(long long rows, int d, bool vec, F f) {
+  if (vec && rows <= 152 && d > 512 && d <= 16384) return f(Int<512>{}, std::true_type{});
   if (d <= 2048) return vec ? f(Int<32>{}, std::true_type{}) : f(Int<32>{}, std::false_type{});
   if (vec && d <= 8192) return f(Int<128>{}, std::true_type{});
   if (vec && d <= 16384) return f(Int<256>{}, std::true_type{});
@@ -290,7 +306,7 @@ cudaError_t quantize_rows_as(int T, int d, const XT* x, long long ld, int8_t* q,
   const bool vec = d % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
                    (T == 1 || ld * sizeof(XT) % 16 == 0) &&
                    reinterpret_cast<uintptr_t>(q) % 8 == 0;
-  return by_row(d, vec, [&](auto w, auto v) {
+  return by_row(T, d, vec, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value;
     return launch_k(quantize_rows_kernel<W, decltype(v)::value, XT>, row_grid<W>(T),
                     row_block<W>(), 0, st, x, ld, T, d, q, scale);
@@ -329,7 +345,7 @@ cudaError_t launch_quantize_gather(const Shape& s, const uint16_t* x, const int3
                                    const int32_t* offsets, QT* xq, float* sx, int* status,
                                    cudaStream_t st) {
   const long long rows = s.TK + (s.S > 0 ? s.T : 0);
-  return by_row(s.d, true, [&](auto w, auto v) {  // d is a multiple of 64, x 16-byte aligned
+  return by_row(rows, s.d, true, [&](auto w, auto v) {  // d is a multiple of 64, x 16-byte aligned
     constexpr int W = decltype(w)::value;
     return launch_k(quantize_gather_kernel<W, decltype(v)::value, QT>, row_grid<W>(rows),
                     row_block<W>(), 0, st, reinterpret_cast<const __nv_bfloat16*>(x), perm_slot,
@@ -340,7 +356,7 @@ cudaError_t launch_quantize_gather(const Shape& s, const uint16_t* x, const int3
 template <typename QT>
 cudaError_t launch_quantize_hidden(const Shape& s, const float* h, const int32_t* offsets, QT* hq,
                                    float* sh, cudaStream_t st) {
-  return by_row(s.f, true, [&](auto w, auto v) {
+  return by_row(s.rows, s.f, true, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value;
     return launch_k(quantize_hidden_kernel<W, decltype(v)::value, QT>, row_grid<W>(s.rows),
                     row_block<W>(), 0, st, h, offsets, s.E, s.f, (int)s.TK, (long long)s.rows, hq,

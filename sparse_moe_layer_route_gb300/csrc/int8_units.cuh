@@ -123,7 +123,7 @@ __device__ __forceinline__ void unit_row(const Int8Gemm& g, const Unit& u, int r
   sx = 0.0f;
   orow = -1;
   if (r >= u.rows) return;
-  sx = g.sx[u.brow0 + r];
+  sx = PASS == kInt8Partial ? 1.0f : g.sx[u.brow0 + r];
   orow = u.row0 + r;
   if (PASS == kInt8Slot && u.seg < g.n_mat) {
     const int slot = g.perm_slot[u.row0 + r];
@@ -185,11 +185,10 @@ struct Panel {
   }
 
   // t: 0..127. The step's rows to the output: channels [ch0, ch0 + CH) of rows orow[0, kCols).
-  static __device__ __forceinline__ void flush(const Int8Gemm& g, const uint8_t* buf,
+  static __device__ __forceinline__ void flush(uint8_t* out, int N, const uint8_t* buf,
                                                const int* orow, int ch0, int t) {
-    uint8_t* out = static_cast<uint8_t*>(g.out);
-    const long long row_bytes = (long long)g.N * kSize;
-    if (ch0 + CH <= g.N && ((row_bytes | reinterpret_cast<long long>(out)) & 15) == 0) {
+    const long long row_bytes = (long long)N * kSize;
+    if (ch0 + CH <= N && ((row_bytes | reinterpret_cast<long long>(out)) & 15) == 0) {
       constexpr int kRows = 128 / kPieces;
       const int piece = t % kPieces, r0 = t / kPieces;
       uint4 v[kCols / kRows];
@@ -203,7 +202,7 @@ struct Panel {
           *reinterpret_cast<uint4*>(out + to * row_bytes + (long long)ch0 * kSize + piece * 16) =
               v[i];
       }
-    } else if (t < CH && ch0 + t < g.N) {  // the last channels, or rows that are not in 16-byte pieces
+    } else if (t < CH && ch0 + t < N) {  // the last channels, or rows that are not in 16-byte pieces
       for (int r = 0; r < kCols; ++r) {
         const int to = orow[r];
         if (to < 0) continue;
