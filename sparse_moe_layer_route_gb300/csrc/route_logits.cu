@@ -2,12 +2,11 @@
 // renormalised weights) and the gradient of its weights and scores to the logits.
 //
 // Forward: one warp per token and persistent warps, so the bias stays in registers and the next row is
-// on its way. Lane l holds experts [l * NV, (l + 1) * NV), NV the power of two with 32 * NV >= E: the
-// lowest lane that holds a value also holds its lowest index. Bound by instructions, not bytes: a row of
-// 256 fp32 logits is 1 KB, 0.15 us of one SM's share of HBM, and its 256 exact sigmoids alone are about
-// 130 warp instructions. So each lane keeps its two best experts, and a round of the top-k is one
-// warp-wide integer maximum over the lanes' best, a ballot for the lowest lane and a shuffle; a lane is
-// searched again only when two of its experts were taken.
+// on its way. Lane l holds experts [l * NV, (l + 1) * NV), NV the power of two with 32 * NV >= E. Bound by
+// instructions, not bytes: a row of 256 fp32 logits is 1 KB, 0.15 us of one SM's share of HBM, and its
+// 256 sigmoids alone are about 110 warp instructions. So the choice looks at few experts one by one: the
+// k-th largest of the lanes' maxima is a bound that at least k experts reach and few others do (about
+// 10 of 256 for k = 8); those, one per lane, are ranked against each other.
 // Backward: one warp per token, or per four tokens where only the chosen experts have a gradient: their
 // values are put into zeroed rows in shared memory, which are written in 16-byte pieces. Bound by HBM.
 #include <cuda_bf16.h>
@@ -158,33 +157,25 @@ __device__ __forceinline__ void load_row(const LT* row, int e0, int E, bool vec,
   }
 }
 
-// The lane's two largest keys and their slots among those whose bit of `gone` is clear; a tie keeps the
-// lower slot first.
+// This lane's keys to its place in the warp's row.
 template <int NV>
-__device__ __forceinline__ void two_best(const uint32_t (&key)[NV], uint32_t gone, uint32_t& b1,
-                                         int& i1, uint32_t& b2, int& i2) {
-  b1 = b2 = 0u;
-  i1 = i2 = 0;
+__device__ __forceinline__ void store_keys(uint32_t* row, int lane, const uint32_t (&key)[NV]) {
+  if constexpr (NV >= 4) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint32_t v = (gone >> i) & 1u ? 0u : key[i];
-    const bool p = v > b1, q = v > b2;
-    i2 = p ? i1 : (q ? i : i2);
-    b2 = max(b2, min(b1, v));
-    i1 = p ? i : i1;
-    b1 = max(b1, v);
+    for (int i = 0; i < NV; i += 4)
+      *reinterpret_cast<uint4*>(row + lane * NV + i) =
+          make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) row[lane * NV + i] = key[i];
   }
 }
 
-// Groups of any size: lane g ranks groups g and g + 32 from a copy of the row's keys in shared memory.
-// Sets the bits of `gone` whose experts' groups are not kept.
+// Groups of any size: lane g ranks groups g and g + 32 from the warp's row of keys. Sets the bits of
+// `gone` whose experts' groups are not kept.
 template <int NV>
-__device__ __forceinline__ void drop_groups(const GateArgs& a, const uint32_t (&key)[NV],
-                                               uint32_t* mine, int e0, int lane, uint32_t& gone) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (e0 + i < a.E) mine[e0 + i] = key[i];
-  __syncwarp();
+__device__ __forceinline__ void drop_groups(const GateArgs& a, const uint32_t* mine, int e0,
+                                            int lane, uint32_t& gone) {
   const int size = a.E / a.G;
   uint32_t gk[2];
 #pragma unroll
@@ -201,7 +192,6 @@ __device__ __forceinline__ void drop_groups(const GateArgs& a, const uint32_t (&
       gk[h] = a.top2 && b2 > kMaskedKey ? rank_key(key_rank(b1) + key_rank(b2)) : b1;
     }
   }
-  __syncwarp();  // the copy is overwritten by the warp's next row
   int before[2] = {0, 0};
   for (int g = 0; g < a.G; ++g) {
     const uint32_t v = __shfl_sync(kFull, g < 32 ? gk[0] : gk[1], g & 31);
@@ -219,8 +209,8 @@ __device__ __forceinline__ void drop_groups(const GateArgs& a, const uint32_t (&
 
 template <int NV, typename LT, bool SIGMOID>
 __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const GateArgs a) {
-  extern __shared__ uint32_t group_smem[];  // [kWarps][E] keys, only for groups that cross lanes
-  __shared__ int picked[kWarps][8];          // a row's choices
+  __shared__ __align__(16) uint32_t keys[kWarps][32 * NV];  // a row's keys
+  __shared__ int picked[kWarps][32];                        // its candidates
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned below = (1u << lane) - 1u;  // lanes before this one
@@ -247,34 +237,39 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
     float s[NV], top = 0.0f, total = 1.0f;
     if (need_scores || (!SIGMOID && !a.renorm)) {
       if (SIGMOID) {
+        // a logit of -infinity gives NaN, which ranks as switched off; finite ones that low take the
+        // division
         bool low = false;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          s[i] = l[i] == -INFINITY ? 0.0f : sigmoid_fast(l[i]);
+          s[i] = sigmoid_fast(l[i]);
           low |= l[i] < -80.0f && l[i] > -INFINITY;
         }
         if (low) {
 #pragma unroll
-          for (int i = 0; i < NV; ++i) s[i] = sigmoid(l[i]);
+          for (int i = 0; i < NV; ++i) s[i] = l[i] == -INFINITY ? NAN : sigmoid(l[i]);
         }
       } else {
         softmax_scores<NV>(l, s, top, total);
       }
       if (a.scores != nullptr) {
         float* to = a.scores + t * a.E + e0;
+        float o[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) o[i] = SIGMOID && l[i] == -INFINITY ? 0.0f : s[i];
         if (a.vec_scores && e0 + NV <= a.E) {
           if constexpr (NV >= 4) {
 #pragma unroll
             for (int i = 0; i < NV; i += 4)
-              *reinterpret_cast<float4*>(to + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+              *reinterpret_cast<float4*>(to + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) to[i] = s[i];
+            for (int i = 0; i < NV; ++i) to[i] = o[i];
           }
         } else {
 #pragma unroll
           for (int i = 0; i < NV; ++i)
-            if (e0 + i < a.E) to[i] = s[i];
+            if (e0 + i < a.E) to[i] = o[i];
         }
       }
     }
@@ -287,12 +282,19 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
       else if (SIGMOID)
         r = s[i];
       // r is NaN where the logit, the softmax or the bias is; past E the key is 0
-      key[i] = l[i] > -INFINITY && r == r ? rank_key(r) : kMaskedKey;
+      key[i] = (SIGMOID || l[i] > -INFINITY) && r == r ? rank_key(r) : kMaskedKey;
       if (e0 + i >= a.E) key[i] = 0u;
     }
-    uint32_t b1, b2, gone = 0u;  // this lane's best two; its slots that are taken or cannot be
-    int i1, i2;
-    two_best<NV>(key, 0u, b1, i1, b2, i2);
+    uint32_t* mine = keys[warp];
+    store_keys<NV>(mine, lane, key);
+    uint32_t b1 = 0u, b2 = 0u;  // this lane's two largest keys
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      b2 = max(b2, min(b1, key[i]));
+      b1 = max(b1, key[i]);
+    }
+    uint32_t gone = 0u;  // slots whose experts cannot be chosen
+    __syncwarp();
     if (a.G > 0) {
       if (a.lanes > 0) {  // a group is `lanes` whole lanes, a power of two
         uint32_t g1 = b1, g2 = b2;
@@ -310,44 +312,75 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
           before += v > g1 || (v == g1 && g < group);
         }
         if (before >= a.Gk) {
-          b1 = b2 = 0u;
+          b1 = 0u;
           gone = 0xffffffffu;
         }
       } else {
-        drop_groups<NV>(a, key, group_smem + warp * a.E, e0, lane, gone);
-        two_best<NV>(key, gone, b1, i1, b2, i2);
+        drop_groups<NV>(a, mine, e0, lane, gone);
+        b1 = 0u;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) b1 = max(b1, (gone >> i) & 1u ? 0u : key[i]);
       }
     }
-    // top-k: the largest key over the lanes, lowest lane first; its lane notes the choice
-    bool one = false;  // this lane's second best moved up: b2 is not its next
+    // the k-th largest of the lanes' maxima (equal ones count once): at least k experts reach it, or it
+    // is 0
+    uint32_t bound = 0u;
     for (int j = 0; j < a.k; ++j) {
-      const uint32_t best = __reduce_max_sync(kFull, b1);
-      const unsigned at = __ballot_sync(kFull, b1 == best);
-      const bool mine = b1 == best && (at & below) == 0u;
-      bool again = false;
-      if (mine) {
-        picked[warp][j] = e0 + i1;
-        gone |= 1u << i1;
-        again = one;
-        b1 = b2;
-        i1 = i2;
-        one = true;
+      bound = __reduce_max_sync(kFull, b1);
+      b1 = b1 == bound ? 0u : b1;
+    }
+    uint32_t cand = 0u;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) cand |= key[i] >= bound && key[i] > 0u ? 1u << i : 0u;
+    cand &= ~gone;
+    const int n = __reduce_add_sync(kFull, __popc(cand));
+    int my_idx = 0, place = 32;  // this lane's expert, and its place among the chosen
+    if (n <= 32) {
+      // one candidate per lane
+      int m = 0;
+      for (unsigned more = __ballot_sync(kFull, cand != 0u); more != 0u;
+           more = __ballot_sync(kFull, cand != 0u)) {
+        if (cand != 0u) picked[warp][m + __popc(more & below)] = e0 + __ffs(cand) - 1;
+        cand &= cand - 1u;
+        m += __popc(more);
       }
-      if (__any_sync(kFull, again)) {
-        uint32_t n1, n2;
-        int m1, m2;
-        two_best<NV>(key, gone, n1, m1, n2, m2);
-        if (again) {
-          b1 = n1, b2 = n2, i1 = m1, i2 = m2;
-          one = false;
+      __syncwarp();
+      uint32_t my_key = 0u;
+      if (lane < n) {
+        my_idx = picked[warp][lane];
+        my_key = mine[my_idx];
+        place = 0;
+      }
+      for (int j = 0; j < n; ++j) {
+        const uint32_t v = __shfl_sync(kFull, my_key, j);
+        const int e = __shfl_sync(kFull, my_idx, j);
+        place += v > my_key || (v == my_key && e < my_idx);
+      }
+    } else {
+      // more than 32 share the bound (many equal logits): one warp-wide maximum per choice, lowest lane
+      // and slot first
+      for (int j = 0; j < a.k; ++j) {
+        uint32_t best = 0u;
+        int slot = 0;
+#pragma unroll
+        for (int i = NV - 1; i >= 0; --i) {
+          const uint32_t v = (gone >> i) & 1u ? 0u : key[i];
+          slot = v >= best ? i : slot;
+          best = max(best, v);
+        }
+        const uint32_t first = __reduce_max_sync(kFull, best);
+        const int owner = __ffs(__ballot_sync(kFull, best == first)) - 1;
+        const int e = __shfl_sync(kFull, e0 + slot, owner);
+        if (lane == owner) gone |= 1u << slot;
+        if (lane == j) {
+          my_idx = e;
+          place = j;
         }
       }
     }
-    __syncwarp();
-    const int my_idx = picked[warp][lane & 7];
-    __syncwarp();  // it is written again for the warp's next row
-    // weights: lane j < k recomputes its choice's score from the logit
-    const bool on = lane < a.k;
+    __syncwarp();  // picked and keys are written again for the warp's next row
+    // weights: the lanes with a place below k recompute their choice's score from the logit
+    const bool on = place < a.k;
     const float sel = on ? load_logit(row + my_idx) : -INFINITY;
     float w;
     if (SIGMOID) {
@@ -363,8 +396,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
       w = sum == 0.0f ? 0.0f : w / sum;
     }
     if (on) {
-      a.idx[t * a.k + lane] = my_idx;
-      a.w[t * a.k + lane] = bad ? NAN : a.scale * w;
+      a.idx[t * a.k + place] = my_idx;
+      a.w[t * a.k + place] = bad ? NAN : a.scale * w;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) l[i] = next[i];
@@ -578,12 +611,11 @@ int lane_values(int E) {
 
 template <int NV, typename LT, bool SIGMOID>
 cudaError_t gate_one(const GateArgs& a, cudaStream_t st) {
-  const size_t smem = a.G > 0 && a.lanes == 0 ? sizeof(uint32_t) * kWarps * a.E : 0;
   // persistent: at most as many CTAs as the GPU holds at once
   const long long ctas = ((long long)a.T + kWarps - 1) / kWarps;
   return launch_k(gate_kernel<NV, LT, SIGMOID>,
                   dim3((unsigned)std::min(ctas, (long long)num_sms() * kCtasPerSm)),
-                  dim3(32 * kWarps), smem, st, a);
+                  dim3(32 * kWarps), 0, st, a);
 }
 template <int NV, typename LT, bool SIGMOID>
 cudaError_t gate_grad_one(const GateGradArgs& a, cudaStream_t st) {
