@@ -110,8 +110,14 @@ __device__ __forceinline__ void softmax_scores(const float (&l)[NV], float (&s)[
   // lanes may differ in the last place of lo only; lane 0's pair is everyone's
   total = __shfl_sync(kFull, __fadd_rn(hi, lo), 0);
   total = total == 0.0f ? 1.0f : total;
+  // the quotient by one correction of e * (1 / total) (Markstein 1990): correctly rounded for normal
+  // quotients, without a branch per element
+  const float inv = 1.0f / total;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) s[i] = s[i] / total;
+  for (int i = 0; i < NV; ++i) {
+    const float q = s[i] * inv;
+    s[i] = fmaf(fmaf(-q, total, s[i]), inv, q);
+  }
 }
 
 // NV consecutive elements from p; vec: p is aligned to min(16, their bytes) and all are there.
@@ -276,14 +282,15 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
     uint32_t key[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float r = l[i];
-      if (a.bias != nullptr)
-        r = s[i] + bias[i];
-      else if (SIGMOID)
-        r = s[i];
-      // r is NaN where the logit, the softmax or the bias is; past E the key is 0
+      // without a bias its registers are 0, which leaves a sigmoid as it is; a softmax without one is
+      // ranked by its logits. r is NaN where the logit, the score or the bias is
+      const float r = SIGMOID || a.bias != nullptr ? s[i] + bias[i] : l[i];
       key[i] = (SIGMOID || l[i] > -INFINITY) && r == r ? rank_key(r) : kMaskedKey;
-      if (e0 + i >= a.E) key[i] = 0u;
+    }
+    if (e0 + NV > a.E) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (e0 + i >= a.E) key[i] = 0u;
     }
     uint32_t* mine = keys[warp];
     store_keys<NV>(mine, lane, key);
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
         if (a.top2 && g2 > kMaskedKey) g1 = rank_key(key_rank(g1) + key_rank(g2));
         // kept when fewer than Gk groups precede it
         int before = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int g = 0; g < a.G; ++g) {
           const uint32_t v = __shfl_sync(kFull, g1, g * a.lanes);
           before += v > g1 || (v == g1 && g < group);
@@ -325,13 +332,16 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
     // the k-th largest of the lanes' maxima (equal ones count once): at least k experts reach it, or it
     // is 0
     uint32_t bound = 0u;
-    for (int j = 0; j < a.k; ++j) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j == a.k) break;
       bound = __reduce_max_sync(kFull, b1);
       b1 = b1 == bound ? 0u : b1;
     }
+    bound = max(bound, 1u);
     uint32_t cand = 0u;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) cand |= key[i] >= bound && key[i] > 0u ? 1u << i : 0u;
+    for (int i = 0; i < NV; ++i) cand |= key[i] >= bound ? 1u << i : 0u;
     cand &= ~gone;
     const int n = __reduce_add_sync(kFull, __popc(cand));
     int my_idx = 0, place = 32;  // this lane's expert, and its place among the chosen
