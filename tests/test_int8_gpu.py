@@ -5,10 +5,11 @@ Tolerances, before any run (u = 2^-24):
   product        integer sums below 2^24 are exact: conversion, scale product and result round once
                  each, 4 u. Larger sums (the all-127 case): at most 2^-23 per 16 products added,
                  K / 16 * 2^-23. bf16 and fp16 outputs are the fp32 output rounded once, bit for bit.
-  experts        against 64 bits. A code moves by one where fp32 and 64 bits round a value to different
-                 sides, bf16 values x / scale that are exact ties (one in a few hundred) among them:
-                 sqrt(1 / 300) / 25 of a row's norm, 2.3e-3, in x and less in H. 5e-3 of the norm of the
-                 whole, and 5e-2 of the largest output for one value.
+  experts        against 64 bits, x quantized by the rule in fp32 (bf16 values x / scale are often exact
+                 ties, which 64 bits would break otherwise). A code of H moves by one where fp32 and 64
+                 bits round its value to different sides, one in a few hundred at most:
+                 sqrt(1 / 300) / 25 of a row's norm, 2.3e-3. 5e-3 of the norm of the whole, and 5e-2 of
+                 the largest output for one value.
 """
 import numpy as np
 import pytest
@@ -174,6 +175,36 @@ def test_largest_sums(rows):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[3, 0, 4], [7], [2, 1, 1, 1, 1, 1], [5, 20, 8], [90, 3]])
+def test_segments_of_few_rows_and_long_sums(counts):
+    """Up to eight rows in all, and products whose K is done in pieces (K = 2064: 17 stages)."""
+    n, rows = len(counts), sum(counts)
+    off = [0] + list(np.cumsum(counts))
+    for K, N in ((2064, 130), (4096, 258), (16, 5)):
+        # codes whose sums stay below 2^24: at most 4096 * 60 * 60
+        qx, qw = (torch.randint(-60, 61, s, generator=gen(9), dtype=torch.int8)
+                  for s in ((rows, K), (n, N, K)))
+        sx, sw = torch.rand(rows, generator=gen(7)), torch.rand(n, N, generator=gen(8))
+        y, status = product(qx, sx, qw, sw, off, torch.float32)
+        want = product64(qx, sx, qw, sw, off)
+        assert status == 0
+        assert ((y.double().cpu() - want).abs() <= 4 * U * want.abs()).all()
+
+
+@pytest.mark.gpu
+def test_a_row_is_the_same_among_few_and_many():
+    """Integer sums do not depend on the path that a number of rows takes."""
+    K, N = 1552, 520
+    qx = torch.randint(-90, 91, (900, K), generator=gen(1), dtype=torch.int8)
+    qw = torch.randint(-90, 91, (1, N, K), generator=gen(2), dtype=torch.int8)
+    sx, sw = torch.rand(900, generator=gen(3)), torch.rand(1, N, generator=gen(4))
+    all_rows, _ = product(qx, sx, qw, sw, None, torch.bfloat16)
+    for rows in (1, 2, 4, 8, 9, 33, 97, 200, 500):
+        y, _ = product(qx[:rows], sx[:rows], qw, sw, None, torch.bfloat16)
+        assert torch.equal(y, all_rows[:rows]), rows
+
+
+@pytest.mark.gpu
 def test_bad_offsets_are_reported_and_contained():
     K, N = 64, 64
     qx, qw = codes(20, K, seed=1), codes(3, N, K, seed=2)
@@ -233,7 +264,8 @@ def layer(T, d, E, k, f, S, cap, seed, one_expert=False):
 
 def experts64(cfg, st, gates=True):
     T, k, E, S, d = cfg.T, cfg.top_k, cfg.E, cfg.n_shared, cfg.d
-    q, s = q64(st["x"].double())
+    q, s = (torch.from_numpy(v).double().cuda() for v in rows32(st["x"].float().cpu().numpy()))
+    s = s[:, None]
     y = torch.full(((k + S) * T, d), float("nan"), dtype=torch.float64, device="cuda")
     off = st["offsets"].tolist()
     for e in range(E):
@@ -279,6 +311,18 @@ def test_experts(T, d, E, k, f, S, cap):
         outs.append(z)
     check(outs[0], experts64(cfg, st, gates=False))
     assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 4, 5, 8, 9])
+@pytest.mark.parametrize("E,k,S", [(256, 8, 1), (8, 3, 4), (40, 2, 0)])
+def test_experts_of_few_tokens(T, E, k, S):
+    cfg, st = layer(T, 192, E, k, 128, S, 0, seed=T + E)
+    y = torch.full(((k + S) * T, 192), float("nan"), dtype=torch.float16, device="cuda")
+    M.grouped_ffn_int8(cfg, st["x"], st["perm_slot"], st["offsets"], st["topk_w"], st["weights"], y,
+                       st["ws"])
+    assert M.device_status(st["ws"]) == 0
+    check(y, experts64(cfg, st))
 
 
 @pytest.mark.gpu
