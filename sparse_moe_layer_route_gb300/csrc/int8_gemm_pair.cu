@@ -7,16 +7,22 @@
 // only half of the rows, which the MMA reads once for both: 40 KB per 64 k against 49 KB of shared-memory
 // bandwidth in the 384 clk that N = 192 takes, and half the widening per MMA.
 //
-// A unit is 256 channels (SwiGLU pass: 128 channels of gate and up) x up to 192 rows of one segment.
+// A unit is 256 channels (SwiGLU pass: 128 channels of gate and up) x up to NT rows of one segment.
 // Rank r of a pair holds channels [128 r, 128 r + 128) and rows [n / 2 * r, n / 2 * (r + 1)) of the n
 // rows the MMA takes (the unit's rows rounded up to 32). SwiGLU pass: rank r holds 64 channels; TMEM lanes
 // 32 w + l, l < 16, hold the gate codes of channel 16 w + l and lanes 32 w + 16 + l the up codes, so that
 // a warp's epilogue swaps halves by shuffles. Roles per CTA (512 threads):
-//   warp 0       TMA producer: the CTA's 128 code rows x 128 B and two [96 rows x 64 k] fp16 tiles a stage
+//   warp 0       TMA producer: the CTA's 128 code rows x 128 B and two [NT / 2 rows x 64 k] fp16 tiles a
+//                step (128 k)
 //   warp 1       MMA issuer (rank 0)
-//   warp 2       TMEM allocator: two accumulators of 192 columns, four 32-column slots of widened codes
-//   warps 4-7    epilogue, overlapping the next unit's MMAs
-//   warps 8-15   widen: four warps the first 64 k of each stage, four the second
+//   warp 2       TMEM allocator: NACC accumulators of NT columns, NSLOT 64-column slots of widened codes
+//   warps 4-7    epilogue, overlapping the next unit's MMAs where there are two accumulators
+//   warps 8-15   widen: four warps the first 64 k of each step, four the second
+// The MMA issuer's barrier operations are few, because one behind a commit costs it about 300 clk, with or
+// without something to wait for: per 128 k it waits once (`ready`: both CTAs' rows have landed and all 16
+// widening warps have stored) and commits once (`done`, to both CTAs), and `done` frees the step's
+// stage and, with it, the slot of widened codes. (With a wait and a commit for each 64 k slot and each
+// stage, a 64 k slot took 480 clk whatever its N.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -29,21 +35,24 @@
 namespace moe {
 namespace {
 
-constexpr int kNT = 192;                            // rows per unit (MMA N)
-constexpr int kABytes = kInt8Ch * kInt8StageK;      // 16 KB of codes
-constexpr int kBSub = kNT / 2 * 128;                // one [96 rows x 64 k] fp16 tile
-constexpr int kStageBytes = kABytes + 2 * kBSub;    // 40 KB
-constexpr int kStages = 5;
-constexpr int kAcc = 2;                             // accumulators
-constexpr int kSlots = 4;                           // widened codes, 64 k each
-constexpr int kSlotCol = kAcc * kNT;                   // their first TMEM column
-constexpr int kBars = 3 * kStages + 2 * kSlots + 2 * kAcc + 1;
-constexpr int kSmemBytes =
-    kStages * kStageBytes + 2 * kInt8StepBytes + 1024 /*align*/ + 512 /*barriers*/;
-static_assert(kSlotCol + kSlots * 32 <= 512, "TMEM columns");
-static_assert(8 * kBars + 8 <= 512, "barrier block");
+constexpr int kABytes = kInt8Ch * kInt8StageK;  // 16 KB of codes
 
-template <int PASS, int OUT>
+template <int NT_, int NACC_, int NSLOT_, int STAGES_>
+struct Cfg {
+  static constexpr int NT = NT_, NACC = NACC_, NSLOT = NSLOT_, STAGES = STAGES_;
+  static constexpr int kBSub = NT / 2 * 128;  // one [NT / 2 rows x 64 k] fp16 tile
+  static constexpr int kStageBytes = kABytes + 2 * kBSub;
+  static constexpr int kSlotCol = NACC * NT;  // first TMEM column of the widened codes
+  static constexpr int kBars = 3 * STAGES + 2 * NACC + 1;
+  static constexpr int kSmemBytes =
+      STAGES * kStageBytes + 2 * kInt8StepBytes + 1024 /*align*/ + 256 /*barriers*/;
+  static_assert(kSlotCol + NSLOT * 64 <= 512, "TMEM columns");
+  static_assert(NSLOT <= STAGES, "a slot's last step is known by its stage's barrier");
+  static_assert(kBSub % 1024 == 0 && NT % 32 == 0, "swizzle atoms; epilogue steps");
+  static_assert(8 * kBars + 8 <= 256, "barrier block");
+};
+
+template <int PASS, int OUT, typename C>
 __global__ void __launch_bounds__(kInt8Threads, 1)
     int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmA,
@@ -52,6 +61,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
                           const __grid_constant__ CUtensorMap tmShA2, const Int8Gemm g) {
   constexpr bool GLU = PASS == kInt8SwiGLU;
   constexpr int UCH = GLU ? 128 : 256;  // output channels per unit
+  constexpr int kNT = C::NT, kStages = C::STAGES, kBSub = C::kBSub, kStageBytes = C::kStageBytes;
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ SegTable segs;
@@ -62,15 +72,13 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   uint8_t* const gbase = smem_raw + (base - raw);
   uint8_t* const stage_out = gbase + kStages * kStageBytes;  // the epilogue's two steps
   const uint32_t bar0 = base + kStages * kStageBytes + 2 * kInt8StepBytes;
-  auto codes_bar = [&](int s) { return bar0 + 8u * s; };              // own codes have landed
-  auto rows_bar = [&](int s) { return bar0 + 8u * (kStages + s); };   // rank 0: both CTAs' rows
-  auto empty_bar = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
-  auto afull_bar = [&](int s) { return bar0 + 8u * (3 * kStages + s); };  // rank 0: both CTAs
-  auto aempty_bar = [&](int s) { return bar0 + 8u * (3 * kStages + kSlots + s); };
-  auto dfull_bar = [&](int b) { return bar0 + 8u * (3 * kStages + 2 * kSlots + b); };
-  auto dempty_bar = [&](int b) { return bar0 + 8u * (3 * kStages + 2 * kSlots + kAcc + b); };  // rank 0
-  const uint32_t mma_done_bar = bar0 + 8u * (kBars - 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stage_out + 2 * kInt8StepBytes + 8 * kBars);
+  auto codes_bar = [&](int s) { return bar0 + 8u * s; };                // own codes have landed
+  auto ready_bar = [&](int s) { return bar0 + 8u * (kStages + s); };    // rank 0: see above
+  auto done_bar = [&](int s) { return bar0 + 8u * (2 * kStages + s); };  // the step's MMAs are done
+  auto dfull_bar = [&](int b) { return bar0 + 8u * (3 * kStages + b); };
+  auto dempty_bar = [&](int b) { return bar0 + 8u * (3 * kStages + C::NACC + b); };  // rank 0
+  const uint32_t mma_done_bar = bar0 + 8u * (C::kBars - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stage_out + 2 * kInt8StepBytes + 8 * C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -81,14 +89,10 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(codes_bar(s), 1);
-      ptx::mbar_init(rows_bar(s), 1);
-      ptx::mbar_init(empty_bar(s), 9);  // eight widening warps and the pair's MMAs
+      ptx::mbar_init(ready_bar(s), 17);  // rows (with their bytes), eight widening warps of each CTA
+      ptx::mbar_init(done_bar(s), 1);
     }
-    for (int s = 0; s < kSlots; ++s) {
-      ptx::mbar_init(afull_bar(s), 8);  // four widening warps of each CTA
-      ptx::mbar_init(aempty_bar(s), 1);
-    }
-    for (int b = 0; b < kAcc; ++b) {
+    for (int b = 0; b < C::NACC; ++b) {
       ptx::mbar_init(dfull_bar(b), 1);
       ptx::mbar_init(dempty_bar(b), 8);  // four epilogue warps of each CTA
     }
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int n_ct = (g.N + UCH - 1) / UCH;
   const int n_sub = (g.K + 63) / 64;
-  const int n_stage = (n_sub + 1) / 2;
+  const int n_step = (n_sub + 1) / 2;
   const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct;
   const long long pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   auto mma_rows = [](const Unit& u) { return (u.rows + 31) & ~31; };
@@ -131,16 +135,16 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         const CUtensorMap* a1 = GLU ? (sh ? &tmShA2 : &tmA2) : a0;
         const int ch0 = u.ct * UCH + (int)rank * (UCH / 2), ch1 = GLU ? ch0 : ch0 + 64;
         const int brow = u.brow0 + (int)rank * (mma_rows(u) / 2);
-        for (int i = 0; i < n_stage; ++i) {
-          if (!ptx::mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, g.status,
-                                              MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
+        for (int i = 0; i < n_step; ++i) {
+          if (!ptx::mbar_wait_bounded(done_bar(stage), phase ^ 1u, abort_flag, g.status,
+                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
             break;
           }
           const uint32_t sA = base + stage * kStageBytes, sB = sA + kABytes;
           const uint32_t cb = codes_bar(stage);
-          const uint32_t rb = leader ? rows_bar(stage) : ptx::mapa_shared(rows_bar(stage), 0);
-          const bool half = 2 * i + 1 < n_sub;  // the stage's second 64 k hold something
+          const uint32_t rb = leader ? ready_bar(stage) : ptx::mapa_shared(ready_bar(stage), 0);
+          const bool half = 2 * i + 1 < n_sub;  // the step's second 64 k hold something
           ptx::mbar_arrive_expect_tx(cb, kABytes);
           ptx::tma_load_3d(sA, a0, cb, i * kInt8StageK, ch0, ex);
           ptx::tma_load_3d(sA + kABytes / 2, a1, cb, i * kInt8StageK, ch1, ex);
@@ -155,62 +159,55 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
           }
         }
       }
-      // never leave while a copy into either CTA's shared memory may still be in flight (the rows
-      // of both are counted on rank 0)
+      // never leave while a copy into this CTA's shared memory may still be in flight. The rows' barrier
+      // also counts the widening warps, so after an abort it may not complete: then the wait runs out
       for (int s = 0; s < kStages; ++s)
         if (issued & (1u << s)) {
           volatile int no_abort = 0;
-          ptx::mbar_wait_bounded(codes_bar(s), (last_parity >> s) & 1u, &no_abort,
-                                         g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
-                                         kInt8WaitNs / 4);
-          if (leader)
-            ptx::mbar_wait_bounded(rows_bar(s), (last_parity >> s) & 1u, &no_abort,
-                                           g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
-                                           kInt8WaitNs / 4);
+          ptx::mbar_wait_bounded(codes_bar(s), (last_parity >> s) & 1u, &no_abort, g.status,
+                                 MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs / 4);
+          ptx::mbar_wait_bounded(done_bar(s), (last_parity >> s) & 1u, &no_abort, g.status,
+                                 MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs / 4);
         }
     }
     __syncwarp();
   } else if (warp == 1) {
     if (leader && ptx::elect_one()) {
       // ---------------------------------------------------------------- MMA issuer (rank 0)
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, sub = 0, acc_phase = 0;  // sub: 64-k slots used so far
+      int stage = 0, slot = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (long long w = pair; w < total && ok; w += n_pairs) {
         const Unit u = find_unit<GLU>(segs, g, n_ct, kNT, w);
         const uint32_t idesc = ptx::idesc_f16kind_f32(256, (uint32_t)mma_rows(u), 0, 0, 0u);
         if (!ptx::mbar_wait_bounded(dempty_bar(acc), acc_phase ^ 1u, abort_flag, g.status,
-                                            MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs))
+                                    MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs))
           break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc * kNT);
-        for (int i = 0; i < n_stage && ok; ++i) {
-          if (!ptx::mbar_wait_bounded(rows_bar(stage), phase, abort_flag, g.status,
-                                              MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
+        for (int i = 0; i < n_step; ++i) {
+          if (!ptx::mbar_wait_bounded(ready_bar(stage), phase, abort_flag, g.status,
+                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
             break;
           }
+          ptx::tc_fence_after();
+          const uint32_t a = tmem_base + C::kSlotCol + slot * 64;
+          // rows: K-major, 128 B each, 8-row groups 1024 B apart; a K step of 16 = +32 B
           const uint64_t bd =
               ptx::smem_desc_sw128(base + stage * kStageBytes + kABytes, 16, 1024);
-          for (int h = 0; h < 2 && 2 * i + h < n_sub; ++h, ++sub) {
-            const uint32_t slot = sub & (kSlots - 1);
-            if (!ptx::mbar_wait_bounded(afull_bar(slot), (sub / kSlots) & 1u, abort_flag,
-                                                g.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
-                                                kInt8WaitNs)) {
-              ok = false;
-              break;
-            }
-            ptx::tc_fence_after();
-            const uint32_t a = tmem_base + kSlotCol + slot * 32;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::umma_f16_ta_cg2(d, a + kk * 8, bd + (uint64_t)(kk * 2), idesc,
+                                 (i | kk) != 0 ? 1u : 0u);
+          if (2 * i + 1 < n_sub) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              // rows: K-major, 128 B each, 8-row groups 1024 B apart; a K step of 16 = +32 B
-              ptx::umma_f16_ta_cg2(d, a + kk * 8, bd + (uint64_t)((h * kBSub + kk * 32) >> 4),
-                                   idesc, (i | h | kk) != 0 ? 1u : 0u);
-            ptx::umma_commit_cg2(aempty_bar(slot), 0x3);
+              ptx::umma_f16_ta_cg2(d, a + 32 + kk * 8, bd + (uint64_t)((kBSub >> 4) + kk * 2),
+                                   idesc, 1u);
           }
-          if (!ok) break;
-          ptx::umma_commit_cg2(empty_bar(stage), 0x3);
+          ptx::umma_commit_cg2(done_bar(stage), 0x3);
+          if (++slot == C::NSLOT) slot = 0;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
@@ -218,7 +215,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         }
         if (!ok) break;
         ptx::umma_commit_cg2(dfull_bar(acc), 0x3);
-        if (++acc == kAcc) {
+        if (++acc == C::NACC) {
           acc = 0;
           acc_phase ^= 1u;
         }
@@ -232,15 +229,15 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ widening warps (both)
-    const int h = (warp - 8) >> 2, q = warp & 3;  // half of the stage; TMEM lanes [32 q, 32 q + 32)
+    const int h = (warp - 8) >> 2, q = warp & 3;  // half of the step; TMEM lanes [32 q, 32 q + 32)
     const int row = GLU ? 16 * q + (lane & 15) + 64 * (lane >> 4) : 32 * q + lane;
-    int stage = 0;
-    uint32_t phase = 0, sub = 0;
+    int stage = 0, slot = 0, dstage = 0;  // dstage: the stage of the step NSLOT before this one
+    uint32_t phase = 0, dphase = 0, step = 0;
     bool ok = true;
     for (long long w = pair; w < total && ok; w += n_pairs) {
-      for (int i = 0; i < n_stage; ++i) {
+      for (int i = 0; i < n_step; ++i, ++step) {
         if (!ptx::mbar_wait_bounded_warp(codes_bar(stage), phase, abort_flag, g.status,
-                                                 MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
+                                         MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
           ok = false;
           break;
         }
@@ -259,35 +256,38 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
             widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
           }
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(empty_bar(stage));  // the codes are in registers
-        if (on) {
-          const uint32_t mine = sub + (uint32_t)(2 * i + h), slot = mine & (kSlots - 1);
-          if (!ptx::mbar_wait_bounded_warp(
-                  aempty_bar(slot), ((mine / kSlots) & 1u) ^ 1u, abort_flag, g.status,
-                  MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
+        if (step >= (uint32_t)C::NSLOT) {  // the MMAs that read this slot last are done
+          if (!ptx::mbar_wait_bounded_warp(done_bar(dstage), dphase, abort_flag, g.status,
+                                           MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
             break;
           }
-          ptx::tc_fence_after();
-          ptx::tmem_st_32x32b_x32(
-              tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(kSlotCol + slot * 32), r);
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (leader)
-              ptx::mbar_arrive(afull_bar(slot));
-            else
-              ptx::mbar_arrive_remote(ptx::mapa_shared(afull_bar(slot), 0));
+          if (++dstage == kStages) {
+            dstage = 0;
+            dphase ^= 1u;
           }
         }
+        if (on) {
+          ptx::tc_fence_after();
+          ptx::tmem_st_32x32b_x32(tmem_base + ((uint32_t)(32 * q) << 16) +
+                                      (uint32_t)(C::kSlotCol + slot * 64 + h * 32),
+                                  r);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            ptx::mbar_arrive(ready_bar(stage));
+          else
+            ptx::mbar_arrive_remote(ptx::mapa_shared(ready_bar(stage), 0));
+        }
+        if (++slot == C::NSLOT) slot = 0;
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      sub += (uint32_t)n_sub;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue (both)
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
           }
         }
       }
-      if (++acc == kAcc) {
+      if (++acc == C::NACC) {
         acc = 0;
         acc_phase ^= 1u;
       }
@@ -387,11 +387,11 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   }
 }
 
-template <int PASS, int OUT>
+template <int PASS, int OUT, typename C>
 cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
   constexpr CUtensorMapDataType kCode = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   CUtensorMap b, a, a2, sa, sa2;
-  bool ok = make_tmap_2d(&b, g.xq, g.x_rows, g.K, 64, kNT / 2, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) &&
+  bool ok = make_tmap_2d(&b, g.xq, g.x_rows, g.K, 64, C::NT / 2, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) &&
             make_tmap_3d(&a, g.qw, g.n_mat, g.N, g.K, kInt8StageK, 64, kCode, 1);
   a2 = a;
   if (ok && PASS == kInt8SwiGLU)
@@ -404,14 +404,14 @@ cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
       ok = make_tmap_3d(&sa2, g.sh_qw2, g.S, g.N, g.K, kInt8StageK, 64, kCode, 1);
   }
   if (!ok) return cudaErrorInvalidValue;
-  auto kern = int8_gemm_pair_kernel<PASS, OUT>;
+  auto kern = int8_gemm_pair_kernel<PASS, OUT, C>;
   const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_sms() / 2 * 2);  // persistent: one CTA pair per two SMs
   cfg.blockDim = dim3(kInt8Threads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -425,18 +425,23 @@ cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, b, a, a2, sa, sa2, g);
 }
 
+template <int PASS, int OUT>
+cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
+  return launch_one<PASS, OUT, Cfg<192, 2, 2, 5>>(g, st);
+}
+
 }  // namespace
 
 cudaError_t launch_int8_gemm_pair(Int8Pass pass, const Int8Gemm& g, cudaStream_t st) {
   switch (pass) {
-    case kInt8SwiGLU: return launch_one<kInt8SwiGLU, MOE_DTYPE_F32>(g, st);
-    case kInt8Slot: return launch_one<kInt8Slot, MOE_DTYPE_F16>(g, st);
+    case kInt8SwiGLU: return launch_pass<kInt8SwiGLU, MOE_DTYPE_F32>(g, st);
+    case kInt8Slot: return launch_pass<kInt8Slot, MOE_DTYPE_F16>(g, st);
     default: break;
   }
   switch (g.out_dtype) {
-    case MOE_DTYPE_F32: return launch_one<kInt8Matrix, MOE_DTYPE_F32>(g, st);
-    case MOE_DTYPE_BF16: return launch_one<kInt8Matrix, MOE_DTYPE_BF16>(g, st);
-    default: return launch_one<kInt8Matrix, MOE_DTYPE_F16>(g, st);
+    case MOE_DTYPE_F32: return launch_pass<kInt8Matrix, MOE_DTYPE_F32>(g, st);
+    case MOE_DTYPE_BF16: return launch_pass<kInt8Matrix, MOE_DTYPE_BF16>(g, st);
+    default: return launch_pass<kInt8Matrix, MOE_DTYPE_F16>(g, st);
   }
 }
 
