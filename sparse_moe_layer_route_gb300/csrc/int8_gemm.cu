@@ -429,15 +429,6 @@ cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
   return launch_k(kern, dim3(num_sms()), dim3(kInt8Threads), C::kSmemBytes, st, b, a, a2, sa, sa2, g);
 }
 
-template <int PASS, int OUT>
-cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
-  // rows per segment on average (an even spread): short segments leave most of a wide tile empty, and
-  // a narrow one leaves shared memory for more weight tiles in flight
-  const long long mean = g.rows / g.n_mat;
-  if (mean <= 32) return launch_one<PASS, OUT, 32, 2, 6>(g, st);
-  return launch_one<PASS, OUT, 96, 2, 2>(g, st);
-}
-
 // y = (sum of the pieces, in their order) * row scale * channel scale; rows past the last segment are left.
 template <typename YT>
 __global__ void __launch_bounds__(256) join_splits_kernel(const float* __restrict__ part,
@@ -489,7 +480,9 @@ cudaError_t launch_int8_split(const Int8Gemm& g, float* part, cudaStream_t st) {
   Int8Gemm p = g;
   p.splits = int8_splits(g.rows, g.K, g.N, g.n_mat);
   p.out = part;
-  cudaError_t e = launch_pass<kInt8Partial, MOE_DTYPE_F32>(p, st);
+  cudaError_t e = g.rows / g.n_mat <= 32
+                      ? launch_one<kInt8Partial, MOE_DTYPE_F32, 32, 2, 6>(p, st)
+                      : launch_one<kInt8Partial, MOE_DTYPE_F32, 96, 2, 2>(p, st);
   if (e != cudaSuccess) return e;
   p.out = g.out;
   const dim3 grid((g.N + 255) / 256, g.rows), block(256);
@@ -502,16 +495,20 @@ cudaError_t launch_int8_split(const Int8Gemm& g, float* part, cudaStream_t st) {
 }
 
 cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st) {
-  if (g.rows / g.n_mat > 96) return launch_int8_gemm_pair(pass, g, st);
+  // by the rows per segment of an even spread. Decode's short segments are bound by the weights, which
+  // single CTAs of 32-row tiles stream better (decode experts, 1 row a segment, 330 against 358 us for
+  // gate and up); from 16 rows on the pairs' cheaper tiles win (64 segments of [2048 x 2048], 24 rows
+  // each: 59 against 63 us)
+  if (g.rows / g.n_mat > 16) return launch_int8_gemm_pair(pass, g, st);
   switch (pass) {
-    case kInt8SwiGLU: return launch_pass<kInt8SwiGLU, MOE_DTYPE_F32>(g, st);
-    case kInt8Slot: return launch_pass<kInt8Slot, MOE_DTYPE_F16>(g, st);
+    case kInt8SwiGLU: return launch_one<kInt8SwiGLU, MOE_DTYPE_F32, 32, 2, 6>(g, st);
+    case kInt8Slot: return launch_one<kInt8Slot, MOE_DTYPE_F16, 32, 2, 6>(g, st);
     default: break;
   }
   switch (g.out_dtype) {
-    case MOE_DTYPE_F32: return launch_pass<kInt8Matrix, MOE_DTYPE_F32>(g, st);
-    case MOE_DTYPE_BF16: return launch_pass<kInt8Matrix, MOE_DTYPE_BF16>(g, st);
-    default: return launch_pass<kInt8Matrix, MOE_DTYPE_F16>(g, st);
+    case MOE_DTYPE_F32: return launch_one<kInt8Matrix, MOE_DTYPE_F32, 32, 2, 6>(g, st);
+    case MOE_DTYPE_BF16: return launch_one<kInt8Matrix, MOE_DTYPE_BF16, 32, 2, 6>(g, st);
+    default: return launch_one<kInt8Matrix, MOE_DTYPE_F16, 32, 2, 6>(g, st);
   }
 }
 

@@ -427,6 +427,10 @@ cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
 
 template <int PASS, int OUT>
 cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
+  // by the rows per segment of an even spread: a tile costs about the same whatever its rows, so the
+  // narrower one, with more slots and stages, is for segments that it holds (64 segments of
+  // [2048 x 2048], 96 rows each: 69 against 72 us; 128 rows each, half of them longer: 93 against 77)
+  if (g.rows / g.n_mat <= 104) return launch_one<PASS, OUT, Cfg<128, 2, 4, 6>>(g, st);
   return launch_one<PASS, OUT, Cfg<192, 2, 2, 5>>(g, st);
 }
 
