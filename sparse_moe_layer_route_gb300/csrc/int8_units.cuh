@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "int8.cuh"
 
@@ -170,7 +171,6 @@ struct Panel {
   static constexpr int kSize = OUT == MOE_DTYPE_F32 ? 4 : 2;
   static constexpr int kRowBytes = CH * kSize;
   static constexpr int kCols = kInt8StepBytes / kRowBytes;  // output rows per step
-  static constexpr int kPieces = kRowBytes / 16;
 
   static __device__ __forceinline__ void put(uint8_t* buf, int col, int ch, float y) {
     uint8_t* at = buf + col * kRowBytes + ch * kSize;
@@ -184,36 +184,41 @@ struct Panel {
       *reinterpret_cast<__half*>(at) = __float2half(y);
   }
 
-  // t: 0..127. The step's rows to the output: channels [ch0, ch0 + CH) of rows orow[0, kCols).
+  // t: 0..127. The step's rows to the output: the first `bytes` of a row's panel at panel + row * row_bytes,
+  // in pieces of VB bytes.
+  template <int VB>
+  static __device__ __forceinline__ void copy(uint8_t* panel, long long row_bytes, int bytes,
+                                              const uint8_t* buf, const int* orow, int t) {
+    using V = std::conditional_t<VB == 16, uint4,
+                                 std::conditional_t<VB == 8, uint2,
+                                                    std::conditional_t<VB == 4, uint32_t, uint16_t>>>;
+    constexpr int kPer = kRowBytes / VB, kN = kInt8StepBytes / (128 * VB);
+    V v[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = *reinterpret_cast<const V*>(buf + (i * 128 + t) * VB);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = (i * 128 + t) % kPer * VB, to = orow[(i * 128 + t) / kPer];
+      if (to >= 0 && at < bytes) *reinterpret_cast<V*>(panel + to * row_bytes + at) = v[i];
+    }
+  }
+  // Channels [ch0, ch0 + CH) of the output rows orow[0, kCols), in the widest pieces that the output's
+  // address, its row length and the panel's channels allow.
   static __device__ __forceinline__ void flush(uint8_t* out, int N, const uint8_t* buf,
                                                const int* orow, int ch0, int t) {
+    const int bytes = min(CH, N - ch0) * kSize;
+    if (bytes <= 0) return;
     const long long row_bytes = (long long)N * kSize;
-    if (ch0 + CH <= N && ((row_bytes | reinterpret_cast<long long>(out)) & 15) == 0) {
-      constexpr int kRows = 128 / kPieces;
-      const int piece = t % kPieces, r0 = t / kPieces;
-      uint4 v[kCols / kRows];
-#pragma unroll
-      for (int i = 0; i < kCols / kRows; ++i)
-        v[i] = *reinterpret_cast<const uint4*>(buf + (r0 + i * kRows) * kRowBytes + piece * 16);
-#pragma unroll
-      for (int i = 0; i < kCols / kRows; ++i) {
-        const int to = orow[r0 + i * kRows];
-        if (to >= 0)
-          *reinterpret_cast<uint4*>(out + to * row_bytes + (long long)ch0 * kSize + piece * 16) =
-              v[i];
-      }
-    } else if (t < CH && ch0 + t < N) {  // the last channels, or rows that are not in 16-byte pieces
-      for (int r = 0; r < kCols; ++r) {
-        const int to = orow[r];
-        if (to < 0) continue;
-        uint8_t* dst = out + to * row_bytes + (long long)(ch0 + t) * kSize;
-        const uint8_t* src = buf + r * kRowBytes + t * kSize;
-        if (kSize == 4)
-          *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
-        else
-          *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
-      }
-    }
+    uint8_t* panel = out + (long long)ch0 * kSize;
+    const unsigned odd = (unsigned)(row_bytes | reinterpret_cast<long long>(out)) | (unsigned)bytes;
+    if ((odd & 15u) == 0u)
+      copy<16>(panel, row_bytes, bytes, buf, orow, t);
+    else if ((odd & 7u) == 0u)
+      copy<8>(panel, row_bytes, bytes, buf, orow, t);
+    else if (kSize == 4 || (odd & 3u) == 0u)
+      copy<4>(panel, row_bytes, bytes, buf, orow, t);
+    else if constexpr (kSize == 2)
+      copy<2>(panel, row_bytes, bytes, buf, orow, t);
   }
 };
 
