@@ -119,10 +119,10 @@ __device__ __forceinline__ uint32_t row_max(uint32_t top, uint32_t* warp_top) {
 }
 
 // One row by W threads, thread t of them. VEC: rows in 16-byte pieces, d a multiple of 8 and at most
-// 64 W; the row stays in registers between its two passes. x / scale is first taken as x * (1 / scale),
-// within 2.3e-5 of the quotient for codes up to 127; where that is within 1e-4 of halfway between two
-// codes (about one value in 5000) the division decides. So the codes are those of the division at a
-// third of its instructions.
+// 64 W; the row stays in registers between its two passes. x / scale is q = x r with r the correctly rounded
+// 1 / scale, then q + (x - q scale) r: the correctly rounded quotient (Markstein 1990) in three
+// instructions without a branch, so the codes are the division's. (Halfway values are common among bf16
+// ones: dividing the near-halfway values alone took 15 of 66 us for 16384 rows of 7168.)
 template <int W, bool VEC, typename XT, typename QT>
 __device__ __forceinline__ void quantize_row(const XT* __restrict__ row, int d,
                                              QT* __restrict__ out, float* __restrict__ scale,
@@ -144,15 +144,14 @@ __device__ __forceinline__ void quantize_row(const XT* __restrict__ row, int d,
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if ((i * W + t) * 8 < d) {
-        float v[8], m[8], far = 0.0f;  // far: the largest distance from a whole number
+        float v[8], m[8];
         x[i].get(v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float y = __fmul_rn(v[j], r);
-          m[j] = __fadd_rn(y, kMagic);
-          far = fmaxf(far, fabsf(__fsub_rn(y, __fsub_rn(m[j], kMagic))));
+          m[j] = __fadd_rn(__fmaf_rn(__fmaf_rn(-y, s, v[j]), r, y), kMagic);
         }
-        if (far > 0.4999f || !plain) {
+        if (!plain) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) m[j] = (float)int8_code(v[j], s) + kMagic;
         }

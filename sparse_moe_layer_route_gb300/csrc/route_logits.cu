@@ -518,8 +518,15 @@ __global__ void __launch_bounds__(32 * kWarps) gate_grad_chosen_kernel(const Gat
   for (int i = 0; i < NV; ++i)
     *reinterpret_cast<float4*>(mine + (i * 32 + lane) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
   const float g = chosen_gradient<SIGMOID, true, 8>(a, on, sel, dw);
+  // the choices of a token are different experts; should one come twice all the same, it adds twice
+  const int place = on ? (lane >> 3) * a.E + my_idx : -1 - lane;
+  const unsigned same = __match_any_sync(kFull, place);
   __syncwarp();
-  if (on) atomicAdd(mine + (lane >> 3) * a.E + my_idx, g);  // an index that comes twice adds twice
+  if (!__any_sync(kFull, (same & (same - 1u)) != 0u)) {
+    if (on) mine[place] = g;
+  } else if (on) {
+    atomicAdd(mine + place, g);
+  }
   __syncwarp();
   LT* out = static_cast<LT*>(a.d_logits) + t0 * a.E;
   if (a.vec) {
