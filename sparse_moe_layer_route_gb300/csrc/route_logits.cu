@@ -497,10 +497,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float
 
 // Only the chosen experts have a gradient (no d_scores, and not a softmax without renormalisation).
 // Eight lanes per token, four consecutive tokens per warp, whose rows of d_logits are one run of 4 E
-// elements, put together in shared memory.
+// elements: zeros in 16-byte pieces, then the chosen experts' values on top (the warp's barrier orders
+// the two; put together in shared memory first, 65536 rows of 256 took 23 instead of 19 us).
 template <int NV, typename LT, bool SIGMOID>
 __global__ void __launch_bounds__(32 * kWarps) gate_grad_chosen_kernel(const GateGradArgs a) {
-  __shared__ __align__(16) float rows[kWarps][4 * 32 * NV];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long t0 = ((long long)blockIdx.x * kWarps + warp) * 4;
@@ -513,34 +513,30 @@ __global__ void __launch_bounds__(32 * kWarps) gate_grad_chosen_kernel(const Gat
   const float dw = on ? a.scale * a.d_w[t * a.k + j] : 0.0f;
   const float sel =
       on ? load_logit(static_cast<const LT*>(a.logits) + t * a.ld + my_idx) : -INFINITY;
-  float* mine = rows[warp];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    *reinterpret_cast<float4*>(mine + (i * 32 + lane) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float g = chosen_gradient<SIGMOID, true, 8>(a, on, sel, dw);
-  // the choices of a token are different experts; should one come twice all the same, it adds twice
-  const int place = on ? (lane >> 3) * a.E + my_idx : -1 - lane;
-  const unsigned same = __match_any_sync(kFull, place);
-  __syncwarp();
-  if (!__any_sync(kFull, (same & (same - 1u)) != 0u)) {
-    if (on) mine[place] = g;
-  } else if (on) {
-    atomicAdd(mine + place, g);
-  }
-  __syncwarp();
   LT* out = static_cast<LT*>(a.d_logits) + t0 * a.E;
   if (a.vec) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = (i * 32 + lane) * 4;
-      if (e < n * a.E) {
-        const float4 v = *reinterpret_cast<const float4*>(mine + e);
-        store4(out + e, v.x, v.y, v.z, v.w);
-      }
+      if (e < n * a.E) store4(out + e, 0.0f, 0.0f, 0.0f, 0.0f);
     }
   } else {
-    for (int e = lane; e < n * a.E; e += 32) store_logit(out + e, mine[e]);
+    for (int e = lane; e < n * a.E; e += 32) store_logit(out + e, 0.0f);
   }
+  float g = chosen_gradient<SIGMOID, true, 8>(a, on, sel, dw);
+  // the choices of a token are different experts; should one come twice all the same, it adds twice
+  const int place = on ? (lane >> 3) * a.E + my_idx : -1 - lane;
+  const unsigned same = __match_any_sync(kFull, place);
+  if (__any_sync(kFull, (same & (same - 1u)) != 0u)) {
+    float sum = 0.0f;
+    for (int l = 0; l < 32; ++l) {
+      const float v = __shfl_sync(kFull, g, l);
+      if ((same >> l) & 1u) sum += v;
+    }
+    g = sum;
+  }
+  __syncwarp();
+  if (on) store_logit(out + place, g);
 }
 
 // Every expert has a gradient. Lane l holds experts i / 4 * 128 + 4 l + i % 4 (NV >= 4), so that rows
