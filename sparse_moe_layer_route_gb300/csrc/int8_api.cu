@@ -10,12 +10,15 @@ namespace moe {
 namespace {
 
 constexpr size_t kHead = 512;  // status word and counter block, as in every workspace
-// Rows up to which int8_gemv.cu is faster than the tensor cores. A product: 8 rows of [14336 x 4096]
-// 22.7 against 24.2 us, 8 of [2048 x 7168] 13.4 against 15.1; 16 rows 38 against 24. The experts read
-// every hit expert once per 8 rows anyway, and gain up to 4 tokens (decode shape: 4 tokens 82 against
-// 91 us, 6 tokens 192 against 145).
-constexpr int kFewRows = 8;
-constexpr int kFewTokens = 4;
+// Where int8_gemv.cu is faster than the tensor cores: few rows, or so little work that a unit's long
+// pipeline (and the launches in front of it) is most of a tensor-core product's time.
+//   product: 8 rows of [14336 x 4096] 15.5 against 24 us, 16 rows 38 against 24; 0.4 G multiply-adds (200
+//   rows of [1000 x 2048]) 12 against 17, 0.6 G (20 segments of 30 rows) 24 against 14.
+//   experts: decode shape, 6 tokens 94 against 144 us, 12 tokens 166 against 204, 24 tokens 289 against
+//   281; 64 + 2 experts of [2048 x 1408], 6 a token, 12 tokens 94 against 95, 16 tokens 108 against 96; of
+//   small layers, 32 tokens, 60 M multiply-adds, 17 against 20, and 64 tokens, 240 M, 38 against 27.
+bool few_rows(long long rows, int K, int N) { return rows <= 8 || rows * K * N <= 400000000ll; }
+bool few_tokens(const Shape& s) { return s.T <= 12 || 3ll * s.rows * s.d * s.f <= 100000000ll; }
 
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 int dtype_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
@@ -39,7 +42,7 @@ size_t matmul_part(int32_t rows, int32_t K) {
   return kHead + ((size_t)rows * K * 2 + 255) / 256 * 256;
 }
 size_t matmul_part_bytes(int32_t rows, int32_t K, int32_t N, int32_t n_mat) {
-  const int splits = rows <= kFewRows ? 1 : int8_splits(rows, K, N, n_mat);
+  const int splits = few_rows(rows, K, N) ? 1 : int8_splits(rows, K, N, n_mat);
   return splits > 1 ? 4ull * splits * rows * N : 0;
 }
 
@@ -140,7 +143,7 @@ moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, co
   g.N = N;
   g.n_mat = n_mat;
   g.T = 1;
-  if (rows <= kFewRows) {
+  if (few_rows(rows, K, N)) {
     g.x8 = q_x;
     return cuda_status(launch_int8_gemv(kInt8Matrix, g, rows, st));
   }
@@ -182,7 +185,7 @@ moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const 
   const FfnLayout L = ffn_layout(s);
   const cudaStream_t st = (cudaStream_t)stream;
   // few tokens: 8-bit codes and integer dot products, else fp16 codes and the tensor cores
-  const bool few = s.T <= kFewTokens;
+  const bool few = few_tokens(s);
   int* status = at<int>(ws, 0);
   Int8Gemm g = {};
   g.xq = at<uint16_t>(ws, L.xq);

@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cstdint>
 
 #include "int8.cuh"
@@ -212,9 +213,12 @@ cudaError_t launch_out(const Int8Gemm& g, int most_rows, cudaStream_t st) {
     if (tiles > 65535) return cudaErrorInvalidValue;
     return launch_k(kern, dim3(gx, (unsigned)tiles), dim3(kThreads), 0, st, g);
   };
-  if (most_rows <= 1) return go(int8_gemv_kernel<PASS, OUT, 1>, 1);
-  if (most_rows <= 2) return go(int8_gemv_kernel<PASS, OUT, 2>, 2);
-  if (most_rows <= 4) return go(int8_gemv_kernel<PASS, OUT, 4>, 4);
+  // rows per tile: no more than any segment has, and no more than twice an even spread's (the rows that
+  // a tile does not have are computed all the same)
+  const long long want = std::min((long long)most_rows, 2 * ((g.rows + g.n_mat - 1ll) / g.n_mat));
+  if (want <= 1) return go(int8_gemv_kernel<PASS, OUT, 1>, 1);
+  if (want <= 2) return go(int8_gemv_kernel<PASS, OUT, 2>, 2);
+  if (want <= 4) return go(int8_gemv_kernel<PASS, OUT, 4>, 4);
   return go(int8_gemv_kernel<PASS, OUT, 8>, 8);
 }
 

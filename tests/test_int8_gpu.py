@@ -146,6 +146,71 @@ def test_one_matrix(rows, K, N, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts,K,N", [
+    ([20], 4096, 5200),                                   # K in pieces, rows of one narrow tile
+    ([129], 1552, 2100), ([700], 1040, 600),              # K in pieces, several row tiles
+    ([10] * 40 + [0] * 4 + [13, 33, 1, 64] * 5, 1232, 520),   # many short segments
+    ([100, 128, 129, 1, 0, 60, 97, 128] * 2, 704, 520),   # 128-row tiles of CTA pairs
+    ([3000], 272, 523), ([1700, 0, 1, 192, 193, 500], 336, 520)])   # 192-row tiles
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_tensor_core_products(counts, K, N, dtype):
+    """Products above the work that integer dot products take."""
+    n, rows = len(counts), sum(counts)
+    off = [0] + [int(v) for v in np.cumsum(counts)]
+    # codes whose sums stay below 2^24: at most 4096 * 60 * 60
+    qx, qw = (torch.randint(-60, 61, s, generator=gen(11), dtype=torch.int8)
+              for s in ((rows, K), (n, N, K)))
+    sx, sw = torch.rand(rows, generator=gen(12)) / 64, torch.rand(n, N, generator=gen(13)) / 64
+    y32, status = product(qx, sx, qw, sw, off if n > 1 else None, torch.float32)
+    assert status == 0
+    if dtype == torch.float32:
+        want = torch.zeros(rows, N, dtype=torch.float64, device="cuda")
+        for e in range(n):
+            r = slice(off[e], off[e + 1])
+            want[r] = (qx[r].cuda().double() @ qw[e].cuda().double().T) * sx[r, None].cuda() \
+                * sw[e].cuda()
+        assert ((y32.double() - want).abs() <= 4 * U * want.abs()).all()
+    else:
+        y, status = product(qx, sx, qw, sw, off if n > 1 else None, dtype)
+        assert status == 0 and torch.equal(y, y32.to(dtype))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,n", [(40, 1), (400, 1), (2000, 1), (1500, 16), (700, 64)])
+def test_largest_sums_on_the_tensor_cores(rows, n):
+    """Sums far past 2^24, with the bound of test_largest_sums; N such that dot products do not
+    take it."""
+    K, N = 4096, max(160, 400000000 // (4096 * rows) + 1)
+    qx = torch.full((rows, K), 127, dtype=torch.int8)
+    qw = torch.full((n, N, K), 127, dtype=torch.int8)
+    qw[:, 1::2] = -128
+    off = [i * rows // n for i in range(n + 1)]
+    y, _ = product(qx, torch.ones(rows), qw, torch.ones(n, N), off if n > 1 else None,
+                   torch.float32)
+    want = torch.full((rows, N), 127.0 * 127 * K, dtype=torch.float64)
+    want[:, 1::2] = -127.0 * 128 * K
+    assert ((y.double().cpu() - want).abs() <= (K / 16 * 2.0 ** -23 + 4 * U) * want.abs()).all()
+
+
+@pytest.mark.gpu
+def test_bad_offsets_and_scales_on_the_tensor_cores():
+    K, N, n, rows = 512, 520, 8, 1600
+    qx, qw = codes(rows, K, seed=1), codes(n, N, K, seed=2)
+    sx, sw = torch.ones(rows), torch.ones(n, N)
+    sx[7] = float("nan")
+    off = [0, 200, 400, 600, 800, 1000, 1200, 1400, 1600]
+    y, status = product(qx, sx, qw, sw, off, torch.float32)
+    assert status == 0 and torch.isnan(y[7]).all() and torch.isfinite(y[:7]).all()
+    assert torch.isfinite(y[8:]).all()
+    for bad in (off[:3] + [300] + off[4:], off[:8] + [5000], [-5] + off[1:]):
+        y, status = product(qx, torch.ones(rows), qw, sw, bad, torch.float32)
+        assert status & M.DEVFAULT_BAD_TILE
+        want = product64(qx[400:600], torch.ones(200), qw[2:3], sw[2:3], [0, 200])
+        if bad[2:4] == [400, 600]:
+            assert (y[400:600].double().cpu() == want).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("counts", [[5, 0, 130, 1, 64], [0, 0, 3], [1, 1, 1, 1, 1, 1, 1, 1],
                                     [300, 2], [0], [16, 17, 15, 33, 128, 127, 129]])
 @pytest.mark.parametrize("K,N", [(96, 130), (1024, 256), (400, 64)])
@@ -294,7 +359,8 @@ def check(y, want):
     (1, 64, 4, 2, 64, 0, 0), (1, 256, 8, 2, 192, 1, 0), (3, 128, 1, 1, 128, 2, 0),
     (7, 192, 16, 4, 320, 1, 0), (16, 512, 8, 8, 256, 0, 0), (64, 256, 32, 2, 128, 1, 2),
     (130, 448, 5, 3, 384, 1, 60), (300, 256, 4, 2, 256, 0, 0), (520, 128, 2, 1, 576, 4, 200),
-    (1000, 320, 7, 2, 192, 2, 0)])
+    (1000, 320, 7, 2, 192, 2, 0), (40, 448, 32, 2, 640, 2, 0), (90, 704, 16, 4, 448, 1, 30),
+    (200, 320, 24, 4, 576, 0, 0), (13, 1088, 8, 8, 832, 0, 0)])
 def test_experts(T, d, E, k, f, S, cap):
     cfg, st = layer(T, d, E, k, f, S, cap, seed=T + d)
     y = torch.full(((k + S) * T, d), float("nan"), dtype=torch.float16, device="cuda")
