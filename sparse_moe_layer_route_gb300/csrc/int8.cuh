@@ -71,6 +71,9 @@ cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
 // matrix pass of this shape; and that product: partial sums to `part` (int8_splits() * rows * N floats),
 // then their sums, scaled, to g.out.
 int int8_splits(long long rows, int K, int N, int n_mat);
+// Rows per segment (an even spread's) up to which a product runs on single CTAs, and up to which CTA
+// pairs take tiles of 128 rows, not 192.
+constexpr int kInt8MeanSingle = 16, kInt8Mean128 = 104;
 cudaError_t launch_int8_split(const Int8Gemm& g, float* part, cudaStream_t st);
 cudaError_t launch_quantize_rows(int T, int d, int dtype, const void* x, long long ld, int8_t* q,
                                  float* scale, cudaStream_t st);

@@ -434,7 +434,7 @@ template <typename YT>
 __global__ void __launch_bounds__(256) join_splits_kernel(const float* __restrict__ part,
                                                           const Int8Gemm g) {
   griddep_wait();
-  const int row = blockIdx.y;
+  const int row = blockIdx.x;
   int seg = 0;
   if (g.offsets != nullptr) {
     // the last segment that begins at or before the row and reaches it (bad offsets were reported by
@@ -451,12 +451,19 @@ __global__ void __launch_bounds__(256) join_splits_kernel(const float* __restric
     const int r0 = g.offsets[seg], r1 = g.offsets[seg + 1];
     if (r0 < 0 || r1 > g.rows || row < r0 || row >= r1) return;
   }
-  const int n = blockIdx.x * 256 + threadIdx.x;
+  const int n = blockIdx.y * 256 + threadIdx.x;
   if (n >= g.N) return;
   const long long at = (long long)row * g.N + n, plane = (long long)g.rows * g.N;
+  const float scale = g.sx[row] * g.sw[(long long)seg * g.N + n];
   float sum = 0.0f;
-  for (int i = 0; i < g.splits; ++i) sum += part[i * plane + at];
-  sum *= g.sx[row] * g.sw[(long long)seg * g.N + n];
+  for (int i = 0; i < g.splits; i += 8) {  // eight loads in flight, added in the pieces' order
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j < g.splits ? part[(i + j) * plane + at] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += v[j];
+  }
+  sum *= scale;
   if constexpr (sizeof(YT) == 4)
     static_cast<float*>(g.out)[at] = sum;
   else if constexpr (std::is_same<YT, __nv_bfloat16>::value)
@@ -468,24 +475,26 @@ __global__ void __launch_bounds__(256) join_splits_kernel(const float* __restric
 }  // namespace
 
 int int8_splits(long long rows, int K, int N, int n_mat) {
-  constexpr int kSms = 152;
-  const long long mean = rows / n_mat, per = mean <= 32 ? 32 : 96;
-  const long long units = (mean + per - 1) / per * n_mat * ((N + 255) / 256);
-  if (units == 0 || units * 2 > kSms || rows > 65535) return 1;
-  // at least four 128-k stages a piece: shorter ones spend their time on filling the pipeline
-  return (int)std::max(1ll, std::min(kSms / units, (long long)(K / kInt8StageK / 4)));
+  const long long mean = rows / n_mat;
+  const bool pair = mean > kInt8MeanSingle;
+  const long long at_once = pair ? 76 : 152;  // units that run at the same time
+  const long long tile = !pair ? 32 : mean <= kInt8Mean128 ? 128 : 192;
+  const long long units = std::max(1ll, (mean + tile - 1) / tile) * n_mat * ((N + 255) / 256);
+  if (units * 2 > at_once || N > 65535 * 256) return 1;
+  // at least four 128-k steps a piece: shorter ones spend their time on filling the pipeline
+  return (int)std::max(1ll, std::min(at_once / units, (long long)(K / kInt8StageK / 4)));
 }
 
 cudaError_t launch_int8_split(const Int8Gemm& g, float* part, cudaStream_t st) {
   Int8Gemm p = g;
   p.splits = int8_splits(g.rows, g.K, g.N, g.n_mat);
   p.out = part;
-  cudaError_t e = g.rows / g.n_mat <= 32
-                      ? launch_one<kInt8Partial, MOE_DTYPE_F32, 32, 2, 6>(p, st)
-                      : launch_one<kInt8Partial, MOE_DTYPE_F32, 96, 2, 2>(p, st);
+  cudaError_t e = g.rows / g.n_mat > kInt8MeanSingle
+                      ? launch_int8_gemm_pair(kInt8Partial, p, st)
+                      : launch_one<kInt8Partial, MOE_DTYPE_F32, 32, 2, 6>(p, st);
   if (e != cudaSuccess) return e;
   p.out = g.out;
-  const dim3 grid((g.N + 255) / 256, g.rows), block(256);
+  const dim3 grid(g.rows, (g.N + 255) / 256), block(256);
   switch (g.out_dtype) {
     case MOE_DTYPE_F32: return launch_k(join_splits_kernel<float>, grid, block, 0, st, part, p);
     case MOE_DTYPE_BF16:
@@ -499,7 +508,7 @@ cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st) 
   // single CTAs of 32-row tiles stream better (decode experts, 1 row a segment, 330 against 358 us for
   // gate and up); from 16 rows on the pairs' cheaper tiles win (64 segments of [2048 x 2048], 24 rows
   // each: 59 against 63 us)
-  if (g.rows / g.n_mat > 16) return launch_int8_gemm_pair(pass, g, st);
+  if (g.rows / g.n_mat > kInt8MeanSingle) return launch_int8_gemm_pair(pass, g, st);
   switch (pass) {
     case kInt8SwiGLU: return launch_one<kInt8SwiGLU, MOE_DTYPE_F32, 32, 2, 6>(g, st);
     case kInt8Slot: return launch_one<kInt8Slot, MOE_DTYPE_F16, 32, 2, 6>(g, st);

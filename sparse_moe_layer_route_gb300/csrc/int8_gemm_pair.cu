@@ -117,7 +117,18 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   const int n_ct = (g.N + UCH - 1) / UCH;
   const int n_sub = (g.K + 63) / 64;
   const int n_step = (n_sub + 1) / 2;
-  const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct;
+  // partial pass: a unit is done in pieces, each some of its steps
+  const int splits = PASS == kInt8Partial ? g.splits : 1;
+  const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct * splits;
+  auto unit_of = [&](long long w) {
+    return find_unit<GLU>(segs, g, n_ct, kNT, PASS == kInt8Partial ? w / splits : w);
+  };
+  auto first_step = [&](long long w) {
+    return PASS == kInt8Partial ? (int)(w % splits) * n_step / splits : 0;
+  };
+  auto end_step = [&](long long w) {
+    return PASS == kInt8Partial ? ((int)(w % splits) + 1) * n_step / splits : n_step;
+  };
   const long long pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   auto mma_rows = [](const Unit& u) { return (u.rows + 31) & ~31; };
 
@@ -128,14 +139,15 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       uint32_t phase = 0, issued = 0, last_parity = 0;  // per stage: ever issued, its parity
       bool ok = true;
       for (long long w = pair; w < total && ok; w += n_pairs) {
-        const Unit u = find_unit<GLU>(segs, g, n_ct, kNT, w);
+        const Unit u = unit_of(w);
         const bool sh = u.seg >= g.n_mat;
         const int ex = sh ? u.seg - g.n_mat : u.seg;
         const CUtensorMap* a0 = sh ? &tmShA : &tmA;
         const CUtensorMap* a1 = GLU ? (sh ? &tmShA2 : &tmA2) : a0;
         const int ch0 = u.ct * UCH + (int)rank * (UCH / 2), ch1 = GLU ? ch0 : ch0 + 64;
         const int brow = u.brow0 + (int)rank * (mma_rows(u) / 2);
-        for (int i = 0; i < n_step; ++i) {
+        const int i1 = end_step(w);
+        for (int i = first_step(w); i < i1; ++i) {
           if (!ptx::mbar_wait_bounded(done_bar(stage), phase ^ 1u, abort_flag, g.status,
                                       MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
@@ -178,14 +190,15 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (long long w = pair; w < total && ok; w += n_pairs) {
-        const Unit u = find_unit<GLU>(segs, g, n_ct, kNT, w);
+        const Unit u = unit_of(w);
         const uint32_t idesc = ptx::idesc_f16kind_f32(256, (uint32_t)mma_rows(u), 0, 0, 0u);
         if (!ptx::mbar_wait_bounded(dempty_bar(acc), acc_phase ^ 1u, abort_flag, g.status,
                                     MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs))
           break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc * kNT);
-        for (int i = 0; i < n_step; ++i) {
+        const int i0 = first_step(w), i1 = end_step(w);
+        for (int i = i0; i < i1; ++i) {
           if (!ptx::mbar_wait_bounded(ready_bar(stage), phase, abort_flag, g.status,
                                       MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
             ok = false;
@@ -199,7 +212,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             ptx::umma_f16_ta_cg2(d, a + kk * 8, bd + (uint64_t)(kk * 2), idesc,
-                                 (i | kk) != 0 ? 1u : 0u);
+                                 ((i - i0) | kk) != 0 ? 1u : 0u);
           if (2 * i + 1 < n_sub) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -235,7 +248,8 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     uint32_t phase = 0, dphase = 0, step = 0;
     bool ok = true;
     for (long long w = pair; w < total && ok; w += n_pairs) {
-      for (int i = 0; i < n_step; ++i, ++step) {
+      const int i1 = end_step(w);
+      for (int i = first_step(w); i < i1; ++i, ++step) {
         if (!ptx::mbar_wait_bounded_warp(codes_bar(stage), phase, abort_flag, g.status,
                                          MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
           ok = false;
@@ -298,13 +312,19 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     int acc = 0, ub = 0, sb = 0;  // accumulator; buffers of the unit's rows and of the step
     uint32_t acc_phase = 0, clamp = 0u;
     for (long long w = pair; w < total; w += n_pairs) {
-      const Unit u = find_unit<GLU>(segs, g, n_ct, kNT, w);
+      const Unit u = unit_of(w);
       const bool sh = u.seg >= g.n_mat;
       const long long ex = sh ? u.seg - g.n_mat : u.seg;
       const int ch0 = u.ct * UCH + (int)rank * (UCH / 2);
       const bool in = ch0 + chl < g.N;
-      const float* sw = (up ? (sh ? g.sh_sw2 : g.sw2) : (sh ? g.sh_sw : g.sw)) + ex * g.N;
-      const float wc = in ? sw[ch0 + chl] : 0.0f;
+      float wc = 1.0f;
+      if (PASS != kInt8Partial) {
+        const float* sw = (up ? (sh ? g.sh_sw2 : g.sw2) : (sh ? g.sh_sw : g.sw)) + ex * g.N;
+        wc = in ? sw[ch0 + chl] : 0.0f;
+      }
+      // partial pass: this piece's plane of the output
+      uint8_t* out = static_cast<uint8_t*>(g.out);
+      if (PASS == kInt8Partial) out += (w % splits) * 4ll * g.rows * g.N;
       float* usx = unit_sx[ub];
       int* orow = unit_orow[ub];
       ub ^= 1;
@@ -348,7 +368,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
             P::put(buf, col, chl, swiglu(gv, uv));
           }
           epilogue_barrier();
-          P::flush(static_cast<uint8_t*>(g.out), g.N, buf, orow + c * 32, ch0, t);
+          P::flush(out, g.N, buf, orow + c * 32, ch0, t);
           sb ^= 1;
         } else {
 #pragma unroll
@@ -362,7 +382,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
                 clamp = max(clamp, mag_bits(y));
             }
             epilogue_barrier();
-            P::flush(static_cast<uint8_t*>(g.out), g.N, buf, orow + c * 32 + j0, ch0, t);
+            P::flush(out, g.N, buf, orow + c * 32 + j0, ch0, t);
             sb ^= 1;
           }
         }
@@ -430,7 +450,7 @@ cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
   // by the rows per segment of an even spread: a tile costs about the same whatever its rows, so the
   // narrower one, with more slots and stages, is for segments that it holds (64 segments of
   // [2048 x 2048], 96 rows each: 69 against 72 us; 128 rows each, half of them longer: 93 against 77)
-  if (g.rows / g.n_mat <= 104) return launch_one<PASS, OUT, Cfg<128, 2, 4, 6>>(g, st);
+  if (g.rows / g.n_mat <= kInt8Mean128) return launch_one<PASS, OUT, Cfg<128, 2, 4, 6>>(g, st);
   return launch_one<PASS, OUT, Cfg<192, 2, 2, 5>>(g, st);
 }
 
@@ -438,6 +458,7 @@ cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
 
 cudaError_t launch_int8_gemm_pair(Int8Pass pass, const Int8Gemm& g, cudaStream_t st) {
   switch (pass) {
+    case kInt8Partial: return launch_pass<kInt8Partial, MOE_DTYPE_F32>(g, st);
     case kInt8SwiGLU: return launch_pass<kInt8SwiGLU, MOE_DTYPE_F32>(g, st);
     case kInt8Slot: return launch_pass<kInt8Slot, MOE_DTYPE_F16>(g, st);
     default: break;
