@@ -17,8 +17,8 @@ constexpr size_t kHead = 512;  // status word and counter block, as in every wor
 //   experts: decode shape, 6 tokens 94 against 144 us, 12 tokens 166 against 204, 24 tokens 289 against
 //   281; 64 + 2 experts of [2048 x 1408], 6 a token, 12 tokens 94 against 95, 16 tokens 108 against 96; of
 //   small layers, 32 tokens, 60 M multiply-adds, 17 against 20, and 64 tokens, 240 M, 38 against 27.
-bool few_rows(long long rows, int K, int N) { return rows <= 8 || rows * K * N <= 400000000ll; }
-bool few_tokens(const Shape& s) { return s.T <= 12 || 3ll * s.rows * s.d * s.f <= 100000000ll; }
+bool few_rows(int rows, int K, int N) { return rows <= 8 || (double)rows * K * N <= 4e8; }
+bool few_tokens(const Shape& s) { return s.T <= 12 || 3.0 * s.rows * s.d * s.f <= 1e8; }
 
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 int dtype_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }

@@ -11,6 +11,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include "int8.cuh"
@@ -115,14 +116,15 @@ __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int 
 
 template <int PASS, int OUT, int R>
 __global__ void __launch_bounds__(kThreads, R == 8 ? 4 : kCtasPerSm)
-    int8_gemv_kernel(const Int8Gemm g) {
+    int8_gemv_kernel(const Int8Gemm g, int ctas_per_tile) {
   constexpr bool GLU = PASS == kInt8SwiGLU;
   constexpr int CH = GLU ? kStreams / 2 : kStreams;  // channels per warp
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Unit u = find_tile<R>(g, GLU, blockIdx.y, lane);  // every warp: no barrier
+  const int tile = blockIdx.x / ctas_per_tile, cta = blockIdx.x - tile * ctas_per_tile;
+  const Unit u = find_tile<R>(g, GLU, tile, lane);  // every warp: no barrier
   if (u.seg < 0) return;
-  const int ch0 = (blockIdx.x * (kThreads / 32) + warp) * CH;
+  const int ch0 = (cta * (kThreads / 32) + warp) * CH;
   if (ch0 >= g.N) return;
   const bool sh = u.seg >= g.n_mat;
   const long long ex = sh ? u.seg - g.n_mat : u.seg;
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? 4 : kCtasPerSm)
       if (k + lane * 16 < g.K) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const int4 a = __ldg(reinterpret_cast<const int4*>(x[r] + k));
+          const int4 a = *reinterpret_cast<const int4*>(x[r] + k);
 #pragma unroll
           for (int c = 0; c < kStreams; ++c) {
             acc[c][r] = __dp4a(v[i][c].x, a.x, acc[c][r]);
@@ -204,14 +206,14 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? 4 : kCtasPerSm)
 template <int PASS, int OUT>
 cudaError_t launch_out(const Int8Gemm& g, int most_rows, cudaStream_t st) {
   constexpr int kCta = kThreads / 32 * (PASS == kInt8SwiGLU ? kStreams / 2 : kStreams);
-  const unsigned gx = (unsigned)((g.N + kCta - 1) / kCta);
+  const int gx = (g.N + kCta - 1) / kCta;
   auto go = [&](auto kern, int R) {
     // an upper bound of the row tiles: a segment's rows over R and one ragged tile each, and no more
     // than one tile per row
     const long long tiles =
         min((long long)g.rows, (long long)g.rows / R + g.n_mat) + (long long)g.S * ((g.T + R - 1) / R);
-    if (tiles > 65535) return cudaErrorInvalidValue;
-    return launch_k(kern, dim3(gx, (unsigned)tiles), dim3(kThreads), 0, st, g);
+    if (tiles * gx > INT_MAX) return cudaErrorInvalidValue;
+    return launch_k(kern, dim3((unsigned)(tiles * gx)), dim3(kThreads), 0, st, g, gx);
   };
   // rows per tile: no more than any segment has, and no more than twice an even spread's (the rows that
   // a tile does not have are computed all the same)

@@ -131,7 +131,8 @@ def product(qx, sx, qw, sw, offsets, dtype):
 @pytest.mark.parametrize("rows,K,N", [(1, 16, 1), (1, 4096, 130), (2, 48, 64), (3, 128, 257),
                                       (8, 1024, 512), (9, 1008, 128), (16, 512, 384),
                                       (17, 64, 100), (40, 768, 1000), (64, 1024, 256),
-                                      (129, 272, 300), (260, 1024, 520), (700, 144, 136)])
+                                      (129, 272, 300), (260, 1024, 520), (700, 144, 136),
+                                      (530000, 16, 3), (2, 16, 70000)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 def test_one_matrix(rows, K, N, dtype):
     qx, qw = codes(rows, K, seed=1, full=True), codes(1, N, K, seed=2, full=True)
