@@ -7,8 +7,11 @@
 // 256 sigmoids alone are about 110 warp instructions. So the choice looks at few experts one by one: the
 // k-th largest of the lanes' maxima is a bound that at least k experts reach and few others do (about
 // 10 of 256 for k = 8); those, one per lane, are ranked against each other.
-// Backward: one warp per token, or per four tokens where only the chosen experts have a gradient: their
-// values are put into zeroed rows in shared memory, which are written in 16-byte pieces. Bound by HBM.
+// 65536 rows of 256 (sigmoid, bias, 8 groups, top-8) 55 us, 763 warp instructions a token and three
+// quarters of the issue slots; with k rounds of a warp maximum over all experts 80.
+// Backward: one warp per token, or per four tokens where only the chosen experts have a gradient: zeroed
+// rows in 16-byte pieces, then the chosen experts' values. Writes of HBM and, for the few chosen logits, a
+// chain of dependent loads: 65536 rows of 256 with eight chosen 18.7 us, 3.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
