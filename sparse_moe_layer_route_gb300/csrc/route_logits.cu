@@ -27,15 +27,28 @@ constexpr int kWarps = 8;      // tokens at a time per CTA
 constexpr int kCtasPerSm = 4;  // resident CTAs of the forward kernel (its registers)
 constexpr unsigned kFull = 0xffffffffu;
 
-// Order-preserving key of a rank: larger float, larger key. 0 is below every key (an expert that
-// cannot be chosen), kMaskedKey is the key of -infinity (a switched-off expert).
-constexpr uint32_t kMaskedKey = 0x007fffffu;
-__device__ __forceinline__ uint32_t rank_key(float r) {
-  const uint32_t u = __float_as_uint(r + 0.0f);  // -0 becomes +0: the two compare equal
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+// The smallest (largest) of the values, NaN if one is NaN, three at a time.
+template <int N>
+__device__ __forceinline__ float least_or_nan(const float (&v)[N]) {
+  float m = v[0];
+  if (N == 2) asm("min.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(v[N - 1]));
+#pragma unroll
+  for (int i = 1; i < N - 1; i += 2)
+    asm("min.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[i]), "f"(v[i + 1]));
+  if (N > 2 && N % 2 == 0) asm("min.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(v[N - 1]));
+  return m;
 }
-__device__ __forceinline__ float key_rank(uint32_t key) {
-  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+template <int N>
+__device__ __forceinline__ float most_or_nan(const float (&v)[N]) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(v[i]));
+  return m;
+}
+__device__ __forceinline__ float warp_reduce_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
@@ -167,57 +180,59 @@ __device__ __forceinline__ void load_run(const __nv_bfloat16* p, float (&v)[NV])
     }
   }
 }
-// This lane's logits of a row; -infinity past E.
+// This lane's logits of a row; `fill` past E.
 template <int NV, typename LT>
-__device__ __forceinline__ void load_row(const LT* row, int e0, int E, bool vec, float (&l)[NV]) {
+__device__ __forceinline__ void load_row(const LT* row, int e0, int E, bool vec, float fill,
+                                         float (&l)[NV]) {
   if (vec && e0 + NV <= E) {
     load_run<NV>(row + e0, l);
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = e0 + i < E ? load_logit(row + e0 + i) : -INFINITY;
+    for (int i = 0; i < NV; ++i) l[i] = e0 + i < E ? load_logit(row + e0 + i) : fill;
   }
 }
 
-// This lane's keys to its place in the warp's row.
+// This lane's ranks to its place in the warp's row.
 template <int NV>
-__device__ __forceinline__ void store_keys(uint32_t* row, int lane, const uint32_t (&key)[NV]) {
+__device__ __forceinline__ void store_ranks(float* row, int lane, const float (&r)[NV]) {
   if constexpr (NV >= 4) {
 #pragma unroll
     for (int i = 0; i < NV; i += 4)
-      *reinterpret_cast<uint4*>(row + lane * NV + i) =
-          make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
+      *reinterpret_cast<float4*>(row + lane * NV + i) =
+          make_float4(r[i], r[i + 1], r[i + 2], r[i + 3]);
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) row[lane * NV + i] = key[i];
+    for (int i = 0; i < NV; ++i) row[lane * NV + i] = r[i];
   }
 }
 
-// Groups of any size: lane g ranks groups g and g + 32 from the warp's row of keys. Sets the bits of
+// Groups of any size: lane g ranks groups g and g + 32 from the warp's row of ranks. Sets the bits of
 // `gone` whose experts' groups are not kept.
 template <int NV>
-__device__ __forceinline__ void drop_groups(const GateArgs& a, const uint32_t* mine, int e0,
-                                            int lane, uint32_t& gone) {
+__device__ __forceinline__ void drop_groups(const GateArgs& a, const float* mine, int e0, int lane,
+                                            uint32_t& gone) {
   const int size = a.E / a.G;
-  uint32_t gk[2];
+  float best[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int g = lane + 32 * h;
-    gk[h] = 0u;
+    best[h] = -INFINITY;
     if (g < a.G) {
-      uint32_t b1 = 0u, b2 = 0u;
+      float b1 = -INFINITY, b2 = -INFINITY;
       for (int i = 0; i < size; ++i) {
-        const uint32_t v = mine[g * size + i];
-        b2 = max(b2, min(b1, v));
-        b1 = max(b1, v);
+        const float v = mine[g * size + i];
+        b2 = fmaxf(b2, fminf(b1, v));
+        b1 = fmaxf(b1, v);
       }
-      gk[h] = a.top2 && b2 > kMaskedKey ? rank_key(key_rank(b1) + key_rank(b2)) : b1;
+      best[h] = a.top2 && b2 > -INFINITY ? b1 + b2 : b1;
     }
   }
   int before[2] = {0, 0};
   for (int g = 0; g < a.G; ++g) {
-    const uint32_t v = __shfl_sync(kFull, g < 32 ? gk[0] : gk[1], g & 31);
+    const float v = __shfl_sync(kFull, g < 32 ? best[0] : best[1], g & 31);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) before[h] += v > gk[h] || (v == gk[h] && g < lane + 32 * h);
+    for (int h = 0; h < 2; ++h)
+      before[h] += v > best[h] || (v == best[h] && g < lane + 32 * h);
   }
   const unsigned keep0 = __ballot_sync(kFull, lane < a.G && before[0] < a.Gk);
   const unsigned keep1 = __ballot_sync(kFull, lane + 32 < a.G && before[1] < a.Gk);
@@ -230,8 +245,10 @@ __device__ __forceinline__ void drop_groups(const GateArgs& a, const uint32_t* m
 
 template <int NV, typename LT, bool SIGMOID>
 __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const GateArgs a) {
-  __shared__ __align__(16) uint32_t keys[kWarps][32 * NV];  // a row's keys
-  __shared__ int picked[kWarps][32];                        // its candidates
+  __shared__ __align__(16) float ranks[kWarps][32 * NV];   // a row's ranks
+  __shared__ __align__(16) float picked_rank[kWarps][32];  // its candidates' ranks
+  __shared__ int picked[kWarps][32];                       // and experts
+  __shared__ int chosen[kWarps][32];                       // the experts of four rows, eight each
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned below = (1u << lane) - 1u;  // lanes before this one
@@ -239,39 +256,83 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
   const int group = a.lanes > 0 ? lane / a.lanes : 0;
   const LT* logits = static_cast<const LT*>(a.logits);
   const long long step = (long long)gridDim.x * kWarps;
+  // sigmoids of -infinity take a detour: past E a 0 stands, whose rank is taken back
+  constexpr float kFill = SIGMOID ? 0.0f : -INFINITY;
   float bias[NV];
+  uint32_t past = 0u;  // slots past E
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
     bias[i] = a.bias != nullptr && e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
+    past |= e0 + i >= a.E ? 1u << i : 0u;
+  }
   const bool need_scores = SIGMOID || a.bias != nullptr || a.scores != nullptr;
+
+  // Weights of up to four rows at once, eight lanes each: the chosen experts' scores once more from
+  // their logits. q < rows: row t0 + q step, the q-th bit of bad: it holds a NaN (softmax: or +infinity).
+  auto weigh = [&](long long t0, int rows, unsigned bad, float top, float total) {
+    const int q = lane >> 3, j = lane & 7;
+    const long long t = t0 + q * step;
+    const bool on = q < rows && j < a.k;
+    __syncwarp();
+    const int e = on ? chosen[warp][lane] : 0;
+    const float sel = on ? load_logit(logits + t * a.ld + e) : -INFINITY;
+    float w;
+    if (SIGMOID) {
+      w = on ? sigmoid(sel) : 0.0f;
+    } else if (a.renorm) {  // softmax over the chosen logits: the same quotient without underflow
+      float m = sel;
+#pragma unroll
+      for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      w = on ? expf(sel - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+    } else {
+      w = expf(sel - top) / total;
+    }
+    if (a.renorm) {
+      float sum = w;
+#pragma unroll
+      for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      w = sum == 0.0f ? 0.0f : w / sum;
+    }
+    if (on) {
+      a.idx[t * a.k + j] = e;
+      a.w[t * a.k + j] = (bad >> q) & 1u ? NAN : a.scale * w;
+    }
+    __syncwarp();
+  };
+
   long long t = (long long)blockIdx.x * kWarps + warp;
   float l[NV];
-  if (t < a.T) load_row<NV>(logits + t * a.ld, e0, a.E, a.vec, l);
+  if (t < a.T) load_row<NV>(logits + t * a.ld, e0, a.E, a.vec, kFill, l);
+  int held = 0;            // rows in `chosen`, and of each:
+  unsigned bad_rows = 0u;  // a NaN (softmax: or +infinity) in it
+  float held_top = 0.0f, held_total = 1.0f;
   for (; t < a.T; t += step) {
     float next[NV];
-    if (t + step < a.T) load_row<NV>(logits + (t + step) * a.ld, e0, a.E, a.vec, next);
-    const LT* row = logits + t * a.ld;
-    bool bad = false;  // a NaN (softmax: or +infinity) in the row
-#pragma unroll
-    for (int i = 0; i < NV; ++i) bad |= SIGMOID ? l[i] != l[i] : !(l[i] < INFINITY);
-    bad = __any_sync(kFull, bad);
+    if (t + step < a.T) load_row<NV>(logits + (t + step) * a.ld, e0, a.E, a.vec, kFill, next);
+    const float edge = SIGMOID ? least_or_nan(l) : most_or_nan(l);
+    if (__any_sync(kFull, SIGMOID ? edge != edge : !(edge < INFINITY))) bad_rows |= 1u << held;
     float s[NV], top = 0.0f, total = 1.0f;
     if (need_scores || (!SIGMOID && !a.renorm)) {
       if (SIGMOID) {
         // a logit of -infinity gives NaN, which ranks as switched off; finite ones that low take the
         // division
-        bool low = false;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          s[i] = sigmoid_fast(l[i]);
-          low |= l[i] < -80.0f && l[i] > -INFINITY;
-        }
-        if (low) {
+        for (int i = 0; i < NV; ++i) s[i] = sigmoid_fast(l[i]);
+        if (!(edge >= -80.0f)) {
+          bool low = false;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) s[i] = l[i] == -INFINITY ? NAN : sigmoid(l[i]);
+          for (int i = 0; i < NV; ++i) low |= l[i] < -80.0f && l[i] > -INFINITY;
+          if (low) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) s[i] = l[i] == -INFINITY ? NAN : sigmoid(l[i]);
+          }
         }
       } else {
         softmax_scores<NV>(l, s, top, total);
+        if (lane >> 3 == held) {
+          held_top = top;
+          held_total = total;
+        }
       }
       if (a.scores != nullptr) {
         float* to = a.scores + t * a.E + e0;
@@ -294,139 +355,143 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
         }
       }
     }
-    uint32_t key[NV];
+    // The ranks: -infinity for a switched-off expert and where the logit, the score or the bias is NaN
+    // (the larger of NaN and -infinity is -infinity). Without a bias its registers are 0, which leaves a
+    // sigmoid as it is; a softmax without one is ranked by its logits.
+    float r[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      // without a bias its registers are 0, which leaves a sigmoid as it is; a softmax without one is
-      // ranked by its logits. r is NaN where the logit, the score or the bias is
-      const float r = SIGMOID || a.bias != nullptr ? s[i] + bias[i] : l[i];
-      key[i] = (SIGMOID || l[i] > -INFINITY) && r == r ? rank_key(r) : kMaskedKey;
+      if (SIGMOID)
+        r[i] = fmaxf(s[i] + bias[i], -INFINITY);
+      else if (a.bias != nullptr)
+        r[i] = l[i] > -INFINITY ? fmaxf(s[i] + bias[i], -INFINITY) : -INFINITY;
+      else
+        r[i] = fmaxf(l[i], -INFINITY);
     }
-    if (e0 + NV > a.E) {
+    if (past != 0u) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (e0 + i >= a.E) key[i] = 0u;
+        if ((past >> i) & 1u) r[i] = -INFINITY;
     }
-    uint32_t* mine = keys[warp];
-    store_keys<NV>(mine, lane, key);
-    uint32_t b1 = 0u, b2 = 0u;  // this lane's two largest keys
+    float* const mine = ranks[warp];
+    store_ranks<NV>(mine, lane, r);
+    float b1 = r[0];  // this lane's largest rank
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      b2 = max(b2, min(b1, key[i]));
-      b1 = max(b1, key[i]);
-    }
-    uint32_t gone = 0u;  // slots whose experts cannot be chosen
+    for (int i = 1; i < NV; ++i) b1 = fmaxf(b1, r[i]);
+    uint32_t gone = past;  // slots whose experts cannot be chosen
     __syncwarp();
     if (a.G > 0) {
       if (a.lanes > 0) {  // a group is `lanes` whole lanes, a power of two
-        uint32_t g1 = b1, g2 = b2;
-        for (int o = 1; o < a.lanes; o <<= 1) {
-          const uint32_t p1 = __shfl_xor_sync(kFull, g1, o), p2 = __shfl_xor_sync(kFull, g2, o);
-          g2 = max(min(g1, p1), max(g2, p2));
-          g1 = max(g1, p1);
+        float g1 = r[0], g2 = -INFINITY;
+        if (a.top2) {
+#pragma unroll
+          for (int i = 1; i < NV; ++i) {
+            g2 = fmaxf(g2, fminf(g1, r[i]));
+            g1 = fmaxf(g1, r[i]);
+          }
+          for (int o = 1; o < a.lanes; o <<= 1) {
+            const float p1 = __shfl_xor_sync(kFull, g1, o), p2 = __shfl_xor_sync(kFull, g2, o);
+            g2 = fmaxf(fminf(g1, p1), fmaxf(g2, p2));
+            g1 = fmaxf(g1, p1);
+          }
+          if (g2 > -INFINITY) g1 += g2;
+        } else {
+          g1 = b1;
+          for (int o = 1; o < a.lanes; o <<= 1) g1 = fmaxf(g1, __shfl_xor_sync(kFull, g1, o));
         }
-        if (a.top2 && g2 > kMaskedKey) g1 = rank_key(key_rank(g1) + key_rank(g2));
-        // kept when fewer than Gk groups precede it
+        // kept when fewer than Gk groups precede it; each of a group's lanes counts some
         int before = 0;
-#pragma unroll 8
-        for (int g = 0; g < a.G; ++g) {
-          const uint32_t v = __shfl_sync(kFull, g1, g * a.lanes);
-          before += v > g1 || (v == g1 && g < group);
+        for (int g0 = 0; g0 < a.G; g0 += a.lanes) {
+          const int g = g0 + (lane & (a.lanes - 1));
+          const float v = __shfl_sync(kFull, g1, g * a.lanes);
+          before += g < a.G && (v > g1 || (v == g1 && g < group));
         }
+        for (int o = 1; o < a.lanes; o <<= 1) before += __shfl_xor_sync(kFull, before, o);
         if (before >= a.Gk) {
-          b1 = 0u;
+          b1 = -INFINITY;
           gone = 0xffffffffu;
         }
       } else {
         drop_groups<NV>(a, mine, e0, lane, gone);
-        b1 = 0u;
+        b1 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) b1 = max(b1, (gone >> i) & 1u ? 0u : key[i]);
+        for (int i = 0; i < NV; ++i) b1 = fmaxf(b1, (gone >> i) & 1u ? -INFINITY : r[i]);
       }
     }
     // the k-th largest of the lanes' maxima (equal ones count once): at least k experts reach it, or it
-    // is 0
-    uint32_t bound = 0u;
+    // is -infinity, which all do
+    float bound = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (j == a.k) break;
-      bound = __reduce_max_sync(kFull, b1);
-      b1 = b1 == bound ? 0u : b1;
+      bound = warp_reduce_max(b1);
+      b1 = b1 == bound ? -INFINITY : b1;
     }
-    bound = max(bound, 1u);
     uint32_t cand = 0u;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) cand |= key[i] >= bound ? 1u << i : 0u;
+    for (int i = 0; i < NV; ++i) cand |= r[i] >= bound ? 1u << i : 0u;
     cand &= ~gone;
-    const int n = __reduce_add_sync(kFull, __popc(cand));
-    int my_idx = 0, place = 32;  // this lane's expert, and its place among the chosen
+    int n = 0;  // candidates, the first 32 of which go to `picked`
+    for (unsigned more = __ballot_sync(kFull, cand != 0u); more != 0u;
+         more = __ballot_sync(kFull, cand != 0u)) {
+      const int at = n + __popc(more & below);
+      if (cand != 0u && at < 32) picked[warp][at] = e0 + __ffs(cand) - 1;
+      cand &= cand - 1u;
+      n += __popc(more);
+    }
+    __syncwarp();
     if (n <= 32) {
-      // one candidate per lane
-      int m = 0;
-      for (unsigned more = __ballot_sync(kFull, cand != 0u); more != 0u;
-           more = __ballot_sync(kFull, cand != 0u)) {
-        if (cand != 0u) picked[warp][m + __popc(more & below)] = e0 + __ffs(cand) - 1;
-        cand &= cand - 1u;
-        m += __popc(more);
-      }
+      // one candidate per lane, ranked against each other
+      const int my_idx = lane < n ? picked[warp][lane] : 0;
+      const float my_rank = lane < n ? mine[my_idx] : -INFINITY;
+      picked_rank[warp][lane] = my_rank;
       __syncwarp();
-      uint32_t my_key = 0u;
-      if (lane < n) {
-        my_idx = picked[warp][lane];
-        my_key = mine[my_idx];
+      int place = 0;
+      for (int j = 0; j < n; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(&picked_rank[warp][j]);
+        place += (v.x > my_rank) + (v.y > my_rank) + (v.z > my_rank) + (v.w > my_rank);
+      }
+      // equal ranks share a place: then the lower expert goes first
+      if (__popc(__reduce_or_sync(kFull, lane < n ? 1u << place : 0u)) != n) {
         place = 0;
+        for (int j = 0; j < n; ++j) {
+          const float v = __shfl_sync(kFull, my_rank, j);
+          const int e = __shfl_sync(kFull, my_idx, j);
+          place += v > my_rank || (v == my_rank && e < my_idx);
+        }
       }
-      for (int j = 0; j < n; ++j) {
-        const uint32_t v = __shfl_sync(kFull, my_key, j);
-        const int e = __shfl_sync(kFull, my_idx, j);
-        place += v > my_key || (v == my_key && e < my_idx);
-      }
+      if (lane < n && place < a.k) chosen[warp][held * 8 + place] = my_idx;
     } else {
       // more than 32 share the bound (many equal logits): one warp-wide maximum per choice, lowest lane
       // and slot first
       for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0u;
-        int slot = 0;
+        float best = -INFINITY;
+        int slot = -1;
 #pragma unroll
         for (int i = NV - 1; i >= 0; --i) {
-          const uint32_t v = (gone >> i) & 1u ? 0u : key[i];
-          slot = v >= best ? i : slot;
-          best = max(best, v);
+          const bool better = !((gone >> i) & 1u) && r[i] >= best;
+          slot = better ? i : slot;
+          best = better ? r[i] : best;
         }
-        const uint32_t first = __reduce_max_sync(kFull, best);
-        const int owner = __ffs(__ballot_sync(kFull, best == first)) - 1;
-        const int e = __shfl_sync(kFull, e0 + slot, owner);
-        if (lane == owner) gone |= 1u << slot;
-        if (lane == j) {
-          my_idx = e;
-          place = j;
+        const float first = warp_reduce_max(best);
+        const int owner = __ffs(__ballot_sync(kFull, slot >= 0 && best == first)) - 1;
+        if (lane == owner) {
+          gone |= 1u << slot;
+          chosen[warp][held * 8 + j] = e0 + slot;
         }
       }
     }
-    __syncwarp();  // picked and keys are written again for the warp's next row
-    // weights: the lanes with a place below k recompute their choice's score from the logit
-    const bool on = place < a.k;
-    const float sel = on ? load_logit(row + my_idx) : -INFINITY;
-    float w;
-    if (SIGMOID) {
-      w = on ? sigmoid(sel) : 0.0f;
-    } else if (a.renorm) {  // softmax over the chosen logits: the same quotient without underflow
-      const float m = warp_max(sel);
-      w = on ? expf(sel - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+    if (++held == 4) {
+      weigh(t - 3 * step, 4, bad_rows, held_top, held_total);
+      held = 0;
+      bad_rows = 0u;
     } else {
-      w = expf(sel - top) / total;
-    }
-    if (a.renorm) {
-      const float sum = warp_sum(w);
-      w = sum == 0.0f ? 0.0f : w / sum;
-    }
-    if (on) {
-      a.idx[t * a.k + place] = my_idx;
-      a.w[t * a.k + place] = bad ? NAN : a.scale * w;
+      __syncwarp();  // picked and ranks are written again for the warp's next row
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) l[i] = next[i];
   }
+  if (held > 0) weigh(t - held * step, held, bad_rows, held_top, held_total);
 }
 
 struct GateGradArgs {
