@@ -192,6 +192,21 @@ __device__ __forceinline__ void load_row(const LT* row, int e0, int E, bool vec,
   }
 }
 
+// The two largest of r[FIRST ... FIRST + N), the second -infinity where there is one only.
+template <int FIRST, int N, int NV>
+__device__ __forceinline__ void two_largest(const float (&r)[NV], float& b1, float& b2) {
+  if constexpr (N == 1) {
+    b1 = r[FIRST];
+    b2 = -INFINITY;
+  } else {
+    float h1, h2, l1, l2;
+    two_largest<FIRST, N / 2>(r, h1, l1);
+    two_largest<FIRST + N / 2, N / 2>(r, h2, l2);
+    b1 = fmaxf(h1, h2);
+    b2 = N == 2 ? fminf(h1, h2) : fmaxf(fminf(h1, h2), fmaxf(l1, l2));
+  }
+}
+
 // This lane's ranks to its place in the warp's row.
 template <int NV>
 __device__ __forceinline__ void store_ranks(float* row, int lane, const float (&r)[NV]) {
@@ -375,20 +390,16 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
     }
     float* const mine = ranks[warp];
     store_ranks<NV>(mine, lane, r);
-    float b1 = r[0];  // this lane's largest rank
-#pragma unroll
-    for (int i = 1; i < NV; ++i) b1 = fmaxf(b1, r[i]);
+    float b1, b2;  // this lane's two largest ranks
+    two_largest<0, NV>(r, b1, b2);
     uint32_t gone = past;  // slots whose experts cannot be chosen
     __syncwarp();
     if (a.G > 0) {
       if (a.lanes > 0) {  // a group is `lanes` whole lanes, a power of two
-        float g1 = r[0], g2 = -INFINITY;
+        float g1 = b1;
         if (a.top2) {
-#pragma unroll
-          for (int i = 1; i < NV; ++i) {
-            g2 = fmaxf(g2, fminf(g1, r[i]));
-            g1 = fmaxf(g1, r[i]);
-          }
+          float g2 = b2;
+#pragma unroll 1
           for (int o = 1; o < a.lanes; o <<= 1) {
             const float p1 = __shfl_xor_sync(kFull, g1, o), p2 = __shfl_xor_sync(kFull, g2, o);
             g2 = fmaxf(fminf(g1, p1), fmaxf(g2, p2));
@@ -396,16 +407,17 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
           }
           if (g2 > -INFINITY) g1 += g2;
         } else {
-          g1 = b1;
+#pragma unroll 1
           for (int o = 1; o < a.lanes; o <<= 1) g1 = fmaxf(g1, __shfl_xor_sync(kFull, g1, o));
         }
         // kept when fewer than Gk groups precede it; each of a group's lanes counts some
-        int before = 0;
-        for (int g0 = 0; g0 < a.G; g0 += a.lanes) {
-          const int g = g0 + (lane & (a.lanes - 1));
+        int before = 0, g = lane & (a.lanes - 1);
+#pragma unroll 1
+        for (int g0 = 0; g0 < a.G; g0 += a.lanes, g += a.lanes) {
           const float v = __shfl_sync(kFull, g1, g * a.lanes);
           before += g < a.G && (v > g1 || (v == g1 && g < group));
         }
+#pragma unroll 1
         for (int o = 1; o < a.lanes; o <<= 1) before += __shfl_xor_sync(kFull, before, o);
         if (before >= a.Gk) {
           b1 = -INFINITY;
@@ -421,11 +433,19 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm) gate_kernel(const Gat
     // the k-th largest of the lanes' maxima (equal ones count once): at least k experts reach it, or it
     // is -infinity, which all do
     float bound = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j == a.k) break;
+    auto lower = [&] {
       bound = warp_reduce_max(b1);
       b1 = b1 == bound ? -INFINITY : b1;
+    };
+    switch (a.k) {  // one jump, not a test per step
+      default: lower();
+      case 7: lower();
+      case 6: lower();
+      case 5: lower();
+      case 4: lower();
+      case 3: lower();
+      case 2: lower();
+      case 1: lower();
     }
     uint32_t cand = 0u;
 #pragma unroll
