@@ -6,9 +6,11 @@
 // instructions, not bytes: a row of 256 fp32 logits is 1 KB, 0.15 us of one SM's share of HBM, and its
 // 256 sigmoids alone are about 110 warp instructions. So the choice looks at few experts one by one: the
 // k-th largest of the lanes' maxima is a bound that at least k experts reach and few others do (about
-// 10 of 256 for k = 8); those, one per lane, are ranked against each other.
-// 65536 rows of 256 (sigmoid, bias, 8 groups, top-8) 55 us, 763 warp instructions a token and three
-// quarters of the issue slots; with k rounds of a warp maximum over all experts 80.
+// 10 of 256 for k = 8); those, one per lane, are ranked against each other, four per shared load. Weights
+// are found for four tokens at once, eight lanes each.
+// 65536 rows of 256 (sigmoid, bias, 8 groups, top-8) 43 us, 590 warp instructions a token and three
+// quarters of the issue slots; with k rounds of a warp maximum over all experts, and one token's weights
+// at a time, 80.
 // Backward: one warp per token, or per four tokens where only the chosen experts have a gradient: zeroed
 // rows in 16-byte pieces, then the chosen experts' values. Bound by HBM, whose reads
 // come 64 bytes at a time: 65536 rows of 256 with eight chosen 17.4 us, 67 MB written and about 30 read.
