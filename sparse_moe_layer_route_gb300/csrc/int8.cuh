@@ -53,6 +53,7 @@ struct Int8Gemm {
   int rows, K, N, n_mat, S, T;
   int out_dtype;             // matrix pass
   int splits;                // partial pass: pieces of K
+  int tile_rows;             // CTA pairs: the tallest row tile
 };
 
 enum Int8Pass {
@@ -72,8 +73,25 @@ cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
 // then their sums, scaled, to g.out.
 int int8_splits(long long rows, int K, int N, int n_mat);
 // Rows per segment (an even spread's) up to which a product runs on single CTAs, and up to which CTA
-// pairs take tiles of 128 rows, not 192.
+// pairs take tiles of at most 128 rows, not 256.
 constexpr int kInt8MeanSingle = 16, kInt8Mean128 = 104;
+// Height of a segment's row tiles, a multiple of 32 up to NT: as few tiles as NT allows, of equal heights,
+// as a tile of up to 192 rows costs the widening of its weights (388 clk per 64 k) whatever it holds.
+// Past 192 it costs its MMAs, 2 clk a row, and some of the overlap with the next tile: taken where that is
+// less than one more tile (400 rows: two of 224 and 176, not three).
+__host__ __device__ inline int int8_tile_height(int rows, int NT) {
+  const int most = rows < 1 ? 1 : rows;
+  int n = (most + NT - 1) / NT;
+  int height = ((most + n - 1) / n + 31) / 32 * 32;
+  if (height > 192) {
+    const int m = (most + 191) / 192;
+    if (n * (2 * height + 40) >= m * 400) {
+      n = m;
+      height = ((most + n - 1) / n + 31) / 32 * 32;
+    }
+  }
+  return height;
+}
 cudaError_t launch_int8_split(const Int8Gemm& g, float* part, cudaStream_t st);
 cudaError_t launch_quantize_rows(int T, int d, int dtype, const void* x, long long ld, int8_t* q,
                                  float* scale, cudaStream_t st);

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   const int splits = PASS == kInt8Partial ? g.splits : 1;
   const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct * splits;
   auto unit_of = [&](long long w) {
-    return find_unit<PAIR>(segs, g, n_ct, NT, PASS == kInt8Partial ? w / splits : w);
+    return find_unit<PAIR>(segs, g, n_ct, PASS == kInt8Partial ? w / splits : w);
   };
   auto first_stage = [&](long long w) {
     return PASS == kInt8Partial ? (int)(w % splits) * n_stage / splits : 0;

@@ -41,18 +41,24 @@ namespace {
 
 constexpr int kABytes = kInt8Ch * kInt8StageK;  // 16 KB of codes
 
-template <int NT_, int NACC_, int NSLOT_, int STAGES_>
+constexpr int kBoxRows = 32;                    // rows of one copy
+
+// Tiles of up to NT rows; two accumulators in ACOLS TMEM columns, NSLOT slots of 64 for widened codes; SA
+// and SB stages of codes and of rows.
+template <int NT_, int ACOLS_, int NSLOT_, int SA_, int SB_>
 struct Cfg {
-  static constexpr int NT = NT_, NACC = NACC_, NSLOT = NSLOT_, STAGES = STAGES_;
+  static constexpr int NT = NT_, ACOLS = ACOLS_, NSLOT = NSLOT_, SA = SA_, SB = SB_;
   static constexpr int kBSub = NT / 2 * 128;  // one [NT / 2 rows x 64 k] fp16 tile
-  static constexpr int kStageBytes = kABytes + 2 * kBSub;
-  static constexpr int kSlotCol = NACC * NT;  // first TMEM column of the widened codes
-  static constexpr int kBars = 3 * STAGES + 2 * NACC + 1;
+  static constexpr int kRows = SA * kABytes;  // where the rows' stages begin
+  static constexpr int kPipeBytes = kRows + SB * 2 * kBSub;
+  static constexpr int kSlotCol = ACOLS;  // first TMEM column of the widened codes
+  static constexpr int kBars = 2 * SA + 2 * SB + 6;
   static constexpr int kSmemBytes =
-      STAGES * kStageBytes + 2 * kInt8StepBytes + 1024 /*align*/ + 256 /*barriers*/;
+      kPipeBytes + 2 * kInt8StepBytes + 1024 /*align*/ + 256 /*barriers*/;
   static_assert(kSlotCol + NSLOT * 64 <= 512, "TMEM columns");
-  static_assert(NSLOT <= STAGES, "a slot's last step is known by its stage's barrier");
-  static_assert(kBSub % 1024 == 0 && NT % 32 == 0, "swizzle atoms; epilogue steps");
+  static_assert(NSLOT <= SB, "a slot's last step is known by its rows' stage's barrier");
+  static_assert(kBSub % 1024 == 0 && NT % (2 * kBoxRows) == 0, "swizzle atoms; whole copies");
+  static_assert(NT <= 256 && ACOLS >= NT, "N of an MMA; a tile's accumulator");
   static_assert(8 * kBars + 8 <= 256, "barrier block");
 };
 
@@ -65,7 +71,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
                           const __grid_constant__ CUtensorMap tmShA2, const Int8Gemm g) {
   constexpr bool GLU = PASS == kInt8SwiGLU;
   constexpr int UCH = GLU ? 128 : 256;  // output channels per unit
-  constexpr int kNT = C::NT, kStages = C::STAGES, kBSub = C::kBSub, kStageBytes = C::kStageBytes;
+  constexpr int kNT = C::NT, kSA = C::SA, kSB = C::SB, kBSub = C::kBSub;
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ SegTable segs;
@@ -74,13 +80,16 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
-  uint8_t* const stage_out = gbase + kStages * kStageBytes;  // the epilogue's two steps
-  const uint32_t bar0 = base + kStages * kStageBytes + 2 * kInt8StepBytes;
-  auto codes_bar = [&](int s) { return bar0 + 8u * s; };                // own codes have landed
-  auto ready_bar = [&](int s) { return bar0 + 8u * (kStages + s); };    // rank 0: see above
-  auto done_bar = [&](int s) { return bar0 + 8u * (2 * kStages + s); };  // the step's MMAs are done
-  auto dfull_bar = [&](int b) { return bar0 + 8u * (3 * kStages + b); };
-  auto dempty_bar = [&](int b) { return bar0 + 8u * (3 * kStages + C::NACC + b); };  // rank 0
+  uint8_t* const stage_out = gbase + C::kPipeBytes;  // the epilogue's two steps
+  const uint32_t bar0 = base + C::kPipeBytes + 2 * kInt8StepBytes;
+  auto codes_bar = [&](int s) { return bar0 + 8u * s; };                   // own codes have landed
+  auto taken_bar = [&](int s) { return bar0 + 8u * (kSA + s); };           // and are in registers
+  auto ready_bar = [&](int s) { return bar0 + 8u * (2 * kSA + s); };       // rank 0: see above
+  auto done_bar = [&](int s) { return bar0 + 8u * (2 * kSA + kSB + s); };  // the step's MMAs are done
+  const uint32_t bar1 = bar0 + 8u * (2 * kSA + 2 * kSB);
+  auto dfull_bar = [&](int b) { return bar1 + 8u * b; };
+  auto dempty_bar = [&](int b) { return bar1 + 8u * (2 + b); };  // rank 0
+  const uint32_t inner_bar = bar1 + 8u * 4;                      // rank 0: see above
   const uint32_t mma_done_bar = bar0 + 8u * (C::kBars - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stage_out + 2 * kInt8StepBytes + 8 * C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -91,15 +100,19 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kSA; ++s) {
       ptx::mbar_init(codes_bar(s), 1);
+      ptx::mbar_init(taken_bar(s), 8);  // the widening warps
+    }
+    for (int s = 0; s < kSB; ++s) {
       ptx::mbar_init(ready_bar(s), 17);  // rows (with their bytes), eight widening warps of each CTA
       ptx::mbar_init(done_bar(s), 1);
     }
-    for (int b = 0; b < C::NACC; ++b) {
+    for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(dfull_bar(b), 1);
       ptx::mbar_init(dempty_bar(b), 8);  // four epilogue warps of each CTA
     }
+    ptx::mbar_init(inner_bar, 8);
     ptx::mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
     ptx::fence_mbarrier_init();
@@ -112,7 +125,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     ptx::tmem_relinquish_cg2();
   }
   griddep_wait();  // everything above touched only shared memory, TMEM and parameters
-  build_segments(segs, g, kNT);
+  build_segments(segs, g, min(g.tile_rows, kNT));
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // the peer's barriers are initialised
@@ -125,7 +138,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   const int splits = PASS == kInt8Partial ? g.splits : 1;
   const long long total = (long long)segs.first[g.n_mat + g.S] * n_ct * splits;
   auto unit_of = [&](long long w) {
-    return find_unit<GLU>(segs, g, n_ct, kNT, PASS == kInt8Partial ? w / splits : w);
+    return find_unit<GLU>(segs, g, n_ct, PASS == kInt8Partial ? w / splits : w);
   };
   auto first_step = [&](long long w) {
     return PASS == kInt8Partial ? (int)(w % splits) * n_step / splits : 0;
@@ -135,10 +148,14 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   };
   const long long pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   auto mma_rows = [](const Unit& u) { return (u.rows + 31) & ~31; };
+  // first column of the accumulator of a unit: even ones begin at the low end, odd ones end at the high
+  auto acc_col = [](int acc, int n) { return acc == 0 ? 0 : C::ACOLS - n; };
+  // columns that a unit shares with the one before it (a multiple of 32)
+  auto shared_cols = [](int n, int n_before) { return max(0, n + n_before - C::ACOLS); };
 
   if (warp == 0) {
     if (ptx::elect_one()) {
-      // ---------------------------------------------------------------- TMA producer (both)
+      // ---------------------------------------------------------------- TMA producer of codes (both)
       int stage = 0;
       uint32_t phase = 0, issued = 0, last_parity = 0;  // per stage: ever issued, its parity
       bool ok = true;
@@ -149,7 +166,45 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         const CUtensorMap* a0 = sh ? &tmShA : &tmA;
         const CUtensorMap* a1 = GLU ? (sh ? &tmShA2 : &tmA2) : a0;
         const int ch0 = u.ct * UCH + (int)rank * (UCH / 2), ch1 = GLU ? ch0 : ch0 + 64;
-        const int brow = u.brow0 + (int)rank * (mma_rows(u) / 2);
+        const int i1 = end_step(w);
+        for (int i = first_step(w); i < i1; ++i) {
+          if (!ptx::mbar_wait_bounded(taken_bar(stage), phase ^ 1u, abort_flag, g.status,
+                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sA = base + stage * kABytes, cb = codes_bar(stage);
+          ptx::mbar_arrive_expect_tx(cb, kABytes);
+          ptx::tma_load_3d(sA, a0, cb, i * kInt8StageK, ch0, ex);
+          ptx::tma_load_3d(sA + kABytes / 2, a1, cb, i * kInt8StageK, ch1, ex);
+          issued |= 1u << stage;
+          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == kSA) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // never leave while a copy into this CTA's shared memory may still be in flight
+      for (int s = 0; s < kSA; ++s)
+        if (issued & (1u << s)) {
+          volatile int no_abort = 0;
+          ptx::mbar_wait_bounded(codes_bar(s), (last_parity >> s) & 1u, &no_abort, g.status,
+                                 MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs / 4);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    if (ptx::elect_one()) {
+      // ---------------------------------------------------------------- TMA producer of rows (both)
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, last_parity = 0;
+      bool ok = true;
+      for (long long w = pair; w < total && ok; w += n_pairs) {
+        const Unit u = unit_of(w);
+        const int half_rows = mma_rows(u) / 2;  // of each CTA
+        const int brow = u.brow0 + (int)rank * half_rows;
+        const int boxes = (half_rows + kBoxRows - 1) / kBoxRows;
         const int i1 = end_step(w);
         for (int i = first_step(w); i < i1; ++i) {
           if (!ptx::mbar_wait_bounded(done_bar(stage), phase ^ 1u, abort_flag, g.status,
@@ -157,31 +212,29 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
             ok = false;
             break;
           }
-          const uint32_t sA = base + stage * kStageBytes, sB = sA + kABytes;
-          const uint32_t cb = codes_bar(stage);
+          const uint32_t sB = base + C::kRows + stage * (2 * kBSub);
           const uint32_t rb = leader ? ready_bar(stage) : ptx::mapa_shared(ready_bar(stage), 0);
           const bool half = 2 * i + 1 < n_sub;  // the step's second 64 k hold something
-          ptx::mbar_arrive_expect_tx(cb, kABytes);
-          ptx::tma_load_3d(sA, a0, cb, i * kInt8StageK, ch0, ex);
-          ptx::tma_load_3d(sA + kABytes / 2, a1, cb, i * kInt8StageK, ch1, ex);
-          if (leader) ptx::mbar_arrive_expect_tx(rb, 2 * (half ? 2 * kBSub : kBSub));
-          ptx::tma_load_2d_cg2(sB, &tmB, rb, i * kInt8StageK, brow);
-          if (half) ptx::tma_load_2d_cg2(sB + kBSub, &tmB, rb, i * kInt8StageK + 64, brow);
+          if (leader) ptx::mbar_arrive_expect_tx(rb, (half ? 4 : 2) * boxes * (kBoxRows * 128));
+          for (int b = 0; b < boxes; ++b) {
+            const uint32_t to = sB + b * (kBoxRows * 128);
+            ptx::tma_load_2d_cg2(to, &tmB, rb, i * kInt8StageK, brow + b * kBoxRows);
+            if (half)
+              ptx::tma_load_2d_cg2(to + kBSub, &tmB, rb, i * kInt8StageK + 64, brow + b * kBoxRows);
+          }
           issued |= 1u << stage;
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
+          if (++stage == kSB) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      // never leave while a copy into this CTA's shared memory may still be in flight. The rows' barrier
-      // also counts the widening warps, so after an abort it may not complete: then the wait runs out
-      for (int s = 0; s < kStages; ++s)
+      // the same for the rows. Their barrier also counts the widening warps, so after an abort it may not
+      // complete: then the wait runs out
+      for (int s = 0; s < kSB; ++s)
         if (issued & (1u << s)) {
           volatile int no_abort = 0;
-          ptx::mbar_wait_bounded(codes_bar(s), (last_parity >> s) & 1u, &no_abort, g.status,
-                                 MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs / 4);
           ptx::mbar_wait_bounded(done_bar(s), (last_parity >> s) & 1u, &no_abort, g.status,
                                  MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs / 4);
         }
@@ -190,17 +243,24 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   } else if (warp == 1) {
     if (leader && ptx::elect_one()) {
       // ---------------------------------------------------------------- MMA issuer (rank 0)
-      int stage = 0, slot = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      int stage = 0, slot = 0, acc = 0, n_before = 0;
+      uint32_t phase = 0, acc_phase = 0, inner_phase = 0;
       bool ok = true;
       for (long long w = pair; w < total && ok; w += n_pairs) {
-        const Unit u = unit_of(w);
-        const uint32_t idesc = ptx::idesc_f16kind_f32(256, (uint32_t)mma_rows(u), 0, 0, 0u);
+        const int n = mma_rows(unit_of(w));
+        const uint32_t idesc = ptx::idesc_f16kind_f32(256, (uint32_t)n, 0, 0, 0u);
         if (!ptx::mbar_wait_bounded(dempty_bar(acc), acc_phase ^ 1u, abort_flag, g.status,
                                     MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs))
           break;
+        if (shared_cols(n, n_before) > 0) {
+          if (!ptx::mbar_wait_bounded(inner_bar, inner_phase, abort_flag, g.status,
+                                      MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs))
+            break;
+          inner_phase ^= 1u;
+        }
+        n_before = n;
         ptx::tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * kNT);
+        const uint32_t d = tmem_base + (uint32_t)acc_col(acc, n);
         const int i0 = first_step(w), i1 = end_step(w);
         for (int i = i0; i < i1; ++i) {
           if (!ptx::mbar_wait_bounded(ready_bar(stage), phase, abort_flag, g.status,
@@ -212,7 +272,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
           const uint32_t a = tmem_base + C::kSlotCol + slot * 64;
           // rows: K-major, 128 B each, 8-row groups 1024 B apart; a K step of 16 = +32 B
           const uint64_t bd =
-              ptx::smem_desc_sw128(base + stage * kStageBytes + kABytes, 16, 1024);
+              ptx::smem_desc_sw128(base + C::kRows + stage * (2 * kBSub), 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             ptx::umma_f16_ta_cg2(d, a + kk * 8, bd + (uint64_t)(kk * 2), idesc,
@@ -225,17 +285,15 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
           }
           ptx::umma_commit_cg2(done_bar(stage), 0x3);
           if (++slot == C::NSLOT) slot = 0;
-          if (++stage == kStages) {
+          if (++stage == kSB) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
         ptx::umma_commit_cg2(dfull_bar(acc), 0x3);
-        if (++acc == C::NACC) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        acc_phase ^= (uint32_t)acc;
+        acc ^= 1;
       }
       // all MMAs issued by this thread have finished before TMEM is released
       ptx::umma_commit_cg2(mma_done_bar, 0x1);
@@ -248,7 +306,8 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     // ------------------------------------------------------------------ widening warps (both)
     const int h = (warp - 8) >> 2, q = warp & 3;  // half of the step; TMEM lanes [32 q, 32 q + 32)
     const int row = GLU ? 16 * q + (lane & 15) + 64 * (lane >> 4) : 32 * q + lane;
-    int stage = 0, slot = 0, dstage = 0;  // dstage: the stage of the step NSLOT before this one
+    int stage = 0, slot = 0;     // of the codes; of the widened ones
+    int bstage = 0, dstage = 0;  // the rows' stage of this step, and of the one NSLOT before it
     uint32_t phase = 0, dphase = 0, step = 0;
     bool ok = true;
     for (long long w = pair; w < total && ok; w += n_pairs) {
@@ -262,7 +321,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         const bool on = 2 * i + h < n_sub;
         uint32_t r[32];
         if (on) {
-          const uint8_t* src = gbase + stage * kStageBytes + row * kInt8StageK;
+          const uint8_t* src = gbase + stage * kABytes + row * kInt8StageK;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             // 16-byte piece 4 h + c of the row sits at piece (4 h + c) ^ (row mod 8)
@@ -280,7 +339,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
             ok = false;
             break;
           }
-          if (++dstage == kStages) {
+          if (++dstage == kSB) {
             dstage = 0;
             dphase ^= 1u;
           }
@@ -295,13 +354,15 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         }
         __syncwarp();
         if (lane == 0) {
+          ptx::mbar_arrive(taken_bar(stage));
           if (leader)
-            ptx::mbar_arrive(ready_bar(stage));
+            ptx::mbar_arrive(ready_bar(bstage));
           else
-            ptx::mbar_arrive_remote(ptx::mapa_shared(ready_bar(stage), 0));
+            ptx::mbar_arrive_remote(ptx::mapa_shared(ready_bar(bstage), 0));
         }
         if (++slot == C::NSLOT) slot = 0;
-        if (++stage == kStages) {
+        if (++bstage == kSB) bstage = 0;
+        if (++stage == kSA) {
           stage = 0;
           phase ^= 1u;
         }
@@ -315,8 +376,16 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     const int chl = GLU ? 16 * q + (lane & 15) : 32 * q + lane;  // channel of the CTA's panel
     int acc = 0, ub = 0, sb = 0;  // accumulator; buffers of the unit's rows and of the step
     uint32_t acc_phase = 0, clamp = 0u;
+    Unit u = {}, ahead = {};
+    if (pair < total) ahead = unit_of(pair);
     for (long long w = pair; w < total; w += n_pairs) {
-      const Unit u = unit_of(w);
+      u = ahead;
+      const int n = mma_rows(u);
+      int inner_steps = 0;  // steps that free the columns of the next unit
+      if (w + n_pairs < total) {
+        ahead = unit_of(w + n_pairs);
+        inner_steps = shared_cols(mma_rows(ahead), n) / 32;
+      }
       const bool sh = u.seg >= g.n_mat;
       const long long ex = sh ? u.seg - g.n_mat : u.seg;
       const int ch0 = u.ct * UCH + (int)rank * (UCH / 2);
@@ -338,9 +407,10 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
                                                     kInt8WaitNs)))
         break;
       ptx::tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * kNT);
+      const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)acc_col(acc, n);
 #pragma unroll 1
-      for (int c = 0; c * 32 < u.rows; ++c) {
+      for (int k = 0; k * 32 < n; ++k) {
+        const int c = acc == 0 ? n / 32 - 1 - k : k;  // the columns next to the other accumulator first
         uint32_t v[32];
         float sx[32];
         ptx::tmem_ld_32x32b_x32(taddr + c * 32, v);
@@ -349,14 +419,19 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         const uint32_t rows_on =
             PASS == kInt8Slot ? __ballot_sync(0xffffffffu, in && orow[c * 32 + lane] >= 0) : 0u;
         ptx::tmem_wait_ld();
-        if ((c + 1) * 32 >= u.rows) {  // the accumulator is in registers
+        const bool last = (k + 1) * 32 >= n, inner = k + 1 == inner_steps;
+        if (last || inner) {  // the accumulator, or those columns of it, are in registers
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (leader)
-              ptx::mbar_arrive(dempty_bar(acc));
-            else
-              ptx::mbar_arrive_remote(ptx::mapa_shared(dempty_bar(acc), 0));
+            auto arrive = [&](uint32_t bar) {
+              if (leader)
+                ptx::mbar_arrive(bar);
+              else
+                ptx::mbar_arrive_remote(ptx::mapa_shared(bar, 0));
+            };
+            if (inner) arrive(inner_bar);
+            if (last) arrive(dempty_bar(acc));
           }
         }
         if constexpr (GLU) {
@@ -391,10 +466,8 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
           }
         }
       }
-      if (++acc == C::NACC) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
+      acc_phase ^= (uint32_t)acc;
+      acc ^= 1;
     }
     if (PASS == kInt8Slot && __any_sync(0xffffffffu, clamp >= kInt8F16Clamp) && lane == 0)
       atomicOr(g.status, MOE_DEVFAULT_FP16_RANGE);
@@ -415,7 +488,7 @@ template <int PASS, int OUT, typename C>
 cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
   constexpr CUtensorMapDataType kCode = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   CUtensorMap b, a, a2, sa, sa2;
-  bool ok = make_tmap_2d(&b, g.xq, g.x_rows, g.K, 64, C::NT / 2, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) &&
+  bool ok = make_tmap_2d(&b, g.xq, g.x_rows, g.K, 64, kBoxRows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16) &&
             make_tmap_3d(&a, g.qw, g.n_mat, g.N, g.K, kInt8StageK, 64, kCode, 1);
   a2 = a;
   if (ok && PASS == kInt8SwiGLU)
@@ -454,8 +527,15 @@ cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
   // by the rows per segment of an even spread: a tile costs about the same whatever its rows, so the
   // narrower one, with more slots and stages, is for segments that it holds (64 segments of
   // [2048 x 2048], 96 rows each: 69 against 72 us; 128 rows each, half of them longer: 93 against 77)
-  if (g.rows / g.n_mat <= kInt8Mean128) return launch_one<PASS, OUT, Cfg<128, 2, 4, 6>>(g, st);
-  return launch_one<PASS, OUT, Cfg<192, 2, 2, 5>>(g, st);
+  const int mean = g.rows / g.n_mat;
+  Int8Gemm t = g;
+  t.tile_rows = 128;
+  if (mean <= kInt8Mean128) return launch_one<PASS, OUT, Cfg<128, 256, 4, 6, 6>>(t, st);
+  // tall tiles (int8_tile_height) where there are units for two rounds of the pairs without them
+  const int ch = PASS == kInt8SwiGLU ? 128 : 256;
+  const long long units = (mean + 191) / 192 * (long long)g.n_mat * ((g.N + ch - 1) / ch);
+  t.tile_rows = PASS != kInt8Partial && units >= num_sms() ? 256 : 192;
+  return launch_one<PASS, OUT, Cfg<256, 384, 2, 4, 4>>(t, st);
 }
 
 }  // namespace

@@ -37,7 +37,7 @@ struct Unit {
   int seg;      // expert, or n_mat + shared expert
   int ct;       // channel tile
   int row0;     // first position
-  int rows;     // 1..NT
+  int rows;     // 1..the segment's tile height
   int brow0;    // first row of the activations
 };
 
@@ -46,10 +46,11 @@ struct SegTable {
   int first[kMaxSegs + 1];
   int row0[kMaxSegs];
   int rows[kMaxSegs];
+  int height[kMaxSegs];  // rows of a row tile (the last one may be lower)
   int warp_tot[kInt8Threads / 32];
 };
 
-// Called by every thread of a CTA of kInt8Threads threads.
+// Called by every thread of a CTA of kInt8Threads threads. NT: the tallest tile.
 __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, int NT) {
   const int n = g.n_mat + g.S, i = threadIdx.x;
   const int lane = i & 31, warp = i >> 5;
@@ -69,7 +70,8 @@ __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, i
     r0 = g.rows + (i - g.n_mat) * g.T;
     nr = g.T;
   }
-  const int nt = (nr + NT - 1) / NT;
+  const int height = int8_tile_height(nr, NT);
+  const int nt = (nr + height - 1) / height;
   int v = nt;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -84,6 +86,7 @@ __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, i
     t.first[i] = base + v - nt;
     t.row0[i] = r0;
     t.rows[i] = nr;
+    t.height[i] = height;
     if (i == n - 1) t.first[n] = base + v;
   }
   __syncthreads();
@@ -91,7 +94,7 @@ __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, i
 
 // X_SHARED: the shared experts all read rows [rows, rows + T) of the activations (SwiGLU pass).
 template <bool X_SHARED>
-__device__ __forceinline__ Unit find_unit(const SegTable& t, const Int8Gemm& g, int n_ct, int NT,
+__device__ __forceinline__ Unit find_unit(const SegTable& t, const Int8Gemm& g, int n_ct,
                                           long long w) {
   int lo = 0, hi = g.n_mat + g.S;  // first[lo] * n_ct <= w < first[hi] * n_ct
   while (hi - lo > 1) {
@@ -110,9 +113,9 @@ __device__ __forceinline__ Unit find_unit(const SegTable& t, const Int8Gemm& g, 
   Unit u;
   u.seg = lo;
   u.ct = blk * kCtBlock + in % wide;
-  const int off = in / wide * NT;
+  const int off = in / wide * t.height[lo];
   u.row0 = t.row0[lo] + off;
-  u.rows = min(NT, t.rows[lo] - off);
+  u.rows = min(t.height[lo], t.rows[lo] - off);
   u.brow0 = X_SHARED && lo >= g.n_mat ? g.rows + off : u.row0;
   return u;
 }
