@@ -8,25 +8,30 @@
 // bandwidth in the 384 clk that N = 192 takes, and half the widening per MMA.
 //
 // 16384 rows of [4096 x 7168] in 482 us in short runs (2.0 PFLOP/s, 1.05 of the measured bf16 peak); a long
-// run settles at the power cap, 535. At N = 192 a 64 k slot's MMAs (384 clk) and its widening (388) take the
-// same time; a narrower tile is bound by the widening.
+// run settles at the power cap, 535. At 192 rows a 64 k slot's MMAs (384 clk) and its widening (388) take the
+// same time; a lower tile is bound by the widening, a taller one by its MMAs.
 //
-// A unit is 256 channels (SwiGLU pass: 128 channels of gate and up) x up to NT rows of one segment.
-// Rank r of a pair holds channels [128 r, 128 r + 128) and rows [n / 2 * r, n / 2 * (r + 1)) of the n
-// rows the MMA takes (the unit's rows rounded up to 32). SwiGLU pass: rank r holds 64 channels; TMEM lanes
-// 32 w + l, l < 16, hold the gate codes of channel 16 w + l and lanes 32 w + 16 + l the up codes, so that
-// a warp's epilogue swaps halves by shuffles. Roles per CTA (512 threads):
-//   warp 0       TMA producer: the CTA's 128 code rows x 128 B and two [NT / 2 rows x 64 k] fp16 tiles a
-//                step (128 k)
+// A unit is 256 channels (SwiGLU pass: 128 channels of gate and up) x a row tile of one segment
+// (int8_tile_height). Rank r of a pair holds channels [128 r, 128 r + 128) and rows [n / 2 * r, n / 2 *
+// (r + 1)) of the n rows the MMA takes (the unit's rows rounded up to 32). SwiGLU pass: rank r holds 64
+// channels; TMEM lanes 32 w + l, l < 16, hold the gate codes of channel 16 w + l and lanes 32 w + 16 + l the
+// up codes, so that a warp's epilogue swaps halves by shuffles. Roles per CTA (512 threads):
+//   warp 0       TMA producer of codes: the CTA's 128 code rows x 128 B a step (128 k)
 //   warp 1       MMA issuer (rank 0)
-//   warp 2       TMEM allocator: NACC accumulators of NT columns, NSLOT 64-column slots of widened codes
-//   warps 4-7    epilogue, overlapping the next unit's MMAs where there are two accumulators
+//   warp 2       TMEM allocator: ACOLS columns of accumulators, NSLOT 64-column slots of widened codes
+//   warp 3       TMA producer of rows: two [n / 2 rows x 64 k] fp16 tiles a step, 32 rows a copy
+//   warps 4-7    epilogue, overlapping the next unit's MMAs
 //   warps 8-15   widen: four warps the first 64 k of each step, four the second
 // The MMA issuer's barrier operations are few, because one behind a commit costs it about 300 clk, with or
 // without something to wait for: per 128 k it waits once (`ready`: both CTAs' rows have landed and all 16
-// widening warps have stored) and commits once (`done`, to both CTAs), and `done` frees the step's
-// stage and, with it, the slot of widened codes. (With a wait and a commit for each 64 k slot and each
-// stage, a 64 k slot took 480 clk whatever its N.)
+// widening warps have stored) and commits once (`done`, to both CTAs), and `done` frees the rows' stage and,
+// with it, the slot of widened codes. (With a wait and a commit for each 64 k slot and each stage, a 64 k
+// slot took 480 clk whatever its N.) The codes' stage is free once they are in registers (`taken`): they come
+// from HBM and need the longer run-up (64 segments of 128 rows of [2048 x 2048] 83 us with four stages of
+// both together, 77 apart).
+// The accumulators of consecutive units begin at opposite ends of the ACOLS columns, so two tiles whose
+// rows add up to ACOLS overlap fully. Where they add up to more, the second one's MMAs wait (`inner`) until
+// the epilogue has read the columns that they share, which it does first.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -524,17 +529,18 @@ cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
 
 template <int PASS, int OUT>
 cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
-  // by the rows per segment of an even spread: a tile costs about the same whatever its rows, so the
-  // narrower one, with more slots and stages, is for segments that it holds (64 segments of
-  // [2048 x 2048], 96 rows each: 69 against 72 us; 128 rows each, half of them longer: 93 against 77)
+  // by the rows per segment of an even spread: a tile costs about the same whatever its rows, so tiles of
+  // 128, with more slots and stages, are for segments that they hold (64 segments of [2048 x 2048], 96 rows
+  // each: 69 against 72 us; 128 rows each, half of them longer: 93 against 77)
   const int mean = g.rows / g.n_mat;
   Int8Gemm t = g;
   t.tile_rows = 128;
   if (mean <= kInt8Mean128) return launch_one<PASS, OUT, Cfg<128, 256, 4, 6, 6>>(t, st);
-  // tall tiles (int8_tile_height) where there are units for two rounds of the pairs without them
+  // tall tiles (int8_tile_height) where there are units for more than one round of the pairs without them
+  // (8 segments of 210 rows of [2048 x 2048] 21.6 against 25.9 us; 4 segments 18 against 16.4)
   const int ch = PASS == kInt8SwiGLU ? 128 : 256;
   const long long units = (mean + 191) / 192 * (long long)g.n_mat * ((g.N + ch - 1) / ch);
-  t.tile_rows = PASS != kInt8Partial && units >= num_sms() ? 256 : 192;
+  t.tile_rows = PASS != kInt8Partial && units > num_sms() / 2 ? 256 : 192;
   return launch_one<PASS, OUT, Cfg<256, 384, 2, 4, 4>>(t, st);
 }
 
