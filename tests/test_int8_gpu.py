@@ -177,6 +177,29 @@ def test_tensor_core_products(counts, K, N, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[200, 224, 225, 256, 257, 400, 449, 512, 513, 700, 1, 0],
+                                    [256] * 9, [400] * 7 + [193, 192] * 3])
+@pytest.mark.parametrize("K,N", [(48, 5200), (400, 2050)])
+def test_tall_row_tiles(counts, K, N):
+    """Segments cut into tiles of up to 256 rows, several units for each pair of CTAs, with K so short that
+    a tile's products are over before the one before it is stored."""
+    n, rows = len(counts), sum(counts)
+    off = [0] + [int(v) for v in np.cumsum(counts)]
+    qx, qw = (torch.randint(-60, 61, s, generator=gen(21), dtype=torch.int8)
+              for s in ((rows, K), (n, N, K)))
+    sx, sw = torch.rand(rows, generator=gen(22)) / 64, torch.rand(n, N, generator=gen(23)) / 64
+    y32, status = product(qx, sx, qw, sw, off, torch.float32)
+    assert status == 0
+    for e in range(n):
+        r = slice(off[e], off[e + 1])
+        want = (qx[r].cuda().double() @ qw[e].cuda().double().T) * sx[r, None].cuda() * sw[e].cuda()
+        assert ((y32[r].double() - want).abs() <= 4 * U * want.abs()).all()
+    for dtype in (torch.bfloat16, torch.float16):
+        y, status = product(qx, sx, qw, sw, off, dtype)
+        assert status == 0 and torch.equal(y, y32.to(dtype))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("rows,n", [(40, 1), (400, 1), (2000, 1), (1500, 16), (700, 64)])
 def test_largest_sums_on_the_tensor_cores(rows, n):
     """Sums far past 2^24, with the bound of test_largest_sums; N such that dot products do not
@@ -386,6 +409,18 @@ def test_experts(T, d, E, k, f, S, cap):
 def test_experts_of_few_tokens(T, E, k, S):
     cfg, st = layer(T, 192, E, k, 128, S, 0, seed=T + E)
     y = torch.full(((k + S) * T, 192), float("nan"), dtype=torch.float16, device="cuda")
+    M.grouped_ffn_int8(cfg, st["x"], st["perm_slot"], st["offsets"], st["topk_w"], st["weights"], y,
+                       st["ws"])
+    assert M.device_status(st["ws"]) == 0
+    check(y, experts64(cfg, st))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,E,k,f,S,cap", [
+    (1200, 1280, 8, 2, 640, 1, 0), (1700, 1088, 12, 2, 896, 0, 250)])
+def test_experts_of_tall_row_tiles(T, d, E, k, f, S, cap):
+    cfg, st = layer(T, d, E, k, f, S, cap, seed=T)
+    y = torch.full(((k + S) * T, d), float("nan"), dtype=torch.float16, device="cuda")
     M.grouped_ffn_int8(cfg, st["x"], st["perm_slot"], st["offsets"], st["topk_w"], st["weights"], y,
                        st["ws"])
     assert M.device_status(st["ws"]) == 0
