@@ -76,7 +76,7 @@ int int8_splits(long long rows, int K, int N, int n_mat);
 // pairs take tiles of at most 128 rows, not 256.
 constexpr int kInt8MeanSingle = 16, kInt8Mean128 = 104;
 // Height of a segment's row tiles, a multiple of 32 up to NT: as few tiles as NT allows, of equal heights,
-// as a tile of up to 192 rows costs the widening of its weights (388 clk per 64 k) whatever it holds.
+// as a tile of up to 192 rows costs the widening of its weights (about 400 clk per 64 k) whatever it holds.
 // Past 192 it costs its MMAs, 2 clk a row, and about 40 for the overlap with the next tile: taken where that
 // is less than one more tile (400 rows: two of 224 and 176, not three). 64 segments of about 200 rows of
 // [2048 x 2048] 91 us, with tiles of up to 192 rows 116; of about 300 rows 141, the same.

@@ -8,23 +8,23 @@
 // bandwidth in the 384 clk that N = 192 takes, and half the widening per MMA.
 //
 // 16384 rows of [4096 x 7168] in 482 us in short runs (2.0 PFLOP/s, 1.05 of the measured bf16 peak); a long
-// run settles at the power cap, 535. At 192 rows a 64 k slot's MMAs (384 clk) and its widening (388) take the
-// same time; a lower tile is bound by the widening, a taller one by its MMAs.
+// run settles at the power cap, 535. A 64 k slot takes 2 clk of MMA a row; widening it takes one set of warps
+// 776, so two sets keep up with 194 rows and three with 130: a lower tile is bound by the widening.
 //
 // A unit is 256 channels (SwiGLU pass: 128 channels of gate and up) x a row tile of one segment
 // (int8_tile_height). Rank r of a pair holds channels [128 r, 128 r + 128) and rows [n / 2 * r, n / 2 *
 // (r + 1)) of the n rows the MMA takes (the unit's rows rounded up to 32). SwiGLU pass: rank r holds 64
 // channels; TMEM lanes 32 w + l, l < 16, hold the gate codes of channel 16 w + l and lanes 32 w + 16 + l the
-// up codes, so that a warp's epilogue swaps halves by shuffles. Roles per CTA (512 threads):
+// up codes, so that a warp's epilogue swaps halves by shuffles. Roles per CTA:
 //   warp 0       TMA producer of codes: the CTA's 128 code rows x 128 B a step (128 k)
 //   warp 1       MMA issuer (rank 0)
 //   warp 2       TMEM allocator: ACOLS columns of accumulators, NSLOT 64-column slots of widened codes
 //   warp 3       TMA producer of rows: two [n / 2 rows x 64 k] fp16 tiles a step, 32 rows a copy
 //   warps 4-7    epilogue, overlapping the next unit's MMAs
-//   warps 8-15   widen: four warps the first 64 k of each step, four the second
+//   warps 8-     widen, in SETS of four warps: the half-steps (64 k) of all units go to the sets in turn
 // The MMA issuer's barrier operations are few, because one behind a commit costs it about 300 clk, with or
-// without something to wait for: per 128 k it waits once (`ready`: both CTAs' rows have landed and all 16
-// widening warps have stored) and commits once (`done`, to both CTAs), and `done` frees the rows' stage and,
+// without something to wait for: per 128 k it waits once (`ready`: both CTAs' rows have landed and the
+// eight warps of each that widen the step have stored) and commits once (`done`, to both CTAs), and `done` frees the rows' stage and,
 // with it, the slot of widened codes. (With a wait and a commit for each 64 k slot and each stage, a 64 k
 // slot took 480 clk whatever its N.) The codes' stage is free once they are in registers (`taken`): they come
 // from HBM and need the longer run-up (64 segments of 128 rows of [2048 x 2048] 83 us with four stages of
@@ -32,6 +32,11 @@
 // The accumulators of consecutive units begin at opposite ends of the ACOLS columns, so two tiles whose
 // rows add up to ACOLS overlap fully. Where they add up to more, the second one's MMAs wait (`inner`) until
 // the epilogue has read the columns that they share, which it does first.
+// Three sets (640 threads: 96 registers each at launch, then 80 for the widening warps and 144 for the
+// epilogue) against two: 48 tokens an expert, 148 against 154 us for the experts of d 2048, d_ff 1408;
+// 16384 rows of [4096 x 7168] 1 to 3 % less. The slot pass of tall tiles keeps two: its units are short (11
+// steps at K = 1408), its epilogue nearly as long as its MMAs, and a third set takes issue slots from it (132
+// against 139 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -45,13 +50,13 @@ namespace moe {
 namespace {
 
 constexpr int kABytes = kInt8Ch * kInt8StageK;  // 16 KB of codes
-
 constexpr int kBoxRows = 32;                    // rows of one copy
 
 // Tiles of up to NT rows; two accumulators in ACOLS TMEM columns, NSLOT slots of 64 for widened codes; SA
-// and SB stages of codes and of rows.
-template <int NT_, int ACOLS_, int NSLOT_, int SA_, int SB_>
+// and SB stages of codes and of rows; SETS of four widening warps.
+template <int NT_, int ACOLS_, int NSLOT_, int SA_, int SB_, int SETS_>
 struct Cfg {
+  static constexpr int SETS = SETS_, kThreads = 256 + 128 * SETS;
   static constexpr int NT = NT_, ACOLS = ACOLS_, NSLOT = NSLOT_, SA = SA_, SB = SB_;
   static constexpr int kBSub = NT / 2 * 128;  // one [NT / 2 rows x 64 k] fp16 tile
   static constexpr int kRows = SA * kABytes;  // where the rows' stages begin
@@ -61,6 +66,7 @@ struct Cfg {
   static constexpr int kSmemBytes =
       kPipeBytes + 2 * kInt8StepBytes + 1024 /*align*/ + 256 /*barriers*/;
   static_assert(kSlotCol + NSLOT * 64 <= 512, "TMEM columns");
+  static_assert(SA >= NSLOT + 2 && SB >= 2, "a set that passes over steps finds each phase");
   static_assert(NSLOT <= SB, "a slot's last step is known by its rows' stage's barrier");
   static_assert(kBSub % 1024 == 0 && NT % (2 * kBoxRows) == 0, "swizzle atoms; whole copies");
   static_assert(NT <= 256 && ACOLS >= NT, "N of an MMA; a tile's accumulator");
@@ -68,7 +74,7 @@ struct Cfg {
 };
 
 template <int PASS, int OUT, typename C>
-__global__ void __launch_bounds__(kInt8Threads, 1)
+__global__ void __launch_bounds__(C::kThreads, 1)
     int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmA2,
@@ -107,7 +113,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSA; ++s) {
       ptx::mbar_init(codes_bar(s), 1);
-      ptx::mbar_init(taken_bar(s), 8);  // the widening warps
+      ptx::mbar_init(taken_bar(s), 8);  // the step's widening warps
     }
     for (int s = 0; s < kSB; ++s) {
       ptx::mbar_init(ready_bar(s), 17);  // rows (with their bytes), eight widening warps of each CTA
@@ -309,72 +315,92 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ widening warps (both)
-    const int h = (warp - 8) >> 2, q = warp & 3;  // half of the step; TMEM lanes [32 q, 32 q + 32)
+    const int set = (warp - 8) >> 2, q = warp & 3;  // TMEM lanes [32 q, 32 q + 32)
     const int row = GLU ? 16 * q + (lane & 15) + 64 * (lane >> 4) : 32 * q + lane;
-    int stage = 0, slot = 0;     // of the codes; of the widened ones
-    int bstage = 0, dstage = 0;  // the rows' stage of this step, and of the one NSLOT before it
-    uint32_t phase = 0, dphase = 0, step = 0;
-    bool ok = true;
-    for (long long w = pair; w < total && ok; w += n_pairs) {
-      const int i1 = end_step(w);
-      for (int i = first_step(w); i < i1; ++i, ++step) {
-        if (!ptx::mbar_wait_bounded_warp(codes_bar(stage), phase, abort_flag, g.status,
-                                         MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
-          ok = false;
-          break;
+    if constexpr (C::SETS == 3) ptx::setmaxnreg_dec<80>();
+    // half-steps of 64 k, numbered through all units, go to the sets in turn. A set passes over steps of the
+    // others, but each barrier's earlier phase is over when it looks: its last step, at most two before this
+    // one, had all but NSLOT of the steps before it done, and SA >= NSLOT + 2
+    uint32_t step = 0;           // step of this set's half-step, and of it:
+    int h = set;                 // the half
+    int stage = 0, slot = 0;     // the stage of the codes; the slot of the widened ones
+    int bstage = 0, dstage = 0;  // the rows' stage, and that of the step NSLOT before it
+    uint32_t phase = 0, dphase = 0;
+    long long w = pair;
+    int i = w < total ? first_step(w) : 0, i1 = w < total ? end_step(w) : 0;
+    auto next_step = [&] {
+      if (++slot == C::NSLOT) slot = 0;
+      if (++bstage == kSB) bstage = 0;
+      if (++stage == kSA) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (step >= (uint32_t)C::NSLOT && ++dstage == kSB) {
+        dstage = 0;
+        dphase ^= 1u;
+      }
+      ++step;
+      if (++i == i1) {
+        w += n_pairs;
+        if (w < total) {
+          i = first_step(w);
+          i1 = end_step(w);
         }
-        const bool on = 2 * i + h < n_sub;
-        uint32_t r[32];
-        if (on) {
-          const uint8_t* src = gbase + stage * kABytes + row * kInt8StageK;
+      }
+    };
+    if (C::SETS == 3 && h == 2) {
+      if (w < total) next_step();
+      h = 0;
+    }
+    while (w < total) {
+      if (!ptx::mbar_wait_bounded_warp(codes_bar(stage), phase, abort_flag, g.status,
+                                       MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs))
+        break;
+      const bool on = 2 * i + h < n_sub;
+      uint32_t r[32];
+      if (on) {
+        const uint8_t* src = gbase + stage * kABytes + row * kInt8StageK;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // 16-byte piece 4 h + c of the row sits at piece (4 h + c) ^ (row mod 8)
-            const uint4 v =
-                *reinterpret_cast<const uint4*>(src + (((4 * h + c) ^ (row & 7)) << 4));
-            widen4(v.x, r[8 * c], r[8 * c + 1]);
-            widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
-            widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
-            widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
-          }
+        for (int c = 0; c < 4; ++c) {
+          // 16-byte piece 4 h + c of the row sits at piece (4 h + c) ^ (row mod 8)
+          const uint4 v = *reinterpret_cast<const uint4*>(src + (((4 * h + c) ^ (row & 7)) << 4));
+          widen4(v.x, r[8 * c], r[8 * c + 1]);
+          widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+          widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+          widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
         }
-        if (step >= (uint32_t)C::NSLOT) {  // the MMAs that read this slot last are done
-          if (!ptx::mbar_wait_bounded_warp(done_bar(dstage), dphase, abort_flag, g.status,
-                                           MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs)) {
-            ok = false;
-            break;
-          }
-          if (++dstage == kSB) {
-            dstage = 0;
-            dphase ^= 1u;
-          }
-        }
-        if (on) {
-          ptx::tc_fence_after();
-          ptx::tmem_st_32x32b_x32(tmem_base + ((uint32_t)(32 * q) << 16) +
-                                      (uint32_t)(C::kSlotCol + slot * 64 + h * 32),
-                                  r);
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(taken_bar(stage));
-          if (leader)
-            ptx::mbar_arrive(ready_bar(bstage));
-          else
-            ptx::mbar_arrive_remote(ptx::mapa_shared(ready_bar(bstage), 0));
-        }
-        if (++slot == C::NSLOT) slot = 0;
-        if (++bstage == kSB) bstage = 0;
-        if (++stage == kSA) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      }
+      // the MMAs that read this slot last are done
+      if (step >= (uint32_t)C::NSLOT &&
+          !ptx::mbar_wait_bounded_warp(done_bar(dstage), dphase, abort_flag, g.status,
+                                       MOE_DEVFAULT_PIPELINE_TIMEOUT, kInt8WaitNs))
+        break;
+      if (on) {
+        ptx::tc_fence_after();
+        ptx::tmem_st_32x32b_x32(tmem_base + ((uint32_t)(32 * q) << 16) +
+                                    (uint32_t)(C::kSlotCol + slot * 64 + h * 32),
+                                r);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(taken_bar(stage));
+        if (leader)
+          ptx::mbar_arrive(ready_bar(bstage));
+        else
+          ptx::mbar_arrive_remote(ptx::mapa_shared(ready_bar(bstage), 0));
+      }
+      // SETS half-steps on
+      next_step();
+      if (C::SETS == 3) {
+        if (h == 1 && w < total) next_step();
+        h ^= 1;
       }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue (both)
+    if constexpr (C::SETS == 3) ptx::setmaxnreg_inc<144>();
     using P = Panel<PASS, OUT, GLU ? 64 : 128>;
     const int q = warp - 4, t = threadIdx.x - 128;
     const int up = GLU ? lane >> 4 : 0;  // this lane's accumulators belong to the up projection
@@ -512,7 +538,7 @@ cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_sms() / 2 * 2);  // persistent: one CTA pair per two SMs
-  cfg.blockDim = dim3(kInt8Threads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -535,13 +561,13 @@ cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
   const int mean = g.rows / g.n_mat;
   Int8Gemm t = g;
   t.tile_rows = 128;
-  if (mean <= kInt8Mean128) return launch_one<PASS, OUT, Cfg<128, 256, 4, 6, 6>>(t, st);
+  if (mean <= kInt8Mean128) return launch_one<PASS, OUT, Cfg<128, 256, 4, 6, 6, 3>>(t, st);
   // tall tiles (int8_tile_height) where there are units for more than one round of the pairs without them
   // (8 segments of 210 rows of [2048 x 2048] 21.6 against 25.9 us; 4 segments 18 against 16.4)
   const int ch = PASS == kInt8SwiGLU ? 128 : 256;
   const long long units = (mean + 191) / 192 * (long long)g.n_mat * ((g.N + ch - 1) / ch);
   t.tile_rows = PASS != kInt8Partial && units > num_sms() / 2 ? 256 : 192;
-  return launch_one<PASS, OUT, Cfg<256, 384, 2, 4, 4>>(t, st);
+  return launch_one<PASS, OUT, Cfg<256, 384, 2, 4, 4, PASS == kInt8Slot ? 2 : 3>>(t, st);
 }
 
 }  // namespace

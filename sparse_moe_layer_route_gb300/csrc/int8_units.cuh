@@ -47,10 +47,10 @@ struct SegTable {
   int row0[kMaxSegs];
   int rows[kMaxSegs];
   int height[kMaxSegs];  // rows of a row tile (the last one may be lower)
-  int warp_tot[kInt8Threads / 32];
+  int warp_tot[32];
 };
 
-// Called by every thread of a CTA of kInt8Threads threads. NT: the tallest tile.
+// Called by every thread of a CTA (of at least kMaxSegs). NT: the tallest tile.
 __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, int NT) {
   const int n = g.n_mat + g.S, i = threadIdx.x;
   const int lane = i & 31, warp = i >> 5;

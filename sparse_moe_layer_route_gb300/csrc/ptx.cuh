@@ -29,6 +29,17 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// A warpgroup's registers per thread, down or up (a multiple of 8). The warpgroups' shares may not add up
+// to more than the block was launched with: a rise waits until there are that many.
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
