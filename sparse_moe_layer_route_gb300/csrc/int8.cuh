@@ -1,5 +1,5 @@
 // 8-bit expert products: the quantization rule and the launch interface between the entry points
-// (int8_api.cu) and the kernels (int8_rows.cu, int8_gemm.cu).
+// (int8_api.cu) and the kernels (int8_rows.cu, int8_gemv.cu, int8_gemm.cu, int8_split.cu).
 #pragma once
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -53,7 +53,7 @@ struct Int8Gemm {
   int rows, K, N, n_mat, S, T;
   int out_dtype;             // matrix pass
   int splits;                // partial pass: pieces of K
-  int tile_rows;             // CTA pairs: the tallest row tile
+  int tile_rows;             // tensor cores: the tallest row tile
 };
 
 enum Int8Pass {
@@ -63,18 +63,17 @@ enum Int8Pass {
   kInt8Partial = 3  // out [splits][rows, N] fp32 = sums over one piece of K, without scales
 };
 
-// Tensor cores: long segments on CTA pairs (int8_gemm_pair.cu), others on single CTAs (int8_gemm.cu).
-cudaError_t launch_int8_gemm_pair(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
+// Tensor cores (int8_gemm.cu).
+cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
 // A few rows (int8_gemv.cu); most_rows: no segment has more.
 cudaError_t launch_int8_gemv(Int8Pass pass, const Int8Gemm& g, int most_rows, cudaStream_t st);
-cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
 // Pieces of K that give a product with few work units something to do on every SM (1: none), for a
 // matrix pass of this shape; and that product: partial sums to `part` (int8_splits() * rows * N floats),
 // then their sums, scaled, to g.out.
 int int8_splits(long long rows, int K, int N, int n_mat);
-// Rows per segment (an even spread's) up to which a product runs on single CTAs, and up to which CTA
-// pairs take tiles of at most 128 rows, not 256.
-constexpr int kInt8MeanSingle = 16, kInt8Mean128 = 104;
+constexpr int kInt8StageK = 128;  // k per shared-memory stage
+// Rows per segment (an even spread's) up to which row tiles have at most 64 and 128 rows, not 256.
+constexpr int kInt8Mean64 = 24, kInt8Mean128 = 104;
 // Height of a segment's row tiles, a multiple of 32 up to NT: as few tiles as NT allows, of equal heights,
 // as a tile of up to 192 rows costs the widening of its weights (about 400 clk per 64 k) whatever it holds.
 // Past 192 it costs its MMAs, 2 clk a row, and about 40 for the overlap with the next tile: taken where that

@@ -12,13 +12,13 @@ namespace {
 constexpr size_t kHead = 512;  // status word and counter block, as in every workspace
 // Where int8_gemv.cu is faster than the tensor cores: few rows, or so little work that a unit's long
 // pipeline (and the launches in front of it) is most of a tensor-core product's time.
-//   product: 8 rows of [14336 x 4096] 16 against 24 us, 12 rows 26 against 24.5; 0.3 G multiply-adds (150
-//   rows of [1000 x 2048]) 11.8 against 13.5 to 22 (three launches, by the host), 0.6 G (20
-//   segments of 30 rows) 28 against 16; between them it depends on the shape (300 segment rows of
-//   [1000 x 1024], 0.3 G, 17 against 16, 300 of [600 x 512] 10 against 16).
-//   experts: decode shape, 6 tokens 92 against 143 us, 12 tokens 163 against 204, 24 tokens 285 against
-//   281; 64 + 2 experts of [2048 x 1408], 6 a token, 12 tokens 88 against 96, 16 tokens 101 against 96; of
-//   small layers, 32 tokens, 60 M multiply-adds, 17 against 20, and 64 tokens, 240 M, 38 against 27.
+//   product: 8 rows of [14336 x 4096] 16 against 21.5 us, 12 rows 26 against 21; 0.3 G multiply-adds (150
+//   rows of [1000 x 2048]) 11 against 16, 0.6 G (20 segments of 30 rows) 28 against 15; between them it
+//   depends on the shape (300 rows in 20 segments of [1000 x 1024], 0.3 G, 17 against 14, of [600 x 512]
+//   9.4 against 14).
+//   experts: decode shape, 6 tokens 92 against 119 us, 12 tokens 162 against 183, 24 tokens 283 against 281;
+//   64 + 2 experts of [2048 x 1408], 6 a token, 12 tokens 88 against 88, 16 tokens 101 against 93; of
+//   small layers, 32 tokens, 60 M multiply-adds, 18 against 22, and 64 tokens, 100 M, 22 against 22.
 bool few_rows(int rows, int K, int N) { return rows <= 8 || (double)rows * K * N <= 4e8; }
 bool few_tokens(const Shape& s) { return s.T <= 12 || 3.0 * s.rows * s.d * s.f <= 1e8; }
 

@@ -9,9 +9,7 @@
 
 namespace moe {
 
-constexpr int kInt8Threads = 512;
 constexpr int kInt8Ch = 128;                       // channels per MMA tile of one CTA (TMEM lanes)
-constexpr int kInt8StageK = 128;                   // k per shared-memory stage
 constexpr uint64_t kInt8WaitNs = 2000000000ull;    // 2 s per wait
 constexpr int kMaxSegs = 256 + 4;
 // Channel tiles per block of units. A prefill product of 16384 x 7168 rows: with 16 tiles in a row of row

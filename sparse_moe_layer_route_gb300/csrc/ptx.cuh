@@ -183,18 +183,6 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// The same with A in tensor memory: a 16-bit A of M = 128 rows has row i in lane i and elements
-// 2 j, 2 j + 1 of the K step in 32-bit column j.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Arrive once on an mbarrier when all previously issued tcgen05.mma of this thread complete.
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile(
@@ -314,7 +302,8 @@ __device__ __forceinline__ void umma_f16_cg2(uint32_t d_tmem, uint64_t a_desc, u
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// The same with A in tensor memory: each CTA's TMEM holds its own 128 rows, at the same columns.
+// The same with A in tensor memory: each CTA's TMEM holds its own 128 rows at the same columns, row i in
+// lane i, 16-bit elements 2 j and 2 j + 1 of the K step in 32-bit column j.
 __device__ __forceinline__ void umma_f16_ta_cg2(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                                 uint32_t idesc, uint32_t accumulate) {
   asm volatile(
