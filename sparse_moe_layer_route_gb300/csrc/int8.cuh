@@ -68,9 +68,11 @@ cudaError_t launch_int8_gemm(Int8Pass pass, const Int8Gemm& g, cudaStream_t st);
 // A few rows (int8_gemv.cu); most_rows: no segment has more.
 cudaError_t launch_int8_gemv(Int8Pass pass, const Int8Gemm& g, int most_rows, cudaStream_t st);
 // Pieces of K that give a product with few work units something to do on every SM (1: none), for a
-// matrix pass of this shape; and that product: partial sums to `part` (int8_splits() * rows * N floats),
+// matrix pass of this shape; and that product: partial sums to `part` (int8_splits() * rows * int8_part_cols(N) floats),
 // then their sums, scaled, to g.out.
 int int8_splits(long long rows, int K, int N, int n_mat);
+// Floats of a row of partial sums: rows begin on 16 bytes whatever N, so they are stored in 16-byte pieces.
+__host__ __device__ inline int int8_part_cols(int N) { return (N + 3) / 4 * 4; }
 constexpr int kInt8StageK = 128;  // k per shared-memory stage
 // Rows per segment (an even spread's) up to which row tiles have at most 64 and 128 rows, not 256.
 constexpr int kInt8Mean64 = 24, kInt8Mean128 = 104;

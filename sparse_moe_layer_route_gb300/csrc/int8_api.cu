@@ -45,7 +45,7 @@ size_t matmul_part(int32_t rows, int32_t K) {
 }
 size_t matmul_part_bytes(int32_t rows, int32_t K, int32_t N, int32_t n_mat) {
   const int splits = few_rows(rows, K, N) ? 1 : int8_splits(rows, K, N, n_mat);
-  return splits > 1 ? 4ull * splits * rows * N : 0;
+  return splits > 1 ? 4ull * splits * rows * int8_part_cols(N) : 0;
 }
 
 // Buffers of one FFN call.

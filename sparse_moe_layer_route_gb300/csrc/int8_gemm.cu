@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       // partial pass: this piece's plane of the output
       uint8_t* out = static_cast<uint8_t*>(g.out);
-      if (PASS == kInt8Partial) out += (w % splits) * 4ll * g.rows * g.N;
+      const int cols = PASS == kInt8Partial ? int8_part_cols(g.N) : g.N;
+      if (PASS == kInt8Partial) out += (w % splits) * 4ll * g.rows * cols;
       float* usx = unit_sx[ub];
       int* orow = unit_orow[ub];
       ub ^= 1;
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             P::put(buf, col, chl, swiglu(gv, uv));
           }
           epilogue_barrier();
-          P::flush(out, g.N, buf, orow + c * 32, ch0, t);
+          P::flush(out, cols, buf, orow + c * 32, ch0, t);
           sb ^= 1;
         } else {
 #pragma unroll
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                 clamp = max(clamp, mag_bits(y));
             }
             epilogue_barrier();
-            P::flush(out, g.N, buf, orow + c * 32 + j0, ch0, t);
+            P::flush(out, cols, buf, orow + c * 32 + j0, ch0, t);
             sb ^= 1;
           }
         }
@@ -567,24 +568,32 @@ cudaError_t launch_one(const Int8Gemm& g, cudaStream_t st) {
 
 template <int PASS, int OUT>
 cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
-  // by the rows per segment of an even spread: a tile costs about the same whatever its rows, so tiles of
-  // 128, with more slots and stages, are for segments that they hold (64 segments of [2048 x 2048], 96 rows
-  // each: 69 against 72 us; 128 rows each, half of them longer: 93 against 77)
-  const int mean = g.rows / g.n_mat;
+  const int mean = g.rows / g.n_mat, pairs = num_sms() / 2, ch = PASS == kInt8SwiGLU ? 128 : 256;
+  // units with tiles of at most `tile` rows, of an even spread of the rows over the segments
+  auto units = [&](int tile) {
+    return ((long long)((mean + tile - 1) / tile) * g.n_mat +
+            (long long)((g.T + tile - 1) / tile) * g.S) *
+           ((g.N + ch - 1) / ch);
+  };
+  // where one round of the pairs holds all units, the lowest tiles for which it does: the round takes as
+  // long as one unit (pieces of K fill the pairs already)
+  auto one_round = [&](int tile) { return PASS != kInt8Partial && units(tile) <= pairs; };
   Int8Gemm t = g;
   // decode: deeper stages, for the weights' sake, where tiles of 64 rows hold every segment (64 tokens, 128 + 1
   // experts of d 7168, d_ff 2048 502 against 514 us; with a shared expert's 512 rows in tiles of 64 541
   // against 524)
   t.tile_rows = 64;
-  if (mean <= kInt8Mean64 && (g.S == 0 || g.T <= 64))
+  if ((mean <= kInt8Mean64 && (g.S == 0 || g.T <= 64)) || one_round(64))
     return launch_one<PASS, OUT, Cfg<64, 128, 4, 9, 6, 3>>(t, st);
+  // a tile costs about the same whatever its rows, so tiles of 128, with more slots and stages, are for
+  // segments that they hold (64 segments of [2048 x 2048], 96 rows each: 69 against 72 us; 128 rows each,
+  // half of them longer: 93 against 77)
   t.tile_rows = 128;
-  if (mean <= kInt8Mean128) return launch_one<PASS, OUT, Cfg<128, 256, 4, 6, 6, 3>>(t, st);
+  if (mean <= kInt8Mean128 || one_round(128))
+    return launch_one<PASS, OUT, Cfg<128, 256, 4, 6, 6, 3>>(t, st);
   // tall tiles (int8_tile_height) where there are units for more than one round of the pairs without them
   // (8 segments of 210 rows of [2048 x 2048] 21.6 against 25.9 us; 4 segments 18 against 16.4)
-  const int ch = PASS == kInt8SwiGLU ? 128 : 256;
-  const long long units = (mean + 191) / 192 * (long long)g.n_mat * ((g.N + ch - 1) / ch);
-  t.tile_rows = PASS != kInt8Partial && units > num_sms() / 2 ? 256 : 192;
+  t.tile_rows = PASS != kInt8Partial && units(192) > pairs ? 256 : 192;
   return launch_one<PASS, OUT, Cfg<256, 384, 2, 4, 4, PASS == kInt8Slot ? 2 : 3>>(t, st);
 }
 

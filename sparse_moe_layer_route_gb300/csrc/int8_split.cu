@@ -36,13 +36,14 @@ __global__ void __launch_bounds__(256) join_splits_kernel(const float* __restric
   }
   const int n = blockIdx.y * 256 + threadIdx.x;
   if (n >= g.N) return;
-  const long long at = (long long)row * g.N + n, plane = (long long)g.rows * g.N;
+  const long long at = (long long)row * g.N + n, cols = int8_part_cols(g.N);
+  const long long from = row * cols + n, plane = g.rows * cols;
   const float scale = g.sx[row] * g.sw[(long long)seg * g.N + n];
   float sum = 0.0f;
   for (int i = 0; i < g.splits; i += 8) {  // eight loads in flight, added in the pieces' order
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = i + j < g.splits ? part[(i + j) * plane + at] : 0.0f;
+    for (int j = 0; j < 8; ++j) v[j] = i + j < g.splits ? part[(i + j) * plane + from] : 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += v[j];
   }
