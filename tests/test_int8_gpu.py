@@ -177,6 +177,28 @@ def test_tensor_core_products(counts, K, N, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts,K,N", [([33], 4096, 3001), ([150, 0, 61], 2064, 1049),
+                                        ([90, 3, 0, 61], 2064, 1400), ([40], 7168, 1502)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_pieces_of_k_in_rows_of_any_length(counts, K, N, dtype):
+    """K in pieces; y's rows on 16 bytes and not, and y itself one element past 16 bytes."""
+    n, rows = len(counts), sum(counts)
+    off = [0] + [int(v) for v in np.cumsum(counts)]
+    # codes whose sums stay below 2^24: at most 7168 * 48 * 48
+    qx, qw = (torch.randint(-48, 49, s, generator=gen(31), dtype=torch.int8)
+              for s in ((rows, K), (n, N, K)))
+    sx, sw = torch.rand(rows, generator=gen(32)) / 64, torch.rand(n, N, generator=gen(33)) / 64
+    y32, status = product(qx, sx, qw, sw, off if n > 1 else None, torch.float32)
+    want = product64(qx, sx, qw, sw, off)
+    assert status == 0 and ((y32.double().cpu() - want).abs() <= 4 * U * want.abs()).all()
+    y = torch.empty(rows * N + 1, dtype=dtype, device="cuda")[1:].view(rows, N)
+    ws = M.alloc_int8_workspace(M.int8_matmul_workspace_size(rows, K, N, n))
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda") if n > 1 else None
+    M.int8_matmul(qx.cuda(), sx.cuda(), qw.cuda(), sw.cuda(), offsets, y, ws)
+    assert M.device_status(ws) == 0 and torch.equal(y, y32.to(dtype))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("counts", [[200, 224, 225, 256, 257, 400, 449, 512, 513, 700, 1, 0],
                                     [256] * 9, [400] * 7 + [193, 192] * 3])
 @pytest.mark.parametrize("K,N", [(48, 5200), (400, 2050)])
