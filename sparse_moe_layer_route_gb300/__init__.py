@@ -459,12 +459,14 @@ def route_logits_backward(gcfg: GateConfig, logits, topk_idx, d_topk_w, d_scores
 
 
 def quantize_rows(x, q, scale, stream=None):
-    """x [T, d] (fp32, bf16 or fp16; rows may be strided) to q int8 [T, d] and scale fp32 [T]."""
+    """x [T, d] (fp32, bf16 or fp16; rows may be strided, but not share elements: an expanded row's
+    stride of 0 means `contiguous` to the library) to q int8 [T, d] and scale fp32 [T]."""
     w, n = "moe_quantize_rows", _names()
     T, d = x.shape
     step, unit = x.stride()
-    if not x.is_cuda or (d > 1 and unit != 1):
-        raise ValueError(f"{w}: x must be a CUDA tensor with unit stride inside a row")
+    if not x.is_cuda or (d > 1 and unit != 1) or (T > 1 and step < d):
+        raise ValueError(f"{w}: x must be a CUDA tensor with unit stride inside a row and rows at "
+                         f"least {d} apart, not strides {x.stride()} on {x.device}")
     _check(lib().moe_quantize_rows(T, d, _dtype_code(x, w), x.data_ptr(), step if T > 1 else d,
                                    _expect(w, "q", q, (T, d), n.i8),
                                    _expect(w, "scale", scale, (T,), n.f32),
