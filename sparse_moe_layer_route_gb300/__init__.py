@@ -386,6 +386,7 @@ class _Torch:
         self.i8, self.i32 = torch.int8, torch.int32
         self.code = {self.f32: DTYPE_F32, self.bf16: DTYPE_BF16, self.f16: DTYPE_F16}
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 _torch_names = None
@@ -398,12 +399,21 @@ def _names() -> _Torch:
     return _torch_names
 
 
-def _stream_of(stream, t):
-    """The raw handle of `stream`, or of the current stream of tensor t's device."""
+def _stream_on(stream, gpu):
+    """The raw handle of `stream`, or of the current stream of the current GPU, number `gpu`."""
     if stream is None:
         raw = _names().raw_stream
-        return raw(t.get_device()) if raw is not None else _stream(None)
+        return raw(gpu) if raw is not None else _stream(None)
     return _stream(stream)
+
+
+def _current_gpu(where, name, t):
+    """The current GPU's number; launches go there, so tensor t, and with it all others, has to be
+    there too."""
+    gpu = t.get_device()
+    if not t.is_cuda or gpu != _names().current_device():
+        raise ValueError(f"{where}: {name} is on {t.device}, which is not the current GPU")
+    return gpu
 
 
 def _dtype_code(t, where):
@@ -413,16 +423,16 @@ def _dtype_code(t, where):
     return code
 
 
-def _expect(where, name, t, shape, dtype):
-    """t: a contiguous tensor of this shape and element type on the GPU. Its address."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor {dtype} {shape}, not "
-                         f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+def _expect(where, name, t, shape, dtype, gpu):
+    """t: a contiguous tensor of this shape and element type on GPU `gpu`. Its address."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != gpu or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous tensor {dtype} {shape} on cuda:{gpu}, "
+                         f"not {t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
     return t.data_ptr()
 
 
 def _expect_logits(where, gcfg, T, E, logits):
-    if logits.shape != (T, E) or not logits.is_cuda or \
+    if logits.shape != (T, E) or \
             _names().code.get(logits.dtype) != gcfg.dtype or \
             logits.stride() != (gcfg.ld or E, 1) and not (
                 (T <= 1 or logits.stride(0) == (gcfg.ld or E)) and
@@ -436,26 +446,28 @@ def route_logits(gcfg: GateConfig, logits, expert_bias, topk_idx, topk_w, scores
     """Experts and weights from given router logits [T, E] (see moe_route_logits); scores: optional
     fp32 [T, E] that receives every expert's score."""
     w, T, E, k, n = "moe_route_logits", gcfg.T, gcfg.E, gcfg.top_k, _names()
+    gpu = _current_gpu(w, "logits", logits)
     _check(lib().moe_route_logits(
         ctypes.byref(gcfg), _expect_logits(w, gcfg, T, E, logits),
-        None if expert_bias is None else _expect(w, "expert_bias", expert_bias, (E,), n.f32),
-        _expect(w, "topk_idx", topk_idx, (T, k), n.i32),
-        _expect(w, "topk_w", topk_w, (T, k), n.f32),
-        None if scores is None else _expect(w, "scores", scores, (T, E), n.f32),
-        _stream_of(stream, logits)), w)
+        None if expert_bias is None else _expect(w, "expert_bias", expert_bias, (E,), n.f32, gpu),
+        _expect(w, "topk_idx", topk_idx, (T, k), n.i32, gpu),
+        _expect(w, "topk_w", topk_w, (T, k), n.f32, gpu),
+        None if scores is None else _expect(w, "scores", scores, (T, E), n.f32, gpu),
+        _stream_on(stream, gpu)), w)
 
 
 def route_logits_backward(gcfg: GateConfig, logits, topk_idx, d_topk_w, d_scores, d_logits,
                           stream=None):
     """d_logits from the gradients of topk_w and scores (either may be None)."""
     w, T, E, k, n = "moe_route_logits_backward", gcfg.T, gcfg.E, gcfg.top_k, _names()
+    gpu = _current_gpu(w, "logits", logits)
     _check(lib().moe_route_logits_backward(
         ctypes.byref(gcfg), _expect_logits(w, gcfg, T, E, logits),
-        _expect(w, "topk_idx", topk_idx, (T, k), n.i32),
-        None if d_topk_w is None else _expect(w, "d_topk_w", d_topk_w, (T, k), n.f32),
-        None if d_scores is None else _expect(w, "d_scores", d_scores, (T, E), n.f32),
-        _expect(w, "d_logits", d_logits, (T, E), logits.dtype),
-        _stream_of(stream, logits)), w)
+        _expect(w, "topk_idx", topk_idx, (T, k), n.i32, gpu),
+        None if d_topk_w is None else _expect(w, "d_topk_w", d_topk_w, (T, k), n.f32, gpu),
+        None if d_scores is None else _expect(w, "d_scores", d_scores, (T, E), n.f32, gpu),
+        _expect(w, "d_logits", d_logits, (T, E), logits.dtype, gpu),
+        _stream_on(stream, gpu)), w)
 
 
 def quantize_rows(x, q, scale, stream=None):
@@ -464,13 +476,14 @@ def quantize_rows(x, q, scale, stream=None):
     w, n = "moe_quantize_rows", _names()
     T, d = x.shape
     step, unit = x.stride()
-    if not x.is_cuda or (d > 1 and unit != 1) or (T > 1 and step < d):
-        raise ValueError(f"{w}: x must be a CUDA tensor with unit stride inside a row and rows at "
-                         f"least {d} apart, not strides {x.stride()} on {x.device}")
+    gpu = _current_gpu(w, "x", x)
+    if (d > 1 and unit != 1) or (T > 1 and step < d):
+        raise ValueError(f"{w}: x must have unit stride inside a row and rows at least {d} apart, not "
+                         f"strides {x.stride()}")
     _check(lib().moe_quantize_rows(T, d, _dtype_code(x, w), x.data_ptr(), step if T > 1 else d,
-                                   _expect(w, "q", q, (T, d), n.i8),
-                                   _expect(w, "scale", scale, (T,), n.f32),
-                                   _stream_of(stream, x)), w)
+                                   _expect(w, "q", q, (T, d), n.i8, gpu),
+                                   _expect(w, "scale", scale, (T,), n.f32, gpu),
+                                   _stream_on(stream, gpu)), w)
 
 
 def quantize_channels(W, stream=None):
@@ -478,11 +491,12 @@ def quantize_channels(W, stream=None):
     [n, N, K], scale fp32 [n, N]), new tensors on W's device."""
     import torch
     n, (K, N) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
-    _expect("moe_quantize_channels", "W", W, tuple(W.shape), torch.bfloat16)
+    gpu = _current_gpu("moe_quantize_channels", "W", W)
+    _expect("moe_quantize_channels", "W", W, tuple(W.shape), torch.bfloat16, gpu)
     q = torch.empty((n, N, K), dtype=torch.int8, device=W.device)
     scale = torch.empty((n, N), dtype=torch.float32, device=W.device)
     _check(lib().moe_quantize_channels(n, K, N, W.data_ptr(), q.data_ptr(), scale.data_ptr(),
-                                       _stream_of(stream, W)), "moe_quantize_channels")
+                                       _stream_on(stream, gpu)), "moe_quantize_channels")
     return q, scale
 
 
@@ -514,26 +528,29 @@ def int8_matmul(q_x, s_x, q_w, s_w, offsets, y, ws, stream=None):
     w, t = "moe_int8_matmul", _names()
     rows, K = q_x.shape
     n, N, _ = q_w.shape
+    gpu = _current_gpu(w, "q_x", q_x)
     _check(lib().moe_int8_matmul(
-        rows, K, N, n, _expect(w, "q_x", q_x, (rows, K), t.i8),
-        _expect(w, "s_x", s_x, (rows,), t.f32), _expect(w, "q_w", q_w, (n, N, K), t.i8),
-        _expect(w, "s_w", s_w, (n, N), t.f32),
-        None if offsets is None else _expect(w, "offsets", offsets, (n + 1,), t.i32),
-        _dtype_code(y, w), _expect(w, "y", y, (rows, N), y.dtype), ws.data_ptr(), ws.numel(),
-        _stream_of(stream, q_x)), w)
+        rows, K, N, n, _expect(w, "q_x", q_x, (rows, K), t.i8, gpu),
+        _expect(w, "s_x", s_x, (rows,), t.f32, gpu), _expect(w, "q_w", q_w, (n, N, K), t.i8, gpu),
+        _expect(w, "s_w", s_w, (n, N), t.f32, gpu),
+        None if offsets is None else _expect(w, "offsets", offsets, (n + 1,), t.i32, gpu),
+        _dtype_code(y, w), _expect(w, "y", y, (rows, N), y.dtype, gpu), ws.data_ptr(), ws.numel(),
+        _stream_on(stream, gpu)), w)
 
 
 def make_int8_weights(gate, up, down, sh_gate=None, sh_up=None, sh_down=None) -> MoeInt8Weights:
-    """From quantize_channels() results (kept alive by the struct)."""
-    mats, t = (gate, up, down, sh_gate, sh_up, sh_down), _names()
+    """From quantize_channels() results (kept alive by the struct), all on one GPU."""
+    mats, t, gpu = (gate, up, down, sh_gate, sh_up, sh_down), _names(), gate[0].get_device()
+    if not gate[0].is_cuda:
+        raise ValueError(f"make_int8_weights: weights on {gate[0].device}")
     for m in mats:
         if m is not None:
             n, N, K = m[0].shape
-            _expect("make_int8_weights", "q", m[0], (n, N, K), t.i8)
-            _expect("make_int8_weights", "scale", m[1], (n, N), t.f32)
+            _expect("make_int8_weights", "q", m[0], (n, N, K), t.i8, gpu)
+            _expect("make_int8_weights", "scale", m[1], (n, N), t.f32, gpu)
     w = MoeInt8Weights(*[MoeInt8Matrix() if m is None else MoeInt8Matrix(_ptr(m[0]), _ptr(m[1]))
                          for m in mats])
-    w._tensors = mats
+    w._tensors, w._gpu = mats, gpu
     w._shapes = tuple(None if m is None else tuple(m[0].shape) for m in mats)
     return w
 
@@ -546,15 +563,17 @@ def grouped_ffn_int8(cfg, x, perm_slot, offsets, topk_w, weights: MoeInt8Weights
     T, d, k, E, f, S = cfg.T, cfg.d, cfg.top_k, cfg.E, cfg.d_ff, cfg.n_shared
     into, back = (E, f, d), (E, d, f)
     want = (into, into, back) + (((S, f, d), (S, f, d), (S, d, f)) if S else ())
-    if weights._shapes[:len(want)] != want:
-        raise ValueError(f"{w}: weights of shapes {weights._shapes} do not fit the configuration")
+    gpu = _current_gpu(w, "x", x)
+    if weights._shapes[:len(want)] != want or weights._gpu != gpu:
+        raise ValueError(f"{w}: weights of shapes {weights._shapes} on cuda:{weights._gpu} do not fit "
+                         f"the configuration on cuda:{gpu}")
     _check(lib().moe_grouped_ffn_int8(
-        ctypes.byref(cfg), _expect(w, "x", x, (T, d), t.bf16),
-        _expect(w, "perm_slot", perm_slot, (T * k,), t.i32),
-        _expect(w, "offsets", offsets, (E + 1,), t.i32),
-        None if topk_w is None else _expect(w, "topk_w", topk_w, (T, k), t.f32),
-        ctypes.byref(weights), _expect(w, "y_slot", y_slot, (T * (k + S), d), t.f16),
-        ws.data_ptr(), ws.numel(), _stream_of(stream, x)), w)
+        ctypes.byref(cfg), _expect(w, "x", x, (T, d), t.bf16, gpu),
+        _expect(w, "perm_slot", perm_slot, (T * k,), t.i32, gpu),
+        _expect(w, "offsets", offsets, (E + 1,), t.i32, gpu),
+        None if topk_w is None else _expect(w, "topk_w", topk_w, (T, k), t.f32, gpu),
+        ctypes.byref(weights), _expect(w, "y_slot", y_slot, (T * (k + S), d), t.f16, gpu),
+        ws.data_ptr(), ws.numel(), _stream_on(stream, gpu)), w)
 
 
 def check_bounded_waits(limit_ns, expired, ws, stream=None):

@@ -68,3 +68,61 @@ def test_row_strides_of_quantize_rows(calls, x, ld):
     M.quantize_rows(OnGpu(x), *rows_out(*x.shape), stream=0)
     (name, args), = calls
     assert name == "moe_quantize_rows" and args[:2] == tuple(x.shape) and args[4] == ld
+
+
+def every_call(at, stream=0, odd=None):
+    """A call of each entry point with its tensors on GPU `at`, but the one named `odd` on the next."""
+    def g(name, *shape, dtype=torch.float32):
+        return OnGpu(torch.zeros(*shape, dtype=dtype), at + (name == odd))
+
+    f16, bf16, i8, i32 = torch.float16, torch.bfloat16, torch.int8, torch.int32
+    gate = M.GateConfig.make(4, 16, 2)
+    cfg = M.MoeConfig.make(8, 128, 4, 2, 64)
+    mats = [(g("q", 4, n, k, dtype=i8), g("scale", 4, n)) for n, k in ((64, 128), (64, 128),
+                                                                      (128, 64))]
+    return {
+        "route_logits": lambda: M.route_logits(
+            gate, g("logits", 4, 16), g("bias", 16), g("idx", 4, 2, dtype=i32), g("w", 4, 2),
+            g("scores", 4, 16), stream=stream),
+        "route_logits_backward": lambda: M.route_logits_backward(
+            gate, g("logits", 4, 16), g("idx", 4, 2, dtype=i32), g("d_w", 4, 2),
+            g("d_scores", 4, 16), g("d_logits", 4, 16), stream=stream),
+        "quantize_rows": lambda: M.quantize_rows(
+            g("x", 4, 64), g("q", 4, 64, dtype=i8), g("scale", 4), stream=stream),
+        "int8_matmul": lambda: M.int8_matmul(
+            g("q_x", 4, 64, dtype=i8), g("s_x", 4), g("q_w", 2, 8, 64, dtype=i8), g("s_w", 2, 8),
+            g("offsets", 3, dtype=i32), g("y", 4, 8), g("ws", 4096, dtype=torch.uint8),
+            stream=stream),
+        "grouped_ffn_int8": lambda: M.grouped_ffn_int8(
+            cfg, g("x", 8, 128, dtype=bf16), g("perm", 16, dtype=i32), g("offsets", 5, dtype=i32),
+            g("w", 8, 2), M.make_int8_weights(*mats), g("y", 16, 128, dtype=f16),
+            g("ws", 4096, dtype=torch.uint8), stream=stream),
+    }
+
+
+TENSORS = [(call, odd) for call, names in (
+    ("route_logits", "logits bias idx w scores"),
+    ("route_logits_backward", "logits idx d_w d_scores d_logits"),
+    ("quantize_rows", "x q scale"),
+    ("int8_matmul", "q_x s_x q_w s_w offsets y"),
+    ("grouped_ffn_int8", "x perm offsets w q scale y")) for odd in names.split()]
+
+
+@pytest.mark.parametrize("call,odd", TENSORS)
+def test_a_tensor_of_another_gpu_is_refused(calls, call, odd):
+    """The launch goes to the current GPU, whose kernels would be given another one's addresses."""
+    every_call(0)[call]()
+    assert [name for name, _ in calls] == ["moe_" + call]
+    with pytest.raises(ValueError):
+        every_call(0, odd=odd)[call]()
+    assert len(calls) == 1
+
+
+@pytest.mark.parametrize("call", sorted({c for c, _ in TENSORS}))
+def test_tensors_of_a_gpu_that_is_not_current_are_refused(calls, monkeypatch, call):
+    with pytest.raises(ValueError):
+        every_call(1)[call]()
+    assert calls == []
+    monkeypatch.setattr(M._names(), "current_device", lambda: 1)
+    every_call(1)[call]()
+    assert len(calls) == 1
