@@ -431,6 +431,14 @@ def _expect(where, name, t, shape, dtype, gpu):
     return t.data_ptr()
 
 
+def _expect_ws(where, ws, gpu):
+    """ws: a tensor whose elements fill their memory on GPU `gpu`. Its address and bytes."""
+    if ws.get_device() != gpu or not ws.is_contiguous():
+        raise ValueError(f"{where}: ws must be a contiguous tensor on cuda:{gpu}, not "
+                         f"{tuple(ws.shape)} (strides {ws.stride()}) on {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _expect_logits(where, gcfg, T, E, logits):
     if logits.shape != (T, E) or \
             _names().code.get(logits.dtype) != gcfg.dtype or \
@@ -534,8 +542,8 @@ def int8_matmul(q_x, s_x, q_w, s_w, offsets, y, ws, stream=None):
         _expect(w, "s_x", s_x, (rows,), t.f32, gpu), _expect(w, "q_w", q_w, (n, N, K), t.i8, gpu),
         _expect(w, "s_w", s_w, (n, N), t.f32, gpu),
         None if offsets is None else _expect(w, "offsets", offsets, (n + 1,), t.i32, gpu),
-        _dtype_code(y, w), _expect(w, "y", y, (rows, N), y.dtype, gpu), ws.data_ptr(), ws.numel(),
-        _stream_on(stream, gpu)), w)
+        _dtype_code(y, w), _expect(w, "y", y, (rows, N), y.dtype, gpu),
+        *_expect_ws(w, ws, gpu), _stream_on(stream, gpu)), w)
 
 
 def make_int8_weights(gate, up, down, sh_gate=None, sh_up=None, sh_down=None) -> MoeInt8Weights:
@@ -573,7 +581,7 @@ def grouped_ffn_int8(cfg, x, perm_slot, offsets, topk_w, weights: MoeInt8Weights
         _expect(w, "offsets", offsets, (E + 1,), t.i32, gpu),
         None if topk_w is None else _expect(w, "topk_w", topk_w, (T, k), t.f32, gpu),
         ctypes.byref(weights), _expect(w, "y_slot", y_slot, (T * (k + S), d), t.f16, gpu),
-        ws.data_ptr(), ws.numel(), _stream_on(stream, gpu)), w)
+        *_expect_ws(w, ws, gpu), _stream_on(stream, gpu)), w)
 
 
 def check_bounded_waits(limit_ns, expired, ws, stream=None):

@@ -126,3 +126,26 @@ def test_tensors_of_a_gpu_that_is_not_current_are_refused(calls, monkeypatch, ca
     monkeypatch.setattr(M._names(), "current_device", lambda: 1)
     every_call(1)[call]()
     assert len(calls) == 1
+
+
+@pytest.mark.parametrize("ws", [
+    torch.zeros(4096, dtype=torch.uint8), OnGpu(torch.zeros(4096, dtype=torch.uint8), 1),
+    OnGpu(torch.zeros(1, dtype=torch.uint8).expand(4096)),
+    OnGpu(torch.zeros(8192, dtype=torch.uint8)[::2])])
+@pytest.mark.parametrize("call", ["int8_matmul", "grouped_ffn_int8"])
+def test_workspaces_that_are_not_bytes_in_a_row_there_are_refused(calls, monkeypatch, call, ws):
+    """The library sees an address and a length: host memory, another GPU's, or a view of fewer bytes than
+    its elements would be written past."""
+    entry = getattr(M, call)
+    monkeypatch.setattr(M, call, lambda *a, **kw: entry(*a[:-1], ws, **kw))
+    with pytest.raises(ValueError):
+        every_call(0)[call]()
+    assert calls == []
+
+
+def test_workspaces_of_any_element_type_count_in_bytes(calls, monkeypatch):
+    entry = M.int8_matmul
+    ws = OnGpu(torch.zeros(1024))
+    monkeypatch.setattr(M, "int8_matmul", lambda *a, **kw: entry(*a[:-1], ws, **kw))
+    every_call(0)["int8_matmul"]()
+    assert calls[0][1][11:13] == (ws.data_ptr(), 4096)
