@@ -32,6 +32,12 @@ __device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& h
   asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
 }
 
+// Whether offsets r0 and r1 bound a segment of the rows [0, rows). One that they do not is empty and reported
+// by the product (MOE_DEVFAULT_BAD_TILE); the others are computed all the same.
+__device__ __forceinline__ bool segment_ok(int r0, int r1, int rows) {
+  return r0 >= 0 && r1 >= r0 && r1 <= rows;
+}
+
 // One grouped product. Segment e < n_mat holds positions [offsets[e], offsets[e + 1]) (offsets
 // NULL: all `rows`); with shared experts, segment n_mat + s is positions
 // [rows + s * T, rows + (s + 1) * T). The activations' codes, in fp16 (exact) or 8 bits, have row p for

@@ -79,7 +79,7 @@ __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int 
       if (g.offsets != nullptr) {
         r0 = bound[p][0];
         r1 = bound[p][1];
-        if (r0 < 0 || r1 < r0 || r1 > g.rows) {
+        if (!segment_ok(r0, r1, g.rows)) {
           atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
           r0 = r1 = 0;
         }

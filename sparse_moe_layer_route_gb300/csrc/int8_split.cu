@@ -3,6 +3,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 #include <cstring>
 #include <type_traits>
@@ -25,19 +26,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_splits_kernel(const float* 
   const int row = blockIdx.x;
   int seg = 0;
   if (g.offsets != nullptr) {
-    // the last segment that begins at or before the row and reaches it (bad offsets were reported by
-    // the product, which left their rows out)
-    int lo = 0, hi = g.n_mat;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (g.offsets[mid] <= row)
-        lo = mid;
-      else
-        hi = mid;
+    // the first sound segment that holds the row; offsets may not ascend, so every one is looked at
+    __shared__ int first;
+    if (threadIdx.x == 0) first = INT_MAX;
+    __syncthreads();
+    for (int e = threadIdx.x; e < g.n_mat; e += kJoinThreads) {
+      const int r0 = g.offsets[e], r1 = g.offsets[e + 1];
+      if (segment_ok(r0, r1, g.rows) && row >= r0 && row < r1) atomicMin(&first, e);
     }
-    seg = lo;
-    const int r0 = g.offsets[seg], r1 = g.offsets[seg + 1];
-    if (r0 < 0 || r1 > g.rows || row < r0 || row >= r1) return;
+    __syncthreads();
+    seg = first;
+    if (seg == INT_MAX) return;
   }
   const int n = (blockIdx.y * kJoinThreads + threadIdx.x) * 4;
   if (n >= g.N) return;

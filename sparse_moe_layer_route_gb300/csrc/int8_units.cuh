@@ -58,7 +58,7 @@ __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, i
     if (g.offsets != nullptr) {
       r0 = g.offsets[i];
       r1 = g.offsets[i + 1];
-      if (r0 < 0 || r1 < r0 || r1 > g.rows) {
+      if (!segment_ok(r0, r1, g.rows)) {
         atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
         r0 = r1 = 0;
       }

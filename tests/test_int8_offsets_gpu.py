@@ -1,0 +1,46 @@
+"""Offsets that descend or leave [0, rows]: the segments they bound are empty and reported, every other
+one is computed, on each path of the 8-bit products.
+
+Codes are at most 60 in magnitude and K at most 4096, so sums stay below 2^24 and are exact; scales are
+1, so outputs are those sums: compared for equality.
+"""
+import pytest
+import torch
+
+import sparse_moe_layer_route_gb300 as M
+
+
+def owners(off, rows):
+    """The segment of each row (-1: none): the first sound one that holds it."""
+    own = [-1] * rows
+    for e in reversed(range(len(off) - 1)):
+        if 0 <= off[e] <= off[e + 1] <= rows:
+            own[off[e]:off[e + 1]] = [e] * (off[e + 1] - off[e])
+    return torch.tensor(own)
+
+
+def check(rows, K, N, off):
+    g, n = torch.Generator().manual_seed(rows + K), len(off) - 1
+    qx, qw = (torch.randint(-60, 61, s, generator=g, dtype=torch.int8).cuda()
+              for s in ((rows, K), (n, N, K)))
+    ws = M.alloc_int8_workspace(M.int8_matmul_workspace_size(rows, K, N, n))
+    y = torch.full((rows, N), float("nan"), device="cuda")
+    M.int8_matmul(qx, torch.ones(rows, device="cuda"), qw, torch.ones(n, N, device="cuda"),
+                  torch.tensor(off, dtype=torch.int32, device="cuda"), y, ws)
+    assert M.device_status(ws) == M.DEVFAULT_BAD_TILE
+    own = owners(off, rows)
+    for e in range(-1, n):
+        r = torch.nonzero(own == e)[:, 0].cuda()
+        if e < 0:
+            assert torch.isnan(y[r]).all()
+        else:
+            assert torch.equal(y[r].double(), qx[r].double() @ qw[e].double().T), e
+
+
+# three paths: integer dot products, tensor cores, tensor cores with K in pieces
+@pytest.mark.gpu
+@pytest.mark.parametrize("off", [[0, 500, 50, 150], [0, 30, 200, 40, 150], [-7, 20, 90, 150],
+                                 [0, 60, 140, 151], [0, 150, -1, 0]])
+@pytest.mark.parametrize("K,N", [(4096, 2048), (64, 300), (4096, 6500)])
+def test_sound_segments_among_unsound_ones(off, K, N):
+    check(150, K, N, off)
