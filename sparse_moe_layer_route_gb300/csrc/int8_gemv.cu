@@ -52,8 +52,8 @@ __device__ __forceinline__ void store_one(void* out, long long at, float y) {
     static_cast<__half*>(out)[at] = __float2half(y);
 }
 
-// Row tile `tile` (R rows) of the segments, counted segment by segment: found by the CTA's first warp,
-// 32 segments at a time. seg -1: past the last tile.
+// Row tile `tile` (R rows) of the segments, counted segment by segment: found by every warp, 32 segments at a
+// time. seg -1: past the last tile. Unsound segments are reported wherever the tile is.
 template <int R>
 __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int tile, int lane) {
   constexpr int kParts = (kMaxSegs + 31) / 32;
@@ -68,6 +68,14 @@ __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int 
       bound[p][1] = g.offsets[s + 1];
     }
   }
+  bool bad = false;
+#pragma unroll
+  for (int p = 0; p < kParts; ++p)
+    if (!segment_ok(bound[p][0], bound[p][1], g.rows)) {
+      bad = true;
+      bound[p][0] = bound[p][1] = 0;
+    }
+  if (bad) atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
   int before = 0;
 #pragma unroll
   for (int p = 0; p < kParts; ++p) {
@@ -79,10 +87,6 @@ __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int 
       if (g.offsets != nullptr) {
         r0 = bound[p][0];
         r1 = bound[p][1];
-        if (!segment_ok(r0, r1, g.rows)) {
-          atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
-          r0 = r1 = 0;
-        }
       }
       nr = r1 - r0;
     } else if (s < n) {

@@ -44,3 +44,13 @@ def check(rows, K, N, off):
 @pytest.mark.parametrize("K,N", [(4096, 2048), (64, 300), (4096, 6500)])
 def test_sound_segments_among_unsound_ones(off, K, N):
     check(150, K, N, off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,n,at,value", [(1, 64, 50, -3), (1, 64, 63, 9), (3, 256, 256, 2),
+                                             (8, 33, 32, 9), (300, 200, 150, 301)])
+def test_unsound_segments_far_behind_the_rows_are_reported(rows, n, at, value):
+    """All rows in the first segment, and a bad offset among many segments without a row."""
+    off = [0] + [rows] * n
+    off[at] = value
+    check(rows, 64, 100, off)
