@@ -467,7 +467,8 @@ moe_status moe_quantize_channels(int32_t n_mat, int32_t K, int32_t N, const uint
 /* y[r, n] = (sum_k q_x[r, k] * q_w[e, n, k]) * s_x[r] * s_w[e, n] for the rows r of segment e,
  * offsets[e] <= r < offsets[e + 1] (offsets: int32 [n_mat + 1] on the device, ascending from 0 to at
  * most rows; NULL: n_mat is 1 and owns every row). Rows past offsets[n_mat] are not written. Offsets
- * that descend or leave [0, rows] make that segment empty and set MOE_DEVFAULT_BAD_TILE.
+ * that descend or leave [0, rows] make that segment empty and set MOE_DEVFAULT_BAD_TILE; the other
+ * segments are computed, and of those that share a row (possible only then) the first has it.
  *   q_x [rows, K], q_w [n_mat, N, K] 16-byte aligned; s_x [rows], s_w [n_mat, N] fp32; y [rows, N] of
  *   y_dtype (moe_dtype; fp16 becomes infinite past its range), aligned to its element.
  *   The sum is exact while every partial sum stays below 2^24 in magnitude, and within fp32's

@@ -33,7 +33,8 @@ __device__ __forceinline__ void widen4(uint32_t codes, uint32_t& lo, uint32_t& h
 }
 
 // Whether offsets r0 and r1 bound a segment of the rows [0, rows). One that they do not is empty and reported
-// by the product (MOE_DEVFAULT_BAD_TILE); the others are computed all the same.
+// by the product (MOE_DEVFAULT_BAD_TILE); the others are computed all the same, and where they share rows (only
+// an unsound segment between two sound ones lets them) the first of them has those rows.
 __device__ __forceinline__ bool segment_ok(int r0, int r1, int rows) {
   return r0 >= 0 && r1 >= r0 && r1 <= rows;
 }

@@ -37,6 +37,7 @@ struct Unit {
   int row0;     // first position
   int rows;     // 1..the segment's tile height
   int brow0;    // first row of the activations
+  bool mixed;   // some segments are unsound: others may share rows
 };
 
 // Row tiles before each segment (first[n_segs] = all of them) and the segments' first positions.
@@ -46,6 +47,7 @@ struct SegTable {
   int rows[kMaxSegs];
   int height[kMaxSegs];  // rows of a row tile (the last one may be lower)
   int warp_tot[32];
+  int mixed;
 };
 
 // Called by every thread of a CTA (of at least kMaxSegs). NT: the tallest tile.
@@ -53,6 +55,7 @@ __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, i
   const int n = g.n_mat + g.S, i = threadIdx.x;
   const int lane = i & 31, warp = i >> 5;
   int r0 = 0, nr = 0;
+  bool bad = false;
   if (i < g.n_mat) {
     int r1 = g.rows;
     if (g.offsets != nullptr) {
@@ -60,6 +63,7 @@ __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, i
       r1 = g.offsets[i + 1];
       if (!segment_ok(r0, r1, g.rows)) {
         atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
+        bad = true;
         r0 = r1 = 0;
       }
     }
@@ -77,7 +81,8 @@ __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, i
     if (lane >= o) v += u;
   }
   if (lane == 31) t.warp_tot[warp] = v;
-  __syncthreads();
+  const int mixed = __syncthreads_or(bad);
+  if (i == 0) t.mixed = mixed;
   int base = 0;
   for (int w = 0; w < warp; ++w) base += t.warp_tot[w];
   if (i < n) {
@@ -115,16 +120,29 @@ __device__ __forceinline__ Unit find_unit(const SegTable& t, const Int8Gemm& g, 
   u.row0 = t.row0[lo] + off;
   u.rows = min(t.height[lo], t.rows[lo] - off);
   u.brow0 = X_SHARED && lo >= g.n_mat ? g.rows + off : u.row0;
+  u.mixed = t.mixed != 0;
   return u;
 }
 
-// The output row and the row scale of position row0 + r of a unit: -1 past the unit's rows or where the slot is out of range.
+// Whether a sound segment before `seg` holds the row as well.
+__device__ __forceinline__ bool row_taken(const int32_t* offsets, int rows, int seg, int row) {
+#pragma unroll 1
+  for (int e = 0; e < seg; ++e) {
+    const int r0 = offsets[e], r1 = offsets[e + 1];
+    if (segment_ok(r0, r1, rows) && row >= r0 && row < r1) return true;
+  }
+  return false;
+}
+
+// The output row and the row scale of position row0 + r of a unit: -1 past the unit's rows, where another
+// segment has the row, or where the slot is out of range.
 template <int PASS>
 __device__ __forceinline__ void unit_row(const Int8Gemm& g, const Unit& u, int r, int& orow,
                                          float& sx) {
   sx = 0.0f;
   orow = -1;
   if (r >= u.rows) return;
+  if (u.mixed && u.seg < g.n_mat && row_taken(g.offsets, g.rows, u.seg, u.row0 + r)) return;
   sx = PASS == kInt8Partial ? 1.0f : g.sx[u.brow0 + r];
   orow = u.row0 + r;
   if (PASS == kInt8Slot && u.seg < g.n_mat) {

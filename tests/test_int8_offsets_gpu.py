@@ -54,3 +54,14 @@ def test_unsound_segments_far_behind_the_rows_are_reported(rows, n, at, value):
     off = [0] + [rows] * n
     off[at] = value
     check(rows, 64, 100, off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,off", [
+    (20, [0, 19, 0, 20]), (20, [8, 16, 0, 20, 4, 12]), (1500, [0, 1400, 0, 1500]),
+    (1500, [700, 900, 100, 1500, 0, 1300])])
+@pytest.mark.parametrize("K,N", [(64, 64), (3008, 600), (336, 5300)])
+def test_rows_of_two_segments_have_the_first_ones_product(rows, off, K, N):
+    """Sound segments between which offsets descend may share rows, and together hold more tiles than any
+    that ascend."""
+    check(rows, K, N, off)
