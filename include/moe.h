@@ -486,7 +486,8 @@ moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, co
  * moe_quantize_rows (H from fp32). moe_combine (MOE_Y_F16) reads y_slot. ws: a workspace of
  * moe_grouped_ffn_int8_workspace_size bytes cleared once by moe_workspace_init; its status word is
  * read by moe_device_status (MOE_DEVFAULT_FP16_RANGE: a slot value was past fp16's range and was
- * clamped; MOE_DEVFAULT_BAD_TILE: offsets or perm_slot were inconsistent). */
+ * clamped; MOE_DEVFAULT_BAD_TILE: offsets or perm_slot were inconsistent: experts whose offsets descend,
+ * leave [0, T*k] or pass offsets[E], and positions whose slot is out of range, write nothing). */
 moe_status moe_grouped_ffn_int8_workspace_size(const moe_config* cfg, size_t* bytes);
 moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const int32_t* perm_slot,
                                 const int32_t* offsets, const float* topk_w,

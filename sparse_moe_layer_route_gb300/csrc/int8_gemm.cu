@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     ptx::tmem_relinquish_cg2();
   }
   griddep_wait();  // everything above touched only shared memory, TMEM and parameters
-  build_segments(segs, g, min(g.tile_rows, kNT));
+  build_segments<PASS>(segs, g, min(g.tile_rows, kNT));
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // the peer's barriers are initialised

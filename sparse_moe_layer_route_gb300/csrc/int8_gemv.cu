@@ -56,11 +56,13 @@ __device__ __forceinline__ void store_one(void* out, long long at, float y) {
 // time. seg -1: past the last tile. unsound: some segment up to the tile's is, or with `all` any of them (the
 // search for a tile ends where it is found; only the last tile's CTAs look at every segment: when each CTA did,
 // 84 rows of [1476 x 1056] took 9.9 us, not 8.3).
-template <int R>
-__device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int tile, int lane,
-                                          bool all, bool& unsound) {
+template <int PASS, int R>
+__device__ __forceinline__ Unit find_tile(const Int8Gemm& g, int tile, int lane, bool all,
+                                          bool& unsound) {
+  constexpr bool X_SHARED = PASS == kInt8SwiGLU;  // all shared experts read the same rows
   constexpr int kParts = (kMaxSegs + 31) / 32;
   const int n = g.n_mat + g.S;
+  const int end = rows_end<PASS>(g);
   int bound[kParts][2];  // every load in flight before the first is needed
 #pragma unroll
   for (int p = 0; p < kParts; ++p) {
@@ -74,7 +76,8 @@ __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int 
   bool bad = false;
   if (all) {
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) bad |= !segment_ok(bound[p][0], bound[p][1], g.rows);
+    for (int p = 0; p < kParts; ++p)
+      bad |= p * 32 + lane < g.n_mat && !segment_ok(bound[p][0], bound[p][1], end);
   }
   int before = 0;
 #pragma unroll
@@ -87,7 +90,7 @@ __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int 
       if (g.offsets != nullptr) {
         r0 = bound[p][0];
         r1 = bound[p][1];
-        if (!segment_ok(r0, r1, g.rows)) {
+        if (!segment_ok(r0, r1, end)) {
           bad = true;
           r0 = r1 = 0;
         }
@@ -114,7 +117,7 @@ __device__ __forceinline__ Unit find_tile(const Int8Gemm& g, bool x_shared, int 
       u.ct = 0;
       u.row0 = __shfl_sync(0xffffffffu, r0, src) + off;
       u.rows = min(R, __shfl_sync(0xffffffffu, nr, src) - off);
-      u.brow0 = x_shared && u.seg >= g.n_mat ? g.rows + off : u.row0;
+      u.brow0 = X_SHARED && u.seg >= g.n_mat ? g.rows + off : u.row0;
       if (bad) atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
       unsound = __any_sync(0xffffffffu, bad);
       u.mixed = unsound;
@@ -157,7 +160,7 @@ __device__ __noinline__ void tiles_past_grid(const Int8Gemm& g, int tile, int ch
   constexpr bool GLU = PASS == kInt8SwiGLU;
   bool unsound;
   for (;;) {
-    const Unit u = find_tile<R>(g, GLU, ++tile, lane, true, unsound);
+    const Unit u = find_tile<PASS, R>(g, ++tile, lane, true, unsound);
     if (u.seg < 0) return;
     const bool sh = u.seg >= g.n_mat;
     const long long ex = sh ? u.seg - g.n_mat : u.seg;
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? kCtasPerSm8 : kCtasPerSm)
   // the last tile's CTAs look at every segment, and take the tiles past the grid where there are any
   const bool last = tile == tiles - 1;
   bool unsound;
-  const Unit u = find_tile<R>(g, GLU, tile, lane, last, unsound);  // every warp: no barrier
+  const Unit u = find_tile<PASS, R>(g, tile, lane, last, unsound);  // every warp: no barrier
   if (u.seg < 0) return;
   const int ch0 = (cta * (kThreads / 32) + warp) * CH;
   if (ch0 >= g.N) return;

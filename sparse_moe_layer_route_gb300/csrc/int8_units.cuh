@@ -50,7 +50,15 @@ struct SegTable {
   int mixed;
 };
 
+// Rows that a segment can have. The experts' positions past the last offset are those of dropped slots: no codes
+// are written there, so an expert that reaches past it is unsound.
+template <int PASS>
+__device__ __forceinline__ int rows_end(const Int8Gemm& g) {
+  return PASS == kInt8SwiGLU || PASS == kInt8Slot ? min(g.rows, g.offsets[g.n_mat]) : g.rows;
+}
+
 // Called by every thread of a CTA (of at least kMaxSegs). NT: the tallest tile.
+template <int PASS>
 __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, int NT) {
   const int n = g.n_mat + g.S, i = threadIdx.x;
   const int lane = i & 31, warp = i >> 5;
@@ -61,7 +69,7 @@ __device__ __forceinline__ void build_segments(SegTable& t, const Int8Gemm& g, i
     if (g.offsets != nullptr) {
       r0 = g.offsets[i];
       r1 = g.offsets[i + 1];
-      if (!segment_ok(r0, r1, g.rows)) {
+      if (!segment_ok(r0, r1, rows_end<PASS>(g))) {
         atomicOr(g.status, MOE_DEVFAULT_BAD_TILE);
         bad = true;
         r0 = r1 = 0;
@@ -125,11 +133,13 @@ __device__ __forceinline__ Unit find_unit(const SegTable& t, const Int8Gemm& g, 
 }
 
 // Whether a sound segment before `seg` holds the row as well.
-__device__ __forceinline__ bool row_taken(const int32_t* offsets, int rows, int seg, int row) {
+template <int PASS>
+__device__ __forceinline__ bool row_taken(const Int8Gemm& g, int seg, int row) {
+  const int end = rows_end<PASS>(g);
 #pragma unroll 1
   for (int e = 0; e < seg; ++e) {
-    const int r0 = offsets[e], r1 = offsets[e + 1];
-    if (segment_ok(r0, r1, rows) && row >= r0 && row < r1) return true;
+    const int r0 = g.offsets[e], r1 = g.offsets[e + 1];
+    if (segment_ok(r0, r1, end) && row >= r0 && row < r1) return true;
   }
   return false;
 }
@@ -142,7 +152,7 @@ __device__ __forceinline__ void unit_row(const Int8Gemm& g, const Unit& u, int r
   sx = 0.0f;
   orow = -1;
   if (r >= u.rows) return;
-  if (u.mixed && u.seg < g.n_mat && row_taken(g.offsets, g.rows, u.seg, u.row0 + r)) return;
+  if (u.mixed && u.seg < g.n_mat && row_taken<PASS>(g, u.seg, u.row0 + r)) return;
   sx = PASS == kInt8Partial ? 1.0f : g.sx[u.brow0 + r];
   orow = u.row0 + r;
   if (PASS == kInt8Slot && u.seg < g.n_mat) {

@@ -65,3 +65,44 @@ def test_rows_of_two_segments_have_the_first_ones_product(rows, off, K, N):
     """Sound segments between which offsets descend may share rows, and together hold more tiles than any
     that ascend."""
     check(rows, K, N, off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,f", [(8, 128, 64), (600, 512, 384)])
+@pytest.mark.parametrize("last", [lambda off: off[-2] - 3, lambda off: off[-3] - 1, lambda off: -1,
+                                  lambda off: off[-1] + 10])
+def test_experts_whose_last_offset_does_not_hold_them(T, d, f, last):
+    """Positions past the last offset have no rows (they are those of dropped slots): an expert that
+    reaches past it is empty and reported, and nothing is computed from what the workspace holds there."""
+    E, k, g = 6, 2, torch.Generator().manual_seed(T)
+
+    def w(K, N):
+        return M.quantize_channels((torch.randn(E, K, N, generator=g) / K ** 0.5).bfloat16().cuda())
+
+    cfg = M.MoeConfig.make(T, d, E, k, f)
+    weights = M.make_int8_weights(w(d, f), w(d, f), w(f, d))
+    x = torch.randn(T, d, generator=g).bfloat16().cuda()
+    off = [T * k * e // E for e in range(E + 1)]
+    perm = torch.randperm(T * k, generator=g).int().cuda()
+    ws = M.alloc_int8_workspace(M.grouped_ffn_int8_workspace_size(cfg))
+    outs = []
+    for offsets in (off, off[:-1] + [last(off)]):
+        y = torch.full((T * k, d), float("nan"), dtype=torch.float16, device="cuda")
+        M.grouped_ffn_int8(cfg, x, perm, torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                           None, weights, y, ws)
+        outs.append((y, M.device_status(ws)))
+        x = -2 * x                # what the workspace holds of the first call is not the second one's
+    (first, status), (y, bad) = outs
+    assert status == 0 and bad == M.DEVFAULT_BAD_TILE and not torch.isnan(first).any()
+    x = x / 4
+    whole = torch.empty_like(y)
+    M.grouped_ffn_int8(cfg, -2 * x, perm, torch.tensor(off, dtype=torch.int32, device="cuda"), None,
+                       weights, whole, ws)
+    end = min(offsets[-1], T * k)
+    for e in range(E):
+        slot = perm[off[e]:off[e + 1]].long()
+        sound = offsets[e] <= offsets[e + 1] <= T * k and offsets[e + 1] <= end
+        if sound:
+            assert torch.equal(y[slot], whole[slot]), e
+        else:
+            assert torch.isnan(y[slot]).all(), e
