@@ -41,7 +41,8 @@ __device__ __forceinline__ bool segment_ok(int r0, int r1, int rows) {
 
 // One grouped product. Segment e < n_mat holds positions [offsets[e], offsets[e + 1]) (offsets
 // NULL: all `rows`); with shared experts, segment n_mat + s is positions
-// [rows + s * T, rows + (s + 1) * T). The activations' codes, in fp16 (exact) or 8 bits, have row p for
+// [rows + s * T, rows + (s + 1) * T). A sum takes the two scales one after the other: their product may be past
+// fp32's range where the result is not. The activations' codes, in fp16 (exact) or 8 bits, have row p for
 // position p, except that the SwiGLU pass's shared experts all read rows [rows, rows + T).
 struct Int8Gemm {
   const uint16_t* xq;      // [x_rows, K] fp16 (tensor cores)

@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             uint8_t* buf = stage_out + sb * kInt8StepBytes;
 #pragma unroll
             for (int j = 0; j < P::kCols; ++j) {
-              const float y = __uint_as_float(v[j0 + j]) * (sx[j0 + j] * wc);
+              const float y = __uint_as_float(v[j0 + j]) * sx[j0 + j] * wc;
               P::put(buf, j, chl, y);
               if (PASS == kInt8Slot && ((rows_on >> (j0 + j)) & 1u))
                 clamp = max(clamp, mag_bits(y));

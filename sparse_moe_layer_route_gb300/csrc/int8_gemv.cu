@@ -143,8 +143,8 @@ __device__ __forceinline__ bool finish(const Int8Gemm& g, const Unit& u, bool sh
     unit_row<PASS>(g, u, r, orow, sx);
     if (orow >= 0) {
       const long long at = (long long)orow * g.N + ch;
-      float y = sum * (sx * (sh ? g.sh_sw : g.sw)[ex * g.N + ch]);
-      if (PASS == kInt8SwiGLU) y = swiglu(y, sum2 * (sx * (sh ? g.sh_sw2 : g.sw2)[ex * g.N + ch]));
+      float y = sum * sx * (sh ? g.sh_sw : g.sw)[ex * g.N + ch];
+      if (PASS == kInt8SwiGLU) y = swiglu(y, sum2 * sx * (sh ? g.sh_sw2 : g.sw2)[ex * g.N + ch]);
       store_one<OUT, PASS == kInt8Slot>(g.out, at, y);
       clamped = PASS == kInt8Slot && mag_bits(y) >= kInt8F16Clamp;
     }

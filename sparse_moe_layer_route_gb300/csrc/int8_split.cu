@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_splits_kernel(const float* 
   YT y[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const float f = sum[c] * (sx * scale[c]);
+    const float f = sum[c] * sx * scale[c];
     if constexpr (sizeof(YT) == 4)
       y[c] = f;
     else if constexpr (std::is_same<YT, __nv_bfloat16>::value)
