@@ -472,7 +472,9 @@ moe_status moe_quantize_channels(int32_t n_mat, int32_t K, int32_t N, const uint
  *   q_x [rows, K], q_w [n_mat, N, K] 16-byte aligned; s_x [rows], s_w [n_mat, N] fp32; y [rows, N] of
  *   y_dtype (moe_dtype; fp16 becomes infinite past its range), aligned to its element.
  *   The sum is exact while every partial sum stays below 2^24 in magnitude, and within fp32's
- *   rounding past that. Limits: 1 <= n_mat <= 256; K a multiple of 16, K <= 65536; 1 <= N < 2^27. */
+ *   rounding past that. Limits: 1 <= n_mat <= 256; K a multiple of 16, K <= 65536; 1 <= N < 2^27.
+ * ws: as many bytes as moe_int8_matmul_workspace_size says for these K, N and n_mat and this number of rows
+ * or any larger one. */
 moe_status moe_int8_matmul_workspace_size(int32_t rows, int32_t K, int32_t N, int32_t n_mat,
                                           size_t* bytes);
 moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, const int8_t* q_x,

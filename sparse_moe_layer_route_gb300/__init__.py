@@ -509,6 +509,7 @@ def quantize_channels(W, stream=None):
 
 
 def int8_matmul_workspace_size(rows, K, N, n_mat) -> int:
+    """Bytes that products of up to `rows` rows need."""
     n = ctypes.c_size_t(0)
     _check(lib().moe_int8_matmul_workspace_size(rows, K, N, n_mat, ctypes.byref(n)),
            "moe_int8_matmul_workspace_size")

@@ -79,6 +79,8 @@ cudaError_t launch_int8_gemv(Int8Pass pass, const Int8Gemm& g, int most_rows, cu
 // matrix pass of this shape; and that product: partial sums to `part` (int8_splits() * rows * int8_part_cols(N) floats),
 // then their sums, scaled, to g.out.
 int int8_splits(long long rows, int K, int N, int n_mat);
+// The largest number of rows with the pieces of this one (more rows never have more).
+long long int8_splits_end(long long rows, int n_mat);
 // Floats of a row of partial sums: rows begin on 16 bytes whatever N, so they are stored in 16-byte pieces.
 __host__ __device__ inline int int8_part_cols(int N) { return (N + 3) / 4 * 4; }
 constexpr int kInt8StageK = 128;  // k per shared-memory stage

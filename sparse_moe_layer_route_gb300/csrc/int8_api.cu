@@ -1,6 +1,7 @@
 // Entry points of the 8-bit weights and activations (declarations and contracts: include/moe.h):
 // validation, workspace carving and launch sequencing.
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cstdint>
 
 #include "int8.cuh"
@@ -46,6 +47,9 @@ size_t matmul_part(int32_t rows, int32_t K) {
 size_t matmul_part_bytes(int32_t rows, int32_t K, int32_t N, int32_t n_mat) {
   const int splits = few_rows(rows, K, N) ? 1 : int8_splits(rows, K, N, n_mat);
   return splits > 1 ? 4ull * splits * rows * int8_part_cols(N) : 0;
+}
+size_t matmul_need(int32_t rows, int32_t K, int32_t N, int32_t n_mat) {
+  return matmul_part(rows, K) + matmul_part_bytes(rows, K, N, n_mat);
 }
 
 // Buffers of one FFN call.
@@ -111,7 +115,14 @@ moe_status moe_int8_matmul_workspace_size(int32_t rows, int32_t K, int32_t N, in
   const moe_status r = check_matmul(rows, K, N, n_mat);
   if (r != MOE_OK) return r;
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-  *bytes = matmul_part(rows, K) + matmul_part_bytes(rows, K, N, n_mat);
+  // the most that any number of rows up to this one needs: fewer may have more pieces of K
+  size_t most = matmul_need(rows, K, N, n_mat);
+  for (long long r = 0; r < rows; ++r) {
+    r = int8_splits_end(r, n_mat);
+    if (r >= rows || int8_splits(r, K, N, n_mat) == 1) break;
+    most = std::max(most, matmul_need((int32_t)r, K, N, n_mat));
+  }
+  *bytes = most;
   return MOE_OK;
 }
 
@@ -127,9 +138,7 @@ moe_status moe_int8_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat, co
   if (!aligned(q_x, 16) || !aligned(q_w, 16) || !aligned(s_x, 4) || !aligned(s_w, 4) ||
       !aligned(offsets, 4) || !aligned(y, dtype_bytes(y_dtype)))
     return MOE_ERR_INVALID_ARG;
-  size_t need = 0;
-  moe_int8_matmul_workspace_size(rows, K, N, n_mat, &need);
-  if ((r = check_ws(ws, ws_bytes, need)) != MOE_OK) return r;
+  if ((r = check_ws(ws, ws_bytes, matmul_need(rows, K, N, n_mat))) != MOE_OK) return r;
   const cudaStream_t st = (cudaStream_t)stream;
   Int8Gemm g = {};
   g.x_rows = rows;

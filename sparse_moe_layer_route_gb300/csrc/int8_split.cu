@@ -100,14 +100,25 @@ cudaError_t launch_join(const float* part, const Int8Gemm& g, cudaStream_t st) {
 
 }  // namespace
 
+namespace {
+long long tile_rows(long long mean) { return mean <= kInt8Mean64 ? 64 : mean <= kInt8Mean128 ? 128 : 192; }
+}  // namespace
+
 int int8_splits(long long rows, int K, int N, int n_mat) {
-  const long long mean = rows / n_mat;
-  const long long at_once = 76;  // units that run at the same time, one on each pair of CTAs
-  const long long tile = mean <= kInt8Mean64 ? 64 : mean <= kInt8Mean128 ? 128 : 192;
+  const long long mean = rows / n_mat, tile = tile_rows(mean);
+  // units that run at the same time, one on each pair of GB300's 152 SMs: a constant, as the size of a workspace
+  // depends on it and may be asked for where there is no GPU
+  const long long at_once = 76;
   const long long units = std::max(1ll, (mean + tile - 1) / tile) * n_mat * ((N + 255) / 256);
   if (units * 2 > at_once || N > 65535 * 4 * kJoinThreads) return 1;
   // at least four 128-k steps a piece: shorter ones spend their time on filling the pipeline
   return (int)std::max(1ll, std::min(at_once / units, (long long)(K / kInt8StageK / 4)));
+}
+
+long long int8_splits_end(long long rows, int n_mat) {
+  const long long mean = rows / n_mat, tile = tile_rows(mean);
+  const long long end = tile == 64 ? kInt8Mean64 : tile == 128 ? kInt8Mean128 : (mean + 191) / 192 * 192;
+  return (end + 1) * n_mat - 1;
 }
 
 cudaError_t launch_int8_split(const Int8Gemm& g, float* part, cudaStream_t st) {
