@@ -21,7 +21,10 @@ constexpr size_t kHead = 512;  // status word and counter block, as in every wor
 //   64 + 2 experts of [2048 x 1408], 6 a token, 12 tokens 88 against 88, 16 tokens 101 against 93; of
 //   small layers, 32 tokens, 60 M multiply-adds, 18 against 22, and 64 tokens, 100 M, 22 against 22.
 bool few_rows(int rows, int K, int N) { return rows <= 8 || (double)rows * K * N <= 4e8; }
-bool few_tokens(const Shape& s) { return s.T <= 12 || 3.0 * s.rows * s.d * s.f <= 1e8; }
+// Sums of up to 2^17 products of activations' and weights' codes (127 * 128) stay in 32 bits.
+bool few_tokens(const Shape& s) {
+  return s.d <= 131072 && s.f <= 131072 && (s.T <= 12 || 3.0 * s.rows * s.d * s.f <= 1e8);
+}
 
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 int dtype_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
