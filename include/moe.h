@@ -454,13 +454,13 @@ typedef struct {
 /* Rows of x [T, d] (dtype: moe_dtype; row stride ld elements, 0: d) to 8 bits: scale[t] =
  * max |x[t]| * fl(1 / 127), q[t, j] = clamp(rint(x[t, j] / scale[t]), -127, 127), rint to nearest even, all in
  * fp32. A zero row has scale 0 and q 0. A row with a NaN or an infinity has that as its scale (NaN
- * before infinity), so products with it are not finite either. q [T, d] contiguous. 1 <= d. x aligned
- * to its element; rows of 16-byte pieces (pointers and strides) move faster. */
+ * before infinity), so products with it are not finite either. q [T, d] contiguous. 1 <= d < 2^31 - 1023.
+ * x aligned to its element; rows of 16-byte pieces (pointers and strides) move faster. */
 moe_status moe_quantize_rows(int32_t T, int32_t d, int32_t dtype, const void* x, int64_t ld,
                              int8_t* q, float* scale, moe_stream_t stream);
 
 /* One-time weight preparation: W [n_mat, K, N] bf16 (this library's weight layout) to q [n_mat, N, K]
- * and scale [n_mat, N], by the same rule over the K weights of each output channel. */
+ * and scale [n_mat, N], by the same rule over the K weights of each output channel. K, N < 2^31 - 1023. */
 moe_status moe_quantize_channels(int32_t n_mat, int32_t K, int32_t N, const uint16_t* W, int8_t* q,
                                  float* scale, moe_stream_t stream);
 
@@ -472,7 +472,8 @@ moe_status moe_quantize_channels(int32_t n_mat, int32_t K, int32_t N, const uint
  *   q_x [rows, K], q_w [n_mat, N, K] 16-byte aligned; s_x [rows], s_w [n_mat, N] fp32; y [rows, N] of
  *   y_dtype (moe_dtype; fp16 becomes infinite past its range), aligned to its element.
  *   The sum is exact while every partial sum stays below 2^24 in magnitude, and within fp32's
- *   rounding past that. Limits: 1 <= n_mat <= 256; K a multiple of 16, K <= 65536; 1 <= N < 2^27.
+ *   rounding past that. Limits: 1 <= n_mat <= 256; K a multiple of 16, K <= 65536; 1 <= N < 2^27;
+ *   rows < 2^31 - 1023.
  * ws: as many bytes as moe_int8_matmul_workspace_size says for these K, N and n_mat and this number of rows
  * or any larger one. */
 moe_status moe_int8_matmul_workspace_size(int32_t rows, int32_t K, int32_t N, int32_t n_mat,

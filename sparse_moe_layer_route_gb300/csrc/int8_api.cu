@@ -26,6 +26,9 @@ bool few_tokens(const Shape& s) {
   return s.d <= 131072 && s.f <= 131072 && (s.T <= 12 || 3.0 * s.rows * s.d * s.f <= 1e8);
 }
 
+// Rows and channels up to this: the kernels add a tile's or a block's size to them in 32 bits.
+constexpr int32_t kMostSize = INT32_MAX - 1023;
+
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 int dtype_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 bool dtype_ok(int dtype) {
@@ -39,7 +42,8 @@ moe_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
 
 moe_status check_matmul(int32_t rows, int32_t K, int32_t N, int32_t n_mat) {
   if (rows < 0 || K < 1 || N < 1 || n_mat < 1) return MOE_ERR_INVALID_ARG;
-  if (n_mat > 256 || K % 16 != 0 || K > 65536 || N >= (1 << 27)) return MOE_ERR_UNSUPPORTED;
+  if (rows > kMostSize || n_mat > 256 || K % 16 != 0 || K > 65536 || N >= (1 << 27))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -98,6 +102,7 @@ extern "C" {
 moe_status moe_quantize_rows(int32_t T, int32_t d, int32_t dtype, const void* x, int64_t ld,
                              int8_t* q, float* scale, moe_stream_t stream) {
   if (T < 0 || d < 1 || !dtype_ok(dtype) || (ld != 0 && ld < d)) return MOE_ERR_INVALID_ARG;
+  if (d > kMostSize) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !q || !scale || !aligned(x, dtype_bytes(dtype)) || !aligned(scale, 4))
     return MOE_ERR_INVALID_ARG;
@@ -109,7 +114,7 @@ moe_status moe_quantize_channels(int32_t n_mat, int32_t K, int32_t N, const uint
                                  float* scale, moe_stream_t stream) {
   if (n_mat < 1 || K < 1 || N < 1 || !W || !q || !scale) return MOE_ERR_INVALID_ARG;
   if (!aligned(W, 2) || !aligned(scale, 4)) return MOE_ERR_INVALID_ARG;
-  if (n_mat > 65535) return MOE_ERR_UNSUPPORTED;
+  if (n_mat > 65535 || K > kMostSize || N > kMostSize) return MOE_ERR_UNSUPPORTED;
   return cuda_status(launch_quantize_channels(n_mat, K, N, W, q, scale, (cudaStream_t)stream));
 }
 

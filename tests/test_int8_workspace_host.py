@@ -28,3 +28,19 @@ def test_expert_workspaces_grow_with_the_tokens(shared):
         size = M.grouped_ffn_int8_workspace_size(M.MoeConfig.make(T, 512, 32, 4, 256, n_shared=shared))
         assert size >= last, T
         last = size
+
+
+MOST = 2 ** 31 - 1
+FAKE = 0x10000000  # never dereferenced
+
+
+@pytest.mark.parametrize("size", [MOST, MOST - 255, MOST - 1022])
+def test_sizes_near_the_end_of_32_bits_are_refused(size):
+    """Sizes to which a tile or a block of threads cannot be added in 32 bits."""
+    lib, n = M.lib(), M.ctypes.c_size_t(0)
+    assert lib.moe_quantize_rows(1, size, 1, FAKE, 0, FAKE, FAKE, None) == 2
+    assert lib.moe_quantize_channels(1, size, 1, FAKE, FAKE, FAKE, None) == 2
+    assert lib.moe_quantize_channels(1, 1, size, FAKE, FAKE, FAKE, None) == 2
+    assert lib.moe_int8_matmul_workspace_size(size, 16, 1, 1, M.ctypes.byref(n)) == 2
+    assert lib.moe_int8_matmul(size, 16, 1, 1, FAKE, FAKE, FAKE, FAKE, None, 0, FAKE, FAKE, 1 << 40,
+                               None) == 2
