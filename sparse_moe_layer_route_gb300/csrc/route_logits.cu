@@ -739,8 +739,8 @@ cudaError_t gate_grad_one(const GateGradArgs& a, cudaStream_t st) {
     return launch_k(gate_grad_chosen_kernel<NV, LT, SIGMOID>,
                     dim3((unsigned)(((long long)a.T + 4 * kWarps - 1) / (4 * kWarps))),
                     dim3(32 * kWarps), 0, st, a);
-  return launch_k(gate_grad_kernel<NV, LT, SIGMOID>, dim3((a.T + kWarps - 1) / kWarps),
-                  dim3(32 * kWarps), 0, st, a);
+  return launch_k(gate_grad_kernel<NV, LT, SIGMOID>,
+                  dim3((unsigned)(((long long)a.T + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0, st, a);
 }
 
 #define MOE_BY_NV(fn, LT, SIG, args, E, st)                                                     \
