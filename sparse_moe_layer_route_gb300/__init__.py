@@ -498,6 +498,9 @@ def quantize_channels(W, stream=None):
     """One-time preparation of bf16 weights W [n, K, N] (or [K, N]) for the 8-bit products: (q int8
     [n, N, K], scale fp32 [n, N]), new tensors on W's device."""
     import torch
+    if W.dim() not in (2, 3):
+        raise ValueError(f"moe_quantize_channels: W of shape {tuple(W.shape)} is neither [n, K, N] nor "
+                         "[K, N]")
     n, (K, N) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
     gpu = _current_gpu("moe_quantize_channels", "W", W)
     _expect("moe_quantize_channels", "W", W, tuple(W.shape), torch.bfloat16, gpu)

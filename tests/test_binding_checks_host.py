@@ -149,3 +149,15 @@ def test_workspaces_of_any_element_type_count_in_bytes(calls, monkeypatch):
     monkeypatch.setattr(M, "int8_matmul", lambda *a, **kw: entry(*a[:-1], ws, **kw))
     every_call(0)["int8_matmul"]()
     assert calls[0][1][11:13] == (ws.data_ptr(), 4096)
+
+
+@pytest.mark.parametrize("shape", [(64,), (2, 3, 64, 32), (1, 2, 2, 16, 8)])
+def test_channels_of_one_or_a_row_of_matrices_alone(calls, monkeypatch, shape):
+    """Of more dimensions the first would count as the matrices, and the others' be left out."""
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: torch.zeros(*a, **kw))
+    with pytest.raises(ValueError):
+        M.quantize_channels(OnGpu(torch.zeros(*shape, dtype=torch.bfloat16)), stream=0)
+    assert calls == []
+    for good in ((64, 32), (3, 64, 32)):
+        M.quantize_channels(OnGpu(torch.zeros(*good, dtype=torch.bfloat16)), stream=0)
+    assert [c[1][:3] for c in calls] == [(1, 64, 32), (3, 64, 32)]
