@@ -531,7 +531,8 @@ struct GateGradArgs {
 
 // Gradient to the logits. With c = scale, dw the gradient of the weights and ds that of the scores:
 //   softmax, renormalised: u = softmax over the chosen logits, dl_j = c u_j (dw_j - sum_i u_i dw_i)
-//   sigmoid, renormalised: D = sum of the chosen s, ds_j += c (dw_j - sum_i dw_i s_i / D) / D
+//   sigmoid, renormalised: u = s / sum of the chosen s, dl_j = c u_j (dw_j - sum_i u_i dw_i) (1 - s_j); the
+//     gradient to s_j itself, with the sum as a divisor, would be past fp32's range where the scores are tiny
 //   not renormalised: ds_j += c dw_j
 //   then softmax: dl += s (ds - sum_e s_e ds_e);  sigmoid: dl = ds s (1 - s).
 __device__ __forceinline__ float lanes_sum(float v, int W) {
@@ -546,29 +547,27 @@ __device__ __forceinline__ float lanes_max(float v, int W) {
 }
 
 // g of a token's chosen experts, one per lane (at most eight) of a row of W = 8 or 32 lanes: the
-// gradient to its score, or to its logit where only the chosen experts have one (TO_LOGIT).
+// gradient to its logit. Not renormalised, and where other experts have a gradient too (!TO_LOGIT): to its score.
 template <bool SIGMOID, bool TO_LOGIT, int W>
 __device__ __forceinline__ float chosen_gradient(const GateGradArgs& a, bool on, float sel,
                                                  float dw) {
-  if (SIGMOID) {
-    float g = dw;
-    if (a.renorm) {
-      const float sj = on ? sigmoid(sel) : 0.0f;
-      const float total = lanes_sum(sj, W);
-      const float dot = lanes_sum(dw * sj, W);
-      g = total == 0.0f ? 0.0f : (dw - dot / total) / total;
-    }
-    if (!TO_LOGIT) return g;
+  if (!a.renorm) {
+    if (!SIGMOID || !TO_LOGIT) return dw;
     // s (1 - s) = x / (1 + x)^2 with x = exp(-|l|): no cancellation at either end
     const float x = expf(-fabsf(sel));
-    return on ? g * (x / ((1.0f + x) * (1.0f + x))) : 0.0f;
+    return on ? dw * (x / ((1.0f + x) * (1.0f + x))) : 0.0f;
   }
-  if (!a.renorm) return dw;
-  const float m = lanes_max(sel, W);
-  float u = on ? expf(sel - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+  float u;
+  if (SIGMOID) {
+    u = on ? sigmoid(sel) : 0.0f;
+  } else {
+    const float m = lanes_max(sel, W);
+    u = on ? expf(sel - (m == -INFINITY ? 0.0f : m)) : 0.0f;
+  }
   const float total = lanes_sum(u, W);
   u = total == 0.0f ? 0.0f : u / total;
-  return u * (dw - lanes_sum(u * dw, W));
+  const float g = u * (dw - lanes_sum(u * dw, W));
+  return SIGMOID ? g * sigmoid(-sel) : g;
 }
 
 // Adds the chosen experts' values to a zeroed row of E floats in shared memory (an index that comes twice
@@ -682,14 +681,15 @@ __global__ void __launch_bounds__(32 * kWarps) gate_grad_kernel(const GateGradAr
   float* mine = rows[warp];
   scatter_row<NV>(mine, lane, my_idx, g);
   float gl[NV];
+  // renormalised, the chosen values are logits' gradients already; else scores'
   if (SIGMOID) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const float x = expf(-fabsf(l[i]));
-      gl[i] = (ds[i] + mine[expert(i)]) * (x / ((1.0f + x) * (1.0f + x)));
+      const float slope = x / ((1.0f + x) * (1.0f + x)), g_i = mine[expert(i)];
+      gl[i] = a.renorm ? ds[i] * slope + g_i : (ds[i] + g_i) * slope;
     }
   } else {
-    // renormalised, the chosen values are logits' gradients already; else scores'
     float s[NV], top, total, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
