@@ -399,19 +399,18 @@ def _names() -> _Torch:
     return _torch_names
 
 
-def _stream_on(stream, gpu):
+def _stream_on(stream, gpu, names):
     """The raw handle of `stream`, or of the current stream of the current GPU, number `gpu`."""
-    if stream is None:
-        raw = _names().raw_stream
-        return raw(gpu) if raw is not None else _stream(None)
+    if stream is None and names.raw_stream is not None:
+        return names.raw_stream(gpu)
     return _stream(stream)
 
 
-def _current_gpu(where, name, t):
+def _current_gpu(where, name, t, names):
     """The current GPU's number; launches go there, so tensor t, and with it all others, has to be
     there too."""
     gpu = t.get_device()
-    if not t.is_cuda or gpu != _names().current_device():
+    if gpu < 0 or gpu != names.current_device():
         raise ValueError(f"{where}: {name} is on {t.device}, which is not the current GPU")
     return gpu
 
@@ -436,7 +435,7 @@ def _expect_ws(where, ws, gpu):
     if ws.get_device() != gpu or not ws.is_contiguous():
         raise ValueError(f"{where}: ws must be a contiguous tensor on cuda:{gpu}, not "
                          f"{tuple(ws.shape)} (strides {ws.stride()}) on {ws.device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def _expect_logits(where, gcfg, T, E, logits):
@@ -454,28 +453,28 @@ def route_logits(gcfg: GateConfig, logits, expert_bias, topk_idx, topk_w, scores
     """Experts and weights from given router logits [T, E] (see moe_route_logits); scores: optional
     fp32 [T, E] that receives every expert's score."""
     w, T, E, k, n = "moe_route_logits", gcfg.T, gcfg.E, gcfg.top_k, _names()
-    gpu = _current_gpu(w, "logits", logits)
+    gpu = _current_gpu(w, "logits", logits, n)
     _check(lib().moe_route_logits(
         ctypes.byref(gcfg), _expect_logits(w, gcfg, T, E, logits),
         None if expert_bias is None else _expect(w, "expert_bias", expert_bias, (E,), n.f32, gpu),
         _expect(w, "topk_idx", topk_idx, (T, k), n.i32, gpu),
         _expect(w, "topk_w", topk_w, (T, k), n.f32, gpu),
         None if scores is None else _expect(w, "scores", scores, (T, E), n.f32, gpu),
-        _stream_on(stream, gpu)), w)
+        _stream_on(stream, gpu, n)), w)
 
 
 def route_logits_backward(gcfg: GateConfig, logits, topk_idx, d_topk_w, d_scores, d_logits,
                           stream=None):
     """d_logits from the gradients of topk_w and scores (either may be None)."""
     w, T, E, k, n = "moe_route_logits_backward", gcfg.T, gcfg.E, gcfg.top_k, _names()
-    gpu = _current_gpu(w, "logits", logits)
+    gpu = _current_gpu(w, "logits", logits, n)
     _check(lib().moe_route_logits_backward(
         ctypes.byref(gcfg), _expect_logits(w, gcfg, T, E, logits),
         _expect(w, "topk_idx", topk_idx, (T, k), n.i32, gpu),
         None if d_topk_w is None else _expect(w, "d_topk_w", d_topk_w, (T, k), n.f32, gpu),
         None if d_scores is None else _expect(w, "d_scores", d_scores, (T, E), n.f32, gpu),
         _expect(w, "d_logits", d_logits, (T, E), logits.dtype, gpu),
-        _stream_on(stream, gpu)), w)
+        _stream_on(stream, gpu, n)), w)
 
 
 def quantize_rows(x, q, scale, stream=None):
@@ -484,14 +483,14 @@ def quantize_rows(x, q, scale, stream=None):
     w, n = "moe_quantize_rows", _names()
     T, d = x.shape
     step, unit = x.stride()
-    gpu = _current_gpu(w, "x", x)
+    gpu = _current_gpu(w, "x", x, n)
     if (d > 1 and unit != 1) or (T > 1 and step < d):
         raise ValueError(f"{w}: x must have unit stride inside a row and rows at least {d} apart, not "
                          f"strides {x.stride()}")
     _check(lib().moe_quantize_rows(T, d, _dtype_code(x, w), x.data_ptr(), step if T > 1 else d,
                                    _expect(w, "q", q, (T, d), n.i8, gpu),
                                    _expect(w, "scale", scale, (T,), n.f32, gpu),
-                                   _stream_on(stream, gpu)), w)
+                                   _stream_on(stream, gpu, n)), w)
 
 
 def quantize_channels(W, stream=None):
@@ -502,12 +501,12 @@ def quantize_channels(W, stream=None):
         raise ValueError(f"moe_quantize_channels: W of shape {tuple(W.shape)} is neither [n, K, N] nor "
                          "[K, N]")
     n, (K, N) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
-    gpu = _current_gpu("moe_quantize_channels", "W", W)
+    gpu = _current_gpu("moe_quantize_channels", "W", W, _names())
     _expect("moe_quantize_channels", "W", W, tuple(W.shape), torch.bfloat16, gpu)
     q = torch.empty((n, N, K), dtype=torch.int8, device=W.device)
     scale = torch.empty((n, N), dtype=torch.float32, device=W.device)
     _check(lib().moe_quantize_channels(n, K, N, W.data_ptr(), q.data_ptr(), scale.data_ptr(),
-                                       _stream_on(stream, gpu)), "moe_quantize_channels")
+                                       _stream_on(stream, gpu, _names())), "moe_quantize_channels")
     return q, scale
 
 
@@ -540,14 +539,14 @@ def int8_matmul(q_x, s_x, q_w, s_w, offsets, y, ws, stream=None):
     w, t = "moe_int8_matmul", _names()
     rows, K = q_x.shape
     n, N, _ = q_w.shape
-    gpu = _current_gpu(w, "q_x", q_x)
+    gpu = _current_gpu(w, "q_x", q_x, t)
     _check(lib().moe_int8_matmul(
         rows, K, N, n, _expect(w, "q_x", q_x, (rows, K), t.i8, gpu),
         _expect(w, "s_x", s_x, (rows,), t.f32, gpu), _expect(w, "q_w", q_w, (n, N, K), t.i8, gpu),
         _expect(w, "s_w", s_w, (n, N), t.f32, gpu),
         None if offsets is None else _expect(w, "offsets", offsets, (n + 1,), t.i32, gpu),
         _dtype_code(y, w), _expect(w, "y", y, (rows, N), y.dtype, gpu),
-        *_expect_ws(w, ws, gpu), _stream_on(stream, gpu)), w)
+        *_expect_ws(w, ws, gpu), _stream_on(stream, gpu, t)), w)
 
 
 def make_int8_weights(gate, up, down, sh_gate=None, sh_up=None, sh_down=None) -> MoeInt8Weights:
@@ -575,7 +574,7 @@ def grouped_ffn_int8(cfg, x, perm_slot, offsets, topk_w, weights: MoeInt8Weights
     T, d, k, E, f, S = cfg.T, cfg.d, cfg.top_k, cfg.E, cfg.d_ff, cfg.n_shared
     into, back = (E, f, d), (E, d, f)
     want = (into, into, back) + (((S, f, d), (S, f, d), (S, d, f)) if S else ())
-    gpu = _current_gpu(w, "x", x)
+    gpu = _current_gpu(w, "x", x, t)
     if weights._shapes[:len(want)] != want or weights._gpu != gpu:
         raise ValueError(f"{w}: weights of shapes {weights._shapes} on cuda:{weights._gpu} do not fit "
                          f"the configuration on cuda:{gpu}")
@@ -585,7 +584,7 @@ def grouped_ffn_int8(cfg, x, perm_slot, offsets, topk_w, weights: MoeInt8Weights
         _expect(w, "offsets", offsets, (E + 1,), t.i32, gpu),
         None if topk_w is None else _expect(w, "topk_w", topk_w, (T, k), t.f32, gpu),
         ctypes.byref(weights), _expect(w, "y_slot", y_slot, (T * (k + S), d), t.f16, gpu),
-        *_expect_ws(w, ws, gpu), _stream_on(stream, gpu)), w)
+        *_expect_ws(w, ws, gpu), _stream_on(stream, gpu, t)), w)
 
 
 def check_bounded_waits(limit_ns, expired, ws, stream=None):
