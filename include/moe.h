@@ -390,16 +390,19 @@ moe_status moe_bias_update(int32_t E, const int32_t* counts, float* expert_bias,
  * weights to the logits. With l the logits of a token:
  *   score   s = softmax over all E experts of l     (MOE_SCORE_SOFTMAX)
  *           s = 1 / (1 + exp(-l))                   (MOE_SCORE_SIGMOID)
- *   rank    r = s + expert_bias (a balance bias; it steers the choice only); an expert whose logit
- *           is -inf (switched off) or NaN ranks below every other, whatever its bias
+ *   rank    r = s + expert_bias (a balance bias; it steers the choice only). A softmax without a bias
+ *           is ranked by its logits, r = l: the order of the scores, also of those that fp32 rounds to
+ *           the same number or to 0. An expert whose logit is -inf (switched off) or NaN ranks below
+ *           every other, whatever its bias
  *   groups  n_groups > 0: E / n_groups consecutive experts form a group, ranked by its largest r
  *           (group_top2 = 0) or by the sum of its two largest (group_top2 = 1; a switched-off second
- *           adds nothing); only the topk_groups best groups are searched
+ *           adds nothing); only the topk_groups best groups are searched. For a softmax without a bias
+ *           that is the sum of two logits; a bias of zeros makes it the sum of two scores
  *   choice  the top_k largest r, r descending
  *   weight  scale * s, or scale * s / (sum of s over the chosen experts) with renormalize = 1
- * Every tie goes to the lower index. Chosen scores that are all zero (every expert of the token
- * switched off, say) have weight 0. A row with a NaN (softmax: or a +inf) still has top_k different
- * experts, and NaN weights. */
+ * Scores are fp32 (a sigmoid of a logit below -88.7 is 0). Every tie goes to the lower index. Chosen
+ * scores that are all zero (every expert of the token switched off, say) have weight 0. A row with a NaN
+ * (softmax: or a +inf) still has top_k different experts, and NaN weights. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
 /* Element types of the entry points that take more than one. */

@@ -547,7 +547,8 @@ __device__ __forceinline__ float lanes_max(float v, int W) {
 }
 
 // g of a token's chosen experts, one per lane (at most eight) of a row of W = 8 or 32 lanes: the
-// gradient to its logit. Not renormalised, and where other experts have a gradient too (!TO_LOGIT): to its score.
+// gradient to its logit. Not renormalised, and where other experts have a gradient too (!TO_LOGIT): to its
+// score.
 template <bool SIGMOID, bool TO_LOGIT, int W>
 __device__ __forceinline__ float chosen_gradient(const GateGradArgs& a, bool on, float sel,
                                                  float dw) {
