@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? kCtasPerSm8 : kCtasPerSm)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tile = blockIdx.x / ctas_per_tile, cta = blockIdx.x - tile * ctas_per_tile;
   // the last tile's CTAs look at every segment, and take the tiles past the grid where there are any
-  const bool last = tile == tiles - 1;
+  const bool last = g.offsets != nullptr && tile == tiles - 1;
   bool unsound;
   const Unit u = find_tile<PASS, R>(g, tile, lane, last, unsound);  // every warp: no barrier
   if (u.seg < 0) return;
