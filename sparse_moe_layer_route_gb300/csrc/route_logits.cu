@@ -558,17 +558,17 @@ __device__ __forceinline__ float chosen_gradient(const GateGradArgs& a, bool on,
     const float x = expf(-fabsf(sel));
     return on ? dw * (x / ((1.0f + x) * (1.0f + x))) : 0.0f;
   }
-  float u;
+  float u, rest = 1.0f;  // rest: 1 - s without cancellation
   if (SIGMOID) {
-    u = on ? sigmoid(sel) : 0.0f;
+    const float e = expf(-sel), sj = 1.0f / (1.0f + e);
+    u = on ? sj : 0.0f;
+    rest = sel < 0.0f ? 1.0f - sj : e * sj;
   } else {
     const float m = lanes_max(sel, W);
     u = on ? expf(sel - (m == -INFINITY ? 0.0f : m)) : 0.0f;
   }
-  const float total = lanes_sum(u, W);
-  u = total == 0.0f ? 0.0f : u / total;
-  const float g = u * (dw - lanes_sum(u * dw, W));
-  return SIGMOID ? g * sigmoid(-sel) : g;
+  const float total = lanes_sum(u, W), dot = lanes_sum(u * dw, W);
+  return total == 0.0f ? 0.0f : u / total * (dw - dot / total) * rest;
 }
 
 // Adds the chosen experts' values to a zeroed row of E floats in shared memory (an index that comes twice
