@@ -87,9 +87,10 @@ constexpr int kInt8StageK = 128;  // k per shared-memory stage
 // Rows per segment (an even spread's) up to which row tiles have at most 64 and 128 rows, not 256.
 constexpr int kInt8Mean64 = 24, kInt8Mean128 = 104;
 // Height of a segment's row tiles, a multiple of 32 up to NT: as few tiles as NT allows, of equal heights,
-// as a tile of up to 192 rows costs the widening of its weights (about 400 clk per 64 k) whatever it holds.
-// Past 192 it costs its MMAs, 2 clk a row, and about 40 for the overlap with the next tile: taken where that
-// is less than one more tile (400 rows: two of 224 and 176, not three). 64 segments of about 200 rows of
+// as a low tile costs the widening of its weights whatever it holds: about 400 clk per 64 k with two sets of
+// widening warps, the MMAs of 194 rows; with three sets that of 130 rows. The rule's numbers are the two
+// sets': past 192 rows a tile costs its MMAs, 2 clk a row, and about 40 for the overlap with the next one,
+// taken where that is less than one more tile of 400 (400 rows: two of 224 and 176, not three). 64 segments of about 200 rows of
 // [2048 x 2048] 91 us, with tiles of up to 192 rows 116; of about 300 rows 141, the same.
 __host__ __device__ inline int int8_tile_height(int rows, int NT) {
   const int most = rows < 1 ? 1 : rows;

@@ -17,9 +17,10 @@
 // 49 KB of shared-memory bandwidth in the 384 clk that N = 192 takes, and half the widening per MMA.
 //
 // Long segments are bound by the tensor cores or, in low tiles, by the widening; short ones by the weight
-// bytes: 128 experts and a shared one of d 7168, d_ff 2048 for 64 tokens 493 us for both products, 7.4 TB/s.
-// 16384 rows of [4096 x 7168] in 482 us in short runs (2.0 PFLOP/s, 1.05 of the measured bf16 peak); a long
-// run settles at the power cap, 535. A 64 k slot takes 2 clk of MMA a row; widening it takes one set of warps
+// bytes: 128 experts and a shared one of d 7168, d_ff 2048 for 64 tokens 492 to 536 us a call from run to run
+// (7.4 to 6.8 TB/s; the two quantizations of rows are about 5 of it). 16384 rows of [4096 x 7168] in 482 us in short
+// runs (2.0 PFLOP/s, 1.05 of the measured bf16 peak); a long run settles at the power cap: 535, 581 with the
+// widening of the rows in front. A 64 k slot takes 2 clk of MMA a row; widening it takes one set of warps
 // 776, so two sets keep up with 194 rows and three with 130: a lower tile is bound by the widening.
 //
 // A unit is 256 channels (SwiGLU pass: 128 channels of gate and up) x a row tile of one segment
@@ -580,7 +581,7 @@ cudaError_t launch_pass(const Int8Gemm& g, cudaStream_t st) {
   auto one_round = [&](int tile) { return PASS != kInt8Partial && units(tile) <= pairs; };
   Int8Gemm t = g;
   // decode: deeper stages, for the weights' sake, where tiles of 64 rows hold every segment (64 tokens, 128 + 1
-  // experts of d 7168, d_ff 2048 502 against 514 us; with a shared expert's 512 rows in tiles of 64 541
+  // experts of d 7168, d_ff 2048 502 against 514 us in turn; with a shared expert's 512 rows in tiles of 64 541
   // against 524)
   t.tile_rows = 64;
   if ((mean <= kInt8Mean64 && (g.S == 0 || g.T <= 64)) || one_round(64))

@@ -1,5 +1,5 @@
-// Grouped products of 8-bit integers for a few rows: every weight is read once, by integer dot products
-// of four (exact in 32 bits), with no tile to fill.
+// Grouped products of 8-bit integers for a few rows: integer dot products of four (exact in 32 bits) that read
+// a segment's weights once for each of its tiles of one to eight rows.
 //
 // Bound by the weight bytes. A warp takes kStreams output channels (SwiGLU pass: half as many channels of
 // gate and of up) of one row tile of R rows and runs down K, 16 codes a lane and step: one 16-byte load per

@@ -279,7 +279,7 @@ namespace {
 
 // Calls f(W, VEC) for rows of d elements: a warp per row up to 2048 elements, else a CTA, with the row in
 // registers up to 8192 (128 threads) or 16384 (256); vec: rows are in 16-byte pieces of eight elements.
-// So few rows that most SMs have none take 512 threads each: then one row's time is the kernel's.
+// At most as many rows as GB300 has SMs (152) take 512 threads each: then one row's time is the kernel's.
 template <int N>
 using Int = std::integral_constant<int, N>;
 template <typename F>

@@ -17,8 +17,8 @@ namespace {
 constexpr int kJoinThreads = 128;
 
 // y = (sum of the pieces, in their order) * row scale * channel scale; rows past the last segment are left.
-// Four channels a thread (one each, 300 rows of 4096 channels in two pieces took 9.3 us, not 3.6; eight
-// loads in flight 4.6). vec: y's rows and the scales begin on four elements.
+// Four channels a thread (one each, 300 rows of 4096 channels in two pieces took 9.3 us of this kernel, not 3.6;
+// eight loads in flight 4.6). vec: y's rows and the scales begin on four elements.
 template <typename YT>
 __global__ void __launch_bounds__(kJoinThreads) join_splits_kernel(const float* __restrict__ part,
                                                                    const Int8Gemm g, bool vec) {
