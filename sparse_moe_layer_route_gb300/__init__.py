@@ -406,6 +406,19 @@ def _stream_on(stream, gpu, names):
     return _stream(stream)
 
 
+def _allocating_for(stream):
+    """A context in which torch allocates for `stream`, so that its kernels may write to the memory at
+    once: the current stream's allocations may still be written to by what that stream has enqueued."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _current_gpu(where, name, t, names):
     """The current GPU's number; launches go there, so tensor t, and with it all others, has to be
     there too."""
@@ -495,7 +508,7 @@ def quantize_rows(x, q, scale, stream=None):
 
 def quantize_channels(W, stream=None):
     """One-time preparation of bf16 weights W [n, K, N] (or [K, N]) for the 8-bit products: (q int8
-    [n, N, K], scale fp32 [n, N]), new tensors on W's device."""
+    [n, N, K], scale fp32 [n, N]), new tensors on W's device that belong to `stream`."""
     import torch
     if W.dim() not in (2, 3):
         raise ValueError(f"moe_quantize_channels: W of shape {tuple(W.shape)} is neither [n, K, N] nor "
@@ -503,8 +516,9 @@ def quantize_channels(W, stream=None):
     n, (K, N) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
     gpu = _current_gpu("moe_quantize_channels", "W", W, _names())
     _expect("moe_quantize_channels", "W", W, tuple(W.shape), torch.bfloat16, gpu)
-    q = torch.empty((n, N, K), dtype=torch.int8, device=W.device)
-    scale = torch.empty((n, N), dtype=torch.float32, device=W.device)
+    with _allocating_for(stream):
+        q = torch.empty((n, N, K), dtype=torch.int8, device=W.device)
+        scale = torch.empty((n, N), dtype=torch.float32, device=W.device)
     _check(lib().moe_quantize_channels(n, K, N, W.data_ptr(), q.data_ptr(), scale.data_ptr(),
                                        _stream_on(stream, gpu, _names())), "moe_quantize_channels")
     return q, scale
