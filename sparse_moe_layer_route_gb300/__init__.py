@@ -543,7 +543,8 @@ def alloc_int8_workspace(nbytes, device="cuda"):
     """A workspace of nbytes for the 8-bit entry points, its status word cleared."""
     import torch
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    workspace_init(ws)
+    with torch.cuda.device(ws.device):
+        workspace_init(ws)
     return ws
 
 

@@ -162,3 +162,26 @@ def test_channels_of_one_or_a_row_of_matrices_alone(calls, monkeypatch, shape):
     for good in ((64, 32), (3, 64, 32)):
         M.quantize_channels(OnGpu(torch.zeros(*good, dtype=torch.bfloat16)))
     assert [c[1][:3] for c in calls] == [(1, 64, 32), (3, 64, 32)]
+
+
+def test_a_workspace_is_cleared_on_its_own_gpu(calls, monkeypatch):
+    """Not on the current one's stream, which nothing orders before the first call there."""
+    entered = []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+
+        def __exit__(self, *exc):
+            entered.pop()
+
+    seen = []
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: OnGpu(torch.zeros(n, dtype=dtype), 1))
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(M, "_stream", lambda stream: seen.append(list(entered)) or 7)
+    ws = M.alloc_int8_workspace(4096, "cuda:1")
+    assert calls == [("moe_workspace_init", (ws.data_ptr(), 4096, 7))]
+    assert seen == [[torch.device("cuda", 1)]] and entered == []
