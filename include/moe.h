@@ -393,7 +393,7 @@ moe_status moe_bias_update(int32_t E, const int32_t* counts, float* expert_bias,
  *   rank    r = s + expert_bias (a balance bias; it steers the choice only). A softmax without a bias
  *           is ranked by its logits, r = l: the order of the scores, also of those that fp32 rounds to
  *           the same number or to 0. An expert whose logit is -inf (switched off) or NaN ranks below
- *           every other, whatever its bias
+ *           every other, whatever its bias; the lowest finite value is a logit like any other
  *   groups  n_groups > 0: E / n_groups consecutive experts form a group, ranked by its largest r
  *           (group_top2 = 0) or by the sum of its two largest (group_top2 = 1; a switched-off second
  *           adds nothing); only the topk_groups best groups are searched. For a softmax without a bias

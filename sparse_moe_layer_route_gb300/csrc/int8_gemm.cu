@@ -37,8 +37,8 @@
 //   warps 8-     widen, in SETS of four warps: the half-steps (64 k) of all units go to the sets in turn
 // The MMA issuer's barrier operations are few, because one behind a commit costs it about 300 clk, with or
 // without something to wait for: per 128 k it waits once (`ready`: both CTAs' rows have landed and the
-// eight warps of each that widen the step have stored) and commits once (`done`, to both CTAs), and `done` frees the rows' stage and,
-// with it, the slot of widened codes. (With a wait and a commit for each 64 k slot and each stage, a 64 k
+// eight warps of each that widen the step have stored) and commits once (`done`, to both CTAs), and `done`
+// frees the rows' stage and, with it, the slot of widened codes. (With a wait and a commit for each 64 k slot and each stage, a 64 k
 // slot took 480 clk whatever its N.) The codes' stage is free once they are in registers (`taken`): they come
 // from HBM and need the longer run-up (64 segments of 128 rows of [2048 x 2048] 83 us with four stages of
 // both together, 77 apart).
