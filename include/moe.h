@@ -500,6 +500,37 @@ moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const 
                                 const moe_int8_weights* w, uint16_t* y_slot, void* ws,
                                 size_t ws_bytes, moe_stream_t stream);
 
+/* ---- The layer for a few tokens ------------------------------------------------------------------
+ * moe_layer_forward for up to MOE_FEW_MAX_TOKENS tokens (sequences being decoded, a speculative
+ * decoder's guesses) in one kernel, bound by reading the chosen experts' weights once where
+ * moe_layer_forward would be bound by its nine launches. Same configuration (bf16 experts; every
+ * routing mode, groups, capacity, shared experts), weights and results; the W_down_f16 copies are not
+ * used, and activations have fp32's range. What differs: sums are taken in another order, the choice is
+ * that of the exact logits up to gaps of about 1e-7 of their size, and H is carried with 16 significant
+ * bits and the slots' outputs in fp32, so out is the exact layer's within its one rounding to bf16.
+ * Returns MOE_ERR_UNSUPPORTED for more tokens, weight_bits != 0, overflow_reroute with a capacity limit,
+ * or d or d_ff above 65536.
+ *   w: W_g, W_gate, W_up, W_down and, with n_shared > 0, the shared experts' (all 16-byte aligned);
+ *   expert_bias and gumbel_u as moe_layer_forward needs them; W_g_t as there. x, out [T, d] bf16, 16-byte
+ *   aligned; out may be x. route_out as in moe_layer_forward.
+ *   ws: moe_few_workspace_size bytes that moe_workspace_init has cleared once (its first 512); calls that
+ *   share it must follow one another. The kernel takes the whole GPU (one CTA per SM, cooperative launch) and
+ *   has two grid barriers, each of which waits at most 2 s: past that MOE_DEVFAULT_PIPELINE_TIMEOUT is
+ *   set, out is not complete, and ws has to be cleared again before its next use. */
+#define MOE_FEW_MAX_TOKENS 16
+moe_status moe_few_workspace_size(const moe_config* cfg, size_t* bytes);
+moe_status moe_layer_forward_few(const moe_config* cfg, const moe_weights* w, const uint16_t* x,
+                                 const float* gumbel_u, uint16_t* out, moe_route_out* route_out,
+                                 void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Steps 5-10 of it for a choice that the caller made (moe_route_logits, say): topk_idx [T, k] int32,
+ * topk_w [T, k] fp32 (NULL: every gate is 1), both 4-byte aligned. An index outside [0, E) sets
+ * MOE_DEVFAULT_BAD_EXPERT_INDEX and its slot is dropped; a token that has an expert twice gets it with
+ * both gates, and both slots count towards the capacity. W_g, mode and groups are not used. */
+moe_status moe_experts_few(const moe_config* cfg, const moe_weights* w, const uint16_t* x,
+                           const int32_t* topk_idx, const float* topk_w, uint16_t* out, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+
 /* Failure-detection check of this device: runs the library's two kinds of bounded device wait,
  * each against a condition that never comes true, with a wait limit of limit_ns (100 us .. 2 s;
  * the layer's own waits use 2 s). One is the mbarrier wait of the tensor-core pipelines (a

@@ -29,6 +29,7 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_prepare_router", "mo
            "moe_pack_f16", "moe_bias_update", "moe_route_logits", "moe_route_logits_backward",
            "moe_quantize_rows", "moe_quantize_channels", "moe_int8_matmul_workspace_size",
            "moe_int8_matmul", "moe_grouped_ffn_int8_workspace_size", "moe_grouped_ffn_int8",
+           "moe_few_workspace_size", "moe_layer_forward_few", "moe_experts_few",
             "moe_check_bounded_waits", "moe_device_status",
            "moe_status_string")
 
@@ -154,6 +155,10 @@ def lib():
         L.moe_grouped_ffn_int8_workspace_size.argtypes = [cfgp, ctypes.POINTER(ctypes.c_size_t)]
         L.moe_grouped_ffn_int8.argtypes = [cfgp, P, P, P, P, ctypes.POINTER(MoeInt8Weights), P, P,
                                            S, P]
+        L.moe_few_workspace_size.argtypes = [cfgp, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_layer_forward_few.argtypes = [cfgp, ctypes.POINTER(MoeWeights), P, P, P,
+                                            ctypes.POINTER(MoeRouteOut), P, S, P]
+        L.moe_experts_few.argtypes = [cfgp, ctypes.POINTER(MoeWeights), P, P, P, P, P, S, P]
         L.moe_status_string.argtypes = [I]
         L.moe_status_string.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -327,6 +332,9 @@ def make_weights(W_g, expert_bias, W_gate, W_up, W_down, Wsh_gate=None, Wsh_up=N
     w = MoeWeights(*[_ptr(t) for t in (W_g, expert_bias, W_gate, W_up, W_down, Wsh_gate,
                                         Wsh_up, Wsh_down, W_down_f16, Wsh_down_f16)])
     w.W_g_t = _ptr(W_g_t)
+    w._tensors = dict(W_g=W_g, expert_bias=expert_bias, W_gate=W_gate, W_up=W_up, W_down=W_down,
+                      Wsh_gate=Wsh_gate, Wsh_up=Wsh_up, Wsh_down=Wsh_down, W_g_t=W_g_t)
+    w._fit = set()                    # configurations that these tensors have been checked against
     if quant is not None:
         w.quant = ctypes.pointer(quant)
         w._quant_ref = quant          # keep the struct alive with the weights
@@ -335,8 +343,9 @@ def make_weights(W_g, expert_bias, W_gate, W_up, W_down, Wsh_gate=None, Wsh_up=N
 
 def make_route_out(topk_idx=None, topk_w=None, counts=None, offsets=None, perm_slot=None,
                    slot_pos=None) -> MoeRouteOut:
-    return MoeRouteOut(*[_ptr(t) for t in (topk_idx, topk_w, counts, offsets, perm_slot,
-                                           slot_pos)])
+    r = MoeRouteOut(*[_ptr(t) for t in (topk_idx, topk_w, counts, offsets, perm_slot, slot_pos)])
+    r._tensors = (topk_idx, topk_w, counts, offsets, perm_slot, slot_pos)
+    return r
 
 
 def layer_forward(cfg, weights: MoeWeights, x, gumbel_u, out, route_out: MoeRouteOut | None,
@@ -600,6 +609,85 @@ def grouped_ffn_int8(cfg, x, perm_slot, offsets, topk_w, weights: MoeInt8Weights
         None if topk_w is None else _expect(w, "topk_w", topk_w, (T, k), t.f32, gpu),
         ctypes.byref(weights), _expect(w, "y_slot", y_slot, (T * (k + S), d), t.f16, gpu),
         *_expect_ws(w, ws, gpu), _stream_on(stream, gpu, t)), w)
+
+
+FEW_MAX_TOKENS = 16
+
+
+def few_workspace_size(cfg: MoeConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_few_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_few_workspace_size")
+    return n.value
+
+
+def alloc_few_workspace(cfg: MoeConfig, device="cuda"):
+    """A workspace for layer_forward_few and experts_few with this configuration, its status word and
+    counters cleared."""
+    return alloc_int8_workspace(few_workspace_size(cfg), device)
+
+
+def _expect_experts(where, cfg, weights, gpu, router):
+    """The weights' tensors fit the configuration on GPU `gpu` (addresses that the program gave instead of
+    tensors are its own affair). Looked at once per configuration."""
+    tensors = getattr(weights, "_tensors", None)
+    if tensors is None:
+        return                        # filled in by hand: addresses alone
+    d, E, f, S, t = cfg.d, cfg.E, cfg.d_ff, cfg.n_shared, _names()
+    bias = router and cfg.mode == ROUTE_BIAS_SELECT
+    key = (d, E, f, S, gpu, router, bias)
+    if key in weights._fit:
+        return
+    want = dict(W_gate=(E, d, f), W_up=(E, d, f), W_down=(E, f, d))
+    if S:
+        want.update(Wsh_gate=(S, d, f), Wsh_up=(S, d, f), Wsh_down=(S, f, d))
+    if router:
+        want.update(W_g=(d, E), W_g_t=(E, d))
+    for name, shape in want.items():
+        m = tensors[name]
+        if m is not None and not isinstance(m, int):
+            _expect(where, name, m, shape, t.bf16, gpu)
+    m = tensors["expert_bias"]
+    if bias and m is not None and not isinstance(m, int):
+        _expect(where, "expert_bias", m, (E,), t.f32, gpu)
+    weights._fit.add(key)
+
+
+def layer_forward_few(cfg, weights: MoeWeights, x, gumbel_u, out, route_out: MoeRouteOut | None, ws,
+                      stream=None):
+    """layer_forward for up to FEW_MAX_TOKENS tokens in one kernel (see moe_layer_forward_few); ws from
+    alloc_few_workspace."""
+    w, t = "moe_layer_forward_few", _names()
+    T, d, E, k = cfg.T, cfg.d, cfg.E, cfg.top_k
+    gpu = _current_gpu(w, "x", x, t)
+    _expect_experts(w, cfg, weights, gpu, True)
+    if route_out is not None:
+        shapes = ((T, k), (T, k), (E,), (E + 1,), (T * k,), (T * k,))
+        given = getattr(route_out, "_tensors", ())
+        for (name, _), r, shape in zip(MoeRouteOut._fields_, given, shapes):
+            if r is not None and not isinstance(r, int):
+                _expect(w, name, r, shape, t.f32 if name == "topk_w" else t.i32, gpu)
+    _check(lib().moe_layer_forward_few(
+        ctypes.byref(cfg), ctypes.byref(weights), _expect(w, "x", x, (T, d), t.bf16, gpu),
+        None if gumbel_u is None else _expect(w, "gumbel_u", gumbel_u, (T, E), t.f32, gpu),
+        _expect(w, "out", out, (T, d), t.bf16, gpu),
+        None if route_out is None else ctypes.byref(route_out), *_expect_ws(w, ws, gpu),
+        _stream_on(stream, gpu, t)), w)
+
+
+def experts_few(cfg, weights: MoeWeights, x, topk_idx, topk_w, out, ws, stream=None):
+    """The experts, shared experts and combine of a layer for up to FEW_MAX_TOKENS tokens, with the choice
+    topk_idx [T, k] and gates topk_w [T, k] (None: 1) given (see moe_experts_few)."""
+    w, t = "moe_experts_few", _names()
+    T, d, k = cfg.T, cfg.d, cfg.top_k
+    gpu = _current_gpu(w, "x", x, t)
+    _expect_experts(w, cfg, weights, gpu, False)
+    _check(lib().moe_experts_few(
+        ctypes.byref(cfg), ctypes.byref(weights), _expect(w, "x", x, (T, d), t.bf16, gpu),
+        _expect(w, "topk_idx", topk_idx, (T, k), t.i32, gpu),
+        None if topk_w is None else _expect(w, "topk_w", topk_w, (T, k), t.f32, gpu),
+        _expect(w, "out", out, (T, d), t.bf16, gpu), *_expect_ws(w, ws, gpu),
+        _stream_on(stream, gpu, t)), w)
 
 
 def check_bounded_waits(limit_ns, expired, ws, stream=None):

@@ -1,0 +1,46 @@
+// The MoE layer for a few tokens (few.cu): launch interface and workspace.
+#pragma once
+#include "internal.h"
+
+namespace moe {
+
+constexpr int kFewMaxCtas = 208;    // persistent CTAs, one counter byte each in FewMeta
+constexpr int kFewMaxSize = 65536;  // d and d_ff: work is counted in 32 bits
+
+// What the kernel keeps in the counter block that moe_workspace_init clears. Every call that completes
+// leaves arrive and piece zero; gen counts the grid barriers passed.
+struct FewMeta {
+  unsigned arrive, gen;
+  unsigned piece[kFewMaxCtas / 4];  // pieces finished of the tile that is cut in CTA i's range: byte i
+  unsigned pad[10];
+};
+static_assert(sizeof(FewMeta) == sizeof(Meta), "it takes the counter block's place");
+
+struct FewArgs {
+  const uint16_t* x;                                  // [T, d]
+  const uint16_t* W_g_t;                              // [E, d], or nullptr: idx_in and w_in are the choice
+  const uint16_t *gate, *up, *down;                   // [E, d, f], [E, d, f], [E, f, d]
+  const uint16_t *sh_gate, *sh_up, *sh_down;          // the same for S
+  const float *bias, *u;                              // BIAS_SELECT, GUMBEL
+  const int32_t* idx_in;                              // [T, k]
+  const float* w_in;                                  // [T, k] or nullptr (every gate 1)
+  moe_route_out ro;                                   // optional results
+  uint16_t* out;                                      // [T, d]
+  float* logits;                                      // [T, E]
+  uint32_t* h;                                        // activations [columns, f]: see few.cu
+  float* part;                                        // partial sums, part_floats per CTA
+  int* status;
+  FewMeta* meta;
+  int T, d, E, k, f, S, mode, G, Gk, C;
+  float tau;
+  int part_floats;
+};
+
+struct FewLayout {
+  size_t meta, logits, h, part, wg_t, total;
+  int part_floats;
+};
+FewLayout few_layout(const Shape& s);
+cudaError_t launch_few(const FewArgs& a, cudaStream_t st);
+
+}  // namespace moe
