@@ -531,6 +531,77 @@ moe_status moe_experts_few(const moe_config* cfg, const moe_weights* w, const ui
                            const int32_t* topk_idx, const float* topk_w, uint16_t* out, void* ws,
                            size_t ws_bytes, moe_stream_t stream);
 
+/* ---- Norms around a block, residual, gates and dropout ---------------------------------------------
+ * What stands around a layer in a block of a model, in one pass over the residual stream:
+ *   u  = norm_after(y)                        y: the block's output (moe_combine's out, say)
+ *   h' = alpha * h + beta * gate * drop(u)    h: the residual stream
+ *   n  = norm_before(h')                      n: the next block's input
+ * norm(v) = (v - m) * r * w + b over the d channels of a token, r = 1 / sqrt(mean((v - m)^2) + eps), with
+ * m = mean(v) (MOE_NORM_LAYER) or 0 (MOE_NORM_RMS); w absent is 1, b absent is 0. Sums are fp32 (squares
+ * that leave its range do so here too), n is taken from h' before that is rounded, and every output is
+ * rounded once, to nearest even (fp16 becomes infinite past its range).
+ * drop(u)[t, c] = u[t, c] / (1 - p) where a random number is at least p * 2^32 (rounded), else 0 whatever
+ * u is. The number is word c % 4 of Philox 4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2,
+ * 3", SC'11) with the counter (c / 4, t, low word of step, high word of step) and seed's words as the key, low
+ * first. seed and step are read on the device when the kernel runs, rng = {seed, step}, so a program
+ * that replays a graph advances rng[1]; no mask is stored, the gradient makes it again from the same rng. */
+typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
+
+typedef struct {
+  int32_t T, d;             /* tokens, channels; 1 <= d <= 65536 */
+  int32_t after, before;    /* moe_norm_kind of the norm of y and of h' */
+  int32_t h_dtype;          /* moe_dtype of h, h_out and their gradients */
+  int32_t y_dtype;          /* of y, n and their gradients */
+  int32_t w_dtype;          /* of the parameters: MOE_DTYPE_F32 or 16 bits like the others */
+  int32_t gate_rows;        /* consecutive tokens that share a row of gates (a sequence); 0: no gates */
+  float eps;                /* >= 0 */
+  float alpha, beta;
+  float p_drop;             /* 0 <= p < 1 */
+  int64_t ld_h, ld_y;       /* elements from one row of h (of the gradient: h_out) and of y to the next;
+                               0: d; other matrices are contiguous */
+} moe_residual_norm_config;
+
+/* Parameters on the device: w and b [d], gate [ceil(T / gate_rows), d], of w_dtype; each may be NULL, gate if
+ * and only if gate_rows is 0. rng: two int64, needed where p_drop > 0. */
+typedef struct {
+  const void *w_after, *b_after, *gate, *w_before, *b_before;
+  const int64_t* rng;
+} moe_residual_norm_params;
+
+/* Their gradients, fp32 of the same shapes; each may be NULL (not wanted). */
+typedef struct {
+  float *w_after, *b_after, *gate, *w_before, *b_before;
+} moe_residual_norm_grads;
+
+/* h [T, d]; y [T, d], or NULL where no block comes before (after NONE, no gates, p_drop 0: h' = alpha h);
+ * h_out [T, d], or NULL (not wanted); n [T, d] if and only if before is not NONE. h_out may be h, and n may
+ * be y, where they have the same rows. Tensors aligned to their element; rows of 16-byte pieces (pointers and
+ * strides) move faster. No workspace. Asynchronous on stream; T = 0 launches nothing. */
+moe_status moe_residual_norm(const moe_residual_norm_config* cfg, const void* h, const void* y,
+                             const moe_residual_norm_params* params, void* h_out, void* n,
+                             moe_stream_t stream);
+
+/* Gradients of a loss whose gradients to h' and n are d_h_out and d_n [T, d] (either may be NULL, not both; d_n
+ * needs a norm before): d_h [T, d] and d_y [T, d] (NULL if and only if y is), and those of the parameters, summed
+ * over the tokens in a fixed order (deterministic). h_out: the stream after the block (only read where d_n is
+ * given; else may be NULL); y as given to the forward pass. d_h may be d_h_out, and d_y may be d_n or y
+ * where the rows are the same. ws: moe_residual_norm_workspace_size bytes, 256-byte aligned, not cleared (it
+ * serves every smaller T). T = 0 clears the parameters' gradients. */
+moe_status moe_residual_norm_workspace_size(const moe_residual_norm_config* cfg, size_t* bytes);
+moe_status moe_residual_norm_backward(const moe_residual_norm_config* cfg, const void* h_out,
+                                      const void* y, const void* d_h_out, const void* d_n,
+                                      const moe_residual_norm_params* params, void* d_h, void* d_y,
+                                      const moe_residual_norm_grads* grads, void* ws, size_t ws_bytes,
+                                      moe_stream_t stream);
+
+/* y [T, d] = residual + drop(x), x and residual (NULL: none) of rows ld_x and ld_r elements apart (0: d), y
+ * contiguous, all of dtype (moe_dtype); drop and rng as above. Its gradient to x is the same call on the
+ * output's gradient, without a residual. y may be x or residual where their rows are contiguous.
+ * 1 <= d < 2^31 - 4096. */
+moe_status moe_dropout(int32_t T, int32_t d, int32_t dtype, const void* x, int64_t ld_x, float p,
+                       const int64_t* rng, const void* residual, int64_t ld_r, void* y,
+                       moe_stream_t stream);
+
 /* Failure-detection check of this device: runs the library's two kinds of bounded device wait,
  * each against a condition that never comes true, with a wait limit of limit_ns (100 us .. 2 s;
  * the layer's own waits use 2 s). One is the mbarrier wait of the tensor-core pipelines (a

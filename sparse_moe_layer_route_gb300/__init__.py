@@ -21,6 +21,7 @@ DEVFAULT_FP16_RANGE = 0x8
 Y_F16, Y_F32 = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 
 EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_prepare_router", "moe_route",
            "moe_permute", "moe_permute_noalloc", "moe_overflow_reroute", "moe_grouped_ffn",
@@ -30,6 +31,8 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_prepare_router", "mo
            "moe_quantize_rows", "moe_quantize_channels", "moe_int8_matmul_workspace_size",
            "moe_int8_matmul", "moe_grouped_ffn_int8_workspace_size", "moe_grouped_ffn_int8",
            "moe_few_workspace_size", "moe_layer_forward_few", "moe_experts_few",
+           "moe_residual_norm", "moe_residual_norm_workspace_size", "moe_residual_norm_backward",
+           "moe_dropout",
             "moe_check_bounded_waits", "moe_device_status",
            "moe_status_string")
 
@@ -99,6 +102,29 @@ class GateConfig(ctypes.Structure):
                    int(bool(renormalize)), scale, dtype, ld)
 
 
+class ResidualNormConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "d", "after", "before", "h_dtype", "y_dtype", "w_dtype", "gate_rows")] + \
+        [(n, ctypes.c_float) for n in ("eps", "alpha", "beta", "p_drop")] + \
+        [(n, ctypes.c_int64) for n in ("ld_h", "ld_y")]
+
+    @classmethod
+    def make(cls, T, d, after=NORM_NONE, before=NORM_RMS, h_dtype=DTYPE_BF16, y_dtype=DTYPE_BF16,
+             w_dtype=DTYPE_BF16, gate_rows=0, eps=1e-6, alpha=1.0, beta=1.0, p_drop=0.0, ld_h=0,
+             ld_y=0):
+        return cls(T, d, after, before, h_dtype, y_dtype, w_dtype, gate_rows, eps, alpha, beta, p_drop,
+                   ld_h, ld_y)
+
+
+class _NormParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w_after", "b_after", "gate", "w_before", "b_before",
+                                               "rng")]
+
+
+class _NormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w_after", "b_after", "gate", "w_before", "b_before")]
+
+
 class MoeInt8Matrix(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
@@ -159,6 +185,12 @@ def lib():
         L.moe_layer_forward_few.argtypes = [cfgp, ctypes.POINTER(MoeWeights), P, P, P,
                                             ctypes.POINTER(MoeRouteOut), P, S, P]
         L.moe_experts_few.argtypes = [cfgp, ctypes.POINTER(MoeWeights), P, P, P, P, P, S, P]
+        normp, paramp = ctypes.POINTER(ResidualNormConfig), ctypes.POINTER(_NormParams)
+        L.moe_residual_norm.argtypes = [normp, P, P, paramp, P, P, P]
+        L.moe_residual_norm_workspace_size.argtypes = [normp, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_residual_norm_backward.argtypes = [normp, P, P, P, P, paramp, P, P,
+                                                 ctypes.POINTER(_NormGrads), P, S, P]
+        L.moe_dropout.argtypes = [i32, i32, i32, P, i64, ctypes.c_float, P, P, i64, P, P]
         L.moe_status_string.argtypes = [I]
         L.moe_status_string.restype = ctypes.c_char_p
         for name in EXPORTS:
@@ -392,8 +424,9 @@ class _Torch:
     def __init__(self):
         import torch
         self.f32, self.bf16, self.f16 = torch.float32, torch.bfloat16, torch.float16
-        self.i8, self.i32 = torch.int8, torch.int32
+        self.i8, self.i32, self.i64 = torch.int8, torch.int32, torch.int64
         self.code = {self.f32: DTYPE_F32, self.bf16: DTYPE_BF16, self.f16: DTYPE_F16}
+        self.dtype = {code: dtype for dtype, code in self.code.items()}
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -688,6 +721,108 @@ def experts_few(cfg, weights: MoeWeights, x, topk_idx, topk_w, out, ws, stream=N
         None if topk_w is None else _expect(w, "topk_w", topk_w, (T, k), t.f32, gpu),
         _expect(w, "out", out, (T, d), t.bf16, gpu), *_expect_ws(w, ws, gpu),
         _stream_on(stream, gpu, t)), w)
+
+
+def _expect_rows(where, name, t, T, d, ld, dtype, gpu):
+    """t [T, d] on GPU `gpu` with unit stride inside a row and rows ld elements apart. Its address."""
+    if t.shape != (T, d) or t.dtype is not dtype or t.get_device() != gpu or \
+            (d > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) != ld):
+        raise ValueError(f"{where}: {name} must be a tensor {dtype} {(T, d)} on cuda:{gpu} with strides "
+                         f"{(ld, 1)}, not {t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+    return t.data_ptr()
+
+
+def _norm_params(where, cfg, names, gpu, w_after, b_after, gate, w_before, b_before, rng):
+    d, dtype = cfg.d, names.dtype.get(cfg.w_dtype)
+    p = _NormParams()
+    for name, t in (("w_after", w_after), ("b_after", b_after), ("w_before", w_before),
+                    ("b_before", b_before)):
+        if t is not None:
+            setattr(p, name, _expect(where, name, t, (d,), dtype, gpu))
+    if gate is not None:
+        p.gate = _expect(where, "gate", gate, (_gate_count(cfg), d), dtype, gpu)
+    if rng is not None:
+        p.rng = _expect(where, "rng", rng, (2,), names.i64, gpu)
+    return p
+
+
+def _gate_count(cfg):
+    return -(-cfg.T // cfg.gate_rows) if cfg.gate_rows > 0 else 0
+
+
+def residual_norm(cfg: ResidualNormConfig, h, y, h_out, n, w_after=None, b_after=None, gate=None,
+                  w_before=None, b_before=None, rng=None, stream=None):
+    """h_out = alpha h + beta gate drop(norm_after(y)) and n = norm_before(h_out) (see moe_residual_norm); y,
+    h_out and n may be None as there. rng: int64 [2] on the GPU, seed and step."""
+    w, t = "moe_residual_norm", _names()
+    T, d = cfg.T, cfg.d
+    gpu = _current_gpu(w, "h", h, t)
+    h_type, y_type = t.dtype.get(cfg.h_dtype), t.dtype.get(cfg.y_dtype)
+    p = _norm_params(w, cfg, t, gpu, w_after, b_after, gate, w_before, b_before, rng)
+    _check(lib().moe_residual_norm(
+        ctypes.byref(cfg), _expect_rows(w, "h", h, T, d, cfg.ld_h or d, h_type, gpu),
+        None if y is None else _expect_rows(w, "y", y, T, d, cfg.ld_y or d, y_type, gpu),
+        ctypes.byref(p), None if h_out is None else _expect(w, "h_out", h_out, (T, d), h_type, gpu),
+        None if n is None else _expect(w, "n", n, (T, d), y_type, gpu), _stream_on(stream, gpu, t)), w)
+
+
+def residual_norm_workspace_size(cfg: ResidualNormConfig) -> int:
+    """Bytes that the gradient of up to cfg.T tokens needs."""
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_residual_norm_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_residual_norm_workspace_size")
+    return n.value
+
+
+def residual_norm_backward(cfg: ResidualNormConfig, h_out, y, d_h_out, d_n, d_h, d_y, ws, w_after=None,
+                           b_after=None, gate=None, w_before=None, rng=None, d_w_after=None,
+                           d_b_after=None, d_gate=None, d_w_before=None, d_b_before=None, stream=None):
+    """Gradients of residual_norm (see moe_residual_norm_backward): d_h, d_y and, fp32, those of the
+    parameters that are given; h_out (the stream after the block), y, d_h_out, d_n and d_y may be None as
+    there."""
+    w, t = "moe_residual_norm_backward", _names()
+    T, d = cfg.T, cfg.d
+    gpu = _current_gpu(w, "d_h", d_h, t)
+    h_type, y_type = t.dtype.get(cfg.h_dtype), t.dtype.get(cfg.y_dtype)
+    p = _norm_params(w, cfg, t, gpu, w_after, b_after, gate, w_before, None, rng)
+    g = _NormGrads()
+    for name, grad, shape in (("w_after", d_w_after, (d,)), ("b_after", d_b_after, (d,)),
+                              ("gate", d_gate, (_gate_count(cfg), d)), ("w_before", d_w_before, (d,)),
+                              ("b_before", d_b_before, (d,))):
+        if grad is not None:
+            setattr(g, name, _expect(w, "d_" + name, grad, shape, t.f32, gpu))
+    _check(lib().moe_residual_norm_backward(
+        ctypes.byref(cfg),
+        None if h_out is None else _expect_rows(w, "h_out", h_out, T, d, cfg.ld_h or d, h_type, gpu),
+        None if y is None else _expect_rows(w, "y", y, T, d, cfg.ld_y or d, y_type, gpu),
+        None if d_h_out is None else _expect(w, "d_h_out", d_h_out, (T, d), h_type, gpu),
+        None if d_n is None else _expect(w, "d_n", d_n, (T, d), y_type, gpu), ctypes.byref(p),
+        _expect(w, "d_h", d_h, (T, d), h_type, gpu),
+        None if d_y is None else _expect(w, "d_y", d_y, (T, d), y_type, gpu), ctypes.byref(g),
+        *_expect_ws(w, ws, gpu), _stream_on(stream, gpu, t)), w)
+
+
+def dropout(x, p, rng, y, residual=None, stream=None):
+    """y [T, d] = residual + x / (1 - p) where the element's number is at least p * 2^32, else residual (0 if
+    None); see moe_dropout. rng: int64 [2] on the GPU, seed and step (None where p is 0). The gradient to
+    x is the same call on y's."""
+    w, t = "moe_dropout", _names()
+    if x.dim() != 2:
+        raise ValueError(f"{w}: x of shape {tuple(x.shape)} is not [T, d]")
+    T, d = x.shape
+    gpu = _current_gpu(w, "x", x, t)
+    ld_x, ld_r = (x.stride(0) if T > 1 else d), d
+    if ld_x < d:
+        raise ValueError(f"{w}: rows of x (strides {x.stride()}) share elements")
+    if residual is not None:
+        ld_r = residual.stride(0) if T > 1 and residual.dim() == 2 else d
+        if ld_r < d:
+            raise ValueError(f"{w}: rows of residual (strides {residual.stride()}) share elements")
+    _check(lib().moe_dropout(
+        T, d, _dtype_code(x, w), _expect_rows(w, "x", x, T, d, ld_x, x.dtype, gpu), ld_x, p,
+        None if rng is None else _expect(w, "rng", rng, (2,), t.i64, gpu),
+        None if residual is None else _expect_rows(w, "residual", residual, T, d, ld_r, x.dtype, gpu), ld_r,
+        _expect(w, "y", y, (T, d), x.dtype, gpu), _stream_on(stream, gpu, t)), w)
 
 
 def check_bounded_waits(limit_ns, expired, ws, stream=None):
