@@ -98,6 +98,7 @@ moe_status moe_residual_norm(const moe_residual_norm_config* cfg, const void* h,
   a.b_before = in(params->b_before, d, cfg->w_dtype);
   a.h_out = out(h_out, d, cfg->h_dtype);
   a.n = out(n, d, cfg->y_dtype);
+  a.wide = d % 8 == 0 && a.h.wide && (!y || a.y.wide) && (!h_out || a.h_out.wide) && (!n || a.n.wide);
   a.T = cfg->T;
   a.d = cfg->d;
   a.after = cfg->after;
@@ -106,7 +107,12 @@ moe_status moe_residual_norm(const moe_residual_norm_config* cfg, const void* h,
   a.eps = cfg->eps;
   a.alpha = cfg->alpha;
   a.beta = cfg->beta;
-  return launch_norm(a, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = !a.wide                          ? launch_norm_any(a, st)
+                        : cfg->h_dtype == MOE_DTYPE_F32  ? launch_norm_f32(a, st)
+                        : cfg->h_dtype == MOE_DTYPE_BF16 ? launch_norm_bf16(a, st)
+                                                         : launch_norm_f16(a, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_residual_norm_workspace_size(const moe_residual_norm_config* cfg, size_t* bytes) {
@@ -164,6 +170,8 @@ moe_status moe_residual_norm_backward(const moe_residual_norm_config* cfg, const
   a.d_w_before = grads->w_before;
   a.d_b_before = grads->b_before;
   a.part = static_cast<float*>(ws);
+  a.wide = d % 8 == 0 && a.d_h.wide && (!d_n || (a.h.wide && a.d_n.wide)) && (!d_h_out || a.d_h_out.wide) &&
+           (!y || (a.y.wide && a.d_y.wide));
   a.T = cfg->T;
   a.d = cfg->d;
   a.after = cfg->after;
@@ -172,7 +180,13 @@ moe_status moe_residual_norm_backward(const moe_residual_norm_config* cfg, const
   a.eps = cfg->eps;
   a.alpha = cfg->alpha;
   a.beta = cfg->beta;
-  return launch_norm_grad(a, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  int ctas = 0;
+  cudaError_t e = !a.wide                          ? launch_norm_grad_any(a, &ctas, st)
+                  : cfg->h_dtype == MOE_DTYPE_F32  ? launch_norm_grad_f32(a, &ctas, st)
+                  : cfg->h_dtype == MOE_DTYPE_BF16 ? launch_norm_grad_bf16(a, &ctas, st)
+                                                   : launch_norm_grad_f16(a, &ctas, st);
+  if (e == cudaSuccess) e = launch_norm_join(a, ctas, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_dropout(int32_t T, int32_t d, int32_t dtype, const void* x, int64_t ld_x, float p,
@@ -192,6 +206,7 @@ moe_status moe_dropout(int32_t T, int32_t d, int32_t dtype, const void* x, int64
   a.x = in(x, ld_x ? ld_x : d, dtype);
   a.residual = in(residual, ld_r ? ld_r : d, dtype);
   a.y = out(y, d, dtype);
+  a.wide = d % 8 == 0 && a.x.wide && a.y.wide && (!residual || a.residual.wide);
   a.T = T;
   a.d = d;
   return launch_dropout(a, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -1,0 +1,18 @@
+// Norms around a block for a stream in f16, rows that start on 16 bytes.
+#include "norm_backward.cuh"
+#include "norm_forward.cuh"
+
+namespace moe {
+
+cudaError_t launch_norm_f16(const NormArgs& a, cudaStream_t st) {
+  return a.y.dtype == MOE_DTYPE_F32    ? launch_forward<F16, F32>(a, st)
+         : a.y.dtype == MOE_DTYPE_BF16 ? launch_forward<F16, BF16>(a, st)
+                                       : launch_forward<F16, F16>(a, st);
+}
+cudaError_t launch_norm_grad_f16(const NormGradArgs& a, int* ctas, cudaStream_t st) {
+  return a.y.dtype == MOE_DTYPE_F32    ? launch_backward<F16, F32>(a, ctas, st)
+         : a.y.dtype == MOE_DTYPE_BF16 ? launch_backward<F16, BF16>(a, ctas, st)
+                                       : launch_backward<F16, F16>(a, ctas, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,186 @@
+// Norms before and after a block with residual, gate and dropout (forward).
+//
+//   h' = alpha h + beta gate * drop(norm_after(y)),   n = norm_before(h')
+//
+// One pass: a row is read once, its sums are taken in registers (layer norm's variance in a second sum around
+// the mean), and h' and n are written; the bytes of h, y, h' and n bound it. CTAs are persistent, and while
+// a row is worked on, the next ones' copies are under way. Instructions are close behind the bytes (44 an
+// element is what the SMs issue in the time of 8 bytes): types are the kernel's, not looked up, and a
+// thread has up to 32 channels to pay for a row's sums and addresses.
+#pragma once
+#include "norm_rows.cuh"
+
+namespace moe {
+namespace {
+
+template <int R, int NC>
+constexpr int forward_ctas() {  // per SM: registers for the values of a row
+  return NC == 4 ? 2 : 3;
+}
+
+template <int R, int NC, bool CLUSTER, class H, class Y>
+__global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
+    norm_kernel(const __grid_constant__ NormArgs a, int cl, int stages) {
+  constexpr int kGroups = norm_threads<R>() / R;
+  constexpr bool kAny = std::is_same_v<H, Any>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) float red[kGroups][RowSum<R, CLUSTER>::kFloats];
+  const int group = kGroups == 1 ? 0 : threadIdx.x / R, tid = threadIdx.x % R, lane = tid % 32;
+  const int rank = CLUSTER ? (int)blockIdx.x % cl : 0;
+  const int base = CLUSTER ? rank * norm_width(a.d, cl) : 0;
+  const int d = CLUSTER ? min(a.d, base + norm_width(a.d, cl)) : a.d;  // this CTA's channels end there
+  RowSum<R, CLUSTER> sum(red[group], group, cl);
+  const int w0 = base + tid / 32 * kWarpCols;  // channels of chunk c: w0 + c * R * 8 + lane * 8 + 0..7
+  const bool block = a.y.p != nullptr;
+  // the warp's memory: [stage] of h and y, then `turn`
+  using In = Input<H, R, NC>;
+  using InY = Input<Y, R, NC>;
+  const uint32_t pitch = In::bytes(a.h.dtype) + (block ? InY::bytes(a.y.dtype) : 0);
+  uint8_t* mine = smem + threadIdx.x / 32 * (stages * pitch + (kAny ? kWarpCols * 4 : 0));
+  float* turn = reinterpret_cast<float*>(mine + stages * pitch);
+  In h;
+  InY y;
+  h.init(a.h, w0, lane, ptx::smem_u32(mine));
+  y.init(a.y, w0, lane, ptx::smem_u32(mine) + In::bytes(a.h.dtype));
+  for (int i = 0; i < stages; ++i) {
+    h.clear(w0, lane, d, i * pitch);
+    if (block) y.clear(w0, lane, d, i * pitch);
+  }
+  const int step = (int)(gridDim.x / cl) * kGroups;
+  long long row = (long long)(blockIdx.x / cl) * kGroups + group;
+  const float inv = 1.f / (float)a.d;
+  int col[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) col[c] = w0 + c * R * 8 + lane * 8;
+  griddep_wait();
+  const DropState ds(a.drop);
+  auto bring = [&](long long r, uint32_t stage) {
+    if (r < a.T) {
+      if (block) y.fetch(r, w0, lane, d, stage);
+      h.fetch(r, w0, lane, d, stage);
+    }
+    copies_commit();
+  };
+  for (int i = 0; i < stages; ++i) bring(row + (long long)i * step, i * pitch);
+  uint32_t stage = 0;
+  for (; row < a.T; row += step) {
+    copies_wait_stage(stages);
+    __syncwarp();
+    float x[NC][8];  // y, then h'
+    if (block) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) y.read(c, lane, stage, x[c]);
+      float mean = 0.f, rstd = 1.f;
+      if (a.after != MOE_NORM_NONE)
+        row_stats<NC, kAny>(sum, a.after, x, col, d, inv, a.eps, mean, rstd);
+      const long long gate_row =
+          a.gate.p != nullptr && a.gate_rows < a.T ? (uint32_t)row / (uint32_t)a.gate_rows : 0;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float v[8];
+        if (a.after == MOE_NORM_LAYER) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] = (x[c][i] - mean) * rstd;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] *= rstd;
+        }
+        if (a.w_after.p != nullptr) {
+          param8(a.w_after, 0, col[c], d, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] *= v[i];
+        }
+        if (a.b_after.p != nullptr) {
+          param8(a.b_after, 0, col[c], d, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] += v[i];
+        }
+        if (a.drop.rng != nullptr) drop8(a.drop, ds, (uint32_t)row, (uint32_t)col[c], x[c]);
+        if (a.gate.p != nullptr) {
+          param8(a.gate, gate_row, col[c], d, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] *= v[i];
+        }
+        h.read(c, lane, stage, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[c][i] = fmaf(a.alpha, v[i], a.beta * x[c][i]);
+        if (kAny || a.after == MOE_NORM_LAYER) {
+          // a layer norm leaves something of its mean past the row's end
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] = col[c] + i < d ? x[c][i] : 0.f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        h.read(c, lane, stage, x[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[c][i] *= a.alpha;
+      }
+    }
+    __syncwarp();  // the stage is read; its next row may come
+    bring(row + (long long)stages * step, stage);
+    stage = stage + pitch == stages * pitch ? 0 : stage + pitch;
+    if (a.h_out.p != nullptr) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) store<H>(a.h_out, row, w0 + c * R * 8, lane, d, x[c], turn);
+    }
+    if (a.before != MOE_NORM_NONE) {
+      float mean, rstd;
+      row_stats<NC, kAny>(sum, a.before, x, col, d, inv, a.eps, mean, rstd);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float v[8];
+        if (a.before == MOE_NORM_LAYER) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] = (x[c][i] - mean) * rstd;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] *= rstd;
+        }
+        if (a.w_before.p != nullptr) {
+          param8(a.w_before, 0, col[c], d, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] *= v[i];
+        }
+        if (a.b_before.p != nullptr) {
+          param8(a.b_before, 0, col[c], d, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] += v[i];
+        }
+        store<Y>(a.n, row, w0 + c * R * 8, lane, d, x[c], turn);
+      }
+    }
+  }
+  copies_wait<0>();
+}
+
+template <int R, int NC, bool CLUSTER, class H, class Y>
+cudaError_t launch_form(const NormArgs& a, int cl, cudaStream_t st) {
+  constexpr int threads = norm_threads<R>(), groups = threads / R, per_sm = forward_ctas<R, NC>();
+  const int pitch = Input<H, R, NC>::bytes(a.h.dtype) +
+                    (a.y.p != nullptr ? Input<Y, R, NC>::bytes(a.y.dtype) : 0);
+  const int turn = std::is_same_v<H, Any> ? kWarpCols * 4 : 0;
+  // rows under way: as many as a CTA's share of shared memory holds, four at most
+  int stages = 4;
+  auto smem = [&] { return threads / 32 * (stages * pitch + turn); };
+  while (stages > 1 && smem() > kNormSmem / per_sm - 2048) --stages;
+  const long long need = ((long long)a.T + groups - 1) / groups, most = (long long)per_sm * num_sms() / cl;
+  return launch_rows<CLUSTER>(norm_kernel<R, NC, CLUSTER, H, Y>, (int)(need < most ? need : most) * cl,
+                              threads, smem(), cl, st, a, cl, stages);
+}
+
+template <class H, class Y>
+cudaError_t launch_forward(const NormArgs& a, cudaStream_t st) {
+  const int d = a.d;
+  if (d <= 512) return launch_form<32, 2, false, H, Y>(a, 1, st);
+  if (d <= 2048) return launch_form<128, 2, false, H, Y>(a, 1, st);
+  if (d <= 4096) return launch_form<256, 2, false, H, Y>(a, 1, st);
+  if (d <= 8192) return launch_form<256, 4, false, H, Y>(a, 1, st);
+  int cl = 2;
+  while (norm_width(d, cl) > 8192) cl *= 2;
+  return launch_form<256, 4, true, H, Y>(a, cl, st);
+}
+
+}  // namespace
+}  // namespace moe

@@ -1,0 +1,449 @@
+// Rows of a matrix in a kernel that works on whole rows (norms around a block, dropout): element access, the
+// generator, and sums over a row.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cooperative_groups.h>
+
+#include "norm.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+// -------------------------------------------------------------------------------------- elements
+// Types of elements. Kernels for rows that start on 16 bytes know theirs; Any looks at the argument.
+struct F32 {};
+struct BF16 {};
+struct F16 {};
+struct Any {};
+
+template <class E>
+__host__ __device__ __forceinline__ int bytes_of(int dtype) {
+  if constexpr (std::is_same_v<E, Any>) return dtype == MOE_DTYPE_F32 ? 4 : 2;
+  return std::is_same_v<E, F32> ? 4 : 2;
+}
+
+// Eight elements as they lie in memory: 16-bit ones in a, 32-bit ones in a and b.
+struct Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ void f32_to(const Raw& r, float (&v)[8]) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void bf16_to(const Raw& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void f16_to(const Raw& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <class E>
+__device__ __forceinline__ void to_float(const Raw& r, int dtype, float (&v)[8]) {
+  if constexpr (std::is_same_v<E, F32>) {
+    f32_to(r, v);
+  } else if constexpr (std::is_same_v<E, BF16>) {
+    bf16_to(r, v);
+  } else if constexpr (std::is_same_v<E, F16>) {
+    f16_to(r, v);
+  } else {
+    if (dtype == MOE_DTYPE_F32)
+      f32_to(r, v);
+    else if (dtype == MOE_DTYPE_BF16)
+      bf16_to(r, v);
+    else
+      f16_to(r, v);
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint4 shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// --------------------------------------------------------------------------------------- copies in
+// A thread has chunks of eight channels, a warp 256 channels in a row. Rows come through shared memory of the
+// warp's own, copied asynchronously while the rows before are worked on; no other warp reads them, so there is
+// no barrier but the warp's. Where rows start on 16 bytes a lane copies and stores its own chunk, else the
+// warp moves its 256 elements one per lane at a time.
+constexpr int kWarpCols = 256;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Until the oldest of `stages` groups of copies is there.
+__device__ __forceinline__ void copies_wait_stage(int stages) {
+  if (stages == 4)
+    copies_wait<3>();
+  else if (stages == 3)
+    copies_wait<2>();
+  else if (stages == 2)
+    copies_wait<1>();
+  else
+    copies_wait<0>();
+}
+
+// One input of a warp: where its rows come from and its place in shared memory, [stage][chunk][256] with
+// stages `pitch` bytes apart. E Any: for any alignment.
+template <class E, int R, int NC>
+struct Input {
+  const char* p;      // row 0, this lane's first chunk (Any: the row's start)
+  long long step;     // bytes between rows
+  uint32_t at;        // in shared memory, stage 0, this lane's first chunk (Any: the warp's)
+  int dtype;
+
+  __device__ __forceinline__ void init(const RowsIn& m, int w0, int lane, uint32_t warp_at) {
+    dtype = m.dtype;
+    const int b = bytes_of<E>(dtype);
+    step = m.ld * b;
+    if constexpr (std::is_same_v<E, Any>) {
+      p = static_cast<const char*>(m.p);
+      at = warp_at;
+    } else {
+      p = static_cast<const char*>(m.p) + (long long)(w0 + lane * 8) * b;
+      at = warp_at + lane * 8 * b;
+    }
+  }
+  // Starts the copies of a row. Chunks past d: whole ones stay as clear() left them, elements become 0.
+  __device__ __forceinline__ void fetch(long long row, int w0, int lane, int d, uint32_t stage) const {
+    const char* from = p + row * step;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if constexpr (!std::is_same_v<E, Any>) {
+        constexpr int b = std::is_same_v<E, F32> ? 4 : 2;
+        if (w0 + c * R * 8 + lane * 8 < d) {
+          copy16(at + stage + c * kWarpCols * b, from + c * R * 8 * b);
+          if constexpr (b == 4) copy16(at + stage + c * kWarpCols * b + 16, from + c * R * 8 * b + 16);
+        }
+      } else if (dtype == MOE_DTYPE_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = w0 + c * R * 8 + i * 32 + lane;
+          copy4(at + stage + (c * kWarpCols + i * 32 + lane) * 4, from + (k < d ? k : 0) * 4ll,
+                k < d ? 4 : 0);
+        }
+      } else {  // two bytes cannot be copied asynchronously
+        uint16_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = w0 + c * R * 8 + i * 32 + lane;
+          v[i] = k < d ? reinterpret_cast<const uint16_t*>(from)[k] : (uint16_t)0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + stage + (c * kWarpCols + i * 32 + lane) * 2),
+                       "h"(v[i])
+                       : "memory");
+      }
+    }
+  }
+  // Chunks past d are 0 from the start.
+  __device__ __forceinline__ void clear(int w0, int lane, int d, uint32_t stage) const {
+    if constexpr (!std::is_same_v<E, Any>) {
+      constexpr int b = std::is_same_v<E, F32> ? 4 : 2;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        if (w0 + c * R * 8 + lane * 8 >= d)
+#pragma unroll
+          for (int k = 0; k < b / 2; ++k)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             at + stage + c * kWarpCols * b + 16 * k),
+                         "r"(0)
+                         : "memory");
+    }
+  }
+  // This lane's chunk c.
+  __device__ __forceinline__ void read(int c, int lane, uint32_t stage, float (&v)[8]) const {
+    Raw r;
+    const int b = bytes_of<E>(dtype);
+    uint32_t from = at + stage + c * kWarpCols * b;
+    if constexpr (std::is_same_v<E, Any>) from += lane * 8 * b;
+    r.a = shared16(from);
+    if (b == 4) r.b = shared16(from + 16);
+    to_float<E>(r, dtype, v);
+  }
+  static __host__ __device__ int bytes(int dtype) { return NC * kWarpCols * bytes_of<E>(dtype); }
+};
+
+// -------------------------------------------------------------------------------------- parameters
+// Eight parameters from channel c on, 0 past the d-th. They are small and stay in L1 from row to row.
+__device__ __forceinline__ void param8(const RowsIn& m, long long row, int c, int d, float (&v)[8]) {
+  Raw r = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  const long long at = row * m.ld + c;
+  if (m.wide && c + 8 <= d) {
+    if (m.dtype == MOE_DTYPE_F32) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(m.p) + at);
+      r.a = __ldg(p);
+      r.b = __ldg(p + 1);
+    } else {
+      r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.p) + at));
+    }
+    to_float<Any>(r, m.dtype, v);
+    return;
+  }
+  const bool f32 = m.dtype == MOE_DTYPE_F32;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = 0.f;
+    if (c + i < d) {
+      if (f32) {
+        v[i] = __ldg(static_cast<const float*>(m.p) + at + i);
+      } else {
+        const uint16_t u = __ldg(static_cast<const uint16_t*>(m.p) + at + i);
+        v[i] = m.dtype == MOE_DTYPE_BF16 ? __uint_as_float((uint32_t)u << 16)
+                                         : __half2float(__ushort_as_half(u));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------ stores
+// Eight elements that start on 16 bytes.
+template <class E>
+__device__ __forceinline__ void store_chunk(void* to, int dtype, const float (&v)[8]) {
+  bool f32 = std::is_same_v<E, F32>, bf16 = std::is_same_v<E, BF16>;
+  if constexpr (std::is_same_v<E, Any>) f32 = dtype == MOE_DTYPE_F32, bf16 = dtype == MOE_DTYPE_BF16;
+  if (f32) {
+    static_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    static_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else if (bf16) {
+    *static_cast<uint4*>(to) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
+                                          bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+  } else {
+    *static_cast<uint4*>(to) = make_uint4(f16_pair(v[0], v[1]), f16_pair(v[2], v[3]),
+                                          f16_pair(v[4], v[5]), f16_pair(v[6], v[7]));
+  }
+}
+// A warp's channels [w0, w0 + 256) of a row, eight per lane; `turn` (1 KB of the warp's shared memory) turns
+// them round where they cannot be stored as they are (Any).
+template <class E>
+__device__ __forceinline__ void store(const RowsOut& m, long long row, int w0, int lane, int d,
+                                      const float (&v)[8], float* turn) {
+  const long long at = row * m.ld + w0;
+  if constexpr (!std::is_same_v<E, Any>) {
+    constexpr int b = std::is_same_v<E, F32> ? 4 : 2;
+    if (w0 + lane * 8 < d) store_chunk<E>(static_cast<char*>(m.p) + (at + lane * 8) * b, 0, v);
+    return;
+  }
+  float4* t = reinterpret_cast<float4*>(turn + lane * 8);
+  t[0] = make_float4(v[0], v[1], v[2], v[3]);
+  t[1] = make_float4(v[4], v[5], v[6], v[7]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = i * 32 + lane;
+    if (w0 + c < d) {
+      if (m.dtype == MOE_DTYPE_F32)
+        static_cast<float*>(m.p)[at + c] = turn[c];
+      else
+        static_cast<uint16_t*>(m.p)[at + c] =
+            (uint16_t)(m.dtype == MOE_DTYPE_BF16 ? bf16_pair(turn[c], 0.f) : f16_pair(turn[c], 0.f));
+    }
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------------------------------- dropout
+// Philox 4x32 with ten rounds (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC'11):
+// each round multiplies two words of the counter by constants, and mixes high halves, the other two
+// words and the key, which moves on by a constant. Seed and step in the form the rounds take them:
+struct DropState {
+  uint32_t k0, k1, s0, s1;
+  __device__ explicit DropState(const Drop& d) : k0(0), k1(0), s0(0), s1(0) {
+    if (d.rng != nullptr) {
+      const unsigned long long seed = d.rng[0], step = d.rng[1];
+      k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+      s0 = (uint32_t)step, s1 = (uint32_t)(step >> 32);
+    }
+  }
+};
+// The random numbers of eight elements of a row from channel c (a multiple of 8) on. Two counters at a time:
+// they share the key.
+__device__ __forceinline__ void philox8(const DropState& s, uint32_t row, uint32_t c, uint32_t (&r)[2][4]) {
+  uint32_t k0 = s.k0, k1 = s.k1;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) r[h][0] = (c >> 2) + h, r[h][1] = row, r[h][2] = s.s0, r[h][3] = s.s1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint64_t a = (uint64_t)0xD2511F53u * r[h][0], b = (uint64_t)0xCD9E8D57u * r[h][2];
+      r[h][0] = (uint32_t)(b >> 32) ^ r[h][1] ^ k0;
+      r[h][1] = (uint32_t)b;
+      r[h][2] = (uint32_t)(a >> 32) ^ r[h][3] ^ k1;
+      r[h][3] = (uint32_t)a;
+    }
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+// Eight elements of a row from channel c on, each times the scale or, dropped, 0 whatever it was.
+__device__ __forceinline__ void drop8(const Drop& d, const DropState& s, uint32_t row, uint32_t c,
+                                      float (&v)[8]) {
+  uint32_t r[2][4];
+  philox8(s, row, c, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = r[i >> 2][i & 3] >= d.least ? v[i] * d.scale : 0.f;
+}
+
+// ----------------------------------------------------------------------------------- sums of a row
+// A row is shared by R threads of one CTA, or by all threads of the cl CTAs of a cluster. Sums go over lanes,
+// warps and CTAs in a fixed order.
+template <int R, bool CLUSTER>
+struct RowSum {
+  static constexpr int kW = R / 32, kMost = CLUSTER ? 8 : 0;
+  static constexpr int kBuf = 2 * (kW + kMost);  // of two sums: [sum][warp], then [CTA][sum]
+  static constexpr int kFloats = 2 * kBuf;
+  float* buf;                                    // 16-byte aligned
+  int group, cl, turn;
+
+  __device__ RowSum(float* b, int g, int n) : buf(b), group(g), cl(n), turn(0) {}
+
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    static_assert(N <= 2, "two at a time");
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    if constexpr (R > 32) {
+      const int warp = threadIdx.x % R / 32, lane = threadIdx.x % 32;
+      // two buffers in turn: between two uses of one there is the other's barrier
+      float* b = buf + turn * kBuf;
+      turn ^= 1;
+      if (lane == 0) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) b[n * kW + warp] = v[n];
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(R) : "memory");
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        float part[kW / 4];
+#pragma unroll
+        for (int w = 0; w < kW / 4; ++w) {
+          const float4 q = *reinterpret_cast<const float4*>(b + n * kW + 4 * w);
+          part[w] = (q.x + q.y) + (q.z + q.w);
+        }
+#pragma unroll
+        for (int w = 1; w < kW / 4; ++w) part[0] += part[w];
+        v[n] = part[0];
+      }
+      if constexpr (CLUSTER) {
+        namespace cg = cooperative_groups;
+        cg::cluster_group cluster = cg::this_cluster();
+        if (threadIdx.x < cl) {
+          float* there = cluster.map_shared_rank(b + kW * 2, threadIdx.x);
+#pragma unroll
+          for (int n = 0; n < N; ++n) there[cluster.block_rank() * 2 + n] = v[n];
+        }
+        cluster.sync();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          v[n] = 0.f;
+          for (int i = 0; i < cl; ++i) v[n] += b[kW * 2 + i * 2 + n];
+        }
+      }
+    }
+  }
+};
+
+// Mean (0 for rms) and one over the deviation of a row (inv: one over its channels) whose threads hold x. What
+// is past the channels that end at d is 0 in x and does not count; EDGE: a chunk may lie across the end.
+template <int NC, bool EDGE, typename Sum>
+__device__ __forceinline__ void row_stats(Sum& sum, int kind, const float (&x)[NC][8], const int (&col)[NC],
+                                          int d, float inv, float eps, float& mean, float& rstd) {
+  mean = 0.f;
+  float q[1] = {0.f};
+  if (kind == MOE_NORM_LAYER) {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += x[c][i];
+    sum(s);
+    mean = s[0] * inv;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (col[c] < d) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float v = !EDGE || col[c] + i < d ? x[c][i] - mean : 0.f;
+          q[0] = fmaf(v, v, q[0]);
+        }
+      }
+  } else {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[0] = fmaf(x[c][i], x[c][i], q[0]);
+  }
+  sum(q);
+  rstd = 1.f / sqrtf(fmaf(q[0], inv, eps));
+}
+
+// How a row is shared: R threads with NC chunks of eight channels each, above 8192 channels a cluster.
+template <int R>
+__host__ __device__ constexpr int norm_threads() {
+  return R < 256 ? 256 : R;
+}
+// Channels of a CTA of a cluster of cl.
+__host__ __device__ __forceinline__ int norm_width(int d, int cl) { return ((d + 7) / 8 + cl - 1) / cl * 8; }
+
+// Launches a kernel of rows: programmatic stream serialization (it waits before it touches memory), and a
+// cluster of cl CTAs where it wants one.
+template <bool CLUSTER, typename... K, typename... A>
+cudaError_t launch_rows(void (*kernel)(K...), int grid, int threads, int smem, int cl, cudaStream_t st,
+                        A&&... args) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem - 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cl;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+}  // namespace moe
