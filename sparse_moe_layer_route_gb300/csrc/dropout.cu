@@ -41,22 +41,21 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
     Raw r;
     if (a.residual.p != nullptr)
       r = stream8<E>(static_cast<const char*>(a.residual.p) + (row * a.residual.ld + c) * b);
-    float v[8], s[8];
+    F2 v[4], s[4];
     if (a.drop.rng != nullptr) {
       uint32_t n[2][4];
       philox8(ds, (uint32_t)row, (uint32_t)c, n);  // while x is on its way
       to_float<E>(x, 0, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = n[i >> 2][i & 3] >= a.drop.least ? v[i] * a.drop.scale : 0.f;
+      each(v, [&](int i, float t) { return n[i >> 2][i & 3] >= a.drop.least ? t * a.drop.scale : 0.f; });
     } else {
       to_float<E>(x, 0, v);
     }
     if (a.residual.p != nullptr) {
       to_float<E>(r, 0, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += s[i];
+      for (int i = 0; i < 4; ++i) v[i] = add2(v[i], s[i]);
     }
-    store_chunk<E>(static_cast<char*>(a.y.p) + (row * a.y.ld + c) * b, 0, v);
+    store_chunk<E>(static_cast<char*>(a.y.p) + (row * a.y.ld + c) * b, v);
     row += hop_rows;
     k += hop_chunks;
     if (k >= chunks) {
@@ -83,7 +82,8 @@ __global__ void __launch_bounds__(kThreads) dropout_any_kernel(const __grid_cons
   for (long long t = (long long)blockIdx.x * (kThreads / 32) + warp; t < tiles; t += step) {
     const long long row = t / across;
     const int w0 = (int)(t - row * across) * kWarpCols;
-    float in[8], res[8], v[8];
+    float in[8], res[8];
+    F2 v[4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = w0 + i * 32 + lane;
@@ -94,11 +94,10 @@ __global__ void __launch_bounds__(kThreads) dropout_any_kernel(const __grid_cons
     for (int i = 0; i < 8; ++i) x[i * 32 + lane] = in[i], r[i * 32 + lane] = res[i];
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = x[lane * 8 + i];
+    for (int i = 0; i < 4; ++i) v[i] = pair(x[lane * 8 + 2 * i], x[lane * 8 + 2 * i + 1]);
     if (a.drop.rng != nullptr) drop8(a.drop, ds, (uint32_t)row, (uint32_t)(w0 + lane * 8), v);
     if (a.residual.p != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += r[lane * 8 + i];
+      each(v, [&](int i, float t) { return t + r[lane * 8 + i]; });
     }
     __syncwarp();
     store<Any>(a.y, row, w0, lane, a.d, v, x);

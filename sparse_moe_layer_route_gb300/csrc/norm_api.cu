@@ -99,6 +99,8 @@ moe_status moe_residual_norm(const moe_residual_norm_config* cfg, const void* h,
   a.h_out = out(h_out, d, cfg->h_dtype);
   a.n = out(n, d, cfg->y_dtype);
   a.wide = d % 8 == 0 && a.h.wide && (!y || a.y.wide) && (!h_out || a.h_out.wide) && (!n || a.n.wide);
+  for (const RowsIn& m : {a.w_after, a.b_after, a.gate, a.w_before, a.b_before})
+    a.wide = a.wide && (m.p == nullptr || m.wide);
   a.T = cfg->T;
   a.d = cfg->d;
   a.after = cfg->after;
@@ -171,7 +173,9 @@ moe_status moe_residual_norm_backward(const moe_residual_norm_config* cfg, const
   a.d_b_before = grads->b_before;
   a.part = static_cast<float*>(ws);
   a.wide = d % 8 == 0 && a.d_h.wide && (!d_n || (a.h.wide && a.d_n.wide)) && (!d_h_out || a.d_h_out.wide) &&
-           (!y || (a.y.wide && a.d_y.wide));
+           (!y || (a.y.wide && a.d_y.wide)) && wide(grads->gate, d, MOE_DTYPE_F32);
+  for (const RowsIn& m : {a.w_after, a.b_after, a.gate, a.w_before})
+    a.wide = a.wide && (m.p == nullptr || m.wide);
   a.T = cfg->T;
   a.d = cfg->d;
   a.after = cfg->after;

@@ -25,25 +25,27 @@ constexpr int stage_bytes() {
   return norm_threads<R>() == R ? 0 : norm_threads<R>() * NC * 8 * 4;
 }
 template <int R, int NC>
-__device__ __forceinline__ void flush(const float (&acc)[NC][8], float* stage, int group, int w0, int lane,
+__device__ __forceinline__ void flush(const F2 (&acc)[NC][4], float* stage, int group, int w0, int lane,
                                       int first, int d, float* dst) {
   constexpr int kGroups = norm_threads<R>() / R, kWidth = R * NC * 8;
   if constexpr (kGroups == 1) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int k = w0 + c * R * 8 + lane * 8 + i;
-        if (k < d) dst[k] = acc[c][i];
+      for (int i = 0; i < 4; ++i) {
+        const int k = w0 + c * R * 8 + lane * 8 + 2 * i;
+        const float2 v = both(acc[c][i]);
+        if (k < d) dst[k] = v.x;
+        if (k + 1 < d) dst[k + 1] = v.y;
       }
     return;
   }
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    float4* to = reinterpret_cast<float4*>(stage + group * kWidth + w0 - first + c * R * 8 + lane * 8);
-    to[0] = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
-    to[1] = make_float4(acc[c][4], acc[c][5], acc[c][6], acc[c][7]);
+    F2* to = reinterpret_cast<F2*>(stage + group * kWidth + w0 - first + c * R * 8 + lane * 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = acc[c][i];
   }
   __syncthreads();
   for (int k = threadIdx.x; first + k < d && k < kWidth; k += norm_threads<R>()) {
@@ -55,22 +57,52 @@ __device__ __forceinline__ void flush(const float (&acc)[NC][8], float* stage, i
 }
 
 // v added to a lane's eight sums in shared memory, 16 bytes of every lane side by side.
-__device__ __forceinline__ void add_shared(float* sums, int lane, const float (&v)[8]) {
-  float4* at = reinterpret_cast<float4*>(sums) + lane;
+__device__ __forceinline__ void add_shared(float* sums, int lane, const F2 (&v)[4]) {
+  ulonglong2* at = reinterpret_cast<ulonglong2*>(sums) + lane;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    float4 s = at[32 * k];
-    s.x += v[4 * k], s.y += v[4 * k + 1], s.z += v[4 * k + 2], s.w += v[4 * k + 3];
+    ulonglong2 s = at[32 * k];
+    s.x = add2(s.x, v[2 * k]);
+    s.y = add2(s.y, v[2 * k + 1]);
     at[32 * k] = s;
   }
 }
-__device__ __forceinline__ void get_shared(const float* sums, int lane, float (&v)[8]) {
-  const float4* at = reinterpret_cast<const float4*>(sums) + lane;
+__device__ __forceinline__ void get_shared(const float* sums, int lane, F2 (&v)[4]) {
+  const ulonglong2* at = reinterpret_cast<const ulonglong2*>(sums) + lane;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const float4 s = at[32 * k];
-    v[4 * k] = s.x, v[4 * k + 1] = s.y, v[4 * k + 2] = s.z, v[4 * k + 3] = s.w;
+    const ulonglong2 s = at[32 * k];
+    v[2 * k] = s.x;
+    v[2 * k + 1] = s.y;
   }
+}
+
+// A thread's share of sum(g x) and, for a layer norm, sum(g).
+template <int NC>
+__device__ __forceinline__ void sums_of(const F2 (&g)[NC][4], const F2 (&x)[NC][4], bool layer, float (&m)[2]) {
+  F2 s[2] = {0, 0}, t[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i & 1] = fma2(g[c][i], x[c][i], s[i & 1]);
+  if (layer) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i & 1] = add2(g[c][i], t[i & 1]);
+  }
+  const float2 a = both(add2(s[0], s[1])), b = both(add2(t[0], t[1]));
+  m[0] = a.x + a.y;
+  m[1] = b.x + b.y;
+}
+// g = r (g - x p - q): a gradient to normed values x becomes one to what was normed.
+template <int NC>
+__device__ __forceinline__ void through_norm(F2 (&g)[NC][4], const F2 (&x)[NC][4], float p, float q, float r) {
+  const F2 np = twice(-p), nq = twice(-q), rr = twice(r);
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[c][i] = mul2(rr, add2(g[c][i], fma2(x[c][i], np, nq)));
 }
 
 // Shared memory of a CTA: what flush needs, and for each warp the biases' sums, `stages` rows of its inputs and
@@ -172,7 +204,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
   };
   for (int i = 0; i < stages; ++i) bring(i * pitch);
   uint32_t stage = 0;
-  float wa[NC][8] = {}, wb[NC][8] = {}, ga[NC][8] = {};
+  F2 wa[NC][4] = {}, wb[NC][4] = {}, ga[NC][4] = {};
   int col[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) col[c] = w0 + c * R * 8 + lane * 8;
@@ -181,130 +213,129 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
     for (long long row = s0 + group; row < s1; row += kGroups) {
       copies_wait_stage(stages);
       __syncwarp();
-      float g[NC][8];
+      F2 g[NC][4];
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[c][i] = 0.f;
+        for (int i = 0; i < 4; ++i) g[c][i] = 0;
       if (normed) {
-        float h[NC][8];
+        F2 h[NC][4];
 #pragma unroll
         for (int c = 0; c < NC; ++c) h_in.read(c, lane, stage, h[c]);
         float mean, rstd;
         row_stats<NC, kAny>(sum, a.before, h, col, d, inv, a.eps, mean, rstd);
-        float m[2] = {0.f, 0.f};
+        scale_rows<NC>(h, a.before == MOE_NORM_LAYER, mean, rstd);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           n_in.read(c, lane, stage, g[c]);
-          if (a.d_b_before != nullptr) add_shared(sums_bb + c * kWarpCols, lane, g[c]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            h[c][i] = (h[c][i] - mean) * rstd;
-            wb[c][i] = fmaf(g[c][i], h[c][i], wb[c][i]);
-          }
-          if (a.w_before.p != nullptr) {
-            float v[8];
-            param8(a.w_before, 0, col[c], d, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[c][i] *= v[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m[0] = fmaf(g[c][i], h[c][i], m[0]);
-          if (a.before == MOE_NORM_LAYER) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m[1] += g[c][i];
-          }
+          for (int i = 0; i < 4; ++i) wb[c][i] = fma2(g[c][i], h[c][i], wb[c][i]);
         }
+        if (a.d_b_before != nullptr) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) add_shared(sums_bb + c * kWarpCols, lane, g[c]);
+        }
+        if (a.w_before.p != nullptr) times_params<kAny>(a.w_before, 0, col, d, g);
+        float m[2];
+        sums_of<NC>(g, h, a.before == MOE_NORM_LAYER, m);
         sum(m);
-        m[0] *= inv;
-        m[1] *= inv;
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) g[c][i] = rstd * (g[c][i] - fmaf(h[c][i], m[0], m[1]));
+        through_norm<NC>(g, h, m[0] * inv, m[1] * inv, rstd);
       }
+      if (direct) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float v[8];
-        if (direct) {
+        for (int c = 0; c < NC; ++c) {
+          F2 v[4];
           g_in.read(c, lane, stage, v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[c][i] += v[i];
+          for (int i = 0; i < 4; ++i) g[c][i] = add2(g[c][i], v[i]);
         }
+      }
+      {
+        const F2 alpha = twice(a.alpha);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = a.alpha * g[c][i];
-        store<H>(a.d_h, row, w0 + c * R * 8, lane, d, v, turn);
+        for (int c = 0; c < NC; ++c) {
+          F2 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = mul2(alpha, g[c][i]);
+          store<H>(a.d_h, row, w0 + c * R * 8, lane, d, v, turn);
+        }
       }
       if (block) {
-        float y[NC][8];
+        F2 y[NC][4];
 #pragma unroll
         for (int c = 0; c < NC; ++c) y_in.read(c, lane, stage, y[c]);
         float mean = 0.f, rstd = 1.f;
-        if (a.after != MOE_NORM_NONE)
+        if (a.after != MOE_NORM_NONE) {
           row_stats<NC, kAny>(sum, a.after, y, col, d, inv, a.eps, mean, rstd);
-        const long long gate_row =
-            a.gate.p != nullptr && a.gate_rows < a.T ? (uint32_t)row / (uint32_t)a.gate_rows : 0;
-        float m[2] = {0.f, 0.f};
+          scale_rows<NC>(y, a.after == MOE_NORM_LAYER, mean, rstd);
+        }
+        const F2 beta = twice(a.beta);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          float v[8], w[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            y[c][i] = (y[c][i] - mean) * rstd;
-            g[c][i] *= a.beta;
-          }
+          for (int i = 0; i < 4; ++i) g[c][i] = mul2(g[c][i], beta);
           if (a.drop.rng != nullptr) drop8(a.drop, ds, (uint32_t)row, (uint32_t)col[c], g[c]);
+        }
+        if (a.gate.p != nullptr) {
+          const uint32_t gate_row = a.gate_rows < a.T ? (uint32_t)row / (uint32_t)a.gate_rows : 0;
+          if (a.d_gate != nullptr) {
+            F2 u[NC][4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = 1.f;
-          if (a.w_after.p != nullptr) param8(a.w_after, 0, col[c], d, w);
-          if (a.gate.p != nullptr) {
-            if (a.d_gate != nullptr) {
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = 0.f;
-              if (a.b_after.p != nullptr) param8(a.b_after, 0, col[c], d, v);
+              for (int i = 0; i < 4; ++i) u[c][i] = y[c][i];
+            if (a.w_after.p != nullptr) times_params<kAny>(a.w_after, 0, col, d, u);
+            if (a.b_after.p != nullptr)
+              with_params<kAny>(a.b_after, 0, col, d, [&](int c, const F2 (&w)[4]) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                // a dropped element is 0 whatever u is
-                const float u = fmaf(y[c][i], w[i], v[i]);
-                v[i] = g[c][i] != 0.f ? g[c][i] * u : 0.f;
-              }
-              if (sum_gates) {
+                for (int i = 0; i < 4; ++i) u[c][i] = add2(u[c][i], w[i]);
+              });
+            if (a.drop.rng != nullptr) {  // a dropped element is 0 whatever u is
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ga[c][i] += v[i];
-              } else {
-                const RowsOut out{a.d_gate, a.d, MOE_DTYPE_F32, true};
-                store<std::conditional_t<kAny, Any, F32>>(out, row, w0 + c * R * 8, lane, d, v, turn);
+              for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 e = both(g[c][i]), v = both(u[c][i]);
+                  u[c][i] = pair(e.x != 0.f ? v.x : 0.f, e.y != 0.f ? v.y : 0.f);
+                }
+            }
+            if (sum_gates) {
+#pragma unroll
+              for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ga[c][i] = fma2(g[c][i], u[c][i], ga[c][i]);
+            } else {
+              const RowsOut out{a.d_gate, a.d, MOE_DTYPE_F32, true};
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[c][i] = mul2(g[c][i], u[c][i]);
+                store<std::conditional_t<kAny, Any, F32>>(out, row, w0 + c * R * 8, lane, d, u[c], turn);
               }
             }
-            param8(a.gate, gate_row, col[c], d, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[c][i] *= v[i];
           }
-          // what is past the row's end adds nothing to its means
-          if (kAny || a.after == MOE_NORM_LAYER || a.before == MOE_NORM_LAYER) {
+          times_params<kAny>(a.gate, gate_row, col, d, g);
+        }
+        // what is past the row's end adds nothing to its means
+        if (kAny || a.after == MOE_NORM_LAYER || a.before == MOE_NORM_LAYER) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g[c][i] = col[c] + i < d ? g[c][i] : 0.f;
-          }
-          if (a.d_b_after != nullptr) add_shared(sums_ba + c * kWarpCols, lane, g[c]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            wa[c][i] = fmaf(g[c][i], y[c][i], wa[c][i]);
-            g[c][i] *= w[i];
-            m[0] = fmaf(g[c][i], y[c][i], m[0]);
-          }
-          if (a.after == MOE_NORM_LAYER) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m[1] += g[c][i];
-          }
+          for (int c = 0; c < NC; ++c)
+            if (kAny || col[c] >= d) each(g[c], [&](int i, float v) { return col[c] + i < d ? v : 0.f; });
         }
         if (a.after != MOE_NORM_NONE) {
-          sum(m);
-          m[0] *= inv;
-          m[1] *= inv;
 #pragma unroll
           for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g[c][i] = rstd * (g[c][i] - fmaf(y[c][i], m[0], m[1]));
+            for (int i = 0; i < 4; ++i) wa[c][i] = fma2(g[c][i], y[c][i], wa[c][i]);
+          if (a.d_b_after != nullptr) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) add_shared(sums_ba + c * kWarpCols, lane, g[c]);
+          }
+          if (a.w_after.p != nullptr) times_params<kAny>(a.w_after, 0, col, d, g);
+          float m[2];
+          sums_of<NC>(g, y, a.after == MOE_NORM_LAYER, m);
+          sum(m);
+          through_norm<NC>(g, y, m[0] * inv, m[1] * inv, rstd);
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -322,7 +353,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ga[c][i] = 0.f;
+        for (int i = 0; i < 4; ++i) ga[c][i] = 0;
     }
     s0 = s1;
   }

@@ -66,56 +66,52 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
   for (; row < a.T; row += step) {
     copies_wait_stage(stages);
     __syncwarp();
-    float x[NC][8];  // y, then h'
+    F2 x[NC][4];  // y, then h'
     if (block) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) y.read(c, lane, stage, x[c]);
       float mean = 0.f, rstd = 1.f;
       if (a.after != MOE_NORM_NONE)
         row_stats<NC, kAny>(sum, a.after, x, col, d, inv, a.eps, mean, rstd);
-      const long long gate_row =
-          a.gate.p != nullptr && a.gate_rows < a.T ? (uint32_t)row / (uint32_t)a.gate_rows : 0;
+      // beta goes with the deviation, and with the bias below
+      scale_rows<NC>(x, a.after == MOE_NORM_LAYER, mean, rstd * a.beta);
+      if (a.w_after.p != nullptr) times_params<kAny>(a.w_after, 0, col, d, x);
+      if (a.b_after.p != nullptr) {
+        const F2 beta = twice(a.beta);
+        with_params<kAny>(a.b_after, 0, col, d, [&](int c, const F2 (&w)[4]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[c][i] = fma2(w[i], beta, x[c][i]);
+        });
+      }
+      if (a.drop.rng != nullptr) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) drop8(a.drop, ds, (uint32_t)row, (uint32_t)col[c], x[c]);
+      }
+      if (a.gate.p != nullptr) {
+        const uint32_t gate_row = a.gate_rows < a.T ? (uint32_t)row / (uint32_t)a.gate_rows : 0;
+        times_params<kAny>(a.gate, gate_row, col, d, x);
+      }
+      const F2 alpha = twice(a.alpha);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        float v[8];
-        if (a.after == MOE_NORM_LAYER) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] = (x[c][i] - mean) * rstd;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] *= rstd;
-        }
-        if (a.w_after.p != nullptr) {
-          param8(a.w_after, 0, col[c], d, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] *= v[i];
-        }
-        if (a.b_after.p != nullptr) {
-          param8(a.b_after, 0, col[c], d, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] += v[i];
-        }
-        if (a.drop.rng != nullptr) drop8(a.drop, ds, (uint32_t)row, (uint32_t)col[c], x[c]);
-        if (a.gate.p != nullptr) {
-          param8(a.gate, gate_row, col[c], d, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] *= v[i];
-        }
+        F2 v[4];
         h.read(c, lane, stage, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[c][i] = fmaf(a.alpha, v[i], a.beta * x[c][i]);
-        if (kAny || a.after == MOE_NORM_LAYER) {
-          // a layer norm leaves something of its mean past the row's end
+        for (int i = 0; i < 4; ++i) x[c][i] = fma2(alpha, v[i], x[c][i]);
+      }
+      if (kAny || a.after == MOE_NORM_LAYER) {
+        // a layer norm leaves something of its mean past the row's end
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] = col[c] + i < d ? x[c][i] : 0.f;
-        }
+        for (int c = 0; c < NC; ++c)
+          if (kAny || col[c] >= d) each(x[c], [&](int i, float v) { return col[c] + i < d ? v : 0.f; });
       }
     } else {
+      const F2 alpha = twice(a.alpha);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         h.read(c, lane, stage, x[c]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[c][i] *= a.alpha;
+        for (int i = 0; i < 4; ++i) x[c][i] = mul2(alpha, x[c][i]);
       }
     }
     __syncwarp();  // the stage is read; its next row may come
@@ -128,28 +124,15 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
     if (a.before != MOE_NORM_NONE) {
       float mean, rstd;
       row_stats<NC, kAny>(sum, a.before, x, col, d, inv, a.eps, mean, rstd);
+      scale_rows<NC>(x, a.before == MOE_NORM_LAYER, mean, rstd);
+      if (a.w_before.p != nullptr) times_params<kAny>(a.w_before, 0, col, d, x);
+      if (a.b_before.p != nullptr)
+        with_params<kAny>(a.b_before, 0, col, d, [&](int c, const F2 (&w)[4]) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float v[8];
-        if (a.before == MOE_NORM_LAYER) {
+          for (int i = 0; i < 4; ++i) x[c][i] = add2(x[c][i], w[i]);
+        });
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] = (x[c][i] - mean) * rstd;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] *= rstd;
-        }
-        if (a.w_before.p != nullptr) {
-          param8(a.w_before, 0, col[c], d, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] *= v[i];
-        }
-        if (a.b_before.p != nullptr) {
-          param8(a.b_before, 0, col[c], d, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] += v[i];
-        }
-        store<Y>(a.n, row, w0 + c * R * 8, lane, d, x[c], turn);
-      }
+      for (int c = 0; c < NC; ++c) store<Y>(a.n, row, w0 + c * R * 8, lane, d, x[c], turn);
     }
   }
   copies_wait<0>();

@@ -23,34 +23,71 @@ __host__ __device__ __forceinline__ int bytes_of(int dtype) {
   return std::is_same_v<E, F32> ? 4 : 2;
 }
 
+// Two floats as the instructions on pairs take them: one issue for two results.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ F2 twice(float a) { return pair(a, a); }
+__device__ __forceinline__ float2 both(F2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+// A thread's chunk of eight channels.
+using Chunk = F2[4];
+// f(i, value) for the eight channels of a chunk, whose value becomes what f returns.
+template <class F>
+__device__ __forceinline__ void each(F2 (&v)[4], F f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = both(v[i]);
+    v[i] = pair(f(2 * i, x.x), f(2 * i + 1, x.y));
+  }
+}
+
 // Eight elements as they lie in memory: 16-bit ones in a, 32-bit ones in a and b.
 struct Raw {
   uint4 a, b;
 };
-__device__ __forceinline__ void f32_to(const Raw& r, float (&v)[8]) {
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+__device__ __forceinline__ void f32_to(const Raw& r, F2 (&v)[4]) {
+  v[0] = pair(__uint_as_float(r.a.x), __uint_as_float(r.a.y));
+  v[1] = pair(__uint_as_float(r.a.z), __uint_as_float(r.a.w));
+  v[2] = pair(__uint_as_float(r.b.x), __uint_as_float(r.b.y));
+  v[3] = pair(__uint_as_float(r.b.z), __uint_as_float(r.b.w));
 }
-__device__ __forceinline__ void bf16_to(const Raw& r, float (&v)[8]) {
+__device__ __forceinline__ void bf16_to(const Raw& r, F2 (&v)[4]) {
   const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ void f16_to(const Raw& r, float (&v)[8]) {
+__device__ __forceinline__ void f16_to(const Raw& r, F2 (&v)[4]) {
   const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+    v[i] = pair(f.x, f.y);
   }
 }
 template <class E>
-__device__ __forceinline__ void to_float(const Raw& r, int dtype, float (&v)[8]) {
+__device__ __forceinline__ void to_float(const Raw& r, int dtype, F2 (&v)[4]) {
   if constexpr (std::is_same_v<E, F32>) {
     f32_to(r, v);
   } else if constexpr (std::is_same_v<E, BF16>) {
@@ -74,6 +111,14 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t bf16_pair(F2 v) {
+  const float2 f = both(v);
+  return bf16_pair(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t f16_pair(F2 v) {
+  const float2 f = both(v);
+  return f16_pair(f.x, f.y);
 }
 
 __device__ __forceinline__ uint4 shared16(uint32_t addr) {
@@ -186,7 +231,7 @@ struct Input {
     }
   }
   // This lane's chunk c.
-  __device__ __forceinline__ void read(int c, int lane, uint32_t stage, float (&v)[8]) const {
+  __device__ __forceinline__ void read(int c, int lane, uint32_t stage, F2 (&v)[4]) const {
     Raw r;
     const int b = bytes_of<E>(dtype);
     uint32_t from = at + stage + c * kWarpCols * b;
@@ -199,68 +244,124 @@ struct Input {
 };
 
 // -------------------------------------------------------------------------------------- parameters
-// Eight parameters from channel c on, 0 past the d-th. They are small and stay in L1 from row to row.
-__device__ __forceinline__ void param8(const RowsIn& m, long long row, int c, int d, float (&v)[8]) {
-  Raw r = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  const long long at = row * m.ld + c;
-  if (m.wide && c + 8 <= d) {
-    if (m.dtype == MOE_DTYPE_F32) {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(m.p) + at);
-      r.a = __ldg(p);
-      r.b = __ldg(p + 1);
-    } else {
-      r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.p) + at));
-    }
-    to_float<Any>(r, m.dtype, v);
-    return;
-  }
-  const bool f32 = m.dtype == MOE_DTYPE_F32;
+// op(c, w) for every chunk c of a thread and its parameters w (0 past the d-th channel). They are small and stay
+// in L1 from row to row; all chunks' are under way before the first is used. ANY: of any alignment.
+template <bool ANY, int NC, class Op>
+__device__ __forceinline__ void with_params(const RowsIn& m, long long row, const int (&col)[NC], int d,
+                                            Op op) {
+  if constexpr (ANY) {
+    const bool f32 = m.dtype == MOE_DTYPE_F32;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = 0.f;
-    if (c + i < d) {
-      if (f32) {
-        v[i] = __ldg(static_cast<const float*>(m.p) + at + i);
-      } else {
-        const uint16_t u = __ldg(static_cast<const uint16_t*>(m.p) + at + i);
-        v[i] = m.dtype == MOE_DTYPE_BF16 ? __uint_as_float((uint32_t)u << 16)
-                                         : __half2float(__ushort_as_half(u));
+    for (int c = 0; c < NC; ++c) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const long long at = row * m.ld + col[c] + i;
+        v[i] = 0.f;
+        if (col[c] + i < d) {
+          if (f32) {
+            v[i] = __ldg(static_cast<const float*>(m.p) + at);
+          } else {
+            const uint16_t u = __ldg(static_cast<const uint16_t*>(m.p) + at);
+            v[i] = m.dtype == MOE_DTYPE_BF16 ? __uint_as_float((uint32_t)u << 16)
+                                             : __half2float(__ushort_as_half(u));
+          }
+        }
+      }
+      const F2 w[4] = {pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])};
+      op(c, w);
+    }
+  } else if (m.dtype == MOE_DTYPE_F32) {
+    const float* p = static_cast<const float*>(m.p) + row * m.ld;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      Raw r = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (col[c] < d) {
+        r.a = __ldg(reinterpret_cast<const uint4*>(p + col[c]));
+        r.b = __ldg(reinterpret_cast<const uint4*>(p + col[c]) + 1);
+      }
+      F2 w[4];
+      f32_to(r, w);
+      op(c, w);
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(m.p) + row * m.ld;
+    Raw r[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      r[c].a = col[c] < d ? __ldg(reinterpret_cast<const uint4*>(p + col[c])) : make_uint4(0u, 0u, 0u, 0u);
+    if (m.dtype == MOE_DTYPE_BF16) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        F2 w[4];
+        bf16_to(r[c], w);
+        op(c, w);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        F2 w[4];
+        f16_to(r[c], w);
+        op(c, w);
       }
     }
   }
 }
 
+// x times the parameters, chunk by chunk.
+template <bool ANY, int NC>
+__device__ __forceinline__ void times_params(const RowsIn& m, long long row, const int (&col)[NC], int d,
+                                             F2 (&x)[NC][4]) {
+  with_params<ANY>(m, row, col, d, [&](int c, const F2 (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[c][i] = mul2(x[c][i], w[i]);
+  });
+}
+
+// (x - mean) * scale; centred: there is a mean.
+template <int NC>
+__device__ __forceinline__ void scale_rows(F2 (&x)[NC][4], bool centred, float mean, float scale) {
+  const F2 m = twice(-mean), s = twice(scale);
+  if (centred) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[c][i] = add2(x[c][i], m);
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[c][i] = mul2(x[c][i], s);
+}
+
 // ------------------------------------------------------------------------------------------ stores
 // Eight elements that start on 16 bytes.
 template <class E>
-__device__ __forceinline__ void store_chunk(void* to, int dtype, const float (&v)[8]) {
-  bool f32 = std::is_same_v<E, F32>, bf16 = std::is_same_v<E, BF16>;
-  if constexpr (std::is_same_v<E, Any>) f32 = dtype == MOE_DTYPE_F32, bf16 = dtype == MOE_DTYPE_BF16;
-  if (f32) {
-    static_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    static_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else if (bf16) {
-    *static_cast<uint4*>(to) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
-                                          bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+__device__ __forceinline__ void store_chunk(void* to, const F2 (&v)[4]) {
+  if constexpr (std::is_same_v<E, F32>) {
+    const float2 a = both(v[0]), b = both(v[1]), c = both(v[2]), d = both(v[3]);
+    static_cast<float4*>(to)[0] = make_float4(a.x, a.y, b.x, b.y);
+    static_cast<float4*>(to)[1] = make_float4(c.x, c.y, d.x, d.y);
+  } else if constexpr (std::is_same_v<E, BF16>) {
+    *static_cast<uint4*>(to) = make_uint4(bf16_pair(v[0]), bf16_pair(v[1]), bf16_pair(v[2]), bf16_pair(v[3]));
   } else {
-    *static_cast<uint4*>(to) = make_uint4(f16_pair(v[0], v[1]), f16_pair(v[2], v[3]),
-                                          f16_pair(v[4], v[5]), f16_pair(v[6], v[7]));
+    *static_cast<uint4*>(to) = make_uint4(f16_pair(v[0]), f16_pair(v[1]), f16_pair(v[2]), f16_pair(v[3]));
   }
 }
 // A warp's channels [w0, w0 + 256) of a row, eight per lane; `turn` (1 KB of the warp's shared memory) turns
 // them round where they cannot be stored as they are (Any).
 template <class E>
 __device__ __forceinline__ void store(const RowsOut& m, long long row, int w0, int lane, int d,
-                                      const float (&v)[8], float* turn) {
+                                      const F2 (&v)[4], float* turn) {
   const long long at = row * m.ld + w0;
   if constexpr (!std::is_same_v<E, Any>) {
     constexpr int b = std::is_same_v<E, F32> ? 4 : 2;
-    if (w0 + lane * 8 < d) store_chunk<E>(static_cast<char*>(m.p) + (at + lane * 8) * b, 0, v);
+    if (w0 + lane * 8 < d) store_chunk<E>(static_cast<char*>(m.p) + (at + lane * 8) * b, v);
     return;
   }
-  float4* t = reinterpret_cast<float4*>(turn + lane * 8);
-  t[0] = make_float4(v[0], v[1], v[2], v[3]);
-  t[1] = make_float4(v[4], v[5], v[6], v[7]);
+  F2* t = reinterpret_cast<F2*>(turn + lane * 8);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = v[i];
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -312,11 +413,10 @@ __device__ __forceinline__ void philox8(const DropState& s, uint32_t row, uint32
 }
 // Eight elements of a row from channel c on, each times the scale or, dropped, 0 whatever it was.
 __device__ __forceinline__ void drop8(const Drop& d, const DropState& s, uint32_t row, uint32_t c,
-                                      float (&v)[8]) {
+                                      F2 (&v)[4]) {
   uint32_t r[2][4];
   philox8(s, row, c, r);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = r[i >> 2][i & 3] >= d.least ? v[i] * d.scale : 0.f;
+  each(v, [&](int i, float x) { return r[i >> 2][i & 3] >= d.least ? x * d.scale : 0.f; });
 }
 
 // ----------------------------------------------------------------------------------- sums of a row
@@ -383,35 +483,42 @@ struct RowSum {
 // Mean (0 for rms) and one over the deviation of a row (inv: one over its channels) whose threads hold x. What
 // is past the channels that end at d is 0 in x and does not count; EDGE: a chunk may lie across the end.
 template <int NC, bool EDGE, typename Sum>
-__device__ __forceinline__ void row_stats(Sum& sum, int kind, const float (&x)[NC][8], const int (&col)[NC],
+__device__ __forceinline__ void row_stats(Sum& sum, int kind, const F2 (&x)[NC][4], const int (&col)[NC],
                                           int d, float inv, float eps, float& mean, float& rstd) {
   mean = 0.f;
-  float q[1] = {0.f};
+  F2 s[4] = {0, 0, 0, 0};  // +0 twice; four chains
   if (kind == MOE_NORM_LAYER) {
-    float s[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += x[c][i];
-    sum(s);
-    mean = s[0] * inv;
+      for (int i = 0; i < 4; ++i) s[i] = add2(s[i], x[c][i]);
+    float2 f = both(add2(add2(s[0], s[1]), add2(s[2], s[3])));
+    float t[1] = {f.x + f.y};
+    sum(t);
+    mean = t[0] * inv;
+    const F2 m = twice(-mean);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = 0;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
       if (col[c] < d) {
+        F2 v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = !EDGE || col[c] + i < d ? x[c][i] - mean : 0.f;
-          q[0] = fmaf(v, v, q[0]);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = add2(x[c][i], m);
+        if constexpr (EDGE) each(v, [&](int i, float y) { return col[c] + i < d ? y : 0.f; });
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = fma2(v[i], v[i], s[i]);
       }
   } else {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[0] = fmaf(x[c][i], x[c][i], q[0]);
+      for (int i = 0; i < 4; ++i) s[i] = fma2(x[c][i], x[c][i], s[i]);
   }
+  const float2 f = both(add2(add2(s[0], s[1]), add2(s[2], s[3])));
+  float q[1] = {f.x + f.y};
   sum(q);
-  rstd = 1.f / sqrtf(fmaf(q[0], inv, eps));
+  rstd = rsqrtf(fmaf(q[0], inv, eps));  // within two units in the last place
 }
 
 // How a row is shared: R threads with NC chunks of eight channels each, above 8192 channels a cluster.
