@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) dropout_any_kernel(const __grid_cons
       each(v, [&](int i, float t) { return t + r[lane * 8 + i]; });
     }
     __syncwarp();
-    store<Any>(a.y, row, w0, lane, a.d, v, x);
+    store<Any, 32>(a.y, (int)row, 0, w0, lane, a.d, v, x);
   }
 }
 

@@ -91,11 +91,11 @@ moe_status moe_residual_norm(const moe_residual_norm_config* cfg, const void* h,
   const long long d = cfg->d;
   a.h = in(h, cfg->ld_h ? cfg->ld_h : d, cfg->h_dtype);
   a.y = in(y, cfg->ld_y ? cfg->ld_y : d, cfg->y_dtype);
-  a.w_after = in(params->w_after, d, cfg->w_dtype);
-  a.b_after = in(params->b_after, d, cfg->w_dtype);
+  a.w_after = in(params->w_after, 0, cfg->w_dtype);
+  a.b_after = in(params->b_after, 0, cfg->w_dtype);
   a.gate = in(params->gate, d, cfg->w_dtype);
-  a.w_before = in(params->w_before, d, cfg->w_dtype);
-  a.b_before = in(params->b_before, d, cfg->w_dtype);
+  a.w_before = in(params->w_before, 0, cfg->w_dtype);
+  a.b_before = in(params->b_before, 0, cfg->w_dtype);
   a.h_out = out(h_out, d, cfg->h_dtype);
   a.n = out(n, d, cfg->y_dtype);
   a.wide = d % 8 == 0 && a.h.wide && (!y || a.y.wide) && (!h_out || a.h_out.wide) && (!n || a.n.wide);
@@ -160,10 +160,10 @@ moe_status moe_residual_norm_backward(const moe_residual_norm_config* cfg, const
   a.y = in(y, cfg->ld_y ? cfg->ld_y : d, cfg->y_dtype);
   a.d_h_out = in(d_h_out, d, cfg->h_dtype);
   a.d_n = in(d_n, d, cfg->y_dtype);
-  a.w_after = in(params->w_after, d, cfg->w_dtype);
-  a.b_after = in(params->b_after, d, cfg->w_dtype);
+  a.w_after = in(params->w_after, 0, cfg->w_dtype);
+  a.b_after = in(params->b_after, 0, cfg->w_dtype);
   a.gate = in(params->gate, d, cfg->w_dtype);
-  a.w_before = in(params->w_before, d, cfg->w_dtype);
+  a.w_before = in(params->w_before, 0, cfg->w_dtype);
   a.d_h = out(d_h, d, cfg->h_dtype);
   a.d_y = out(d_y, d, cfg->y_dtype);
   a.d_w_after = grads->w_after;

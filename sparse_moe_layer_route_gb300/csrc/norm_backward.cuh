@@ -77,24 +77,6 @@ __device__ __forceinline__ void get_shared(const float* sums, int lane, F2 (&v)[
   }
 }
 
-// A thread's share of sum(g x) and, for a layer norm, sum(g).
-template <int NC>
-__device__ __forceinline__ void sums_of(const F2 (&g)[NC][4], const F2 (&x)[NC][4], bool layer, float (&m)[2]) {
-  F2 s[2] = {0, 0}, t[2] = {0, 0};
-#pragma unroll
-  for (int c = 0; c < NC; ++c)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i & 1] = fma2(g[c][i], x[c][i], s[i & 1]);
-  if (layer) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) t[i & 1] = add2(g[c][i], t[i & 1]);
-  }
-  const float2 a = both(add2(s[0], s[1])), b = both(add2(t[0], t[1]));
-  m[0] = a.x + a.y;
-  m[1] = b.x + b.y;
-}
 // g = r (g - x p - q): a gradient to normed values x becomes one to what was normed.
 template <int NC>
 __device__ __forceinline__ void through_norm(F2 (&g)[NC][4], const F2 (&x)[NC][4], float p, float q, float r) {
@@ -117,7 +99,11 @@ __host__ __device__ __forceinline__ int bias_bytes(const NormGradArgs& a) {
   return ((a.d_b_after != nullptr) + (a.d_b_before != nullptr)) * NC * kWarpCols * 4;  // of a warp
 }
 
-template <int R, int NC, bool CLUSTER, class H, class Y>
+// a + b, but not past the end (token numbers go up to 2^31 - 1).
+__device__ __forceinline__ int at_most(int a, int b, int end) { return b < end - a ? a + b : end; }
+
+// LAYER: a norm may be a layer norm, whose sums follow one another; others' are taken together.
+template <int R, int NC, bool CLUSTER, class H, class Y, bool LAYER>
 __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
     norm_grad_kernel(const __grid_constant__ NormGradArgs a, int cl, int stages) {
   constexpr int kGroups = norm_threads<R>() / R;
@@ -130,7 +116,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
   const int base = CLUSTER ? rank * norm_width(a.d, cl) : 0;
   const int d = CLUSTER ? min(a.d, base + norm_width(a.d, cl)) : a.d;  // this CTA's channels end there
   const int per = norm_rows_per_cta(a.T, ctas);
-  const long long r0 = (long long)cta * per, r1 = r0 + per < a.T ? r0 + per : a.T;
+  const int r0 = (int)((long long)cta * per), r1 = at_most(r0, per, a.T);
   RowSum<R, CLUSTER> sum(red[group], group, cl);
   const int w0 = base + tid / 32 * kWarpCols;  // channels of chunk c: w0 + c * R * 8 + lane * 8 + 0..7
   const float inv = 1.f / (float)a.d;
@@ -145,25 +131,17 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
   float* sums_ba = sums_bb + (a.d_b_before != nullptr ? NC * kWarpCols : 0);
   mine += bias_bytes<NC>(a);
   float* turn = reinterpret_cast<float*>(mine + stages * pitch);
-  Input<H, R, NC> h_in, g_in;
-  Input<Y, R, NC> n_in, y_in;
+  using In = Input<H, R, NC>;
+  using InY = Input<Y, R, NC>;
+  const uint32_t sh = ptx::smem_u32(mine);
+  const uint32_t sn = sh + (normed ? In::bytes(a.d_h.dtype) : 0);
+  const uint32_t sg = sn + (normed ? InY::bytes(a.y.dtype) : 0);
+  const uint32_t sy = sg + (direct ? In::bytes(a.d_h.dtype) : 0);
   {
-    uint32_t at = ptx::smem_u32(mine);
-    if (normed) {
-      h_in.init(a.h, w0, lane, at);
-      at += h_in.bytes(a.h.dtype);
-      n_in.init(a.d_n, w0, lane, at);
-      at += n_in.bytes(a.d_n.dtype);
-    }
-    if (direct) {
-      g_in.init(a.d_h_out, w0, lane, at);
-      at += g_in.bytes(a.d_h_out.dtype);
-    }
-    if (block) y_in.init(a.y, w0, lane, at);
-    for (int i = 0; i < stages; ++i) {
-      if (normed) h_in.clear(w0, lane, d, i * pitch), n_in.clear(w0, lane, d, i * pitch);
-      if (direct) g_in.clear(w0, lane, d, i * pitch);
-      if (block) y_in.clear(w0, lane, d, i * pitch);
+    for (uint32_t i = 0; i < stages * pitch; i += pitch) {
+      if (normed) In::clear(a.h, w0, lane, d, sh + i), InY::clear(a.d_n, w0, lane, d, sn + i);
+      if (direct) In::clear(a.d_h_out, w0, lane, d, sg + i);
+      if (block) InY::clear(a.y, w0, lane, d, sy + i);
     }
     for (int i = lane; i < bias_bytes<NC>(a) / 4; i += 32) sums_bb[i] = 0.f;
     __syncwarp();
@@ -175,16 +153,16 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
   // do not depend on it
   const bool sum_gates = a.gate.p != nullptr && a.gate_rows > 1;
   // a segment: tokens with the same row of gates, dealt out to the row groups
-  auto segment_end = [&](long long s0) {
+  auto segment_end = [&](int s0) {
     if (!sum_gates) return r1;
-    const long long end = (s0 / a.gate_rows + 1) * a.gate_rows;
-    return end < r1 ? end : r1;
+    const uint32_t end = ((uint32_t)s0 / (uint32_t)a.gate_rows + 1) * (uint32_t)a.gate_rows;  // up to 2^32 - 2
+    return end < (uint32_t)r1 ? (int)end : r1;
   };
   // this group's next token to bring and the end of its segment
-  long long next = r0 + group, next_end = segment_end(r0);
+  int next = at_most(r0, group, r1), next_end = segment_end(r0);
   auto settle = [&] {
     while (next >= next_end && next_end < r1) {
-      next = next_end + group;
+      next = at_most(next_end, group, r1);
       next_end = segment_end(next_end);
     }
   };
@@ -192,12 +170,12 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
   auto bring = [&](uint32_t stage) {
     if (next < next_end) {
       if (normed) {
-        h_in.fetch(next, w0, lane, d, stage);
-        n_in.fetch(next, w0, lane, d, stage);
+        In::fetch(a.h, next, w0, lane, d, sh + stage);
+        InY::fetch(a.d_n, next, w0, lane, d, sn + stage);
       }
-      if (direct) g_in.fetch(next, w0, lane, d, stage);
-      if (block) y_in.fetch(next, w0, lane, d, stage);
-      next += kGroups;
+      if (direct) In::fetch(a.d_h_out, next, w0, lane, d, sg + stage);
+      if (block) InY::fetch(a.y, next, w0, lane, d, sy + stage);
+      next = at_most(next, kGroups, r1);
       if (next >= next_end) settle();
     }
     copies_commit();
@@ -208,9 +186,9 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
   int col[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) col[c] = w0 + c * R * 8 + lane * 8;
-  for (long long s0 = r0; s0 < r1;) {
-    const long long s1 = segment_end(s0);
-    for (long long row = s0 + group; row < s1; row += kGroups) {
+  for (int s0 = r0; s0 < r1;) {
+    const int s1 = segment_end(s0);
+    for (int row = at_most(s0, group, s1); row < s1; row = at_most(row, kGroups, s1)) {
       copies_wait_stage(stages);
       __syncwarp();
       F2 g[NC][4];
@@ -218,34 +196,74 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[c][i] = 0;
+      // what needs no other sum is summed first, all at once: squares (a layer norm's follow its mean) and, with
+      // an rms norm, the product that its gradient subtracts
+      F2 h[NC][4], y[NC][4];
+      float hm = 0.f, hr = 1.f, ym = 0.f, yr = 1.f;
       if (normed) {
-        F2 h[NC][4];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) h_in.read(c, lane, stage, h[c]);
-        float mean, rstd;
-        row_stats<NC, kAny>(sum, a.before, h, col, d, inv, a.eps, mean, rstd);
-        scale_rows<NC>(h, a.before == MOE_NORM_LAYER, mean, rstd);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          n_in.read(c, lane, stage, g[c]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) wb[c][i] = fma2(g[c][i], h[c][i], wb[c][i]);
+          In::read(a.h, c, lane, sh + stage, h[c]);
+          InY::read(a.d_n, c, lane, sn + stage, g[c]);
         }
         if (a.d_b_before != nullptr) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) add_shared(sums_bb + c * kWarpCols, lane, g[c]);
         }
+      }
+      if (!LAYER && normed) {
+        float t[4];
+        t[0] = dot<NC>(h, h);
         if (a.w_before.p != nullptr) times_params<kAny>(a.w_before, 0, col, d, g);
-        float m[2];
-        sums_of<NC>(g, h, a.before == MOE_NORM_LAYER, m);
-        sum(m);
-        through_norm<NC>(g, h, m[0] * inv, m[1] * inv, rstd);
+        t[1] = dot<NC>(g, h);
+        t[2] = t[3] = 0.f;
+        if (block && a.after == MOE_NORM_RMS) {
+          F2 s[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            F2 v[4];
+            InY::read(a.y, c, lane, sy + stage, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = fma2(v[i], v[i], s[i]);
+          }
+          t[2] = total(s[0], s[1], s[2], s[3]);
+        }
+        sum(t);
+        hr = deviation(t[0], inv, a.eps);
+        if (block && a.after == MOE_NORM_RMS) yr = deviation(t[2], inv, a.eps);
+        scale_rows<NC>(h, false, 0.f, hr);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          F2 v[4];
+          InY::read(a.d_n, c, lane, sn + stage, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) wb[c][i] = fma2(v[i], h[c][i], wb[c][i]);
+        }
+        through_norm<NC>(g, h, t[1] * hr * inv, 0.f, hr);
+      } else {
+        if (LAYER && normed) {
+          row_stats<NC, kAny>(sum, a.before, h, col, d, inv, a.eps, hm, hr);
+          scale_rows<NC>(h, a.before == MOE_NORM_LAYER, hm, hr);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wb[c][i] = fma2(g[c][i], h[c][i], wb[c][i]);
+          if (a.w_before.p != nullptr) times_params<kAny>(a.w_before, 0, col, d, g);
+          float m[2] = {dot<NC>(g, h), a.before == MOE_NORM_LAYER ? plain_sum<NC>(g) : 0.f};
+          sum(m);
+          through_norm<NC>(g, h, m[0] * inv, m[1] * inv, hr);
+        }
+        if (block && a.after != MOE_NORM_NONE) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) InY::read(a.y, c, lane, sy + stage, y[c]);
+          row_stats<NC, kAny>(sum, a.after, y, col, d, inv, a.eps, ym, yr);
+        }
       }
       if (direct) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           F2 v[4];
-          g_in.read(c, lane, stage, v);
+          In::read(a.d_h_out, c, lane, sg + stage, v);
 #pragma unroll
           for (int i = 0; i < 4; ++i) g[c][i] = add2(g[c][i], v[i]);
         }
@@ -257,98 +275,113 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
           F2 v[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = mul2(alpha, g[c][i]);
-          store<H>(a.d_h, row, w0 + c * R * 8, lane, d, v, turn);
+          store<H, R>(a.d_h, row, c, w0, lane, d, v, turn);
         }
       }
       if (block) {
-        F2 y[NC][4];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) y_in.read(c, lane, stage, y[c]);
-        float mean = 0.f, rstd = 1.f;
-        if (a.after != MOE_NORM_NONE) {
-          row_stats<NC, kAny>(sum, a.after, y, col, d, inv, a.eps, mean, rstd);
-          scale_rows<NC>(y, a.after == MOE_NORM_LAYER, mean, rstd);
-        }
-        const F2 beta = twice(a.beta);
+        const uint32_t gate_row =
+            a.gate.p != nullptr && a.gate_rows < a.T ? (uint32_t)row / (uint32_t)a.gate_rows : 0;
+        const F2 beta = twice(a.beta), ymm = twice(-ym), yrr = twice(yr);
+        // e: the gradient to u, without the gate. g becomes the normed values' gradient, e gate w
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
+          if (kAny && w0 + c * R * 8 >= d) {  // nothing of the warp's is there
 #pragma unroll
-          for (int i = 0; i < 4; ++i) g[c][i] = mul2(g[c][i], beta);
-          if (a.drop.rng != nullptr) drop8(a.drop, ds, (uint32_t)row, (uint32_t)col[c], g[c]);
-        }
-        if (a.gate.p != nullptr) {
-          const uint32_t gate_row = a.gate_rows < a.T ? (uint32_t)row / (uint32_t)a.gate_rows : 0;
-          if (a.d_gate != nullptr) {
-            F2 u[NC][4];
+            for (int i = 0; i < 4; ++i) g[c][i] = y[c][i] = 0;
+            continue;
+          }
+          Raw rw, rg;
+          if (a.w_after.p != nullptr) rw = param_raw<kAny>(a.w_after, 0, col[c], d);
+          if (a.gate.p != nullptr) rg = param_raw<kAny>(a.gate, gate_row, col[c], d);
+          F2 e[4];
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+          for (int i = 0; i < 4; ++i) e[i] = mul2(g[c][i], beta);
+          if (a.drop.rng != nullptr) drop8(a.drop, ds, row, col[c], e);
+          InY::read(a.y, c, lane, sy + stage, y[c]);
+          if (LAYER && a.after == MOE_NORM_LAYER) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) u[c][i] = y[c][i];
-            if (a.w_after.p != nullptr) times_params<kAny>(a.w_after, 0, col, d, u);
-            if (a.b_after.p != nullptr)
-              with_params<kAny>(a.b_after, 0, col, d, [&](int c, const F2 (&w)[4]) {
+            for (int i = 0; i < 4; ++i) y[c][i] = add2(y[c][i], ymm);
+          }
+          if (a.after != MOE_NORM_NONE) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) u[c][i] = add2(u[c][i], w[i]);
-              });
-            if (a.drop.rng != nullptr) {  // a dropped element is 0 whatever u is
+            for (int i = 0; i < 4; ++i) y[c][i] = mul2(y[c][i], yrr);
+          }
 #pragma unroll
-              for (int c = 0; c < NC; ++c)
+          for (int i = 0; i < 4; ++i) g[c][i] = e[i];
+          if (a.w_after.p != nullptr) {
+            F2 w[4];
+            to_float<Any>(rw, a.w_after.dtype, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[c][i] = mul2(g[c][i], w[i]);
+          }
+          if (a.gate.p != nullptr) {
+            if (a.d_gate != nullptr) {
+              F2 u[4];  // e u = (e w) y^ + e b
+#pragma unroll
+              for (int i = 0; i < 4; ++i) u[i] = mul2(g[c][i], y[c][i]);
+              if (a.drop.rng != nullptr) {  // a dropped element is 0 whatever u is
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const float2 e = both(g[c][i]), v = both(u[c][i]);
-                  u[c][i] = pair(e.x != 0.f ? v.x : 0.f, e.y != 0.f ? v.y : 0.f);
+                  const float2 k = both(e[i]), v = both(u[i]);
+                  u[i] = pair(k.x != 0.f ? v.x : 0.f, k.y != 0.f ? v.y : 0.f);
                 }
-            }
-            if (sum_gates) {
+              }
+              if (a.b_after.p != nullptr) {
+                F2 w[4];
+                to_float<Any>(param_raw<kAny>(a.b_after, 0, col[c], d), a.b_after.dtype, w);
 #pragma unroll
-              for (int c = 0; c < NC; ++c)
+                for (int i = 0; i < 4; ++i) u[i] = fma2(e[i], w[i], u[i]);
+              }
+              if (sum_gates) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ga[c][i] = fma2(g[c][i], u[c][i], ga[c][i]);
-            } else {
-              const RowsOut out{a.d_gate, a.d, MOE_DTYPE_F32, true};
-#pragma unroll
-              for (int c = 0; c < NC; ++c) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[c][i] = mul2(g[c][i], u[c][i]);
-                store<std::conditional_t<kAny, Any, F32>>(out, row, w0 + c * R * 8, lane, d, u[c], turn);
+                for (int i = 0; i < 4; ++i) ga[c][i] = add2(ga[c][i], u[i]);
+              } else {
+                const RowsOut out{a.d_gate, a.d, MOE_DTYPE_F32, true};
+                store<std::conditional_t<kAny, Any, F32>, R>(out, row, c, w0, lane, d, u, turn);
               }
             }
-          }
-          times_params<kAny>(a.gate, gate_row, col, d, g);
-        }
-        // what is past the row's end adds nothing to its means
-        if (kAny || a.after == MOE_NORM_LAYER || a.before == MOE_NORM_LAYER) {
+            F2 w[4];
+            to_float<Any>(rg, a.gate.dtype, w);
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (kAny || col[c] >= d) each(g[c], [&](int i, float v) { return col[c] + i < d ? v : 0.f; });
+            for (int i = 0; i < 4; ++i) {
+              e[i] = mul2(e[i], w[i]);
+              g[c][i] = mul2(g[c][i], w[i]);
+            }
+          }
+          if (a.after != MOE_NORM_NONE) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wa[c][i] = fma2(e[i], y[c][i], wa[c][i]);
+            if (a.d_b_after != nullptr) add_shared(sums_ba + c * kWarpCols, lane, e);
+          }
         }
         if (a.after != MOE_NORM_NONE) {
+          // what is past the row's end adds nothing to its means
+          if (kAny || LAYER) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) wa[c][i] = fma2(g[c][i], y[c][i], wa[c][i]);
-          if (a.d_b_after != nullptr) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) add_shared(sums_ba + c * kWarpCols, lane, g[c]);
+            for (int c = 0; c < NC; ++c)
+              if (kAny || col[c] >= d) each(g[c], [&](int i, float v) { return col[c] + i < d ? v : 0.f; });
           }
-          if (a.w_after.p != nullptr) times_params<kAny>(a.w_after, 0, col, d, g);
-          float m[2];
-          sums_of<NC>(g, y, a.after == MOE_NORM_LAYER, m);
-          sum(m);
-          through_norm<NC>(g, y, m[0] * inv, m[1] * inv, rstd);
+          if (LAYER && a.after == MOE_NORM_LAYER) {
+            float m[2] = {dot<NC>(g, y), plain_sum<NC>(g)};
+            sum(m);
+            through_norm<NC>(g, y, m[0] * inv, m[1] * inv, yr);
+          } else {
+            float m[1] = {dot<NC>(g, y)};
+            sum(m);
+            through_norm<NC>(g, y, m[0] * inv, 0.f, yr);
+          }
         }
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-          store<Y>(a.d_y, row, w0 + c * R * 8, lane, d, g[c], turn);
+        for (int c = 0; c < NC; ++c) store<Y, R>(a.d_y, row, c, w0, lane, d, g[c], turn);
       }
       __syncwarp();  // the stage is read; its next row may come
       bring(stage);
       stage = stage + pitch == stages * pitch ? 0 : stage + pitch;
     }
     if (sum_gates && a.d_gate != nullptr) {
-      const long long first = s0 / a.gate_rows * a.gate_rows;
+      const int first = s0 / a.gate_rows * a.gate_rows;
       const bool whole = first >= r0 && (s1 < r1 || s1 == a.T || s1 % a.gate_rows == 0);
-      float* dst = whole ? a.d_gate + s0 / a.gate_rows * a.d : part + (first < r0 ? 4 : 5) * a.d;
+      float* dst = whole ? a.d_gate + (long long)(s0 / a.gate_rows) * a.d : part + (first < r0 ? 4 : 5) * a.d;
       flush<R, NC>(ga, stage_s, group, w0, lane, base, d, dst);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
@@ -390,8 +423,14 @@ cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStrea
   *ctas = (int)(need < most ? need : most);
   const int per = norm_rows_per_cta(a.T, *ctas);
   *ctas = (int)(((long long)a.T + per - 1) / per);  // the runs are equal, so fewer may do
-  return launch_rows<CLUSTER>(norm_grad_kernel<R, NC, CLUSTER, H, Y>, *ctas * cl, threads, smem(), cl, st, a,
-                              cl, stages);
+  const bool layer = a.after == MOE_NORM_LAYER || a.before == MOE_NORM_LAYER;
+  if (layer || std::is_same_v<H, Any>)
+    return launch_rows<CLUSTER>(norm_grad_kernel<R, NC, CLUSTER, H, Y, true>, *ctas * cl, threads, smem(), cl,
+                                st, a, cl, stages);
+  if constexpr (!std::is_same_v<H, Any>)
+    return launch_rows<CLUSTER>(norm_grad_kernel<R, NC, CLUSTER, H, Y, false>, *ctas * cl, threads, smem(), cl,
+                                st, a, cl, stages);
+  return cudaErrorInvalidValue;
 }
 
 template <class H, class Y>

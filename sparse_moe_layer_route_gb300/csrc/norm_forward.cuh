@@ -38,38 +38,38 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
   const uint32_t pitch = In::bytes(a.h.dtype) + (block ? InY::bytes(a.y.dtype) : 0);
   uint8_t* mine = smem + threadIdx.x / 32 * (stages * pitch + (kAny ? kWarpCols * 4 : 0));
   float* turn = reinterpret_cast<float*>(mine + stages * pitch);
-  In h;
-  InY y;
-  h.init(a.h, w0, lane, ptx::smem_u32(mine));
-  y.init(a.y, w0, lane, ptx::smem_u32(mine) + In::bytes(a.h.dtype));
+  const uint32_t sh = ptx::smem_u32(mine), sy = sh + In::bytes(a.h.dtype);
   for (int i = 0; i < stages; ++i) {
-    h.clear(w0, lane, d, i * pitch);
-    if (block) y.clear(w0, lane, d, i * pitch);
+    In::clear(a.h, w0, lane, d, sh + i * pitch);
+    if (block) InY::clear(a.y, w0, lane, d, sy + i * pitch);
   }
   const int step = (int)(gridDim.x / cl) * kGroups;
-  long long row = (long long)(blockIdx.x / cl) * kGroups + group;
+  const long long first = (long long)(blockIdx.x / cl) * kGroups + group;
   const float inv = 1.f / (float)a.d;
   int col[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) col[c] = w0 + c * R * 8 + lane * 8;
   griddep_wait();
   const DropState ds(a.drop);
-  auto bring = [&](long long r, uint32_t stage) {
-    if (r < a.T) {
-      if (block) y.fetch(r, w0, lane, d, stage);
-      h.fetch(r, w0, lane, d, stage);
+  int next = first < a.T ? (int)first : a.T;
+  auto bring = [&](uint32_t stage) {
+    if (next < a.T) {
+      if (block) InY::fetch(a.y, next, w0, lane, d, sy + stage);
+      In::fetch(a.h, next, w0, lane, d, sh + stage);
+      next = step < a.T - next ? next + step : a.T;
     }
     copies_commit();
   };
-  for (int i = 0; i < stages; ++i) bring(row + (long long)i * step, i * pitch);
+  for (int i = 0; i < stages; ++i) bring(i * pitch);
   uint32_t stage = 0;
-  for (; row < a.T; row += step) {
+  for (long long r = first; r < a.T; r += step) {
+    const int row = (int)r;
     copies_wait_stage(stages);
     __syncwarp();
     F2 x[NC][4];  // y, then h'
     if (block) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) y.read(c, lane, stage, x[c]);
+      for (int c = 0; c < NC; ++c) InY::read(a.y, c, lane, sy + stage, x[c]);
       float mean = 0.f, rstd = 1.f;
       if (a.after != MOE_NORM_NONE)
         row_stats<NC, kAny>(sum, a.after, x, col, d, inv, a.eps, mean, rstd);
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
       }
       if (a.drop.rng != nullptr) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) drop8(a.drop, ds, (uint32_t)row, (uint32_t)col[c], x[c]);
+        for (int c = 0; c < NC; ++c) if (!kAny || w0 + c * R * 8 < d) drop8(a.drop, ds, row, col[c], x[c]);
       }
       if (a.gate.p != nullptr) {
         const uint32_t gate_row = a.gate_rows < a.T ? (uint32_t)row / (uint32_t)a.gate_rows : 0;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         F2 v[4];
-        h.read(c, lane, stage, v);
+        In::read(a.h, c, lane, sh + stage, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[c][i] = fma2(alpha, v[i], x[c][i]);
       }
@@ -109,17 +109,17 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
       const F2 alpha = twice(a.alpha);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        h.read(c, lane, stage, x[c]);
+        In::read(a.h, c, lane, sh + stage, x[c]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[c][i] = mul2(alpha, x[c][i]);
       }
     }
     __syncwarp();  // the stage is read; its next row may come
-    bring(row + (long long)stages * step, stage);
+    bring(stage);
     stage = stage + pitch == stages * pitch ? 0 : stage + pitch;
     if (a.h_out.p != nullptr) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) store<H>(a.h_out, row, w0 + c * R * 8, lane, d, x[c], turn);
+      for (int c = 0; c < NC; ++c) store<H, R>(a.h_out, row, c, w0, lane, d, x[c], turn);
     }
     if (a.before != MOE_NORM_NONE) {
       float mean, rstd;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
           for (int i = 0; i < 4; ++i) x[c][i] = add2(x[c][i], w[i]);
         });
 #pragma unroll
-      for (int c = 0; c < NC; ++c) store<Y>(a.n, row, w0 + c * R * 8, lane, d, x[c], turn);
+      for (int c = 0; c < NC; ++c) store<Y, R>(a.n, row, c, w0, lane, d, x[c], turn);
     }
   }
   copies_wait<0>();

@@ -161,149 +161,141 @@ __device__ __forceinline__ void copies_wait_stage(int stages) {
     copies_wait<0>();
 }
 
-// One input of a warp: where its rows come from and its place in shared memory, [stage][chunk][256] with
-// stages `pitch` bytes apart. E Any: for any alignment.
+// One input of a warp and its place in shared memory, [chunk][256] at `at` (a stage's; this warp's). What a
+// lane needs is worked out where it is used: the arguments stay where the launch put them, and few registers
+// are held from row to row. E Any: for any alignment.
 template <class E, int R, int NC>
 struct Input {
-  const char* p;      // row 0, this lane's first chunk (Any: the row's start)
-  long long step;     // bytes between rows
-  uint32_t at;        // in shared memory, stage 0, this lane's first chunk (Any: the warp's)
-  int dtype;
+  static constexpr int kBytes = std::is_same_v<E, F32> ? 4 : 2;  // but for Any
+  static __host__ __device__ int bytes(int dtype) { return NC * kWarpCols * bytes_of<E>(dtype); }
 
-  __device__ __forceinline__ void init(const RowsIn& m, int w0, int lane, uint32_t warp_at) {
-    dtype = m.dtype;
-    const int b = bytes_of<E>(dtype);
-    step = m.ld * b;
-    if constexpr (std::is_same_v<E, Any>) {
-      p = static_cast<const char*>(m.p);
-      at = warp_at;
-    } else {
-      p = static_cast<const char*>(m.p) + (long long)(w0 + lane * 8) * b;
-      at = warp_at + lane * 8 * b;
-    }
-  }
   // Starts the copies of a row. Chunks past d: whole ones stay as clear() left them, elements become 0.
-  __device__ __forceinline__ void fetch(long long row, int w0, int lane, int d, uint32_t stage) const {
-    const char* from = p + row * step;
+  static __device__ __forceinline__ void fetch(const RowsIn& m, int row, int w0, int lane, int d, uint32_t at) {
+    const char* from = static_cast<const char*>(m.p) + (size_t)(uint32_t)row * (m.ld * bytes_of<E>(m.dtype));
+    if constexpr (!std::is_same_v<E, Any>) {
+      from += (w0 + lane * 8) * kBytes;
+      at += lane * 8 * kBytes;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      if constexpr (!std::is_same_v<E, Any>) {
-        constexpr int b = std::is_same_v<E, F32> ? 4 : 2;
+      for (int c = 0; c < NC; ++c)
         if (w0 + c * R * 8 + lane * 8 < d) {
-          copy16(at + stage + c * kWarpCols * b, from + c * R * 8 * b);
-          if constexpr (b == 4) copy16(at + stage + c * kWarpCols * b + 16, from + c * R * 8 * b + 16);
+          copy16(at + c * kWarpCols * kBytes, from + c * R * 8 * kBytes);
+          if constexpr (kBytes == 4) copy16(at + c * kWarpCols * 4 + 16, from + c * R * 32 + 16);
         }
-      } else if (dtype == MOE_DTYPE_F32) {
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = w0 + c * R * 8 + i * 32 + lane;
-          copy4(at + stage + (c * kWarpCols + i * 32 + lane) * 4, from + (k < d ? k : 0) * 4ll,
-                k < d ? 4 : 0);
+      for (int c = 0; c < NC; ++c) {
+        const int left = d - (w0 + c * R * 8 + lane);  // this lane's elements are 32 apart
+        if (w0 + c * R * 8 >= d) continue;
+        if (m.dtype == MOE_DTYPE_F32) {
+          const char* q = from + (w0 + c * R * 8 + lane) * 4ll;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool there = i * 32 < left;
+            copy4(at + (c * kWarpCols + i * 32 + lane) * 4, there ? q + i * 128 : from, there ? 4 : 0);
+          }
+        } else {  // two bytes cannot be copied asynchronously
+          uint16_t v[8];
+          const uint16_t* q = reinterpret_cast<const uint16_t*>(from) + (w0 + c * R * 8 + lane);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = i * 32 < left ? q[i * 32] : (uint16_t)0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + (c * kWarpCols + i * 32 + lane) * 2),
+                         "h"(v[i])
+                         : "memory");
         }
-      } else {  // two bytes cannot be copied asynchronously
-        uint16_t v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = w0 + c * R * 8 + i * 32 + lane;
-          v[i] = k < d ? reinterpret_cast<const uint16_t*>(from)[k] : (uint16_t)0;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + stage + (c * kWarpCols + i * 32 + lane) * 2),
-                       "h"(v[i])
-                       : "memory");
       }
     }
   }
   // Chunks past d are 0 from the start.
-  __device__ __forceinline__ void clear(int w0, int lane, int d, uint32_t stage) const {
-    if constexpr (!std::is_same_v<E, Any>) {
-      constexpr int b = std::is_same_v<E, F32> ? 4 : 2;
+  static __device__ __forceinline__ void clear(const RowsIn& m, int w0, int lane, int d, uint32_t at) {
+    const int b = bytes_of<E>(m.dtype);
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        if (w0 + c * R * 8 + lane * 8 >= d)
-#pragma unroll
-          for (int k = 0; k < b / 2; ++k)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             at + stage + c * kWarpCols * b + 16 * k),
-                         "r"(0)
-                         : "memory");
-    }
+    for (int c = 0; c < NC; ++c)
+      if (w0 + c * R * 8 + (std::is_same_v<E, Any> ? 0 : lane * 8) >= d)
+        for (int k = 0; k < b / 2; ++k)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                           at + (c * kWarpCols + lane * 8) * b + 16 * k),
+                       "r"(0)
+                       : "memory");
   }
   // This lane's chunk c.
-  __device__ __forceinline__ void read(int c, int lane, uint32_t stage, F2 (&v)[4]) const {
+  static __device__ __forceinline__ void read(const RowsIn& m, int c, int lane, uint32_t at, F2 (&v)[4]) {
     Raw r;
-    const int b = bytes_of<E>(dtype);
-    uint32_t from = at + stage + c * kWarpCols * b;
-    if constexpr (std::is_same_v<E, Any>) from += lane * 8 * b;
+    const int b = bytes_of<E>(m.dtype);
+    const uint32_t from = at + (c * kWarpCols + lane * 8) * b;
     r.a = shared16(from);
     if (b == 4) r.b = shared16(from + 16);
-    to_float<E>(r, dtype, v);
+    to_float<E>(r, m.dtype, v);
   }
-  static __host__ __device__ int bytes(int dtype) { return NC * kWarpCols * bytes_of<E>(dtype); }
 };
 
 // -------------------------------------------------------------------------------------- parameters
-// op(c, w) for every chunk c of a thread and its parameters w (0 past the d-th channel). They are small and stay
-// in L1 from row to row; all chunks' are under way before the first is used. ANY: of any alignment.
+// A thread's chunk of a row of parameters as it lies in memory, from channel c on, 0 past the d-th. They are
+// small and stay in L1 from row to row. ANY: of any alignment.
+template <bool ANY>
+__device__ __forceinline__ Raw param_raw(const RowsIn& m, long long row, int c, int d) {
+  Raw r = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (c >= d) return r;
+  const bool f32 = m.dtype == MOE_DTYPE_F32;
+  const long long at = row * m.ld + c;
+  if (!ANY || (m.wide && c + 8 <= d)) {
+    if (f32) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(m.p) + at);
+      r.a = __ldg(p);
+      r.b = __ldg(p + 1);
+    } else {
+      r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(m.p) + at));
+    }
+    return r;
+  }
+  uint32_t v[8];
+  if (f32) {
+    const uint32_t* p = static_cast<const uint32_t*>(m.p) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < d ? __ldg(p + i) : 0u;
+    r.a = make_uint4(v[0], v[1], v[2], v[3]);
+    r.b = make_uint4(v[4], v[5], v[6], v[7]);
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(m.p) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < d ? __ldg(p + i) : 0u;
+    r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
+  return r;
+}
+// op(c, w) for every chunk c of a thread and its parameters w; all chunks' are under way before the first is used.
 template <bool ANY, int NC, class Op>
 __device__ __forceinline__ void with_params(const RowsIn& m, long long row, const int (&col)[NC], int d,
                                             Op op) {
-  if constexpr (ANY) {
-    const bool f32 = m.dtype == MOE_DTYPE_F32;
+  if (ANY || m.dtype == MOE_DTYPE_F32) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const long long at = row * m.ld + col[c] + i;
-        v[i] = 0.f;
-        if (col[c] + i < d) {
-          if (f32) {
-            v[i] = __ldg(static_cast<const float*>(m.p) + at);
-          } else {
-            const uint16_t u = __ldg(static_cast<const uint16_t*>(m.p) + at);
-            v[i] = m.dtype == MOE_DTYPE_BF16 ? __uint_as_float((uint32_t)u << 16)
-                                             : __half2float(__ushort_as_half(u));
-          }
-        }
-      }
-      const F2 w[4] = {pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])};
+      const Raw r = param_raw<ANY>(m, row, col[c], d);
+      F2 w[4];
+      to_float<Any>(r, m.dtype, w);
       op(c, w);
     }
-  } else if (m.dtype == MOE_DTYPE_F32) {
-    const float* p = static_cast<const float*>(m.p) + row * m.ld;
+    return;
+  }
+  const uint16_t* p = static_cast<const uint16_t*>(m.p) + row * m.ld;
+  Raw r[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    r[c].a = col[c] < d ? __ldg(reinterpret_cast<const uint4*>(p + col[c])) : make_uint4(0u, 0u, 0u, 0u);
+  if (m.dtype == MOE_DTYPE_BF16) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      Raw r = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-      if (col[c] < d) {
-        r.a = __ldg(reinterpret_cast<const uint4*>(p + col[c]));
-        r.b = __ldg(reinterpret_cast<const uint4*>(p + col[c]) + 1);
-      }
       F2 w[4];
-      f32_to(r, w);
+      bf16_to(r[c], w);
       op(c, w);
     }
   } else {
-    const uint16_t* p = static_cast<const uint16_t*>(m.p) + row * m.ld;
-    Raw r[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-      r[c].a = col[c] < d ? __ldg(reinterpret_cast<const uint4*>(p + col[c])) : make_uint4(0u, 0u, 0u, 0u);
-    if (m.dtype == MOE_DTYPE_BF16) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        F2 w[4];
-        bf16_to(r[c], w);
-        op(c, w);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        F2 w[4];
-        f16_to(r[c], w);
-        op(c, w);
-      }
+    for (int c = 0; c < NC; ++c) {
+      F2 w[4];
+      f16_to(r[c], w);
+      op(c, w);
     }
   }
 }
@@ -348,33 +340,39 @@ __device__ __forceinline__ void store_chunk(void* to, const F2 (&v)[4]) {
     *static_cast<uint4*>(to) = make_uint4(f16_pair(v[0]), f16_pair(v[1]), f16_pair(v[2]), f16_pair(v[3]));
   }
 }
-// A warp's channels [w0, w0 + 256) of a row, eight per lane; `turn` (1 KB of the warp's shared memory) turns
-// them round where they cannot be stored as they are (Any).
-template <class E>
-__device__ __forceinline__ void store(const RowsOut& m, long long row, int w0, int lane, int d,
+// This lane's chunk c of a row. Any: `turn` (1 KB of the warp's shared memory) turns chunks round, as they
+// cannot be stored as they are.
+template <class E, int R>
+__device__ __forceinline__ void store(const RowsOut& m, int row, int c, int w0, int lane, int d,
                                       const F2 (&v)[4], float* turn) {
-  const long long at = row * m.ld + w0;
+  char* to = static_cast<char*>(m.p) + (size_t)(uint32_t)row * (m.ld * bytes_of<E>(m.dtype));
+  const int w = w0 + c * R * 8;
   if constexpr (!std::is_same_v<E, Any>) {
     constexpr int b = std::is_same_v<E, F32> ? 4 : 2;
-    if (w0 + lane * 8 < d) store_chunk<E>(static_cast<char*>(m.p) + (at + lane * 8) * b, v);
-    return;
-  }
-  F2* t = reinterpret_cast<F2*>(turn + lane * 8);
+    if (w + lane * 8 < d) store_chunk<E>(to + (w0 + lane * 8) * b + c * R * 8 * b, v);
+  } else {
+    if (w >= d) return;
+    F2* t = reinterpret_cast<F2*>(turn + lane * 8);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t[i] = v[i];
-  __syncwarp();
+    for (int i = 0; i < 4; ++i) t[i] = v[i];
+    __syncwarp();
+    const int left = d - w - lane;
+    if (m.dtype == MOE_DTYPE_F32) {
+      float* q = reinterpret_cast<float*>(to) + w + lane;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = i * 32 + lane;
-    if (w0 + c < d) {
-      if (m.dtype == MOE_DTYPE_F32)
-        static_cast<float*>(m.p)[at + c] = turn[c];
-      else
-        static_cast<uint16_t*>(m.p)[at + c] =
-            (uint16_t)(m.dtype == MOE_DTYPE_BF16 ? bf16_pair(turn[c], 0.f) : f16_pair(turn[c], 0.f));
+      for (int i = 0; i < 8; ++i)
+        if (i * 32 < left) q[i * 32] = turn[i * 32 + lane];
+    } else {
+      uint16_t* q = reinterpret_cast<uint16_t*>(to) + w + lane;
+      const bool bf16 = m.dtype == MOE_DTYPE_BF16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = turn[i * 32 + lane];
+        if (i * 32 < left) q[i * 32] = (uint16_t)(bf16 ? bf16_pair(f, 0.f) : f16_pair(f, 0.f));
+      }
     }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------------------- dropout
@@ -421,11 +419,12 @@ __device__ __forceinline__ void drop8(const Drop& d, const DropState& s, uint32_
 
 // ----------------------------------------------------------------------------------- sums of a row
 // A row is shared by R threads of one CTA, or by all threads of the cl CTAs of a cluster. Sums go over lanes,
-// warps and CTAs in a fixed order.
+// warps and CTAs in a fixed order. Of several sums a warp's halves (quarters) first take one each, so that four
+// cost six shuffles, not twenty.
 template <int R, bool CLUSTER>
 struct RowSum {
   static constexpr int kW = R / 32, kMost = CLUSTER ? 8 : 0;
-  static constexpr int kBuf = 2 * (kW + kMost);  // of two sums: [sum][warp], then [CTA][sum]
+  static constexpr int kBuf = 4 * (kW + kMost);  // of four sums: [sum][warp], then [CTA][sum]
   static constexpr int kFloats = 2 * kBuf;
   float* buf;                                    // 16-byte aligned
   int group, cl, turn;
@@ -434,20 +433,31 @@ struct RowSum {
 
   template <int N>
   __device__ __forceinline__ void operator()(float (&v)[N]) {
-    static_assert(N <= 2, "two at a time");
+    static_assert(N == 1 || N == 2 || N == 4, "one, two or four at a time");
+    const int lane = threadIdx.x % 32;
+    float s = v[0];
+    if constexpr (N == 4) {
+      const bool up = lane & 16;
+      const float a = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16) + (up ? v[2] : v[0]);
+      const float b = __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16) + (up ? v[3] : v[1]);
+      const bool odd = lane & 8;
+      s = __shfl_xor_sync(0xffffffffu, odd ? a : b, 8) + (odd ? b : a);
+    } else if constexpr (N == 2) {
+      const bool up = lane & 16;
+      s = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16) + (up ? v[1] : v[0]);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 16 / N; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    // lanes n * 32 / N and on have sum n
+    if constexpr (R == 32) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-    if constexpr (R > 32) {
-      const int warp = threadIdx.x % R / 32, lane = threadIdx.x % 32;
+      for (int n = 0; n < N; ++n) v[n] = N == 1 ? s : __shfl_sync(0xffffffffu, s, n * (32 / N));
+    } else {
+      const int warp = threadIdx.x % R / 32;
       // two buffers in turn: between two uses of one there is the other's barrier
       float* b = buf + turn * kBuf;
       turn ^= 1;
-      if (lane == 0) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) b[n * kW + warp] = v[n];
-      }
+      if (lane % (32 / N) == 0) b[lane / (32 / N) * kW + warp] = s;
       asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(R) : "memory");
 #pragma unroll
       for (int n = 0; n < N; ++n) {
@@ -465,60 +475,83 @@ struct RowSum {
         namespace cg = cooperative_groups;
         cg::cluster_group cluster = cg::this_cluster();
         if (threadIdx.x < cl) {
-          float* there = cluster.map_shared_rank(b + kW * 2, threadIdx.x);
+          float* there = cluster.map_shared_rank(b + kW * 4, threadIdx.x);
 #pragma unroll
-          for (int n = 0; n < N; ++n) there[cluster.block_rank() * 2 + n] = v[n];
+          for (int n = 0; n < N; ++n) there[cluster.block_rank() * 4 + n] = v[n];
         }
         cluster.sync();
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           v[n] = 0.f;
-          for (int i = 0; i < cl; ++i) v[n] += b[kW * 2 + i * 2 + n];
+          for (int i = 0; i < cl; ++i) v[n] += b[kW * 4 + i * 4 + n];
         }
       }
     }
   }
 };
 
-// Mean (0 for rms) and one over the deviation of a row (inv: one over its channels) whose threads hold x. What
-// is past the channels that end at d is 0 in x and does not count; EDGE: a chunk may lie across the end.
+__device__ __forceinline__ float total(F2 a, F2 b, F2 c, F2 d) {
+  const float2 f = both(add2(add2(a, b), add2(c, d)));
+  return f.x + f.y;
+}
+// A thread's share of sum(x y).
+template <int NC>
+__device__ __forceinline__ float dot(const F2 (&x)[NC][4], const F2 (&y)[NC][4]) {
+  F2 s[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = fma2(x[c][i], y[c][i], s[i]);
+  return total(s[0], s[1], s[2], s[3]);
+}
+template <int NC>
+__device__ __forceinline__ float plain_sum(const F2 (&x)[NC][4]) {
+  F2 s[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = add2(x[c][i], s[i]);
+  return total(s[0], s[1], s[2], s[3]);
+}
+// A thread's share of sum((x - mean)^2) over channels before d; EDGE: a chunk may lie across the end.
+template <int NC, bool EDGE>
+__device__ __forceinline__ float around(const F2 (&x)[NC][4], float mean, const int (&col)[NC], int d) {
+  const F2 m = twice(-mean);
+  F2 s[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    if (col[c] < d) {
+      F2 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = add2(x[c][i], m);
+      if constexpr (EDGE) each(v, [&](int i, float y) { return col[c] + i < d ? y : 0.f; });
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = fma2(v[i], v[i], s[i]);
+    }
+  return total(s[0], s[1], s[2], s[3]);
+}
+// One over the deviation from its squares' sum, within two units in the last place.
+__device__ __forceinline__ float deviation(float squares, float inv, float eps) {
+  return rsqrtf(fmaf(squares, inv, eps));
+}
+
+// Mean (0 for rms) and one over the deviation of a row (inv: one over its channels) whose threads hold x; what
+// is past the channels that end at d is 0 in x and does not count.
 template <int NC, bool EDGE, typename Sum>
 __device__ __forceinline__ void row_stats(Sum& sum, int kind, const F2 (&x)[NC][4], const int (&col)[NC],
                                           int d, float inv, float eps, float& mean, float& rstd) {
   mean = 0.f;
-  F2 s[4] = {0, 0, 0, 0};  // +0 twice; four chains
+  float q[1];
   if (kind == MOE_NORM_LAYER) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = add2(s[i], x[c][i]);
-    float2 f = both(add2(add2(s[0], s[1]), add2(s[2], s[3])));
-    float t[1] = {f.x + f.y};
-    sum(t);
-    mean = t[0] * inv;
-    const F2 m = twice(-mean);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = 0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-      if (col[c] < d) {
-        F2 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = add2(x[c][i], m);
-        if constexpr (EDGE) each(v, [&](int i, float y) { return col[c] + i < d ? y : 0.f; });
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = fma2(v[i], v[i], s[i]);
-      }
+    q[0] = plain_sum<NC>(x);
+    sum(q);
+    mean = q[0] * inv;
+    q[0] = around<NC, EDGE>(x, mean, col, d);
   } else {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = fma2(x[c][i], x[c][i], s[i]);
+    q[0] = dot<NC>(x, x);
   }
-  const float2 f = both(add2(add2(s[0], s[1]), add2(s[2], s[3])));
-  float q[1] = {f.x + f.y};
   sum(q);
-  rstd = rsqrtf(fmaf(q[0], inv, eps));  // within two units in the last place
+  rstd = deviation(q[0], inv, eps);
 }
 
 // How a row is shared: R threads with NC chunks of eight channels each, above 8192 channels a cluster.
