@@ -4,24 +4,27 @@
 // expert, no more than one token for most of them. One persistent CTA per SM (cooperative launch) goes
 // through four parts, with a grid barrier after the first and the third:
 //   router   one expert per CTA: logits of all tokens. Eight products at a time are summed in fp32, the
-//            sums of eight in an unevaluated pair of floats and at last in fp64, so the choice is that of
-//            the exact logits but for gaps of about 1e-8 of the logits' size;
+//            sums of eight in an unevaluated pair of floats, so the choice is that of the exact logits but
+//            for gaps of about 1e-8 of the logits' size;
 //   choice   every CTA makes it for itself, one warp per token, and lists the experts that were hit,
 //            their tokens ("columns") and gates;
 //   gate/up  H = silu(x W_gate) * (x W_up) of the listed experts' columns;
 //   down     out = sum over experts of gate * (H W_down), summed over all of them at once.
-// Gate/up and down are cut into tiles of 64 weight columns; the tiles' K steps, one after the other,
+// Gate/up and down are cut into tiles of 64 weight channels; the tiles' K steps, one after the other,
 // are dealt out to the CTAs in equal runs, so every SM streams the same number of bytes whatever the
 // number of experts. A tile that is cut between CTAs leaves partial sums in the workspace; the CTA that
 // finishes last adds them in order of their pieces (the result does not depend on who that is).
 //
-// Weights go through mma.sync m16n8k16 as the M operand, eight columns as N. They lie with the output
-// channel contiguous, so a lane reads four rows of 8 channels, 16 bytes each, and pairs rows by byte
-// permutes into the fragments of four MMAs; which channel is which fragment row is settled when results
-// are stored. Every lane reads back only what it copied itself (cp.async into its own slots of a ring),
-// so the ring needs no barrier. tcgen05 would want 128 rows of a token operand that has one.
+// Weights go through mma.sync m16n8k16 as the M operand, eight columns as N. Every warp has a ring of tiles of
+// 16 K rows x 64 channels that TMA brings (128-byte swizzle) and that no other warp reads. They lie with the
+// output channel contiguous, so a lane reads four rows of 8 channels, 16 bytes each, and pairs rows by byte
+// permutes into the fragments of four MMAs; which channel is which fragment row is settled when results are
+// stored. (The same pieces by cp.async or plain loads, 16 bytes a lane, come at 3.8 to 4.1 TB/s however many are
+// under way, by TMA at 5.4.) The columns' values come by cp.async into slots that only their lane reads.
+// tcgen05 would want 128 rows of a token operand that has one.
 // H is carried as two bf16 numbers (value and remainder, 2^-17 of it), as the second MMA is free here.
 #include <cuda_bf16.h>
+#include <cuda.h>
 #include <cmath>
 
 #include "few.cuh"
@@ -43,8 +46,8 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -93,12 +96,13 @@ struct Plan {
   uint8_t tok[kCols];        // token of a column
   float gate[kCols];
   int n_seg;
-  int fail, last;
+  volatile int fail;  // a wait ran past its limit
+  int last[2];
   unsigned gen;
 };
 // Scratch of router and choice, in the ring's memory before the ring is used.
 struct Scratch {
-  double red[kWarps];
+  float2 red[kWarps];
   float score[MOE_FEW_MAX_TOKENS][256];
   unsigned all[256][kSlots / 32];   // slots of an expert
   unsigned keep[256][kSlots / 32];  // those that are a column: kept, the first of their token
@@ -140,25 +144,51 @@ __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
   return p.fail == 0;
 }
 
-// One piece of a tile is in the workspace. True in every thread of the CTA that brought the last of n.
-__device__ __forceinline__ bool piece_done(const FewArgs& a, Plan& p, int owner, int n) {
+// A CTA's run of K steps begins and ends inside tiles, as a rule: at most two of its pieces, the first (0)
+// and the last (1), are parts of a tile whose other parts are other CTAs'. Those leave their sums in the
+// workspace, and only when the run is done does the CTA say so (under load a fence and an atomic take 4 us, in
+// which nothing would be read) and sees which tiles it has to join: those that it was the last to bring a part of.
+struct Cuts {
+  int head = -1, tail = -1;  // their tiles
+};
+__device__ __forceinline__ float* cut_sums(const FewArgs& a, int cta, int which) {
+  return a.part + (size_t)cta * a.part_floats + which * (a.part_floats / 2);
+}
+// Which of its two cut pieces of a tile of K steps is CTA b's, when a run is `per` steps.
+__device__ __forceinline__ int cut_of(int b, int per, int tile, int K) { return b * per <= tile * K ? 1 : 0; }
+
+__device__ __forceinline__ unsigned bring_part(const FewArgs& a, int tile, int K, int per) {
+  if (tile < 0) return 0;
+  const int owner = tile * K / per;
+  return atomicAdd(&a.meta->piece[owner >> 2], 1u << (owner & 3) * 8);
+}
+__device__ __forceinline__ int was_last(const FewArgs& a, unsigned before, int tile, int K, int per) {
+  if (tile < 0) return 0;
+  const int owner = tile * K / per, at = (owner & 3) * 8;
+  const unsigned n = ((tile + 1) * K - 1) / per - owner + 1;
+  if ((before >> at & 255u) != n - 1) return 0;
+  atomicSub(&a.meta->piece[owner >> 2], n << at);  // zero again for the next part and the next call
+  return 1;
+}
+__device__ __forceinline__ void say_cuts(const FewArgs& a, Plan& p, const Cuts& cuts, int K, int per) {
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    unsigned* word = &a.meta->piece[owner >> 2];
-    const int at = (owner & 3) * 8;
-    const unsigned before = (atomicAdd(word, 1u << at) >> at) & 255u;
-    p.last = before == (unsigned)(n - 1);
-    if (p.last) {
-      atomicSub(word, (unsigned)n << at);  // zero again for the next part and the next call
-      __threadfence();
-    }
+    const unsigned head = bring_part(a, cuts.head, K, per), tail = bring_part(a, cuts.tail, K, per);
+    p.last[0] = was_last(a, head, cuts.head, K, per);
+    p.last[1] = was_last(a, tail, cuts.tail, K, per);
+    __threadfence();
   }
   __syncthreads();
-  return p.last != 0;
 }
 
 // ------------------------------------------------------------------------------------------ router
+// hi + s exactly: the rounding error of the sum (Knuth) goes to lo.
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float s) {
+  const float sum = hi + s, back = sum - hi;
+  lo += (hi - (sum - back)) + (s - back);
+  hi = sum;
+}
 // logits[t, e] of expert e for every token; warps share out tokens, then the pieces of d.
 __device__ void router(const FewArgs& a, Scratch& sc, int warp, int lane) {
   int wpt = kWarps;  // warps per token
@@ -181,22 +211,25 @@ __device__ void router(const FewArgs& a, Scratch& sc, int warp, int lane) {
         s = fmaf(bf16_hi(wv.z), bf16_hi(xv.z), s);
         s = fmaf(bf16_lo(wv.w), bf16_lo(xv.w), s);
         s = fmaf(bf16_hi(wv.w), bf16_hi(xv.w), s);
-        // hi + s exactly: the rounding error of the sum (Knuth) goes to lo
-        const float sum = hi + s, back = sum - hi;
-        lo += (hi - (sum - back)) + (s - back);
-        hi = sum;
+        add_exact(hi, lo, s);
       }
-      // of an infinite sum only hi says which
-      double v = isfinite(hi) ? (double)hi + lo : (double)hi;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-      if (lane == 0) sc.red[warp] = v;
+      for (int o = 16; o > 0; o >>= 1) {
+        lo += __shfl_xor_sync(kFull, lo, o);
+        add_exact(hi, lo, __shfl_xor_sync(kFull, hi, o));
+      }
+      if (lane == 0) sc.red[warp] = make_float2(hi, lo);
     }
     __syncthreads();
     if (threadIdx.x < a.T) {
-      double v = 0.;
-      for (int i = 0; i < wpt; ++i) v += sc.red[threadIdx.x * wpt + i];
-      a.logits[threadIdx.x * a.E + e] = (float)v;
+      float2 v = sc.red[threadIdx.x * wpt];
+      for (int i = 1; i < wpt; ++i) {
+        const float2 w = sc.red[threadIdx.x * wpt + i];
+        v.y += w.y;
+        add_exact(v.x, v.y, w.x);
+      }
+      // of an infinite sum only the first part says which
+      a.logits[threadIdx.x * a.E + e] = isfinite(v.x) ? v.x + v.y : v.x;
     }
     __syncthreads();
   }
@@ -299,7 +332,7 @@ __device__ __forceinline__ int rank_of(const unsigned (&m)[kSlots / 32], int s) 
 // the same expert twice has one column with both gates. Of an expert's slots the first C count.
 __device__ void make_plan(const FewArgs& a, Plan& p, Scratch& sc, int warp, int lane) {
   const int n = a.T * a.k, tid = threadIdx.x;
-  for (int i = tid; i < 256 * (kSlots / 32); i += kThreads) {
+  for (int i = tid; i < a.E * (kSlots / 32); i += kThreads) {
     (&sc.all[0][0])[i] = 0;
     (&sc.keep[0][0])[i] = 0;
   }
@@ -425,20 +458,50 @@ struct Deal {
   __device__ int end() const { return min(total, ((int)blockIdx.x + 1) * per); }
 };
 
-// A lane's side of the ring: slot s of `kSlot` bytes holds four 16-byte pieces of weights (rows 4 q .. 4 q
-// + 3 of the K step, channels 8 g .. 8 g + 7) and, per 8 columns, its piece of the other operand.
-template <int NT>
+// A warp's ring: kStages tiles of weights (16 rows of 64 channels, 2 KB) and, for each, its lanes' pieces of the
+// columns' values (16 bytes per lane and 8 columns). Tiles are taken in the order they were asked for.
+template <int NT, int kStages>
 struct Ring {
-  static constexpr int kSlot = 2048 + 512 * NT;
-  uint32_t w, b;  // addresses of the lane's pieces in slot 0
-  __device__ Ring(uint32_t base, int lane) : w(base + lane * 16), b(base + 2048 + lane * 16) {}
+  static constexpr int kTile = 2048, kPiece = 512 * NT;
+  uint32_t w, b, bar;  // slot 0: the tile, this lane's piece, the tile's mbarrier
+  int slot;            // the next tile to be taken
+  uint32_t phase;
+
+  __device__ __forceinline__ uint32_t tile(int i) const { return w + i * kTile; }
+  __device__ __forceinline__ uint32_t piece(int i) const { return b + i * kPiece; }
+  __device__ __forceinline__ int later(int i) const {  // the slot i places on
+    const int k = slot + i;
+    return k >= kStages ? k - kStages : k;
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == kStages) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  // Until the tile and this lane's piece are there. A wait that runs past its limit lets the kernel go on with
+  // what there is (later waits give up at once), and the status word says so.
+  __device__ __forceinline__ void wait(const FewArgs& a, Plan& p) const {
+    ptx::mbar_wait_bounded_warp(bar + 8 * slot, phase, &p.fail, a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
+                                kWaitLimitNs);
+    cp_wait<kStages - 1>();
+  }
+  // One lane asks for a tile. What the warp read of the slot before is in registers.
+  __device__ __forceinline__ void ask(int i, const CUtensorMap* map, int c, int row, int matrix) const {
+    const uint32_t m = bar + 8 * i;
+    ptx::mbar_arrive_expect_tx(m, kTile);
+    ptx::tma_load_3d(tile(i), map, m, c, row, matrix);
+  }
 };
 
-// Reads a slot's weights into the fragments of four MMAs: rows of fragment j are channels 8 g + 2 j (its
-// rows 0-7) and 8 g + 2 j + 1 (rows 8-15).
-__device__ __forceinline__ void fragments(uint32_t addr, uint32_t (&f)[4][4]) {
-  const uint4 r0 = lds16(addr), r1 = lds16(addr + 512), r2 = lds16(addr + 1024),
-              r3 = lds16(addr + 1536);
+// Reads a tile into the fragments of four MMAs: rows of fragment j are channels 8 g + 2 j (its rows 0-7) and
+// 8 g + 2 j + 1 (rows 8-15) for lane 4 g + q, whose K rows are 2 q, 2 q + 1, 2 q + 8, 2 q + 9. Swizzled: 16-byte
+// piece c of row r is at c ^ (r % 8), so the eight lanes of a quarter of a load read eight different ones.
+__device__ __forceinline__ void fragments(uint32_t tile, int lane, uint32_t (&f)[4][4]) {
+  const int g = lane >> 2, q = lane & 3;
+  const uint32_t even = tile + q * 256 + ((g ^ (2 * q)) << 4);
+  const uint32_t odd = tile + q * 256 + 128 + ((g ^ (2 * q + 1)) << 4);
+  const uint4 r0 = lds16(even), r1 = lds16(odd), r2 = lds16(even + 1024), r3 = lds16(odd + 1024);
   const uint32_t a0[4] = {r0.x, r0.y, r0.z, r0.w}, a1[4] = {r1.x, r1.y, r1.z, r1.w};
   const uint32_t a2[4] = {r2.x, r2.y, r2.z, r2.w}, a3[4] = {r3.x, r3.y, r3.z, r3.w};
 #pragma unroll
@@ -450,25 +513,21 @@ __device__ __forceinline__ void fragments(uint32_t addr, uint32_t (&f)[4][4]) {
   }
 }
 
-__device__ __forceinline__ void issue_weights(uint32_t slot, const uint16_t* src, size_t ld) {
-#pragma unroll
-  for (int r = 0; r < 4; ++r) cp_async16(slot + 512 * r, src + r * ld, 16);
-}
-
 // Where a warp is in its K steps of gate/up: tile j (expert and 64 channels), step s of it.
-template <int NT>
+template <int NT, int kStages>
 struct UpFeed {
   const FewArgs& a;
+  const FewMaps& maps;
   const Plan& p;
   const Deal& deal;
-  int slice, lane, mat, j, s, kend;
-  const uint16_t* w;
+  int slice, lane, mat, j, s, kend, channel, matrix;
+  const CUtensorMap* map;
   const uint16_t* x[NT];
   uint32_t bytes[NT];
   bool more;
 
-  __device__ UpFeed(const FewArgs& a_, const Plan& p_, const Deal& d_, int warp, int lane_)
-      : a(a_), p(p_), deal(d_), slice(warp >> 1), lane(lane_), mat(warp & 1) {
+  __device__ UpFeed(const FewArgs& a_, const FewMaps& m_, const Plan& p_, const Deal& d_, int warp, int lane_)
+      : a(a_), maps(m_), p(p_), deal(d_), slice(warp >> 1), lane(lane_), mat(warp & 1) {
     j = deal.begin() / deal.K;
     s = deal.begin() - j * deal.K + slice;
     kend = min(deal.K, deal.end() - j * deal.K);
@@ -479,17 +538,16 @@ struct UpFeed {
     }
   }
   __device__ void tile() {
-    const int nfb = a.f / 64, seg = j / nfb, fb = j - seg * nfb, e = p.seg_e[seg];
-    const uint16_t* m = e < a.E ? (mat ? a.up : a.gate) + (size_t)e * a.d * a.f
-                                : (mat ? a.sh_up : a.sh_gate) + (size_t)(e - a.E) * a.d * a.f;
-    const int g = lane >> 2, q = lane & 3;
-    w = m + (size_t)(4 * q) * a.f + fb * 64 + g * 8;
-    const int base = p.seg_base[seg], cnt = p.seg_base[seg + 1] - base;
+    const int nfb = a.f / 64, seg = j / nfb, e = p.seg_e[seg];
+    map = e < a.E ? (mat ? &maps.up : &maps.gate) : (mat ? &maps.sh_up : &maps.sh_gate);
+    matrix = e < a.E ? e : e - a.E;
+    channel = (j - seg * nfb) * 64;
+    const int g = lane >> 2, q = lane & 3, base = p.seg_base[seg], cnt = p.seg_base[seg + 1] - base;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const bool there = g + 8 * n < cnt;
-      bytes[n] = there ? 8 : 0;
-      x[n] = a.x + (size_t)(there ? p.tok[base + g + 8 * n] : 0) * a.d + 4 * q;
+      bytes[n] = there ? 4 : 0;
+      x[n] = a.x + (size_t)(there ? p.tok[base + g + 8 * n] : 0) * a.d + 2 * q;
     }
   }
   __device__ void settle() {
@@ -504,12 +562,15 @@ struct UpFeed {
       tile();
     }
   }
-  __device__ __forceinline__ void issue(const Ring<NT>& r, int slot) {
+  __device__ __forceinline__ void issue(const Ring<NT, kStages>& r, int slot) {
     if (more) {
-      const uint32_t o = slot * Ring<NT>::kSlot;
-      issue_weights(r.w + o, w + (size_t)s * 16 * a.f, a.f);
+      if (lane == 0) r.ask(slot, map, channel, s * 16, matrix);
+      const uint32_t to = r.piece(slot);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) cp_async8(r.b + o + 512 * n, x[n] + s * 16, bytes[n]);
+      for (int n = 0; n < NT; ++n) {
+        cp_async4(to + 512 * n, x[n] + s * 16, bytes[n]);
+        cp_async4(to + 512 * n + 4, x[n] + s * 16 + 8, bytes[n]);
+      }
       s += 8;
       if (s >= kend) settle();
     }
@@ -539,8 +600,9 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// Four channels of H as 16 bytes: four bf16 values, then the four remainders.
-__device__ __forceinline__ uint4 split_h(float4 g, float4 u) {
+// Four channels of H, 4 c4 and on, of a column's row. 16 channels are 64 bytes: for each q the bf16 values of
+// channels 2 q, 2 q + 1, 2 q + 8, 2 q + 9, then the four remainders (a lane's K rows of an MMA).
+__device__ __forceinline__ void store_h(uint32_t* row, int c4, float4 g, float4 u) {
   const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
   uint32_t hi[4], lo[4];
 #pragma unroll
@@ -552,35 +614,39 @@ __device__ __forceinline__ uint4 split_h(float4 g, float4 u) {
     // an infinite or NaN value has no remainder
     lo[i] = isfinite(back) ? __bfloat16_as_ushort(__float2bfloat16_rn(h - back)) : 0;
   }
-  return make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  uint32_t* to = row + (c4 >> 2) * 16 + (c4 & 1) * 8 + ((c4 >> 1) & 1);
+  to[0] = hi[0] | hi[1] << 16;
+  to[2] = lo[0] | lo[1] << 16;
+  to[4] = hi[2] | hi[3] << 16;
+  to[6] = lo[2] | lo[3] << 16;
 }
 
 template <int NT, int kStages>
-__device__ void gate_up(const FewArgs& a, Plan& p, float* acc_s, uint32_t ring_base, int warp, int lane) {
+__device__ void gate_up(const FewArgs& a, const FewMaps& maps, Plan& p, float* acc_s,
+                        Ring<NT, kStages>& ring, int warp, int lane) {
   const int nfb = a.f / 64;
   // a tile of up to 32 steps (four of a warp) is not cut: joining the pieces would take longer
   const Deal deal(a.d / 16, p.n_seg * nfb, 32);
-  UpFeed<NT> feed(a, p, deal, warp, lane);
-  const Ring<NT> ring(ring_base, lane);
+  UpFeed<NT, kStages> feed(a, maps, p, deal, warp, lane);
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) feed.issue(ring, i);
-  int slot = 0;
+  for (int i = 0; i < kStages; ++i) feed.issue(ring, ring.later(i));
   const int slice = warp >> 1, begin = deal.begin(), end = deal.end();
+  Cuts cuts;
   for (int at = begin; at < end;) {
     const int j = at / deal.K, k0 = at - j * deal.K, k1 = min(deal.K, end - j * deal.K);
     const int seg = j / nfb, fb = j - seg * nfb;
     const int base = p.seg_base[seg], cnt = p.seg_base[seg + 1] - base;
     float acc[NT][4][4] = {};
     for (int s = k0 + slice; s < k1; s += 8) {
-      cp_wait<kStages - 1>();
-      const uint32_t o = slot * Ring<NT>::kSlot;
+      ring.wait(a, p);
       uint32_t f[4][4];
-      fragments(ring.w + o, f);
+      fragments(ring.tile(ring.slot), lane, f);
       uint2 b[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) b[n] = lds8(ring.b + o + 512 * n);
-      feed.issue(ring, slot);
-      slot = slot + 1 == kStages ? 0 : slot + 1;
+      for (int n = 0; n < NT; ++n) b[n] = lds8(ring.piece(ring.slot) + 512 * n);
+      __syncwarp();
+      feed.issue(ring, ring.slot);
+      ring.next();
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         if (n == 0 || cnt > 8)
@@ -590,8 +656,9 @@ __device__ void gate_up(const FewArgs& a, Plan& p, float* acc_s, uint32_t ring_b
     store_sums<NT>(acc_s + warp * (8 * NT) * kAccLd, acc, cnt, lane);
     __syncthreads();
     const bool whole = k0 == 0 && k1 == deal.K;
-    const int first = j * deal.K / deal.per, last = ((j + 1) * deal.K - 1) / deal.per;
-    float* part = a.part + (size_t)blockIdx.x * a.part_floats + (k0 == 0 ? a.part_floats / 2 : 0);
+    const int which = k0 == 0 ? 1 : 0;
+    if (!whole) (k0 == 0 ? cuts.tail : cuts.head) = j;
+    float4* part = reinterpret_cast<float4*>(cut_sums(a, blockIdx.x, which));
     for (int i = threadIdx.x; i < cnt * 16; i += kThreads) {
       const int c = i >> 4, c4 = i & 15;
       float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
@@ -602,94 +669,96 @@ __device__ void gate_up(const FewArgs& a, Plan& p, float* acc_s, uint32_t ring_b
         u = add4(u, *reinterpret_cast<const float4*>(row + (8 * NT) * kAccLd));
       }
       if (whole) {
-        reinterpret_cast<uint4*>(a.h + (size_t)(base + c) * a.f)[fb * 16 + c4] = split_h(g, u);
+        store_h(a.h + (size_t)(base + c) * a.f, fb * 16 + c4, g, u);
       } else {
-        reinterpret_cast<float4*>(part)[i] = g;
-        reinterpret_cast<float4*>(part)[16 * MOE_FEW_MAX_TOKENS + i] = u;
-      }
-    }
-    if (!whole && piece_done(a, p, first, last - first + 1)) {
-      for (int i = threadIdx.x; i < cnt * 16; i += kThreads) {
-        float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
-        for (int b = first; b <= last; ++b) {
-          const float4* from = reinterpret_cast<const float4*>(
-              a.part + (size_t)b * a.part_floats + (b * deal.per <= j * deal.K ? a.part_floats / 2 : 0));
-          g = add4(g, __ldcg(from + i));
-          u = add4(u, __ldcg(from + 16 * MOE_FEW_MAX_TOKENS + i));
-        }
-        reinterpret_cast<uint4*>(a.h + (size_t)(base + (i >> 4)) * a.f)[fb * 16 + (i & 15)] =
-            split_h(g, u);
+        part[i] = g;
+        part[16 * MOE_FEW_MAX_TOKENS + i] = u;
       }
     }
     at = j * deal.K + k1;
     __syncthreads();  // the sums' memory is free again
   }
   cp_wait<0>();
+  say_cuts(a, p, cuts, deal.K, deal.per);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!p.last[k]) continue;
+    const int j = k == 0 ? cuts.head : cuts.tail, seg = j / nfb, fb = j - seg * nfb;
+    const int base = p.seg_base[seg], cnt = p.seg_base[seg + 1] - base;
+    const int first = j * deal.K / deal.per, last = ((j + 1) * deal.K - 1) / deal.per;
+    for (int i = threadIdx.x; i < cnt * 16; i += kThreads) {
+      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+#pragma unroll 4
+      for (int b = first; b <= last; ++b) {
+        const float4* from = reinterpret_cast<const float4*>(cut_sums(a, b, cut_of(b, deal.per, j, deal.K)));
+        g = add4(g, __ldcg(from + i));
+        u = add4(u, __ldcg(from + 16 * MOE_FEW_MAX_TOKENS + i));
+      }
+      store_h(a.h + (size_t)(base + (i >> 4)) * a.f, fb * 16 + (i & 15), g, u);
+    }
+  }
 }
 
-// Where a warp is in its K steps of down: column group cg, step s of all experts' channels in a row.
-template <int NT>
+// Where a warp is in its K steps of down: tile j (64 channels), step s of all experts' channels in a row.
+template <int NT, int kStages>
 struct DownFeed {
   const FewArgs& a;
+  const FewMaps& maps;
   const Plan& p;
   const Deal& deal;
-  int cw, ks, wc, slice, lane, fs, cg, s, kend, seg;
-  const uint16_t* w;
+  int slice, lane, fs, j, s, kend, seg, matrix;
+  const CUtensorMap* map;
   const uint4* h[NT];
   uint32_t bytes[NT];
   bool more;
 
-  __device__ DownFeed(const FewArgs& a_, const Plan& p_, const Deal& d_, int cw_, int warp, int lane_)
-      : a(a_), p(p_), deal(d_), cw(cw_), ks(kWarps / cw_), wc(warp % cw_), slice(warp / cw_),
-        lane(lane_), fs(a_.f / 16) {
-    cg = deal.begin() < deal.end() ? deal.begin() / deal.K : 0;
-    s = deal.begin() - cg * deal.K + slice;
-    kend = min(deal.K, deal.end() - cg * deal.K);
+  __device__ DownFeed(const FewArgs& a_, const FewMaps& m_, const Plan& p_, const Deal& d_, int warp, int lane_)
+      : a(a_), maps(m_), p(p_), deal(d_), slice(warp), lane(lane_), fs(a_.f / 16) {
+    j = deal.begin() / deal.K;
+    s = deal.begin() - j * deal.K + slice;
+    kend = min(deal.K, deal.end() - j * deal.K);
     more = deal.begin() < deal.end();
     if (more) settle();
   }
-  // Channels past d are nobody's: such a warp has no steps in this column group.
-  __device__ bool there() const { return (cg * cw + wc) * 64 < a.d; }
   __device__ void expert() {
     const int e = p.seg_e[seg], g = lane >> 2, q = lane & 3;
-    const uint16_t* m = e < a.E ? a.down + (size_t)e * a.f * a.d
-                                : a.sh_down + (size_t)(e - a.E) * a.f * a.d;
-    w = m + (size_t)(4 * q) * a.d + (cg * cw + wc) * 64 + g * 8;
+    map = e < a.E ? &maps.down : &maps.sh_down;
+    matrix = e < a.E ? e : e - a.E;
     const int base = p.seg_base[seg], cnt = p.seg_base[seg + 1] - base;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const bool col = g + 8 * n < cnt;
-      bytes[n] = col ? 16 : 0;
-      h[n] = reinterpret_cast<const uint4*>(a.h + (size_t)(base + (col ? g + 8 * n : 0)) * a.f) + q;
+      const bool there = g + 8 * n < cnt;
+      bytes[n] = there ? 16 : 0;
+      h[n] = reinterpret_cast<const uint4*>(a.h + (size_t)(base + (there ? g + 8 * n : 0)) * a.f) + q;
     }
   }
   __device__ void settle() {
-    while (s >= kend || !there()) {
-      ++cg;
-      if (cg * deal.K >= deal.end()) {
+    while (s >= kend) {
+      ++j;
+      if (j * deal.K >= deal.end()) {
         more = false;
         return;
       }
       s = slice;
-      kend = min(deal.K, deal.end() - cg * deal.K);
+      kend = min(deal.K, deal.end() - j * deal.K);
     }
     seg = s / fs;
     expert();
   }
-  __device__ __forceinline__ void issue_w(const Ring<NT>& r, int slot) const {
-    if (more)
-      issue_weights(r.w + slot * Ring<NT>::kSlot, w + (size_t)(s - seg * fs) * 16 * a.d, a.d);
+  __device__ __forceinline__ void issue_w(const Ring<NT, kStages>& r, int slot) const {
+    if (more && lane == 0) r.ask(slot, map, j * 64, (s - seg * fs) * 16, matrix);
   }
-  __device__ __forceinline__ void issue_h(const Ring<NT>& r, int slot) const {
+  __device__ __forceinline__ void issue_h(const Ring<NT, kStages>& r, int slot) const {
     if (more) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        cp_async16(r.b + slot * Ring<NT>::kSlot + 512 * n, h[n] + (s - seg * fs) * 4, bytes[n]);
+        cp_async16(r.piece(slot) + 512 * n, h[n] + (s - seg * fs) * 4, bytes[n]);
     }
+    cp_commit();
   }
   __device__ __forceinline__ void next() {
     if (!more) return;
-    s += ks;
+    s += kWarps;
     if (s >= kend) {
       settle();
     } else if (s >= (seg + 1) * fs) {
@@ -735,113 +804,82 @@ __device__ __forceinline__ uint2 bf16x4(float4 v) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Warps side by side in `down`: the widest group that leaves at most an eighth of its channels unused.
-// A CTA's H is then the smaller the wider the group is.
-__device__ __forceinline__ int down_width(int d) {
-  const int nb = d / 64;
-  for (int cw = 8; cw > 1; cw >>= 1)
-    if ((nb + cw - 1) / cw * cw * 8 <= nb * 9) return cw;
-  return 1;
-}
-
 template <int NT, int kStages>
-__device__ bool down(const FewArgs& a, Plan& p, float* acc_s, uint32_t ring_base, int warp, int lane) {
-  const int cw = down_width(a.d), ks = kWarps / cw, fs = a.f / 16;
-  const int nb = a.d / 64, ncg = (nb + cw - 1) / cw, width = cw * 64;
-  const Deal deal(p.n_seg * fs, ncg, 4 * ks);
+__device__ void down(const FewArgs& a, const FewMaps& maps, Plan& p, float* acc_s, Ring<NT, kStages>& ring,
+                     int warp, int lane) {
+  const int fs = a.f / 16;
+  // as in gate/up a tile is not cut below four steps of a warp
+  const Deal deal(p.n_seg * fs, a.d / 64, 4 * kWarps);
   const int begin = deal.begin(), end = deal.end();
-  DownFeed<NT> feed(a, p, deal, cw, warp, lane);
-  const Ring<NT> ring(ring_base, lane);
+  Cuts cuts;
+  DownFeed<NT, kStages> feed(a, maps, p, deal, warp, lane);
   {
     // the first weights are on their way while the other CTAs finish H
-    DownFeed<NT> ahead = feed;
+    DownFeed<NT, kStages> ahead = feed;
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
-      ahead.issue_w(ring, i);
+      ahead.issue_w(ring, ring.later(i));
       ahead.next();
     }
   }
   float* mine = acc_s + warp * (8 * NT) * kAccLd;
   for (int i = lane; i < a.T * kAccLd; i += 32) mine[i] = 0.f;
   __syncwarp();
-  if (!barrier_wait(a, p)) {
-    cp_commit();
-    cp_wait<0>();
-    return false;
-  }
+  barrier_wait(a, p);  // past its limit the rest runs on what there is, and takes the copies under way
 #pragma unroll
   for (int i = 0; i < kStages; ++i) {
-    feed.issue_h(ring, i);
-    cp_commit();
+    feed.issue_h(ring, ring.later(i));
     feed.next();
   }
-  int slot = 0;
-  const int wc = warp % cw, slice = warp / cw;
   for (int at = begin; at < end;) {
-    const int cg = at / deal.K, k0 = at - cg * deal.K, k1 = min(deal.K, end - cg * deal.K);
-    if ((cg * cw + wc) * 64 < a.d) {
-      float acc[NT][4][4] = {};
-      int seg = (k0 + slice) / fs, cnt = 0, seg_end = 0;
-      for (int s = k0 + slice; s < k1; s += ks) {
-        if (s >= seg_end) {
-          if (seg_end > 0) add_sums<NT>(mine, acc, p, seg, lane);
-          seg = s / fs;
-          seg_end = (seg + 1) * fs;
-          cnt = p.seg_base[seg + 1] - p.seg_base[seg];
-        }
-        cp_wait<kStages - 1>();
-        const uint32_t o = slot * Ring<NT>::kSlot;
-        uint32_t f[4][4];
-        fragments(ring.w + o, f);
-        uint4 b[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) b[n] = lds16(ring.b + o + 512 * n);
-        feed.issue_w(ring, slot);
-        feed.issue_h(ring, slot);
-        cp_commit();
-        feed.next();
-        slot = slot + 1 == kStages ? 0 : slot + 1;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (n == 0 || cnt > 8)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              mma(acc[n][m], f[m], b[n].x, b[n].y);
-              mma(acc[n][m], f[m], b[n].z, b[n].w);
-            }
+    const int j = at / deal.K, k0 = at - j * deal.K, k1 = min(deal.K, end - j * deal.K);
+    float acc[NT][4][4] = {};
+    int seg = 0, cnt = 0, seg_end = 0;
+    for (int s = k0 + warp; s < k1; s += kWarps) {
+      if (s >= seg_end) {
+        if (seg_end > 0) add_sums<NT>(mine, acc, p, seg, lane);
+        seg = s / fs;
+        seg_end = (seg + 1) * fs;
+        cnt = p.seg_base[seg + 1] - p.seg_base[seg];
       }
-      if (seg_end > 0) add_sums<NT>(mine, acc, p, seg, lane);
+      ring.wait(a, p);
+      uint32_t f[4][4];
+      fragments(ring.tile(ring.slot), lane, f);
+      uint4 b[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) b[n] = lds16(ring.piece(ring.slot) + 512 * n);
+      __syncwarp();
+      feed.issue_w(ring, ring.slot);
+      feed.issue_h(ring, ring.slot);
+      feed.next();
+      ring.next();
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (n == 0 || cnt > 8)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            mma(acc[n][m], f[m], b[n].x, b[n].y);
+            mma(acc[n][m], f[m], b[n].z, b[n].w);
+          }
     }
+    if (seg_end > 0) add_sums<NT>(mine, acc, p, seg, lane);
     __syncthreads();
     const bool whole = k0 == 0 && k1 == deal.K;
-    const int first = cg * deal.K / deal.per, last = ((cg + 1) * deal.K - 1) / deal.per;
-    float* part = a.part + (size_t)blockIdx.x * a.part_floats + (k0 == 0 ? a.part_floats / 2 : 0);
-    const int quads = min(width, a.d - cg * width) / 4;  // of this group's channels
-    for (int i = threadIdx.x; i < a.T * quads; i += kThreads) {
-      const int t = i / quads, c4 = i - t * quads;
+    const int which = k0 == 0 ? 1 : 0;
+    if (!whole) (k0 == 0 ? cuts.tail : cuts.head) = j;
+    float4* part = reinterpret_cast<float4*>(cut_sums(a, blockIdx.x, which));
+    for (int i = threadIdx.x; i < a.T * 16; i += kThreads) {
+      const int t = i >> 4, c4 = i & 15;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < ks; ++k)
-        v = add4(v, *reinterpret_cast<const float4*>(
-                        acc_s + ((k * cw + (c4 >> 4)) * (8 * NT) + t) * kAccLd + 4 * (c4 & 15)));
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        v = add4(v, *reinterpret_cast<const float4*>(acc_s + (w * (8 * NT) + t) * kAccLd + 4 * c4));
       if (whole)
-        *reinterpret_cast<uint2*>(a.out + (size_t)t * a.d + cg * width + 4 * c4) = bf16x4(v);
+        *reinterpret_cast<uint2*>(a.out + (size_t)t * a.d + j * 64 + 4 * c4) = bf16x4(v);
       else
-        reinterpret_cast<float4*>(part)[i] = v;
+        part[i] = v;
     }
-    if (!whole && piece_done(a, p, first, last - first + 1)) {
-      for (int i = threadIdx.x; i < a.T * quads; i += kThreads) {
-        const int t = i / quads, c4 = i - t * quads;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int b = first; b <= last; ++b)
-          v = add4(v, __ldcg(reinterpret_cast<const float4*>(
-                                 a.part + (size_t)b * a.part_floats +
-                                 (b * deal.per <= cg * deal.K ? a.part_floats / 2 : 0)) +
-                             i));
-        *reinterpret_cast<uint2*>(a.out + (size_t)t * a.d + cg * width + 4 * c4) = bf16x4(v);
-      }
-    }
-    at = cg * deal.K + k1;
+    at = j * deal.K + k1;
     __syncthreads();
     if (at < end) {
       for (int i = lane; i < a.T * kAccLd; i += 32) mine[i] = 0.f;
@@ -849,23 +887,63 @@ __device__ bool down(const FewArgs& a, Plan& p, float* acc_s, uint32_t ring_base
     }
   }
   cp_wait<0>();
-  return true;
+  say_cuts(a, p, cuts, deal.K, deal.per);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!p.last[k]) continue;
+    const int j = k == 0 ? cuts.head : cuts.tail, first = j * deal.K / deal.per, last = ((j + 1) * deal.K - 1) / deal.per;
+    for (int i = threadIdx.x; i < a.T * 16; i += kThreads) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int b = first; b <= last; ++b)
+        v = add4(v, __ldcg(reinterpret_cast<const float4*>(
+                               cut_sums(a, b, cut_of(b, deal.per, j, deal.K))) +
+                           i));
+      *reinterpret_cast<uint2*>(a.out + (size_t)(i >> 4) * a.d + j * 64 + 4 * (i & 15)) = bf16x4(v);
+    }
+  }
 }
 
+template <int NT, int kStages>
+constexpr int ring_bytes() {
+  return kWarps * kStages * (Ring<NT, kStages>::kTile + Ring<NT, kStages>::kPiece);
+}
 template <int NT, int kStages>
 constexpr int smem_bytes() {
-  return kWarps * (kStages * Ring<NT>::kSlot + 8 * NT * kAccLd * 4);
+  return 1024 + ring_bytes<NT, kStages>() + kWarps * 8 * NT * kAccLd * 4;  // 1024: swizzled tiles' alignment
 }
 
 template <int NT, int kStages>
-__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 1)
+    few_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ FewMaps maps) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Plan p;
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  uint8_t* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Scratch& sc = *reinterpret_cast<Scratch*>(smem);
-  static_assert(sizeof(Scratch) <= kWarps * kStages * Ring<NT>::kSlot, "it lies in the ring");
-  const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * Ring<NT>::kSlot;
-  float* acc_s = reinterpret_cast<float*>(smem + kWarps * kStages * Ring<NT>::kSlot);
+  static_assert(sizeof(Scratch) <= ring_bytes<NT, kStages>(), "it lies in the ring");
+  float* acc_s = reinterpret_cast<float*>(smem + ring_bytes<NT, kStages>());
+  Ring<NT, kStages> ring;
+  ring.w = ptx::smem_u32(smem) + warp * kStages * ring.kTile;
+  ring.b = ptx::smem_u32(smem) + kWarps * kStages * ring.kTile + warp * kStages * ring.kPiece + lane * 16;
+  ring.bar = ptx::smem_u32(&bars[warp][0]);
+  ring.slot = 0;
+  ring.phase = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) ptx::mbar_init(ring.bar + 8 * i, 1);
+    ptx::fence_mbarrier_init();
+  }
+  if (threadIdx.x == kThreads - 1) {
+    ptx::prefetch_tmap(&maps.gate);
+    ptx::prefetch_tmap(&maps.up);
+    ptx::prefetch_tmap(&maps.down);
+    if (a.S > 0) {
+      ptx::prefetch_tmap(&maps.sh_gate);
+      ptx::prefetch_tmap(&maps.sh_up);
+      ptx::prefetch_tmap(&maps.sh_down);
+    }
+  }
   if (threadIdx.x == 0) {
     p.fail = 0;
     p.gen = *reinterpret_cast<volatile unsigned*>(&a.meta->gen);
@@ -888,13 +966,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       reinterpret_cast<uint2*>(a.out)[i] = make_uint2(0u, 0u);
     return;
   }
-  gate_up<NT, kStages>(a, p, acc_s, ring, warp, lane);
+  ptx::fence_proxy_async_smem();  // the scratch gives way to tiles that TMA writes
+  __syncthreads();
+  gate_up<NT, kStages>(a, maps, p, acc_s, ring, warp, lane);
   barrier_arrive(a, p);
-  down<NT, kStages>(a, p, acc_s, ring, warp, lane);
+  down<NT, kStages>(a, maps, p, acc_s, ring, warp, lane);
 }
 
 template <int NT, int kStages>
-cudaError_t launch(const FewArgs& a, cudaStream_t st) {
+cudaError_t launch(const FewArgs& a, const FewMaps& maps, cudaStream_t st) {
   constexpr int smem = smem_bytes<NT, kStages>();
   cudaError_t e = cudaFuncSetAttribute(few_kernel<NT, kStages>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -909,7 +989,7 @@ cudaError_t launch(const FewArgs& a, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<NT, kStages>, a);
+  return cudaLaunchKernelEx(&cfg, few_kernel<NT, kStages>, a, maps);
 }
 
 }  // namespace
@@ -925,8 +1005,7 @@ FewLayout few_layout(const Shape& s) {
   L.meta = 256;
   L.logits = take(4ull * s.T * s.E);
   L.h = take(4ull * s.T * (s.k + s.S) * s.f);
-  // two pieces of a CTA: of gate and up (64 channels of 16 columns each), or of 512 channels of down
-  L.part_floats = 2 * (2 * MOE_FEW_MAX_TOKENS * 64 > s.T * 512 ? 2 * MOE_FEW_MAX_TOKENS * 64 : s.T * 512);
+  L.part_floats = 2 * 2 * MOE_FEW_MAX_TOKENS * 64;  // two pieces of a CTA, of gate and up: 64 channels, 16 columns
   L.part = take(4ull * kFewMaxCtas * L.part_floats);
   L.wg_t = take(2ull * s.d * s.E);
   L.total = o;
@@ -934,7 +1013,17 @@ FewLayout few_layout(const Shape& s) {
 }
 
 cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
-  return a.T <= 8 ? launch<1, 4>(a, st) : launch<2, 3>(a, st);
+  FewMaps maps = {};
+  const auto map = [&](CUtensorMap& m, const uint16_t* w, int n, int rows, int cols) {
+    return make_tmap_3d(&m, w, n, rows, cols, 64, 16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, false);
+  };
+  bool ok = map(maps.gate, a.gate, a.E, a.d, a.f) && map(maps.up, a.up, a.E, a.d, a.f) &&
+            map(maps.down, a.down, a.E, a.f, a.d);
+  if (a.S > 0)
+    ok = ok && map(maps.sh_gate, a.sh_gate, a.S, a.d, a.f) && map(maps.sh_up, a.sh_up, a.S, a.d, a.f) &&
+         map(maps.sh_down, a.sh_down, a.S, a.f, a.d);
+  if (!ok) return cudaErrorInvalidValue;
+  return a.T <= 8 ? launch<1, 4>(a, maps, st) : launch<2, 3>(a, maps, st);
 }
 
 }  // namespace moe

@@ -36,6 +36,11 @@ struct FewArgs {
   int part_floats;
 };
 
+// Tensor maps of the weights: tiles of 16 rows x 64 columns.
+struct FewMaps {
+  CUtensorMap gate, up, down, sh_gate, sh_up, sh_down;
+};
+
 struct FewLayout {
   size_t meta, logits, h, part, wg_t, total;
   int part_floats;

@@ -796,7 +796,8 @@ bool make_tmap_2d(CUtensorMap* m, const void* ptr, long long rows, long long col
 }
 
 bool make_tmap_3d(CUtensorMap* m, const void* ptr, long long n, long long rows, long long cols,
-                  int box_cols, int box_rows, CUtensorMapDataType dt, int elem_bytes) {
+                  int box_cols, int box_rows, CUtensorMapDataType dt, int elem_bytes,
+                  bool wide_l2) {
   auto fn = encode_fn_impl();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
@@ -806,7 +807,8 @@ bool make_tmap_3d(CUtensorMap* m, const void* ptr, long long n, long long rows, 
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            wide_l2 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_grouped_ffn(const Shape& s, const FfnPtrs& p, cudaStream_t st,

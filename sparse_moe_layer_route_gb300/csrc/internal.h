@@ -246,9 +246,10 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
 bool make_tmap_2d(CUtensorMap* m, const void* ptr, long long rows, long long cols, int box_cols,
                   int box_rows, CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 // 3-D over a row-major [n, rows, cols] tensor (elem_bytes each) with a box of
-// box_cols x box_rows x 1.
+// box_cols x box_rows x 1. wide_l2: a miss brings 256 bytes into L2 (for boxes whose neighbours are wanted too).
 bool make_tmap_3d(CUtensorMap* m, const void* ptr, long long n, long long rows, long long cols,
                   int box_cols, int box_rows,
-                  CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, int elem_bytes = 2);
+                  CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, int elem_bytes = 2,
+                  bool wide_l2 = true);
 
 }  // namespace moe
