@@ -25,6 +25,7 @@
 // H is carried as two bf16 numbers (value and remainder, 2^-17 of it), as the second MMA is free here.
 #include <cuda_bf16.h>
 #include <cuda.h>
+#include <climits>
 #include <cmath>
 
 #include "few.cuh"
@@ -34,7 +35,13 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMostWarps = 16;
+constexpr int kStages = 2;                  // tiles of a warp under way
+// A CTA's warps: W that stream weights (the workers), one that deals units of work out, one that joins them.
+constexpr int workers(int W) { return 32 * W; }
+constexpr int threads(int W) { return 32 * W + 64; }
+constexpr int kQueue = 8;                   // units known ahead
+constexpr int kList = 16;                   // tiles for the workers to join
 constexpr int kSlots = MOE_FEW_MAX_TOKENS * 8;          // T * top_k at most
 constexpr int kSegs = kSlots + 4;                       // hit experts and shared ones
 constexpr int kCols = kSlots + 4 * MOE_FEW_MAX_TOKENS;  // columns of all of them
@@ -44,10 +51,6 @@ constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -64,12 +67,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 lds8(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -97,12 +94,15 @@ struct Plan {
   float gate[kCols];
   int n_seg;
   volatile int fail;  // a wait ran past its limit
-  int last[2];
   unsigned gen;
+  // units of work: numbers of the first `known` (a ring), how many are done and accounted for, and where an
+  // overrun ended the list
+  volatile int unit[kQueue], known, done, joined, limit;
+  int list[kList], n_list;  // tiles whose last unit this CTA brought
 };
 // Scratch of router and choice, in the ring's memory before the ring is used.
 struct Scratch {
-  float2 red[kWarps];
+  float2 red[kMostWarps];
   float score[MOE_FEW_MAX_TOKENS][256];
   unsigned all[256][kSlots / 32];   // slots of an expert
   unsigned keep[256][kSlots / 32];  // those that are a column: kept, the first of their token
@@ -144,42 +144,135 @@ __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
   return p.fail == 0;
 }
 
-// A CTA's run of K steps begins and ends inside tiles, as a rule: at most two of its pieces, the first (0)
-// and the last (1), are parts of a tile whose other parts are other CTAs'. Those leave their sums in the
-// workspace, and only when the run is done does the CTA say so (under load a fence and an atomic take 4 us, in
-// which nothing would be read) and sees which tiles it has to join: those that it was the last to bring a part of.
-struct Cuts {
-  int head = -1, tail = -1;  // their tiles
-};
-__device__ __forceinline__ float* cut_sums(const FewArgs& a, int cta, int which) {
-  return a.part + (size_t)cta * a.part_floats + which * (a.part_floats / 2);
-}
-// Which of its two cut pieces of a tile of K steps is CTA b's, when a run is `per` steps.
-__device__ __forceinline__ int cut_of(int b, int per, int tile, int K) { return b * per <= tile * K ? 1 : 0; }
-
-__device__ __forceinline__ unsigned bring_part(const FewArgs& a, int tile, int K, int per) {
-  if (tile < 0) return 0;
-  const int owner = tile * K / per;
-  return atomicAdd(&a.meta->piece[owner >> 2], 1u << (owner & 3) * 8);
-}
-__device__ __forceinline__ int was_last(const FewArgs& a, unsigned before, int tile, int K, int per) {
-  if (tile < 0) return 0;
-  const int owner = tile * K / per, at = (owner & 3) * 8;
-  const unsigned n = ((tile + 1) * K - 1) / per - owner + 1;
-  if ((before >> at & 255u) != n - 1) return 0;
-  atomicSub(&a.meta->piece[owner >> 2], n << at);  // zero again for the next part and the next call
-  return 1;
-}
-__device__ __forceinline__ void say_cuts(const FewArgs& a, Plan& p, const Cuts& cuts, int K, int per) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    const unsigned head = bring_part(a, cuts.head, K, per), tail = bring_part(a, cuts.tail, K, per);
-    p.last[0] = was_last(a, head, cuts.head, K, per);
-    p.last[1] = was_last(a, tail, cuts.tail, K, per);
-    __threadfence();
+// ------------------------------------------------------------------------------------------- units
+// A part of the kernel (gate/up, down) is `tiles` tiles of 64 channels with K steps each. A tile is cut into
+// `parts` units, so that a CTA has about ten, and the first few units are a CTA's by its number, the rest go to
+// whoever is next: SMs get up to a fifth more or less of the memory's rate than others, which equal shares wait for
+// (one token of the decode shape: CTAs were done with gate/up 35 to 48 us after its start). Which CTA took a
+// unit does not matter to the result: a cut tile's units leave their sums in the workspace, and whoever brings the
+// last one adds them in order.
+//
+// Numbers are fetched, and done units made known, by two warps of their own while the workers stream: fences and
+// atomics take microseconds under load. The tiles that a CTA has to join wait for the end of its units, when all
+// its warps are free for them.
+struct Units {
+  int K, tiles, parts, total, ahead;
+  bool dealt;  // false: every slice of K has too few steps to look ahead by units, a CTA's are by its number
+  __device__ Units(int K_, int tiles_, int slices) : K(K_), tiles(tiles_) {
+    const int want = (kFewUnits * (int)gridDim.x / 8 + tiles - 1) / tiles;
+    parts = max(1, min(want, K / (kFewSteps * slices)));
+    total = tiles * parts;
+    const int steps = K / parts / slices;
+    dealt = steps > 0;
+    ahead = 1 + (dealt ? (kStages + steps - 1) / steps : 0);  // units that a warp's copies may run ahead
   }
-  __syncthreads();
+  __device__ int begin(int q) const { return (int)((long long)q * K / parts); }
+  // The i-th unit of this CTA, one that is known; total or more: there is none.
+  __device__ int number(const Plan& p, int i) const {
+    if (!dealt) return (long long)i * gridDim.x + blockIdx.x < total ? i * (int)gridDim.x + (int)blockIdx.x : total;
+    return i < p.limit ? p.unit[i % kQueue] : total;
+  }
+  // By one thread, before a barrier of the CTA.
+  __device__ void start(Plan& p) const {
+    for (int i = 0; i <= ahead; ++i) p.unit[i] = min(total, i * (int)gridDim.x + (int)blockIdx.x);
+    p.known = ahead + 1;
+    p.done = 0;
+    p.joined = parts > 1 ? 0 : INT_MAX;
+    p.limit = INT_MAX;
+    p.n_list = 0;
+  }
+};
+
+// Until `now()`; past the limit the status word says so.
+template <class F>
+__device__ __forceinline__ bool wait_units(const FewArgs& a, Plan& p, F now) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (unsigned it = 1; !now(); ++it)
+    if ((it & 63u) == 0 && (p.fail || ptx::globaltimer_ns() - t0 > 2 * kWaitLimitNs)) {
+      atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
+      p.fail = 1;
+      return false;
+    }
+  __threadfence_block();
+  return true;
+}
+
+template <int W>
+__device__ __forceinline__ void workers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(workers(W)) : "memory");
+}
+// After a unit's sums are in the workspace or its results stored, and before anything reuses their memory: the
+// next units are known.
+template <int W>
+__device__ __forceinline__ void unit_done(const FewArgs& a, Plan& p, const Units& units, int i) {
+  // the list ends where no more is known, for all workers after the same unit
+  if (threadIdx.x == 0 && units.dealt &&
+      !wait_units(a, p, [&] { return p.known >= i + 2 + units.ahead; }))
+    p.limit = i + 1;
+  workers_sync<W>();
+  if (threadIdx.x == 0) {
+    __threadfence_block();
+    p.done = i + 1;
+  }
+}
+
+// The dealer: while unit i is worked on, the number of the unit after the known ones.
+__device__ void deal_units(const FewArgs& a, Plan& p, const Units& units, int* work, int lane) {
+  if (!units.dealt || lane != 0) return;
+  for (int i = 0; units.number(p, i) < units.total; ++i) {
+    const int next = i + units.ahead + 1;  // in the place of unit i + ahead - 7, that is i - 2 or earlier
+    int v = units.total;
+    if (p.unit[(next - 1) % kQueue] < units.total)
+      v = min(units.total, (units.ahead + 1) * (int)gridDim.x + atomicAdd(work, 1));
+    if (!wait_units(a, p, [&] { return p.joined >= i - 1; })) return;
+    p.unit[next % kQueue] = v;
+    __threadfence_block();
+    p.known = next + 1;
+    if (!wait_units(a, p, [&] { return p.done > i; })) return;
+  }
+}
+
+// The joiner: says that units are done, and lists the tiles that are complete with them. Past the list's end it
+// joins them itself. tile_of(unit): the tile that a unit is of; join(tile, row): adds a row's parts, by a warp.
+template <class Tile, class Rows, class Join>
+__device__ void join_units(const FewArgs& a, Plan& p, const Units& units, int* brought, int lane, Tile tile_of,
+                           Rows rows_of, Join join) {
+  if (!units.dealt || units.parts == 1) return;
+  for (int i = 0;; ++i) {
+    int tile = -1;
+    if (lane == 0) {
+      const int u = units.number(p, i);
+      if (u < units.total && wait_units(a, p, [&] { return p.done > i; })) {
+        tile = tile_of(u);
+        __threadfence();
+        const bool last = atomicAdd(brought + tile, 1) == units.parts - 1;
+        p.joined = i + 1;
+        if (!last)
+          tile = -2;
+        else if (p.n_list < kList) {
+          p.list[p.n_list++] = tile;
+          tile = -2;
+        }
+      }
+    }
+    tile = __shfl_sync(kFull, tile, 0);
+    if (tile == -1) break;
+    if (tile >= 0) {
+      __threadfence();
+      const int2 rows = rows_of(tile);
+      for (int r = rows.x; r < rows.y; ++r) join(tile, r, lane);
+    }
+  }
+}
+// After a barrier behind both: the listed tiles, rows by warps of the whole CTA.
+template <class Rows, class Join>
+__device__ void join_list(const Plan& p, int warp, int lane, Rows rows_of, Join join) {
+  if (p.n_list == 0) return;
+  __threadfence();
+  for (int k = 0; k < p.n_list; ++k) {
+    const int2 rows = rows_of(p.list[k]);
+    for (int r = rows.x + warp; r < rows.y; r += (int)blockDim.x / 32) join(p.list[k], r, lane);
+  }
 }
 
 // ------------------------------------------------------------------------------------------ router
@@ -190,13 +283,13 @@ __device__ __forceinline__ void add_exact(float& hi, float& lo, float s) {
   hi = sum;
 }
 // logits[t, e] of expert e for every token; warps share out tokens, then the pieces of d.
+template <int W>
 __device__ void router(const FewArgs& a, Scratch& sc, int warp, int lane) {
-  int wpt = kWarps;  // warps per token
-  while (wpt * a.T > kWarps) wpt >>= 1;
-  const int t = warp / wpt, part = warp % wpt;
-  const int nv = a.d / 8;
+  int wpt = W;  // warps per token
+  while (wpt > 1 && wpt * a.T > W) wpt >>= 1;
+  const int part = warp % wpt, nv = a.d / 8;
   for (int e = blockIdx.x; e < a.E; e += gridDim.x) {
-    if (t < a.T) {
+    for (int t = warp / wpt; warp < W && t < a.T; t += W / wpt) {
       const uint4* w = reinterpret_cast<const uint4*>(a.W_g_t + (size_t)e * a.d);
       const uint4* x = reinterpret_cast<const uint4*>(a.x + (size_t)t * a.d);
       float hi = 0.f, lo = 0.f;
@@ -218,7 +311,7 @@ __device__ void router(const FewArgs& a, Scratch& sc, int warp, int lane) {
         lo += __shfl_xor_sync(kFull, lo, o);
         add_exact(hi, lo, __shfl_xor_sync(kFull, hi, o));
       }
-      if (lane == 0) sc.red[warp] = make_float2(hi, lo);
+      if (lane == 0) sc.red[t * wpt + part] = make_float2(hi, lo);
     }
     __syncthreads();
     if (threadIdx.x < a.T) {
@@ -332,7 +425,7 @@ __device__ __forceinline__ int rank_of(const unsigned (&m)[kSlots / 32], int s) 
 // the same expert twice has one column with both gates. Of an expert's slots the first C count.
 __device__ void make_plan(const FewArgs& a, Plan& p, Scratch& sc, int warp, int lane) {
   const int n = a.T * a.k, tid = threadIdx.x;
-  for (int i = tid; i < a.E * (kSlots / 32); i += kThreads) {
+  for (int i = tid; i < a.E * (kSlots / 32); i += (int)blockDim.x) {
     (&sc.all[0][0])[i] = 0;
     (&sc.keep[0][0])[i] = 0;
   }
@@ -401,7 +494,7 @@ __device__ void make_plan(const FewArgs& a, Plan& p, Scratch& sc, int warp, int 
     p.tok[c] = (uint8_t)(tid / a.k);
     p.gate[c] = gate;
   }
-  for (int i = tid; i < a.S * a.T; i += kThreads) {
+  for (int i = tid; i < a.S * a.T; i += (int)blockDim.x) {
     p.tok[i] = (uint8_t)(i % a.T);
     p.gate[i] = 1.f;
   }
@@ -434,7 +527,7 @@ __device__ void make_plan(const FewArgs& a, Plan& p, Scratch& sc, int warp, int 
     }
     __syncthreads();
     if (ro.offsets)
-      for (int i = tid; i <= a.E; i += kThreads) ro.offsets[i] = sc.off[i];
+      for (int i = tid; i <= a.E; i += (int)blockDim.x) ro.offsets[i] = sc.off[i];
     if (tid < n) {
       const int pos = sound && rank < a.C ? sc.off[e] + rank : -1;
       if (ro.slot_pos) ro.slot_pos[tid] = pos;
@@ -448,24 +541,17 @@ __device__ void make_plan(const FewArgs& a, Plan& p, Scratch& sc, int warp, int 
 }
 
 // ------------------------------------------------------------------------------------------- tiles
-// How the K steps of `tiles` tiles of K steps each are dealt out: run i is [i * per, (i + 1) * per).
-struct Deal {
-  int K, total, per;
-  __device__ Deal(int K_, int tiles, int least) : K(K_), total(K_ * tiles) {
-    per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, min(K, least));
-  }
-  __device__ int begin() const { return min(total, (int)blockIdx.x * per); }
-  __device__ int end() const { return min(total, ((int)blockIdx.x + 1) * per); }
-};
-
-// A warp's ring: kStages tiles of weights (16 rows of 64 channels, 2 KB) and, for each, its lanes' pieces of the
-// columns' values (16 bytes per lane and 8 columns). Tiles are taken in the order they were asked for.
-template <int NT, int kStages>
+// A warp's ring: kStages tiles of weights (32 rows of 64 channels, 4 KB) and, for each, its lanes' pieces of the
+// columns' values (32 bytes per lane and 8 columns: a value in bf16 or, for down, two). Tiles are taken in the order
+// they were asked for. A tile costs a warp about a microsecond from wait to MMAs, so one of 2 KB would hold an SM
+// to 30 GB/s of the 44 that it has to take.
+template <int NT>
 struct Ring {
-  static constexpr int kTile = 2048, kPiece = 512 * NT;
+  static constexpr int kTile = 4096, kPiece = 1024 * NT;
   uint32_t w, b, bar;  // slot 0: the tile, this lane's piece, the tile's mbarrier
   int slot;            // the next tile to be taken
   uint32_t phase;
+  int out;             // tiles asked for and not taken
 
   __device__ __forceinline__ uint32_t tile(int i) const { return w + i * kTile; }
   __device__ __forceinline__ uint32_t piece(int i) const { return b + i * kPiece; }
@@ -474,6 +560,7 @@ struct Ring {
     return k >= kStages ? k - kStages : k;
   }
   __device__ __forceinline__ void next() {
+    --out;
     if (++slot == kStages) {
       slot = 0;
       phase ^= 1u;
@@ -482,9 +569,30 @@ struct Ring {
   // Until the tile and this lane's piece are there. A wait that runs past its limit lets the kernel go on with
   // what there is (later waits give up at once), and the status word says so.
   __device__ __forceinline__ void wait(const FewArgs& a, Plan& p) const {
-    ptx::mbar_wait_bounded_warp(bar + 8 * slot, phase, &p.fail, a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT,
-                                kWaitLimitNs);
+    const uint32_t m = bar + 8 * slot;
+    if (!ptx::mbar_try_wait(m, phase)) {
+      uint64_t t0 = 0;  // the timer is slow to read: not before a tile is very late
+      for (unsigned it = 1; !ptx::mbar_try_wait(m, phase); ++it)
+        if ((it & 255u) == 0) {
+          const uint64_t now = ptx::globaltimer_ns();
+          if (t0 == 0) t0 = now;
+          if (p.fail || now - t0 > kWaitLimitNs) {
+            atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
+            p.fail = 1;
+            break;
+          }
+        }
+    }
+    __syncwarp();
     cp_wait<kStages - 1>();
+  }
+  // Takes what is still on its way (there is nothing unless a wait ran past its limit).
+  __device__ __forceinline__ void drain(const FewArgs& a, Plan& p) {
+    while (out > 0) {
+      wait(a, p);
+      next();
+    }
+    cp_wait<0>();
   }
   // One lane asks for a tile. What the warp read of the slot before is in registers.
   __device__ __forceinline__ void ask(int i, const CUtensorMap* map, int c, int row, int matrix) const {
@@ -494,8 +602,8 @@ struct Ring {
   }
 };
 
-// Reads a tile into the fragments of four MMAs: rows of fragment j are channels 8 g + 2 j (its rows 0-7) and
-// 8 g + 2 j + 1 (rows 8-15) for lane 4 g + q, whose K rows are 2 q, 2 q + 1, 2 q + 8, 2 q + 9. Swizzled: 16-byte
+// Reads 16 rows of a tile into the fragments of four MMAs: rows of fragment j are channels 8 g + 2 j (its rows 0-7)
+// and 8 g + 2 j + 1 (rows 8-15) for lane 4 g + q, whose K rows are 2 q, 2 q + 1, 2 q + 8, 2 q + 9. Swizzled: 16-byte
 // piece c of row r is at c ^ (r % 8), so the eight lanes of a quarter of a load read eight different ones.
 __device__ __forceinline__ void fragments(uint32_t tile, int lane, uint32_t (&f)[4][4]) {
   const int g = lane >> 2, q = lane & 3;
@@ -512,66 +620,75 @@ __device__ __forceinline__ void fragments(uint32_t tile, int lane, uint32_t (&f)
     f[j][3] = __byte_perm(a2[j], a3[j], 0x7632);
   }
 }
+// The columns' values of 32 K rows lie so that a lane's are 16 bytes: for each q the bf16 values of rows 2 q,
+// 2 q + 1, 2 q + 8, 2 q + 9 and those 16 later. x is put in that order first (its bytes are few), H is stored so.
+__device__ __forceinline__ void order_x(const FewArgs& a) {
+  const int n = a.T * (a.d / 8);  // uint4s
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(a.x) + (i >> 2) * 16 + (i & 3);
+    reinterpret_cast<uint4*>(a.xf)[i] = make_uint4(__ldg(from), __ldg(from + 4), __ldg(from + 8), __ldg(from + 12));
+  }
+}
 
-// Where a warp is in its K steps of gate/up: tile j (expert and 64 channels), step s of it.
-template <int NT, int kStages>
+// Where a warp is in its K steps of gate/up: the CTA's i-th unit (expert, 64 channels, a part of K), step s of it.
+// Of units that lie side by side in memory (channels) the numbers follow one another.
+struct UpUnit {
+  int seg, fb, q;
+  __device__ UpUnit(int u, int nfb, int parts) {
+    const int r = u / nfb;
+    fb = u - r * nfb;
+    seg = r / parts;
+    q = r - seg * parts;
+  }
+};
+template <int NT, int W>
 struct UpFeed {
   const FewArgs& a;
   const FewMaps& maps;
   const Plan& p;
-  const Deal& deal;
-  int slice, lane, mat, j, s, kend, channel, matrix;
+  const Units& units;
+  int slice, lane, mat, i, s, kend, channel, matrix;
   const CUtensorMap* map;
-  const uint16_t* x[NT];
+  const uint4* x[NT];
   uint32_t bytes[NT];
   bool more;
 
-  __device__ UpFeed(const FewArgs& a_, const FewMaps& m_, const Plan& p_, const Deal& d_, int warp, int lane_)
-      : a(a_), maps(m_), p(p_), deal(d_), slice(warp >> 1), lane(lane_), mat(warp & 1) {
-    j = deal.begin() / deal.K;
-    s = deal.begin() - j * deal.K + slice;
-    kend = min(deal.K, deal.end() - j * deal.K);
-    more = deal.begin() < deal.end();
-    if (more) {
-      tile();
-      settle();
-    }
+  __device__ UpFeed(const FewArgs& a_, const FewMaps& m_, const Plan& p_, const Units& u_, int warp, int lane_)
+      : a(a_), maps(m_), p(p_), units(u_), slice(warp >> 1), lane(lane_), mat(warp & 1), i(-1), s(0), kend(0),
+        more(true) {
+    settle();
   }
-  __device__ void tile() {
-    const int nfb = a.f / 64, seg = j / nfb, e = p.seg_e[seg];
-    map = e < a.E ? (mat ? &maps.up : &maps.gate) : (mat ? &maps.sh_up : &maps.sh_gate);
-    matrix = e < a.E ? e : e - a.E;
-    channel = (j - seg * nfb) * 64;
-    const int g = lane >> 2, q = lane & 3, base = p.seg_base[seg], cnt = p.seg_base[seg + 1] - base;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const bool there = g + 8 * n < cnt;
-      bytes[n] = there ? 4 : 0;
-      x[n] = a.x + (size_t)(there ? p.tok[base + g + 8 * n] : 0) * a.d + 2 * q;
-    }
-  }
+  // To the next unit in which this warp has a step.
   __device__ void settle() {
     while (s >= kend) {
-      ++j;
-      if (j * deal.K >= deal.end()) {
+      const int u = units.number(p, ++i);
+      if (u >= units.total) {
         more = false;
         return;
       }
-      s = slice;
-      kend = min(deal.K, deal.end() - j * deal.K);
-      tile();
-    }
-  }
-  __device__ __forceinline__ void issue(const Ring<NT, kStages>& r, int slot) {
-    if (more) {
-      if (lane == 0) r.ask(slot, map, channel, s * 16, matrix);
-      const uint32_t to = r.piece(slot);
+      const UpUnit at(u, a.f / 64, units.parts);
+      s = units.begin(at.q) + slice;
+      kend = units.begin(at.q + 1);
+      const int e = p.seg_e[at.seg];
+      map = e < a.E ? (mat ? &maps.up : &maps.gate) : (mat ? &maps.sh_up : &maps.sh_gate);
+      matrix = e < a.E ? e : e - a.E;
+      channel = at.fb * 64;
+      const int g = lane >> 2, q = lane & 3, base = p.seg_base[at.seg], cnt = p.seg_base[at.seg + 1] - base;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        cp_async4(to + 512 * n, x[n] + s * 16, bytes[n]);
-        cp_async4(to + 512 * n + 4, x[n] + s * 16 + 8, bytes[n]);
+        const bool there = g + 8 * n < cnt;
+        bytes[n] = there ? 16 : 0;
+        x[n] = reinterpret_cast<const uint4*>(a.xf) + (there ? p.tok[base + g + 8 * n] : 0) * (a.d / 8) + q;
       }
-      s += 8;
+    }
+  }
+  __device__ __forceinline__ void issue(Ring<NT>& r, int slot) {
+    if (more) {
+      if (lane == 0) r.ask(slot, map, channel, s * 32, matrix);
+      ++r.out;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) cp_async16(r.piece(slot) + 1024 * n, x[n] + s * 4, bytes[n]);
+      s += W / 2;
       if (s >= kend) settle();
     }
     cp_commit();
@@ -596,17 +713,13 @@ __device__ __forceinline__ void store_sums(float* acc_s, const float (&acc)[NT][
     }
 }
 
-__device__ __forceinline__ float4 add4(float4 a, float4 b) {
-  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-}
-
-// Four channels of H, 4 c4 and on, of a column's row. 16 channels are 64 bytes: for each q the bf16 values of
-// channels 2 q, 2 q + 1, 2 q + 8, 2 q + 9, then the four remainders (a lane's K rows of an MMA).
-__device__ __forceinline__ void store_h(uint32_t* row, int c4, float4 g, float4 u) {
-  const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
-  uint32_t hi[4], lo[4];
+// Channels 2 k and 2 k + 1 of H in a column's row: 32 channels are 128 bytes, the values of the four q as above,
+// then the remainders.
+__device__ __forceinline__ void store_h(uint32_t* row, int k, float g0, float g1, float u0, float u1) {
+  const float gv[2] = {g0, g1}, uv[2] = {u0, u1};
+  uint32_t hi[2], lo[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const float h = gv[i] / (1.f + expf(-gv[i])) * uv[i];
     const __nv_bfloat16 b = __float2bfloat16_rn(h);
     const float back = __bfloat162float(b);
@@ -614,113 +727,112 @@ __device__ __forceinline__ void store_h(uint32_t* row, int c4, float4 g, float4 
     // an infinite or NaN value has no remainder
     lo[i] = isfinite(back) ? __bfloat16_as_ushort(__float2bfloat16_rn(h - back)) : 0;
   }
-  uint32_t* to = row + (c4 >> 2) * 16 + (c4 & 1) * 8 + ((c4 >> 1) & 1);
+  uint32_t* to = row + (k >> 4) * 32 + (k & 3) * 4 + (k >> 2 & 3);
   to[0] = hi[0] | hi[1] << 16;
-  to[2] = lo[0] | lo[1] << 16;
-  to[4] = hi[2] | hi[3] << 16;
-  to[6] = lo[2] | lo[3] << 16;
+  to[16] = lo[0] | lo[1] << 16;
 }
 
-template <int NT, int kStages>
-__device__ void gate_up(const FewArgs& a, const FewMaps& maps, Plan& p, float* acc_s,
-                        Ring<NT, kStages>& ring, int warp, int lane) {
-  const int nfb = a.f / 64;
-  // a tile of up to 32 steps (four of a warp) is not cut: joining the pieces would take longer
-  const Deal deal(a.d / 16, p.n_seg * nfb, 32);
-  UpFeed<NT, kStages> feed(a, maps, p, deal, warp, lane);
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+
+// Sums of a gate/up unit in the workspace: [part][gate, up][column][channel].
+__device__ __forceinline__ float2* up_part(const FewArgs& a, int columns, int part, int mat, int column,
+                                           int channel) {
+  return reinterpret_cast<float2*>(a.part + ((size_t)(part * 2 + mat) * columns + column) * a.f + channel);
+}
+
+template <int NT, int W>
+__device__ void gate_up(const FewArgs& a, const FewMaps& maps, Plan& p, const Units& units, float* acc_s,
+                        Ring<NT>& ring, int warp, int lane) {
+  const int nfb = a.f / 64, columns = p.seg_base[p.n_seg], slice = warp >> 1;
+  UpFeed<NT, W> feed(a, maps, p, units, warp, lane);
 #pragma unroll
   for (int i = 0; i < kStages; ++i) feed.issue(ring, ring.later(i));
-  const int slice = warp >> 1, begin = deal.begin(), end = deal.end();
-  Cuts cuts;
-  for (int at = begin; at < end;) {
-    const int j = at / deal.K, k0 = at - j * deal.K, k1 = min(deal.K, end - j * deal.K);
-    const int seg = j / nfb, fb = j - seg * nfb;
-    const int base = p.seg_base[seg], cnt = p.seg_base[seg + 1] - base;
+  for (int i = 0;; ++i) {
+    const int u = units.number(p, i);
+    if (u >= units.total) break;
+    const UpUnit at(u, nfb, units.parts);
+    const int base = p.seg_base[at.seg], cnt = p.seg_base[at.seg + 1] - base;
+    const int k1 = units.begin(at.q + 1);
     float acc[NT][4][4] = {};
-    for (int s = k0 + slice; s < k1; s += 8) {
+    for (int s = units.begin(at.q) + slice; s < k1; s += W / 2) {
       ring.wait(a, p);
-      uint32_t f[4][4];
-      fragments(ring.tile(ring.slot), lane, f);
-      uint2 b[NT];
+      const uint32_t tile = ring.tile(ring.slot);
+      uint32_t f[2][4][4];
+      fragments(tile, lane, f[0]);
+      fragments(tile + 2048, lane, f[1]);
+      uint4 b[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) b[n] = lds8(ring.piece(ring.slot) + 512 * n);
+      for (int n = 0; n < NT; ++n) b[n] = lds16(ring.piece(ring.slot) + 1024 * n);
       __syncwarp();
-      feed.issue(ring, ring.slot);
+      const int slot = ring.slot;
       ring.next();
+      feed.issue(ring, slot);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (n == 0 || cnt > 8)
+        if (n == 0 || cnt > 8) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) mma(acc[n][m], f[m], b[n].x, b[n].y);
+          for (int m = 0; m < 4; ++m) mma(acc[n][m], f[0][m], b[n].x, b[n].y);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) mma(acc[n][m], f[1][m], b[n].z, b[n].w);
+        }
     }
     store_sums<NT>(acc_s + warp * (8 * NT) * kAccLd, acc, cnt, lane);
-    __syncthreads();
-    const bool whole = k0 == 0 && k1 == deal.K;
-    const int which = k0 == 0 ? 1 : 0;
-    if (!whole) (k0 == 0 ? cuts.tail : cuts.head) = j;
-    float4* part = reinterpret_cast<float4*>(cut_sums(a, blockIdx.x, which));
-    for (int i = threadIdx.x; i < cnt * 16; i += kThreads) {
-      const int c = i >> 4, c4 = i & 15;
-      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+    workers_sync<W>();
+    for (int k = threadIdx.x; k < cnt * 32; k += workers(W)) {
+      const int c = k >> 5, pair = k & 31;
+      float2 g = make_float2(0.f, 0.f), v = g;
 #pragma unroll
-      for (int w = 0; w < kWarps; w += 2) {
-        const float* row = acc_s + (w * (8 * NT) + c) * kAccLd + 4 * c4;
-        g = add4(g, *reinterpret_cast<const float4*>(row));
-        u = add4(u, *reinterpret_cast<const float4*>(row + (8 * NT) * kAccLd));
+      for (int w = 0; w < W; w += 2) {
+        const float* row = acc_s + (w * (8 * NT) + c) * kAccLd + 2 * pair;
+        g = add2(g, *reinterpret_cast<const float2*>(row));
+        v = add2(v, *reinterpret_cast<const float2*>(row + (8 * NT) * kAccLd));
       }
-      if (whole) {
-        store_h(a.h + (size_t)(base + c) * a.f, fb * 16 + c4, g, u);
+      if (units.parts == 1) {
+        store_h(a.h + (size_t)(base + c) * a.f, at.fb * 32 + pair, g.x, g.y, v.x, v.y);
       } else {
-        part[i] = g;
-        part[16 * MOE_FEW_MAX_TOKENS + i] = u;
+        *up_part(a, columns, at.q, 0, base + c, at.fb * 64 + 2 * pair) = g;
+        *up_part(a, columns, at.q, 1, base + c, at.fb * 64 + 2 * pair) = v;
       }
     }
-    at = j * deal.K + k1;
-    __syncthreads();  // the sums' memory is free again
+    unit_done<W>(a, p, units, i);
   }
-  cp_wait<0>();
-  say_cuts(a, p, cuts, deal.K, deal.per);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (!p.last[k]) continue;
-    const int j = k == 0 ? cuts.head : cuts.tail, seg = j / nfb, fb = j - seg * nfb;
-    const int base = p.seg_base[seg], cnt = p.seg_base[seg + 1] - base;
-    const int first = j * deal.K / deal.per, last = ((j + 1) * deal.K - 1) / deal.per;
-    for (int i = threadIdx.x; i < cnt * 16; i += kThreads) {
-      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
-#pragma unroll 4
-      for (int b = first; b <= last; ++b) {
-        const float4* from = reinterpret_cast<const float4*>(cut_sums(a, b, cut_of(b, deal.per, j, deal.K)));
-        g = add4(g, __ldcg(from + i));
-        u = add4(u, __ldcg(from + 16 * MOE_FEW_MAX_TOKENS + i));
-      }
-      store_h(a.h + (size_t)(base + (i >> 4)) * a.f, fb * 16 + (i & 15), g, u);
-    }
-  }
+  ring.drain(a, p);
 }
 
-// Where a warp is in its K steps of down: tile j (64 channels), step s of all experts' channels in a row.
-template <int NT, int kStages>
+// The parts of a column of a tile of gate/up added up, a lane two channels.
+__device__ __forceinline__ void join_up(const FewArgs& a, const Plan& p, const Units& units, int fb, int c,
+                                        int lane) {
+  const int columns = p.seg_base[p.n_seg];
+  float2 g = make_float2(0.f, 0.f), u = g;
+#pragma unroll 8
+  for (int q = 0; q < units.parts; ++q) {
+    g = add2(g, __ldcg(up_part(a, columns, q, 0, c, fb * 64 + 2 * lane)));
+    u = add2(u, __ldcg(up_part(a, columns, q, 1, c, fb * 64 + 2 * lane)));
+  }
+  store_h(a.h + (size_t)c * a.f, fb * 32 + lane, g.x, g.y, u.x, u.y);
+}
+
+// Where a warp is in its K steps of down: the CTA's i-th unit (64 channels, a part of all experts' channels in a
+// row), step s of it.
+template <int NT, int W>
 struct DownFeed {
   const FewArgs& a;
   const FewMaps& maps;
   const Plan& p;
-  const Deal& deal;
-  int slice, lane, fs, j, s, kend, seg, matrix;
+  const Units& units;
+  int slice, lane, fs, i, s, kend, seg, channel, matrix;
   const CUtensorMap* map;
   const uint4* h[NT];
   uint32_t bytes[NT];
   bool more;
 
-  __device__ DownFeed(const FewArgs& a_, const FewMaps& m_, const Plan& p_, const Deal& d_, int warp, int lane_)
-      : a(a_), maps(m_), p(p_), deal(d_), slice(warp), lane(lane_), fs(a_.f / 16) {
-    j = deal.begin() / deal.K;
-    s = deal.begin() - j * deal.K + slice;
-    kend = min(deal.K, deal.end() - j * deal.K);
-    more = deal.begin() < deal.end();
-    if (more) settle();
+  __device__ DownFeed(const FewArgs& a_, const FewMaps& m_, const Plan& p_, const Units& u_, int warp, int lane_)
+      : a(a_), maps(m_), p(p_), units(u_), slice(warp), lane(lane_), fs(a_.f / 32), i(-1), s(0), kend(0),
+        more(true) {
+    settle();
   }
   __device__ void expert() {
+    seg = s / fs;
     const int e = p.seg_e[seg], g = lane >> 2, q = lane & 3;
     map = e < a.E ? &maps.down : &maps.sh_down;
     matrix = e < a.E ? e : e - a.E;
@@ -734,37 +846,39 @@ struct DownFeed {
   }
   __device__ void settle() {
     while (s >= kend) {
-      ++j;
-      if (j * deal.K >= deal.end()) {
+      const int u = units.number(p, ++i);
+      if (u >= units.total) {
         more = false;
         return;
       }
-      s = slice;
-      kend = min(deal.K, deal.end() - j * deal.K);
+      const int q = u / units.tiles;
+      channel = (u - q * units.tiles) * 64;
+      s = units.begin(q) + slice;
+      kend = units.begin(q + 1);
     }
-    seg = s / fs;
     expert();
   }
-  __device__ __forceinline__ void issue_w(const Ring<NT, kStages>& r, int slot) const {
-    if (more && lane == 0) r.ask(slot, map, j * 64, (s - seg * fs) * 16, matrix);
+  __device__ __forceinline__ void issue_w(const Ring<NT>& r, int slot) const {
+    if (more && lane == 0) r.ask(slot, map, channel, (s - seg * fs) * 32, matrix);
   }
-  __device__ __forceinline__ void issue_h(const Ring<NT, kStages>& r, int slot) const {
+  __device__ __forceinline__ void issue_h(Ring<NT>& r, int slot) const {
     if (more) {
+      ++r.out;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        cp_async16(r.piece(slot) + 512 * n, h[n] + (s - seg * fs) * 4, bytes[n]);
+      for (int n = 0; n < NT; ++n) {
+        cp_async16(r.piece(slot) + 1024 * n, h[n] + (s - seg * fs) * 8, bytes[n]);
+        cp_async16(r.piece(slot) + 1024 * n + 512, h[n] + (s - seg * fs) * 8 + 4, bytes[n]);
+      }
     }
     cp_commit();
   }
   __device__ __forceinline__ void next() {
     if (!more) return;
-    s += kWarps;
-    if (s >= kend) {
+    s += W;
+    if (s >= kend)
       settle();
-    } else if (s >= (seg + 1) * fs) {
-      seg = s / fs;
+    else if (s >= (seg + 1) * fs)
       expert();
-    }
   }
 };
 
@@ -799,43 +913,48 @@ __device__ __forceinline__ void add_sums(float* acc_s, float (&acc)[NT][4][4], c
       for (int i = 0; i < 4; ++i) acc[n][m][i] = 0.f;
 }
 
-__device__ __forceinline__ uint2 bf16x4(float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ uint32_t bf16x2(float2 v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void store_out(const FewArgs& a, int t, int channel, float2 v) {
+  *reinterpret_cast<uint32_t*>(a.out + (size_t)t * a.d + channel) = bf16x2(v);
+}
+// Sums of a down unit in the workspace: [part][token][channel].
+__device__ __forceinline__ float2* down_part(const FewArgs& a, int part, int t, int channel) {
+  return reinterpret_cast<float2*>(a.part + ((size_t)part * a.T + t) * a.d + channel);
 }
 
-template <int NT, int kStages>
-__device__ void down(const FewArgs& a, const FewMaps& maps, Plan& p, float* acc_s, Ring<NT, kStages>& ring,
-                     int warp, int lane) {
-  const int fs = a.f / 16;
-  // as in gate/up a tile is not cut below four steps of a warp
-  const Deal deal(p.n_seg * fs, a.d / 64, 4 * kWarps);
-  const int begin = deal.begin(), end = deal.end();
-  Cuts cuts;
-  DownFeed<NT, kStages> feed(a, maps, p, deal, warp, lane);
-  {
-    // the first weights are on their way while the other CTAs finish H
-    DownFeed<NT, kStages> ahead = feed;
+// The first weights, which need nothing of the other CTAs: they are on their way while those finish H.
+template <int NT, int W>
+__device__ void down_ahead(const DownFeed<NT, W>& feed, const Ring<NT>& ring) {
+  DownFeed<NT, W> ahead = feed;
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) {
-      ahead.issue_w(ring, ring.later(i));
-      ahead.next();
-    }
+  for (int i = 0; i < kStages; ++i) {
+    ahead.issue_w(ring, ring.later(i));
+    ahead.next();
   }
+}
+
+template <int NT, int W>
+__device__ void down(const FewArgs& a, Plan& p, const Units& units, DownFeed<NT, W>& feed, float* acc_s,
+                     Ring<NT>& ring, int warp, int lane) {
+  const int fs = a.f / 32;
   float* mine = acc_s + warp * (8 * NT) * kAccLd;
-  for (int i = lane; i < a.T * kAccLd; i += 32) mine[i] = 0.f;
-  __syncwarp();
-  barrier_wait(a, p);  // past its limit the rest runs on what there is, and takes the copies under way
 #pragma unroll
   for (int i = 0; i < kStages; ++i) {
     feed.issue_h(ring, ring.later(i));
     feed.next();
   }
-  for (int at = begin; at < end;) {
-    const int j = at / deal.K, k0 = at - j * deal.K, k1 = min(deal.K, end - j * deal.K);
+  for (int i = 0;; ++i) {
+    const int u = units.number(p, i);
+    if (u >= units.total) break;
+    const int q = u / units.tiles, channel = (u - q * units.tiles) * 64, k1 = units.begin(q + 1);
+    for (int k = lane; k < a.T * kAccLd; k += 32) mine[k] = 0.f;
+    __syncwarp();
     float acc[NT][4][4] = {};
     int seg = 0, cnt = 0, seg_end = 0;
-    for (int s = k0 + warp; s < k1; s += kWarps) {
+    for (int s = units.begin(q) + warp; s < k1; s += W) {
       if (s >= seg_end) {
         if (seg_end > 0) add_sums<NT>(mine, acc, p, seg, lane);
         seg = s / fs;
@@ -843,98 +962,93 @@ __device__ void down(const FewArgs& a, const FewMaps& maps, Plan& p, float* acc_
         cnt = p.seg_base[seg + 1] - p.seg_base[seg];
       }
       ring.wait(a, p);
-      uint32_t f[4][4];
-      fragments(ring.tile(ring.slot), lane, f);
-      uint4 b[NT];
+      const uint32_t tile = ring.tile(ring.slot);
+      uint32_t f[2][4][4];
+      fragments(tile, lane, f[0]);
+      fragments(tile + 2048, lane, f[1]);
+      uint4 b[NT], lo[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) b[n] = lds16(ring.piece(ring.slot) + 512 * n);
+      for (int n = 0; n < NT; ++n) {
+        b[n] = lds16(ring.piece(ring.slot) + 1024 * n);
+        lo[n] = lds16(ring.piece(ring.slot) + 1024 * n + 512);
+      }
       __syncwarp();
-      feed.issue_w(ring, ring.slot);
-      feed.issue_h(ring, ring.slot);
-      feed.next();
+      const int slot = ring.slot;
       ring.next();
+      feed.issue_w(ring, slot);
+      feed.issue_h(ring, slot);
+      feed.next();
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (n == 0 || cnt > 8)
+        if (n == 0 || cnt > 8) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            mma(acc[n][m], f[m], b[n].x, b[n].y);
-            mma(acc[n][m], f[m], b[n].z, b[n].w);
-          }
+          for (int m = 0; m < 4; ++m) mma(acc[n][m], f[0][m], b[n].x, b[n].y);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) mma(acc[n][m], f[1][m], b[n].z, b[n].w);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) mma(acc[n][m], f[0][m], lo[n].x, lo[n].y);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) mma(acc[n][m], f[1][m], lo[n].z, lo[n].w);
+        }
     }
     if (seg_end > 0) add_sums<NT>(mine, acc, p, seg, lane);
-    __syncthreads();
-    const bool whole = k0 == 0 && k1 == deal.K;
-    const int which = k0 == 0 ? 1 : 0;
-    if (!whole) (k0 == 0 ? cuts.tail : cuts.head) = j;
-    float4* part = reinterpret_cast<float4*>(cut_sums(a, blockIdx.x, which));
-    for (int i = threadIdx.x; i < a.T * 16; i += kThreads) {
-      const int t = i >> 4, c4 = i & 15;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    workers_sync<W>();
+    for (int k = threadIdx.x; k < a.T * 32; k += workers(W)) {
+      const int t = k >> 5, pair = k & 31;
+      float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        v = add4(v, *reinterpret_cast<const float4*>(acc_s + (w * (8 * NT) + t) * kAccLd + 4 * c4));
-      if (whole)
-        *reinterpret_cast<uint2*>(a.out + (size_t)t * a.d + j * 64 + 4 * c4) = bf16x4(v);
+      for (int w = 0; w < W; ++w)
+        v = add2(v, *reinterpret_cast<const float2*>(acc_s + (w * (8 * NT) + t) * kAccLd + 2 * pair));
+      if (units.parts == 1)
+        store_out(a, t, channel + 2 * pair, v);
       else
-        part[i] = v;
+        *down_part(a, q, t, channel + 2 * pair) = v;
     }
-    at = j * deal.K + k1;
-    __syncthreads();
-    if (at < end) {
-      for (int i = lane; i < a.T * kAccLd; i += 32) mine[i] = 0.f;
-      __syncwarp();
-    }
+    unit_done<W>(a, p, units, i);
   }
-  cp_wait<0>();
-  say_cuts(a, p, cuts, deal.K, deal.per);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (!p.last[k]) continue;
-    const int j = k == 0 ? cuts.head : cuts.tail, first = j * deal.K / deal.per, last = ((j + 1) * deal.K - 1) / deal.per;
-    for (int i = threadIdx.x; i < a.T * 16; i += kThreads) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int b = first; b <= last; ++b)
-        v = add4(v, __ldcg(reinterpret_cast<const float4*>(
-                               cut_sums(a, b, cut_of(b, deal.per, j, deal.K))) +
-                           i));
-      *reinterpret_cast<uint2*>(a.out + (size_t)(i >> 4) * a.d + j * 64 + 4 * (i & 15)) = bf16x4(v);
-    }
-  }
+  ring.drain(a, p);
 }
 
-template <int NT, int kStages>
+// The parts of a token's channels of a tile of down added up, a lane two.
+__device__ __forceinline__ void join_down(const FewArgs& a, const Units& units, int tile, int t, int lane) {
+  float2 v = make_float2(0.f, 0.f);
+#pragma unroll 8
+  for (int q = 0; q < units.parts; ++q) v = add2(v, __ldcg(down_part(a, q, t, tile * 64 + 2 * lane)));
+  store_out(a, t, tile * 64 + 2 * lane, v);
+}
+
+template <int NT, int W>
 constexpr int ring_bytes() {
-  return kWarps * kStages * (Ring<NT, kStages>::kTile + Ring<NT, kStages>::kPiece);
+  return W * kStages * (Ring<NT>::kTile + Ring<NT>::kPiece);
 }
-template <int NT, int kStages>
+template <int NT, int W>
 constexpr int smem_bytes() {
-  return 1024 + ring_bytes<NT, kStages>() + kWarps * 8 * NT * kAccLd * 4;  // 1024: swizzled tiles' alignment
+  return 1024 + ring_bytes<NT, W>() + W * 8 * NT * kAccLd * 4;  // 1024: swizzled tiles' alignment
 }
 
-template <int NT, int kStages>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int NT, int W>
+__global__ void __launch_bounds__(threads(W), 1)
     few_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ FewMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Plan p;
-  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  __shared__ __align__(8) uint64_t bars[W][kStages];
   uint8_t* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Scratch& sc = *reinterpret_cast<Scratch*>(smem);
-  static_assert(sizeof(Scratch) <= ring_bytes<NT, kStages>(), "it lies in the ring");
-  float* acc_s = reinterpret_cast<float*>(smem + ring_bytes<NT, kStages>());
-  Ring<NT, kStages> ring;
+  static_assert(sizeof(Scratch) <= ring_bytes<NT, W>(), "it lies in the ring");
+  float* acc_s = reinterpret_cast<float*>(smem + ring_bytes<NT, W>());
+  Ring<NT> ring;
   ring.w = ptx::smem_u32(smem) + warp * kStages * ring.kTile;
-  ring.b = ptx::smem_u32(smem) + kWarps * kStages * ring.kTile + warp * kStages * ring.kPiece + lane * 16;
+  ring.b = ptx::smem_u32(smem) + W * kStages * ring.kTile + warp * kStages * ring.kPiece + lane * 16;
   ring.bar = ptx::smem_u32(&bars[warp][0]);
   ring.slot = 0;
   ring.phase = 0;
-  if (lane == 0) {
+  ring.out = 0;
+  if (warp < W && lane == 0) {
     for (int i = 0; i < kStages; ++i) ptx::mbar_init(ring.bar + 8 * i, 1);
     ptx::fence_mbarrier_init();
   }
-  if (threadIdx.x == kThreads - 1) {
+  if (threadIdx.x == threads(W) - 1) {
     ptx::prefetch_tmap(&maps.gate);
     ptx::prefetch_tmap(&maps.up);
     ptx::prefetch_tmap(&maps.down);
@@ -948,40 +1062,89 @@ __global__ void __launch_bounds__(kThreads, 1)
     p.fail = 0;
     p.gen = *reinterpret_cast<volatile unsigned*>(&a.meta->gen);
   }
+  // the units' counters: work and brought of gate/up, then of down
+  constexpr int kMostTiles = kFewUnits * kFewMaxCtas / 8;
+  for (int i = blockIdx.x * threads(W) + threadIdx.x; i < 2 * (1 + kMostTiles); i += gridDim.x * threads(W))
+    a.count[i] = 0;
+  order_x(a);
   if (a.W_g_t != nullptr) {
-    router(a, sc, warp, lane);
+    router<W>(a, sc, warp, lane);
     barrier_arrive(a, p);
     if (!barrier_wait(a, p)) return;
-    for (int t = warp; t < a.T; t += kWarps) choose(a, p, sc.score[t], t, lane);
+    for (int t = warp; t < a.T; t += threads(W) / 32) choose(a, p, sc.score[t], t, lane);
   } else {
-    for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
+    barrier_arrive(a, p);
+    for (int i = threadIdx.x; i < a.T * a.k; i += threads(W)) {
       p.idx[i] = __ldg(a.idx_in + i);
       p.w[i] = a.w_in != nullptr ? __ldg(a.w_in + i) : 1.f;
     }
   }
   __syncthreads();
   make_plan(a, p, sc, warp, lane);
+  if (a.W_g_t == nullptr && !barrier_wait(a, p)) return;
   if (p.n_seg == 0) {  // not one sound index
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.T * a.d / 4; i += gridDim.x * kThreads)
+    for (int i = blockIdx.x * threads(W) + threadIdx.x; i < a.T * a.d / 4; i += gridDim.x * threads(W))
       reinterpret_cast<uint2*>(a.out)[i] = make_uint2(0u, 0u);
     return;
   }
   ptx::fence_proxy_async_smem();  // the scratch gives way to tiles that TMA writes
+  const Units up(a.d / 32, p.n_seg * (a.f / 64), W / 2);
+  if (threadIdx.x == 0) up.start(p);
   __syncthreads();
-  gate_up<NT, kStages>(a, maps, p, acc_s, ring, warp, lane);
+  {
+    const int nfb = a.f / 64;
+    const auto rows = [&](int tile) {
+      const int seg = tile / nfb;
+      return make_int2(p.seg_base[seg], p.seg_base[seg + 1]);
+    };
+    const auto join = [&](int tile, int c, int l) { join_up(a, p, up, tile % nfb, c, l); };
+    if (warp < W)
+      gate_up<NT, W>(a, maps, p, up, acc_s, ring, warp, lane);
+    else if (warp == W)
+      deal_units(a, p, up, a.count, lane);
+    else
+      join_units(a, p, up, a.count + 1, lane,
+                 [&](int u) {
+                   const UpUnit at(u, nfb, up.parts);
+                   return at.seg * nfb + at.fb;
+                 },
+                 rows, join);
+    __syncthreads();
+    join_list(p, warp, lane, rows, join);
+    __syncthreads();
+  }
+  const Units dn(p.n_seg * (a.f / 32), a.d / 64, W);
+  if (threadIdx.x == 0) dn.start(p);
   barrier_arrive(a, p);
-  down<NT, kStages>(a, maps, p, acc_s, ring, warp, lane);
+  int* count = a.count + 1 + kMostTiles;
+  const auto rows = [&](int) { return make_int2(0, a.T); };
+  const auto join = [&](int tile, int t, int l) { join_down(a, dn, tile, t, l); };
+  // past its limit the barrier lets the rest run on what there is, and take the copies under way
+  if (warp < W) {
+    DownFeed<NT, W> feed(a, maps, p, dn, warp, lane);
+    down_ahead(feed, ring);
+    barrier_wait(a, p);
+    down<NT, W>(a, p, dn, feed, acc_s, ring, warp, lane);
+  } else {
+    barrier_wait(a, p);
+    if (warp == W)
+      deal_units(a, p, dn, count, lane);
+    else
+      join_units(a, p, dn, count + 1, lane, [&](int u) { return u % dn.tiles; }, rows, join);
+  }
+  __syncthreads();
+  join_list(p, warp, lane, rows, join);
 }
 
-template <int NT, int kStages>
+template <int NT, int W>
 cudaError_t launch(const FewArgs& a, const FewMaps& maps, cudaStream_t st) {
-  constexpr int smem = smem_bytes<NT, kStages>();
-  cudaError_t e = cudaFuncSetAttribute(few_kernel<NT, kStages>,
+  constexpr int smem = smem_bytes<NT, W>();
+  cudaError_t e = cudaFuncSetAttribute(few_kernel<NT, W>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_sms() < kFewMaxCtas ? num_sms() : kFewMaxCtas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads(W));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -989,7 +1152,7 @@ cudaError_t launch(const FewArgs& a, const FewMaps& maps, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<NT, kStages>, a, maps);
+  return cudaLaunchKernelEx(&cfg, few_kernel<NT, W>, a, maps);
 }
 
 }  // namespace
@@ -1004,9 +1167,15 @@ FewLayout few_layout(const Shape& s) {
   };
   L.meta = 256;
   L.logits = take(4ull * s.T * s.E);
+  L.xf = take(2ull * s.T * s.d);
   L.h = take(4ull * s.T * (s.k + s.S) * s.f);
-  L.part_floats = 2 * 2 * MOE_FEW_MAX_TOKENS * 64;  // two pieces of a CTA, of gate and up: 64 channels, 16 columns
-  L.part = take(4ull * kFewMaxCtas * L.part_floats);
+  // counters of units, and the parts of cut tiles. A tile is cut into at most one part more than the most units
+  // are times the number of tiles: of gate/up one for 64 channels of an expert, of down for 64 of d
+  constexpr size_t units = kFewUnits * kFewMaxCtas / 8;
+  L.count = take(4 * 2 * (1 + units));
+  const size_t up = 2 * (64 * units * s.T + (size_t)s.T * (s.k + s.S) * s.f);
+  const size_t down = s.T * (64 * units + s.d);
+  L.part = take(4 * (up > down ? up : down));
   L.wg_t = take(2ull * s.d * s.E);
   L.total = o;
   return L;
@@ -1015,7 +1184,7 @@ FewLayout few_layout(const Shape& s) {
 cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
   FewMaps maps = {};
   const auto map = [&](CUtensorMap& m, const uint16_t* w, int n, int rows, int cols) {
-    return make_tmap_3d(&m, w, n, rows, cols, 64, 16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, false);
+    return make_tmap_3d(&m, w, n, rows, cols, 64, 32, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, false);
   };
   bool ok = map(maps.gate, a.gate, a.E, a.d, a.f) && map(maps.up, a.up, a.E, a.d, a.f) &&
             map(maps.down, a.down, a.E, a.f, a.d);
@@ -1023,7 +1192,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
     ok = ok && map(maps.sh_gate, a.sh_gate, a.S, a.d, a.f) && map(maps.sh_up, a.sh_up, a.S, a.d, a.f) &&
          map(maps.sh_down, a.sh_down, a.S, a.f, a.d);
   if (!ok) return cudaErrorInvalidValue;
-  return a.T <= 8 ? launch<1, 4>(a, maps, st) : launch<2, 3>(a, maps, st);
+  return a.T <= 8 ? launch<1, 16>(a, maps, st) : launch<2, 12>(a, maps, st);
 }
 
 }  // namespace moe

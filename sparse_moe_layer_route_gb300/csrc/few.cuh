@@ -4,15 +4,16 @@
 
 namespace moe {
 
-constexpr int kFewMaxCtas = 208;    // persistent CTAs, one counter byte each in FewMeta
+constexpr int kFewMaxCtas = 208;    // persistent CTAs at most
+constexpr int kFewUnits = 5;        // units of work for eight CTAs, at least
+constexpr int kFewSteps = 2;        // tiles of a warp in a unit, at least, where tiles are cut
 constexpr int kFewMaxSize = 65536;  // d and d_ff: work is counted in 32 bits
 
-// What the kernel keeps in the counter block that moe_workspace_init clears. Every call that completes
-// leaves arrive and piece zero; gen counts the grid barriers passed.
+// The grid barrier, in the counter block that moe_workspace_init clears. Every call that completes leaves arrive
+// zero; gen counts the barriers passed.
 struct FewMeta {
   unsigned arrive, gen;
-  unsigned piece[kFewMaxCtas / 4];  // pieces finished of the tile that is cut in CTA i's range: byte i
-  unsigned pad[10];
+  unsigned pad[62];
 };
 static_assert(sizeof(FewMeta) == sizeof(Meta), "it takes the counter block's place");
 
@@ -27,13 +28,14 @@ struct FewArgs {
   moe_route_out ro;                                   // optional results
   uint16_t* out;                                      // [T, d]
   float* logits;                                      // [T, E]
+  uint16_t* xf;                                       // x in the order of MMA operands: see few.cu
   uint32_t* h;                                        // activations [columns, f]: see few.cu
-  float* part;                                        // partial sums, part_floats per CTA
+  int* count;                                         // of units: see few.cu
+  float* part;                                        // sums of tiles' parts
   int* status;
   FewMeta* meta;
   int T, d, E, k, f, S, mode, G, Gk, C;
   float tau;
-  int part_floats;
 };
 
 // Tensor maps of the weights: tiles of 16 rows x 64 columns.
@@ -42,8 +44,7 @@ struct FewMaps {
 };
 
 struct FewLayout {
-  size_t meta, logits, h, part, wg_t, total;
-  int part_floats;
+  size_t meta, logits, xf, h, count, part, wg_t, total;
 };
 FewLayout few_layout(const Shape& s);
 cudaError_t launch_few(const FewArgs& a, cudaStream_t st);

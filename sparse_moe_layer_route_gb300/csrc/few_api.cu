@@ -48,7 +48,9 @@ FewArgs common(const Shape& s, const FewLayout& L, const moe_weights* w, const u
   a.sh_down = w->Wsh_down;
   a.out = out;
   a.logits = at<float>(ws, L.logits);
+  a.xf = at<uint16_t>(ws, L.xf);
   a.h = at<uint32_t>(ws, L.h);
+  a.count = at<int>(ws, L.count);
   a.part = at<float>(ws, L.part);
   a.status = at<int>(ws, 0);
   a.meta = at<FewMeta>(ws, L.meta);
@@ -63,7 +65,6 @@ FewArgs common(const Shape& s, const FewLayout& L, const moe_weights* w, const u
   a.Gk = s.Gk;
   a.C = s.C;
   a.tau = s.tau;
-  a.part_floats = L.part_floats;
   return a;
 }
 
