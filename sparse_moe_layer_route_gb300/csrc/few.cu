@@ -36,7 +36,6 @@ namespace moe {
 namespace {
 
 constexpr int kMostWarps = 16;
-constexpr int kStages = 2;                  // tiles of a warp under way
 // A CTA's warps: W that stream weights (the workers), one that deals units of work out, one that joins them.
 constexpr int workers(int W) { return 32 * W; }
 constexpr int threads(int W) { return 32 * W + 64; }
@@ -94,7 +93,7 @@ struct Plan {
   float gate[kCols];
   int n_seg;
   volatile int fail;  // a wait ran past its limit
-  unsigned gen;
+  unsigned long long target;  // of the barrier that this CTA has arrived at
   // units of work: numbers of the first `known` (a ring), how many are done and accounted for, and where an
   // overrun ended the list
   volatile int unit[kQueue], known, done, joined, limit;
@@ -110,35 +109,36 @@ struct Scratch {
 };
 
 // ------------------------------------------------------------------------------------ grid barrier
+// Arrivals are counted through, call after call: the count a barrier waits for is the next multiple of the number
+// of CTAs above what it was before this CTA's own arrival. That is one atomic and one line to watch.
 // Arrival and wait are apart, so that copies that need nothing of the other CTAs can be started
-// between them. The wait is bounded; past it the status word says so and the kernel ends.
+// between them. The wait is bounded; past it the status word says so.
 __device__ __forceinline__ void barrier_arrive(const FewArgs& a, Plan& p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    if (atomicAdd(&a.meta->arrive, 1u) == gridDim.x - 1) {
-      atomicExch(&a.meta->arrive, 0u);
-      __threadfence();
-      atomicExch(&a.meta->gen, p.gen + 1);
-    }
+    const unsigned long long n = gridDim.x, before = atomicAdd(&a.meta->arrived, 1ull);
+    p.target = (before / n + 1) * n;
   }
 }
 __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
   if (threadIdx.x == 0) {
-    const unsigned g = p.gen;
-    const uint64_t t0 = ptx::globaltimer_ns();
+    uint64_t t0 = 0;
     for (unsigned it = 1;; ++it) {
-      unsigned now;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(&a.meta->gen) : "memory");
-      if (now != g) break;
-      if ((it & 63u) == 0 && ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
-        atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
-        p.fail = 1;
-        break;
+      unsigned long long now;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(now) : "l"(&a.meta->arrived) : "memory");
+      if (now >= p.target) break;
+      if ((it & 63u) == 0) {
+        const uint64_t t = ptx::globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
+          atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
+          p.fail = 1;
+          break;
+        }
       }
     }
     __threadfence();
-    p.gen = g + 1;
   }
   __syncthreads();
   return p.fail == 0;
@@ -158,13 +158,13 @@ __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
 struct Units {
   int K, tiles, parts, total, ahead;
   bool dealt;  // false: every slice of K has too few steps to look ahead by units, a CTA's are by its number
-  __device__ Units(int K_, int tiles_, int slices) : K(K_), tiles(tiles_) {
+  __device__ Units(int K_, int tiles_, int slices, int stages) : K(K_), tiles(tiles_) {
     const int want = (kFewUnits * (int)gridDim.x / 8 + tiles - 1) / tiles;
     parts = max(1, min(want, K / (kFewSteps * slices)));
     total = tiles * parts;
     const int steps = K / parts / slices;
     dealt = steps > 0;
-    ahead = 1 + (dealt ? (kStages + steps - 1) / steps : 0);  // units that a warp's copies may run ahead
+    ahead = 1 + (dealt ? (stages + steps - 1) / steps : 0);  // units that a warp's copies may run ahead
   }
   __device__ int begin(int q) const { return (int)((long long)q * K / parts); }
   // The i-th unit of this CTA, one that is known; total or more: there is none.
@@ -421,6 +421,61 @@ __device__ __forceinline__ int rank_of(const unsigned (&m)[kSlots / 32], int s) 
   return n;
 }
 
+// The plan of up to 32 slots, by one warp: lane i has slot i.
+__device__ void plan_warp(const FewArgs& a, Plan& p, int lane) {
+  const int n = a.T * a.k, e = lane < n ? p.idx[lane] : -1;
+  const bool sound = (unsigned)e < (unsigned)a.E;
+  if (lane < n && !sound && blockIdx.x == 0) atomicOr(a.status, MOE_DEVFAULT_BAD_EXPERT_INDEX);
+  const unsigned below = (1u << lane) - 1u, same = __match_any_sync(kFull, sound ? e : -1 - lane);
+  const int t0 = lane / a.k * a.k, rank = __popc(same & below);
+  // the token's own slots of this expert, the earliest of which has the column
+  const unsigned own = same & (a.k == 32 ? kFull : ((1u << a.k) - 1u) << t0);
+  const bool column = sound && rank < a.C && !(own & below);
+  float gate = 0.f;
+  for (int j = 0; j < a.k; ++j) {
+    const int s = t0 + j;
+    const float w = __shfl_sync(kFull, lane < n ? p.w[lane] : 0.f, s & 31);
+    if ((own >> (s & 31) & 1) && __popc(same & ((1u << (s & 31)) - 1u)) < a.C) gate += w;
+  }
+  const unsigned columns = __ballot_sync(kFull, column), mine = same & columns;
+  const bool leader = column && !(mine & below);
+  const unsigned leaders = __ballot_sync(kFull, leader);
+  // in ascending order of experts, as below
+  int place = 0, before = 0, total = 0;
+  for (unsigned rest = leaders; rest; rest &= rest - 1) {
+    const int l = __ffs(rest) - 1, other = __shfl_sync(kFull, e, l);
+    const int cnt = __popc(__shfl_sync(kFull, mine, l));
+    total += cnt;
+    if (other < e) {
+      ++place;
+      before += cnt;
+    }
+  }
+  const int shared = a.S * a.T;
+  const int base = shared + before;
+  if (lane < a.S) {
+    p.seg_e[lane] = a.E + lane;
+    p.seg_base[lane] = lane * a.T;
+  }
+  if (leader) {
+    p.seg_e[a.S + place] = e;
+    p.seg_base[a.S + place] = base;
+  }
+  if (column) {
+    const int c = base + __popc(mine & below);
+    p.tok[c] = (uint8_t)(lane / a.k);
+    p.gate[c] = gate;
+  }
+  for (int i = lane; i < shared; i += 32) {
+    p.tok[i] = (uint8_t)(i % a.T);
+    p.gate[i] = 1.f;
+  }
+  if (lane == 0) {
+    p.n_seg = a.S + __popc(leaders);
+    p.seg_base[p.n_seg] = shared + total;
+  }
+}
+
 // Lists the experts that were hit, shared ones first, with their columns and gates. A token that was given
 // the same expert twice has one column with both gates. Of an expert's slots the first C count.
 __device__ void make_plan(const FewArgs& a, Plan& p, Scratch& sc, int warp, int lane) {
@@ -547,6 +602,7 @@ __device__ void make_plan(const FewArgs& a, Plan& p, Scratch& sc, int warp, int 
 // to 30 GB/s of the 44 that it has to take.
 template <int NT>
 struct Ring {
+  static constexpr int kStages = 2;  // tiles under way
   static constexpr int kTile = 4096, kPiece = 1024 * NT;
   uint32_t w, b, bar;  // slot 0: the tile, this lane's piece, the tile's mbarrier
   int slot;            // the next tile to be taken
@@ -746,7 +802,7 @@ __device__ void gate_up(const FewArgs& a, const FewMaps& maps, Plan& p, const Un
   const int nfb = a.f / 64, columns = p.seg_base[p.n_seg], slice = warp >> 1;
   UpFeed<NT, W> feed(a, maps, p, units, warp, lane);
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) feed.issue(ring, ring.later(i));
+  for (int i = 0; i < Ring<NT>::kStages; ++i) feed.issue(ring, ring.later(i));
   for (int i = 0;; ++i) {
     const int u = units.number(p, i);
     if (u >= units.total) break;
@@ -930,7 +986,7 @@ template <int NT, int W>
 __device__ void down_ahead(const DownFeed<NT, W>& feed, const Ring<NT>& ring) {
   DownFeed<NT, W> ahead = feed;
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) {
+  for (int i = 0; i < Ring<NT>::kStages; ++i) {
     ahead.issue_w(ring, ring.later(i));
     ahead.next();
   }
@@ -942,7 +998,7 @@ __device__ void down(const FewArgs& a, Plan& p, const Units& units, DownFeed<NT,
   const int fs = a.f / 32;
   float* mine = acc_s + warp * (8 * NT) * kAccLd;
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) {
+  for (int i = 0; i < Ring<NT>::kStages; ++i) {
     feed.issue_h(ring, ring.later(i));
     feed.next();
   }
@@ -1019,7 +1075,7 @@ __device__ __forceinline__ void join_down(const FewArgs& a, const Units& units, 
 
 template <int NT, int W>
 constexpr int ring_bytes() {
-  return W * kStages * (Ring<NT>::kTile + Ring<NT>::kPiece);
+  return W * Ring<NT>::kStages * (Ring<NT>::kTile + Ring<NT>::kPiece);
 }
 template <int NT, int W>
 constexpr int smem_bytes() {
@@ -1031,21 +1087,21 @@ __global__ void __launch_bounds__(threads(W), 1)
     few_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ FewMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Plan p;
-  __shared__ __align__(8) uint64_t bars[W][kStages];
+  __shared__ __align__(8) uint64_t bars[W][Ring<NT>::kStages];
   uint8_t* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Scratch& sc = *reinterpret_cast<Scratch*>(smem);
   static_assert(sizeof(Scratch) <= ring_bytes<NT, W>(), "it lies in the ring");
   float* acc_s = reinterpret_cast<float*>(smem + ring_bytes<NT, W>());
   Ring<NT> ring;
-  ring.w = ptx::smem_u32(smem) + warp * kStages * ring.kTile;
-  ring.b = ptx::smem_u32(smem) + W * kStages * ring.kTile + warp * kStages * ring.kPiece + lane * 16;
+  ring.w = ptx::smem_u32(smem) + warp * Ring<NT>::kStages * ring.kTile;
+  ring.b = ptx::smem_u32(smem) + W * Ring<NT>::kStages * ring.kTile + warp * Ring<NT>::kStages * ring.kPiece + lane * 16;
   ring.bar = ptx::smem_u32(&bars[warp][0]);
   ring.slot = 0;
   ring.phase = 0;
   ring.out = 0;
   if (warp < W && lane == 0) {
-    for (int i = 0; i < kStages; ++i) ptx::mbar_init(ring.bar + 8 * i, 1);
+    for (int i = 0; i < Ring<NT>::kStages; ++i) ptx::mbar_init(ring.bar + 8 * i, 1);
     ptx::fence_mbarrier_init();
   }
   if (threadIdx.x == threads(W) - 1) {
@@ -1058,10 +1114,7 @@ __global__ void __launch_bounds__(threads(W), 1)
       ptx::prefetch_tmap(&maps.sh_down);
     }
   }
-  if (threadIdx.x == 0) {
-    p.fail = 0;
-    p.gen = *reinterpret_cast<volatile unsigned*>(&a.meta->gen);
-  }
+  if (threadIdx.x == 0) p.fail = 0;
   // the units' counters: work and brought of gate/up, then of down
   constexpr int kMostTiles = kFewUnits * kFewMaxCtas / 8;
   for (int i = blockIdx.x * threads(W) + threadIdx.x; i < 2 * (1 + kMostTiles); i += gridDim.x * threads(W))
@@ -1080,7 +1133,18 @@ __global__ void __launch_bounds__(threads(W), 1)
     }
   }
   __syncthreads();
-  make_plan(a, p, sc, warp, lane);
+  const moe_route_out& ro = a.ro;
+  if (a.T * a.k <= 32 && !(ro.counts || ro.offsets || ro.perm_slot || ro.slot_pos)) {
+    if (warp == 0) {
+      plan_warp(a, p, lane);
+    } else if (warp == 1 && blockIdx.x == 0 && lane < a.T * a.k) {
+      if (ro.topk_idx) ro.topk_idx[lane] = p.idx[lane];
+      if (ro.topk_w) ro.topk_w[lane] = p.w[lane];
+    }
+    __syncthreads();
+  } else {
+    make_plan(a, p, sc, warp, lane);
+  }
   if (a.W_g_t == nullptr && !barrier_wait(a, p)) return;
   if (p.n_seg == 0) {  // not one sound index
     for (int i = blockIdx.x * threads(W) + threadIdx.x; i < a.T * a.d / 4; i += gridDim.x * threads(W))
@@ -1088,7 +1152,7 @@ __global__ void __launch_bounds__(threads(W), 1)
     return;
   }
   ptx::fence_proxy_async_smem();  // the scratch gives way to tiles that TMA writes
-  const Units up(a.d / 32, p.n_seg * (a.f / 64), W / 2);
+  const Units up(a.d / 32, p.n_seg * (a.f / 64), W / 2, Ring<NT>::kStages);
   if (threadIdx.x == 0) up.start(p);
   __syncthreads();
   {
@@ -1113,7 +1177,7 @@ __global__ void __launch_bounds__(threads(W), 1)
     join_list(p, warp, lane, rows, join);
     __syncthreads();
   }
-  const Units dn(p.n_seg * (a.f / 32), a.d / 64, W);
+  const Units dn(p.n_seg * (a.f / 32), a.d / 64, W, Ring<NT>::kStages);
   if (threadIdx.x == 0) dn.start(p);
   barrier_arrive(a, p);
   int* count = a.count + 1 + kMostTiles;
@@ -1192,7 +1256,7 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
     ok = ok && map(maps.sh_gate, a.sh_gate, a.S, a.d, a.f) && map(maps.sh_up, a.sh_up, a.S, a.d, a.f) &&
          map(maps.sh_down, a.sh_down, a.S, a.f, a.d);
   if (!ok) return cudaErrorInvalidValue;
-  return a.T <= 8 ? launch<1, 16>(a, maps, st) : launch<2, 12>(a, maps, st);
+  return a.T <= 8 ? launch<1, 14>(a, maps, st) : launch<2, 12>(a, maps, st);
 }
 
 }  // namespace moe

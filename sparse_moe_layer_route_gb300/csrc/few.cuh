@@ -9,10 +9,10 @@ constexpr int kFewUnits = 5;        // units of work for eight CTAs, at least
 constexpr int kFewSteps = 2;        // tiles of a warp in a unit, at least, where tiles are cut
 constexpr int kFewMaxSize = 65536;  // d and d_ff: work is counted in 32 bits
 
-// The grid barrier, in the counter block that moe_workspace_init clears. Every call that completes leaves arrive
-// zero; gen counts the barriers passed.
+// The grid barriers' count of arrivals, in the counter block that moe_workspace_init clears: a multiple of the
+// number of CTAs after every call that completes.
 struct FewMeta {
-  unsigned arrive, gen;
+  unsigned long long arrived;
   unsigned pad[62];
 };
 static_assert(sizeof(FewMeta) == sizeof(Meta), "it takes the counter block's place");
