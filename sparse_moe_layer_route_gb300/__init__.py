@@ -726,24 +726,21 @@ def experts_few(cfg, weights: MoeWeights, x, topk_idx, topk_w, out, ws, stream=N
 def _expect_rows(where, name, t, T, d, ld, dtype, gpu):
     """t [T, d] on GPU `gpu` with unit stride inside a row and rows ld elements apart. Its address."""
     if t.shape != (T, d) or t.dtype is not dtype or t.get_device() != gpu or \
-            (d > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) != ld):
+            t.stride() != (ld, 1) and ((d > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) != ld)):
         raise ValueError(f"{where}: {name} must be a tensor {dtype} {(T, d)} on cuda:{gpu} with strides "
                          f"{(ld, 1)}, not {t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
     return t.data_ptr()
 
 
-def _norm_params(where, cfg, names, gpu, w_after, b_after, gate, w_before, b_before, rng):
-    d, dtype = cfg.d, names.dtype.get(cfg.w_dtype)
-    p = _NormParams()
-    for name, t in (("w_after", w_after), ("b_after", b_after), ("w_before", w_before),
-                    ("b_before", b_before)):
-        if t is not None:
-            setattr(p, name, _expect(where, name, t, (d,), dtype, gpu))
-    if gate is not None:
-        p.gate = _expect(where, "gate", gate, (_gate_count(cfg), d), dtype, gpu)
-    if rng is not None:
-        p.rng = _expect(where, "rng", rng, (2,), names.i64, gpu)
-    return p
+def _norm_params(where, cfg, d, names, gpu, w_after, b_after, gate, w_before, b_before, rng):
+    dtype, vector = names.dtype.get(cfg.w_dtype), (d,)
+    return _NormParams(
+        None if w_after is None else _expect(where, "w_after", w_after, vector, dtype, gpu),
+        None if b_after is None else _expect(where, "b_after", b_after, vector, dtype, gpu),
+        None if gate is None else _expect(where, "gate", gate, (_gate_count(cfg), d), dtype, gpu),
+        None if w_before is None else _expect(where, "w_before", w_before, vector, dtype, gpu),
+        None if b_before is None else _expect(where, "b_before", b_before, vector, dtype, gpu),
+        None if rng is None else _expect(where, "rng", rng, (2,), names.i64, gpu))
 
 
 def _gate_count(cfg):
@@ -758,7 +755,7 @@ def residual_norm(cfg: ResidualNormConfig, h, y, h_out, n, w_after=None, b_after
     T, d = cfg.T, cfg.d
     gpu = _current_gpu(w, "h", h, t)
     h_type, y_type = t.dtype.get(cfg.h_dtype), t.dtype.get(cfg.y_dtype)
-    p = _norm_params(w, cfg, t, gpu, w_after, b_after, gate, w_before, b_before, rng)
+    p = _norm_params(w, cfg, d, t, gpu, w_after, b_after, gate, w_before, b_before, rng)
     _check(lib().moe_residual_norm(
         ctypes.byref(cfg), _expect_rows(w, "h", h, T, d, cfg.ld_h or d, h_type, gpu),
         None if y is None else _expect_rows(w, "y", y, T, d, cfg.ld_y or d, y_type, gpu),
@@ -784,13 +781,14 @@ def residual_norm_backward(cfg: ResidualNormConfig, h_out, y, d_h_out, d_n, d_h,
     T, d = cfg.T, cfg.d
     gpu = _current_gpu(w, "d_h", d_h, t)
     h_type, y_type = t.dtype.get(cfg.h_dtype), t.dtype.get(cfg.y_dtype)
-    p = _norm_params(w, cfg, t, gpu, w_after, b_after, gate, w_before, None, rng)
-    g = _NormGrads()
-    for name, grad, shape in (("w_after", d_w_after, (d,)), ("b_after", d_b_after, (d,)),
-                              ("gate", d_gate, (_gate_count(cfg), d)), ("w_before", d_w_before, (d,)),
-                              ("b_before", d_b_before, (d,))):
-        if grad is not None:
-            setattr(g, name, _expect(w, "d_" + name, grad, shape, t.f32, gpu))
+    p = _norm_params(w, cfg, d, t, gpu, w_after, b_after, gate, w_before, None, rng)
+    vector = (d,)
+    g = _NormGrads(
+        None if d_w_after is None else _expect(w, "d_w_after", d_w_after, vector, t.f32, gpu),
+        None if d_b_after is None else _expect(w, "d_b_after", d_b_after, vector, t.f32, gpu),
+        None if d_gate is None else _expect(w, "d_gate", d_gate, (_gate_count(cfg), d), t.f32, gpu),
+        None if d_w_before is None else _expect(w, "d_w_before", d_w_before, vector, t.f32, gpu),
+        None if d_b_before is None else _expect(w, "d_b_before", d_b_before, vector, t.f32, gpu))
     _check(lib().moe_residual_norm_backward(
         ctypes.byref(cfg),
         None if h_out is None else _expect_rows(w, "h_out", h_out, T, d, cfg.ld_h or d, h_type, gpu),

@@ -144,11 +144,12 @@ cudaError_t launch_form(const NormArgs& a, int cl, cudaStream_t st) {
   const int pitch = Input<H, R, NC>::bytes(a.h.dtype) +
                     (a.y.p != nullptr ? Input<Y, R, NC>::bytes(a.y.dtype) : 0);
   const int turn = std::is_same_v<H, Any> ? kWarpCols * 4 : 0;
-  // rows under way: as many as a CTA's share of shared memory holds, four at most
-  int stages = 4;
+  const long long need = ((long long)a.T + groups - 1) / groups, most = (long long)per_sm * num_sms() / cl;
+  // rows under way: as many as a CTA has and its share of shared memory holds, four at most
+  const long long rows = (need + most - 1) / most;
+  int stages = rows < 4 ? (int)rows : 4;
   auto smem = [&] { return threads / 32 * (stages * pitch + turn); };
   while (stages > 1 && smem() > kNormSmem / per_sm - 2048) --stages;
-  const long long need = ((long long)a.T + groups - 1) / groups, most = (long long)per_sm * num_sms() / cl;
   return launch_rows<CLUSTER>(norm_kernel<R, NC, CLUSTER, H, Y>, (int)(need < most ? need : most) * cl,
                               threads, smem(), cl, st, a, cl, stages);
 }
