@@ -10,19 +10,24 @@
 //            their tokens ("columns") and gates;
 //   gate/up  H = silu(x W_gate) * (x W_up) of the listed experts' columns;
 //   down     out = sum over experts of gate * (H W_down), summed over all of them at once.
-// Gate/up and down are cut into tiles of 64 weight channels; the tiles' K steps, one after the other,
-// are dealt out to the CTAs in equal runs, so every SM streams the same number of bytes whatever the
-// number of experts. A tile that is cut between CTAs leaves partial sums in the workspace; the CTA that
-// finishes last adds them in order of their pieces (the result does not depend on who that is).
+// Gate/up and down are cut into tiles of 64 weight channels, and where those are few, along K as well, into units
+// of work. CTAs take units as they get free. Of a tile that is cut the units leave partial sums in the
+// workspace, and the CTA that finishes last adds them in order (the result does not depend on who that is).
 //
 // Weights go through mma.sync m16n8k16 as the M operand, eight columns as N. Every warp has a ring of tiles of
-// 16 K rows x 64 channels that TMA brings (128-byte swizzle) and that no other warp reads. They lie with the
+// 32 K rows x 64 channels that TMA brings (128-byte swizzle) and that no other warp reads. They lie with the
 // output channel contiguous, so a lane reads four rows of 8 channels, 16 bytes each, and pairs rows by byte
 // permutes into the fragments of four MMAs; which channel is which fragment row is settled when results are
 // stored. (The same pieces by cp.async or plain loads, 16 bytes a lane, come at 3.8 to 4.1 TB/s however many are
 // under way, by TMA at 5.4.) The columns' values come by cp.async into slots that only their lane reads.
 // tcgen05 would want 128 rows of a token operand that has one.
 // H is carried as two bf16 numbers (value and remainder, 2^-17 of it), as the second MMA is free here.
+//
+// Measured with 128 + 1 experts, d 7168, d_ff 2048, top-2 (decode): one token 60 us (266 MB, 4.4 TB/s), of which 9
+// pass before the first weight is asked for, 29 in gate/up (6.1 TB/s), 3 at the barrier, 14 in down; 16 tokens 370
+// to 395 us (2.4 to 2.6 GB by how many experts are hit: 6.6 TB/s). With 64 + 2 experts, d 2048, d_ff 1408, top-6, five
+// tokens: 79 to 88 us (465 MB). A layer of d 256, d_ff 512: 21 us, the launch's and the barriers'. Bringing the shared
+// experts' weights to L2 before the choice is known slows the router by what it gains (60 us with 16 MB, 62 with 64).
 #include <cuda_bf16.h>
 #include <cuda.h>
 #include <climits>
@@ -146,11 +151,13 @@ __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
 
 // ------------------------------------------------------------------------------------------- units
 // A part of the kernel (gate/up, down) is `tiles` tiles of 64 channels with K steps each. A tile is cut into
-// `parts` units, so that a CTA has about ten, and the first few units are a CTA's by its number, the rest go to
-// whoever is next: SMs get up to a fifth more or less of the memory's rate than others, which equal shares wait for
-// (one token of the decode shape: CTAs were done with gate/up 35 to 48 us after its start). Which CTA took a
-// unit does not matter to the result: a cut tile's units leave their sums in the workspace, and whoever brings the
-// last one adds them in order.
+// `parts` units where there would be fewer than five for eight CTAs, and the first few units are a CTA's by its
+// number, the rest go to whoever is next: SMs get up to a fifth more or less of the memory's rate than others, which
+// equal shares wait for (of one token of the decode shape CTAs with equal shares were done with gate/up 35 to 48 us
+// after its start). Smaller units cost more than they even
+// out: with 5, 8, 12, 16 and 32 for eight CTAs one token of the decode shape took 66, 81, 79, 84 and 90 us, 16 tokens
+// 419, 443, 458, 458 and 450, as every cut tile's sums go through the workspace. Which CTA took a unit does not
+// matter to the result: a cut tile's units leave their sums there, and whoever brings the last one adds them in order.
 //
 // Numbers are fetched, and done units made known, by two warps of their own while the workers stream: fences and
 // atomics take microseconds under load. The tiles that a CTA has to join wait for the end of its units, when all
@@ -602,7 +609,8 @@ __device__ void make_plan(const FewArgs& a, Plan& p, Scratch& sc, int warp, int 
 // to 30 GB/s of the 44 that it has to take.
 template <int NT>
 struct Ring {
-  static constexpr int kStages = 2;  // tiles under way
+  // tiles under way: with 3 and 12 workers, 4 and 10, one token of the decode shape took 70 us, with 2 and 14 66
+  static constexpr int kStages = 2;
   static constexpr int kTile = 4096, kPiece = 1024 * NT;
   uint32_t w, b, bar;  // slot 0: the tile, this lane's piece, the tile's mbarrier
   int slot;            // the next tile to be taken
@@ -1256,6 +1264,9 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
     ok = ok && map(maps.sh_gate, a.sh_gate, a.S, a.d, a.f) && map(maps.sh_up, a.sh_up, a.S, a.d, a.f) &&
          map(maps.sh_down, a.sh_down, a.S, a.f, a.d);
   if (!ok) return cudaErrorInvalidValue;
+  // Up to eight tokens an expert has one group of eight columns at most; a second one's slots of the ring leave room
+  // for 12 workers. 16 workers and the two others would leave a thread 96 registers: it spilled, and one token of the
+  // decode shape took 80 us instead of 66 with 14 or 12.
   return a.T <= 8 ? launch<1, 14>(a, maps, st) : launch<2, 12>(a, maps, st);
 }
 

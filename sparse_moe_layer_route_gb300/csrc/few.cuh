@@ -5,7 +5,7 @@
 namespace moe {
 
 constexpr int kFewMaxCtas = 208;    // persistent CTAs at most
-constexpr int kFewUnits = 5;        // units of work for eight CTAs, at least
+constexpr int kFewUnits = 5;        // units of work for eight CTAs, at least (see few.cu)
 constexpr int kFewSteps = 2;        // tiles of a warp in a unit, at least, where tiles are cut
 constexpr int kFewMaxSize = 65536;  // d and d_ff: work is counted in 32 bits
 
@@ -38,7 +38,7 @@ struct FewArgs {
   float tau;
 };
 
-// Tensor maps of the weights: tiles of 16 rows x 64 columns.
+// Tensor maps of the weights: tiles of 32 rows x 64 columns.
 struct FewMaps {
   CUtensorMap gate, up, down, sh_gate, sh_up, sh_down;
 };
