@@ -1,5 +1,6 @@
 // Dropout by itself: y = residual + drop(x). Bound by its bytes; the generator's 40 multiplications for eight
-// elements are about as much work (norm_rows.cuh).
+// elements are about as much work (norm_rows.cuh). Measured: 16384 x 7168 onto a residual, bf16: 119 us (705 MB,
+// 5.9 TB/s); 1000 x 1027 in fp32, rows 1032 apart: 6 us, the call's.
 #include "norm_rows.cuh"
 
 namespace moe {

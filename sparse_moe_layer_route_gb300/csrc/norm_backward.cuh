@@ -12,6 +12,11 @@
 // which few have, in shared memory); the CTAs' sums go to the workspace and are added there in order by a
 // second, small kernel. A row of gates whose tokens are all in one CTA's run is complete there; one that
 // is shared leaves a partial sum in each.
+//
+// Measured: 8192 x 4096, rms norms, a 32-bit stream, gates per channel, dropout: 171 us (604 MB, 3.5 TB/s). A thread
+// holds a row's values and the sums of its channels, 128 registers, so 16 warps an SM have to cover two sums over the
+// row in a chain of 74 instructions an element (issue 45 % of peak); the joining kernel is 8 us of it. 2051 x 2048,
+// a layer norm before the next block only, gates per sequence: 29 us.
 #pragma once
 #include "norm_rows.cuh"
 
@@ -433,10 +438,14 @@ cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStrea
   return cudaErrorInvalidValue;
 }
 
+// As in the forward direction (3001 x 1024 with every gradient: 31 us with one chunk, 52 with two). A third one's sums
+// and values are more than a thread's registers; forms whose number of warps follows the row's width at run time
+// cost 8192 x 4096 250 us instead of 171.
 template <class H, class Y>
 cudaError_t launch_backward(const NormGradArgs& a, int* ctas, cudaStream_t st) {
   const int d = a.d;
   if (d <= 512) return launch_grad_form<32, 2, false, H, Y>(a, 1, ctas, st);
+  if (d <= 1024) return launch_grad_form<128, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 2048) return launch_grad_form<128, 2, false, H, Y>(a, 1, ctas, st);
   if (d <= 4096) return launch_grad_form<256, 2, false, H, Y>(a, 1, ctas, st);
   if (d <= 8192) return launch_grad_form<512, 2, false, H, Y>(a, 1, ctas, st);

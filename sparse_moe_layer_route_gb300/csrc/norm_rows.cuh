@@ -567,7 +567,7 @@ __host__ __device__ __forceinline__ int norm_width(int d, int cl) { return ((d +
 template <bool CLUSTER, typename... K, typename... A>
 cudaError_t launch_rows(void (*kernel)(K...), int grid, int threads, int smem, int cl, cudaStream_t st,
                         A&&... args) {
-  if (smem > 47 * 1024) {  // a kernel has up to 1 KB of its own besides
+  if (smem > 46 * 1024) {  // a kernel has up to 2 KB of its own besides
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem - 1024);
     if (e != cudaSuccess) return e;
