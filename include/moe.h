@@ -514,7 +514,8 @@ moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const 
  *   expert_bias and gumbel_u as moe_layer_forward needs them; W_g_t as there. x, out [T, d] bf16, 16-byte
  *   aligned; out may be x. route_out as in moe_layer_forward.
  *   ws: moe_few_workspace_size bytes that moe_workspace_init has cleared once (its first 512); calls that
- *   share it must follow one another. The kernel takes the whole GPU (one CTA per SM, cooperative launch) and
+ *   share it must follow one another. It may also be moe_layer_forward's (bf16 experts, no re-route) where it is
+ *   as large as both need; other entry points have one of their own. The kernel takes the whole GPU (one CTA per SM, cooperative launch) and
  *   has two grid barriers, each of which waits at most 2 s: past that MOE_DEVFAULT_PIPELINE_TIMEOUT is
  *   set, out is not complete, and ws has to be cleared again before its next use. */
 #define MOE_FEW_MAX_TOKENS 16

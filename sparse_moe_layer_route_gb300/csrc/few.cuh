@@ -10,12 +10,14 @@ constexpr int kFewSteps = 2;        // tiles of a warp in a unit, at least, wher
 constexpr int kFewMaxSize = 65536;  // d and d_ff: work is counted in 32 bits
 
 // The grid barriers' count of arrivals, in the counter block that moe_workspace_init clears: a multiple of the
-// number of CTAs after every call that completes.
+// number of CTAs after every call that completes. It lies behind what the layer of many tokens counts there.
 struct FewMeta {
+  unsigned others[16];
   unsigned long long arrived;
-  unsigned pad[62];
+  unsigned pad[46];
 };
 static_assert(sizeof(FewMeta) == sizeof(Meta), "it takes the counter block's place");
+static_assert(offsetof(FewMeta, arrived) >= offsetof(Meta, pad), "nothing else writes there");
 
 struct FewArgs {
   const uint16_t* x;                                  // [T, d]

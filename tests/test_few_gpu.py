@@ -232,6 +232,27 @@ def test_configurations_share_a_workspace():
     assert M.device_status(ws) == 0
 
 
+def test_a_workspace_of_both_layers():
+    """The layer of many tokens and of few, in turn on one workspace, as prefill and decoding use it."""
+    d, E, k, f, S = 512, 16, 3, 384, 1
+    p = R.make(16, d, E, k, f, S, seed=23)
+    w = weights_of(p)
+    few, many = (M.MoeConfig.make(T, d, E, k, f, n_shared=S) for T in (16, 300))
+    ws = M.alloc_workspace(many)
+    if ws.numel() < M.few_workspace_size(few):
+        ws = M.alloc_int8_workspace(M.few_workspace_size(few))
+    x = torch.randn(300, d, generator=torch.Generator().manual_seed(24)).bfloat16().cuda()
+    alone, want = torch.empty_like(x), torch.empty_like(p["x"])
+    M.layer_forward(many, w, x, None, alone, None, M.alloc_workspace(many))
+    M.layer_forward_few(few, w, p["x"], None, want, None, M.alloc_few_workspace(few))
+    for _ in range(3):
+        for cfg, layer, inp, expected in ((many, M.layer_forward, x, alone),
+                                          (few, M.layer_forward_few, p["x"], want)):
+            out = torch.full_like(expected, float("nan"))
+            layer(cfg, w, inp, None, out, None, ws)
+            assert torch.equal(out, expected) and M.device_status(ws) == 0
+
+
 def test_graphs_and_streams():
     """Two captured graphs share a workspace, replayed in turn; calls on two streams with workspaces of
     their own run side by side."""
