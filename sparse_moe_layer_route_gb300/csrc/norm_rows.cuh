@@ -327,20 +327,26 @@ __device__ __forceinline__ void scale_rows(F2 (&x)[NC][4], bool centred, float m
 }
 
 // ------------------------------------------------------------------------------------------ stores
-// Past L1, where the parameters stay (16384 x 7168 forward: 172 -> 154 us). Not for 32-bit elements, whose two
-// stores share sectors (8192 x 4096 backward would take 175 us instead of 171).
+// Past L1, where the parameters stay (16384 x 7168 forward: 172 -> 150 us).
 __device__ __forceinline__ void store16(void* to, uint4 v) {
   asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(to), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
                : "memory");
 }
-// Eight elements that start on 16 bytes.
+// Eight elements that start on 16 bytes. Of 32-bit ones two 16-byte stores past L1 would each write half sectors (8192
+// x 4096 backward: 175 us instead of 171), so only one of 32 bytes goes there.
 template <class E>
 __device__ __forceinline__ void store_chunk(void* to, const F2 (&v)[4]) {
   if constexpr (std::is_same_v<E, F32>) {
     const float2 a = both(v[0]), b = both(v[1]), c = both(v[2]), d = both(v[3]);
-    static_cast<float4*>(to)[0] = make_float4(a.x, a.y, b.x, b.y);
-    static_cast<float4*>(to)[1] = make_float4(c.x, c.y, d.x, d.y);
+    if (reinterpret_cast<uintptr_t>(to) % 32 == 0) {
+      asm volatile("st.global.L1::no_allocate.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(a.x),
+                   "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y)
+                   : "memory");
+    } else {
+      static_cast<float4*>(to)[0] = make_float4(a.x, a.y, b.x, b.y);
+      static_cast<float4*>(to)[1] = make_float4(c.x, c.y, d.x, d.y);
+    }
   } else if constexpr (std::is_same_v<E, BF16>) {
     store16(to, make_uint4(bf16_pair(v[0]), bf16_pair(v[1]), bf16_pair(v[2]), bf16_pair(v[3])));
   } else {
