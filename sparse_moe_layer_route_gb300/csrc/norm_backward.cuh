@@ -13,10 +13,10 @@
 // second, small kernel. A row of gates whose tokens are all in one CTA's run is complete there; one that
 // is shared leaves a partial sum in each.
 //
-// Measured: 8192 x 4096, rms norms, a 32-bit stream, gates per channel, dropout: 171 us (604 MB, 3.5 TB/s). A thread
+// Measured: 8192 x 4096, rms norms, a 32-bit stream, gates per channel, dropout: 167 us (604 MB, 3.6 TB/s). A thread
 // holds a row's values and the sums of its channels, 128 registers, so 16 warps an SM have to cover two sums over the
-// row in a chain of 74 instructions an element (issue 45 % of peak); the joining kernel is 8 us of it. 2051 x 2048,
-// a layer norm before the next block only, gates per sequence: 29 us.
+// row in a chain of 74 instructions an element (issue 45 % of peak). 2051 x 2048, a layer norm before the next block
+// only, gates per sequence: 27 us. Both with the joining kernel.
 #pragma once
 #include "norm_rows.cuh"
 
@@ -440,7 +440,7 @@ cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStrea
 
 // As in the forward direction (3001 x 1024 with every gradient: 31 us with one chunk, 52 with two). A third one's sums
 // and values are more than a thread's registers; forms whose number of warps follows the row's width at run time
-// cost 8192 x 4096 250 us instead of 171.
+// cost 8192 x 4096 250 us instead of 171 then.
 template <class H, class Y>
 cudaError_t launch_backward(const NormGradArgs& a, int* ctas, cudaStream_t st) {
   const int d = a.d;
