@@ -238,6 +238,32 @@ def test_outputs_in_the_place_of_inputs():
             assert torch.equal(dh, g["d_h"]) and torch.equal(dn if other == "d_n" else y, g["d_y"])
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("T,d,pad", [(1, 1, 0), (4, 1, 0), (3, 2, 1), (5, 256, 0), (5, 255, 2), (4, 513, 0),
+                                     (7, 1027, 3), (3, 2304, 1), (2, 8200, 1)])
+def test_tensors_that_start_in_the_middle_of_a_word(T, d, pad, dtype):
+    """Inputs and outputs one element into their buffers: rows that start on words and between them in turn, nothing
+    before the first one, and what lies around the outputs stays."""
+    c = Case(T, d, R.RMS, R.LAYER, h=dtype, y=dtype, w=dtype, gate=2, bias=True, p=0.1, pad_h=pad, pad_y=pad)
+
+    def inside(v, pad=0):
+        buf = torch.full((T * (d + pad) + 2,), float("nan"), dtype=dtype, device="cuda")
+        view = buf[1:-1].view(T, d + pad)[:, :d]
+        view.copy_(v)
+        return view, buf
+
+    c.h, c.y = inside(c.h, pad)[0], inside(c.y, pad)[0]
+    (h_out, h_buf), (n, n_buf) = inside(c.d_n), inside(c.d_n)
+    M.residual_norm(c.cfg, c.h, c.y, h_out, n, **c.w, rng=c.rng)
+    h64, n64, dh, dn = R.forward(c.c, c.tensors(), c.m)
+    R.assert_close("h_out", h_out, h64, dh)
+    R.assert_close("n", n, n64, dn)
+    c.d_h_out, c.d_n = inside(c.d_h_out)[0], inside(c.d_n)[0]
+    c.check_backward(c.d_h_out, c.d_n)
+    for buf in (h_buf, n_buf):
+        assert buf[0].isnan() and buf[-1].isnan()
+
+
 def test_what_lies_between_and_behind_rows_stays():
     T, d, pad = 6, 100, 28
     for base in (torch.full((T + 1, d + pad), 7.0, dtype=BF16, device="cuda"),):
