@@ -122,7 +122,9 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
   const int d = CLUSTER ? min(a.d, base + norm_width(a.d, cl)) : a.d;  // this CTA's channels end there
   const int per = norm_rows_per_cta(a.T, ctas);
   const int r0 = (int)((long long)cta * per), r1 = at_most(r0, per, a.T);
-  RowSum<R, CLUSTER> sum(red[group], group, cl);
+  // where there are several groups, all their threads meet to write sums
+  const int live = kGroups > 1 ? R / 32 : live_warps<R, CLUSTER>(d);
+  RowSum<R, CLUSTER> sum(red[group], group, cl, live);
   const int w0 = base + tid / 32 * kWarpCols;  // channels of chunk c: w0 + c * R * 8 + lane * 8 + 0..7
   const float inv = 1.f / (float)a.d;
   const bool normed = a.d_n.p != nullptr;  // the norm before the next block has a gradient
@@ -152,6 +154,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
     __syncwarp();
   }
   griddep_wait();
+  if (tid / 32 >= live) return;
   const DropState ds(a.drop);
   float* part = a.part + (size_t)cta * kNormParts * a.d;
   // the tokens are taken in the same order whether or not the gates' gradient is wanted, so that the others
@@ -446,6 +449,7 @@ cudaError_t launch_backward(const NormGradArgs& a, int* ctas, cudaStream_t st) {
   const int d = a.d;
   if (d <= 512) return launch_grad_form<32, 2, false, H, Y>(a, 1, ctas, st);
   if (d <= 1024) return launch_grad_form<128, 1, false, H, Y>(a, 1, ctas, st);
+  if (d <= 1536) return launch_grad_form<256, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 2048) return launch_grad_form<128, 2, false, H, Y>(a, 1, ctas, st);
   if (d <= 4096) return launch_grad_form<256, 2, false, H, Y>(a, 1, ctas, st);
   if (d <= 8192) return launch_grad_form<512, 2, false, H, Y>(a, 1, ctas, st);

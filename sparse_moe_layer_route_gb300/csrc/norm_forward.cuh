@@ -33,7 +33,8 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
   const int rank = CLUSTER ? (int)blockIdx.x % cl : 0;
   const int base = CLUSTER ? rank * norm_width(a.d, cl) : 0;
   const int d = CLUSTER ? min(a.d, base + norm_width(a.d, cl)) : a.d;  // this CTA's channels end there
-  RowSum<R, CLUSTER> sum(red[group], group, cl);
+  const int live = live_warps<R, CLUSTER>(d);
+  RowSum<R, CLUSTER> sum(red[group], group, cl, live);
   const int w0 = base + tid / 32 * kWarpCols;  // channels of chunk c: w0 + c * R * 8 + lane * 8 + 0..7
   const bool block = a.y.p != nullptr;
   // the warp's memory: [stage] of h and y, then `turn`
@@ -54,6 +55,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
 #pragma unroll
   for (int c = 0; c < NC; ++c) col[c] = w0 + c * R * 8 + lane * 8;
   griddep_wait();
+  if (tid / 32 >= live) return;
   const DropState ds(a.drop);
   int next = first < a.T ? (int)first : a.T;
   auto bring = [&](uint32_t stage) {
@@ -144,7 +146,9 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
 
 template <int R, int NC, bool CLUSTER, class H, class Y>
 cudaError_t launch_form(const NormArgs& a, int cl, cudaStream_t st) {
-  constexpr int threads = norm_threads<R>(), groups = threads / R, per_sm = forward_ctas<R, NC>();
+  constexpr int groups = norm_threads<R>() / R;
+  const int threads = groups > 1 ? norm_threads<R>() : 32 * live_warps<R, CLUSTER>(a.d);
+  const int per_sm = forward_ctas<R, NC>() * norm_threads<R>() / threads;
   const int pitch = Input<H, R, NC>::bytes(a.h.dtype) +
                     (a.y.p != nullptr ? Input<Y, R, NC>::bytes(a.y.dtype) : 0);
   const int turn = std::is_same_v<H, Any> ? kWarpCols * 4 : 0;
@@ -166,6 +170,7 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t st) {
   const int d = a.d;
   if (d <= 512) return launch_form<32, 2, false, H, Y>(a, 1, st);
   if (d <= 1024) return launch_form<128, 1, false, H, Y>(a, 1, st);
+  if (d <= 1536) return launch_form<256, 1, false, H, Y>(a, 1, st);
   if (d <= 2048) return launch_form<128, 2, false, H, Y>(a, 1, st);
   if (d <= 4096) return launch_form<256, 2, false, H, Y>(a, 1, st);
   if (d <= 8192) return launch_form<256, 4, false, H, Y>(a, 1, st);

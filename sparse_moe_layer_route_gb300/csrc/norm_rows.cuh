@@ -230,6 +230,14 @@ struct Input {
   }
 };
 
+// Warps of a row of d channels whose first chunk lies in it; the others have nothing to do (not of a cluster's rows:
+// all its threads meet).
+template <int R, bool CLUSTER>
+__host__ __device__ __forceinline__ int live_warps(int d) {
+  const int all = R / 32, wanted = (d + kWarpCols - 1) / kWarpCols;
+  return CLUSTER || wanted > all ? all : wanted;
+}
+
 // -------------------------------------------------------------------------------------- parameters
 // A thread's chunk of a row of parameters as it lies in memory, from channel c on, 0 past the d-th. They are
 // small and stay in L1 from row to row. ANY: of any alignment.
@@ -440,9 +448,14 @@ struct RowSum {
   static constexpr int kBuf = 4 * (kW + kMost);  // of four sums: [sum][warp], then [CTA][sum]
   static constexpr int kFloats = 2 * kBuf;
   float* buf;                                    // 16-byte aligned
-  int group, cl, turn;
+  int group, cl, turn, threads;
 
-  __device__ RowSum(float* b, int g, int n) : buf(b), group(g), cl(n), turn(0) {}
+  // live: warps that take part, the first ones; the others' places are 0 from before the first barrier on.
+  __device__ RowSum(float* b, int g, int n, int live) : buf(b), group(g), cl(n), turn(0), threads(32 * live) {
+    const int tid = threadIdx.x % R;
+    if (R > 32 && tid < 8)
+      for (int w = live; w < kW; ++w) buf[tid / 4 * kBuf + tid % 4 * kW + w] = 0.f;
+  }
 
   template <int N>
   __device__ __forceinline__ void operator()(float (&v)[N]) {
@@ -471,7 +484,7 @@ struct RowSum {
       float* b = buf + turn * kBuf;
       turn ^= 1;
       if (lane % (32 / N) == 0) b[lane / (32 / N) * kW + warp] = s;
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(R) : "memory");
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         float part[kW / 4];
