@@ -7,7 +7,8 @@
 namespace moe {
 
 constexpr int kNormMaxSize = 65536;  // d: eight CTAs of a cluster with 8192 channels each
-constexpr int kNormMaxCtas = 320;    // of the gradient, each with partial sums in the workspace
+// CTAs of the gradient at most, each with partial sums in the workspace: three an SM of narrow rows, else two.
+__host__ __device__ __forceinline__ int norm_max_ctas(int d) { return d <= 2048 ? 480 : 320; }
 constexpr int kNormSmem = 227 * 1024;
 
 // Rows of a matrix: elements between rows, type, and whether every row starts on 16 bytes.

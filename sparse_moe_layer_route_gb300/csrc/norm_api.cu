@@ -64,7 +64,7 @@ bool params_ok(const moe_residual_norm_config* c, const moe_residual_norm_params
 }
 
 size_t need(const moe_residual_norm_config* c) {
-  const int ctas = c->T < kNormMaxCtas ? c->T : kNormMaxCtas;
+  const int ctas = c->T < norm_max_ctas(c->d) ? c->T : norm_max_ctas(c->d);
   return (4ull * kNormParts * c->d * ctas + 255) / 256 * 256;
 }
 

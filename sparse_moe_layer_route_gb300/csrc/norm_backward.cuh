@@ -415,7 +415,8 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
 
 template <int R, int NC, bool CLUSTER, class H, class Y>
 cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStream_t st) {
-  constexpr int threads = norm_threads<R>(), groups = threads / R, per_sm = R == 512 ? 1 : 2;
+  constexpr int groups = norm_threads<R>() / R;
+  const int threads = groups > 1 ? norm_threads<R>() : 32 * live_warps<R, CLUSTER>(a.d), per_sm = 512 / threads;
   // one stage of four 32-bit inputs, both biases' sums and what turns rows round: 208 KB
   static_assert(16 * (2 * 2 * 1024 + 4 * 2 * 1024 + 1024) <= kNormSmem - 2048, "the widest form fits");
   const int pitch = grad_pitch<NC, H, Y>(a), turn = std::is_same_v<H, Any> ? kWarpCols * 4 : 0;
@@ -426,7 +427,7 @@ cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStrea
   };
   while (stages > 1 && smem() > kNormSmem / per_sm - 2048) --stages;
   const int room = per_sm * num_sms() / cl;
-  const int most = room < kNormMaxCtas ? room : kNormMaxCtas;
+  const int most = room < norm_max_ctas(a.d) ? room : norm_max_ctas(a.d);
   const long long need = ((long long)a.T + groups - 1) / groups;
   *ctas = (int)(need < most ? need : most);
   const int per = norm_rows_per_cta(a.T, *ctas);
@@ -441,16 +442,15 @@ cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStrea
   return cudaErrorInvalidValue;
 }
 
-// As in the forward direction (3001 x 1024 with every gradient: 31 us with one chunk, 52 with two). A third one's sums
-// and values are more than a thread's registers; forms whose number of warps follows the row's width at run time
-// cost 8192 x 4096 250 us instead of 171 then.
+// As in the forward direction, but one chunk is faster up to 2048 channels: two chunks' sums and values are more than
+// a thread's registers (3001 rows with every gradient, one chunk and two: 1024 channels 29 us and 52, 1032 37 and 54,
+// 2048 53 and 67). Of 4096 one chunk of 512 threads was no faster.
 template <class H, class Y>
 cudaError_t launch_backward(const NormGradArgs& a, int* ctas, cudaStream_t st) {
   const int d = a.d;
   if (d <= 512) return launch_grad_form<32, 2, false, H, Y>(a, 1, ctas, st);
   if (d <= 1024) return launch_grad_form<128, 1, false, H, Y>(a, 1, ctas, st);
-  if (d <= 1536) return launch_grad_form<256, 1, false, H, Y>(a, 1, ctas, st);
-  if (d <= 2048) return launch_grad_form<128, 2, false, H, Y>(a, 1, ctas, st);
+  if (d <= 2048) return launch_grad_form<256, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 4096) return launch_grad_form<256, 2, false, H, Y>(a, 1, ctas, st);
   if (d <= 8192) return launch_grad_form<512, 2, false, H, Y>(a, 1, ctas, st);
   int cl = 2;

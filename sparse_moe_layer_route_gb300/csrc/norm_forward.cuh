@@ -9,7 +9,7 @@
 // thread has up to 32 channels to pay for a row's sums and addresses.
 //
 // Measured: 16384 x 7168, rms norms, gates per channel, bf16: 150 us (940 MB, 6.3 TB/s); 3001 x 1027, layer norms with
-// biases, gates per sequence, dropout (rows of any alignment, one element at a time): 31 us; 16 x 7168: 7.4 us, the
+// biases, gates per sequence, dropout (rows of any alignment, one element at a time): 26 us; 16 x 7168: 7.4 us, the
 // call's.
 #pragma once
 #include "norm_rows.cuh"
@@ -162,9 +162,10 @@ cudaError_t launch_form(const NormArgs& a, int cl, cudaStream_t st) {
                               threads, smem(), cl, st, a, cl, stages);
 }
 
-// The narrowest form that holds a row: what a form has past the row's end costs as much as channels do (3001 rows
-// of 1024, layer norms, gates and dropout: 14 us with 128 threads of one chunk, 19 with two). As much work for
-// a thread as registers allow pays for a row's sums: 16384 x 7168 has four chunks and two CTAs per SM.
+// The narrowest form that holds a row, as what a form has past the row's end costs as much as channels do (3001 rows
+// of 1024, layer norms, gates and dropout: 14 us with one chunk of 128 threads, 19 with two). With one chunk of 256
+// threads a CTA has as many warps as the row needs: up to six of the eight that is faster than two chunks of 128
+// threads (1027 channels: 26 us instead of 31; 1800: 26 instead of 23).
 template <class H, class Y>
 cudaError_t launch_forward(const NormArgs& a, cudaStream_t st) {
   const int d = a.d;
