@@ -444,11 +444,12 @@ cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStrea
 
 // As in the forward direction, but one chunk is faster up to 2048 channels: two chunks' sums and values are more than
 // a thread's registers (3001 rows with every gradient, one chunk and two: 1024 channels 29 us and 52, 1032 37 and 54,
-// 2048 53 and 67). Of 4096 one chunk of 512 threads was no faster.
+// 2048 53 and 67; 50000 of 128 74 and 146, 20000 of 512 76 and 80). Of 4096 one chunk of 512 threads was no faster.
 template <class H, class Y>
 cudaError_t launch_backward(const NormGradArgs& a, int* ctas, cudaStream_t st) {
   const int d = a.d;
-  if (d <= 512) return launch_grad_form<32, 2, false, H, Y>(a, 1, ctas, st);
+  if (d <= 256) return launch_grad_form<32, 1, false, H, Y>(a, 1, ctas, st);
+  if (d <= 512) return launch_grad_form<64, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 1024) return launch_grad_form<128, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 2048) return launch_grad_form<256, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 4096) return launch_grad_form<256, 2, false, H, Y>(a, 1, ctas, st);

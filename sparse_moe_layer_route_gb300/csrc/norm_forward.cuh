@@ -163,12 +163,14 @@ cudaError_t launch_form(const NormArgs& a, int cl, cudaStream_t st) {
 }
 
 // The narrowest form that holds a row, as what a form has past the row's end costs as much as channels do (3001 rows
-// of 1024, layer norms, gates and dropout: 14 us with one chunk of 128 threads, 19 with two). With one chunk of 256
+// of 1024, layer norms, gates and dropout: 14 us with one chunk of 128 threads, 19 with two; 50000 of 128: 40 us with
+// one chunk of a warp, 57 with two; but 20000 of 512 32 us so, 41 with one chunk of 64 threads). With one chunk of 256
 // threads a CTA has as many warps as the row needs: up to six of the eight that is faster than two chunks of 128
 // threads (1027 channels: 26 us instead of 31; 1800: 26 instead of 23).
 template <class H, class Y>
 cudaError_t launch_forward(const NormArgs& a, cudaStream_t st) {
   const int d = a.d;
+  if (d <= 256) return launch_form<32, 1, false, H, Y>(a, 1, st);
   if (d <= 512) return launch_form<32, 2, false, H, Y>(a, 1, st);
   if (d <= 1024) return launch_form<128, 1, false, H, Y>(a, 1, st);
   if (d <= 1536) return launch_form<256, 1, false, H, Y>(a, 1, st);

@@ -444,7 +444,7 @@ __device__ __forceinline__ void drop8(const Drop& d, const DropState& s, uint32_
 // cost six shuffles, not twenty.
 template <int R, bool CLUSTER>
 struct RowSum {
-  static constexpr int kW = R / 32, kMost = CLUSTER ? 8 : 0;
+  static constexpr int kW = (R / 32 + 3) / 4 * 4, kMost = CLUSTER ? 8 : 0;  // warps, read four at a time
   static constexpr int kBuf = 4 * (kW + kMost);  // of four sums: [sum][warp], then [CTA][sum]
   static constexpr int kFloats = 2 * kBuf;
   float* buf;                                    // 16-byte aligned
