@@ -104,7 +104,7 @@ class Case:
 KINDS = [(R.RMS, R.RMS), (R.NONE, R.RMS), (R.LAYER, R.LAYER), (R.RMS, R.NONE), (R.NONE, R.LAYER),
          (R.NONE, R.NONE)]
 # every form of rows (one warp to clusters), its edges, odd ones
-WIDTHS = [1, 7, 8, 255, 256, 257, 512, 513, 1024, 1027, 2048, 2049, 4096, 4100, 7168, 8192, 8200, 16384, 16385]
+WIDTHS = [1, 7, 8, 255, 256, 257, 512, 513, 1024, 1027, 1536, 1537, 2048, 2049, 4096, 4100, 7168, 8192, 8200, 16384, 16385]
 
 
 @pytest.mark.parametrize("after,before", KINDS)
@@ -262,6 +262,34 @@ def test_tensors_that_start_in_the_middle_of_a_word(T, d, pad, dtype):
     c.check_backward(c.d_h_out, c.d_n)
     for buf in (h_buf, n_buf):
         assert buf[0].isnan() and buf[-1].isnan()
+
+
+@pytest.mark.parametrize("d", [64, 1024, 2304])
+def test_32_bit_rows_on_16_bytes_but_not_on_32(d):
+    T = 5
+    c = Case(T, d, R.RMS, R.LAYER, h=F32, y=F32, gate=1, p=0.1)
+
+    def off():
+        buf = torch.full((T * d + 8,), 3.0, device="cuda")
+        return buf[4:-4].view(T, d), buf
+
+    want = c.run()
+    (h_out, h_buf), (n, n_buf), (d_h, dh_buf), (d_y, dy_buf) = off(), off(), off(), off()
+    M.residual_norm(c.cfg, c.h, c.y, h_out, n, **c.w, rng=c.rng)
+    assert torch.equal(h_out, want[0]) and torch.equal(n, want[1])
+    g = c.gradients(want[0], c.d_h_out, c.d_n)
+    (d_gate, dg_buf) = off()
+    ws = torch.empty(M.residual_norm_workspace_size(c.cfg), dtype=torch.uint8, device="cuda")
+    M.residual_norm_backward(c.cfg, h_out, c.y, c.d_h_out, c.d_n, d_h, d_y, ws,
+                             **{k: v for k, v in c.w.items() if k != "b_before"}, rng=c.rng, d_gate=d_gate)
+    assert torch.equal(d_h, g["d_h"]) and torch.equal(d_y, g["d_y"]) and torch.equal(d_gate, g["d_gate"])
+    x, x_buf = off()
+    M.dropout(c.h, 0.1, c.rng, x)
+    aligned = torch.empty_like(c.h)
+    M.dropout(c.h, 0.1, c.rng, aligned)
+    assert torch.equal(x, aligned)
+    for buf in (h_buf, n_buf, dh_buf, dy_buf, dg_buf, x_buf):
+        assert (buf[:4] == 3).all() and (buf[-4:] == 3).all()
 
 
 def test_what_lies_between_and_behind_rows_stays():
