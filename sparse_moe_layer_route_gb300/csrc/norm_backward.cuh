@@ -13,7 +13,7 @@
 // second, small kernel. A row of gates whose tokens are all in one CTA's run is complete there; one that
 // is shared leaves a partial sum in each.
 //
-// Measured: 8192 x 4096, rms norms, a 32-bit stream, gates per channel, dropout: 167 us (604 MB, 3.6 TB/s). A thread
+// Measured: 8192 x 4096, rms norms, a 32-bit stream, gates per channel, dropout: 156 us (604 MB, 3.9 TB/s). A thread
 // holds a row's values and the sums of its channels, 128 registers, so 16 warps an SM have to cover two sums over the
 // row in a chain of 74 instructions an element (issue 45 % of peak). 2051 x 2048, a layer norm before the next block
 // only, gates per sequence: 27 us. Both with the joining kernel.
@@ -442,9 +442,10 @@ cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStrea
   return cudaErrorInvalidValue;
 }
 
-// As in the forward direction, but one chunk is faster up to 2048 channels: two chunks' sums and values are more than
+// As in the forward direction, but one chunk is faster wherever it holds a row: two chunks' sums and values are more than
 // a thread's registers (3001 rows with every gradient, one chunk and two: 1024 channels 29 us and 52, 1032 37 and 54,
-// 2048 53 and 67; 50000 of 128 74 and 146, 20000 of 512 76 and 80). Of 4096 one chunk of 512 threads was no faster.
+// 2048 53 and 67, 2304 78 and 83, 4096 113 and 110, with rms norms 71 and 81; 50000 of 128 74 and 146, 20000 of 512 76
+// and 80).
 template <class H, class Y>
 cudaError_t launch_backward(const NormGradArgs& a, int* ctas, cudaStream_t st) {
   const int d = a.d;
@@ -452,7 +453,7 @@ cudaError_t launch_backward(const NormGradArgs& a, int* ctas, cudaStream_t st) {
   if (d <= 512) return launch_grad_form<64, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 1024) return launch_grad_form<128, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 2048) return launch_grad_form<256, 1, false, H, Y>(a, 1, ctas, st);
-  if (d <= 4096) return launch_grad_form<256, 2, false, H, Y>(a, 1, ctas, st);
+  if (d <= 4096) return launch_grad_form<512, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 8192) return launch_grad_form<512, 2, false, H, Y>(a, 1, ctas, st);
   int cl = 2;
   while (norm_width(d, cl) > 8192) cl *= 2;
