@@ -485,6 +485,13 @@ def _expect(where, name, t, shape, dtype, gpu):
     return t.data_ptr()
 
 
+def _expect_int32(where, **sizes):
+    """Sizes that the library takes as 32-bit numbers: past their range they would arrive as others."""
+    for name, n in sizes.items():
+        if n >= 2 ** 31:
+            raise ValueError(f"{where}: {name} = {n} is not below 2^31")
+
+
 def _expect_ws(where, ws, gpu):
     """ws: a tensor whose elements fill their memory on GPU `gpu`. Its address and bytes."""
     if ws.get_device() != gpu or not ws.is_contiguous():
@@ -808,6 +815,7 @@ def dropout(x, p, rng, y, residual=None, stream=None):
     if x.dim() != 2:
         raise ValueError(f"{w}: x of shape {tuple(x.shape)} is not [T, d]")
     T, d = x.shape
+    _expect_int32(w, T=T, d=d)
     gpu = _current_gpu(w, "x", x, t)
     ld_x, ld_r = (x.stride(0) if T > 1 else d), d
     if ld_x < d:
