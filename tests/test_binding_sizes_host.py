@@ -25,7 +25,7 @@ def drop(T, d, residual=False, p=0.5):
 
 
 @pytest.mark.parametrize("T,d", [(2 ** 32, 64), (2 ** 32 + 3, 1), (2 ** 31, 8), (1, 2 ** 32 + 8), (1, 2 ** 31),
-                                 (2, 2 ** 33), (2 ** 32, 2 ** 32)])
+                                 (2, 2 ** 33)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_dropout(calls, T, d, residual):  # noqa: F811
     with pytest.raises(ValueError):
