@@ -544,6 +544,7 @@ def quantize_rows(x, q, scale, stream=None):
     stride of 0 means `contiguous` to the library) to q int8 [T, d] and scale fp32 [T]."""
     w, n = "moe_quantize_rows", _names()
     T, d = x.shape
+    _expect_int32(w, T=T, d=d)
     step, unit = x.stride()
     gpu = _current_gpu(w, "x", x, n)
     if (d > 1 and unit != 1) or (T > 1 and step < d):
@@ -563,6 +564,7 @@ def quantize_channels(W, stream=None):
         raise ValueError(f"moe_quantize_channels: W of shape {tuple(W.shape)} is neither [n, K, N] nor "
                          "[K, N]")
     n, (K, N) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
+    _expect_int32("moe_quantize_channels", n=n, K=K, N=N)
     gpu = _current_gpu("moe_quantize_channels", "W", W, _names())
     _expect("moe_quantize_channels", "W", W, tuple(W.shape), torch.bfloat16, gpu)
     with _allocating_for(stream):
@@ -576,6 +578,7 @@ def quantize_channels(W, stream=None):
 def int8_matmul_workspace_size(rows, K, N, n_mat) -> int:
     """Bytes that products of up to `rows` rows need."""
     n = ctypes.c_size_t(0)
+    _expect_int32("moe_int8_matmul_workspace_size", rows=rows, K=K, N=N, n_mat=n_mat)
     _check(lib().moe_int8_matmul_workspace_size(rows, K, N, n_mat, ctypes.byref(n)),
            "moe_int8_matmul_workspace_size")
     return n.value
@@ -603,6 +606,7 @@ def int8_matmul(q_x, s_x, q_w, s_w, offsets, y, ws, stream=None):
     w, t = "moe_int8_matmul", _names()
     rows, K = q_x.shape
     n, N, _ = q_w.shape
+    _expect_int32(w, rows=rows, K=K, N=N, n=n)
     gpu = _current_gpu(w, "q_x", q_x, t)
     _check(lib().moe_int8_matmul(
         rows, K, N, n, _expect(w, "q_x", q_x, (rows, K), t.i8, gpu),

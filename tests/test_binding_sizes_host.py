@@ -37,3 +37,35 @@ def test_dropout_s_largest_sizes_reach_the_library(calls):  # noqa: F811
     drop(2 ** 31 - 1, 1)
     drop(1, 2 ** 31 - 1)                 # which the library itself refuses
     assert [args[:2] for _, args in calls] == [(2 ** 31 - 1, 1), (1, 2 ** 31 - 1)]
+
+
+BIG = 2 ** 32 + 16
+
+
+def rows(T, d):
+    M.quantize_rows(meta(T, d), meta(T, d, dtype=I8), meta(T, dtype=F32), stream=0)
+
+
+def product(T, K, N, n):
+    ws = Meta(torch.zeros(1 << 16, dtype=torch.uint8))
+    M.int8_matmul(meta(T, K, dtype=I8), meta(T, dtype=F32), meta(n, N, K, dtype=I8), meta(n, N, dtype=F32),
+                  meta(n + 1, dtype=torch.int32), meta(T, N), ws, stream=0)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: rows(BIG, 64), lambda: rows(2 ** 32, 1), lambda: rows(1, BIG), lambda: rows(0, 2 ** 31),
+    lambda: product(BIG, 16, 16, 1), lambda: product(4, BIG, 16, 1), lambda: product(4, 16, BIG, 1),
+    lambda: product(4, 16, 16, BIG), lambda: M.int8_matmul_workspace_size(BIG, 16, 16, 1),
+    lambda: M.int8_matmul_workspace_size(4, BIG, 16, 1), lambda: M.int8_matmul_workspace_size(4, 16, BIG, 1),
+    lambda: M.int8_matmul_workspace_size(4, 16, 16, BIG), lambda: M.quantize_channels(meta(BIG, 16, 16), stream=0),
+    lambda: M.quantize_channels(meta(1, BIG, 16), stream=0), lambda: M.quantize_channels(meta(16, BIG), stream=0)])
+def test_8_bit_entry_points(calls, call):  # noqa: F811
+    with pytest.raises(ValueError):
+        call()
+    assert calls == []
+
+
+def test_8_bit_sizes_below_reach_the_library(calls):  # noqa: F811
+    rows(2 ** 31 - 1, 1)
+    product(2 ** 31 - 1, 16, 16, 1)
+    assert [args[0] for _, args in calls] == [2 ** 31 - 1] * 2
