@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), R == 512 ? 1 : 2)
     copies_commit();
   };
   for (int i = 0; i < stages; ++i) bring(i * pitch);
+  sum.all_started();
   uint32_t stage = 0;
   F2 wa[NC][4] = {}, wb[NC][4] = {}, ga[NC][4] = {};
   int col[NC];

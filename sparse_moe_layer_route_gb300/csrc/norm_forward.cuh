@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(norm_threads<R>(), forward_ctas<R, NC>())
     copies_commit();
   };
   for (int i = 0; i < stages; ++i) bring(i * pitch);
+  sum.all_started();
   uint32_t stage = 0;
   for (long long r = first; r < a.T; r += step) {
     const int row = (int)r;

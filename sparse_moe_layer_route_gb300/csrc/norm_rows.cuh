@@ -453,8 +453,21 @@ struct RowSum {
   // live: warps that take part, the first ones; the others' places are 0 from before the first barrier on.
   __device__ RowSum(float* b, int g, int n, int live) : buf(b), group(g), cl(n), turn(0), threads(32 * live) {
     const int tid = threadIdx.x % R;
-    if (R > 32 && tid < 8)
+    if constexpr (CLUSTER) {
+      static_assert(R / 32 == kW, "no place to clear");
+      cooperative_groups::this_cluster().barrier_arrive();
+    } else if (R > 32 && tid < 8) {
       for (int w = live; w < kW; ++w) buf[tid / 4 * kBuf + tid % 4 * kW + w] = 0.f;
+    }
+  }
+
+  // By all threads, once, before the first sum: a CTA may write to another's shared memory only when that has started.
+  // Between this and the arrival above are the first rows' copies, so nothing waits long here.
+  __device__ __forceinline__ void all_started() const {
+    if constexpr (CLUSTER) {
+      __syncwarp();
+      cooperative_groups::this_cluster().barrier_wait();
+    }
   }
 
   template <int N>
