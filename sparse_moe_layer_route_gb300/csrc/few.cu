@@ -126,7 +126,10 @@ __device__ __forceinline__ void barrier_arrive(const FewArgs& a, Plan& p) {
     p.target = (before / n + 1) * n;
   }
 }
+// All threads get the same answer. They may come from different branches, so it is a barrier by number: warps with
+// different tasks wait at different places.
 __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
+  int late = 0;
   if (threadIdx.x == 0) {
     uint64_t t0 = 0;
     for (unsigned it = 1;; ++it) {
@@ -138,15 +141,21 @@ __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
         if (t0 == 0) t0 = t;
         if (t - t0 > kWaitLimitNs) {
           atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
-          p.fail = 1;
+          p.fail = late = 1;
           break;
         }
       }
     }
     __threadfence();
   }
-  __syncthreads();
-  return p.fail == 0;
+  __syncwarp();
+  int any;
+  asm volatile(
+      "{\n .reg .pred l, o;\n setp.ne.s32 l, %1, 0;\n bar.red.or.pred o, 2, l;\n selp.s32 %0, 1, 0, o;\n}"
+      : "=r"(any)
+      : "r"(late)
+      : "memory");
+  return any == 0;
 }
 
 // ------------------------------------------------------------------------------------------- units
