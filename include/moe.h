@@ -617,6 +617,15 @@ moe_status moe_dropout(int32_t T, int32_t d, int32_t dtype, const void* x, int64
 moe_status moe_check_bounded_waits(int64_t limit_ns, int32_t* expired, void* ws, size_t ws_bytes,
                                    moe_stream_t stream);
 
+/* The same for the waits of the few-token layer (moe_experts_few with these arguments, every gate 1, T > 0): its
+ * kernel runs with a wait limit of limit_ns (100 us .. 2 s) and one condition that never comes true. which 0 and 1:
+ * the first and the second grid barrier wait for a CTA more than there are; 2: the arrival of one tile of weights
+ * is never reported. The kernel must give up after a few times limit_ns at most, record MOE_DEVFAULT_PIPELINE_TIMEOUT,
+ * take every copy that it has asked for and return; out is not complete. ws may be used again without being cleared. */
+moe_status moe_check_few_waits(const moe_config* cfg, const moe_weights* w, const uint16_t* x,
+                               const int32_t* topk_idx, uint16_t* out, void* ws, size_t ws_bytes, int32_t which,
+                               int64_t limit_ns, moe_stream_t stream);
+
 /* Synchronises stream, reads the device status word of ws into *fault_bits (MOE_DEVFAULT_*),
  * clears it, and returns MOE_ERR_DEVICE_FAULT if any bit was set, MOE_ERR_CUDA if the stream
  * reported an error, else MOE_OK. */

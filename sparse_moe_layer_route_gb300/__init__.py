@@ -33,7 +33,7 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_prepare_router", "mo
            "moe_few_workspace_size", "moe_layer_forward_few", "moe_experts_few",
            "moe_residual_norm", "moe_residual_norm_workspace_size", "moe_residual_norm_backward",
            "moe_dropout",
-            "moe_check_bounded_waits", "moe_device_status",
+            "moe_check_bounded_waits", "moe_check_few_waits", "moe_device_status",
            "moe_status_string")
 
 
@@ -170,6 +170,8 @@ def lib():
         L.moe_bias_update.argtypes = [ctypes.c_int32, P, P, ctypes.c_float, ctypes.c_float, P]
         L.moe_device_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
         L.moe_check_bounded_waits.argtypes = [ctypes.c_int64, P, P, S, P]
+        L.moe_check_few_waits.argtypes = [cfgp, ctypes.POINTER(MoeWeights), P, P, P, P, S, ctypes.c_int32,
+                                          ctypes.c_int64, P]
         gcfgp, i64 = ctypes.POINTER(GateConfig), ctypes.c_int64
         L.moe_route_logits.argtypes = [gcfgp, P, P, P, P, P, P]
         L.moe_route_logits_backward.argtypes = [gcfgp, P, P, P, P, P, P]
@@ -840,6 +842,19 @@ def check_bounded_waits(limit_ns, expired, ws, stream=None):
     expired: int32 device tensor of 2. Read the result with device_status()."""
     _check(lib().moe_check_bounded_waits(int(limit_ns), _ptr(expired), _ptr(ws), ws.numel(),
                                          _stream(stream)), "moe_check_bounded_waits")
+
+
+def check_few_waits(cfg, weights: MoeWeights, x, topk_idx, out, ws, which, limit_ns, stream=None):
+    """The waits of experts_few against a condition that never comes true (see moe_check_few_waits): which 0 and 1 the
+    grid barriers, 2 a tile of weights. Read the result with device_status()."""
+    w, t = "moe_check_few_waits", _names()
+    T, d, k = cfg.T, cfg.d, cfg.top_k
+    gpu = _current_gpu(w, "x", x, t)
+    _expect_experts(w, cfg, weights, gpu, False)
+    _check(lib().moe_check_few_waits(
+        ctypes.byref(cfg), ctypes.byref(weights), _expect(w, "x", x, (T, d), t.bf16, gpu),
+        _expect(w, "topk_idx", topk_idx, (T, k), t.i32, gpu), _expect(w, "out", out, (T, d), t.bf16, gpu),
+        *_expect_ws(w, ws, gpu), int(which), int(limit_ns), _stream_on(stream, gpu, t)), w)
 
 
 def device_status(ws, stream=None) -> int:

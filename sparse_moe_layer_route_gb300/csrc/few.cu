@@ -50,7 +50,6 @@ constexpr int kSlots = MOE_FEW_MAX_TOKENS * 8;          // T * top_k at most
 constexpr int kSegs = kSlots + 4;                       // hit experts and shared ones
 constexpr int kCols = kSlots + 4 * MOE_FEW_MAX_TOKENS;  // columns of all of them
 constexpr int kAccLd = 68;       // floats between rows of 64 sums in shared memory (16-byte pieces)
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -117,19 +116,20 @@ struct Scratch {
 // Arrivals are counted through, call after call: the count a barrier waits for is the next multiple of the number
 // of CTAs above what it was before this CTA's own arrival. That is one atomic and one line to watch.
 // Arrival and wait are apart, so that copies that need nothing of the other CTAs can be started
-// between them. The wait is bounded; past it the status word says so.
+// between them. The wait is bounded; past it the status word says so. a.absent: 1 in the check of these waits, for
+// which a CTA more than there are has to arrive.
 __device__ __forceinline__ void barrier_arrive(const FewArgs& a, Plan& p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    const unsigned long long n = gridDim.x, before = atomicAdd(&a.meta->arrived, 1ull);
+    const unsigned long long n = gridDim.x + a.absent, before = atomicAdd(&a.meta->arrived, 1ull);
     p.target = (before / n + 1) * n;
   }
 }
-// All threads get the same answer. They may come from different branches, so it is a barrier by number: warps with
+// All threads get the same answer: whether all CTAs have arrived and no wait of this one has given up. They may come from different branches, so it is a barrier by number: warps with
 // different tasks wait at different places.
 __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
-  int late = 0;
+  int late = p.fail;
   if (threadIdx.x == 0) {
     uint64_t t0 = 0;
     for (unsigned it = 1;; ++it) {
@@ -139,7 +139,7 @@ __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
       if ((it & 63u) == 0) {
         const uint64_t t = ptx::globaltimer_ns();
         if (t0 == 0) t0 = t;
-        if (t - t0 > kWaitLimitNs) {
+        if (t - t0 > a.limit_ns) {
           atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
           p.fail = late = 1;
           break;
@@ -204,7 +204,7 @@ template <class F>
 __device__ __forceinline__ bool wait_units(const FewArgs& a, Plan& p, F now) {
   const uint64_t t0 = ptx::globaltimer_ns();
   for (unsigned it = 1; !now(); ++it)
-    if ((it & 63u) == 0 && (p.fail || ptx::globaltimer_ns() - t0 > 2 * kWaitLimitNs)) {
+    if ((it & 63u) == 0 && (p.fail || ptx::globaltimer_ns() - t0 > 2 * a.limit_ns)) {
       atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
       p.fail = 1;
       return false;
@@ -639,32 +639,36 @@ struct Ring {
       phase ^= 1u;
     }
   }
-  // Until the tile and this lane's piece are there. A wait that runs past its limit lets the kernel go on with
-  // what there is (later waits give up at once), and the status word says so.
-  __device__ __forceinline__ void wait(const FewArgs& a, Plan& p) const {
-    const uint32_t m = bar + 8 * slot;
-    if (!ptx::mbar_try_wait(m, phase)) {
-      uint64_t t0 = 0;  // the timer is slow to read: not before a tile is very late
-      for (unsigned it = 1; !ptx::mbar_try_wait(m, phase); ++it)
-        if ((it & 255u) == 0) {
-          const uint64_t now = ptx::globaltimer_ns();
-          if (t0 == 0) t0 = now;
-          if (p.fail || now - t0 > kWaitLimitNs) {
-            atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
-            p.fail = 1;
-            break;
-          }
-        }
-    }
-    __syncwarp();
+  // Until the tile and this lane's piece are there; false if a wait gave up, here or elsewhere in the CTA. The warp
+  // then keeps its place, asks for nothing more (the caller sees to that) and goes on to the end without tiles.
+  __device__ __forceinline__ bool wait(const FewArgs& a, Plan& p) const {
+    if (!__all_sync(kFull, ptx::mbar_try_wait(bar + 8 * slot, phase)) && !wait_long(a, p, true)) return false;
     cp_wait<kStages - 1>();
+    return true;
   }
-  // Takes what is still on its way (there is nothing unless a wait ran past its limit).
-  __device__ __forceinline__ void drain(const FewArgs& a, Plan& p) {
-    while (out > 0) {
-      wait(a, p);
-      next();
+  // All lanes take the same answer. with_others: a wait elsewhere that gave up ends this one.
+  __device__ bool wait_long(const FewArgs& a, Plan& p, bool with_others) const {
+    uint64_t t0 = 0;  // the timer is slow to read: not before a tile is very late
+    for (unsigned it = 1; !__all_sync(kFull, ptx::mbar_try_wait(bar + 8 * slot, phase)); ++it) {
+      bool stop = with_others && p.fail;
+      if ((it & 255u) == 0) {
+        const uint64_t now = ptx::globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > a.limit_ns) {
+          atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
+          p.fail = 1;
+          stop = true;
+        }
+      }
+      if (__any_sync(kFull, stop)) return false;
     }
+    return true;
+  }
+  // Takes what is still on its way (there is nothing unless a wait gave up), so that no copy is left that would write to
+  // shared memory of a CTA that has ended. A tile gets the whole limit once more, whatever happened elsewhere; the ones
+  // asked for after it have had as long.
+  __device__ void drain(const FewArgs& a, Plan& p) {
+    while (out > 0 && wait_long(a, p, false)) next();
     cp_wait<0>();
   }
   // One lane asks for a tile. What the warp read of the slot before is in registers.
@@ -828,7 +832,10 @@ __device__ void gate_up(const FewArgs& a, const FewMaps& maps, Plan& p, const Un
     const int k1 = units.begin(at.q + 1);
     float acc[NT][4][4] = {};
     for (int s = units.begin(at.q) + slice; s < k1; s += W / 2) {
-      ring.wait(a, p);
+      if (!ring.wait(a, p)) {
+        feed.more = false;
+        continue;
+      }
       const uint32_t tile = ring.tile(ring.slot);
       uint32_t f[2][4][4];
       fragments(tile, lane, f[0]);
@@ -931,12 +938,13 @@ struct DownFeed {
     }
     expert();
   }
-  __device__ __forceinline__ void issue_w(const Ring<NT>& r, int slot) const {
-    if (more && lane == 0) r.ask(slot, map, channel, (s - seg * fs) * 32, matrix);
+  __device__ __forceinline__ void issue_w(Ring<NT>& r, int slot) const {
+    if (!more) return;
+    if (lane == 0) r.ask(slot, map, channel, (s - seg * fs) * 32, matrix);
+    ++r.out;
   }
-  __device__ __forceinline__ void issue_h(Ring<NT>& r, int slot) const {
+  __device__ __forceinline__ void issue_h(const Ring<NT>& r, int slot) const {
     if (more) {
-      ++r.out;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         cp_async16(r.piece(slot) + 1024 * n, h[n] + (s - seg * fs) * 8, bytes[n]);
@@ -1000,7 +1008,7 @@ __device__ __forceinline__ float2* down_part(const FewArgs& a, int part, int t, 
 
 // The first weights, which need nothing of the other CTAs: they are on their way while those finish H.
 template <int NT, int W>
-__device__ void down_ahead(const DownFeed<NT, W>& feed, const Ring<NT>& ring) {
+__device__ void down_ahead(const DownFeed<NT, W>& feed, Ring<NT>& ring) {
   DownFeed<NT, W> ahead = feed;
 #pragma unroll
   for (int i = 0; i < Ring<NT>::kStages; ++i) {
@@ -1034,7 +1042,10 @@ __device__ void down(const FewArgs& a, Plan& p, const Units& units, DownFeed<NT,
         seg_end = (seg + 1) * fs;
         cnt = p.seg_base[seg + 1] - p.seg_base[seg];
       }
-      ring.wait(a, p);
+      if (!ring.wait(a, p)) {
+        feed.more = false;
+        continue;
+      }
       const uint32_t tile = ring.tile(ring.slot);
       uint32_t f[2][4][4];
       fragments(tile, lane, f[0]);
@@ -1118,7 +1129,8 @@ __global__ void __launch_bounds__(threads(W), 1)
   ring.phase = 0;
   ring.out = 0;
   if (warp < W && lane == 0) {
-    for (int i = 0; i < Ring<NT>::kStages; ++i) ptx::mbar_init(ring.bar + 8 * i, 1);
+    for (int i = 0; i < Ring<NT>::kStages; ++i)
+      ptx::mbar_init(ring.bar + 8 * i, a.withheld && i + warp + blockIdx.x == 0 ? 2 : 1);
     ptx::fence_mbarrier_init();
   }
   if (threadIdx.x == threads(W) - 1) {
@@ -1200,14 +1212,16 @@ __global__ void __launch_bounds__(threads(W), 1)
   int* count = a.count + 1 + kMostTiles;
   const auto rows = [&](int) { return make_int2(0, a.T); };
   const auto join = [&](int tile, int t, int l) { join_down(a, dn, tile, t, l); };
-  // past its limit the barrier lets the rest run on what there is, and take the copies under way
+  // Where a wait of this CTA has given up before, or does so here, the workers take the copies under way and that is all.
   if (warp < W) {
     DownFeed<NT, W> feed(a, maps, p, dn, warp, lane);
+    if (__any_sync(kFull, p.fail)) feed.more = false;
     down_ahead(feed, ring);
-    barrier_wait(a, p);
-    down<NT, W>(a, p, dn, feed, acc_s, ring, warp, lane);
-  } else {
-    barrier_wait(a, p);
+    if (barrier_wait(a, p))
+      down<NT, W>(a, p, dn, feed, acc_s, ring, warp, lane);
+    else
+      ring.drain(a, p);
+  } else if (barrier_wait(a, p)) {
     if (warp == W)
       deal_units(a, p, dn, count, lane);
     else

@@ -7,6 +7,7 @@ namespace moe {
 constexpr int kFewMaxCtas = 208;    // persistent CTAs at most
 constexpr int kFewUnits = 5;        // units of work for eight CTAs, at least (see few.cu)
 constexpr int kFewSteps = 2;        // tiles of a warp in a unit, at least, where tiles are cut
+constexpr unsigned long long kFewWaitNs = 2000000000ull;  // the longest that a wait takes
 constexpr int kFewMaxSize = 65536;  // d and d_ff: work is counted in 32 bits
 
 // The grid barriers' count of arrivals, in the counter block that moe_workspace_init clears: a multiple of the
@@ -38,6 +39,9 @@ struct FewArgs {
   FewMeta* meta;
   int T, d, E, k, f, S, mode, G, Gk, C;
   float tau;
+  // of waits: the limit; in the check of them, CTAs that barriers wait for in vain, and whether a tile is not reported
+  unsigned long long limit_ns;
+  int absent, withheld;
 };
 
 // Tensor maps of the weights: tiles of 32 rows x 64 columns.

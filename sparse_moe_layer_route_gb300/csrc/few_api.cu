@@ -65,6 +65,7 @@ FewArgs common(const Shape& s, const FewLayout& L, const moe_weights* w, const u
   a.Gk = s.Gk;
   a.C = s.C;
   a.tau = s.tau;
+  a.limit_ns = kFewWaitNs;
   return a;
 }
 
@@ -124,22 +125,60 @@ moe_status moe_layer_forward_few(const moe_config* cfg, const moe_weights* w, co
   return launch_few(a, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+}  // extern "C"
+
+namespace {
+
+// moe_experts_few up to its launch.
+moe_status prepare_experts(const moe_config* cfg, const moe_weights* w, const uint16_t* x, const int32_t* topk_idx,
+                           const float* topk_w, uint16_t* out, void* ws, size_t ws_bytes, FewArgs& a) {
+  if (!x || !topk_idx || !out || !aligned(x, 16) || !aligned(out, 16) || !aligned(topk_idx, 4) ||
+      !aligned(topk_w, 4) || !experts_ok(cfg, w))
+    return MOE_ERR_INVALID_ARG;
+  const Shape s = make_shape(*cfg);
+  const FewLayout L = few_layout(s);
+  const moe_status r = check_ws(ws, ws_bytes, L.total);
+  if (r != MOE_OK) return r;
+  a = common(s, L, w, x, out, ws);
+  a.idx_in = topk_idx;
+  a.w_in = topk_w;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
 moe_status moe_experts_few(const moe_config* cfg, const moe_weights* w, const uint16_t* x,
                            const int32_t* topk_idx, const float* topk_w, uint16_t* out, void* ws,
                            size_t ws_bytes, moe_stream_t stream) {
   moe_status r = check(cfg);
   if (r != MOE_OK) return r;
   if (cfg->T == 0) return MOE_OK;
-  if (!x || !topk_idx || !out || !aligned(x, 16) || !aligned(out, 16) || !aligned(topk_idx, 4) ||
-      !aligned(topk_w, 4) || !experts_ok(cfg, w))
-    return MOE_ERR_INVALID_ARG;
-  const Shape s = make_shape(*cfg);
-  const FewLayout L = few_layout(s);
-  if ((r = check_ws(ws, ws_bytes, L.total)) != MOE_OK) return r;
-  FewArgs a = common(s, L, w, x, out, ws);
-  a.idx_in = topk_idx;
-  a.w_in = topk_w;
+  FewArgs a = {};
+  if ((r = prepare_experts(cfg, w, x, topk_idx, topk_w, out, ws, ws_bytes, a)) != MOE_OK) return r;
   return launch_few(a, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_check_few_waits(const moe_config* cfg, const moe_weights* w, const uint16_t* x,
+                               const int32_t* topk_idx, uint16_t* out, void* ws, size_t ws_bytes, int32_t which,
+                               int64_t limit_ns, moe_stream_t stream) {
+  moe_status r = check(cfg);
+  if (r != MOE_OK) return r;
+  if (cfg->T == 0 || which < 0 || which > 2 || limit_ns < 100000 || limit_ns > (int64_t)kFewWaitNs)
+    return MOE_ERR_INVALID_ARG;
+  FewArgs a = {};
+  if ((r = prepare_experts(cfg, w, x, topk_idx, nullptr, out, ws, ws_bytes, a)) != MOE_OK) return r;
+  a.limit_ns = (unsigned long long)limit_ns;
+  a.absent = which < 2;
+  a.withheld = which == 2;
+  // With one CTA more to wait for than there are, a count from 0 leaves the first barrier short by one; from 1 it is
+  // the second one's turn. (The count's low byte comes first in memory.)
+  const cudaStream_t st = (cudaStream_t)stream;
+  const bool ok = cudaMemsetAsync(&a.meta->arrived, 0, 8, st) == cudaSuccess &&
+                  (which != 1 || cudaMemsetAsync(&a.meta->arrived, 1, 1, st) == cudaSuccess) &&
+                  launch_few(a, st) == cudaSuccess && cudaMemsetAsync(&a.meta->arrived, 0, 8, st) == cudaSuccess;
+  return ok ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"
