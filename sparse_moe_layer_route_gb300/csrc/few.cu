@@ -612,6 +612,25 @@ __device__ void make_plan(const FewArgs& a, Plan& p, Scratch& sc, int warp, int 
 }
 
 // ------------------------------------------------------------------------------------------- tiles
+// The rest of a wait for a tile that was not there at once; with_others: a wait elsewhere that gave up ends this one.
+__device__ __noinline__ bool wait_long(uint32_t m, uint32_t phase, unsigned long long limit_ns, int* status,
+                                       volatile int* fail, bool with_others) {
+  uint64_t t0 = 0;  // the timer is slow to read: not before a tile is very late
+  for (unsigned it = 1; !ptx::mbar_try_wait(m, phase); ++it) {
+    if ((it & 15u) == 0 && with_others && *fail) return false;
+    if ((it & 255u) == 0) {
+      const uint64_t now = ptx::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) {
+        atomicOr(status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
+        *fail = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 // A warp's ring: kStages tiles of weights (32 rows of 64 channels, 4 KB) and, for each, its lanes' pieces of the
 // columns' values (32 bytes per lane and 8 columns: a value in bf16 or, for down, two). Tiles are taken in the order
 // they were asked for. A tile costs a warp about a microsecond from wait to MMAs, so one of 2 KB would hold an SM
@@ -639,37 +658,32 @@ struct Ring {
       phase ^= 1u;
     }
   }
-  // Until the tile and this lane's piece are there; false if a wait gave up, here or elsewhere in the CTA. The warp
-  // then keeps its place, asks for nothing more (the caller sees to that) and goes on to the end without tiles.
-  __device__ __forceinline__ bool wait(const FewArgs& a, Plan& p) const {
-    if (!__all_sync(kFull, ptx::mbar_try_wait(bar + 8 * slot, phase)) && !wait_long(a, p, true)) return false;
-    cp_wait<kStages - 1>();
-    return true;
-  }
-  // All lanes take the same answer. with_others: a wait elsewhere that gave up ends this one.
-  __device__ bool wait_long(const FewArgs& a, Plan& p, bool with_others) const {
-    uint64_t t0 = 0;  // the timer is slow to read: not before a tile is very late
-    for (unsigned it = 1; !__all_sync(kFull, ptx::mbar_try_wait(bar + 8 * slot, phase)); ++it) {
-      bool stop = with_others && p.fail;
-      if ((it & 255u) == 0) {
-        const uint64_t now = ptx::globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > a.limit_ns) {
-          atomicOr(a.status, MOE_DEVFAULT_PIPELINE_TIMEOUT);
-          p.fail = 1;
-          stop = true;
-        }
+  // Until the tile and this lane's piece are there; false if a wait gave up, here or elsewhere in the CTA. The lane
+  // then asks for nothing more (the caller sees to that), stays at this tile (next() comes back to it) and goes on to
+  // the end of its units with what is there. Lanes need not agree on it: whatever one of them takes for a tile lies in
+  // the ring, and the copies are lane 0's affair.
+  __device__ __forceinline__ bool wait(const FewArgs& a, Plan& p) {
+    bool there = ptx::mbar_try_wait(bar + 8 * slot, phase);
+    if (!there) {
+      there = wait_long(bar + 8 * slot, phase, a.limit_ns, a.status, &p.fail, true);
+      if (!there) {
+        ++out;
+        phase ^= slot == 0;
+        slot = later(kStages - 1);
       }
-      if (__any_sync(kFull, stop)) return false;
     }
-    return true;
+    __syncwarp();
+    cp_wait<kStages - 1>();
+    return there;
   }
   // Takes what is still on its way (there is nothing unless a wait gave up), so that no copy is left that would write to
   // shared memory of a CTA that has ended. A tile gets the whole limit once more, whatever happened elsewhere; the ones
   // asked for after it have had as long.
-  __device__ void drain(const FewArgs& a, Plan& p) {
-    while (out > 0 && wait_long(a, p, false)) next();
+  __device__ void drain(const FewArgs& a, Plan& p, int lane) {
+    if (lane == 0)
+      while (out > 0 && wait_long(bar + 8 * slot, phase, a.limit_ns, a.status, &p.fail, false)) next();
     cp_wait<0>();
+    __syncwarp();
   }
   // One lane asks for a tile. What the warp read of the slot before is in registers.
   __device__ __forceinline__ void ask(int i, const CUtensorMap* map, int c, int row, int matrix) const {
@@ -832,10 +846,7 @@ __device__ void gate_up(const FewArgs& a, const FewMaps& maps, Plan& p, const Un
     const int k1 = units.begin(at.q + 1);
     float acc[NT][4][4] = {};
     for (int s = units.begin(at.q) + slice; s < k1; s += W / 2) {
-      if (!ring.wait(a, p)) {
-        feed.more = false;
-        continue;
-      }
+      if (!ring.wait(a, p)) feed.more = false;
       const uint32_t tile = ring.tile(ring.slot);
       uint32_t f[2][4][4];
       fragments(tile, lane, f[0]);
@@ -876,7 +887,7 @@ __device__ void gate_up(const FewArgs& a, const FewMaps& maps, Plan& p, const Un
     }
     unit_done<W>(a, p, units, i);
   }
-  ring.drain(a, p);
+  ring.drain(a, p, lane);
 }
 
 // The parts of a column of a tile of gate/up added up, a lane two channels.
@@ -1042,10 +1053,7 @@ __device__ void down(const FewArgs& a, Plan& p, const Units& units, DownFeed<NT,
         seg_end = (seg + 1) * fs;
         cnt = p.seg_base[seg + 1] - p.seg_base[seg];
       }
-      if (!ring.wait(a, p)) {
-        feed.more = false;
-        continue;
-      }
+      if (!ring.wait(a, p)) feed.more = false;
       const uint32_t tile = ring.tile(ring.slot);
       uint32_t f[2][4][4];
       fragments(tile, lane, f[0]);
@@ -1090,7 +1098,7 @@ __device__ void down(const FewArgs& a, Plan& p, const Units& units, DownFeed<NT,
     }
     unit_done<W>(a, p, units, i);
   }
-  ring.drain(a, p);
+  ring.drain(a, p, lane);
 }
 
 // The parts of a token's channels of a tile of down added up, a lane two.
@@ -1220,7 +1228,7 @@ __global__ void __launch_bounds__(threads(W), 1)
     if (barrier_wait(a, p))
       down<NT, W>(a, p, dn, feed, acc_s, ring, warp, lane);
     else
-      ring.drain(a, p);
+      ring.drain(a, p, lane);
   } else if (barrier_wait(a, p)) {
     if (warp == W)
       deal_units(a, p, dn, count, lane);
