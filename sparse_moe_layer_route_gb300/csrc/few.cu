@@ -291,6 +291,19 @@ __device__ void join_list(const Plan& p, int warp, int lane, Rows rows_of, Join 
   }
 }
 
+// x may be out, which this kernel writes later, so its loads are ordinary ones (__ldg is for what no thread of the
+// kernel writes).
+__device__ __forceinline__ uint4 load_x(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_x(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // ------------------------------------------------------------------------------------------ router
 // hi + s exactly: the rounding error of the sum (Knuth) goes to lo.
 __device__ __forceinline__ void add_exact(float& hi, float& lo, float s) {
@@ -311,7 +324,7 @@ __device__ void router(const FewArgs& a, Scratch& sc, int warp, int lane) {
       float hi = 0.f, lo = 0.f;
 #pragma unroll 4
       for (int i = part * 32 + lane; i < nv; i += wpt * 32) {
-        const uint4 wv = __ldg(w + i), xv = __ldg(x + i);
+        const uint4 wv = __ldg(w + i), xv = load_x(x + i);
         float s = bf16_lo(wv.x) * bf16_lo(xv.x);
         s = fmaf(bf16_hi(wv.x), bf16_hi(xv.x), s);
         s = fmaf(bf16_lo(wv.y), bf16_lo(xv.y), s);
@@ -717,7 +730,7 @@ __device__ __forceinline__ void order_x(const FewArgs& a) {
   const int n = a.T * (a.d / 8);  // uint4s
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
     const uint32_t* from = reinterpret_cast<const uint32_t*>(a.x) + (i >> 2) * 16 + (i & 3);
-    reinterpret_cast<uint4*>(a.xf)[i] = make_uint4(__ldg(from), __ldg(from + 4), __ldg(from + 8), __ldg(from + 12));
+    reinterpret_cast<uint4*>(a.xf)[i] = make_uint4(load_x(from), load_x(from + 4), load_x(from + 8), load_x(from + 12));
   }
 }
 
