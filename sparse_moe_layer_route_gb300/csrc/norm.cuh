@@ -7,9 +7,26 @@
 namespace moe {
 
 constexpr int kNormMaxSize = 65536;  // d: eight CTAs of a cluster with 8192 channels each
-// CTAs of the gradient at most, each with partial sums in the workspace: three an SM of narrow rows, else two.
-__host__ __device__ __forceinline__ int norm_max_ctas(int d) { return d <= 2048 ? 480 : 320; }
+constexpr int kNormMaxSms = 160;     // of a full GPU of this kind
 constexpr int kNormSmem = 227 * 1024;
+
+// Channels of a CTA of a cluster of cl, and the CTAs that share a row.
+__host__ __device__ __forceinline__ int norm_width(int d, int cl) { return ((d + 7) / 8 + cl - 1) / cl * 8; }
+__host__ __device__ __forceinline__ int norm_cluster(int d) {
+  int cl = 1;
+  while (norm_width(d, cl) > 8192) cl *= 2;
+  return cl;
+}
+// Runs of tokens of the gradient at most (of a CTA, or of a cluster's), each with partial sums in the workspace: an SM
+// has 512 threads of them, and up to 1024 channels a CTA has 256, above that as many warps as a row has pieces of 256
+// channels.
+__host__ __device__ __forceinline__ int norm_grad_threads(int d) {
+  const int pieces = (d + 255) / 256;
+  return d <= 1024 ? 256 : pieces < 16 ? 32 * pieces : 512;
+}
+__host__ __device__ __forceinline__ int norm_grad_runs(int d, int sms) {
+  return 512 / norm_grad_threads(d) * sms / norm_cluster(d);
+}
 
 // Rows of a matrix: elements between rows, type, and whether every row starts on 16 bytes.
 struct RowsIn {
@@ -47,12 +64,12 @@ struct NormGradArgs {
   RowsIn w_after, b_after, gate, w_before;
   RowsOut d_h, d_y;
   float *d_w_after, *d_b_after, *d_gate, *d_w_before, *d_b_before;
-  float* part;                // [CTAs][kNormParts][d]
+  float* part;                // [runs][kNormParts][d]
   Drop drop;
   int T, d, after, before, gate_rows;
   float eps, alpha, beta;
 };
-// Partial sums of a CTA: gradients of w_after, b_after, w_before, b_before, and of the gates that it shares
+// Partial sums of a run: gradients of w_after, b_after, w_before, b_before, and of the gates that it shares
 // with the CTA before it and the one after it.
 constexpr int kNormParts = 6;
 

@@ -64,8 +64,8 @@ bool params_ok(const moe_residual_norm_config* c, const moe_residual_norm_params
 }
 
 size_t need(const moe_residual_norm_config* c) {
-  const int ctas = c->T < norm_max_ctas(c->d) ? c->T : norm_max_ctas(c->d);
-  return (4ull * kNormParts * c->d * ctas + 255) / 256 * 256;
+  const int most = norm_grad_runs(c->d, kNormMaxSms), runs = c->T < most ? c->T : most;
+  return (4ull * kNormParts * c->d * runs + 255) / 256 * 256;
 }
 
 }  // namespace

@@ -427,8 +427,8 @@ cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStrea
     return stage_bytes<R, NC>() + threads / 32 * (bias_bytes<NC>(a) + stages * pitch + turn);
   };
   while (stages > 1 && smem() > kNormSmem / per_sm - 2048) --stages;
-  const int room = per_sm * num_sms() / cl;
-  const int most = room < norm_max_ctas(a.d) ? room : norm_max_ctas(a.d);
+  if (threads != norm_grad_threads(a.d) || cl != norm_cluster(a.d)) return cudaErrorInvalidConfiguration;
+  const int most = norm_grad_runs(a.d, num_sms() < kNormMaxSms ? num_sms() : kNormMaxSms);
   const long long need = ((long long)a.T + groups - 1) / groups;
   *ctas = (int)(need < most ? need : most);
   const int per = norm_rows_per_cta(a.T, *ctas);
@@ -456,9 +456,7 @@ cudaError_t launch_backward(const NormGradArgs& a, int* ctas, cudaStream_t st) {
   if (d <= 2048) return launch_grad_form<256, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 4096) return launch_grad_form<512, 1, false, H, Y>(a, 1, ctas, st);
   if (d <= 8192) return launch_grad_form<512, 2, false, H, Y>(a, 1, ctas, st);
-  int cl = 2;
-  while (norm_width(d, cl) > 8192) cl *= 2;
-  return launch_grad_form<512, 2, true, H, Y>(a, cl, ctas, st);
+  return launch_grad_form<512, 2, true, H, Y>(a, norm_cluster(d), ctas, st);
 }
 
 }  // namespace

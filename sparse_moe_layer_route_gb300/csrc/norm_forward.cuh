@@ -178,9 +178,7 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t st) {
   if (d <= 2048) return launch_form<128, 2, false, H, Y>(a, 1, st);
   if (d <= 4096) return launch_form<256, 2, false, H, Y>(a, 1, st);
   if (d <= 8192) return launch_form<256, 4, false, H, Y>(a, 1, st);
-  int cl = 2;
-  while (norm_width(d, cl) > 8192) cl *= 2;
-  return launch_form<256, 4, true, H, Y>(a, cl, st);
+  return launch_form<256, 4, true, H, Y>(a, norm_cluster(d), st);
 }
 
 }  // namespace

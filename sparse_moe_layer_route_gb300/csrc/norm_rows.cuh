@@ -598,8 +598,6 @@ template <int R>
 __host__ __device__ constexpr int norm_threads() {
   return R < 256 ? 256 : R;
 }
-// Channels of a CTA of a cluster of cl.
-__host__ __device__ __forceinline__ int norm_width(int d, int cl) { return ((d + 7) / 8 + cl - 1) / cl * 8; }
 
 // Launches a kernel of rows: programmatic stream serialization (it waits before it touches memory), and a
 // cluster of cl CTAs where it wants one.
