@@ -77,14 +77,25 @@ class MoeQWeights(ctypes.Structure):
     _fields_ = [(n, MoeQMatrix) for n in ("gate", "up", "down", "sh_gate", "sh_up", "sh_down")]
 
 
-class MoeWeights(ctypes.Structure):
+class _Holding(ctypes.Structure):
+    """Addresses, with the tensors that some of them are of in `_tensors`: a field set anew lets its tensor go."""
+
+    def __setattr__(self, name, value):
+        held = self.__dict__.get("_tensors")
+        if held is not None and name in held:
+            held[name] = None
+            self.__dict__.pop("_fit", None)
+        super().__setattr__(name, value)
+
+
+class MoeWeights(_Holding):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("W_g", "expert_bias", "W_gate", "W_up", "W_down", "Wsh_gate", "Wsh_up",
                  "Wsh_down", "W_down_f16", "Wsh_down_f16")] + \
         [("quant", ctypes.POINTER(MoeQWeights)), ("W_g_t", ctypes.c_void_p)]
 
 
-class MoeRouteOut(ctypes.Structure):
+class MoeRouteOut(_Holding):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("topk_idx", "topk_w", "counts", "offsets", "perm_slot", "slot_pos")]
 
@@ -363,12 +374,15 @@ def combine(cfg, y_slot, slot_pos, out, ws, stream=None):
 def make_weights(W_g, expert_bias, W_gate, W_up, W_down, Wsh_gate=None, Wsh_up=None,
                  Wsh_down=None, W_down_f16=None, Wsh_down_f16=None,
                  quant: MoeQWeights | None = None, W_g_t=None) -> MoeWeights:
+    """The weights' addresses. The struct holds the tensors: their memory stays as long as it does, and the few-token
+    entry points check them. An address that the program sets in a field itself is its own affair: it is not checked, the
+    program keeps its memory, and the tensor that was there is let go."""
     w = MoeWeights(*[_ptr(t) for t in (W_g, expert_bias, W_gate, W_up, W_down, Wsh_gate,
                                         Wsh_up, Wsh_down, W_down_f16, Wsh_down_f16)])
     w.W_g_t = _ptr(W_g_t)
     w._tensors = dict(W_g=W_g, expert_bias=expert_bias, W_gate=W_gate, W_up=W_up, W_down=W_down,
-                      Wsh_gate=Wsh_gate, Wsh_up=Wsh_up, Wsh_down=Wsh_down, W_g_t=W_g_t)
-    w._fit = set()                    # configurations that these tensors have been checked against
+                      Wsh_gate=Wsh_gate, Wsh_up=Wsh_up, Wsh_down=Wsh_down, W_g_t=W_g_t,
+                      W_down_f16=W_down_f16, Wsh_down_f16=Wsh_down_f16)
     if quant is not None:
         w.quant = ctypes.pointer(quant)
         w._quant_ref = quant          # keep the struct alive with the weights
@@ -377,8 +391,10 @@ def make_weights(W_g, expert_bias, W_gate, W_up, W_down, Wsh_gate=None, Wsh_up=N
 
 def make_route_out(topk_idx=None, topk_w=None, counts=None, offsets=None, perm_slot=None,
                    slot_pos=None) -> MoeRouteOut:
-    r = MoeRouteOut(*[_ptr(t) for t in (topk_idx, topk_w, counts, offsets, perm_slot, slot_pos)])
-    r._tensors = (topk_idx, topk_w, counts, offsets, perm_slot, slot_pos)
+    """The struct holds its tensors as make_weights' does."""
+    tensors = (topk_idx, topk_w, counts, offsets, perm_slot, slot_pos)
+    r = MoeRouteOut(*[_ptr(t) for t in tensors])
+    r._tensors = {name: t for (name, _), t in zip(MoeRouteOut._fields_, tensors)}
     return r
 
 
@@ -681,8 +697,9 @@ def _expect_experts(where, cfg, weights, gpu, router):
         return                        # filled in by hand: addresses alone
     d, E, f, S, t = cfg.d, cfg.E, cfg.d_ff, cfg.n_shared, _names()
     bias = router and cfg.mode == ROUTE_BIAS_SELECT
+    fit = weights.__dict__.setdefault("_fit", set())  # configurations that these tensors have been checked against
     key = (d, E, f, S, gpu, router, bias)
-    if key in weights._fit:
+    if key in fit:
         return
     want = dict(W_gate=(E, d, f), W_up=(E, d, f), W_down=(E, f, d))
     if S:
@@ -696,7 +713,7 @@ def _expect_experts(where, cfg, weights, gpu, router):
     m = tensors["expert_bias"]
     if bias and m is not None and not isinstance(m, int):
         _expect(where, "expert_bias", m, (E,), t.f32, gpu)
-    weights._fit.add(key)
+    fit.add(key)
 
 
 def layer_forward_few(cfg, weights: MoeWeights, x, gumbel_u, out, route_out: MoeRouteOut | None, ws,
@@ -709,8 +726,9 @@ def layer_forward_few(cfg, weights: MoeWeights, x, gumbel_u, out, route_out: Moe
     _expect_experts(w, cfg, weights, gpu, True)
     if route_out is not None:
         shapes = ((T, k), (T, k), (E,), (E + 1,), (T * k,), (T * k,))
-        given = getattr(route_out, "_tensors", ())
-        for (name, _), r, shape in zip(MoeRouteOut._fields_, given, shapes):
+        given = getattr(route_out, "_tensors", {})
+        for (name, _), shape in zip(MoeRouteOut._fields_, shapes):
+            r = given.get(name)
             if r is not None and not isinstance(r, int):
                 _expect(w, name, r, shape, t.f32 if name == "topk_w" else t.i32, gpu)
     _check(lib().moe_layer_forward_few(
