@@ -512,7 +512,7 @@ moe_status moe_grouped_ffn_int8(const moe_config* cfg, const uint16_t* x, const 
  * or d or d_ff above 65536.
  *   w: W_g, W_gate, W_up, W_down and, with n_shared > 0, the shared experts' (all 16-byte aligned);
  *   expert_bias and gumbel_u as moe_layer_forward needs them; W_g_t as there. x, out [T, d] bf16, 16-byte
- *   aligned; out may be x. route_out as in moe_layer_forward.
+ *   aligned; out may be x. route_out as in moe_layer_forward, its arrays 4-byte aligned.
  *   ws: moe_few_workspace_size bytes that moe_workspace_init has cleared once (its first 512); calls that
  *   share it must follow one another. It may also be moe_layer_forward's (bf16 experts, no re-route) where it is
  *   as large as both need; other entry points have one of their own. The kernel takes the whole GPU (one CTA per SM, cooperative launch) and

@@ -94,6 +94,11 @@ moe_status moe_layer_forward_few(const moe_config* cfg, const moe_weights* w, co
   moe_status r = check(cfg);
   if (r != MOE_OK) return r;
   const cudaStream_t st = (cudaStream_t)stream;
+  if (route_out != nullptr)
+    for (const void* p : {(const void*)route_out->topk_idx, (const void*)route_out->topk_w,
+                          (const void*)route_out->counts, (const void*)route_out->offsets,
+                          (const void*)route_out->perm_slot, (const void*)route_out->slot_pos})
+      if (!aligned(p, 4)) return MOE_ERR_INVALID_ARG;
   if (cfg->T == 0) {  // as in moe_layer_forward: every expert receives nothing
     if (route_out == nullptr) return MOE_OK;
     cudaError_t e = cudaSuccess;
