@@ -3,9 +3,10 @@
 // With few tokens the layer is the reading of the chosen experts' weights, each once: 6 d f bytes an
 // expert, no more than one token for most of them. One persistent CTA per SM (cooperative launch) goes
 // through four parts, with a grid barrier after the first and the third:
-//   router   one expert per CTA: logits of all tokens. Eight products at a time are summed in fp32, the
-//            sums of eight in an unevaluated pair of floats, so the choice is that of the exact logits but
-//            for gaps of about 1e-8 of the logits' size;
+//   router   one expert per CTA: logits of all tokens. Eight products (exact in fp32) at a time are summed in fp32, the
+//            sums of eight in an unevaluated pair of floats, which becomes one fp32 logit. So a logit is off by at most
+//            7 * 2^-24 of sum |x_i w_i|, from the seven adds inside the eights, and 2^-24 of itself; experts whose
+//            scores are nearer to one another than that may change places;
 //   choice   every CTA makes it for itself, one warp per token, and lists the experts that were hit,
 //            their tokens ("columns") and gates;
 //   gate/up  H = silu(x W_gate) * (x W_up) of the listed experts' columns;
@@ -25,8 +26,11 @@
 //
 // Measured with 128 + 1 experts, d 7168, d_ff 2048, top-2 (decode): one token 60 us (266 MB, 4.4 TB/s), of which 9
 // pass before the first weight is asked for, 29 in gate/up (6.1 TB/s), 3 at the barrier, 14 in down; 16 tokens 370
-// to 395 us (2.4 to 2.6 GB by how many experts are hit: 6.6 TB/s). With 64 + 2 experts, d 2048, d_ff 1408, top-6, five
-// tokens: 79 to 88 us (465 MB). A layer of d 256, d_ff 512: 21 us, the launch's and the barriers'. Bringing the shared
+// to 421 us (2.4 to 2.7 GB by how many experts are hit, and by the GPU: 386 us on equal inputs, 6.7 TB/s). With 64 + 2
+// experts, d 2048, d_ff 1408, top-6, five tokens: 77 to 88 us (465 MB). A layer of d 256, d_ff 512: 21 us, the launch's
+// and the barriers'. The layer of many tokens (nine launches, tiles of 128 rows) takes 117 us for one token of the
+// decode shape where this takes 60, 259 for eight (226) and 429 for sixteen (416); with 16 experts of d 4096, d_ff 14336
+// 597 for eight (557) and 748 for sixteen (755): at sixteen tokens the two are alike. Bringing the shared
 // experts' weights to L2 before the choice is known slows the router by what it gains (60 us with 16 MB, 62 with 64).
 #include <cuda_bf16.h>
 #include <cuda.h>
@@ -126,8 +130,8 @@ __device__ __forceinline__ void barrier_arrive(const FewArgs& a, Plan& p) {
     p.target = (before / n + 1) * n;
   }
 }
-// All threads get the same answer: whether all CTAs have arrived and no wait of this one has given up. They may come from different branches, so it is a barrier by number: warps with
-// different tasks wait at different places.
+// All threads get the same answer: whether all CTAs have arrived and no wait of this one has given up. They may come
+// from different branches, so it is a barrier by number: warps with different tasks wait at different places.
 __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
   int late = p.fail;
   if (threadIdx.x == 0) {
@@ -165,8 +169,10 @@ __device__ __forceinline__ bool barrier_wait(const FewArgs& a, Plan& p) {
 // equal shares wait for (of one token of the decode shape CTAs with equal shares were done with gate/up 35 to 48 us
 // after its start). Smaller units cost more than they even
 // out: with 5, 8, 12, 16 and 32 for eight CTAs one token of the decode shape took 66, 81, 79, 84 and 90 us, 16 tokens
-// 419, 443, 458, 458 and 450, as every cut tile's sums go through the workspace. Which CTA took a unit does not
-// matter to the result: a cut tile's units leave their sums there, and whoever brings the last one adds them in order.
+// 419, 443, 458, 458 and 450, as every cut tile's sums go through the workspace. (Measured on that layer alone, whose 96
+// and 112 tiles five for eight CTAs leaves whole; 56 of 152 SMs then have no unit of gate/up.) Which CTA took a unit
+// does not matter to the result: a cut tile's units leave their sums there, and whoever brings the last one adds
+// them in order.
 //
 // Numbers are fetched, and done units made known, by two warps of their own while the workers stream: fences and
 // atomics take microseconds under load. The tiles that a CTA has to join wait for the end of its units, when all
@@ -1233,7 +1239,8 @@ __global__ void __launch_bounds__(threads(W), 1)
   int* count = a.count + 1 + kMostTiles;
   const auto rows = [&](int) { return make_int2(0, a.T); };
   const auto join = [&](int tile, int t, int l) { join_down(a, dn, tile, t, l); };
-  // Where a wait of this CTA has given up before, or does so here, the workers take the copies under way and that is all.
+  // Where a wait of this CTA has given up before, or does so here, the workers take the copies under way and that is
+  // all.
   if (warp < W) {
     DownFeed<NT, W> feed(a, maps, p, dn, warp, lane);
     if (__any_sync(kFull, p.fail)) feed.more = false;
@@ -1310,7 +1317,8 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
   if (!ok) return cudaErrorInvalidValue;
   // Up to eight tokens an expert has one group of eight columns at most; a second one's slots of the ring leave room
   // for 12 workers. 16 workers and the two others would leave a thread 96 registers: it spilled, and one token of the
-  // decode shape took 80 us instead of 66 with 14 or 12.
+  // decode shape took 80 us instead of 66 with 14 or 12. With 14 nothing is spilled; the form for two groups, whose
+  // sums are 32 registers, spills about 80 bytes of a thread with its 128 (16 tokens: HBM all the same).
   return a.T <= 8 ? launch<1, 14>(a, maps, st) : launch<2, 12>(a, maps, st);
 }
 

@@ -16,7 +16,10 @@
 // Measured: 8192 x 4096, rms norms, a 32-bit stream, gates per channel, dropout: 156 us (604 MB, 3.9 TB/s). A thread
 // holds a row's values and the sums of its channels, up to 128 registers, so 16 warps an SM have to cover two sums
 // over the row in a chain of some 95 instructions an element (issue 44 % of peak). 2051 x 2048, a layer norm before the next block
-// only, gates per sequence: 27 us. Both with the joining kernel.
+// only, gates per sequence: 27 us. 8192 x 7168, bf16, rms norms, gates per channel: 251 us (704 MB, 2.8 TB/s), without
+// gates and a norm after 133: above 4096 channels a thread has two chunks, whose sums and values are more than its 128
+// registers (128 to 152 bytes spilled, of a cluster's rows 164 to 216, of rows of any alignment 404 to 416; waits for
+// memory are the first stall). All with the joining kernel.
 #pragma once
 #include "norm_rows.cuh"
 
@@ -446,7 +449,8 @@ cudaError_t launch_grad_form(const NormGradArgs& a, int cl, int* ctas, cudaStrea
 // As in the forward direction, but one chunk is faster wherever it holds a row: two chunks' sums and values are more than
 // a thread's registers (3001 rows with every gradient, one chunk and two: 1024 channels 29 us and 52, 1032 37 and 54,
 // 2048 53 and 67, 2304 78 and 83, 4096 113 and 110, with rms norms 71 and 81; 50000 of 128 74 and 146, 20000 of 512 76
-// and 80).
+// and 80). From 2049 channels on an SM has one CTA, with as many warps as a row has pieces: 9 at 2304, 16 at 4096 (4096
+// rows, rms norms: 2560 channels 51 us of a floor of 19, 3584 60 of 26).
 template <class H, class Y>
 cudaError_t launch_backward(const NormGradArgs& a, int* ctas, cudaStream_t st) {
   const int d = a.d;
